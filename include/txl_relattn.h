@@ -12,6 +12,8 @@
  *     [memory ; segment];
  *   - txl_relattn_forward_roll: both of the above in one call (the roll
  *     done by the attention kernel from the tiles it loads, where it can);
+ *   - txl_pages_* and txl_relattn_forward_paged: the memory of a ragged batch
+ *     kept in pages of a pool, and the attention over it;
  *   - txl_sinusoid_rel: the parameter-free sinusoidal distance table R.
  *
  * Conventions shared by every entry point
@@ -72,7 +74,8 @@ typedef enum {
   TXL_ERR_UNSUPPORTED = 2,    /* valid request outside what this build supports */
   TXL_ERR_ALIAS = 3,          /* an output range overlaps an input range */
   TXL_ERR_CUDA = 4,           /* a CUDA runtime / driver call failed */
-  TXL_ERR_DEVICE_TIMEOUT = 5  /* a kernel's bounded wait expired (see below) */
+  TXL_ERR_DEVICE_TIMEOUT = 5, /* a kernel's bounded wait expired (see below) */
+  TXL_ERR_PAGES = 6           /* a paged call refused an entry on the device (see "Paged memory") */
 } txl_status;
 
 /*
@@ -430,6 +433,174 @@ TXL_API int txl_stack_forward(const void* h, void* out, int n_layers, void* cons
                               size_t workspace_bytes, int* start_out, int* m_out, cudaStream_t stream);
 
 /*
+ * Paged memory.
+ *
+ * The memory of a ragged batch of sequences, kept in pages of a pool instead
+ * of one buffer or ring per sequence: sequences of unlike age share a launch,
+ * several sequences may share the pages of a common beginning, and a sequence
+ * that ends gives its pages back.  It stores the same rows as the memory of
+ * the other calls ("Transformer-XL, explained", method steps 2 and 6); paging
+ * has no counterpart in the sources cited here.
+ *
+ *   k_pages, v_pages  device, [n_pages, H, page_rows, D]: a head's rows of a
+ *                     page are contiguous, so that a tile of keys is one block
+ *   book              host struct of device arrays (int32) and sizes:
+ *     table  [n_slots, max_pages]  the pages of each slot, oldest rows first,
+ *                                  -1 past the slot's last page
+ *     start  [n_slots]  dead rows at the head of the slot's first page
+ *                       (0 <= start < page_rows; 0 in an empty slot)
+ *     rows   [n_slots]  live rows
+ *     refs   [n_pages]  how often the page stands in the table, 0: free
+ *     page_rows         a power of two, 16 to 1024
+ *
+ * Live row j of a slot is row (start + j) % page_rows of page
+ * table[slot][(start + j) / page_rows].  An empty book is table -1, the
+ * others 0.  What a page holds outside live rows is never used, NaN included.
+ *
+ * A step of a stack of layers calls txl_pages_reserve once; then, per layer,
+ * txl_pages_append and txl_relattn_forward_paged on that layer's pools; then
+ * txl_pages_free where old rows leave.  The entries of a call name slots
+ * (slots [n]) and, where rows come with them, cu [n + 1]: entry i owns rows
+ * cu[i] .. cu[i+1]-1 of the call's [T, H, D] tensors.  All of it is read on
+ * the device: the calls synchronise nothing, allocate nothing, and may be
+ * captured into a graph whose replays find other lengths.  Calls that read or
+ * change one book follow each other on one stream (or are ordered by events).
+ *
+ * Refusals on the device.  An entry whose slot, length, start or page is out
+ * of range, a slot that a call changes and that an earlier entry of the call
+ * names too, rows that do not fit the table or the free pages: such an entry
+ * changes nothing, its output rows stay as they were, and
+ * txl_get_device_status returns TXL_ERR_PAGES.  The other entries are served.
+ * A page id out of range inside a slot's table is never followed.
+ *
+ * Limits (TXL_ERR_UNSUPPORTED): n_slots and n at most 16384, n_pages at most
+ * 2^28, max_pages * page_rows at most 2^30.
+ */
+typedef struct {
+  int* table;
+  int* start;
+  int* rows;
+  int* refs;
+  int n_slots, max_pages, n_pages, page_rows;
+} txl_page_book;
+
+/*
+ * txl_pages_reserve -- pages for the new rows of n slots.
+ *
+ * Entry i adds cu[i+1] - cu[i] rows to slot slots[i].  Free pages are given
+ * out by ascending id, in the order of the entries.  Where the slot's last
+ * page has room but other slots hold it too (refs > 1), the slot gets a page
+ * of its own first and the pair is named for txl_pages_append to copy.  An
+ * entry is served when its pages and those of the entries before it are free;
+ * once one does not fit, later ones that need pages do not either.
+ *
+ *   granted            device, [n] out: the entry's row count, 0 when refused
+ *   copy_src, copy_dst device, [n] out: pages to copy from and to, or -1
+ * table, rows and refs are updated (rows already count the new rows).
+ * A page freed by the copy on write may be given out again by the next
+ * reserve, so the layers' txl_pages_append come before that.
+ */
+TXL_API int txl_pages_reserve(const txl_page_book* book, const int* slots, const int* cu, int n, int* granted,
+                              int* copy_src, int* copy_dst, cudaStream_t stream);
+
+/*
+ * txl_pages_append -- the new rows of n slots into the pages that
+ * txl_pages_reserve gave them, for one layer's pools.
+ *
+ * Rows cu[i] .. cu[i+1]-1 of k_new, v_new become the last rows of slot
+ * slots[i]; before that the rows of page copy_src[i] ahead of them are copied
+ * to page copy_dst[i] (where both are >= 0).  Entries with granted[i] == 0
+ * are left out.  Rows are copied bit for bit.
+ *
+ *   k_new, v_new  device, [T, H, D] `dtype`, rows before cu[0] and from cu[n]
+ *                 on are not read
+ *   copy_src, copy_dst  both NULL: nothing is copied
+ * D <= 256.  The pools must not overlap each other, the new rows or the book
+ * (TXL_ERR_ALIAS).
+ */
+TXL_API int txl_pages_append(const txl_page_book* book, void* k_pages, void* v_pages, int H, int D, const int* slots,
+                             const int* cu, int n, const int* granted, const int* copy_src, const int* copy_dst,
+                             const void* k_new, const void* v_new, int T, txl_dtype dtype, cudaStream_t stream);
+
+/*
+ * txl_pages_copy -- whole pages src[i] -> dst[i] (i < n) of both pools; a
+ * pair with a negative page is left out, one past n_pages refused (see
+ * "Refusals").  page_elems: H * page_rows * D.  A page must not be the dst
+ * of two pairs, nor src of one and dst of another: their order is undefined.
+ */
+TXL_API int txl_pages_copy(void* k_pages, void* v_pages, int n_pages, long long page_elems, const int* src,
+                           const int* dst, int n, txl_dtype dtype, cudaStream_t stream);
+
+/*
+ * txl_pages_fork -- slot dst[i] becomes a copy of slot src[i] that shares its
+ * pages (refs + 1 each); no row moves.  dst[i] must be empty, named once, and
+ * neither src[i] itself nor any entry's src.  ok: device, [n] out, 1 or 0
+ * (refused).
+ */
+TXL_API int txl_pages_fork(const txl_page_book* book, const int* src, const int* dst, int n, int* ok,
+                           cudaStream_t stream);
+
+/*
+ * txl_pages_free -- slot slots[i] keeps its newest keep[i] rows (all of them
+ * when it has fewer, none when keep is NULL or keep[i] <= 0): the memory roll
+ * of txl_mem_update, by giving pages back.  Pages without a kept row leave
+ * the slot's table (refs - 1).
+ */
+TXL_API int txl_pages_free(const txl_page_book* book, const int* slots, const int* keep, int n, cudaStream_t stream);
+
+/*
+ * txl_pages_compact -- the N live pages (refs > 0) get the ids 0 .. N-1.
+ *
+ * Live pages below N keep their id; the k-th live page at or past N takes the
+ * k-th free id below N.  table and refs are rewritten; the rows move by
+ * txl_pages_copy(k_pages, v_pages, ..., copy_src, copy_dst, n_pages) on each
+ * layer's pools, before anything else reads them.
+ *
+ *   new_id             device, [n_pages] out: the page's new id, -1 if free
+ *   copy_src, copy_dst device, [n_pages] out: the moves, then -1
+ *   count              device, [1] out: how many pages move
+ */
+TXL_API int txl_pages_compact(const txl_page_book* book, int* new_id, int* copy_src, int* copy_dst, int* count,
+                              cudaStream_t stream);
+
+/*
+ * txl_relattn_forward_paged -- txl_relattn_forward of the new tokens of a
+ * ragged batch over a paged memory that already holds their keys and values.
+ *
+ * Entry i has n_i = cu[i+1] - cu[i] queries, rows cu[i] .. of q, the last n_i
+ * positions of slot slots[i]: query t sits at position m + t, m = rows - n_i,
+ * and with live rows j = 0 .. rows-1
+ *
+ *   s[t,j] = scale * ( (q_t + u_h) . k_j + (q_t + v_h) . r_{m+t-j} )   j <= m+t
+ *   o_t    = sum_j softmax_j(s[t,.]) v_j        lse_t = log sum_j exp(s[t,j])
+ *
+ * One token per entry is the step of a decoder, a whole segment per entry the
+ * forward of txl_relattn_forward with the memory rows in front.  A query at a
+ * negative position (n_i > rows) sees no row: o_t = 0, lse_t = -inf.  Rows of
+ * o and lse that no entry owns are left as they were.
+ *
+ *   q        device, [T, H, D] `dtype`
+ *   slots, cu, book  as above; one slot may be named by several entries
+ *   max_new  the largest n_i, or more (an entry with more is refused)
+ *   r        device, [n_r, H, D] `dtype`, row d: distance d; an entry with
+ *            more than n_r live rows is refused
+ *   o        device, [T, H, D] `o_dtype`;  lse  device, [H, T] fp32 or NULL
+ *   workspace  device, txl_relattn_paged_workspace_bytes(...) bytes, 256-byte
+ *            aligned; its content matters to no other call.  Calls that may
+ *            run at the same time need a workspace each.
+ * dtype, o_dtype, D, scale, alignments and alias rules as in
+ * txl_relattn_forward.
+ */
+TXL_API size_t txl_relattn_paged_workspace_bytes(int n, int T, int H, int D, txl_dtype dtype);
+
+TXL_API int txl_relattn_forward_paged(const void* q, const void* k_pages, const void* v_pages,
+                                      const txl_page_book* book, const int* slots, const int* cu, int n, int T,
+                                      int max_new, const void* r, const float* bias_u, const float* bias_v, void* o,
+                                      float* lse, int H, int D, int n_r, float scale, txl_dtype dtype,
+                                      txl_dtype o_dtype, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
+/*
  * txl_relattn_backward -- gradients of txl_relattn_forward.
  *
  * Given dout = dL/do for the forward's o, writes the gradients of L through
@@ -511,6 +682,7 @@ TXL_API int txl_sinusoid_rel(void* R, int n_dist, int dim, txl_dtype dtype, cuda
  * device status word of the current device.  Returns TXL_OK, or
  * TXL_ERR_DEVICE_TIMEOUT when a kernel gave up a bounded wait (it then exits
  * cleanly, leaving its outputs undefined, and the context stays usable), or
+ * TXL_ERR_PAGES when a paged call refused an entry (and none timed out), or
  * TXL_ERR_CUDA if the synchronisation itself failed.
  */
 TXL_API int txl_get_device_status(cudaStream_t stream);

@@ -22,6 +22,8 @@ __all__ = [
     "txl_mem_ring_append",
     "txl_layer_forward", "txl_layer_workspace_bytes", "LAYER_WEIGHT_NAMES", "txl_dense", "txl_stack_forward",
     "txl_stack_workspace_bytes",
+    "txl_pages_reserve", "txl_pages_append", "txl_pages_copy", "txl_pages_fork", "txl_pages_free",
+    "txl_pages_compact", "txl_relattn_forward_paged", "txl_relattn_paged_workspace_bytes",
     "txl_sinusoid_rel",
     "txl_get_device_status", "txl_release_cached", "txl_status_string", "txl_version",
     "txl_debug_set_wait_limit_ns", "txl_debug_inject_stall", "txl_debug_force_split",
@@ -38,7 +40,7 @@ __all__ = [
 TXL_F32 = 0
 TXL_BF16 = 1
 _STATUS = {0: "TXL_OK", 1: "TXL_ERR_INVALID_ARG", 2: "TXL_ERR_UNSUPPORTED", 3: "TXL_ERR_ALIAS",
-           4: "TXL_ERR_CUDA", 5: "TXL_ERR_DEVICE_TIMEOUT"}
+           4: "TXL_ERR_CUDA", 5: "TXL_ERR_DEVICE_TIMEOUT", 6: "TXL_ERR_PAGES"}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtxl_relattn.so")
 if not os.path.exists(library_path):
@@ -91,6 +93,31 @@ lib.txl_mem_update.restype = _i
 lib.txl_mem_update_kv.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _i, _i, _i, _ll, _ll, _ll, ctypes.POINTER(_i), _i,
                                   _p]
 lib.txl_mem_update_kv.restype = _i
+
+
+class _PageBook(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "start", "rows", "refs")] + [
+        (n, ctypes.c_int) for n in ("n_slots", "max_pages", "n_pages", "page_rows")]
+
+
+_pb = ctypes.POINTER(_PageBook)
+lib.txl_pages_reserve.argtypes = [_pb, _p, _p, _i, _p, _p, _p, _p]
+lib.txl_pages_reserve.restype = _i
+lib.txl_pages_append.argtypes = [_pb, _p, _p, _i, _i, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _p]
+lib.txl_pages_append.restype = _i
+lib.txl_pages_copy.argtypes = [_p, _p, _i, _ll, _p, _p, _i, _i, _p]
+lib.txl_pages_copy.restype = _i
+lib.txl_pages_fork.argtypes = [_pb, _p, _p, _i, _p, _p]
+lib.txl_pages_fork.restype = _i
+lib.txl_pages_free.argtypes = [_pb, _p, _p, _i, _p]
+lib.txl_pages_free.restype = _i
+lib.txl_pages_compact.argtypes = [_pb, _p, _p, _p, _p, _p]
+lib.txl_pages_compact.restype = _i
+lib.txl_relattn_paged_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+lib.txl_relattn_paged_workspace_bytes.restype = ctypes.c_size_t
+lib.txl_relattn_forward_paged.argtypes = [_p, _p, _p, _pb, _p, _p, _i, _i, _i, _p, _p, _p, _p, _p, _i, _i, _i, _f, _i,
+                                          _i, _p, ctypes.c_size_t, _p]
+lib.txl_relattn_forward_paged.restype = _i
 lib.txl_sinusoid_rel.argtypes = [_p, _i, _i, _i, _p]
 lib.txl_sinusoid_rel.restype = _i
 lib.txl_get_device_status.argtypes = [_p]
@@ -385,6 +412,179 @@ def txl_dense(x, W, y, bias=None, relu=False, stream=None):
                        _stream(stream))
     _check(st, "txl_dense")
     return y
+
+
+def _int32(name, t, n=None):
+    """Raises unless t is a contiguous int32 vector (of n entries)."""
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous int32 vector" + ("" if n is None else f" of {n} entries"))
+
+
+def _on_device(*tensors):
+    """Raises unless every tensor lives on the current device, where the call
+    launches."""
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError("tensors must live in the current device's memory")
+
+
+def _book(book, page_rows):
+    """The C struct of a page book: a dict of int32 tensors table [slots,
+    max_pages], start and rows [slots], refs [pages]."""
+    table = book["table"]
+    if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 [slots, max_pages] tensor")
+    n_slots, max_pages = table.shape
+    _int32("start", book["start"], n_slots)
+    _int32("rows", book["rows"], n_slots)
+    _int32("refs", book["refs"])
+    _on_device(table, book["start"], book["rows"], book["refs"])
+    return _PageBook(_ptr(table), _ptr(book["start"]), _ptr(book["rows"]), _ptr(book["refs"]), n_slots, max_pages,
+                     book["refs"].shape[0], int(page_rows))
+
+
+def _pools(k_pages, v_pages, n_pages=None):
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages, v_pages must be [pages, H, page_rows, D] of one dtype")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    if n_pages is not None and k_pages.shape[0] != n_pages:
+        raise ValueError("the pools' pages must be those that refs counts")
+    _on_device(k_pages, v_pages)
+
+
+def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, stream=None):
+    """Pages for cu[i+1] - cu[i] new rows of slot slots[i], for every i.  book:
+    dict of int32 tensors table [slots, max_pages], start, rows [slots], refs
+    [pages].  granted, copy_src, copy_dst (int32 [n]) receive the rows granted
+    and the pages that txl_pages_append has to copy."""
+    b = _book(book, page_rows)
+    n = slots.shape[0]
+    for name, t, m in (("slots", slots, n), ("cu", cu, n + 1), ("granted", granted, n), ("copy_src", copy_src, n),
+                       ("copy_dst", copy_dst, n)):
+        _int32(name, t, m)
+    _on_device(slots, cu, granted, copy_src, copy_dst)
+    _check(lib.txl_pages_reserve(ctypes.byref(b), _ptr(slots), _ptr(cu), n, _ptr(granted), _ptr(copy_src),
+                                 _ptr(copy_dst), _stream(stream)), "txl_pages_reserve")
+
+
+def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new, stream=None):
+    """Rows cu[i] .. cu[i+1]-1 of k_new, v_new [T, H, D] into the last rows of
+    slot slots[i] of the pools [pages, H, page_rows, D], after the copies that
+    txl_pages_reserve named (copy_src, copy_dst, or None and None)."""
+    _pools(k_pages, v_pages, book["refs"].shape[0])
+    _, H, P, D = k_pages.shape
+    b = _book(book, P)
+    n = slots.shape[0]
+    for name, t, m in (("slots", slots, n), ("cu", cu, n + 1), ("granted", granted, n)):
+        _int32(name, t, m)
+    if (copy_src is None) != (copy_dst is None):
+        raise ValueError("copy_src and copy_dst come together")
+    if copy_src is not None:
+        _int32("copy_src", copy_src, n)
+        _int32("copy_dst", copy_dst, n)
+    if k_new.dim() != 3 or k_new.shape[1:] != (H, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new, v_new must be [T, H, D]")
+    if not (k_new.dtype == v_new.dtype == k_pages.dtype):
+        raise ValueError("the pools and the new rows share a dtype")
+    if not (k_new.is_contiguous() and v_new.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    _on_device(slots, cu, granted, copy_src, copy_dst, k_new, v_new)
+    _check(lib.txl_pages_append(ctypes.byref(b), _ptr(k_pages), _ptr(v_pages), H, D, _ptr(slots), _ptr(cu), n,
+                                _ptr(granted), _ptr(copy_src), _ptr(copy_dst), _ptr(k_new), _ptr(v_new),
+                                k_new.shape[0], _dtype_code(k_pages.dtype), _stream(stream)), "txl_pages_append")
+
+
+def txl_pages_copy(k_pages, v_pages, src, dst, stream=None):
+    """Whole pages src[i] -> dst[i] of both pools; pairs with -1 are left out."""
+    _pools(k_pages, v_pages)
+    _int32("src", src)
+    _int32("dst", dst, src.shape[0])
+    _on_device(src, dst)
+    _check(lib.txl_pages_copy(_ptr(k_pages), _ptr(v_pages), k_pages.shape[0], math.prod(k_pages.shape[1:]),
+                              _ptr(src), _ptr(dst), src.shape[0], _dtype_code(k_pages.dtype), _stream(stream)),
+           "txl_pages_copy")
+
+
+def txl_pages_fork(book, page_rows, src, dst, ok, stream=None):
+    """Empty slot dst[i] shares the pages of slot src[i]; ok (int32 [n])
+    receives 1, or 0 where refused."""
+    b = _book(book, page_rows)
+    n = src.shape[0]
+    for name, t in (("src", src), ("dst", dst), ("ok", ok)):
+        _int32(name, t, n)
+    _on_device(src, dst, ok)
+    _check(lib.txl_pages_fork(ctypes.byref(b), _ptr(src), _ptr(dst), n, _ptr(ok), _stream(stream)),
+           "txl_pages_fork")
+
+
+def txl_pages_free(book, page_rows, slots, keep=None, stream=None):
+    """Slot slots[i] keeps its newest keep[i] rows (None: none)."""
+    b = _book(book, page_rows)
+    n = slots.shape[0]
+    _int32("slots", slots)
+    if keep is not None:
+        _int32("keep", keep, n)
+    _on_device(slots, keep)
+    _check(lib.txl_pages_free(ctypes.byref(b), _ptr(slots), _ptr(keep), n, _stream(stream)), "txl_pages_free")
+
+
+def txl_pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, stream=None):
+    """The live pages get the lowest ids.  new_id, copy_src, copy_dst (int32
+    [pages]) and count (int32 [1]) receive the new ids and the moves, which
+    txl_pages_copy(k_pages, v_pages, copy_src, copy_dst) then makes."""
+    b = _book(book, page_rows)
+    for name, t, m in (("new_id", new_id, b.n_pages), ("copy_src", copy_src, b.n_pages),
+                       ("copy_dst", copy_dst, b.n_pages), ("count", count, 1)):
+        _int32(name, t, m)
+    _on_device(new_id, copy_src, copy_dst, count)
+    _check(lib.txl_pages_compact(ctypes.byref(b), _ptr(new_id), _ptr(copy_src), _ptr(copy_dst), _ptr(count),
+                                 _stream(stream)), "txl_pages_compact")
+
+
+def txl_relattn_paged_workspace_bytes(n, T, H, D, dtype):
+    """Bytes of workspace for n entries with T new tokens in all."""
+    return int(lib.txl_relattn_paged_workspace_bytes(int(n), int(T), int(H), int(D), _dtype_code(dtype)))
+
+
+def txl_relattn_forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, bias_v, o, workspace, lse=None,
+                              max_new=None, scale=None, stream=None):
+    """o [T, H, D] <- relative attention of q [T, H, D]: rows cu[i] ..
+    cu[i+1]-1 are the newest positions of slot slots[i], whose rows the pools
+    [pages, H, page_rows, D] hold.  r [n_r, H, D], biases [H, D] fp32; lse
+    [H, T] fp32 or None; max_new: the largest number of new rows of an entry
+    (T when None); workspace: uint8, txl_relattn_paged_workspace_bytes(...).
+    scale defaults to 1/sqrt(D)."""
+    _pools(k_pages, v_pages, book["refs"].shape[0])
+    _, H, P, D = k_pages.shape
+    b = _book(book, P)
+    n = slots.shape[0]
+    _int32("slots", slots)
+    _int32("cu", cu, n + 1)
+    T = q.shape[0]
+    if q.shape != (T, H, D) or o.shape != q.shape:
+        raise ValueError("q and o must be [T, H, D]")
+    if r.dim() != 3 or r.shape[1:] != (H, D) or bias_u.shape != (H, D) or bias_v.shape != (H, D):
+        raise ValueError("r must be [n_r, H, D]; biases [H, D]")
+    if bias_u.dtype != torch.float32 or bias_v.dtype != torch.float32:
+        raise ValueError("biases are fp32")
+    if not (q.dtype == k_pages.dtype == r.dtype):
+        raise ValueError("q, the pools and r share a dtype")
+    if lse is not None and (lse.shape != (H, T) or lse.dtype != torch.float32):
+        raise ValueError("lse must be fp32 [H, T]")
+    for t in (q, r, bias_u, bias_v, o, workspace) + ((lse,) if lse is not None else ()):
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    _on_device(q, slots, cu, r, bias_u, bias_v, o, workspace, lse)
+    if scale is None:
+        scale = D ** -0.5
+    st = lib.txl_relattn_forward_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), ctypes.byref(b), _ptr(slots), _ptr(cu),
+                                       n, T, T if max_new is None else int(max_new), _ptr(r), _ptr(bias_u),
+                                       _ptr(bias_v), _ptr(o), _ptr(lse), H, D, r.shape[0], float(scale),
+                                       _dtype_code(q.dtype), _dtype_code(o.dtype), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "txl_relattn_forward_paged")
+    return o
 
 
 def txl_mem_ring_append(mem, start, m, h, stream=None):

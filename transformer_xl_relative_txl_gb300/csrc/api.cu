@@ -14,6 +14,7 @@
 #include <mutex>
 #include <utility>
 
+#include "pages.h"
 #include "txl_internal.h"
 #include "txl_relattn.h"
 
@@ -358,6 +359,13 @@ int ring_append_impl(void* const* mem, const void* const* h, int n, int cap, int
 
 }  // namespace
 
+namespace txl {
+
+int api_wait_ctl(WaitCtl* wc) { return wait_ctl(wc); }
+PFN_cuTensorMapEncodeTiled_v12000 api_tensor_map_encoder() { return tensor_map_encoder(); }
+
+}  // namespace txl
+
 extern "C" {
 
 int txl_version(void) { return TXL_VERSION; }
@@ -370,6 +378,7 @@ const char* txl_status_string(int status) {
     case TXL_ERR_ALIAS: return "TXL_ERR_ALIAS";
     case TXL_ERR_CUDA: return "TXL_ERR_CUDA";
     case TXL_ERR_DEVICE_TIMEOUT: return "TXL_ERR_DEVICE_TIMEOUT";
+    case TXL_ERR_PAGES: return "TXL_ERR_PAGES";
     default: return "TXL_ERR_UNKNOWN";
   }
 }
@@ -456,7 +465,7 @@ int txl_get_device_status(cudaStream_t stream) {
       return TXL_ERR_CUDA;
     return TXL_ERR_DEVICE_TIMEOUT;
   }
-  return TXL_OK;
+  return (v & txl::kStatusPagesBit) != 0 ? TXL_ERR_PAGES : TXL_OK;
 }
 
 int txl_release_cached(void) {

@@ -1,0 +1,608 @@
+// The paged memory's book-keeping and its data movement: pages reserved for
+// new rows (copy on write where a page is shared), rows written, pages
+// copied, slots forked, the oldest rows freed, the live pages compacted.
+//
+// A slot's live rows are rows start .. start + rows - 1 of the concatenation
+// of its pages table[slot][0], table[slot][1], ... (page_rows rows each);
+// refs[p] counts the table entries that name page p, 0: free.  Every call
+// works on device state alone (no host copy of a length), so a serving step
+// can be captured into a graph and replayed, and every result is a function
+// of the state before the call: free pages are given out by ascending id in
+// the order of the call's entries, whatever order the threads run in.
+//
+// Bad entries (a slot, page or length out of range, the same slot twice) are
+// refused, touch nothing and raise the pages bit of the status word.
+#include <climits>
+#include <cstdint>
+
+#include "pages.h"
+#include "pdl.cuh"
+#include "txl_internal.h"
+
+namespace txl {
+namespace {
+
+constexpr int kBlock = 1024;    // threads of the single-CTA kernels
+constexpr int kPerThread = 16;  // refs a thread looks at per tile
+
+__device__ __forceinline__ void report_pages(unsigned int* status) { atomicOr(status, kStatusPagesBit); }
+
+__device__ __forceinline__ int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
+
+// Inclusive sum over the CTA, saturating at `cap` (min(a + b, cap) is
+// associative for non-negative terms; cap < 2^30, so no sum overflows).
+// warp_sums[31] holds the CTA's sum until the next call.
+__device__ int block_scan(int x, int cap, int* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x = min(x + y, cap);
+  }
+  __syncthreads();  // warp_sums of the scan before has been read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s = min(s + y, cap);
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  return warp > 0 ? min(x + warp_sums[warp - 1], cap) : x;
+}
+static_assert(kBlock == 1024, "block_scan sums 32 warps");
+
+// A slot's state as the calls read it; ok: the slot and its lengths are in
+// range.
+struct Slot {
+  int s, start, rows;
+  bool ok;
+};
+
+__device__ __forceinline__ Slot read_slot(const PageBook& b, int s) {
+  Slot r{s, 0, 0, s >= 0 && s < b.n_slots};
+  if (r.ok) {
+    r.start = b.start[s];
+    r.rows = b.rows[s];
+    r.ok = r.start >= 0 && r.start < b.page_rows && r.rows >= 0 &&
+           static_cast<long long>(r.start) + r.rows <= static_cast<long long>(b.max_pages) * b.page_rows;
+  }
+  return r;
+}
+
+__device__ __forceinline__ int* table_row(const PageBook& b, int s) {
+  return b.table + static_cast<size_t>(s) * b.max_pages;
+}
+
+// The 16 refs of this thread in the tile at `base`, as a mask of the pages
+// in use (past the end: in use).
+__device__ __forceinline__ uint32_t used_mask(const PageBook& b, int base) {
+  const int p0 = base + threadIdx.x * kPerThread;
+  uint32_t m = 0;
+  if (p0 + kPerThread <= b.n_pages && (reinterpret_cast<uintptr_t>(b.refs) & 15) == 0) {
+#pragma unroll
+    for (int q = 0; q < kPerThread / 4; ++q) {
+      const int4 v = *reinterpret_cast<const int4*>(b.refs + p0 + 4 * q);
+      m |= ((v.x != 0) | (v.y != 0) << 1 | (v.z != 0) << 2 | (v.w != 0) << 3) << (4 * q);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kPerThread; ++q) m |= (p0 + q >= b.n_pages || b.refs[p0 + q] != 0 ? 1u : 0u) << q;
+  }
+  return m;
+}
+
+// ---------------------------------------------------------------------------
+// reserve
+// ---------------------------------------------------------------------------
+// One CTA: the entries' needs are summed in order, then the free pages are
+// found by scanning refs in ascending order, 16384 pages a step, only as far
+// as the needs go.  A free page's rank names its entry (binary search in the
+// sums) and its place in the entry's table row.
+__global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* __restrict__ slots,
+                                                         const int* __restrict__ cu, int n, int* granted,
+                                                         int* copy_src, int* copy_dst, unsigned int* status) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  extern __shared__ int smem[];
+  int* first = smem;             // [n_slots] the entry that names the slot first
+  int* upto = smem + b.n_slots;  // [n] pages needed by entries 0 .. i
+  __shared__ int warp_sums[32];
+  __shared__ int s_lim;
+  const int tid = threadIdx.x;
+  const int cap = b.n_pages + 1;
+
+  for (int i = tid; i < n; i += kBlock)
+    if (const int s = slots[i]; s >= 0 && s < b.n_slots) first[s] = INT_MAX;
+  __syncthreads();
+  for (int i = tid; i < n; i += kBlock)
+    if (const int s = slots[i]; s >= 0 && s < b.n_slots) atomicMin(&first[s], i);
+  if (tid == 0) s_lim = 0;
+  __syncthreads();
+
+  // What entry i asks for: pages (0 where it asks for none or is refused),
+  // whether its last page is shared and so copied, and whether it is valid.
+  struct Ask {
+    Slot sl;
+    int count, need, last;
+    bool ok, shared;
+  };
+  auto ask = [&](int i) {
+    Ask a{read_slot(b, slots[i]), cu[i + 1] - cu[i], 0, -1, false, false};
+    a.ok = a.sl.ok && a.count > 0 && first[a.sl.s] == i;
+    if (a.ok) {
+      const long long end = static_cast<long long>(a.sl.start) + a.sl.rows;
+      const int have = ceil_div(end, b.page_rows);
+      const long long want = (end + a.count + b.page_rows - 1) / b.page_rows;
+      a.ok = want <= b.max_pages;
+      if (a.ok && end % b.page_rows != 0) {
+        a.last = table_row(b, a.sl.s)[have - 1];
+        a.ok = a.last >= 0 && a.last < b.n_pages;
+        a.shared = a.ok && b.refs[a.last] > 1;
+      }
+      if (a.ok) a.need = static_cast<int>(want) - have + (a.shared ? 1 : 0);
+    }
+    return a;
+  };
+
+  int carry = 0;
+  for (int base = 0; base < n; base += kBlock) {
+    const int i = base + tid;
+    const int need = i < n ? min(ask(i).need, cap) : 0;
+    const int sum = min(carry + block_scan(need, cap, warp_sums), cap);
+    if (i < n) upto[i] = sum;
+    carry = min(carry + warp_sums[31], cap);
+  }
+  __syncthreads();
+  const int total = carry;
+
+  // Free pages there are, counted as far as `total`; lim: pages given out.
+  int lim = total;
+  if (total > 0) {
+    int found = 0;
+    for (int base = 0; base < b.n_pages && found < total; base += kBlock * kPerThread) {
+      block_scan(kPerThread - __popc(used_mask(b, base)), cap, warp_sums);
+      found = min(found + warp_sums[31], cap);
+    }
+    if (found < total) {
+      for (int i = tid; i < n; i += kBlock)
+        if (upto[i] <= found) atomicMax(&s_lim, upto[i]);
+      __syncthreads();
+      lim = s_lim;
+    }
+  }
+
+  // The entries' answers, from the state before any change; the pages of
+  // the copies follow below.
+  for (int i = tid; i < n; i += kBlock) {
+    const Ask a = ask(i);
+    const bool given = a.ok && (a.need == 0 || upto[i] <= lim);
+    granted[i] = given ? a.count : 0;
+    copy_src[i] = given && a.shared ? a.last : -1;
+    copy_dst[i] = -1;
+    if (!given && !(a.sl.ok && a.count == 0)) report_pages(status);
+  }
+  __syncthreads();
+
+  // Free pages 0 .. lim-1 to their places.  A page's ref changes only after
+  // the thread that owns it has read it.
+  int rank0 = 0;
+  for (int base = 0; base < b.n_pages && rank0 < lim; base += kBlock * kPerThread) {
+    const uint32_t used = used_mask(b, base);
+    const int mine = kPerThread - __popc(used);
+    int rank = rank0 + block_scan(mine, cap, warp_sums) - mine;
+    rank0 += warp_sums[31];
+    for (uint32_t m = ~used & 0xffffu; m != 0 && rank < lim; m &= m - 1, ++rank) {
+      const int page = base + tid * kPerThread + __ffs(m) - 1;
+      int lo = 0, hi = n - 1;  // the first entry with upto > rank
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (upto[mid] > rank)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      const int j = rank - (lo > 0 ? upto[lo - 1] : 0);
+      const int s = slots[lo];
+      const int have = ceil_div(static_cast<long long>(b.start[s]) + b.rows[s], b.page_rows);
+      const int copied = copy_src[lo] >= 0 ? 1 : 0;
+      b.refs[page] = 1;
+      table_row(b, s)[have + j - copied] = page;
+      if (j < copied) copy_dst[lo] = page;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kBlock) {
+    if (granted[i] > 0) b.rows[slots[i]] += granted[i];
+    if (copy_src[i] >= 0) atomicSub(&b.refs[copy_src[i]], 1);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+// CTA (x, i) writes rows of entry i: first the rows of the copied page that
+// lie before the new ones, then the new rows, each as H pieces of D values.
+template <typename V>
+__global__ void __launch_bounds__(256) append_kernel(PageBook b, V* __restrict__ kp, V* __restrict__ vp, int H, int DV,
+                                                     const int* __restrict__ slots, const int* __restrict__ cu,
+                                                     const int* __restrict__ granted,
+                                                     const int* __restrict__ copy_src,
+                                                     const int* __restrict__ copy_dst, const V* __restrict__ kn,
+                                                     const V* __restrict__ vn, int T, unsigned int* status) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int i = blockIdx.y;
+  const int count = granted[i];
+  if (count <= 0) return;
+  const int t0 = cu[i];
+  const Slot sl = read_slot(b, slots[i]);
+  if (!sl.ok || count > sl.rows || t0 < 0 || count != cu[i + 1] - t0 || static_cast<long long>(t0) + count > T) {
+    if (threadIdx.x == 0) report_pages(status);
+    return;
+  }
+  const int P = b.page_rows;
+  const int x0 = sl.start + sl.rows - count;  // first new row
+  int from = -1, to = -1;
+  if (copy_src != nullptr) from = copy_src[i], to = copy_dst[i];
+  const bool copies = from >= 0 && to >= 0;
+  if (copies && (from >= b.n_pages || to >= b.n_pages)) {
+    if (threadIdx.x == 0) report_pages(status);
+    return;
+  }
+  const int old = copies ? x0 % P : 0;
+  const int* row = table_row(b, sl.s);
+  const long long per = static_cast<long long>(H) * DV;  // vectors of a row
+  const long long total = (old + static_cast<long long>(count)) * per;
+  const size_t page = static_cast<size_t>(H) * P * DV;
+  bool bad = false;
+  constexpr int U = 4;
+  const long long step = static_cast<long long>(gridDim.x) * 256 * U;
+  for (long long e0 = static_cast<long long>(blockIdx.x) * 256 * U + threadIdx.x; e0 < total; e0 += step) {
+    V kx[U], vx[U];
+    size_t dst[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long e = e0 + u * 256;
+      on[u] = e < total;
+      if (!on[u]) continue;
+      const int y = static_cast<int>(e / per), rem = static_cast<int>(e % per);
+      const int h = rem / DV, c = rem % DV;
+      if (y < old) {
+        const size_t at = (static_cast<size_t>(h) * P + y) * DV + c;
+        dst[u] = to * page + at;
+        kx[u] = kp[from * page + at];
+        vx[u] = vp[from * page + at];
+      } else {
+        const int x = x0 + y - old;
+        const int id = row[x / P];
+        on[u] = id >= 0 && id < b.n_pages;
+        bad |= !on[u];
+        dst[u] = id * page + (static_cast<size_t>(h) * P + x % P) * DV + c;
+        const size_t src = static_cast<size_t>(t0 + y - old) * per + rem;
+        kx[u] = __ldg(kn + src);
+        vx[u] = __ldg(vn + src);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (on[u]) {
+        kp[dst[u]] = kx[u];
+        vp[dst[u]] = vx[u];
+      }
+  }
+  if (bad) report_pages(status);
+}
+
+// ---------------------------------------------------------------------------
+// copy
+// ---------------------------------------------------------------------------
+// Whole pages src[i] -> dst[i] of both pools, in chunks of 256 x 4 vectors
+// spread over the CTAs; each CTA looks 256 of its chunks ahead at a time, so
+// that the entries without a copy (-1) cost one load per 256.
+template <typename V>
+__global__ void __launch_bounds__(256) copy_kernel(V* kp, V* vp, int n_pages, long long page_vecs,
+                                                   const int* __restrict__ src, const int* __restrict__ dst, int n,
+                                                   unsigned int* status) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  constexpr int U = 4;
+  __shared__ int list[256];
+  __shared__ int counts[8];
+  const long long per = (page_vecs + 256 * U - 1) / (256 * U);  // chunks of a page of one pool
+  const long long total = 2 * per * n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (long long k0 = 0; blockIdx.x + k0 * gridDim.x < total; k0 += 256) {
+    const long long q = blockIdx.x + (k0 + threadIdx.x) * gridDim.x;
+    bool on = false;
+    if (q < total) {
+      const int i = static_cast<int>(q / (2 * per));
+      const int a = src[i], z = dst[i];
+      on = a >= 0 && z >= 0;
+      if (on && (a >= n_pages || z >= n_pages)) {
+        report_pages(status);
+        on = false;
+      }
+    }
+    const uint32_t votes = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) counts[warp] = __popc(votes);
+    __syncthreads();
+    int at = 0, m = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      at += w < warp ? counts[w] : 0;
+      m += counts[w];
+    }
+    if (on) list[at + __popc(votes & ((1u << lane) - 1))] = threadIdx.x;
+    __syncthreads();
+    for (int y = 0; y < m; ++y) {
+      const long long c = blockIdx.x + (k0 + list[y]) * gridDim.x;
+      const int i = static_cast<int>(c / (2 * per));
+      const long long part = c % (2 * per);
+      V* pool = part < per ? kp : vp;
+      const V* from = pool + src[i] * static_cast<size_t>(page_vecs);
+      V* to = pool + dst[i] * static_cast<size_t>(page_vecs);
+      const long long e0 = (part < per ? part : part - per) * (256 * U) + threadIdx.x;
+      V x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (e0 + u * 256 < page_vecs) x[u] = from[e0 + u * 256];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (e0 + u * 256 < page_vecs) to[e0 + u * 256] = x[u];
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fork, free
+// ---------------------------------------------------------------------------
+// CTA i: dst[i] becomes a second owner of src[i]'s pages.  dst must be empty
+// and named once, src not named as a dst: then no CTA writes what another
+// reads, and the counts' atomic sums do not depend on their order.
+__global__ void __launch_bounds__(128) fork_kernel(PageBook b, const int* __restrict__ src,
+                                                   const int* __restrict__ dst, int n, int* ok_out,
+                                                   unsigned int* status) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int i = blockIdx.x;
+  const int d = dst[i];
+  const Slot a = read_slot(b, src[i]);
+  bool ok = a.ok && d >= 0 && d < b.n_slots && d != a.s;
+  for (int j = threadIdx.x; ok && j < n; j += blockDim.x) ok = dst[j] != a.s && (j >= i || dst[j] != d);
+  if (ok) ok = b.rows[d] == 0;
+  ok = __syncthreads_and(ok);
+  int pages = 0;
+  if (ok) {
+    pages = ceil_div(static_cast<long long>(a.start) + a.rows, b.page_rows);
+    const int* row = table_row(b, a.s);
+    for (int j = threadIdx.x; ok && j < pages; j += blockDim.x) ok = row[j] >= 0 && row[j] < b.n_pages;
+  }
+  ok = __syncthreads_and(ok);
+  if (threadIdx.x == 0) {
+    ok_out[i] = ok ? 1 : 0;
+    if (!ok) report_pages(status);
+  }
+  if (!ok || a.rows == 0) return;
+  const int* row = table_row(b, a.s);
+  int* out = table_row(b, d);
+  for (int j = threadIdx.x; j < pages; j += blockDim.x) {
+    const int p = row[j];
+    out[j] = p;
+    atomicAdd(&b.refs[p], 1);
+  }
+  if (threadIdx.x == 0) {
+    b.start[d] = a.start;
+    b.rows[d] = a.rows;
+  }
+}
+
+// CTA i: slot slots[i] keeps its newest keep[i] rows; pages that hold none of
+// them leave the table row, which moves up and is filled with -1.
+__global__ void __launch_bounds__(128) free_kernel(PageBook b, const int* __restrict__ slots,
+                                                   const int* __restrict__ keep, int n, unsigned int* status) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int i = blockIdx.x;
+  const int s = slots[i];
+  bool ok = s >= 0 && s < b.n_slots;
+  for (int j = threadIdx.x; ok && j < i; j += blockDim.x) ok = slots[j] != s;
+  ok = __syncthreads_and(ok);
+  // Only the entry that names the slot first reads its state, which no other
+  // CTA then writes.
+  Slot a{s, 0, 0, false};
+  if (ok) a = read_slot(b, s);
+  ok = __syncthreads_and(a.ok);
+  if (!ok) {
+    if (threadIdx.x == 0) report_pages(status);
+    return;
+  }
+  const int kept = min(a.rows, max(keep == nullptr ? 0 : keep[i], 0));
+  const int begin = a.start + (a.rows - kept);  // in range: start + rows <= max_pages * page_rows
+  const int pages = ceil_div(static_cast<long long>(a.start) + a.rows, b.page_rows);
+  const int dead = kept > 0 ? begin / b.page_rows : pages;
+  if (threadIdx.x == 0) {
+    b.start[a.s] = kept > 0 ? begin % b.page_rows : 0;
+    b.rows[a.s] = kept;
+  }
+  if (dead == 0) return;
+  int* row = table_row(b, a.s);
+  bool bad = false;
+  for (int j = threadIdx.x; j < dead; j += blockDim.x) {
+    const int p = row[j];
+    if (p >= 0 && p < b.n_pages)
+      atomicSub(&b.refs[p], 1);
+    else
+      bad = true;
+  }
+  if (bad) report_pages(status);
+  // The row moves up `dead` places, a block of entries at a time: a block's
+  // entries are read before any is written, and lie above every entry written
+  // before it.
+  for (int j0 = 0; j0 < pages; j0 += blockDim.x) {
+    const int j = j0 + threadIdx.x;
+    const int p = j + dead < pages ? row[j + dead] : -1;
+    __syncthreads();
+    if (j < pages) row[j] = p;
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------
+// One CTA: the live pages are counted (N), then the k-th live page at or
+// past N and the k-th free page before N are paired by rank.
+__global__ void __launch_bounds__(kBlock) compact_kernel(PageBook b, int* __restrict__ new_id,
+                                                         int* __restrict__ copy_src, int* __restrict__ copy_dst,
+                                                         int* __restrict__ count) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  __shared__ int warp_sums[32];
+  const int cap = b.n_pages + 1;
+  constexpr int kTile = kBlock * kPerThread;
+  int live = 0;
+  for (int base = 0; base < b.n_pages; base += kTile) {
+    const int past = max(0, min(kPerThread, base + static_cast<int>(threadIdx.x + 1) * kPerThread - b.n_pages));
+    block_scan(__popc(used_mask(b, base)) - past, cap, warp_sums);
+    live += warp_sums[31];
+  }
+  int holes = 0, moved = 0;
+  for (int base = 0; base < b.n_pages; base += kTile) {
+    const int p0 = base + threadIdx.x * kPerThread;
+    const uint32_t used = used_mask(b, base);
+    uint32_t hole = 0, move = 0;
+#pragma unroll
+    for (int q = 0; q < kPerThread; ++q) {
+      const int p = p0 + q;
+      if (p >= b.n_pages) continue;
+      const bool u = used >> q & 1;
+      hole |= (!u && p < live ? 1u : 0u) << q;
+      move |= (u && p >= live ? 1u : 0u) << q;
+      if (!u || p < live) new_id[p] = u ? p : -1;
+    }
+    int h = holes + block_scan(__popc(hole), cap, warp_sums) - __popc(hole);
+    holes += warp_sums[31];
+    int m = moved + block_scan(__popc(move), cap, warp_sums) - __popc(move);
+    moved += warp_sums[31];
+    for (; hole != 0; hole &= hole - 1) copy_dst[h++] = p0 + __ffs(hole) - 1;
+    for (; move != 0; move &= move - 1) copy_src[m++] = p0 + __ffs(move) - 1;
+  }
+  __syncthreads();
+  // As many holes before N as live pages past it: N pages are live.
+  for (int k = threadIdx.x; k < b.n_pages; k += kBlock) {
+    if (k < moved) {
+      const int a = copy_src[k], z = copy_dst[k];
+      new_id[a] = z;
+      b.refs[z] = b.refs[a];
+      b.refs[a] = 0;
+    } else {
+      copy_src[k] = copy_dst[k] = -1;
+    }
+  }
+  if (threadIdx.x == 0) *count = moved;
+}
+
+// Table entries to their pages' new ids.
+__global__ void __launch_bounds__(256) rename_kernel(PageBook b, const int* __restrict__ new_id,
+                                                     unsigned int* status) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const long long total = static_cast<long long>(b.n_slots) * b.max_pages;
+  for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < total;
+       e += static_cast<long long>(gridDim.x) * 256) {
+    const int p = b.table[e];
+    if (p < 0) continue;
+    if (p < b.n_pages)
+      b.table[e] = new_id[p];
+    else
+      report_pages(status);
+  }
+}
+
+unsigned grid_for(long long work, long long most) {
+  return static_cast<unsigned>(work < 1 ? 1 : (work < most ? work : most));
+}
+
+// Calls f with a vector type that divides `bits` (addresses and sizes or'ed).
+template <typename F>
+cudaError_t by_vector(uintptr_t bits, F f) {
+  if (bits % 16 == 0) return f(uint4());
+  if (bits % 4 == 0) return f(uint32_t());
+  return f(uint16_t());
+}
+
+}  // namespace
+
+cudaError_t launch_pages_reserve(const PageBook& b, const int* slots, const int* cu, int n, int* granted,
+                                 int* copy_src, int* copy_dst, unsigned int* status, cudaStream_t stream) {
+  const size_t smem = (static_cast<size_t>(b.n_slots) + n) * sizeof(int);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               2 * kMaxSlots * static_cast<int>(sizeof(int)));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(reserve_kernel, dim3(1), dim3(kBlock), smem, stream, b, slots, cu, n, granted, copy_src,
+                          copy_dst, status);
+}
+
+cudaError_t launch_pages_append(const PageBook& b, void* kp, void* vp, int H, int D, int elem, const int* slots,
+                                const int* cu, int n, const int* granted, const int* copy_src, const int* copy_dst,
+                                const void* kn, const void* vn, int T, unsigned int* status, cudaStream_t stream) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(kp) | reinterpret_cast<uintptr_t>(vp) |
+                         reinterpret_cast<uintptr_t>(kn) | reinterpret_cast<uintptr_t>(vn) |
+                         static_cast<uintptr_t>(D * elem);
+  return by_vector(bits, [&](auto v) {
+    using V = decltype(v);
+    const int dv = D * elem / static_cast<int>(sizeof(V));
+    // CTAs of an entry: by its mean share of the new rows and half a page of
+    // copied ones, within about 8 CTAs per SM over all entries.
+    const long long rows = T / n + 1 + (copy_src != nullptr ? b.page_rows / 2 : 0);
+    const long long most = (152 * 8 + n - 1) / n;
+    const dim3 grid(grid_for((rows * H * dv + 1023) / 1024, most), static_cast<unsigned>(n));
+    return launch_dependent(append_kernel<V>, grid, dim3(256), 0, stream, b, static_cast<V*>(kp),
+                            static_cast<V*>(vp), H, dv, slots, cu, granted, copy_src, copy_dst,
+                            static_cast<const V*>(kn), static_cast<const V*>(vn), T, status);
+  });
+}
+
+cudaError_t launch_pages_copy(void* kp, void* vp, int n_pages, long long page_bytes, const int* src, const int* dst,
+                              int n, unsigned int* status, cudaStream_t stream) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(kp) | reinterpret_cast<uintptr_t>(vp) |
+                         static_cast<uintptr_t>(page_bytes);
+  return by_vector(bits, [&](auto v) {
+    using V = decltype(v);
+    const long long vecs = page_bytes / static_cast<long long>(sizeof(V));
+    const long long chunks = 2 * ((vecs + 1023) / 1024) * n;
+    return launch_dependent(copy_kernel<V>, dim3(grid_for(chunks, 152 * 8)), dim3(256), 0, stream,
+                            static_cast<V*>(kp), static_cast<V*>(vp), n_pages, vecs, src, dst, n, status);
+  });
+}
+
+cudaError_t launch_pages_fork(const PageBook& b, const int* src, const int* dst, int n, int* ok,
+                              unsigned int* status, cudaStream_t stream) {
+  return launch_dependent(fork_kernel, dim3(n), dim3(128), 0, stream, b, src, dst, n, ok, status);
+}
+
+cudaError_t launch_pages_free(const PageBook& b, const int* slots, const int* keep, int n, unsigned int* status,
+                              cudaStream_t stream) {
+  return launch_dependent(free_kernel, dim3(n), dim3(128), 0, stream, b, slots, keep, n, status);
+}
+
+cudaError_t launch_pages_compact(const PageBook& b, int* new_id, int* copy_src, int* copy_dst, int* count,
+                                 unsigned int* status, cudaStream_t stream) {
+  cudaError_t e =
+      launch_dependent(compact_kernel, dim3(1), dim3(kBlock), 0, stream, b, new_id, copy_src, copy_dst, count);
+  if (e != cudaSuccess) return e;
+  const long long entries = static_cast<long long>(b.n_slots) * b.max_pages;
+  return launch_dependent(rename_kernel, dim3(grid_for((entries + 255) / 256, 152 * 8)), dim3(256), 0, stream, b,
+                          static_cast<const int*>(new_id), status);
+}
+
+}  // namespace txl

@@ -12,6 +12,7 @@ namespace txl {
 
 // Bits of the device status word.
 constexpr unsigned int kStatusTimeoutBit = 1u;  // a bounded wait expired
+constexpr unsigned int kStatusPagesBit = 2u;    // a paged call refused an entry (pages.cu)
 
 struct WaitCtl {
   unsigned int* status;           // device status word
