@@ -779,6 +779,16 @@ TXL_API int txl_debug_unit_plan(int B, int H, int W, int M, int ctas, int* table
  * Returns 0, -1 for bad arguments, -2 if a capacity is short. */
 TXL_API int txl_debug_bwd_pairs_work(int B, int W, int M, int H, int split_qt, int* n_ctas, int* n_tiles,
                                      int* ctas, int cap_ctas, int* tiles, int cap_tiles);
+/* Test hook, host only: how txl_relattn_forward_paged divides its work over
+ * `ctas` CTAs.  kind 0: the decode kernel (entries of up to 4 tokens; key
+ * steps of 64 rows at D = 64, 32 at D = 128), 1: the kernel for longer
+ * entries (tiles of 128 queries, key steps of 64 rows).  n sequences of rows[i] live
+ * rows after start[i] dead ones, n_new[i] of them new.  Writes rows (CTA,
+ * sequence, head, query tile, first key step, key steps, CTA of the unit's
+ * first piece, index of this piece, pieces, place in the workspace) to out
+ * [cap][10].  Returns their number, -1 if cap is short, -2 for bad arguments. */
+TXL_API int txl_debug_paged_pieces(int kind, int D, int H, int n, const int* start, const int* rows, const int* n_new,
+                                   int ctas, int* out, int cap);
 
 #ifdef __cplusplus
 }

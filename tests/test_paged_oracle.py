@@ -241,3 +241,54 @@ def test_binding_refuses(lib):
         lib.txl_pages_free(dict(book, start=z(3)), 16, z(1))
     with pytest.raises(ValueError):
         lib.txl_pages_copy(torch.zeros(8, 1, 16, 4), torch.zeros(8, 1, 16, 5), z(1), z(1))
+
+
+def steps(start, rows, n, first, count, BK):
+    """Key steps that queries first .. first + count - 1 of n can see."""
+    x = start + rows - n + min(first + count, n) - 1
+    return [start // BK] if x < start else list(range(start // BK, x // BK + 1))
+
+
+@pytest.mark.parametrize("kind,D", [(0, 64), (0, 128), (1, 64)])
+def test_every_step_has_one_cta(lib, kind, D):
+    """The division of the paged attention: every key step of every unit on one CTA, the pieces of a unit numbered in
+    key order on consecutive CTAs, their places distinct, and no CTA with much more than its share."""
+    rng = np.random.default_rng(kind + D)
+    BK = 32 if kind == 0 and D == 128 else 64
+    for trial in range(120):
+        n = int(rng.integers(1, [2, 5, 60][trial % 3] + 1))
+        H = int(rng.integers(1, 9))
+        start = rng.integers(0, [1, 16, 1024][trial % 3], n)
+        rows = (10 ** rng.uniform(0, 4.5, n)).astype(int) * (rng.random(n) > 0.1)
+        new = rng.integers(1, 5, n) if kind == 0 else rng.integers(5, 700, n)
+        ctas = int(rng.choice([1, 7, 152, 304]))
+        got = lib.txl_debug_paged_pieces(kind, D, H, start, rows, new, ctas)
+        assert (np.diff(got[:, 0]) >= 0).all() and got[:, 0].max() < ctas
+        units, places, load = {}, set(), np.zeros(ctas)
+        for c, i, h, qt, t0, nks, first, index, pieces, place in got.tolist():
+            assert nks > 0 and first + index == c and 0 <= index < pieces
+            units.setdefault((i, h, qt), []).append((index, t0, nks, pieces))
+            if pieces > 1:
+                assert place not in places and place // 2 == c
+                places.add(place)
+            load[c] += 2 * nks + 3
+        count = {}
+        for (i, h, qt), p in units.items():
+            want = steps(start[i], rows[i], new[i], 128 * qt if kind else 0, 128 if kind else 4, BK)
+            assert [x[0] for x in p] == list(range(p[0][3]))
+            assert [t for _, t0, nks, _ in p for t in range(t0, t0 + nks)] == want
+            count[i] = count.get(i, 0) + 1
+            first_pieces = [c for c, *r in got.tolist() if tuple(r[:3]) == (i, h, qt)] if n < 4 else []
+            assert first_pieces == sorted(set(first_pieces))
+        for i in range(n):
+            assert count[i] == H * (-(-int(new[i]) // 128) if kind else 1)
+        # a CTA's range, a step more at its end, and what a unit costs besides its steps at each end
+        whole = sum(2 * x[2] for p in units.values() for x in p) + 3 * len(units)
+        assert load.max() <= whole / min(ctas, max(1, whole // 4)) + 2 + 2 * 3
+
+
+def test_one_split_unit_starts_per_cta(lib):
+    """The merge counters: no CTA has the first piece of two split units."""
+    got = lib.txl_debug_paged_pieces(0, 64, 16, [3] * 40, list(range(100, 4100, 100)), [1] * 40, 304)
+    firsts = [c for c, i, h, qt, t0, nks, first, index, pieces, place in got.tolist() if pieces > 1 and index == 0]
+    assert len(firsts) == len(set(firsts)) and len(firsts) > 100

@@ -35,6 +35,7 @@ __all__ = [
     "txl_debug_unit_plan",
     "txl_debug_attention_split",
     "txl_debug_attention_items",
+    "txl_debug_paged_pieces",
 ]
 
 TXL_F32 = 0
@@ -151,6 +152,8 @@ lib.txl_debug_attention_split.argtypes = [_i, _i, _i, _i, _i]
 lib.txl_debug_attention_split.restype = _i
 lib.txl_debug_attention_items.argtypes = [_i, _i, _i, _i, _i, _p, _i, ctypes.POINTER(_i)]
 lib.txl_debug_attention_items.restype = _i
+lib.txl_debug_paged_pieces.argtypes = [_i, _i, _i, _i, _p, _p, _p, _i, _p, _i]
+lib.txl_debug_paged_pieces.restype = _i
 
 
 class TxlError(RuntimeError):
@@ -850,3 +853,20 @@ def txl_debug_attention_items(B, H, W, M, nsplit):
     if lib.txl_debug_attention_items(*args, items.ctypes.data, n.value, ctypes.byref(n)) != 0:
         raise TxlError(1, "txl_debug_attention_items")
     return items
+
+
+def txl_debug_paged_pieces(kind, D, H, start, rows, n_new, ctas):
+    """Test hook (host only): the paged attention's division over `ctas` CTAs,
+    an int32 array of rows (CTA, sequence, head, query tile, first key step,
+    key steps, first CTA, index, pieces, place); kind 0: the decode kernel, 1:
+    the kernel for longer entries."""
+    import numpy as np
+
+    s, r, m = (np.ascontiguousarray(x, np.int32) for x in (start, rows, n_new))
+    tiles = sum(-(-int(x) // 128) for x in m) if kind else len(m)
+    out = np.zeros((int(H) * tiles + int(ctas) + 1, 10), np.int32)
+    n = lib.txl_debug_paged_pieces(int(kind), int(D), int(H), len(s), s.ctypes.data, r.ctypes.data, m.ctypes.data,
+                                   int(ctas), out.ctypes.data, out.shape[0])
+    if n < 0:
+        raise TxlError(1, "txl_debug_paged_pieces")
+    return out[:n]

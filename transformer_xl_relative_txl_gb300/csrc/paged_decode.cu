@@ -1,0 +1,461 @@
+// Relative attention of a few new tokens per sequence (up to 4) over a paged
+// memory, bf16 storage, head dimension 64 or 128.
+//
+//   s[t,j] = scale * ((q_t + u) . k_j + (q_t + v) . r_{m+t-j}),  j <= m + t
+//
+// Bound by reading K and V once: 2 * 2 D bytes per (sequence, head, row), and
+// about 6 D flops per query on them, far below what a tensor core tile of 128
+// queries would need to pay.  So the kernel's care is the loads: a producer
+// warp keeps NS key tiles of K, V and r in flight per CTA by TMA (two CTAs per
+// SM), straight from the pages, and four warps consume whole tiles in turn,
+// each with a softmax state of its own; they meet only at the end of a unit.
+//
+// The products run as mma.sync m16n8k16 with the long operand on the M side:
+// S^T[keys x 8] = K [keys x D] Q^T, O^T[D x 8] += V^T P.  The 8 columns hold
+// 4 queries as two bf16 parts each, x = hi + lo: (q + u) and (q + v), scaled
+// in fp32, and the weights keep 16 bits of significand that way, at no cost,
+// since the columns are there.  Adding the two columns of a query is an add
+// of two accumulators of one thread.
+//
+// The distance term needs no shift in registers: key c of a tile meets row
+// BK-1-c + t of the tile of r that starts at distance m - j0 - (BK-1), so
+// query t's rows of r are addressed upside down by ldmatrix, and the product
+// accumulates on top of the content term; the other queries' columns of the
+// right-hand side are zero for it.
+#include <cmath>
+#include <cstdint>
+
+#include "paged_plan.cuh"
+#include "pdl.cuh"
+#include "relattn_tc_common.cuh"
+#include "txl_device.cuh"
+#include "txl_internal.h"
+
+namespace txl {
+namespace {
+
+constexpr int kWarps = 4;  // consumers
+constexpr int kThreads = 32 * (kWarps + 1);
+
+template <int D>
+struct Cfg {
+  static constexpr int BK = D == 64 ? 64 : 32;  // rows of a key tile: 8 KB either way
+  static constexpr int NS = D == 64 ? 4 : 3;
+  static constexpr int BR = BK + 8;  // rows of r: 3 more than a tile for the later queries
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTile = BK * D * 2, kTileR = BR * D * 2;
+  static constexpr int kStage = 2 * kTile + kTileR;
+  static constexpr int kRow = D + 2;  // a query's partial result: o, m, l
+  static constexpr int kOffPart = NS * kStage;
+  static constexpr int kOffBar = kOffPart + 2 * kWarps * kDecodeRows * kRow * 4;
+  static constexpr int kSmem = kOffBar + 256 + 1024;
+  using Walk = PlanWalk<DecodeCost, BK, 0>;  // DecodeWalk64, DecodeWalk32
+};
+
+struct Params {
+  PageBook book;
+  const __nv_bfloat16* q;
+  const float* bias_u;
+  const float* bias_v;
+  void* o;
+  float* lse;
+  int T, H, n_r;
+  float scale_log2e;
+  const PlanHead* head;
+  const PlanSeq* seqs;
+  const int* starts;
+  int* counters;
+  float* part;
+  unsigned int* status;
+  unsigned long long wait_ns;
+};
+
+struct Bars {
+  uint64_t full[4], empty[4], joined;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block too large");
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The bf16 part `lo` (0: the value rounded, 1: what the rounding left) of a
+// and b, packed.
+__device__ __forceinline__ uint32_t split_part(float a, float b, bool lo) {
+  const uint32_t hi = pack_bf16x2(a, b);
+  return lo ? pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi)) : hi;
+}
+
+template <int D, bool O_BF16>
+__global__ void __launch_bounds__(kThreads, kDecodePerSm)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_r, const Params p) {
+  using C = Cfg<D>;
+  constexpr int BK = C::BK, NS = C::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* joint = reinterpret_cast<float*>(smem + C::kOffPart);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->joined, kWarps);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const uint64_t wait_ns = p.wait_ns;
+  typename C::Walk w;
+  bool more = w.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+
+  if (warp == kWarps) {
+    // ============================== producer ===============================
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_r);
+    }
+    const int P = p.book.page_rows;
+    const int box = min(P, BK), boxes = BK / box;  // a tile is `boxes` boxes of rows
+    uint32_t g = 0;
+    bool ok = true, bad = false;
+    for (; ok && more; more = w.next()) {
+      const int* row = p.book.table + static_cast<size_t>(w.s.slot) * p.book.max_pages;
+      const int last = w.s.start + w.s.rows - 1;
+      const int m = w.s.start + w.s.rows - w.s.n;
+      int id = -1, id0 = -32;  // this lane's page of the boxes from id0 on
+      for (int t = w.p.t0; t < w.p.t0 + w.p.nks; ++t, ++g) {
+        if (t * boxes - id0 + boxes > 32) {  // the next 32 boxes' pages at once (boxes divides 32)
+          id0 = t * boxes;
+          const long long x = static_cast<long long>(id0 + lane) * box;
+          id = -1;
+          if (x <= last && x + box > w.s.start) {
+            id = row[x / P];
+            if (id < 0 || id >= p.book.n_pages) bad = true, id = p.book.n_pages;  // zero rows, nothing read
+          }
+        }
+        const int s = g % NS;
+        ok = warp_wait(&bars->empty[s], ((g / NS) & 1) ^ 1, wait_ns, abort);
+        if (!ok) break;
+        uint8_t* stage = smem + s * C::kStage;
+        const uint32_t mask = __ballot_sync(0xffffffffu, id >= 0) >> (t * boxes - id0) & ((1u << boxes) - 1);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&bars->full[s], C::kTileR + 2 * static_cast<uint32_t>(__popc(mask)) * box * D * 2);
+        for (int y = 0; y < boxes; ++y) {
+          const int page = __shfl_sync(0xffffffffu, id, t * boxes - id0 + y);
+          if (lane != 0 || page < 0) continue;
+          const int x = (t * BK + y * box) % P;
+#pragma unroll
+          for (int c = 0; c < C::kBoxes; ++c) {
+            uint8_t* at = stage + c * BK * 128 + y * box * 128;
+            tma_load_4d(at, &tm_k, &bars->full[s], c * 64, x, w.h, page);
+            tma_load_4d(at + C::kTile, &tm_v, &bars->full[s], c * 64, x, w.h, page);
+          }
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int c = 0; c < C::kBoxes; ++c)
+            tma_load_3d(stage + 2 * C::kTile + c * C::BR * 128, &tm_r, &bars->full[s], c * 64, w.h,
+                        m - t * BK - (BK - 1));
+        }
+        __syncwarp();
+      }
+    }
+    if (bad) atomicOr(p.status, kStatusPagesBit);
+    if (!ok && lane == 0) report_timeout(abort, p.status);
+    // This warp's copies land before the CTA may exit.
+    for (uint32_t s = 0; s < NS && s < g; ++s) {
+      const uint32_t n = s + ((g - 1 - s) / NS) * NS;
+      mbar_wait_own(&bars->full[s], (n / NS) & 1, wait_ns);
+    }
+    return;
+  }
+
+  // =============================== consumers ================================
+  const int col_q = lane >> 3, part = lane >> 2 & 1;  // query and part of this lane's right-hand column
+  const int my_q = lane & 3;                          // query of this lane's accumulators
+  uint32_t g = 0, units = 0;
+  bool ok = true;
+  for (; ok && more; more = w.next(), ++units) {
+    const int n = w.s.n, h = w.h;
+    // (q + u), (q + v) in log2 units, as right-hand fragments.
+    uint32_t qu[D / 8], qv[D / 8];
+    {
+      const __nv_bfloat16* q = p.q + (static_cast<size_t>(w.s.tok0 + min(col_q, n - 1)) * p.H + h) * D;
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        const int d = e * 8 + 2 * (lane & 3);
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d);
+        const float f = col_q < n ? p.scale_log2e : 0.f;
+        const float x0 = bf16_lo(x), x1 = bf16_hi(x);
+        const float* bu = p.bias_u + h * D + d;
+        const float* bv = p.bias_v + h * D + d;
+        qu[e] = col_q < n ? split_part((x0 + bu[0]) * f, (x1 + bu[1]) * f, part) : 0u;
+        qv[e] = col_q < n ? split_part((x0 + bv[0]) * f, (x1 + bv[1]) * f, part) : 0u;
+      }
+    }
+    const int last = w.s.start + w.s.rows - 1;
+    const int lim = w.s.start + w.s.rows - n + my_q;  // last row this lane's query sees
+    float m_run = -INFINITY, l_run = 0.f;
+    float acc[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) acc[e][y] = 0.f;
+
+    // This warp's tiles: those that the CTA loaded as number g with
+    // g % kWarps == warp.
+    const uint32_t g0 = g;
+    g += w.p.nks;
+    for (uint32_t x = g0 + ((warp - g0) & (kWarps - 1)); x < g; x += kWarps) {
+      const int row0 = (w.p.t0 + static_cast<int>(x - g0)) * BK;
+      const int s = x % NS;
+      ok = warp_wait(&bars->full[s], (x / NS) & 1, wait_ns, abort);
+      if (!ok) break;
+      const uint32_t sk = smem_u32(smem + s * C::kStage), sv = sk + C::kTile, sr = sk + 2 * C::kTile;
+      const int r16 = lane & 15, half = lane >> 4;
+      float z[BK / 16][4];
+#pragma unroll
+      for (int y = 0; y < BK / 16; ++y) {
+        z[y][0] = z[y][1] = z[y][2] = z[y][3] = 0.f;
+        const int rk = 16 * y + r16;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          uint32_t a[4];
+          ldsm4(sk + (e / 4) * BK * 128 + rk * 128 + ((((e % 4) * 2 + half) ^ (rk & 7)) << 4), a);
+          mma16816(z[y], a, qu[2 * e], qu[2 * e + 1]);
+        }
+      }
+      for (int t = 0; t < n; ++t) {
+        const bool mine = col_q == t;
+#pragma unroll
+        for (int y = 0; y < BK / 16; ++y) {
+          const int rr = BK - 1 - (16 * y + r16) + t;
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            uint32_t a[4];
+            ldsm4(sr + (e / 4) * C::BR * 128 + rr * 128 + ((((e % 4) * 2 + half) ^ (rr & 7)) << 4), a);
+            mma16816(z[y], a, mine ? qv[2 * e] : 0u, mine ? qv[2 * e + 1] : 0u);
+          }
+        }
+      }
+      // Scores of query my_q: rows row0 + 16 y + lane / 4 (+ 8).
+      const bool edge = row0 < w.s.start || row0 + BK - 1 > last - (n - 1);
+      float sc[BK / 16][2];
+      float best = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < BK / 16; ++y)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float f = z[y][2 * u] + z[y][2 * u + 1];
+          if (edge) {
+            const int row = row0 + 16 * y + 8 * u + (lane >> 2);
+            f = row >= w.s.start && row <= lim ? f : -INFINITY;
+          }
+          sc[y][u] = f;
+          best = fmaxf(best, f);
+        }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+      const float m_new = fmaxf(m_run, best);
+      const float m_eff = m_new == -INFINITY ? 0.f : m_new;
+      if (__any_sync(0xffffffffu, m_new > m_run)) {
+        const float f = ex2(m_run - m_eff);  // 2^-inf = 0 before the first visible row
+        l_run *= f;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) acc[e][y] *= f;
+        m_run = m_new;
+      }
+      uint32_t pt[BK / 16][2];  // weights as right-hand fragments
+#pragma unroll
+      for (int y = 0; y < BK / 16; ++y)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float f = ex2(sc[y][u] - m_eff);
+          l_run += f;
+          const float hi = __bfloat162float(__float2bfloat16(f));
+          pt[y][u] = transpose8x8(pack_bf16x2(hi, f - hi));
+        }
+#pragma unroll
+      for (int y = 0; y < BK / 16; ++y) {
+        // Rows outside [start, last] hold leftovers: their values leave the
+        // product as zeros, since 0 times NaN is not 0.
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (edge) {
+          auto live = [&](int row) { return row >= w.s.start && row <= last; };
+          const int row = row0 + 16 * y + 2 * (lane & 3);
+          keep0 = (live(row) ? 0xffffu : 0u) | (live(row + 1) ? 0xffff0000u : 0u);
+          keep1 = (live(row + 8) ? 0xffffu : 0u) | (live(row + 9) ? 0xffff0000u : 0u);
+        }
+        const int rv = 16 * y + (half << 3) + (lane & 7);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          uint32_t a[4];
+          ldsm4_t(sv + (e / 4) * BK * 128 + rv * 128 + ((((e % 4) * 2 + (lane >> 3 & 1)) ^ (rv & 7)) << 4), a);
+          a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
+          mma16816(acc[e], a, pt[y][0], pt[y][1]);
+        }
+      }
+      warp_arrive(&bars->empty[s]);
+    }
+    if (!ok) break;
+
+    // The warps' results meet: warp t joins query t.
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, d);
+    float* mine = joint + (((units & 1) * kWarps + warp) * kDecodeRows + my_q) * C::kRow;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+      mine[16 * e + (lane >> 2)] = acc[e][0] + acc[e][1];
+      mine[16 * e + 8 + (lane >> 2)] = acc[e][2] + acc[e][3];
+    }
+    if (lane < 4) mine[D] = m_run, mine[D + 1] = l_run;
+    warp_arrive(&bars->joined);
+    ok = warp_wait(&bars->joined, units & 1, wait_ns, abort);
+    if (!ok) break;
+    if (warp >= n) continue;
+    const float* from = joint + ((units & 1) * kWarps * kDecodeRows + warp) * C::kRow;
+    constexpr int kStride = kDecodeRows * C::kRow;
+    float o[D / 32], m_all = -INFINITY, l_all = 0.f;
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) m_all = fmaxf(m_all, from[y * kStride + D]);
+    const float m_eff = m_all == -INFINITY ? 0.f : m_all;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) {
+      const float f = ex2(from[y * kStride + D] - m_eff);
+      l_all += f * from[y * kStride + D + 1];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[y * kStride + e * 32 + lane], o[e]);
+    }
+    if (w.p.pieces > 1) {
+      // A piece's result goes to the workspace; the last of the unit's pieces
+      // to arrive joins them in order, so the result does not depend on which
+      // it is.
+      float* out = p.part + (static_cast<size_t>(plan_place(blockIdx.x, w.p.index)) * kDecodeRows + warp) * C::kRow;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) __stcg(out + e * 32 + lane, o[e]);
+      if (lane == 0) __stcg(out + D, m_all), __stcg(out + D + 1, l_all);
+      __threadfence();
+      __syncwarp();
+      int arrived = 0;
+      if (lane == 0) arrived = atomicAdd(p.counters + w.p.first * 4 + warp, 1);
+      if (__shfl_sync(0xffffffffu, arrived, 0) != w.p.pieces - 1) continue;
+      __threadfence();
+      m_all = -INFINITY;
+      for (int y = 0; y < w.p.pieces; ++y)
+        m_all = fmaxf(m_all, __ldcg(p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + warp) *
+                                                 C::kRow + D));
+      const float m_eff2 = m_all == -INFINITY ? 0.f : m_all;
+      l_all = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+      for (int y = 0; y < w.p.pieces; ++y) {
+        const float* in = p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + warp) * C::kRow;
+        const float f = ex2(__ldcg(in + D) - m_eff2);
+        l_all += f * __ldcg(in + D + 1);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, __ldcg(in + e * 32 + lane), o[e]);
+      }
+    }
+    const bool none = m_all == -INFINITY;
+    const float inv = none ? 0.f : 1.f / l_all;
+    const size_t at = (static_cast<size_t>(w.s.tok0 + warp) * p.H + h) * D;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      if (O_BF16)
+        static_cast<__nv_bfloat16*>(p.o)[at + e * 32 + lane] = __float2bfloat16(o[e] * inv);
+      else
+        static_cast<float*>(p.o)[at + e * 32 + lane] = o[e] * inv;
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[static_cast<size_t>(h) * p.T + w.s.tok0 + warp] =
+          none ? -INFINITY : (m_all + log2f(l_all)) * 0.69314718055994531f;
+  }
+  if (!ok && lane == 0) report_timeout(abort, p.status);
+}
+
+template <int D, bool O_BF16>
+cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc, cudaStream_t stream) {
+  using C = Cfg<D>;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = api_tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const PageBook& b = a.book;
+  CUtensorMap tm_k, tm_v, tm_r;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  auto enc = [&](CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  {
+    const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(b.page_rows), static_cast<cuuint64_t>(a.H),
+                                static_cast<cuuint64_t>(b.n_pages)};
+    const cuuint64_t strides[3] = {D * 2, static_cast<cuuint64_t>(b.page_rows) * D * 2,
+                                   static_cast<cuuint64_t>(a.H) * b.page_rows * D * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(b.page_rows < C::BK ? b.page_rows : C::BK), 1, 1};
+    if (!enc(&tm_k, a.kp, 4, dims, strides, box) || !enc(&tm_v, a.vp, 4, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(a.n_r)};
+    const cuuint64_t strides[2] = {D * 2, static_cast<cuuint64_t>(a.H) * D * 2};
+    const cuuint32_t box[3] = {64, 1, C::BR};
+    if (!enc(&tm_r, a.r, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  Params p{b, static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H, a.n_r,
+           a.scale * 1.4426950408889634f, s.heads, s.seqs[0], s.starts[0], s.counters[0], s.part[0], wc.status,
+           wc.limit_ns};
+  auto kern = paged_decode_kernel<D, O_BF16>;
+  static unsigned configured = 0;  // one bit per device ordinal < 32
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 32 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1u << dev))) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess)
+      return e;
+    if (dev < 32) __atomic_fetch_or(&configured, 1u << dev, __ATOMIC_RELEASE);
+  }
+  return launch_dependent(kern, dim3(kDecodePerSm * sms), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, tm_r, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc,
+                                cudaStream_t stream) {
+  if (a.D == 64) return a.o_bf16 ? launch<64, true>(a, s, sms, wc, stream) : launch<64, false>(a, s, sms, wc, stream);
+  return a.o_bf16 ? launch<128, true>(a, s, sms, wc, stream) : launch<128, false>(a, s, sms, wc, stream);
+}
+
+}  // namespace txl

@@ -192,9 +192,4 @@ cudaError_t launch_paged_simt(const PagedAttn& a, unsigned int* status, cudaStre
                   : launch<__nv_bfloat16, float>(a, status, stream);
 }
 
-size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16) {
-  (void)n, (void)T, (void)H, (void)D, (void)bf16;
-  return 256;
-}
-
 }  // namespace txl

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "paged_plan.cuh"
 #include "pages.h"
 #include "txl_relattn.h"
 
@@ -230,9 +231,19 @@ int txl_relattn_forward_paged(const void* q, const void* k_pages, const void* v_
   if (aliased(outs, ins)) return TXL_ERR_ALIAS;
   txl::PagedAttn a{b, q, k_pages, v_pages, r, bias_u, bias_v, o, lse, slots, cu, n, T, max_new, H, D, n_r, scale,
                    dtype == TXL_BF16, o_dtype == TXL_BF16, workspace};
-  unsigned int* status;
-  if (status_word(&status) != TXL_OK) return TXL_ERR_CUDA;
-  return from_cuda(txl::launch_paged_simt(a, status, stream));
+  txl::WaitCtl wc;
+  if (txl::api_wait_ctl(&wc) != TXL_OK) return TXL_ERR_CUDA;
+  return from_cuda(txl::launch_paged_attn(a, wc, stream));
+}
+
+int txl_debug_paged_pieces(int kind, int D, int H, int n, const int* start, const int* rows, const int* n_new,
+                           int ctas, int* out, int cap) {
+  if (kind < 0 || kind > 1 || (D != 64 && D != 128) || H <= 0 || n < 0 || ctas <= 0 || cap < 0 || start == nullptr ||
+      rows == nullptr || n_new == nullptr || out == nullptr)
+    return -2;
+  for (int i = 0; i < n; ++i)
+    if (start[i] < 0 || rows[i] < 0 || n_new[i] <= 0) return -2;
+  return txl::paged_pieces(kind, D, H, n, start, rows, n_new, ctas, out, cap);
 }
 
 }  // extern "C"
