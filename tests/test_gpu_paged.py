@@ -124,6 +124,10 @@ ONE_TOKEN = [
     (32, 8, 128, [(a, 1 + 37 * a) for a in range(12)]),
     (1024, 2, 64, [(1000, 400), (0, 1024), (512, 1)]),
     (16, 16, 64, [(i % 16, 40 + 3 * i) for i in range(33)]),
+    # many key tiles per CTA: each stage of the ring is filled over and over
+    (32, 16, 128, [(i % 32, 2000 + 31 * i) for i in range(16)]),
+    (64, 16, 64, [(i % 64, 4000 + 61 * i) for i in range(16)]),
+    (16, 1, 128, [(7, 5000)]),
 ]
 
 

@@ -1,0 +1,74 @@
+"""The decode kernel's ring of key tiles on a model of mbarrier phases under
+random schedules.
+
+A barrier's wait for a parity returns as soon as the barrier's current phase
+has the other parity, whichever phase that is.  The producer fills stage
+g % NS with tile g once the stage's last tile has been given back, loads land
+some time later; tile g goes to warp g % warps.  A warp that takes a tile must
+find that tile, landed, in the stage."""
+
+import random
+
+import pytest
+
+
+class Bar:
+    def __init__(self):
+        self.phase = 0  # phases completed
+
+    def passes(self, parity):
+        return (self.phase & 1) != parity
+
+
+def run(NS, warps, tiles, rng):
+    """None, or what went wrong."""
+    full, empty = [Bar() for _ in range(NS)], [Bar() for _ in range(NS)]
+    held = [None] * NS       # tile landed in the stage
+    flying = []              # loads in flight
+    made = 0
+    at = list(range(warps))  # next tile of each warp
+    taken = [False] * warps
+    while made < tiles or flying or any(x < tiles for x in at):
+        moves = []
+        if made < tiles and empty[made % NS].passes(((made // NS) & 1) ^ 1):
+            moves.append(("load", made))
+        moves += [("land", g) for g in flying]
+        for w in range(warps):
+            if taken[w]:
+                moves.append(("give", w))
+            elif at[w] < tiles and full[at[w] % NS].passes((at[w] // NS) & 1):
+                moves.append(("take", w))
+        if not moves:
+            return "deadlock"
+        what, x = rng.choice(moves)
+        if what == "load":
+            if any(at[w] % NS == x % NS and taken[w] for w in range(warps)):
+                return "overwritten while read"
+            flying.append(x)
+            made += 1
+        elif what == "land":
+            flying.remove(x)
+            held[x % NS] = x
+            full[x % NS].phase += 1
+        elif what == "take":
+            if held[at[x] % NS] != at[x]:
+                return "another tile"
+            taken[x] = True
+        else:
+            empty[at[x] % NS].phase += 1
+            taken[x] = False
+            at[x] += warps
+    return None
+
+
+@pytest.mark.parametrize("n", [3, 4])
+def test_ring(n):
+    """As many warps as stages (3 at D = 128, 4 at D = 64)."""
+    for seed in range(300):
+        rng = random.Random(seed)
+        assert run(n, n, rng.randint(1, 40), rng) is None
+
+
+def test_a_stage_shared_by_warps_is_caught():
+    """Three stages and four warps: a warp does not see every phase of a stage."""
+    assert any(run(3, 4, 40, random.Random(seed)) for seed in range(300))

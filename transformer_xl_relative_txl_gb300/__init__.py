@@ -417,43 +417,66 @@ def txl_dense(x, W, y, bias=None, relu=False, stream=None):
     return y
 
 
-def _int32(name, t, n=None):
-    """Raises unless t is a contiguous int32 vector (of n entries)."""
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous int32 vector" + ("" if n is None else f" of {n} entries"))
-
-
-def _on_device(*tensors):
-    """Raises unless every tensor lives on the current device, where the call
-    launches."""
+def _vectors(dev, n, *tensors):
+    """Pointers of contiguous int32 vectors of n entries on device dev, where
+    the call launches; None stays None."""
+    out = []
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"expected a contiguous int32 vector of {n} entries")
+        if t.get_device() != dev:
             raise ValueError("tensors must live in the current device's memory")
+        out.append(t.data_ptr())
+    return out
 
 
-def _book(book, page_rows):
+def _tensors(dev, *tensors):
+    """Pointers of contiguous tensors on device dev; None stays None."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError("tensors must live in the current device's memory")
+        out.append(t.data_ptr())
+    return out
+
+
+def _device(t):
+    """Device index of t, which must be the current device: the call launches
+    there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must live in the current device's memory")
+    return dev
+
+
+def _book(dev, book, page_rows):
     """The C struct of a page book: a dict of int32 tensors table [slots,
     max_pages], start and rows [slots], refs [pages]."""
-    table = book["table"]
-    if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
+    table, refs = book["table"], book["refs"]
+    if table.dtype is not torch.int32 or table.dim() != 2:
         raise ValueError("table must be a contiguous int32 [slots, max_pages] tensor")
     n_slots, max_pages = table.shape
-    _int32("start", book["start"], n_slots)
-    _int32("rows", book["rows"], n_slots)
-    _int32("refs", book["refs"])
-    _on_device(table, book["start"], book["rows"], book["refs"])
-    return _PageBook(_ptr(table), _ptr(book["start"]), _ptr(book["rows"]), _ptr(book["refs"]), n_slots, max_pages,
-                     book["refs"].shape[0], int(page_rows))
+    n_pages = refs.numel()
+    ptrs = _tensors(dev, table) + _vectors(dev, n_slots, book["start"], book["rows"]) + _vectors(dev, n_pages, refs)
+    return _PageBook(*ptrs, n_slots, max_pages, n_pages, page_rows)
 
 
-def _pools(k_pages, v_pages, n_pages=None):
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+def _pools(dev, k_pages, v_pages, n_pages=None):
+    """Pointers and shape of the pools."""
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not k_pages.dtype:
         raise ValueError("k_pages, v_pages must be [pages, H, page_rows, D] of one dtype")
-    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
-        raise ValueError("tensors must be contiguous")
-    if n_pages is not None and k_pages.shape[0] != n_pages:
+    if n_pages is not None and shape[0] != n_pages:
         raise ValueError("the pools' pages must be those that refs counts")
-    _on_device(k_pages, v_pages)
+    return *_tensors(dev, k_pages, v_pages), shape
 
 
 def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, stream=None):
@@ -461,88 +484,69 @@ def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, s
     dict of int32 tensors table [slots, max_pages], start, rows [slots], refs
     [pages].  granted, copy_src, copy_dst (int32 [n]) receive the rows granted
     and the pages that txl_pages_append has to copy."""
-    b = _book(book, page_rows)
-    n = slots.shape[0]
-    for name, t, m in (("slots", slots, n), ("cu", cu, n + 1), ("granted", granted, n), ("copy_src", copy_src, n),
-                       ("copy_dst", copy_dst, n)):
-        _int32(name, t, m)
-    _on_device(slots, cu, granted, copy_src, copy_dst)
-    _check(lib.txl_pages_reserve(ctypes.byref(b), _ptr(slots), _ptr(cu), n, _ptr(granted), _ptr(copy_src),
-                                 _ptr(copy_dst), _stream(stream)), "txl_pages_reserve")
+    dev, n = _device(slots), slots.numel()
+    b = _book(dev, book, page_rows)
+    s, g, src, dst = _vectors(dev, n, slots, granted, copy_src, copy_dst)
+    c, = _vectors(dev, n + 1, cu)
+    _check(lib.txl_pages_reserve(ctypes.byref(b), s, c, n, g, src, dst, _stream(stream)), "txl_pages_reserve")
 
 
 def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new, stream=None):
     """Rows cu[i] .. cu[i+1]-1 of k_new, v_new [T, H, D] into the last rows of
     slot slots[i] of the pools [pages, H, page_rows, D], after the copies that
     txl_pages_reserve named (copy_src, copy_dst, or None and None)."""
-    _pools(k_pages, v_pages, book["refs"].shape[0])
-    _, H, P, D = k_pages.shape
-    b = _book(book, P)
-    n = slots.shape[0]
-    for name, t, m in (("slots", slots, n), ("cu", cu, n + 1), ("granted", granted, n)):
-        _int32(name, t, m)
-    if (copy_src is None) != (copy_dst is None):
+    dev, n = _device(slots), slots.numel()
+    kp, vp, (_, H, P, D) = _pools(dev, k_pages, v_pages, book["refs"].numel())
+    b = _book(dev, book, P)
+    s, g, src, dst = _vectors(dev, n, slots, granted, copy_src, copy_dst)
+    c, = _vectors(dev, n + 1, cu)
+    if (src is None) != (dst is None):
         raise ValueError("copy_src and copy_dst come together")
-    if copy_src is not None:
-        _int32("copy_src", copy_src, n)
-        _int32("copy_dst", copy_dst, n)
-    if k_new.dim() != 3 or k_new.shape[1:] != (H, D) or v_new.shape != k_new.shape:
+    T = k_new.shape[0]
+    if k_new.shape != (T, H, D) or v_new.shape != (T, H, D):
         raise ValueError("k_new, v_new must be [T, H, D]")
-    if not (k_new.dtype == v_new.dtype == k_pages.dtype):
+    if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
         raise ValueError("the pools and the new rows share a dtype")
-    if not (k_new.is_contiguous() and v_new.is_contiguous()):
-        raise ValueError("tensors must be contiguous")
-    _on_device(slots, cu, granted, copy_src, copy_dst, k_new, v_new)
-    _check(lib.txl_pages_append(ctypes.byref(b), _ptr(k_pages), _ptr(v_pages), H, D, _ptr(slots), _ptr(cu), n,
-                                _ptr(granted), _ptr(copy_src), _ptr(copy_dst), _ptr(k_new), _ptr(v_new),
-                                k_new.shape[0], _dtype_code(k_pages.dtype), _stream(stream)), "txl_pages_append")
+    kn, vn = _tensors(dev, k_new, v_new)
+    _check(lib.txl_pages_append(ctypes.byref(b), kp, vp, H, D, s, c, n, g, src, dst, kn, vn, T,
+                                _dtype_code(k_pages.dtype), _stream(stream)), "txl_pages_append")
 
 
 def txl_pages_copy(k_pages, v_pages, src, dst, stream=None):
     """Whole pages src[i] -> dst[i] of both pools; pairs with -1 are left out."""
-    _pools(k_pages, v_pages)
-    _int32("src", src)
-    _int32("dst", dst, src.shape[0])
-    _on_device(src, dst)
-    _check(lib.txl_pages_copy(_ptr(k_pages), _ptr(v_pages), k_pages.shape[0], math.prod(k_pages.shape[1:]),
-                              _ptr(src), _ptr(dst), src.shape[0], _dtype_code(k_pages.dtype), _stream(stream)),
+    dev, n = _device(src), src.numel()
+    kp, vp, (N, H, P, D) = _pools(dev, k_pages, v_pages)
+    s, d = _vectors(dev, n, src, dst)
+    _check(lib.txl_pages_copy(kp, vp, N, H * P * D, s, d, n, _dtype_code(k_pages.dtype), _stream(stream)),
            "txl_pages_copy")
 
 
 def txl_pages_fork(book, page_rows, src, dst, ok, stream=None):
     """Empty slot dst[i] shares the pages of slot src[i]; ok (int32 [n])
     receives 1, or 0 where refused."""
-    b = _book(book, page_rows)
-    n = src.shape[0]
-    for name, t in (("src", src), ("dst", dst), ("ok", ok)):
-        _int32(name, t, n)
-    _on_device(src, dst, ok)
-    _check(lib.txl_pages_fork(ctypes.byref(b), _ptr(src), _ptr(dst), n, _ptr(ok), _stream(stream)),
-           "txl_pages_fork")
+    dev, n = _device(src), src.numel()
+    b = _book(dev, book, page_rows)
+    s, d, k = _vectors(dev, n, src, dst, ok)
+    _check(lib.txl_pages_fork(ctypes.byref(b), s, d, n, k, _stream(stream)), "txl_pages_fork")
 
 
 def txl_pages_free(book, page_rows, slots, keep=None, stream=None):
     """Slot slots[i] keeps its newest keep[i] rows (None: none)."""
-    b = _book(book, page_rows)
-    n = slots.shape[0]
-    _int32("slots", slots)
-    if keep is not None:
-        _int32("keep", keep, n)
-    _on_device(slots, keep)
-    _check(lib.txl_pages_free(ctypes.byref(b), _ptr(slots), _ptr(keep), n, _stream(stream)), "txl_pages_free")
+    dev, n = _device(slots), slots.numel()
+    b = _book(dev, book, page_rows)
+    s, k = _vectors(dev, n, slots, keep)
+    _check(lib.txl_pages_free(ctypes.byref(b), s, k, n, _stream(stream)), "txl_pages_free")
 
 
 def txl_pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, stream=None):
     """The live pages get the lowest ids.  new_id, copy_src, copy_dst (int32
     [pages]) and count (int32 [1]) receive the new ids and the moves, which
     txl_pages_copy(k_pages, v_pages, copy_src, copy_dst) then makes."""
-    b = _book(book, page_rows)
-    for name, t, m in (("new_id", new_id, b.n_pages), ("copy_src", copy_src, b.n_pages),
-                       ("copy_dst", copy_dst, b.n_pages), ("count", count, 1)):
-        _int32(name, t, m)
-    _on_device(new_id, copy_src, copy_dst, count)
-    _check(lib.txl_pages_compact(ctypes.byref(b), _ptr(new_id), _ptr(copy_src), _ptr(copy_dst), _ptr(count),
-                                 _stream(stream)), "txl_pages_compact")
+    dev = _device(new_id)
+    b = _book(dev, book, page_rows)
+    ids, s, d = _vectors(dev, b.n_pages, new_id, copy_src, copy_dst)
+    c, = _vectors(dev, 1, count)
+    _check(lib.txl_pages_compact(ctypes.byref(b), ids, s, d, c, _stream(stream)), "txl_pages_compact")
 
 
 def txl_relattn_paged_workspace_bytes(n, T, H, D, dtype):
@@ -558,34 +562,27 @@ def txl_relattn_forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, b
     [H, T] fp32 or None; max_new: the largest number of new rows of an entry
     (T when None); workspace: uint8, txl_relattn_paged_workspace_bytes(...).
     scale defaults to 1/sqrt(D)."""
-    _pools(k_pages, v_pages, book["refs"].shape[0])
-    _, H, P, D = k_pages.shape
-    b = _book(book, P)
-    n = slots.shape[0]
-    _int32("slots", slots)
-    _int32("cu", cu, n + 1)
-    T = q.shape[0]
+    dev, n = _device(slots), slots.numel()
+    kp, vp, (_, H, P, D) = _pools(dev, k_pages, v_pages, book["refs"].numel())
+    b = _book(dev, book, P)
+    s, = _vectors(dev, n, slots)
+    c, = _vectors(dev, n + 1, cu)
+    T, n_r = q.shape[0], r.shape[0]
     if q.shape != (T, H, D) or o.shape != q.shape:
         raise ValueError("q and o must be [T, H, D]")
-    if r.dim() != 3 or r.shape[1:] != (H, D) or bias_u.shape != (H, D) or bias_v.shape != (H, D):
+    if r.shape != (n_r, H, D) or bias_u.shape != (H, D) or bias_v.shape != (H, D):
         raise ValueError("r must be [n_r, H, D]; biases [H, D]")
-    if bias_u.dtype != torch.float32 or bias_v.dtype != torch.float32:
+    if bias_u.dtype is not torch.float32 or bias_v.dtype is not torch.float32:
         raise ValueError("biases are fp32")
-    if not (q.dtype == k_pages.dtype == r.dtype):
+    if q.dtype is not k_pages.dtype or r.dtype is not k_pages.dtype:
         raise ValueError("q, the pools and r share a dtype")
-    if lse is not None and (lse.shape != (H, T) or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != (H, T) or lse.dtype is not torch.float32):
         raise ValueError("lse must be fp32 [H, T]")
-    for t in (q, r, bias_u, bias_v, o, workspace) + ((lse,) if lse is not None else ()):
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-    _on_device(q, slots, cu, r, bias_u, bias_v, o, workspace, lse)
-    if scale is None:
-        scale = D ** -0.5
-    st = lib.txl_relattn_forward_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), ctypes.byref(b), _ptr(slots), _ptr(cu),
-                                       n, T, T if max_new is None else int(max_new), _ptr(r), _ptr(bias_u),
-                                       _ptr(bias_v), _ptr(o), _ptr(lse), H, D, r.shape[0], float(scale),
-                                       _dtype_code(q.dtype), _dtype_code(o.dtype), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    qp, rp, up, vbp, op, lp, wp = _tensors(dev, q, r, bias_u, bias_v, o, lse, workspace)
+    st = lib.txl_relattn_forward_paged(qp, kp, vp, ctypes.byref(b), s, c, n, T, T if max_new is None else max_new, rp,
+                                       up, vbp, op, lp, H, D, n_r, D ** -0.5 if scale is None else scale,
+                                       _dtype_code(q.dtype), _dtype_code(o.dtype), wp, workspace.nbytes,
+                                       _stream(stream))
     _check(st, "txl_relattn_forward_paged")
     return o
 

@@ -7,7 +7,7 @@
 // about 6 D flops per query on them, far below what a tensor core tile of 128
 // queries would need to pay.  So the kernel's care is the loads: a producer
 // warp keeps NS key tiles of K, V and r in flight per CTA by TMA (two CTAs per
-// SM), straight from the pages, and four warps consume whole tiles in turn,
+// SM), straight from the pages, and as many warps consume whole tiles in turn,
 // each with a softmax state of its own; they meet only at the end of a unit.
 //
 // The products run as mma.sync m16n8k16 with the long operand on the M side:
@@ -34,13 +34,17 @@
 namespace txl {
 namespace {
 
-constexpr int kWarps = 4;  // consumers
-constexpr int kThreads = 32 * (kWarps + 1);
-
 template <int D>
 struct Cfg {
   static constexpr int BK = D == 64 ? 64 : 32;  // rows of a key tile: 8 KB either way
+  // Stages, and consumer warps.  Tile g lies in stage g % NS and goes to warp
+  // g % kWarps.  With as many of one as of the other a stage is one warp's for
+  // good, which then sees every phase of the stage's barriers; a warp that
+  // met only some of them could take an old phase of equal parity for the one
+  // it waits for.
   static constexpr int NS = D == 64 ? 4 : 3;
+  static constexpr int kWarps = NS;
+  static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int BR = BK + 8;  // rows of r: 3 more than a tile for the later queries
   static constexpr int kBoxes = D / 64;
   static constexpr int kTile = BK * D * 2, kTileR = BR * D * 2;
@@ -108,11 +112,11 @@ __device__ __forceinline__ uint32_t split_part(float a, float b, bool lo) {
 }
 
 template <int D, bool O_BF16>
-__global__ void __launch_bounds__(kThreads, kDecodePerSm)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_r, const Params p) {
   using C = Cfg<D>;
-  constexpr int BK = C::BK, NS = C::NS;
+  constexpr int BK = C::BK, NS = C::NS, kWarps = C::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* joint = reinterpret_cast<float*>(smem + C::kOffPart);
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kDecodePerSm)
     // g % kWarps == warp.
     const uint32_t g0 = g;
     g += w.p.nks;
-    for (uint32_t x = g0 + ((warp - g0) & (kWarps - 1)); x < g; x += kWarps) {
+    for (uint32_t x = g0 + (warp + kWarps - g0 % kWarps) % kWarps; x < g; x += kWarps) {
       const int row0 = (w.p.t0 + static_cast<int>(x - g0)) * BK;
       const int s = x % NS;
       ok = warp_wait(&bars->full[s], (x / NS) & 1, wait_ns, abort);
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, kDecodePerSm)
     }
     if (!ok) break;
 
-    // The warps' results meet: warp t joins query t.
+    // The warps' results meet; each warp joins a query.
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, d);
     float* mine = joint + (((units & 1) * kWarps + warp) * kDecodeRows + my_q) * C::kRow;
@@ -342,65 +346,66 @@ __global__ void __launch_bounds__(kThreads, kDecodePerSm)
     warp_arrive(&bars->joined);
     ok = warp_wait(&bars->joined, units & 1, wait_ns, abort);
     if (!ok) break;
-    if (warp >= n) continue;
-    const float* from = joint + ((units & 1) * kWarps * kDecodeRows + warp) * C::kRow;
-    constexpr int kStride = kDecodeRows * C::kRow;
-    float o[D / 32], m_all = -INFINITY, l_all = 0.f;
+    for (int t = warp; t < n; t += kWarps) {
+      const float* from = joint + ((units & 1) * kWarps * kDecodeRows + t) * C::kRow;
+      constexpr int kStride = kDecodeRows * C::kRow;
+      float o[D / 32], m_all = -INFINITY, l_all = 0.f;
 #pragma unroll
-    for (int y = 0; y < kWarps; ++y) m_all = fmaxf(m_all, from[y * kStride + D]);
-    const float m_eff = m_all == -INFINITY ? 0.f : m_all;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-#pragma unroll
-    for (int y = 0; y < kWarps; ++y) {
-      const float f = ex2(from[y * kStride + D] - m_eff);
-      l_all += f * from[y * kStride + D + 1];
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[y * kStride + e * 32 + lane], o[e]);
-    }
-    if (w.p.pieces > 1) {
-      // A piece's result goes to the workspace; the last of the unit's pieces
-      // to arrive joins them in order, so the result does not depend on which
-      // it is.
-      float* out = p.part + (static_cast<size_t>(plan_place(blockIdx.x, w.p.index)) * kDecodeRows + warp) * C::kRow;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) __stcg(out + e * 32 + lane, o[e]);
-      if (lane == 0) __stcg(out + D, m_all), __stcg(out + D + 1, l_all);
-      __threadfence();
-      __syncwarp();
-      int arrived = 0;
-      if (lane == 0) arrived = atomicAdd(p.counters + w.p.first * 4 + warp, 1);
-      if (__shfl_sync(0xffffffffu, arrived, 0) != w.p.pieces - 1) continue;
-      __threadfence();
-      m_all = -INFINITY;
-      for (int y = 0; y < w.p.pieces; ++y)
-        m_all = fmaxf(m_all, __ldcg(p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + warp) *
-                                                 C::kRow + D));
-      const float m_eff2 = m_all == -INFINITY ? 0.f : m_all;
-      l_all = 0.f;
+      for (int y = 0; y < kWarps; ++y) m_all = fmaxf(m_all, from[y * kStride + D]);
+      const float m_eff = m_all == -INFINITY ? 0.f : m_all;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-      for (int y = 0; y < w.p.pieces; ++y) {
-        const float* in = p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + warp) * C::kRow;
-        const float f = ex2(__ldcg(in + D) - m_eff2);
-        l_all += f * __ldcg(in + D + 1);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, __ldcg(in + e * 32 + lane), o[e]);
+      for (int y = 0; y < kWarps; ++y) {
+        const float f = ex2(from[y * kStride + D] - m_eff);
+        l_all += f * from[y * kStride + D + 1];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[y * kStride + e * 32 + lane], o[e]);
       }
-    }
-    const bool none = m_all == -INFINITY;
-    const float inv = none ? 0.f : 1.f / l_all;
-    const size_t at = (static_cast<size_t>(w.s.tok0 + warp) * p.H + h) * D;
+      if (w.p.pieces > 1) {
+        // A piece's result goes to the workspace; the last of the unit's pieces
+        // to arrive joins them in order, so the result does not depend on which
+        // it is.
+        float* out = p.part + (static_cast<size_t>(plan_place(blockIdx.x, w.p.index)) * kDecodeRows + t) * C::kRow;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      if (O_BF16)
-        static_cast<__nv_bfloat16*>(p.o)[at + e * 32 + lane] = __float2bfloat16(o[e] * inv);
-      else
-        static_cast<float*>(p.o)[at + e * 32 + lane] = o[e] * inv;
+        for (int e = 0; e < D / 32; ++e) __stcg(out + e * 32 + lane, o[e]);
+        if (lane == 0) __stcg(out + D, m_all), __stcg(out + D + 1, l_all);
+        __threadfence();
+        __syncwarp();
+        int arrived = 0;
+        if (lane == 0) arrived = atomicAdd(p.counters + w.p.first * 4 + t, 1);
+        if (__shfl_sync(0xffffffffu, arrived, 0) != w.p.pieces - 1) continue;
+        __threadfence();
+        m_all = -INFINITY;
+        for (int y = 0; y < w.p.pieces; ++y)
+          m_all = fmaxf(m_all, __ldcg(p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + t) *
+                                                   C::kRow + D));
+        const float m_eff2 = m_all == -INFINITY ? 0.f : m_all;
+        l_all = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+        for (int y = 0; y < w.p.pieces; ++y) {
+          const float* in = p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + t) * C::kRow;
+          const float f = ex2(__ldcg(in + D) - m_eff2);
+          l_all += f * __ldcg(in + D + 1);
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, __ldcg(in + e * 32 + lane), o[e]);
+        }
+      }
+      const bool none = m_all == -INFINITY;
+      const float inv = none ? 0.f : 1.f / l_all;
+      const size_t at = (static_cast<size_t>(w.s.tok0 + t) * p.H + h) * D;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        if (O_BF16)
+          static_cast<__nv_bfloat16*>(p.o)[at + e * 32 + lane] = __float2bfloat16(o[e] * inv);
+        else
+          static_cast<float*>(p.o)[at + e * 32 + lane] = o[e] * inv;
+      }
+      if (p.lse != nullptr && lane == 0)
+        p.lse[static_cast<size_t>(h) * p.T + w.s.tok0 + t] =
+            none ? -INFINITY : (m_all + log2f(l_all)) * 0.69314718055994531f;
     }
-    if (p.lse != nullptr && lane == 0)
-      p.lse[static_cast<size_t>(h) * p.T + w.s.tok0 + warp] =
-          none ? -INFINITY : (m_all + log2f(l_all)) * 0.69314718055994531f;
   }
   if (!ok && lane == 0) report_timeout(abort, p.status);
 }
@@ -447,7 +452,7 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCt
       return e;
     if (dev < 32) __atomic_fetch_or(&configured, 1u << dev, __ATOMIC_RELEASE);
   }
-  return launch_dependent(kern, dim3(kDecodePerSm * sms), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, tm_r, p);
+  return launch_dependent(kern, dim3(kDecodePerSm * sms), dim3(C::kThreads), C::kSmem, stream, tm_k, tm_v, tm_r, p);
 }
 
 }  // namespace
