@@ -72,3 +72,48 @@ def test_ring(n):
 def test_a_stage_shared_by_warps_is_caught():
     """Three stages and four warps: a warp does not see every phase of a stage."""
     assert any(run(3, 4, 40, random.Random(seed)) for seed in range(300))
+
+
+# ---------------------------------------------------------------------------
+# the D = 64 kernel of longer entries: softmax warps that wait for a value tile
+# ---------------------------------------------------------------------------
+def with_dead_rows(progs, dead, build_first):
+    """The roles of test_loader_protocol.py, where the softmax of the steps in `dead` needs its value tile landed before
+    it hands over its weights, and builds the next unit's operands before that (build_first) or after."""
+    progs = dict(progs)
+    for name in ("sm0", "sm1"):
+        prog, out, i = progs[name], [], 0
+        while i < len(prog):
+            act, deps = prog[i]
+            if act[0] == "P" and act[1] in dead:
+                handed = (act, deps + [("LV", act[1])])
+                if build_first and i + 1 < len(prog) and prog[i + 1][0][0] == "B":
+                    out.append(prog[i + 1])
+                    i += 1
+                out.append(handed)
+            else:
+                out.append((act, deps))
+            i += 1
+        progs[name] = out
+    return progs
+
+
+MIXES = [[1] * 9, [2] * 8, [1, 2, 1, 1, 3, 1, 1], [5, 1, 4, 1, 1], [16, 14, 2, 1, 3]]
+
+
+@pytest.mark.parametrize("nks", MIXES)
+def test_value_waits_do_not_deadlock(nks):
+    from test_loader_protocol import _programs, _run
+
+    for seed in range(60):
+        rng = random.Random(seed)
+        dead = {g for g in range(sum(nks)) if rng.random() < 0.5} if seed else set(range(sum(nks)))
+        ok, pc = _run(with_dead_rows(_programs(nks, 2, flush=True), dead, True), rng)
+        assert ok, (nks, seed, pc)
+
+
+def test_waiting_before_the_build_is_caught():
+    from test_loader_protocol import _programs, _run
+
+    ok, _ = _run(with_dead_rows(_programs([1] * 9, 2, flush=True), set(range(9)), False), random.Random(0))
+    assert not ok

@@ -1,9 +1,10 @@
 // The division of the bf16 paged attention's work (paged_plan.cuh), made on
 // the device at the head of each call, and the call's dispatch.
 #include <algorithm>
+#include <cmath>
 #include <vector>
 
-#include "paged_plan.cuh"
+#include "paged_tiles.cuh"
 #include "pdl.cuh"
 
 namespace txl {
@@ -178,14 +179,57 @@ size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16) {
   return bf16 ? plan_space(nullptr, n, T, D, nullptr) : 256;
 }
 
+namespace {
+
+cudaError_t launch_tiles(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc, cudaStream_t stream) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = api_tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const PageBook& b = a.book;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  auto enc = [&](CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t D = a.D, H = a.H, P = b.page_rows;
+  TileMaps m;
+  {
+    const cuuint64_t dims[4] = {D, P, H, static_cast<cuuint64_t>(b.n_pages)};
+    const cuuint64_t strides[3] = {D * 2, P * D * 2, H * P * D * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(std::min<cuuint64_t>(P, 64)), 1, 1};
+    if (!enc(&m.k, a.kp, 4, dims, strides, box) || !enc(&m.v, a.vp, 4, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  const cuuint64_t row[2] = {D * 2, H * D * 2};
+  const cuuint64_t tokens[3] = {D, H, static_cast<cuuint64_t>(a.T)};
+  const cuuint64_t distances[3] = {D, H, static_cast<cuuint64_t>(a.n_r)};
+  const cuuint32_t box_q[3] = {64, 1, kTileQueries}, box_r[3] = {64, 1, 64}, box_o[3] = {64, 1, 32};
+  if (!enc(&m.q, a.q, 3, tokens, row, box_q) || !enc(&m.r, a.r, 3, distances, row, box_r))
+    return cudaErrorInvalidValue;
+  m.o = m.q;  // stands in where the output is not bf16 and never touched
+  if (a.o_bf16 && !enc(&m.o, a.o, 3, tokens, row, box_o)) return cudaErrorInvalidValue;
+  // The sign of the scale is folded into (q+u), (q+v) (exact in bf16); a zero
+  // scale becomes 1e-30, for which every visible exponent rounds to 2^0 in
+  // fp32 exactly as with 0, while masked keys keep an exponent of -inf.
+  const TileParams p{b, a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H,
+                     std::max(std::fabs(a.scale), 1e-30f) * 1.4426950408889634f, a.scale < 0.f ? -1.f : 1.f,
+                     s.heads + 1, s.seqs[1], s.starts[1], s.counters[1], s.part[1], wc.status, wc.limit_ns};
+  return a.D == 64 ? launch_paged_tc64(m, p, a.o_bf16, sms, stream)
+                   : launch_paged_tc128(m, p, a.o_bf16, sms, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_t stream) {
-  if (!a.bf16 || a.max_new > kDecodeRows) return launch_paged_simt(a, wc.status, stream);
+  if (!a.bf16) return launch_paged_simt(a, wc.status, stream);
   PlanSpace s;
   plan_space(a.workspace, a.n, a.T, a.D, &s);
   const int sms = paged_sms();
   cudaError_t e = launch_paged_plan(a, s, sms, wc.status, stream);
-  if (e != cudaSuccess) return e;
-  return launch_paged_decode(a, s, sms, wc, stream);
+  if (e == cudaSuccess) e = launch_paged_decode(a, s, sms, wc, stream);
+  if (e == cudaSuccess && a.max_new > kDecodeRows) e = launch_tiles(a, s, sms, wc, stream);
+  return e;
 }
 
 }  // namespace txl

@@ -1,0 +1,577 @@
+// bf16 relative attention of new tokens over a paged memory on the tensor
+// cores, head dimension 128: tiles of 128 queries of a ragged batch.
+//
+//   s[t,j] = scale * ((q_t + u) . k_j + (q_t + v) . r_{m+t-j}),  j <= m + t
+//   o_t = softmax(s[t,.]) V
+//
+// The pipeline is that of relattn_tc.cu: three MMA issuers (content score,
+// distance score into a three-slot ring of 64-distance tiles, P.V), eight
+// softmax warps of which two share a lane quadrant and halve each 64-key step,
+// the distance window shifted per lane.  Keys are counted in page rows, the
+// work is divided on the device and cut units joined, value rows that are not
+// live are zeroed, as in paged_tc64.cu.
+//
+// TMEM (512 columns): O [0,128), P0, P1 [128,192) (bf16 pairs), S0, S1
+// [192,320), distance ring [320,512).  Warps: 0-7 softmax (warp w: lane
+// quadrant w%4, key columns 32 (w/4) .. + 31); 8 TMA loader; 9 content-score
+// MMA issuer (owns the TMEM allocation); 10 PV MMA issuer; 11 distance-score
+// MMA issuer.  Every wait is bounded.
+#include <cmath>
+#include <cstdint>
+
+#include "paged_tiles.cuh"
+#include "pdl.cuh"
+#include "relattn_tc_common.cuh"
+#include "txl_device.cuh"
+#include "txl_internal.h"
+
+namespace txl {
+namespace {
+
+constexpr int D = 128;
+constexpr int BM = 128;  // query rows per unit (TMEM lanes)
+constexpr int BN = 64;   // keys per step, distances per ring tile
+constexpr int kLoaderWarp = 8;
+constexpr int kMmaWarp = 9;   // S = (q+u)K^T issuer; owns the TMEM allocation
+constexpr int kPvWarp = 10;   // O += P V issuer
+constexpr int kQrWarp = 11;   // G = (q+v)R^T (distance ring) issuer
+constexpr int kThreads = 384;
+constexpr uint32_t kColO = 0;
+constexpr uint32_t kColP = 128;  // P0, P1: 32 columns each
+constexpr uint32_t kColS = 192;  // S0, S1: 64 columns each
+constexpr uint32_t kColG = 320;  // distance ring: 3 slots of 64 columns
+constexpr int kSlots = 3;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLazy = 8.0f;  // log2 headroom before the running max moves
+
+constexpr int kChunks = D / 64;
+constexpr int kRowChunk = BN * 128;  // 64 rows x 128 B
+constexpr int kRowTile = kChunks * kRowChunk;
+constexpr int kQChunk = BM * 128;    // 128 rows x 128 B
+constexpr int kQTile = kChunks * kQChunk;
+constexpr int NK = 2, NV = 2, NR = 2;
+constexpr int kOffQ = 0;
+constexpr int kOffQu = kOffQ + kQTile;
+constexpr int kOffQv = kOffQu + kQTile;
+constexpr int kOffK = kOffQv + kQTile;
+constexpr int kOffV = kOffK + NK * kRowTile;
+constexpr int kOffR = kOffV + NV * kRowTile;
+constexpr int kOffRed = kOffR + NR * kRowTile;
+constexpr int kRedFloats = 2 * 2 * BM + 2 * BM;  // [step parity][half][row] maxima, [unit parity][row] sums
+constexpr int kOffBar = kOffRed + kRedFloats * 4;
+constexpr int kBarBytes = 1024;
+constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct Bars {
+  uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
+  uint64_t q_full, q_empty;
+  uint64_t q_ready, s_full[2], s_free[2], p_full[2], pv_done[2], o_full, o_free, g_free[kSlots], mma_final,
+      pv_final;
+  uint64_t g_full[2], qr_final;  // distance tile of a step ready (per S buffer parity); QR issuer done
+  uint64_t xbar[4];  // row-max exchange of warps quad and quad+4 (64 arrivals per step)
+  uint64_t lbar[4];  // row-sum hand-over at the end of a unit (32 arrivals)
+  TileUnit units[kUnitRing];
+  int any;  // the CTA has a unit
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block too large");
+
+template <bool O_BF16>
+__global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_constant__ TileMaps tm, const TileParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  uint8_t* sQ = smem + kOffQ;
+  uint8_t* sQu = smem + kOffQu;
+  uint8_t* sQv = smem + kOffQv;
+  uint8_t* sK = smem + kOffK;
+  uint8_t* sV = smem + kOffV;
+  uint8_t* sR = smem + kOffR;
+  float* red = reinterpret_cast<float*>(smem + kOffRed);
+  float* lred = red + 2 * 2 * BM;
+  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
+  volatile int* abort = &bars->abort;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->fullK[s], 1);
+      mbar_init(&bars->emptyK[s], 1);
+      mbar_init(&bars->fullV[s], 1);
+      mbar_init(&bars->emptyV[s], 1);
+      mbar_init(&bars->fullR[s], 1);
+      mbar_init(&bars->emptyR[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      if (s < kSlots) mbar_init(&bars->g_free[s], 8);
+      mbar_init(&bars->xbar[s], 64);
+      mbar_init(&bars->lbar[s], 32);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->g_full[s], 1);
+      mbar_init(&bars->s_free[s], 8);
+      mbar_init(&bars->p_full[s], 8);
+      mbar_init(&bars->pv_done[s], 1);
+    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 128);
+    mbar_init(&bars->q_ready, 128);
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->o_free, 4);
+    mbar_init(&bars->mma_final, 1);
+    mbar_init(&bars->qr_final, 1);
+    mbar_init(&bars->pv_final, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  // The kernels ahead on the stream, the plan among them, have completed from
+  // here on.
+  grid_dep_wait();
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  TileWalk walk;
+  if (threadIdx.x == kLoaderWarp * 32) {
+    const bool some = walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+    bars->any = some ? 1 : 0;
+    if (some) publish_unit(walk, bars->units, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const bool any = bars->any != 0;
+  const uint64_t wait_ns = p.wait_ns;
+
+  if (warp == kLoaderWarp) {
+    // ============================ TMA loader ===============================
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.q);
+      tma_prefetch_desc(&tm.k);
+      tma_prefetch_desc(&tm.v);
+      tma_prefetch_desc(&tm.r);
+      uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
+      bool ok = true;
+      const PageMap pm(p.book);
+      auto acquire = [&](uint64_t* empty, uint64_t* full, uint32_t n, int ns, int bytes) -> bool {
+        const int s = static_cast<int>(n % ns);
+        if (!mbar_wait(&empty[s], ((n / ns) & 1) ^ 1, wait_ns, abort)) return false;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        return true;
+      };
+      for (uint32_t un = 0; any && ok; ++un) {
+        const TileUnit w = bars->units[un % kUnitRing];
+        if (w.next_h >= 0) publish_unit(walk, bars->units, un + 1);
+        if (!(ok = acquire(&bars->q_empty, &bars->q_full, nQ, 1, kQTile))) break;
+        for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + c * kQChunk, &tm.q, &bars->q_full, c * 64, w.h, w.row0);
+        ++nQ;
+        auto load_r = [&](int d0) -> bool {
+          if (!acquire(bars->emptyR, bars->fullR, nR, NR, kRowTile)) return false;
+          const int s = nR % NR;
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_3d(sR + s * kRowTile + c * kRowChunk, &tm.r, &bars->fullR[s], c * 64, w.h, d0);
+          ++nR;
+          return true;
+        };
+        TilePages next = pm.pages(w, w.t0);
+        // distance tiles -2 and -1 of the unit's first step
+        ok = load_r(w.d0 - BN * (w.t0 - 1)) && load_r(w.d0 - BN * w.t0);
+        for (int t = w.t0; ok && t < w.t0 + w.nks; ++t) {
+          const TilePages pages = next;
+          if (t + 1 < w.t0 + w.nks) next = pm.pages(w, t + 1);  // on its way while this tile's loads are issued
+          int s = static_cast<int>(nK % NK);
+          if (!(ok = mbar_wait(&bars->emptyK[s], ((nK / NK) & 1) ^ 1, wait_ns, abort))) break;
+          load_tile<D>(pm, w, t, pages, &tm.k, sK + s * kRowTile, &bars->fullK[s], p.status);
+          ++nK;
+          if (!(ok = load_r(w.d0 - BN * (t + 1)))) break;
+          s = static_cast<int>(nV % NV);
+          if (!(ok = mbar_wait(&bars->emptyV[s], ((nV / NV) & 1) ^ 1, wait_ns, abort))) break;
+          load_tile<D>(pm, w, t, pages, &tm.v, sV + s * kRowTile, &bars->fullV[s], p.status);
+          ++nV;
+        }
+        if (w.next_h < 0) break;
+      }
+      if (!ok) report_timeout(abort, p.status);
+      // Let this thread's own copies land before the CTA may exit.
+      auto drain = [&](uint64_t* full, uint32_t n, int ns) {
+        for (int s = 0; s < ns && static_cast<uint32_t>(s) < n; ++s) {
+          const uint32_t last = s + ((n - 1 - s) / ns) * ns;
+          mbar_wait_own(&full[s], (last / ns) & 1, wait_ns);
+        }
+      };
+      drain(&bars->q_full, nQ, 1);
+      drain(bars->fullK, nK, NK);
+      drain(bars->fullV, nV, NV);
+      drain(bars->fullR, nR, NR);
+    }
+  } else if (warp == kMmaWarp) {
+    // ============================ MMA issuer ===============================
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
+      // Descriptor bases; the start-address field holds address / 16 in its
+      // low 14 bits, so byte offsets inside shared memory are added as
+      // offset / 16 (no carry: shared addresses stay below 256 KB).
+      const uint64_t dQu = sdesc_sw128(smem_u32(sQu), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      constexpr uint32_t kTile16 = kRowTile >> 4;
+      uint32_t nK = 0, gt = 0, un = 0;
+      bool ok = true;
+      while (any && ok) {
+        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
+        const TileUnit w = bars->units[un % kUnitRing];
+        tc_fence_after();
+        const uint32_t g0 = gt;
+        for (int t = 0; t < w.nks; ++t) {
+          const uint32_t g = g0 + t, sb = g & 1;
+          if (g >= 2 && !(ok = mbar_wait(&bars->s_free[sb], ((g - 2) >> 1) & 1, wait_ns, abort))) break;
+          const int sk = nK % NK;
+          if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
+          tc_fence_after();
+          {
+            const uint64_t dk = dK + sk * kTile16;
+            const uint32_t sd = tmem + kColS + sb * BN;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t koff16 = ((kk / 4) * kRowChunk + (kk % 4) * 32) >> 4;
+              mma_ss(sd, dQu + (((kk / 4) * kQChunk + (kk % 4) * 32) >> 4), dk + koff16, idS, kk > 0);
+            }
+          }
+          tc_commit(&bars->emptyK[sk]);
+          ++nK;
+          tc_commit(&bars->s_full[sb]);
+        }
+        if (!ok || w.next_h < 0) break;
+        gt = g0 + w.nks;
+        ++un;
+      }
+      if (!ok) report_timeout(abort, p.status);
+      tc_commit(&bars->mma_final);
+      mbar_wait_own(&bars->mma_final, 0, wait_ns);
+    }
+  } else if (warp == kPvWarp) {
+    // ============================ PV issuer ================================
+    if (lane == 0) {
+      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+      const uint64_t dV = sdesc_sw128(smem_u32(sV), kRowChunk, 1024);
+      constexpr uint32_t kTile16 = kRowTile >> 4;
+      uint32_t nV = 0, g = 0, un = 0;
+      bool ok = true;
+      while (any && ok) {
+        // The unit is read behind the barrier of its first weights.
+        int nks = 1, next_h = -1;
+        for (int t = 0; t < nks; ++t, ++g) {
+          if (!(ok = mbar_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
+          if (t == 0) {
+            nks = bars->units[un % kUnitRing].nks;
+            next_h = bars->units[un % kUnitRing].next_h;
+          }
+          const int sv = nV % NV;
+          if (!(ok = mbar_wait(&bars->fullV[sv], (nV / NV) & 1, wait_ns, abort))) break;
+          if (t == 0 && un > 0 && !(ok = mbar_wait(&bars->o_free, (un - 1) & 1, wait_ns, abort))) break;
+          tc_fence_after();
+          const uint64_t dv = dV + sv * kTile16;
+          const uint32_t pa = tmem + kColP + (g & 1) * 32;
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + kColO, pa + kk * 8, dv + ((kk * 16 * 128) >> 4), idO, (t > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(&bars->emptyV[sv]);
+          tc_commit(&bars->pv_done[g & 1]);
+          ++nV;
+        }
+        if (!ok) break;
+        tc_commit(&bars->o_full);
+        ++un;
+        if (next_h < 0) break;
+      }
+      if (!ok) report_timeout(abort, p.status);
+      tc_commit(&bars->pv_final);
+      mbar_wait_own(&bars->pv_final, 0, wait_ns);
+    }
+  } else if (warp == kQrWarp) {
+    // ========================= distance-ring issuer =========================
+    // G tile e = (q+v) R_e^T into ring slot (e+2) % 3 once the softmax has
+    // released the slot's previous tile; tiles -2 and -1 of a unit with its
+    // first step.  Its own thread, so the ring never waits behind the S
+    // MMAs' barriers (and the reverse); it commits g_full per step.
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
+      const uint64_t dQv = sdesc_sw128(smem_u32(sQv), 16, 1024);
+      const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
+      constexpr uint32_t kTile16 = kRowTile >> 4;
+      uint32_t nR = 0, gt = 0, un = 0;
+      uint32_t gsu0 = 0, gsu1 = 0, gsu2 = 0;  // writes per ring slot so far
+      bool ok = true;
+      while (any && ok) {
+        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
+        const TileUnit w = bars->units[un % kUnitRing];
+        tc_fence_after();
+        const uint32_t g0 = gt;
+        for (int t = 0; t < w.nks; ++t) {
+          const uint32_t g = g0 + t, sb = g & 1;
+          for (int e = (t == 0 ? -2 : t); ok && e <= t; ++e) {
+            const int slot = (e + 2) % kSlots;
+            const uint32_t used = slot == 0 ? gsu0 : (slot == 1 ? gsu1 : gsu2);
+            if (used > 0 && !(ok = mbar_wait(&bars->g_free[slot], (used - 1) & 1, wait_ns, abort))) break;
+            const int sr = nR % NR;
+            if (!(ok = mbar_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
+            tc_fence_after();
+            const uint64_t dr = dR + sr * kTile16;
+            const uint32_t gd = tmem + kColG + slot * BN;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t koff16 = ((kk / 4) * kRowChunk + (kk % 4) * 32) >> 4;
+              mma_ss(gd, dQv + (((kk / 4) * kQChunk + (kk % 4) * 32) >> 4), dr + koff16, idS, kk > 0);
+            }
+            tc_commit(&bars->emptyR[sr]);
+            ++nR;
+            gsu0 += slot == 0;
+            gsu1 += slot == 1;
+            gsu2 += slot == 2;
+          }
+          if (!ok) break;
+          tc_commit(&bars->g_full[sb]);
+        }
+        if (!ok || w.next_h < 0) break;
+        gt = g0 + w.nks;
+        ++un;
+      }
+      if (!ok) report_timeout(abort, p.status);
+      tc_commit(&bars->qr_final);
+      mbar_wait_own(&bars->qr_final, 0, wait_ns);
+    }
+  } else {
+    // ============================ softmax warps ============================
+    const int half = warp >> 2;  // 0: key columns 0-31 of a step, 1: columns 32-63
+    const int quad = warp & 3;   // TMEM lane quadrant
+    const int a = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const float sl2 = p.scale_log2e;
+    uint32_t gt = 0, un = 0, nQ = 0;
+    bool ok = true;
+
+    // (q + u), (q + v) for this thread's row of a unit of head h: bf16,
+    // 128B-swizzled K-major shared-memory tiles.
+    auto build_q = [&](int h) -> bool {
+      if (!warp_wait(&bars->q_full, nQ & 1, wait_ns, abort)) return false;
+      const float* bu = p.bias_u + h * D;
+      const float* bv = p.bias_v + h * D;
+      uint32_t qu[D / 2], qv[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const int kc = c / 8, cc = c % 8;
+        const int off = kc * kQChunk + (a / 8) * 1024 + (a % 8) * 128 + ((cc ^ (a % 8)) * 16);
+        const uint4 raw = *reinterpret_cast<const uint4*>(sQ + off);
+        const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = c * 8 + 2 * e;
+          const float x0 = bf16_lo(w4[e]), x1 = bf16_hi(w4[e]);
+          qu[c * 4 + e] = pack_bf16x2((x0 + __ldg(bu + d)) * p.qsign, (x1 + __ldg(bu + d + 1)) * p.qsign);
+          qv[c * 4 + e] = pack_bf16x2((x0 + __ldg(bv + d)) * p.qsign, (x1 + __ldg(bv + d + 1)) * p.qsign);
+        }
+      }
+      mbar_arrive(&bars->q_empty);
+      ++nQ;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const int kc = c / 8, cc = c % 8;
+        const int off = kc * kQChunk + (a / 8) * 1024 + (a % 8) * 128 + ((cc ^ (a % 8)) * 16);
+        *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[4 * c], qu[4 * c + 1], qu[4 * c + 2], qu[4 * c + 3]);
+        *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[4 * c], qv[4 * c + 1], qv[4 * c + 2], qv[4 * c + 3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->q_ready);
+      return true;
+    };
+
+    if (any && half == 1) ok = build_q(bars->units[0].h);
+
+    while (any && ok) {
+      // Unit 0 is published before the CTA's first barrier, unit un + 1 before
+      // the loads of unit un's keys.
+      const TileUnit* unit = &bars->units[un % kUnitRing];
+      const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
+      float m_use = -INFINITY;  // running max in log2 units (lazy)
+      float l_half = 0.f;       // row sum over this half's columns
+      const uint32_t g0 = gt;
+      for (int t = 0; t < nks; ++t) {
+        const uint32_t g = g0 + t, sb = g & 1;
+        if (!(ok = warp_wait(&bars->s_full[sb], (g >> 1) & 1, wait_ns, abort))) break;
+        if (!(ok = warp_wait(&bars->g_full[sb], (g >> 1) & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        uint32_t sraw[32], x0[32], x1[32];
+        tmem_ld32(tmem + lane_base + kColS + sb * BN + 32 * half, sraw);
+        // Distance window of this warp: ring-relative index z = 64 + a - c
+        // (z < 64: tile t, < 128: tile t-1, else tile t-2); the warp reads
+        // z in [zq, zq + 64) and lane l uses z = zq + 32 + l - k for column k.
+        const int zq = 32 * (1 + quad - half);
+        const uint32_t c0 = kColG + ((t - (zq >> 6) + 2) % kSlots) * BN + (zq & 63);
+        const uint32_t c1 = kColG + ((t - ((zq + 32) >> 6) + 2) % kSlots) * BN + ((zq + 32) & 63);
+        tmem_ld32(tmem + lane_base + c0, x0);
+        tmem_ld32(tmem + lane_base + c1, x1);
+        tmem_wait_ld(sraw);
+        tmem_wait_ld(x0);
+        tmem_wait_ld(x1);
+        warp_arrive_tc(&bars->s_free[sb]);              // S buffer may be refilled
+        warp_arrive_tc(&bars->g_free[t % kSlots]);      // distance tile t-2: last read
+        uint32_t bd[16];
+        window_shift(x0, x1, lane, bd);
+        // x[k] = content + distance score of key column 32*half + k; the
+        // distance value sits at window position 31 - k.
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int i = 31 - k;
+          x[k] = (i & 1) ? add_bf16hi(bd[i >> 1], __uint_as_float(sraw[k]))
+                         : add_bf16lo(bd[i >> 1], __uint_as_float(sraw[k]));
+        }
+        const int kt = t0 + t;                           // key step of the tile
+        const int lim = d0 - BN * kt + a - 32 * half;    // column k visible iff low <= k <= lim
+        const int low = start - BN * kt - 32 * half;
+        if (d0 - BN * kt + quad * 32 - 32 * half < 31 || low > 0) {  // some lane of the warp masks
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = (k <= lim && k >= low) ? x[k] : -INFINITY;
+        }
+        float t3[11];
+#pragma unroll
+        for (int n = 0; n < 10; ++n) t3[n] = max3f(x[3 * n], x[3 * n + 1], x[3 * n + 2]);
+        t3[10] = fmaxf(x[30], x[31]);
+        float mx = max3f(max3f(t3[0], t3[1], t3[2]), max3f(t3[3], t3[4], t3[5]),
+                         max3f(max3f(t3[6], t3[7], t3[8]), t3[9], t3[10]));
+        // row max over both halves of the step
+        float* rs = red + (g & 1) * 2 * BM;
+        rs[half * BM + a] = mx;
+        mbar_arrive(&bars->xbar[quad]);
+        if (!(ok = warp_wait(&bars->xbar[quad], g & 1, wait_ns, abort))) break;
+        mx = fmaxf(mx, rs[(1 - half) * BM + a]) * sl2;
+        float m_new = m_use, alpha = 1.f;
+        if (mx > m_use + kLazy) {
+          m_new = mx;
+          alpha = ex2(m_use - mx);
+        }
+        // A row with no visible key yet keeps m_new = -inf; its exponents are
+        // then taken against 0 (all -inf, so every p is 0).
+        const float m_eff = m_new == -INFINITY ? 0.f : m_new;
+        uint32_t pk[16];
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_eff, -m_eff);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const float2 y = __ffma2_rn(make_float2(x[2 * n], x[2 * n + 1]), sc2, nm2);
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          if (n & 1)
+            acc1 = __fadd2_rn(acc1, e);
+          else
+            acc0 = __fadd2_rn(acc0, e);
+          pk[n] = pack_bf16x2(e.x, e.y);
+        }
+        l_half = l_half * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
+        if (half == 0 && t > 0 && __any_sync(0xffffffffu, alpha < 1.f)) {
+          // O holds PV up to step t-1; rescale once that PV has completed.
+          if (!(ok = warp_wait(&bars->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, wait_ns, abort))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int oc = 0; oc < D / 32; ++oc) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + lane_base + kColO + oc * 32, ov);
+            tmem_wait_ld(ov);
+#pragma unroll
+            for (int n = 0; n < 32; ++n) ov[n] = __float_as_uint(__uint_as_float(ov[n]) * alpha);
+            tmem_st32(tmem + lane_base + kColO + oc * 32, ov);
+          }
+        }
+        m_use = m_new;
+        // P buffer sb was last read by the PV of step g-2.
+        if (g >= 2 && !(ok = warp_wait(&bars->pv_done[sb], ((g - 2) >> 1) & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        tmem_st16(tmem + lane_base + kColP + sb * 32 + 16 * half, pk);
+        tmem_wait_st();
+        if (has_dead_rows(*unit, kt)) {
+          // The stage's phases go by in order before this warp: the P.V two
+          // steps back is done, and the stage is refilled only after this
+          // step's.
+          if (!(ok = warp_wait(&bars->fullV[g % NV], (g / NV) & 1, wait_ns, abort))) break;
+          zero_dead_rows<D>(*unit, kt, sV + (g % NV) * kRowTile, warp, 8, lane);
+          fence_proxy_async_smem();
+        }
+        warp_arrive_tc(&bars->p_full[sb]);
+      }
+      if (!ok) break;
+      // Distance tiles nks-2 and nks-1 are not read any more in this unit.
+      warp_arrive_tc(&bars->g_free[nks % kSlots]);
+      warp_arrive_tc(&bars->g_free[(nks + 1) % kSlots]);
+      float* ls = lred + (un & 1) * BM;
+      if (half == 1) {
+        ls[a] = l_half;
+        mbar_arrive(&bars->lbar[quad]);
+      }
+      if (half == 0) {
+        if (!(ok = warp_wait(&bars->lbar[quad], un & 1, wait_ns, abort))) break;
+        const float l = l_half + ls[a];
+        if (!(ok = warp_wait(&bars->o_full, un & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        const bool seen = m_use != -INFINITY;  // the row sees a key of this piece
+        const float inv_l = seen ? 1.f / l : 0.f;
+        const float lse2 = seen ? m_use + __log2f(l) : -INFINITY;
+        float ov[D];
+#pragma unroll
+        for (int oc = 0; oc < D / 32; ++oc) {
+          uint32_t tmp[32];
+          tmem_ld32(tmem + lane_base + kColO + oc * 32, tmp);
+          tmem_wait_ld(tmp);
+#pragma unroll
+          for (int n = 0; n < 32; ++n) ov[oc * 32 + n] = __uint_as_float(tmp[n]) * inv_l;
+        }
+        warp_arrive_tc(&bars->o_free);
+        if (unit->pieces > 1)
+          store_piece<D, O_BF16>(*unit, quad, lane, ov, lse2, p.part, p.counters, p.o, p.lse, p.T, p.H);
+        else
+          store_row<D, O_BF16>(*unit, a, ov, lse2, p.o, p.lse, p.T, p.H);
+      } else if (unit->next_h >= 0 && !(ok = build_q(unit->next_h))) {
+        break;
+      }
+      if (unit->next_h < 0) break;
+      gt = g0 + nks;
+      ++un;
+    }
+    if (!ok) report_timeout(abort, p.status);
+  }
+
+  // ---- teardown ------------------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool O_BF16>
+cudaError_t launch(const TileMaps& m, const TileParams& p, int sms, cudaStream_t stream) {
+  auto kern = paged_tc128_kernel<O_BF16>;
+  static unsigned configured = 0;  // one bit per device ordinal < 32
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 32 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1u << dev))) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
+      return e;
+    if (dev < 32) __atomic_fetch_or(&configured, 1u << dev, __ATOMIC_RELEASE);
+  }
+  return launch_dependent(kern, dim3(sms), dim3(kThreads), kSmemBytes, stream, m, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc128(const TileMaps& m, const TileParams& p, bool o_bf16, int sms, cudaStream_t stream) {
+  return o_bf16 ? launch<true>(m, p, sms, stream) : launch<false>(m, p, sms, stream);
+}
+
+}  // namespace txl

@@ -1,0 +1,742 @@
+// bf16 relative attention of new tokens over a paged memory on the tensor
+// cores, head dimension 64: tiles of 128 queries of a ragged batch.
+//
+//   s[t,j] = scale * ((q_t + u) . k_j + (q_t + v) . r_{m+t-j}),  j <= m + t
+//   o_t = softmax(s[t,.]) V
+//
+// The pipeline is that of relattn_tc64.cu: three MMA issuers (content score,
+// distance score into a ring of 64-distance tiles, P.V), eight softmax warps
+// that take alternate 64-key steps, the distance window shifted per lane, two
+// output accumulators merged at the end of a unit.  What is of its own:
+//
+//   * Keys are counted in page rows, from the slot's first page, so a 64-row
+//     key tile is a box of one page (or 2 or 4 boxes of smaller pages) and
+//     never straddles more; rows before the first live one are masked, and
+//     distances are differences of page rows.
+//   * The division of the work comes from the device (paged_plan.cuh): equal
+//     ranges of key steps per CTA, so that ragged lengths, few sequences and
+//     long memories are all one case; a unit that a range cuts is joined
+//     through the workspace.  The loader publishes the units (paged_tiles.cuh).
+//   * Value rows that are not live are zeroed in shared memory by the softmax
+//     warps of the step.
+//   * A 32-row box of output whose rows are all the unit's leaves by TMA, the
+//     last rows of a sequence by plain stores.
+//
+// TMEM (512 columns): O0 [0,64) O1 [64,128) S0 [128,192) S1 [192,256)
+// distance ring [256,512).  Warps: 0-7 softmax (warp w: lane quadrant w%4,
+// step parity w/4); 8 TMA loader; 9 content-score MMA issuer (owns the TMEM
+// allocation); 10 PV MMA issuer; 11 distance-score MMA issuer.  Every wait is
+// bounded; a wait that runs out raises a CTA abort flag and the device status
+// word, every role unwinds and the TMEM is freed before exit.
+#include <cmath>
+#include <cstdint>
+
+#include "paged_tiles.cuh"
+#include "pdl.cuh"
+#include "relattn_tc_common.cuh"
+#include "txl_device.cuh"
+#include "txl_internal.h"
+
+namespace txl {
+namespace {
+
+constexpr int BM = kTileRows;
+constexpr int BN = kStepKeys;
+constexpr int D = 64;
+constexpr int kLoaderWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kPvWarp = 10;
+constexpr int kQrWarp = 11;
+constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, three MMA issuers)
+// Register split (launch: 168 per thread, 384 x 168 = 64512): softmax
+// warpgroups 224, producer warpgroup 56; 2*128*224 + 128*56 = 64512, and per
+// scheduler 224 + 224 + 56 = 504 <= 512 per thread-slot.
+constexpr uint32_t kRegsSoftmax = 224;
+constexpr uint32_t kRegsProducer = 56;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");
+constexpr uint32_t kColO = 0;    // O0, O1: 64 columns each
+constexpr uint32_t kColS = 128;  // S0, S1: 64 columns each
+constexpr uint32_t kColG = 256;  // distance ring: 4 slots of 64 columns
+constexpr int kSlots = 4;
+static_assert(kSlots == 4, "ring slot counters and barrier init assume four slots");
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLazy = 8.0f;  // log2 headroom before a running max moves
+
+constexpr int kRowTile = BN * 128;  // 64 rows x 64 bf16 (8 KB)
+constexpr int kQTile = BM * 128;    // 128 rows x 64 bf16 (16 KB)
+constexpr int NK = 4, NV = 4, NR = 4;  // K, V, R tile stages
+static_assert(NK == NV, "K and V tiles share the loader's stage logic");
+constexpr int kOffQ = 0;                        // raw q tile of the next unit (TMA)
+constexpr int kOffQu = kOffQ + kQTile;          // (q+u): 2 buffers
+constexpr int kOffQv = kOffQu + 2 * kQTile;     // (q+v): 2 buffers
+constexpr int kOffK = kOffQv + 2 * kQTile;
+constexpr int kOffV = kOffK + NK * kRowTile;
+constexpr int kOffR = kOffV + NV * kRowTile;
+constexpr int kOffP = kOffR + NR * kRowTile;    // P (bf16): 2 buffers, same layout as (q+u)
+constexpr int kOffRed = kOffP + 2 * kQTile;     // [unit parity][m, l][row] handed to the epilogue
+constexpr int kOffBias = kOffRed + 2 * 2 * BM * 4;  // per softmax warp: 32 dims of u, then of v (fp32)
+constexpr int kOffBar = kOffBias + 8 * 64 * 4;
+constexpr int kBarBytes = 1152;
+constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct VTile {
+  uint32_t unit;  // number of the CTA's unit
+  int t;          // key step
+  TilePages pages;
+};
+
+struct Bars {
+  uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
+  uint64_t q_full, q_empty;
+  uint64_t q_ready, s_full[2], p_full[2], pv_done[2], o_full, o_free;
+  uint64_t sread[4];  // step g's S and distance window have been read (index g % 4, phase g / 4)
+  uint64_t mma_final, pv_final, qr_final;
+  uint64_t lbar[4];   // per quadrant: the non-owning warp's (m, l) of a unit is in `red`
+  uint64_t lfree[4];  // per quadrant: the epilogue has read it
+  VTile vq[4];        // loader: queued V tiles, by V count % 4
+  TileUnit units[kUnitRing];
+  int any;            // the CTA has a unit
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block too large");
+
+template <bool O_BF16>
+__global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_constant__ TileMaps tm, const TileParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  uint8_t* sQ = smem + kOffQ;
+  uint8_t* sQu = smem + kOffQu;
+  uint8_t* sQv = smem + kOffQv;
+  uint8_t* sK = smem + kOffK;
+  uint8_t* sV = smem + kOffV;
+  uint8_t* sR = smem + kOffR;
+  uint8_t* sP = smem + kOffP;
+  float* red = reinterpret_cast<float*>(smem + kOffRed);
+  float* sbias = reinterpret_cast<float*>(smem + kOffBias);
+  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
+  volatile int* abort = &bars->abort;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars->fullK[s], 1);
+      mbar_init(&bars->emptyK[s], 1);
+      mbar_init(&bars->fullV[s], 1);
+      mbar_init(&bars->emptyV[s], 1);
+      mbar_init(&bars->fullR[s], 1);
+      mbar_init(&bars->emptyR[s], 1);
+      mbar_init(&bars->lbar[s], 32);
+      mbar_init(&bars->lfree[s], 1);
+      mbar_init(&bars->sread[s], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 2);  // content and distance MMAs of a step
+      mbar_init(&bars->p_full[s], 4);
+      mbar_init(&bars->pv_done[s], 1);
+    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 8);
+    mbar_init(&bars->q_ready, 8);
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->o_free, 4);
+    mbar_init(&bars->mma_final, 1);
+    mbar_init(&bars->pv_final, 1);
+    mbar_init(&bars->qr_final, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  // The kernels ahead on the stream, the plan among them, have completed from
+  // here on.
+  grid_dep_wait();
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  TileWalk walk;
+  if (threadIdx.x == kLoaderWarp * 32) {
+    const bool some = walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+    bars->any = some ? 1 : 0;
+    if (some) publish_unit(walk, bars->units, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const bool any = bars->any != 0;
+  const uint64_t wait_ns = p.wait_ns;
+
+  if (warp == kLoaderWarp) {
+    // ============================ TMA loader ===============================
+    setmaxnreg_dec<kRegsProducer>();
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.q);
+      tma_prefetch_desc(&tm.k);
+      tma_prefetch_desc(&tm.v);
+      tma_prefetch_desc(&tm.r);
+      uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
+      bool ok = true;
+      const PageMap pm(p.book);
+      auto acquire = [&](uint64_t* empty, uint64_t* full, uint32_t n, int ns, int bytes) -> bool {
+        const int s = static_cast<int>(n % ns);
+        if (!mbar_wait(&empty[s], ((n / ns) & 1) ^ 1, wait_ns, abort)) return false;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        return true;
+      };
+      // The raw q tile of a unit is loaded one unit ahead: the softmax warps
+      // build (q+u), (q+v) from it during the unit before.
+      auto load_q = [&](const TileUnit& w) -> bool {
+        if (!mbar_wait(&bars->q_empty, (nQ & 1) ^ 1, wait_ns, abort)) return false;
+        mbar_arrive_expect_tx(&bars->q_full, kQTile);
+        tma_load_3d(sQ, &tm.q, &bars->q_full, 0, w.h, w.row0);
+        ++nQ;
+        return true;
+      };
+      // V tiles trail the K and R tiles by kVLag tiles.  A V stage is freed
+      // only when the P.V MMA of its step completes, after that step's
+      // softmax, while a K stage is free as soon as its score MMA is done; in
+      // one issue order K(t), R(t+1), V(t), every K load would wait behind
+      // the V stage of step t-4 and land just in time.  Queued V tiles wait in
+      // bars->vq (this thread only).  Before the raw q of the unit after next
+      // is loaded, every queued V of a unit two or more back goes out: that
+      // load waits for the (q+u), (q+v) build of the next unit, which waits
+      // for the epilogue of the unit before, which needs all of that unit's V
+      // tiles (a unit of one step would otherwise hold them behind the load).
+      constexpr uint32_t kVLag = 2;
+      uint32_t nVq = 0;  // V tiles queued; nVq - nV of them not yet issued
+      auto issue_v = [&]() -> bool {
+        const VTile& e = bars->vq[nV % 4];
+        const int s = static_cast<int>(nV % NV);
+        if (!mbar_wait(&bars->emptyV[s], ((nV / NV) & 1) ^ 1, wait_ns, abort)) return false;
+        load_tile<D>(pm, bars->units[e.unit % kUnitRing], e.t, e.pages, &tm.v, sV + s * kRowTile, &bars->fullV[s],
+                     p.status);
+        ++nV;
+        return true;
+      };
+      if (any) ok = load_q(bars->units[0]);
+      for (uint32_t un = 0; any && ok; ++un) {
+        const TileUnit w = bars->units[un % kUnitRing];
+        while (ok && nV < nVq && bars->vq[nV % 4].unit + 2 <= un) ok = issue_v();
+        if (!ok) break;
+        if (w.next_h >= 0) {
+          publish_unit(walk, bars->units, un + 1);
+          if (!(ok = load_q(bars->units[(un + 1) % kUnitRing]))) break;
+        }
+        auto load_r = [&](int d0) -> bool {
+          if (!acquire(bars->emptyR, bars->fullR, nR, NR, kRowTile)) return false;
+          tma_load_3d(sR + (nR % NR) * kRowTile, &tm.r, &bars->fullR[nR % NR], 0, w.h, d0);
+          ++nR;
+          return true;
+        };
+        TilePages next = pm.pages(w, w.t0);
+        // distance tiles -2 and -1 of the unit's first step
+        ok = load_r(w.d0 - BN * (w.t0 - 1)) && load_r(w.d0 - BN * w.t0);
+        for (int t = w.t0; ok && t < w.t0 + w.nks; ++t) {
+          const TilePages pages = next;
+          if (t + 1 < w.t0 + w.nks) next = pm.pages(w, t + 1);  // on its way while this tile's loads are issued
+          const int s = static_cast<int>(nK % NK);
+          if (!(ok = mbar_wait(&bars->emptyK[s], ((nK / NK) & 1) ^ 1, wait_ns, abort))) break;
+          load_tile<D>(pm, w, t, pages, &tm.k, sK + s * kRowTile, &bars->fullK[s], p.status);
+          ++nK;
+          if (!(ok = load_r(w.d0 - BN * (t + 1)))) break;
+          bars->vq[nVq % 4] = VTile{un, t, pages};
+          ++nVq;
+          if (nVq - nV > kVLag) ok = issue_v();
+        }
+        if (w.next_h < 0) break;
+      }
+      while (ok && nV < nVq) ok = issue_v();  // the last kVLag V tiles
+      if (!ok) report_timeout(abort, p.status);
+      auto drain = [&](uint64_t* full, uint32_t n, int ns) {
+        for (int s = 0; s < ns && static_cast<uint32_t>(s) < n; ++s) {
+          const uint32_t last = s + ((n - 1 - s) / ns) * ns;
+          mbar_wait_own(&full[s], (last / ns) & 1, wait_ns);
+        }
+      };
+      drain(&bars->q_full, nQ, 1);
+      drain(bars->fullK, nK, NK);
+      drain(bars->fullV, nV, NV);
+      drain(bars->fullR, nR, NR);
+    }
+  } else if (warp == kMmaWarp) {
+    // ===================== content-score MMA issuer ========================
+    setmaxnreg_dec<kRegsProducer>();
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
+      const uint64_t dQu = sdesc_sw128(smem_u32(sQu), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      constexpr uint32_t kTile16 = kRowTile >> 4;
+      uint32_t nK = 0, gt = 0, un = 0;
+      bool ok = true;
+      while (any && ok) {
+        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
+        const TileUnit w = bars->units[un % kUnitRing];
+        tc_fence_after();
+        const uint32_t g0 = gt;
+        for (int t = 0; t < w.nks; ++t) {
+          const uint32_t g = g0 + t, sb = g & 1;
+          // S buffer sb was last read by step g-2.
+          if (g >= 2 && !(ok = mbar_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
+          const int sk = nK % NK;
+          if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
+          tc_fence_after();
+          const uint64_t dk = dK + sk * kTile16;
+          const uint32_t sd = tmem + kColS + sb * BN;
+          const uint64_t dq = dQu + (un & 1) * (kQTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) mma_ss(sd, dq + kk * 2, dk + kk * 2, idS, kk > 0);
+          tc_commit(&bars->emptyK[sk]);
+          tc_commit(&bars->s_full[sb]);
+          ++nK;
+        }
+        if (!ok || w.next_h < 0) break;
+        gt = g0 + w.nks;
+        ++un;
+      }
+      if (!ok) report_timeout(abort, p.status);
+      tc_commit(&bars->mma_final);
+      mbar_wait_own(&bars->mma_final, 0, wait_ns);
+    }
+  } else if (warp == kQrWarp) {
+    // ==================== distance-score MMA issuer ========================
+    setmaxnreg_dec<kRegsProducer>();
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
+      const uint64_t dQv = sdesc_sw128(smem_u32(sQv), 16, 1024);
+      const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
+      constexpr uint32_t kTile16 = kRowTile >> 4;
+      uint32_t nR = 0, gt = 0, un = 0;
+      // Last global step that reads the tile now in each ring slot (-1: none).
+      int last0 = -1, last1 = -1, last2 = -1, last3 = -1;
+      int rb = 0;  // ring slot of the first distance tile (-2) of the unit
+      bool ok = true;
+      while (any && ok) {
+        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
+        const TileUnit w = bars->units[un % kUnitRing];
+        tc_fence_after();
+        const uint32_t g0 = gt;
+        const uint64_t dq = dQv + (un & 1) * (kQTile >> 4);
+        for (int t = 0; ok && t < w.nks; ++t) {
+          const uint32_t sb = (g0 + t) & 1;
+          for (int e = (t == 0 ? -2 : t); e <= t; ++e) {
+            const int slot = (rb + e + 2) & (kSlots - 1);
+            // The slot's previous tile is free once every step up to its
+            // last reader L has read: steps of one parity read in order, so
+            // waiting for steps L and L-1 covers both parities.  (Four
+            // barriers by step % 4 keep these waits from aliasing: step L+3
+            // cannot have read before this tile exists.)
+            const int L = slot == 0 ? last0 : (slot == 1 ? last1 : (slot == 2 ? last2 : last3));
+            if (L >= 0 && !(ok = mbar_wait(&bars->sread[L & 3], (L >> 2) & 1, wait_ns, abort))) break;
+            if (L >= 1 && !(ok = mbar_wait(&bars->sread[(L - 1) & 3], ((L - 1) >> 2) & 1, wait_ns, abort))) break;
+            const int sr = nR % NR;
+            if (!(ok = mbar_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
+            tc_fence_after();
+            const uint64_t dr = dR + sr * kTile16;
+            const uint32_t gd = tmem + kColG + slot * BN;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) mma_ss(gd, dq + kk * 2, dr + kk * 2, idS, kk > 0);
+            tc_commit(&bars->emptyR[sr]);
+            ++nR;
+            const int lr = static_cast<int>(g0) + min(e + 2, w.nks - 1);  // tile e's last reader
+            last0 = slot == 0 ? lr : last0;
+            last1 = slot == 1 ? lr : last1;
+            last2 = slot == 2 ? lr : last2;
+            last3 = slot == 3 ? lr : last3;
+          }
+          if (!ok) break;
+          tc_commit(&bars->s_full[sb]);
+        }
+        if (!ok || w.next_h < 0) break;
+        gt = g0 + w.nks;
+        ++un;
+        rb = (rb + w.nks + 2) & (kSlots - 1);
+      }
+      if (!ok) report_timeout(abort, p.status);
+      tc_commit(&bars->qr_final);
+      mbar_wait_own(&bars->qr_final, 0, wait_ns);
+    }
+  } else if (warp == kPvWarp) {
+    // ============================ PV issuer ================================
+    setmaxnreg_dec<kRegsProducer>();
+    if (lane == 0) {
+      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+      const uint64_t dV = sdesc_sw128(smem_u32(sV), BN * 128, 1024);
+      const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);
+      constexpr uint32_t kTile16 = kRowTile >> 4;
+      uint32_t nV = 0, g = 0, un = 0;
+      bool ok = true;
+      while (any && ok) {
+        // The unit is read behind the barrier of its first weights.
+        int nks = 1, next_h = -1;
+        for (int t = 0; t < nks; ++t, ++g) {
+          if (!(ok = mbar_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
+          if (t == 0) {
+            nks = bars->units[un % kUnitRing].nks;
+            next_h = bars->units[un % kUnitRing].next_h;
+          }
+          const int sv = nV % NV;
+          if (!(ok = mbar_wait(&bars->fullV[sv], (nV / NV) & 1, wait_ns, abort))) break;
+          // The first PV into each accumulator of a unit overwrites it: the
+          // previous unit's epilogue must have read both.
+          if (t < 2 && un > 0 && !(ok = mbar_wait(&bars->o_free, (un - 1) & 1, wait_ns, abort))) break;
+          tc_fence_after();
+          const uint64_t dv = dV + sv * kTile16;
+          const uint64_t dp = dP + (g & 1) * (kQTile >> 4);
+          const uint32_t od = tmem + kColO + (g & 1) * D;
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ss(od, dp + kk * 2, dv + ((kk * 16 * 128) >> 4), idO, t >= 2 || kk > 0);
+          tc_commit(&bars->emptyV[sv]);
+          tc_commit(&bars->pv_done[g & 1]);
+          ++nV;
+        }
+        if (!ok) break;
+        tc_commit(&bars->o_full);
+        ++un;
+        if (next_h < 0) break;
+      }
+      if (!ok) report_timeout(abort, p.status);
+      tc_commit(&bars->pv_final);
+      mbar_wait_own(&bars->pv_final, 0, wait_ns);
+    }
+  } else {
+    // ============================ softmax warps ============================
+    setmaxnreg_inc<kRegsSoftmax>();
+    const int par = warp >> 2;  // step parity taken by this warp
+    const int quad = warp & 3;  // TMEM lane quadrant
+    const int a = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const float sl2 = p.scale_log2e;
+    uint32_t gt = 0, un = 0, nQ = 0;
+    int rb = 0;  // ring slot of the unit's distance tile -2 (continues across units)
+    bool store_pending = false;  // lane 0 has a TMA store out of this warp's P quadrant
+    bool ok = true;
+
+    // (q + u), (q + v) of a unit into buffer `buf` (128B-swizzled K-major
+    // tiles): this warp's row, head dimensions [32 par, 32 par + 32).
+    // bu_l, bv_l: this lane's dims 32 par + lane of the unit's u and v (loaded
+    // ahead by the caller, so their latency overlaps other work).
+    auto build_q = [&](int buf, float bu_l, float bv_l) -> bool {
+      // This warp's 32 dims of u and v, staged once for broadcast reads.
+      float* sb_w = sbias + warp * 64;
+      sb_w[lane] = bu_l;
+      sb_w[32 + lane] = bv_l;
+      __syncwarp();
+      if (!warp_wait(&bars->q_full, nQ & 1, wait_ns, abort)) return false;
+      uint4 raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 4 * par + j;
+        raw[j] = *reinterpret_cast<const uint4*>(sQ + (a / 8) * 1024 + (a % 8) * 128 + ((c ^ (a % 8)) * 16));
+      }
+      warp_arrive(&bars->q_empty);
+      ++nQ;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 4 * par + j;
+        const int off = buf * kQTile + (a / 8) * 1024 + (a % 8) * 128 + ((c ^ (a % 8)) * 16);
+        const uint32_t w4[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        const float4 u0 = *reinterpret_cast<const float4*>(sb_w + 8 * j);
+        const float4 u1 = *reinterpret_cast<const float4*>(sb_w + 8 * j + 4);
+        const float4 v0 = *reinterpret_cast<const float4*>(sb_w + 32 + 8 * j);
+        const float4 v1 = *reinterpret_cast<const float4*>(sb_w + 32 + 8 * j + 4);
+        const float ub[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        const float vb[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t qu[4], qv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x0 = bf16_lo(w4[e]), x1 = bf16_hi(w4[e]);
+          qu[e] = pack_bf16x2((x0 + ub[2 * e]) * p.qsign, (x1 + ub[2 * e + 1]) * p.qsign);
+          qv[e] = pack_bf16x2((x0 + vb[2 * e]) * p.qsign, (x1 + vb[2 * e + 1]) * p.qsign);
+        }
+        *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[0], qu[1], qu[2], qu[3]);
+        *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[0], qv[1], qv[2], qv[3]);
+      }
+      warp_arrive_smem(&bars->q_ready);
+      __syncwarp();  // sb_w is rewritten by the next build
+      return true;
+    };
+
+    auto bias_of = [&](int h, const float* bias) -> float { return __ldg(bias + h * D + 32 * par + lane); };
+    if (any) ok = build_q(0, bias_of(bars->units[0].h, p.bias_u), bias_of(bars->units[0].h, p.bias_v));
+
+    while (any && ok) {
+      // Published before the q tile that the build above waited for.
+      const TileUnit* unit = &bars->units[un % kUnitRing];
+      const int next_h = unit->next_h, nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
+      const uint32_t g0 = gt;
+      const bool has_next = next_h >= 0;
+      const float bu_next = has_next ? bias_of(next_h, p.bias_u) : 0.f;
+      const float bv_next = has_next ? bias_of(next_h, p.bias_v) : 0.f;
+      const int tl = nks - 1;
+      const int first = (par - static_cast<int>(g0)) & 1;  // first local step of this warp
+      float m_use = -INFINITY;  // running max in log2 units (lazy)
+      float l_run = 0.f;
+      for (int t = first; t <= tl; t += 2) {
+        const uint32_t g = g0 + t, sb = g & 1;
+        if (!(ok = warp_wait(&bars->s_full[sb], (g >> 1) & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        // Distance window of this warp: ring-relative index z = 64 + a - c
+        // (z < 64: tile t, < 128: tile t-1, else tile t-2).  Columns 0-31 use
+        // z in [32 quad + 32, 32 quad + 96), columns 32-63 z in
+        // [32 quad, 32 quad + 64); lane l of column k (within its half) sits
+        // at window position l + 32 - k.
+        auto zcol = [&](int z) -> uint32_t {
+          return kColG + ((rb + t - (z >> 6) + 2) & (kSlots - 1)) * BN + (z & 63);
+        };
+        const uint32_t sc = tmem + lane_base + kColS + sb * BN;
+        const int kt = t0 + t;              // key step of the tile
+        const int lim = d0 - BN * kt + a;   // column c visible iff low <= c <= lim
+        const int low = start - BN * kt;
+        const bool diag = d0 - BN * kt + quad * 32 < 63 || low > 0;  // some lane of the warp masks
+        const float m_old = m_use;
+        float m_new = m_use;
+        // All of this step's TMEM reads at once -- the 96-distance window and
+        // both halves of S -- then one arrival hands the S buffer and the
+        // ring slots back to the MMA issuers.
+        float x[64];  // scores of the step's 64 columns
+        {
+          uint32_t bd0[16], bd1[16];
+          uint32_t s0[32], s1[32];
+          {
+            uint32_t xa[32], xb[32], xc[32];
+            tmem_ld32(tmem + lane_base + zcol(32 * quad), xa);
+            tmem_ld32(tmem + lane_base + zcol(32 * quad + 32), xb);
+            tmem_ld32(tmem + lane_base + zcol(32 * quad + 64), xc);
+            tmem_ld32(sc, s0);
+            tmem_ld32(sc + 32, s1);
+            tmem_wait_ld(xa);
+            tmem_wait_ld(xb);
+            tmem_wait_ld(xc);
+            tmem_wait_ld(s0);
+            tmem_wait_ld(s1);
+            warp_arrive_tc(&bars->sread[g & 3]);
+            uint32_t pa[16], pb[16], pc[16];
+            pack32(xa, pa);
+            pack32(xb, pb);
+            pack32(xc, pc);
+            // columns 0-31 use window positions [32, 96), columns 32-63 [0, 64)
+            window_shift_packed(pb, pc, lane, bd0);
+            window_shift_packed(pa, pb, lane, bd1);
+          }
+          float* x0 = x;
+          float* x1 = x + 32;
+          add_window(s0, bd0, x0);
+          add_window(s1, bd1, x1);
+        }
+        if (diag) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) x[k] = (k <= lim && k >= low) ? x[k] : -INFINITY;
+        }
+        // Lazy running max over the step's 64 scores (log2 units).
+        float t3[22];
+#pragma unroll
+        for (int n = 0; n < 21; ++n) t3[n] = max3f(x[3 * n], x[3 * n + 1], x[3 * n + 2]);
+        t3[21] = x[63];
+        float u7[8];
+#pragma unroll
+        for (int n = 0; n < 7; ++n) u7[n] = max3f(t3[3 * n], t3[3 * n + 1], t3[3 * n + 2]);
+        u7[7] = t3[21];
+        const float mx = max3f(max3f(u7[0], u7[1], u7[2]), max3f(u7[3], u7[4], u7[5]), fmaxf(u7[6], u7[7])) * sl2;
+        if (mx > m_new + kLazy) m_new = mx;
+        const float alpha = (m_old == -INFINITY) ? 0.f : ex2(m_old - m_new);  // m_new >= m_old
+        // The PV of step g-2 (same P buffer, same accumulator) must be done
+        // before P is overwritten or O rescaled.
+        if (g >= 2 && !(ok = warp_wait(&bars->pv_done[sb], ((g - 2) >> 1) & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        if (t > first && __any_sync(0xffffffffu, m_new > m_old)) {
+          // O of this parity holds PV up to step t-2; rescale it in place.
+          const uint32_t oc0 = tmem + lane_base + kColO + par * D;
+#pragma unroll
+          for (int oc = 0; oc < D / 32; ++oc) {
+            uint32_t ov[32];
+            tmem_ld32(oc0 + oc * 32, ov);
+            tmem_wait_ld(ov);
+#pragma unroll
+            for (int n = 0; n < 32; ++n) ov[n] = __float_as_uint(__uint_as_float(ov[n]) * alpha);
+            tmem_st32(oc0 + oc * 32, ov);
+          }
+          tmem_wait_st();
+        }
+        m_use = m_new;
+        if (store_pending) {  // the last epilogue staged its output here
+          if (lane == 0) bulk_wait_group_read0();
+          __syncwarp();
+          store_pending = false;
+        }
+        // A row with no visible key yet keeps m_new = -inf; its exponents are
+        // then taken against 0 (all -inf, so every p is 0).
+        const float m_eff = (m_new == -INFINITY) ? 0.f : m_new;
+        float sum;
+        {
+          // Exponentials, their row sum, and the P row a into buffer sb
+          // (128B-swizzled K-major, as (q+u)), eight columns per store.
+          uint8_t* prow = sP + sb * kQTile + (a / 8) * 1024 + (a % 8) * 128;
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+          const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_eff, -m_eff);
+#pragma unroll
+          for (int c = 0; c < BN / 8; ++c) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int n = 4 * c + i;
+              const float2 y = __ffma2_rn(make_float2(x[2 * n], x[2 * n + 1]), sc2, nm2);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              if (i & 1)
+                acc1 = __fadd2_rn(acc1, e);
+              else
+                acc0 = __fadd2_rn(acc0, e);
+              pk[i] = pack_bf16x2(e.x, e.y);
+            }
+            *reinterpret_cast<uint4*>(prow + ((c ^ (a % 8)) * 16)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        }
+        l_run = l_run * alpha + sum;
+        // The next unit's (q+u), (q+v) go to the other buffer once this
+        // warp's first step of this unit has seen its scores: the MMAs of the
+        // unit before, which read that buffer, are complete by then.
+        bool build = t == first && has_next;
+        if (has_dead_rows(*unit, kt)) {
+          // The value tile may wait in the loader's queue behind the load of
+          // the q after next, which waits for this build: so that goes first.
+          if (build && !(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
+          build = false;
+          // The stage's phases go by in order before this warp: the P.V two
+          // steps back is done, and the stage is refilled only after this
+          // step's.
+          if (!(ok = warp_wait(&bars->fullV[g % NV], (g / NV) & 1, wait_ns, abort))) break;
+          zero_dead_rows<D>(*unit, kt, sV + (g % NV) * kRowTile, quad, 4, lane);
+        }
+        tc_fence_before();  // orders the O rescale's tcgen05.st before the arrive
+        warp_arrive_smem(&bars->p_full[sb]);
+        if (build && !(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
+      }
+      if (!ok) break;
+      if (first > tl && has_next) {
+        // No step of this unit: build after its last step's scores instead.
+        const uint32_t gl = g0 + tl;
+        if (!(ok = warp_wait(&bars->s_full[gl & 1], (gl >> 1) & 1, wait_ns, abort))) break;
+        if (!(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
+      }
+      // The warps of the unit's last step merge the two accumulators and
+      // write the output; the other parity hands over its (m, l) and moves on
+      // to the next unit, whose first step is its own.
+      float* rm = red + (un & 1) * 2 * BM;
+      const int owner = static_cast<int>((g0 + tl) & 1);
+      if (par != owner) {
+        // The owner of the previous unit has read that unit's (m, l).
+        if (un > 0 && !(ok = warp_wait(&bars->lfree[quad], (un - 1) & 1, wait_ns, abort))) break;
+        rm[a] = m_use;
+        rm[BM + a] = l_run;
+        mbar_arrive(&bars->lbar[quad]);
+      } else {
+        if (!(ok = warp_wait(&bars->lbar[quad], un & 1, wait_ns, abort))) break;
+        const float m1 = rm[a], l1 = rm[BM + a];
+        warp_arrive(&bars->lfree[quad]);
+        if (!(ok = warp_wait(&bars->o_full, un & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        // merge this parity's accumulator (0) with the other's (1)
+        const bool has0 = first <= tl;        // this warp had steps
+        const bool has1 = (first ^ 1) <= tl;  // the other parity's warp had steps
+        const float m = fmaxf(has0 ? m_use : -INFINITY, has1 ? m1 : -INFINITY);
+        const bool seen = m != -INFINITY;  // the row sees a key of this piece
+        const float a0 = (has0 && seen) ? ex2(m_use - m) : 0.f;
+        const float a1 = (has1 && seen) ? ex2(m1 - m) : 0.f;
+        const float l = a0 * l_run + a1 * l1;
+        const float inv_l = seen ? 1.f / l : 0.f;
+        const float lse2 = seen ? m + __log2f(l) : -INFINITY;
+        const float c0 = a0 * inv_l, c1 = a1 * inv_l;
+        // Read both accumulators into registers and hand them back to the PV
+        // issuer before the stores.
+        float ov[D];
+#pragma unroll
+        for (int oc = 0; oc < D / 32; ++oc) {
+          uint32_t t0[32], t1[32];
+          if (has0) {
+            tmem_ld32(tmem + lane_base + kColO + par * D + oc * 32, t0);
+            tmem_wait_ld(t0);
+          }
+          if (has1) {
+            tmem_ld32(tmem + lane_base + kColO + (par ^ 1) * D + oc * 32, t1);
+            tmem_wait_ld(t1);
+          }
+#pragma unroll
+          for (int n = 0; n < 32; ++n)
+            ov[oc * 32 + n] =
+                (has0 ? __uint_as_float(t0[n]) * c0 : 0.f) + (has1 ? __uint_as_float(t1[n]) * c1 : 0.f);
+        }
+        warp_arrive_tc(&bars->o_free);
+        const TileUnit w = *unit;
+        if (w.pieces > 1) {
+          store_piece<D, O_BF16>(w, quad, lane, ov, lse2, p.part, p.counters, p.o, p.lse, p.T, p.H);
+        } else if (O_BF16 && 32 * quad + 32 <= w.nq) {
+          // bf16 rows into this warp's quadrant of its own P buffer (free
+          // until its next step: the last PV that read it is complete), then
+          // one TMA store of the 32-row box, all of them the unit's.
+          uint8_t* orow_s = sP + par * kQTile + (a / 8) * 1024 + (a % 8) * 128;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4*>(orow_s + ((c ^ (a % 8)) * 16)) =
+                make_uint4(pack_bf16x2(ov[8 * c], ov[8 * c + 1]), pack_bf16x2(ov[8 * c + 2], ov[8 * c + 3]),
+                           pack_bf16x2(ov[8 * c + 4], ov[8 * c + 5]), pack_bf16x2(ov[8 * c + 6], ov[8 * c + 7]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm.o, sP + par * kQTile + quad * 4096, 0, w.h, w.row0 + 32 * quad);
+            bulk_commit_group();
+          }
+          store_pending = true;
+          if (p.lse != nullptr)
+            p.lse[static_cast<size_t>(w.h) * p.T + w.row0 + a] =
+                lse2 == -INFINITY ? -INFINITY : lse2 * 0.69314718055994531f;
+        } else {
+          store_row<D, O_BF16>(w, a, ov, lse2, p.o, p.lse, p.T, p.H);
+        }
+      }
+      if (!has_next) break;
+      gt = g0 + nks;
+      ++un;
+      rb = (rb + nks + 2) & (kSlots - 1);
+    }
+    if (!ok) report_timeout(abort, p.status);
+    // Output stores in flight must finish before the CTA's shared memory goes.
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool O_BF16>
+cudaError_t launch(const TileMaps& m, const TileParams& p, int sms, cudaStream_t stream) {
+  auto kern = paged_tc64_kernel<O_BF16>;
+  static unsigned configured = 0;  // one bit per device ordinal < 32
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 32 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1u << dev))) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
+      return e;
+    if (dev < 32) __atomic_fetch_or(&configured, 1u << dev, __ATOMIC_RELEASE);
+  }
+  return launch_dependent(kern, dim3(sms), dim3(kThreads), kSmemBytes, stream, m, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc64(const TileMaps& m, const TileParams& p, bool o_bf16, int sms, cudaStream_t stream) {
+  return o_bf16 ? launch<true>(m, p, sms, stream) : launch<false>(m, p, sms, stream);
+}
+
+}  // namespace txl
