@@ -194,3 +194,40 @@ def tolerance(q, k, v, r, u, vb, scale, step, terms, out_step):
             do[t, h] = (p * e) @ (va[:seen, h] + np.abs(o[t, h])) + out_step * np.abs(o[t, h])
             dl[h, t] = p @ e + step * abs(lse[h, t])
     return o, lse, do, dl
+
+
+def spread(q, k, v, r, u, vb, scale, step, out_step):
+    """The sum over all elements of o of the variance that independent
+    roundings give them to first order, an upper bound.
+
+    A rounding to nearest moves a value x by at most step * |x|, evenly spread,
+    so its variance is at most s2 x^2, s2 = step^2 / 3.  With z_j = scale
+    (a . k_j + b . r_j), a = q + u, b = q + v, and o = sum_j p_j v_j,
+    do = sum_j p_j (v_j - o) dz_j, so per element of o
+      a rounded:            s2 sum_d (scale a_d)^2 (sum_j p_j (v_j - o) k_jd)^2
+      b rounded:            the same with b and r_j
+      b . r_j rounded:      s2 sum_j (p_j (v_j - o) scale b.r_j)^2
+      p_j rounded (for the product with v alone):  s2 sum_j (p_j v_j)^2
+      o rounded:            (out_step^2 / 3) o^2.
+    """
+    q, k, v, r, u, vb = (np.asarray(x, np.float64) for x in (q, k, v, r, u, vb))
+    o, lse, _ = attend(q, k, v, r, u, vb, scale)
+    n, H, _ = o.shape
+    m = len(k) - n
+    s2 = step ** 2 / 3
+    total = out_step ** 2 / 3 * (o ** 2).sum()
+    for h in range(H):
+        for t in range(n):
+            seen = m + t + 1
+            if seen <= 0:
+                continue
+            a, b = q[t, h] + u[h], q[t, h] + vb[h]
+            kk, rr, vv = k[:seen, h], r[m + t - np.arange(seen), h], v[:seen, h]
+            far = rr @ b
+            p = np.exp(scale * (kk @ a + far) - lse[h, t])[:, None]
+            away = p * (vv - o[t, h])  # [j, element]
+            total += s2 * (((scale * a) ** 2) @ (kk.T @ away) ** 2).sum()
+            total += s2 * (((scale * b) ** 2) @ (rr.T @ away) ** 2).sum()
+            total += s2 * ((away * (scale * far)[:, None]) ** 2).sum()
+            total += s2 * ((p * vv) ** 2).sum()
+    return total

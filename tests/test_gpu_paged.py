@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from gpu_util import BF16_REL_L2
-from oracle.pages_oracle import Book, tolerance
+from oracle.pages_oracle import Book, spread, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -94,7 +94,7 @@ def attend_case(txl, rng, spans, counts, P, H, D, dtype, o_dtype=None, slots=Non
     else:
         step, terms = 2.0 ** -24, 2 * D + longest
     out = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}[o.dtype]
-    num = den = 0.0
+    off = room = 0.0
     for i, s in enumerate(slots):
         rows = slice(cu[i], cu[i + 1])
         kk, vv = (book.gather(x.float().numpy(), s) for x in pools)
@@ -106,9 +106,11 @@ def attend_case(txl, rng, spans, counts, P, H, D, dtype, o_dtype=None, slots=Non
         none = np.isneginf(want_l)
         assert (np.isneginf(got_l[:, rows]) == none).all()
         assert (np.abs(got_l[:, rows][~none] - want_l[~none]) <= dl[~none] + 1e-6).all()
-        num, den = num + (e ** 2).sum(), den + (want ** 2).sum()
-    if dtype == torch.bfloat16 and den > 0:
-        assert (num / den) ** 0.5 <= BF16_REL_L2
+        if dtype == torch.bfloat16:  # the elements' worst case is wide: the whole is held to what roundings leave
+            off += (e ** 2).sum()
+            room += spread(q[rows].float().numpy(), kk, vv, r.float().numpy(), u.numpy(), vb.numpy(), scale, step, out)
+    # 1e-9: fp32 sums where nothing is rounded to bf16 (an output of fp32 that is one value row)
+    assert off <= room + 1e-9 * T * H * D
     assert (got[cu[-1]:] == 7.0).all() and (got_l[:, cu[-1]:] == 7.0).all()
     return args, kw
 
@@ -444,7 +446,7 @@ def test_a_server(txl, D, n):
     where = [0, 1, 2]
     r = (0.5 * torch.from_numpy(rng.normal(size=(M + n, H, D)))).to(BF).cuda()
     u, vb = (0.3 * torch.from_numpy(rng.normal(size=(H, D))).float().cuda() for _ in range(2))
-    num = den = 0.0
+    off = room = 0.0
     for step in range(12 if n > 1 else 130):
         counts = [n] * len(where) if n == 1 else rng.integers(1, n + 1, len(where)).tolist()
         cu = cu_of(counts)
@@ -462,7 +464,9 @@ def test_a_server(txl, D, n):
                                            vb.cpu().numpy(), D ** -0.5, 2.0 ** -8, 2, 2.0 ** -8)
                 e = np.abs(host[3][rows] - want)
                 assert (e <= do).all()
-                num, den = num + (e ** 2).sum(), den + (want ** 2).sum()
+                off += (e ** 2).sum()
+                room += spread(host[0][rows], kk, vv, r.float().cpu().numpy(), u.cpu().numpy(), vb.cpu().numpy(),
+                               D ** -0.5, 2.0 ** -8, 2.0 ** -8)
             model[i] = model[i][-M:]
         if step == 5:  # sequence 1 forks into slots 3 and 4
             ok = ints([0, 0])
@@ -478,7 +482,7 @@ def test_a_server(txl, D, n):
             assert not dev["refs"][live:].any()
             where, model = where[1:], model[1:]
     assert txl.txl_get_device_status() == 0
-    assert (num / den) ** 0.5 <= BF16_REL_L2
+    assert off <= room
 
 
 @pytest.mark.parametrize("n,max_new", [(1, 1), (30, 40)])

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import txl_oracle as O
-from oracle.pages_oracle import Book, attend, tolerance
+from oracle.pages_oracle import Book, attend, spread, tolerance
 
 INVALID, UNSUPPORTED, ALIAS = 1, 2, 3
 
@@ -114,8 +114,29 @@ def test_tolerance_covers_rounded_operands():
     assert (np.abs(rounded(0) - o) <= do).all()
     # The elements' worst case is wide; what independent roundings leave of
     # the whole is not, and that bound tells a distance that is off by one.
-    off = [np.linalg.norm(rounded(shift) - o) / np.linalg.norm(o) for shift in (0, 1)]
-    assert off[0] <= 5e-3 and off[1] > 0.1
+    room = spread(q, k, v, r, u, vb, 0.125, 2.0 ** -8, 2.0 ** -8)
+    assert ((rounded(0) - o) ** 2).sum() <= room < ((rounded(1) - o) ** 2).sum() / 100
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.125, -0.2, 1.0])
+def test_spread_is_what_roundings_leave(scale):
+    """Over many draws the squared error is below the bound, and not far below."""
+    import torch
+
+    rng = np.random.default_rng(4)
+    bf = lambda x: torch.tensor(x).to(torch.bfloat16).double().numpy()  # noqa: E731
+    n, L, D = 1, 60, 64
+    got = room = 0.0
+    for _ in range(40):
+        q, k, v, r = (bf(rng.normal(size=(x, 1, D))) for x in (n, L, L, L))
+        r = 0.5 * r
+        u, vb = 0.3 * rng.normal(size=(1, D)), 0.3 * rng.normal(size=(1, D))
+        o, _, _ = attend(q, k, v, r, u, vb, scale)
+        z = scale * (bf(q[0, 0] + u[0]) @ k[:, 0].T + bf(bf(q[0, 0] + vb[0]) @ r[::-1, 0].T))
+        w = np.exp(z - z.max())
+        got += ((bf(bf(w) @ v[:, 0] / w.sum()) - o[0, 0]) ** 2).sum()
+        room += spread(q, k, v, r, u, vb, scale, 2.0 ** -8, 2.0 ** -8)
+    assert 0.1 * room <= got <= room
 
 
 @pytest.fixture(scope="module")
