@@ -212,8 +212,11 @@ def test_refused_entries_stay(txl, dtype, D, new):
     rows = [slice(i * new, (i + 1) * new) for i in range(6)]
     for i in (0, 2, 3, 4):
         assert (o[rows[i]] == 7.0).all()
+    # Which CTA has which key steps goes by the whole batch: the others' results may round elsewhere, and two results
+    # that are each within the tolerance of the exact one are within twice that of each other.
+    near = lambda a, b: ((a.double() - b.double()).norm() / b.double().norm()).item() <= 2 * BF16_REL_L2  # noqa: E731
     for i in (1, 5):
-        assert torch.equal(o[rows[i]], good[rows[i]])
+        assert near(o[rows[i]], good[rows[i]])
     # an entry with more rows than max_new is refused, as is one past q's end
     dev["rows"].fill_(new + 20)
     dev["start"].fill_(0)
@@ -222,7 +225,7 @@ def test_refused_entries_stay(txl, dtype, D, new):
     far[6] = len(q) + 1
     txl.txl_relattn_forward_paged(q, k, v, dev, slots, far, r, u, vb, o, ws, **kw)
     assert txl.txl_get_device_status() == 6
-    assert (o[rows[5]] == 7.0).all() and torch.equal(o[:5 * new], good[:5 * new])
+    assert (o[rows[5]] == 7.0).all() and near(o[:5 * new], good[:5 * new])
 
 
 @pytest.mark.parametrize("dtype,D,new", [(BF, 64, 1), (BF, 128, 90), (BF, 64, 90), (F32, 16, 5)])
