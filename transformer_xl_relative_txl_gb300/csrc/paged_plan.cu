@@ -212,7 +212,7 @@ cudaError_t launch_tiles(const PagedAttn& a, const PlanSpace& s, int sms, const 
   // The sign of the scale is folded into (q+u), (q+v) (exact in bf16); a zero
   // scale becomes 1e-30, for which every visible exponent rounds to 2^0 in
   // fp32 exactly as with 0, while masked keys keep an exponent of -inf.
-  const TileParams p{b, a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H,
+  const TileParams p{b, __builtin_ctz(b.page_rows), a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H,
                      std::max(std::fabs(a.scale), 1e-30f) * 1.4426950408889634f, a.scale < 0.f ? -1.f : 1.f,
                      s.heads + 1, s.seqs[1], s.starts[1], s.counters[1], s.part[1], wc.status, wc.limit_ns};
   return a.D == 64 ? launch_paged_tc64(m, p, a.o_bf16, sms, stream)

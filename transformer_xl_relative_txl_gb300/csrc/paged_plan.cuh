@@ -66,12 +66,11 @@ struct Piece {
   int t0, nks, first, index, pieces;
 };
 
-// CTA c's piece of the unit at cost position a with `steps` key steps from
-// step `base`; nks = 0: none of its steps are c's.
+// CTA c's (range [lo, hi)) piece of the unit at cost position a with `steps`
+// key steps from step `base`; nks = 0: none of its steps are c's.
 template <typename Cost>
-__host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int base, int c, long long total,
-                                                     int ctas) {
-  const long long lo = c * total / ctas, hi = (c + 1LL) * total / ctas;
+__host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int base, int c, long long lo,
+                                                     long long hi, long long total, int ctas) {
   const long long s0 = a + Cost::kUnit;
   long long from = lo < s0 ? 0 : (lo - s0) / Cost::kStep;
   long long to = hi < s0 ? 0 : (hi - s0) / Cost::kStep;
@@ -80,9 +79,14 @@ __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int
   Piece p;
   p.t0 = base + static_cast<int>(from);
   p.nks = static_cast<int>(to - from);
-  p.first = plan_owner(s0 + Cost::kStep - 1, total, ctas);
-  p.index = c - p.first;
-  p.pieces = plan_owner(s0 + static_cast<long long>(Cost::kStep) * steps - 1, total, ctas) - p.first + 1;
+  p.first = c;
+  p.index = 0;
+  p.pieces = 1;
+  if (p.nks > 0 && p.nks < steps) {
+    p.first = plan_owner(s0 + Cost::kStep - 1, total, ctas);
+    p.index = c - p.first;
+    p.pieces = plan_owner(s0 + static_cast<long long>(Cost::kStep) * steps - 1, total, ctas) - p.first + 1;
+  }
   return p;
 }
 
@@ -99,7 +103,7 @@ struct PlanWalk {
   PlanHead head;
   int H, c, i, h, qt;
   PlanSeq s;
-  long long a, hi;  // cost position of the unit, end of the CTA's range
+  long long a, lo, hi;  // cost position of the unit, the CTA's range
   Piece p;
 
   __host__ __device__ __forceinline__ int steps_of(int tile) const {
@@ -127,7 +131,7 @@ struct PlanWalk {
     if (c >= head.ctas) return false;
     i = starts[c];
     s = seqs[i];
-    const long long lo = c * head.total / head.ctas;
+    lo = c * head.total / head.ctas;
     hi = (c + 1LL) * head.total / head.ctas;
     const long long per = cost_of_head();
     h = static_cast<int>((lo - s.pre) / per);
@@ -152,7 +156,7 @@ struct PlanWalk {
   }
   __host__ __device__ __forceinline__ bool settle() {
     for (; i < head.count && a < hi; step_unit()) {
-      p = plan_piece<Cost>(a, steps_of(qt), s.start / BK, c, head.total, head.ctas);
+      p = plan_piece<Cost>(a, steps_of(qt), s.start / BK, c, lo, hi, head.total, head.ctas);
       if (p.nks > 0) return true;
     }
     return false;

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
       tma_prefetch_desc(&tm.r);
       uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
       bool ok = true;
-      const PageMap pm(p.book);
+      const PageMap pm(p.book, p.log_page_rows);
       auto acquire = [&](uint64_t* empty, uint64_t* full, uint32_t n, int ns, int bytes) -> bool {
         const int s = static_cast<int>(n % ns);
         if (!mbar_wait(&empty[s], ((n / ns) & 1) ^ 1, wait_ns, abort)) return false;

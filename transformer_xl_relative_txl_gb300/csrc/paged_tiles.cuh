@@ -50,35 +50,33 @@ __device__ __forceinline__ void publish_unit(TileWalk& walk, TileUnit* ring, uin
 }
 
 // The pages of a 64-row key tile, in boxes of min(page_rows, 64) rows.
+// (Page rows stay below 2^30, so a tile's row numbers are ints.)
 struct TilePages {
-  int id[4];  // -1: the box holds no live row
+  int id[4];  // of the boxes that hold a live row
 };
 struct PageMap {
   const int* table;
-  int max_pages, n_pages, page_rows, box, boxes;
-  __device__ __forceinline__ explicit PageMap(const PageBook& b)
-      : table(b.table), max_pages(b.max_pages), n_pages(b.n_pages), page_rows(b.page_rows),
-        box(min(b.page_rows, kStepKeys)), boxes(kStepKeys / min(b.page_rows, kStepKeys)) {}
+  int max_pages, n_pages, log_page, log_box, boxes;
+  __device__ __forceinline__ PageMap(const PageBook& b, int log_page_rows)
+      : table(b.table), max_pages(b.max_pages), n_pages(b.n_pages), log_page(log_page_rows),
+        log_box(min(log_page_rows, 6)), boxes(kStepKeys >> min(log_page_rows, 6)) {}
+  // Whether box y of tile t holds a live row.
+  __device__ __forceinline__ bool live(const TileUnit& u, int t, int y) const {
+    const int x = t * kStepKeys + (y << log_box);
+    return y < boxes && x <= u.last && x + (1 << log_box) > u.start;
+  }
   __device__ __forceinline__ TilePages pages(const TileUnit& u, int t) const {
+    const int* row = table + static_cast<size_t>(u.slot) * max_pages;
     TilePages p;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const long long x = static_cast<long long>(t) * kStepKeys + y * box;
-      p.id[y] = -1;
-      if (y < boxes && x <= u.last && x + box > u.start)
-        p.id[y] = table[static_cast<size_t>(u.slot) * max_pages + x / page_rows];
-    }
+    for (int y = 0; y < 4; ++y) p.id[y] = live(u, t, y) ? row[(t * kStepKeys + (y << log_box)) >> log_page] : 0;
     return p;
-  }
-  // Whether box y holds live rows; a page out of range then reads as zeros
-  // (a TMA box outside its tensor) and is reported.
-  __device__ __forceinline__ bool live(const TileUnit& u, int t, int y) const {
-    const long long x = static_cast<long long>(t) * kStepKeys + y * box;
-    return y < boxes && x <= u.last && x + box > u.start;
   }
 };
 
-// Loads tile t of unit u into a stage of D / 64 chunks of 64 rows x 128 bytes.
+// Loads tile t of unit u into a stage of D / 64 chunks of 64 rows x 128
+// bytes.  A page out of range reads as zeros (a TMA box outside its tensor)
+// and is reported.
 template <int D>
 __device__ __forceinline__ void load_tile(const PageMap& m, const TileUnit& u, int t, const TilePages& pg,
                                           const CUtensorMap* map, uint8_t* stage, uint64_t* full,
@@ -86,19 +84,19 @@ __device__ __forceinline__ void load_tile(const PageMap& m, const TileUnit& u, i
   int n = 0;
 #pragma unroll
   for (int y = 0; y < 4; ++y) n += m.live(u, t, y) ? 1 : 0;
-  mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) * m.box * D * 2);
+  mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) << (m.log_box + (D == 64 ? 7 : 8)));
+  const int x = (t * kStepKeys) & ((1 << m.log_page) - 1);  // row in the page; 0 for pages of up to 64 rows
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
     if (!m.live(u, t, y)) continue;
     int page = pg.id[y];
-    if (page < 0 || page >= m.n_pages) {
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(m.n_pages)) {
       atomicOr(status, kStatusPagesBit);
       page = m.n_pages;
     }
-    const int x = static_cast<int>((static_cast<long long>(t) * kStepKeys + y * m.box) % m.page_rows);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      tma_load_4d(stage + c * kStepKeys * 128 + y * m.box * 128, map, full, c * 64, x, u.h, page);
+      tma_load_4d(stage + c * kStepKeys * 128 + (y << (m.log_box + 7)), map, full, c * 64, x, u.h, page);
   }
 }
 
@@ -215,6 +213,7 @@ __device__ __forceinline__ void store_piece(const TileUnit& u, int quad, int lan
 // Kernel parameters common to both.
 struct TileParams {
   PageBook book;
+  int log_page_rows;
   const float* bias_u;
   const float* bias_v;
   void* o;
