@@ -49,7 +49,7 @@ constexpr int kRowChunk = BN * 128;  // 64 rows x 128 B
 constexpr int kRowTile = kChunks * kRowChunk;
 constexpr int kQChunk = BM * 128;    // 128 rows x 128 B
 constexpr int kQTile = kChunks * kQChunk;
-constexpr int NK = 2, NV = 2, NR = 2;
+constexpr int NK = 2, NV = 2, NR = 2;  // the loader takes one stage count
 constexpr int kOffQ = 0;
 constexpr int kOffQu = kOffQ + kQTile;
 constexpr int kOffQv = kOffQu + kQTile;
@@ -72,6 +72,7 @@ struct Bars {
   uint64_t xbar[4];  // row-max exchange of warps quad and quad+4 (64 arrivals per step)
   uint64_t lbar[4];  // row-sum hand-over at the end of a unit (32 arrivals)
   TileUnit units[kUnitRing];
+  TileWalk walk;
   int any;  // the CTA has a unit
   uint32_t tmem_base;
   int abort;
@@ -136,11 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  TileWalk walk;
   if (threadIdx.x == kLoaderWarp * 32) {
-    const bool some = walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+    const bool some = bars->walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
     bars->any = some ? 1 : 0;
-    if (some) publish_unit(walk, bars->units, 0);
+    if (some) publish_unit(bars->walk, bars->units, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -151,65 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
 
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
-    if (lane == 0) {
-      tma_prefetch_desc(&tm.q);
-      tma_prefetch_desc(&tm.k);
-      tma_prefetch_desc(&tm.v);
-      tma_prefetch_desc(&tm.r);
-      uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
-      bool ok = true;
-      const PageMap pm(p.book, p.log_page_rows);
-      auto acquire = [&](uint64_t* empty, uint64_t* full, uint32_t n, int ns, int bytes) -> bool {
-        const int s = static_cast<int>(n % ns);
-        if (!mbar_wait(&empty[s], ((n / ns) & 1) ^ 1, wait_ns, abort)) return false;
-        mbar_arrive_expect_tx(&full[s], bytes);
-        return true;
-      };
-      for (uint32_t un = 0; any && ok; ++un) {
-        const TileUnit w = bars->units[un % kUnitRing];
-        if (w.next_h >= 0) publish_unit(walk, bars->units, un + 1);
-        if (!(ok = acquire(&bars->q_empty, &bars->q_full, nQ, 1, kQTile))) break;
-        for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + c * kQChunk, &tm.q, &bars->q_full, c * 64, w.h, w.row0);
-        ++nQ;
-        auto load_r = [&](int d0) -> bool {
-          if (!acquire(bars->emptyR, bars->fullR, nR, NR, kRowTile)) return false;
-          const int s = nR % NR;
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_3d(sR + s * kRowTile + c * kRowChunk, &tm.r, &bars->fullR[s], c * 64, w.h, d0);
-          ++nR;
-          return true;
-        };
-        TilePages next = pm.pages(w, w.t0);
-        // distance tiles -2 and -1 of the unit's first step
-        ok = load_r(w.d0 - BN * (w.t0 - 1)) && load_r(w.d0 - BN * w.t0);
-        for (int t = w.t0; ok && t < w.t0 + w.nks; ++t) {
-          const TilePages pages = next;
-          if (t + 1 < w.t0 + w.nks) next = pm.pages(w, t + 1);  // on its way while this tile's loads are issued
-          int s = static_cast<int>(nK % NK);
-          if (!(ok = mbar_wait(&bars->emptyK[s], ((nK / NK) & 1) ^ 1, wait_ns, abort))) break;
-          load_tile<D>(pm, w, t, pages, &tm.k, sK + s * kRowTile, &bars->fullK[s], p.status);
-          ++nK;
-          if (!(ok = load_r(w.d0 - BN * (t + 1)))) break;
-          s = static_cast<int>(nV % NV);
-          if (!(ok = mbar_wait(&bars->emptyV[s], ((nV / NV) & 1) ^ 1, wait_ns, abort))) break;
-          load_tile<D>(pm, w, t, pages, &tm.v, sV + s * kRowTile, &bars->fullV[s], p.status);
-          ++nV;
-        }
-        if (w.next_h < 0) break;
-      }
-      if (!ok) report_timeout(abort, p.status);
-      // Let this thread's own copies land before the CTA may exit.
-      auto drain = [&](uint64_t* full, uint32_t n, int ns) {
-        for (int s = 0; s < ns && static_cast<uint32_t>(s) < n; ++s) {
-          const uint32_t last = s + ((n - 1 - s) / ns) * ns;
-          mbar_wait_own(&full[s], (last / ns) & 1, wait_ns);
-        }
-      };
-      drain(&bars->q_full, nQ, 1);
-      drain(bars->fullK, nK, NK);
-      drain(bars->fullV, nV, NV);
-      drain(bars->fullR, nR, NR);
-    }
+    run_tile_loader<D, NK, 0, false>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ============================ MMA issuer ===============================
     if (lane == 0) {

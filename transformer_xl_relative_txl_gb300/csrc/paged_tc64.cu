@@ -65,7 +65,7 @@ constexpr float kLazy = 8.0f;  // log2 headroom before a running max moves
 constexpr int kRowTile = BN * 128;  // 64 rows x 64 bf16 (8 KB)
 constexpr int kQTile = BM * 128;    // 128 rows x 64 bf16 (16 KB)
 constexpr int NK = 4, NV = 4, NR = 4;  // K, V, R tile stages
-static_assert(NK == NV, "K and V tiles share the loader's stage logic");
+static_assert(NK == NV && NK == NR, "the loader takes one stage count");
 constexpr int kOffQ = 0;                        // raw q tile of the next unit (TMA)
 constexpr int kOffQu = kOffQ + kQTile;          // (q+u): 2 buffers
 constexpr int kOffQv = kOffQu + 2 * kQTile;     // (q+v): 2 buffers
@@ -80,12 +80,6 @@ constexpr int kBarBytes = 1152;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
-struct VTile {
-  uint32_t unit;  // number of the CTA's unit
-  int t;          // key step
-  TilePages pages;
-};
-
 struct Bars {
   uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
   uint64_t q_full, q_empty;
@@ -94,8 +88,8 @@ struct Bars {
   uint64_t mma_final, pv_final, qr_final;
   uint64_t lbar[4];   // per quadrant: the non-owning warp's (m, l) of a unit is in `red`
   uint64_t lfree[4];  // per quadrant: the epilogue has read it
-  VTile vq[4];        // loader: queued V tiles, by V count % 4
   TileUnit units[kUnitRing];
+  TileWalk walk;
   int any;            // the CTA has a unit
   uint32_t tmem_base;
   int abort;
@@ -157,11 +151,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  TileWalk walk;
   if (threadIdx.x == kLoaderWarp * 32) {
-    const bool some = walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+    const bool some = bars->walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
     bars->any = some ? 1 : 0;
-    if (some) publish_unit(walk, bars->units, 0);
+    if (some) publish_unit(bars->walk, bars->units, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -173,95 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
     setmaxnreg_dec<kRegsProducer>();
-    if (lane == 0) {
-      tma_prefetch_desc(&tm.q);
-      tma_prefetch_desc(&tm.k);
-      tma_prefetch_desc(&tm.v);
-      tma_prefetch_desc(&tm.r);
-      uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
-      bool ok = true;
-      const PageMap pm(p.book, p.log_page_rows);
-      auto acquire = [&](uint64_t* empty, uint64_t* full, uint32_t n, int ns, int bytes) -> bool {
-        const int s = static_cast<int>(n % ns);
-        if (!mbar_wait(&empty[s], ((n / ns) & 1) ^ 1, wait_ns, abort)) return false;
-        mbar_arrive_expect_tx(&full[s], bytes);
-        return true;
-      };
-      // The raw q tile of a unit is loaded one unit ahead: the softmax warps
-      // build (q+u), (q+v) from it during the unit before.
-      auto load_q = [&](const TileUnit& w) -> bool {
-        if (!mbar_wait(&bars->q_empty, (nQ & 1) ^ 1, wait_ns, abort)) return false;
-        mbar_arrive_expect_tx(&bars->q_full, kQTile);
-        tma_load_3d(sQ, &tm.q, &bars->q_full, 0, w.h, w.row0);
-        ++nQ;
-        return true;
-      };
-      // V tiles trail the K and R tiles by kVLag tiles.  A V stage is freed
-      // only when the P.V MMA of its step completes, after that step's
-      // softmax, while a K stage is free as soon as its score MMA is done; in
-      // one issue order K(t), R(t+1), V(t), every K load would wait behind
-      // the V stage of step t-4 and land just in time.  Queued V tiles wait in
-      // bars->vq (this thread only).  Before the raw q of the unit after next
-      // is loaded, every queued V of a unit two or more back goes out: that
-      // load waits for the (q+u), (q+v) build of the next unit, which waits
-      // for the epilogue of the unit before, which needs all of that unit's V
-      // tiles (a unit of one step would otherwise hold them behind the load).
-      constexpr uint32_t kVLag = 2;
-      uint32_t nVq = 0;  // V tiles queued; nVq - nV of them not yet issued
-      auto issue_v = [&]() -> bool {
-        const VTile& e = bars->vq[nV % 4];
-        const int s = static_cast<int>(nV % NV);
-        if (!mbar_wait(&bars->emptyV[s], ((nV / NV) & 1) ^ 1, wait_ns, abort)) return false;
-        load_tile<D>(pm, bars->units[e.unit % kUnitRing], e.t, e.pages, &tm.v, sV + s * kRowTile, &bars->fullV[s],
-                     p.status);
-        ++nV;
-        return true;
-      };
-      if (any) ok = load_q(bars->units[0]);
-      for (uint32_t un = 0; any && ok; ++un) {
-        const TileUnit w = bars->units[un % kUnitRing];
-        while (ok && nV < nVq && bars->vq[nV % 4].unit + 2 <= un) ok = issue_v();
-        if (!ok) break;
-        if (w.next_h >= 0) {
-          publish_unit(walk, bars->units, un + 1);
-          if (!(ok = load_q(bars->units[(un + 1) % kUnitRing]))) break;
-        }
-        auto load_r = [&](int d0) -> bool {
-          if (!acquire(bars->emptyR, bars->fullR, nR, NR, kRowTile)) return false;
-          tma_load_3d(sR + (nR % NR) * kRowTile, &tm.r, &bars->fullR[nR % NR], 0, w.h, d0);
-          ++nR;
-          return true;
-        };
-        TilePages next = pm.pages(w, w.t0);
-        // distance tiles -2 and -1 of the unit's first step
-        ok = load_r(w.d0 - BN * (w.t0 - 1)) && load_r(w.d0 - BN * w.t0);
-        for (int t = w.t0; ok && t < w.t0 + w.nks; ++t) {
-          const TilePages pages = next;
-          if (t + 1 < w.t0 + w.nks) next = pm.pages(w, t + 1);  // on its way while this tile's loads are issued
-          const int s = static_cast<int>(nK % NK);
-          if (!(ok = mbar_wait(&bars->emptyK[s], ((nK / NK) & 1) ^ 1, wait_ns, abort))) break;
-          load_tile<D>(pm, w, t, pages, &tm.k, sK + s * kRowTile, &bars->fullK[s], p.status);
-          ++nK;
-          if (!(ok = load_r(w.d0 - BN * (t + 1)))) break;
-          bars->vq[nVq % 4] = VTile{un, t, pages};
-          ++nVq;
-          if (nVq - nV > kVLag) ok = issue_v();
-        }
-        if (w.next_h < 0) break;
-      }
-      while (ok && nV < nVq) ok = issue_v();  // the last kVLag V tiles
-      if (!ok) report_timeout(abort, p.status);
-      auto drain = [&](uint64_t* full, uint32_t n, int ns) {
-        for (int s = 0; s < ns && static_cast<uint32_t>(s) < n; ++s) {
-          const uint32_t last = s + ((n - 1 - s) / ns) * ns;
-          mbar_wait_own(&full[s], (last / ns) & 1, wait_ns);
-        }
-      };
-      drain(&bars->q_full, nQ, 1);
-      drain(bars->fullK, nK, NK);
-      drain(bars->fullV, nV, NV);
-      drain(bars->fullR, nR, NR);
-    }
+    run_tile_loader<D, NK, 2, true>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ===================== content-score MMA issuer ========================
     setmaxnreg_dec<kRegsProducer>();

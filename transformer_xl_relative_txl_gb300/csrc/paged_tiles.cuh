@@ -49,57 +49,6 @@ __device__ __forceinline__ void publish_unit(TileWalk& walk, TileUnit* ring, uin
   ring[k % kUnitRing] = u;
 }
 
-// The pages of a 64-row key tile, in boxes of min(page_rows, 64) rows.
-// (Page rows stay below 2^30, so a tile's row numbers are ints.)
-struct TilePages {
-  int id[4];  // of the boxes that hold a live row
-};
-struct PageMap {
-  const int* table;
-  int max_pages, n_pages, log_page, log_box, boxes;
-  __device__ __forceinline__ PageMap(const PageBook& b, int log_page_rows)
-      : table(b.table), max_pages(b.max_pages), n_pages(b.n_pages), log_page(log_page_rows),
-        log_box(min(log_page_rows, 6)), boxes(kStepKeys >> min(log_page_rows, 6)) {}
-  // Whether box y of tile t holds a live row.
-  __device__ __forceinline__ bool live(const TileUnit& u, int t, int y) const {
-    const int x = t * kStepKeys + (y << log_box);
-    return y < boxes && x <= u.last && x + (1 << log_box) > u.start;
-  }
-  __device__ __forceinline__ TilePages pages(const TileUnit& u, int t) const {
-    const int* row = table + static_cast<size_t>(u.slot) * max_pages;
-    TilePages p;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) p.id[y] = live(u, t, y) ? row[(t * kStepKeys + (y << log_box)) >> log_page] : 0;
-    return p;
-  }
-};
-
-// Loads tile t of unit u into a stage of D / 64 chunks of 64 rows x 128
-// bytes.  A page out of range reads as zeros (a TMA box outside its tensor)
-// and is reported.
-template <int D>
-__device__ __forceinline__ void load_tile(const PageMap& m, const TileUnit& u, int t, const TilePages& pg,
-                                          const CUtensorMap* map, uint8_t* stage, uint64_t* full,
-                                          unsigned int* status) {
-  int n = 0;
-#pragma unroll
-  for (int y = 0; y < 4; ++y) n += m.live(u, t, y) ? 1 : 0;
-  mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) << (m.log_box + (D == 64 ? 7 : 8)));
-  const int x = (t * kStepKeys) & ((1 << m.log_page) - 1);  // row in the page; 0 for pages of up to 64 rows
-#pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    if (!m.live(u, t, y)) continue;
-    int page = pg.id[y];
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(m.n_pages)) {
-      atomicOr(status, kStatusPagesBit);
-      page = m.n_pages;
-    }
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-      tma_load_4d(stage + c * kStepKeys * 128 + (y << (m.log_box + 7)), map, full, c * 64, x, u.h, page);
-  }
-}
-
 // Zeroes the rows of a landed value tile that are not live: weight 0 times a
 // leftover that is no number would not be 0.  The tile's rows are shared by
 // `warps` warps; the caller's proxy fence and arrival on the barrier that the
@@ -236,6 +185,171 @@ struct TileParams {
 struct TileMaps {
   CUtensorMap q, k, v, r, o;
 };
+
+// The loader warp of both kernels, all lanes in step: K, V and r tiles (and
+// the raw q tiles) of the CTA's units in order, and the units published.
+// Bars has the rings' barriers, the units and the walker (in shared memory:
+// it is used once per unit, and the warp has few registers).
+//
+// Pages.  A 64-row tile is one box of a page, or 2 or 4 boxes of pages of 32
+// or 16 rows.  Lane y (and 4 + y for V) has box y: its page id is fetched a
+// tile ahead, and one TMA instruction issues all the boxes.  Boxes without a
+// live row are left out; a page id out of range reads as zeros (a box outside
+// its tensor) and is reported.  With one lane doing all of it the loader bound
+// the kernel: 1.57 us a step at D = 64 where the softmax takes 0.8.
+//
+// LAG: V tiles trail the K and r tiles by so many.  A V stage is freed only
+// when the P.V MMA of its step completes, after that step's softmax, while a K
+// stage is free as soon as its score MMA is done; in one issue order K(t),
+// R(t+1), V(t), every K load would wait behind the V stage of step t - NS and
+// land just in time.  AHEAD: the raw q tile of a unit is loaded a unit ahead;
+// before that of the unit after next, every queued V of a unit two or more
+// back goes out, since the load waits for the (q+u), (q+v) build of the next
+// unit, which waits for the epilogue of the unit before, which needs all of
+// that unit's V tiles (a unit of one step would otherwise hold them behind the
+// load).
+template <int D, int NS, int LAG, bool AHEAD, typename Bars>
+__device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
+                                                uint8_t* sK, uint8_t* sV, uint8_t* sR) {
+  constexpr int kChunk = kStepKeys * 128, kTile = kChunk * (D / 64), kQChunk = kTileQueries * 128;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+  const uint64_t wait_ns = p.wait_ns;
+  const int log_page = p.log_page_rows, log_box = min(log_page, 6);
+  const int y = lane & 3;
+  const bool mine = lane < 8 && y < (kStepKeys >> log_box);
+  const int off = y << log_box;                  // first row of this lane's box in a tile
+  const uint32_t at = static_cast<uint32_t>(off) * 128;  // its place in a stage's chunk
+  if (lane == 0) {
+    tma_prefetch_desc(&tm.q);
+    tma_prefetch_desc(&tm.k);
+    tma_prefetch_desc(&tm.v);
+    tma_prefetch_desc(&tm.r);
+  }
+  uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
+  bool ok = bars->any != 0, bad = false;
+  const bool any = ok;
+
+  auto load_q = [&](uint32_t un) {
+    if (!(ok = warp_wait(&bars->q_empty, (nQ & 1) ^ 1, wait_ns, abort))) return;
+    if (lane == 0) {
+      const TileUnit& w = bars->units[un % kUnitRing];
+      mbar_arrive_expect_tx(&bars->q_full, kQChunk * (D / 64));
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tma_load_3d(sQ + c * kQChunk, &tm.q, &bars->q_full, c * 64, w.h, w.row0);
+    }
+    ++nQ;
+  };
+  auto load_r = [&](int h, int dist) {
+    const int s = static_cast<int>(nR % NS);
+    if (!(ok = ok && warp_wait(&bars->emptyR[s], ((nR / NS) & 1) ^ 1, wait_ns, abort))) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars->fullR[s], kTile);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(sR + s * kTile + c * kChunk, &tm.r, &bars->fullR[s], c * 64, h, dist);
+    }
+    ++nR;
+  };
+  // A tile of keys or values: this lane's page (-1: no live row), the row in
+  // the page, the head, the tile's bytes, the unit.
+  struct Tile {
+    int page, x, h;
+    uint32_t bytes, unit;
+  };
+  auto load_tile = [&](const Tile& e, uint64_t* empty, uint64_t* full, uint32_t& n, const CUtensorMap* map,
+                       uint8_t* stages, bool issues) {
+    const int s = static_cast<int>(n % NS);
+    if (!(ok = ok && warp_wait(&empty[s], ((n / NS) & 1) ^ 1, wait_ns, abort))) return;
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], e.bytes);
+    __syncwarp();
+    if (issues && e.page >= 0) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_4d(stages + s * kTile + c * kChunk + at, map, &full[s], c * 64, e.x, e.h, e.page);
+    }
+    ++n;
+  };
+  Tile queue[LAG > 0 ? LAG : 1];  // queue[0] the oldest
+  int queued = 0;
+  auto issue_v = [&](const Tile& e) {
+    load_tile(e, bars->emptyV, bars->fullV, nV, &tm.v, sV, lane >= 4);
+  };
+  auto pop_v = [&]() {
+    issue_v(queue[0]);
+#pragma unroll
+    for (int e = 0; e + 1 < LAG; ++e) queue[e] = queue[e + 1];
+    --queued;
+  };
+
+  if (AHEAD && any) load_q(0);
+  for (uint32_t un = 0; any && ok; ++un) {
+    const TileUnit& w = bars->units[un % kUnitRing];
+    const int next_h = w.next_h, h = w.h, d0 = w.d0, start = w.start, last = w.last, tend = w.t0 + w.nks;
+    const int* row = p.book.table + static_cast<size_t>(w.slot) * p.book.max_pages;
+    int t = w.t0;
+    if (LAG > 0)
+      while (ok && queued > 0 && queue[0].unit + 2 <= un) pop_v();
+    if (!ok) break;
+    if (next_h >= 0) {
+      if (lane == 0) publish_unit(bars->walk, bars->units, un + 1);
+      __syncwarp();
+      if (AHEAD) load_q(un + 1);
+    }
+    if (!AHEAD) load_q(un);
+    if (!ok) break;
+    auto live = [&](int tile) {
+      const int x = tile * kStepKeys + off;
+      return mine && x <= last && x + (1 << log_box) > start;
+    };
+    int id = live(t) ? row[(t * kStepKeys + off) >> log_page] : 0;
+    // distance tiles -2 and -1 of the unit's first step
+    load_r(h, d0 - kStepKeys * (t - 1));
+    load_r(h, d0 - kStepKeys * t);
+    for (; ok && t < tend; ++t) {
+      const bool lv = live(t);
+      Tile e;
+      e.page = -1;
+      if (lv) {
+        const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.book.n_pages);
+        bad |= !good;
+        e.page = good ? id : p.book.n_pages;
+      }
+      if (t + 1 < tend) id = live(t + 1) ? row[((t + 1) * kStepKeys + off) >> log_page] : 0;
+      e.bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lv) & 0xf)) << (log_box + (D == 64 ? 7 : 8));
+      e.x = (t * kStepKeys) & ((1 << log_page) - 1);  // 0 for pages of up to 64 rows
+      e.h = h;
+      e.unit = un;
+      load_tile(e, bars->emptyK, bars->fullK, nK, &tm.k, sK, lane < 4);
+      load_r(h, d0 - kStepKeys * (t + 1));
+      if (LAG == 0) {
+        issue_v(e);
+      } else {
+        if (ok && queued == LAG) pop_v();
+#pragma unroll
+        for (int q = 0; q < LAG; ++q)
+          if (q == queued) queue[q] = e;
+        ++queued;
+      }
+    }
+    if (next_h < 0) break;
+  }
+  if (LAG > 0)
+    while (ok && queued > 0) pop_v();
+  if (bad) atomicOr(p.status, kStatusPagesBit);
+  if (any && !ok && lane == 0) report_timeout(abort, p.status);
+  // This warp's own copies land before the CTA may exit.
+  auto drain = [&](uint64_t* full, uint32_t n, int ns) {
+    for (int s = 0; s < ns && static_cast<uint32_t>(s) < n; ++s) {
+      const uint32_t z = s + ((n - 1 - s) / ns) * ns;
+      mbar_wait_own(&full[s], (z / ns) & 1, wait_ns);
+    }
+  };
+  drain(&bars->q_full, nQ, 1);
+  drain(bars->fullK, nK, NS);
+  drain(bars->fullV, nV, NS);
+  drain(bars->fullR, nR, NS);
+}
 
 cudaError_t launch_paged_tc64(const TileMaps& m, const TileParams& p, bool o_bf16, int sms, cudaStream_t stream);
 cudaError_t launch_paged_tc128(const TileMaps& m, const TileParams& p, bool o_bf16, int sms, cudaStream_t stream);
