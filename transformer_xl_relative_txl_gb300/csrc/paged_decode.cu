@@ -440,7 +440,7 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCt
     if (!enc(&tm_r, a.r, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   Params p{b, static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H, a.n_r,
-           a.scale * 1.4426950408889634f, s.heads, s.seqs[0], s.starts[0], s.counters[0], s.part[0], wc.status,
+           a.scale * 1.4426950408889634f, s.heads, s.seqs[0], s.starts[0], s.counters, s.part[0], wc.status,
            wc.limit_ns};
   auto kern = paged_decode_kernel<D, O_BF16>;
   static unsigned configured = 0;  // one bit per device ordinal < 32

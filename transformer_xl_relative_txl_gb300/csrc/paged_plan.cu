@@ -110,7 +110,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PagedAttn a, const
     }
     sp.starts[kind][c] = x;
   }
-  for (int e = threadIdx.x; e < ctas * 4; e += kThreads) sp.counters[kind][e] = 0;
+  if (kind == 0)
+    for (int e = threadIdx.x; e < ctas * 4; e += kThreads) sp.counters[e] = 0;
+  else
+    for (int c = threadIdx.x; c < tile_ctas; c += kThreads) sp.cuts[c].pieces = 0;
 }
 
 }  // namespace
@@ -214,7 +217,7 @@ cudaError_t launch_tiles(const PagedAttn& a, const PlanSpace& s, int sms, const 
   // fp32 exactly as with 0, while masked keys keep an exponent of -inf.
   const TileParams p{b, __builtin_ctz(b.page_rows), a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H,
                      std::max(std::fabs(a.scale), 1e-30f) * 1.4426950408889634f, a.scale < 0.f ? -1.f : 1.f,
-                     s.heads + 1, s.seqs[1], s.starts[1], s.counters[1], s.part[1], wc.status, wc.limit_ns};
+                     s.heads + 1, s.seqs[1], s.starts[1], s.cuts, s.part[1], wc.status, wc.limit_ns};
   return a.D == 64 ? launch_paged_tc64(m, p, a.o_bf16, sms, stream)
                    : launch_paged_tc128(m, p, a.o_bf16, sms, stream);
 }
@@ -229,6 +232,7 @@ cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_
   cudaError_t e = launch_paged_plan(a, s, sms, wc.status, stream);
   if (e == cudaSuccess) e = launch_paged_decode(a, s, sms, wc, stream);
   if (e == cudaSuccess && a.max_new > kDecodeRows) e = launch_tiles(a, s, sms, wc, stream);
+  if (e == cudaSuccess && a.max_new > kDecodeRows) e = launch_paged_join(a, s, sms, stream);
   return e;
 }
 

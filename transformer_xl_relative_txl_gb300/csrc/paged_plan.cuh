@@ -176,12 +176,18 @@ __host__ __device__ __forceinline__ int plan_ctas(long long total, int count, in
   return count == 0 ? 0 : (want >= most ? most : (want < 1 ? 1 : static_cast<int>(want)));
 }
 
+// A tile unit that a cut divides, noted by the CTA that has its first piece.
+struct TileCut {
+  int row0, nq, h, pieces;  // pieces 0: none
+};
+
 // The workspace of a call.
 struct PlanSpace {
   PlanHead* heads;    // [2] decode, tiles
   int* starts[2];     // [CTAs of the kind] first sequence of each CTA
   PlanSeq* seqs[2];   // [n]
-  int* counters[2];   // [CTAs][4] pieces of the unit that the CTA starts which have arrived
+  int* counters;      // [decode CTAs][4] pieces of the unit that the CTA starts which have arrived
+  TileCut* cuts;      // [tile CTAs]
   float* part[2];     // [2 CTAs] partial results
 };
 constexpr int kDecodeCtas = kDecodePerSm * kMaxSms, kTileCtas = kMaxSms;
@@ -206,7 +212,10 @@ inline size_t plan_space(void* base, int n, int T, int D, PlanSpace* out) {
     if (k == 1 && !tiles) break;
     s.starts[k] = reinterpret_cast<int*>(take(ctas * sizeof(int)));
     s.seqs[k] = reinterpret_cast<PlanSeq*>(take(static_cast<size_t>(n) * sizeof(PlanSeq)));
-    s.counters[k] = reinterpret_cast<int*>(take(ctas * 4 * sizeof(int)));
+    if (k == 0)
+      s.counters = reinterpret_cast<int*>(take(ctas * 4 * sizeof(int)));
+    else
+      s.cuts = reinterpret_cast<TileCut*>(take(ctas * sizeof(TileCut)));
     s.part[k] = reinterpret_cast<float*>(
         take(2 * static_cast<size_t>(ctas) * (k == 0 ? decode_part(D) : tile_part(D)) * sizeof(float)));
   }
@@ -216,6 +225,7 @@ inline size_t plan_space(void* base, int n, int T, int D, PlanSpace* out) {
 
 cudaError_t launch_paged_plan(const PagedAttn& a, const PlanSpace& s, int decode_bk, int sms, unsigned int* status,
                               cudaStream_t stream);
+cudaError_t launch_paged_join(const PagedAttn& a, const PlanSpace& s, int sms, cudaStream_t stream);
 cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc,
                                 cudaStream_t stream);
 // The pieces of every CTA of a kind (0: decode at head dimension D, 1: tiles) for n valid sequences, as rows (cta,

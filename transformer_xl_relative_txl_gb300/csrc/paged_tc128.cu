@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
   if (threadIdx.x == kLoaderWarp * 32) {
     const bool some = bars->walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
     bars->any = some ? 1 : 0;
-    if (some) publish_unit(bars->walk, bars->units, 0);
+    if (some) publish_unit(bars->walk, bars->units, 0, p.cuts);
   }
   tc_fence_before();
   __syncthreads();
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         }
         warp_arrive_tc(&bars->o_free);
         if (unit->pieces > 1)
-          store_piece<D, O_BF16>(*unit, quad, lane, ov, lse2, p.part, p.counters, p.o, p.lse, p.T, p.H);
+          store_piece<D>(*unit, a, ov, lse2, p.part);
         else
           store_row<D, O_BF16>(*unit, a, ov, lse2, p.o, p.lse, p.T, p.H);
       } else if (unit->next_h >= 0 && !(ok = build_q(unit->next_h))) {

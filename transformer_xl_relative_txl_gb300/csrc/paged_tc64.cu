@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   if (threadIdx.x == kLoaderWarp * 32) {
     const bool some = bars->walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
     bars->any = some ? 1 : 0;
-    if (some) publish_unit(bars->walk, bars->units, 0);
+    if (some) publish_unit(bars->walk, bars->units, 0, p.cuts);
   }
   tc_fence_before();
   __syncthreads();
@@ -186,6 +186,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           const uint32_t g = g0 + t, sb = g & 1;
           // S buffer sb was last read by step g-2.
           if (g >= 2 && !(ok = mbar_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
+          // The two parities run best half a step's time apart.  They start
+          // together (their first steps wait for the same instruction fetches)
+          // and would stay so: 0.98 us a step instead of 0.8.  Once, the odd
+          // one's scores are held back until the even one has read its own.
+          if (g == 3 && !(ok = mbar_wait(&bars->sread[2], 0, wait_ns, abort))) break;
           const int sk = nK % NK;
           if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
           tc_fence_after();
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         warp_arrive_tc(&bars->o_free);
         const TileUnit w = *unit;
         if (w.pieces > 1) {
-          store_piece<D, O_BF16>(w, quad, lane, ov, lse2, p.part, p.counters, p.o, p.lse, p.T, p.H);
+          store_piece<D>(w, a, ov, lse2, p.part);
         } else if (O_BF16 && 32 * quad + 32 <= w.nq) {
           // bf16 rows into this warp's quadrant of its own P buffer (free
           // until its next step: the last PV that read it is complete), then

@@ -25,12 +25,13 @@ struct TileUnit {
   int d0;              // page row of query 0: query a sees rows start .. d0 + a at distance d0 + a - row
   int start, last;     // live page rows
   int slot;
-  int first, index, pieces;
+  int index, pieces;
   int next_h;          // head of the CTA's next unit, -1: none
 };
 
-// The walker's unit; moves the walker on.
-__device__ __forceinline__ void publish_unit(TileWalk& walk, TileUnit* ring, uint32_t k) {
+// The walker's unit; moves the walker on.  The first piece of a cut unit is
+// noted for the kernel that joins the pieces.
+__device__ __forceinline__ void publish_unit(TileWalk& walk, TileUnit* ring, uint32_t k, TileCut* cuts) {
   TileUnit u;
   u.h = walk.h;
   const int i0 = walk.qt * kTileQueries;
@@ -42,9 +43,9 @@ __device__ __forceinline__ void publish_unit(TileWalk& walk, TileUnit* ring, uin
   u.start = walk.s.start;
   u.last = walk.s.start + walk.s.rows - 1;
   u.slot = walk.s.slot;
-  u.first = walk.p.first;
   u.index = walk.p.index;
   u.pieces = walk.p.pieces;
+  if (u.pieces > 1 && u.index == 0) cuts[blockIdx.x] = TileCut{u.row0, u.nq, u.h, u.pieces};
   u.next_h = walk.next() ? walk.h : -1;
   ring[k % kUnitRing] = u;
 }
@@ -90,73 +91,17 @@ __device__ __forceinline__ void store_row(const TileUnit& u, int a, const float 
     lse[static_cast<size_t>(u.h) * T + u.row0 + a] = lse2 == -INFINITY ? -INFINITY : lse2 * 0.69314718055994531f;
 }
 
-// A piece's row goes to the workspace; the warp whose 32 rows complete their
-// unit joins the pieces in order, so the result does not depend on which it
-// is, with weights 2^(lse_c - max).
-template <int D, bool O_BF16>
-__device__ __forceinline__ void store_piece(const TileUnit& u, int quad, int lane, const float (&ov)[D], float lse2,
-                                            float* part, int* counters, void* o, float* lse, int T, int H) {
-  const int a = quad * 32 + lane;
-  constexpr size_t kPart = kTileQueries * (D + 1);
-  {
-    float* mine = part + plan_place(static_cast<int>(blockIdx.x), u.index) * kPart;
-    float4* po = reinterpret_cast<float4*>(mine + a * D);
+// A piece's row goes to the workspace, joined by the kernel behind this one
+// (paged_join.cu).  (With the last piece to arrive joining in this kernel, its
+// warps held up the CTA's softmax: 131 us instead of 90 for 22 sequences of
+// 512 tokens over 512 rows, 8 heads, where every CTA has two pieces.)
+template <int D>
+__device__ __forceinline__ void store_piece(const TileUnit& u, int a, const float (&ov)[D], float lse2, float* part) {
+  float* mine = part + plan_place(static_cast<int>(blockIdx.x), u.index) * static_cast<size_t>(tile_part(D));
+  float4* po = reinterpret_cast<float4*>(mine + a * D);
 #pragma unroll
-    for (int c = 0; c < D / 4; ++c) __stcg(po + c, make_float4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]));
-    __stcg(mine + kTileQueries * D + a, lse2);
-  }
-  __threadfence();  // the piece's rows are visible before it is counted
-  __syncwarp();
-  int arrived = 0;
-  if (lane == 0) arrived = atomicAdd(counters + u.first * 4 + quad, 1);
-  if (__shfl_sync(0xffffffffu, arrived, 0) != u.pieces - 1) return;
-  __threadfence();
-  float top = -INFINITY;
-  for (int y = 0; y < u.pieces; ++y)
-    top = fmaxf(top, __ldcg(part + plan_place(u.first + y, y) * kPart + kTileQueries * D + a));
-  const float eff = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  for (int y = 0; y < u.pieces; ++y)
-    sum += ex2(__ldcg(part + plan_place(u.first + y, y) * kPart + kTileQueries * D + a) - eff);
-  const float inv = top == -INFINITY ? 0.f : 1.f / sum;
-  if (a >= u.nq) return;
-  const size_t at = (static_cast<size_t>(u.row0 + a) * H + u.h) * D;
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    float acc[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-    for (int y = 0; y < u.pieces; ++y) {
-      const float* from = part + plan_place(u.first + y, y) * kPart;
-      const float w = ex2(__ldcg(from + kTileQueries * D + a) - eff);
-      const float4* src = reinterpret_cast<const float4*>(from + a * D + c0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float4 x = __ldcg(src + e);
-        acc[4 * e] = fmaf(w, x.x, acc[4 * e]);
-        acc[4 * e + 1] = fmaf(w, x.y, acc[4 * e + 1]);
-        acc[4 * e + 2] = fmaf(w, x.z, acc[4 * e + 2]);
-        acc[4 * e + 3] = fmaf(w, x.w, acc[4 * e + 3]);
-      }
-    }
-    if (O_BF16) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o) + at + c0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        dst[e] = make_uint4(
-            pack_bf16x2(acc[8 * e] * inv, acc[8 * e + 1] * inv), pack_bf16x2(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
-            pack_bf16x2(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
-            pack_bf16x2(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
-    } else {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(o) + at + c0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        dst[e] = make_float4(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
-    }
-  }
-  if (lse != nullptr)
-    lse[static_cast<size_t>(u.h) * T + u.row0 + a] =
-        top == -INFINITY ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+  for (int c = 0; c < D / 4; ++c) po[c] = make_float4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
+  mine[kTileQueries * D + a] = lse2;
 }
 
 // Kernel parameters common to both.
@@ -292,7 +237,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
       while (ok && queued > 0 && queue[0].unit + 2 <= un) pop_v();
     if (!ok) break;
     if (next_h >= 0) {
-      if (lane == 0) publish_unit(bars->walk, bars->units, un + 1);
+      if (lane == 0) publish_unit(bars->walk, bars->units, un + 1, p.cuts);
       __syncwarp();
       if (AHEAD) load_q(un + 1);
     }
