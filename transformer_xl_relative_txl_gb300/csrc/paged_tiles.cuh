@@ -118,7 +118,7 @@ struct TileParams {
   const PlanHead* head;
   const PlanSeq* seqs;
   const int* starts;
-  int* counters;
+  TileCut* cuts;
   float* part;
   unsigned int* status;
   unsigned long long wait_ns;
