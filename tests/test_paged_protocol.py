@@ -81,6 +81,10 @@ def with_dead_rows(progs, dead, build_first):
     """The roles of test_loader_protocol.py, where the softmax of the steps in `dead` needs its value tile landed before
     it hands over its weights, and builds the next unit's operands before that (build_first) or after."""
     progs = dict(progs)
+    # the loader waits for the stages of K(t), R(t+1) and V(t-2) before it issues any of the three
+    loader = progs["loader"]
+    progs["loader"] = [(act, deps + ([d for a, more in loader[i + 1:i + 3] if a[0] in ("LR", "LV") for d in more]
+                                     if act[0] == "LK" else [])) for i, (act, deps) in enumerate(loader)]
     for name in ("sm0", "sm1"):
         prog, out, i = progs[name], [], 0
         while i < len(prog):

@@ -206,10 +206,15 @@ cudaError_t launch_tiles(const PagedAttn& a, const PlanSpace& s, int sms, const 
   }
   const cuuint64_t row[2] = {D * 2, H * D * 2};
   const cuuint64_t tokens[3] = {D, H, static_cast<cuuint64_t>(a.T)};
-  const cuuint64_t distances[3] = {D, H, static_cast<cuuint64_t>(a.n_r)};
-  const cuuint32_t box_q[3] = {64, 1, kTileQueries}, box_r[3] = {64, 1, 64}, box_o[3] = {64, 1, 32};
-  if (!enc(&m.q, a.q, 3, tokens, row, box_q) || !enc(&m.r, a.r, 3, distances, row, box_r))
-    return cudaErrorInvalidValue;
+  const cuuint32_t box_q[3] = {64, 1, kTileQueries}, box_o[3] = {64, 1, 32};
+  if (!enc(&m.q, a.q, 3, tokens, row, box_q)) return cudaErrorInvalidValue;
+  {
+    // Four dimensions as the pools', so that one instruction loads boxes of both.
+    const cuuint64_t n_r = a.n_r, dims[4] = {D, n_r, H, 1};
+    const cuuint64_t strides[3] = {H * D * 2, D * 2, H * D * n_r * 2};
+    const cuuint32_t box[4] = {64, 64, 1, 1};
+    if (!enc(&m.r, a.r, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  }
   m.o = m.q;  // stands in where the output is not bf16 and never touched
   if (a.o_bf16 && !enc(&m.o, a.o, 3, tokens, row, box_o)) return cudaErrorInvalidValue;
   // The sign of the scale is folded into (q+u), (q+v) (exact in bf16); a zero

@@ -126,57 +126,84 @@ struct TileParams {
 
 // Tensor maps: q over {D, H, T} with a {64, 1, 128} box, the pools over
 // {D, page_rows, H, n_pages} with {64, min(page_rows, 64), 1, 1}, r over
-// {D, H, n_r} with {64, 1, 64}; o (bf16) over {D, H, T} with {64, 1, 32}.
+// {D, n_r, H, 1} with {64, 64, 1, 1}; o (bf16) over {D, H, T} with {64, 1, 32}.
 struct TileMaps {
   CUtensorMap q, k, v, r, o;
 };
 
-// The loader warp of both kernels, all lanes in step: K, V and r tiles (and
-// the raw q tiles) of the CTA's units in order, and the units published.
-// Bars has the rings' barriers, the units and the walker (in shared memory:
-// it is used once per unit, and the warp has few registers).
+// The loader warp of both kernels: K, V and r tiles (and the raw q tiles) of
+// the CTA's units in order, and the units published.  Bars has the rings'
+// barriers, the units and the walker (in shared memory: it is used once per
+// unit, and the warp has few registers).
 //
-// Pages.  A 64-row tile is one box of a page, or 2 or 4 boxes of pages of 32
-// or 16 rows.  Lane y (and 4 + y for V) has box y: its page id is fetched a
-// tile ahead, and one TMA instruction issues all the boxes.  Boxes without a
-// live row are left out; a page id out of range reads as zeros (a box outside
-// its tensor) and is reported.  With one lane doing all of it the loader bound
-// the kernel: 1.57 us a step at D = 64 where the softmax takes 0.8.
+// The lanes share a step's work: lanes 0-3 have the boxes of its K tile, 4-7
+// those of a V tile, 8 its r tile.  A 64-row tile of keys is one box of a page,
+// or 2 or 4 boxes of pages of 32 or 16 rows; a lane fetches its box's page id a
+// tile ahead.  Lanes 0, 4 and 8 wait for their stages at the same time, then
+// one instruction arms the three barriers and one issues every box.  (One lane
+// doing all in turn took 2900 cycles a step at D = 64, all lanes doing it in
+// turn 2500; the softmax takes 1460.)  Boxes without a live row are left out; a
+// page id out of range reads as zeros (a box outside its tensor) and is
+// reported.
 //
 // LAG: V tiles trail the K and r tiles by so many.  A V stage is freed only
 // when the P.V MMA of its step completes, after that step's softmax, while a K
-// stage is free as soon as its score MMA is done; in one issue order K(t),
-// R(t+1), V(t), every K load would wait behind the V stage of step t - NS and
-// land just in time.  AHEAD: the raw q tile of a unit is loaded a unit ahead;
-// before that of the unit after next, every queued V of a unit two or more
-// back goes out, since the load waits for the (q+u), (q+v) build of the next
-// unit, which waits for the epilogue of the unit before, which needs all of
-// that unit's V tiles (a unit of one step would otherwise hold them behind the
-// load).
+// stage is free as soon as its score MMA is done; with V(t) beside K(t), K
+// would wait for the P.V of step t - NS and land just in time.  AHEAD: the raw
+// q tile of a unit is loaded a unit ahead; before that of the unit after next,
+// every queued V of a unit two or more back goes out, since the load waits for
+// the (q+u), (q+v) build of the next unit, which waits for the epilogue of the
+// unit before, which needs all of that unit's V tiles (a unit of one step would
+// otherwise hold them behind the load).
 template <int D, int NS, int LAG, bool AHEAD, typename Bars>
 __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
                                                 uint8_t* sK, uint8_t* sV, uint8_t* sR) {
+  static_assert((NS & (NS - 1)) == 0 && LAG <= 2, "stage arithmetic, queue");
   constexpr int kChunk = kStepKeys * 128, kTile = kChunk * (D / 64), kQChunk = kTileQueries * 128;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
-  const uint64_t wait_ns = p.wait_ns;
   const int log_page = p.log_page_rows, log_box = min(log_page, 6);
-  const int y = lane & 3;
-  const bool mine = lane < 8 && y < (kStepKeys >> log_box);
-  const int off = y << log_box;                  // first row of this lane's box in a tile
-  const uint32_t at = static_cast<uint32_t>(off) * 128;  // its place in a stage's chunk
-  if (lane == 0) {
-    tma_prefetch_desc(&tm.q);
-    tma_prefetch_desc(&tm.k);
-    tma_prefetch_desc(&tm.v);
-    tma_prefetch_desc(&tm.r);
-  }
-  uint32_t nQ = 0, nK = 0, nV = 0, nR = 0;
-  bool ok = bars->any != 0, bad = false;
-  const bool any = ok;
+  const bool is_k = lane < 4, is_v = lane >= 4 && lane < 8, is_r = lane == 8, leads = (lane & 3) == 0 && lane <= 8;
+  const bool boxed = lane < 8 && (lane & 3) < (kStepKeys >> log_box);
+  const int off = (lane & 3) << log_box;  // first row of this lane's box in a tile
+  uint64_t* const empty = is_v ? bars->emptyV : (is_r ? bars->emptyR : bars->emptyK);
+  uint64_t* const full = is_v ? bars->fullV : (is_r ? bars->fullR : bars->fullK);
+  uint8_t* const stages = is_v ? sV : (is_r ? sR : sK);
+  const CUtensorMap* const map = is_v ? &tm.v : (is_r ? &tm.r : &tm.k);
+  uint8_t* const mine = stages + (is_r ? 0 : off * 128);
+  if (lane <= 8 && leads) tma_prefetch_desc(map);
+  uint32_t n = 0;   // tiles of this lane's ring so far
+  uint32_t nQ = 0;  // q tiles so far
+  const bool any = bars->any != 0;
+  bool ok = any, bad = false;
 
+  // One tile of each ring whose lanes are `active`.
+  auto issue = [&](bool active, int page, int x, int h, uint32_t bytes) {
+    const uint32_t s = n & (NS - 1);
+    const bool lead = active && leads;
+    uint64_t since = 0;
+    for (uint32_t tries = 1;; ++tries) {
+      const bool done = !lead || mbar_try_wait(&empty[s], ((n / NS) & 1) ^ 1);
+      if (__all_sync(0xffffffffu, done)) break;
+      if ((tries & 15) == 0) {
+        const uint64_t now = global_timer_ns();
+        if (since == 0) since = now;
+        if (__any_sync(0xffffffffu, *abort != 0 || now - since > p.wait_ns)) {
+          ok = false;
+          return;
+        }
+      }
+    }
+    if (lead) mbar_arrive_expect_tx(&full[s], bytes);
+    __syncwarp();
+    if (active && page >= 0) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tma_load_4d(mine + s * kTile + c * kChunk, map, &full[s], c * 64, x, h, page);
+    }
+    if (active) ++n;
+  };
   auto load_q = [&](uint32_t un) {
-    if (!(ok = warp_wait(&bars->q_empty, (nQ & 1) ^ 1, wait_ns, abort))) return;
+    if (!(ok = warp_wait(&bars->q_empty, (nQ & 1) ^ 1, p.wait_ns, abort))) return;
     if (lane == 0) {
       const TileUnit& w = bars->units[un % kUnitRing];
       mbar_arrive_expect_tx(&bars->q_full, kQChunk * (D / 64));
@@ -185,56 +212,29 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     }
     ++nQ;
   };
-  auto load_r = [&](int h, int dist) {
-    const int s = static_cast<int>(nR % NS);
-    if (!(ok = ok && warp_wait(&bars->emptyR[s], ((nR / NS) & 1) ^ 1, wait_ns, abort))) return;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars->fullR[s], kTile);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_3d(sR + s * kTile + c * kChunk, &tm.r, &bars->fullR[s], c * 64, h, dist);
-    }
-    ++nR;
-  };
-  // A tile of keys or values: this lane's page (-1: no live row), the row in
-  // the page, the head, the tile's bytes, the unit.
+  // V tiles that wait their turn, the oldest in v0: this lane's page (-1: no
+  // live row), the row in the page, the head, the tile's bytes, the unit.
   struct Tile {
     int page, x, h;
     uint32_t bytes, unit;
   };
-  auto load_tile = [&](const Tile& e, uint64_t* empty, uint64_t* full, uint32_t& n, const CUtensorMap* map,
-                       uint8_t* stages, bool issues) {
-    const int s = static_cast<int>(n % NS);
-    if (!(ok = ok && warp_wait(&empty[s], ((n / NS) & 1) ^ 1, wait_ns, abort))) return;
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], e.bytes);
-    __syncwarp();
-    if (issues && e.page >= 0) {
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_4d(stages + s * kTile + c * kChunk + at, map, &full[s], c * 64, e.x, e.h, e.page);
-    }
-    ++n;
-  };
-  Tile queue[LAG > 0 ? LAG : 1];  // queue[0] the oldest
+  Tile v0{}, v1{};
   int queued = 0;
-  auto issue_v = [&](const Tile& e) {
-    load_tile(e, bars->emptyV, bars->fullV, nV, &tm.v, sV, lane >= 4);
-  };
-  auto pop_v = [&]() {
-    issue_v(queue[0]);
-#pragma unroll
-    for (int e = 0; e + 1 < LAG; ++e) queue[e] = queue[e + 1];
-    --queued;
+  auto flush_v = [&](uint32_t upto) {  // of units up to `upto`
+    while (ok && queued > 0 && v0.unit <= upto) {
+      issue(is_v, v0.page, v0.x, v0.h, v0.bytes);
+      v0 = v1;
+      --queued;
+    }
   };
 
   if (AHEAD && any) load_q(0);
-  for (uint32_t un = 0; any && ok; ++un) {
+  for (uint32_t un = 0; ok; ++un) {
     const TileUnit& w = bars->units[un % kUnitRing];
     const int next_h = w.next_h, h = w.h, d0 = w.d0, start = w.start, last = w.last, tend = w.t0 + w.nks;
     const int* row = p.book.table + static_cast<size_t>(w.slot) * p.book.max_pages;
     int t = w.t0;
-    if (LAG > 0)
-      while (ok && queued > 0 && queue[0].unit + 2 <= un) pop_v();
+    if (LAG > 0 && un >= 2) flush_v(un - 2);
     if (!ok) break;
     if (next_h >= 0) {
       if (lane == 0) publish_unit(bars->walk, bars->units, un + 1, p.cuts);
@@ -245,12 +245,12 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     if (!ok) break;
     auto live = [&](int tile) {
       const int x = tile * kStepKeys + off;
-      return mine && x <= last && x + (1 << log_box) > start;
+      return boxed && x <= last && x + (1 << log_box) > start;
     };
     int id = live(t) ? row[(t * kStepKeys + off) >> log_page] : 0;
     // distance tiles -2 and -1 of the unit's first step
-    load_r(h, d0 - kStepKeys * (t - 1));
-    load_r(h, d0 - kStepKeys * t);
+    issue(is_r, 0, d0 - kStepKeys * (t - 1), h, kTile);
+    if (ok) issue(is_r, 0, d0 - kStepKeys * t, h, kTile);
     for (; ok && t < tend; ++t) {
       const bool lv = live(t);
       Tile e;
@@ -265,35 +265,36 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
       e.x = (t * kStepKeys) & ((1 << log_page) - 1);  // 0 for pages of up to 64 rows
       e.h = h;
       e.unit = un;
-      load_tile(e, bars->emptyK, bars->fullK, nK, &tm.k, sK, lane < 4);
-      load_r(h, d0 - kStepKeys * (t + 1));
-      if (LAG == 0) {
-        issue_v(e);
-      } else {
-        if (ok && queued == LAG) pop_v();
-#pragma unroll
-        for (int q = 0; q < LAG; ++q)
-          if (q == queued) queue[q] = e;
+      const bool has_v = LAG == 0 || queued == LAG;
+      const Tile& v = LAG == 0 ? e : v0;
+      issue(is_k || is_r || (is_v && has_v), is_r ? 0 : (is_v ? v.page : e.page),
+            is_r ? d0 - kStepKeys * (t + 1) : (is_v ? v.x : e.x), is_v ? v.h : h,
+            is_r ? static_cast<uint32_t>(kTile) : (is_v ? v.bytes : e.bytes));
+      if (LAG > 0) {
+        if (has_v) {
+          v0 = v1;
+          --queued;
+        }
+        if (queued == 0)
+          v0 = e;
+        else
+          v1 = e;
         ++queued;
       }
     }
     if (next_h < 0) break;
   }
-  if (LAG > 0)
-    while (ok && queued > 0) pop_v();
+  if (LAG > 0) flush_v(0xffffffffu);
   if (bad) atomicOr(p.status, kStatusPagesBit);
   if (any && !ok && lane == 0) report_timeout(abort, p.status);
   // This warp's own copies land before the CTA may exit.
-  auto drain = [&](uint64_t* full, uint32_t n, int ns) {
-    for (int s = 0; s < ns && static_cast<uint32_t>(s) < n; ++s) {
-      const uint32_t z = s + ((n - 1 - s) / ns) * ns;
-      mbar_wait_own(&full[s], (z / ns) & 1, wait_ns);
+  if (nQ > 0) mbar_wait_own(&bars->q_full, (nQ - 1) & 1, p.wait_ns);
+  if (leads)
+    for (uint32_t s = 0; s < NS && s < n; ++s) {
+      const uint32_t z = s + ((n - 1 - s) / NS) * NS;
+      mbar_wait_own(&full[s], (z / NS) & 1, p.wait_ns);
     }
-  };
-  drain(&bars->q_full, nQ, 1);
-  drain(bars->fullK, nK, NS);
-  drain(bars->fullV, nV, NS);
-  drain(bars->fullR, nR, NS);
+  __syncwarp();
 }
 
 cudaError_t launch_paged_tc64(const TileMaps& m, const TileParams& p, bool o_bf16, int sms, cudaStream_t stream);
