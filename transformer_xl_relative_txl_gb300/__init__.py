@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -101,7 +102,9 @@ class _PageBook(ctypes.Structure):
         (n, ctypes.c_int) for n in ("n_slots", "max_pages", "n_pages", "page_rows")]
 
 
-_pb = ctypes.POINTER(_PageBook)
+_pack_book = struct.Struct("4P4i").pack  # the same struct as bytes, in a third of the time
+assert struct.calcsize("4P4i") == ctypes.sizeof(_PageBook)
+_pb = _p  # a pointer to the struct, or its bytes
 lib.txl_pages_reserve.argtypes = [_pb, _p, _p, _i, _p, _p, _p, _p]
 lib.txl_pages_reserve.restype = _i
 lib.txl_pages_append.argtypes = [_pb, _p, _p, _i, _i, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _p]
@@ -425,7 +428,7 @@ def _vectors(dev, n, *tensors):
         if t is None:
             out.append(None)
             continue
-        if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"expected a contiguous int32 vector of {n} entries")
         if t.get_device() != dev:
             raise ValueError("tensors must live in the current device's memory")
@@ -457,16 +460,30 @@ def _device(t):
     return dev
 
 
+# The current stream's handle without the Stream object, which costs as much
+# as a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(dev, stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
 def _book(dev, book, page_rows):
-    """The C struct of a page book: a dict of int32 tensors table [slots,
-    max_pages], start and rows [slots], refs [pages]."""
+    """The C struct of a page book as bytes, and its number of pages: a dict
+    of int32 tensors table [slots, max_pages], start and rows [slots], refs
+    [pages]."""
     table, refs = book["table"], book["refs"]
     if table.dtype is not torch.int32 or table.dim() != 2:
         raise ValueError("table must be a contiguous int32 [slots, max_pages] tensor")
     n_slots, max_pages = table.shape
     n_pages = refs.numel()
-    ptrs = _tensors(dev, table) + _vectors(dev, n_slots, book["start"], book["rows"]) + _vectors(dev, n_pages, refs)
-    return _PageBook(*ptrs, n_slots, max_pages, n_pages, page_rows)
+    table_p, = _tensors(dev, table)
+    start_p, rows_p = _vectors(dev, n_slots, book["start"], book["rows"])
+    refs_p, = _vectors(dev, n_pages, refs)
+    return _pack_book(table_p, start_p, rows_p, refs_p, n_slots, max_pages, n_pages, page_rows), n_pages
 
 
 def _pools(dev, k_pages, v_pages, n_pages=None):
@@ -485,10 +502,10 @@ def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, s
     [pages].  granted, copy_src, copy_dst (int32 [n]) receive the rows granted
     and the pages that txl_pages_append has to copy."""
     dev, n = _device(slots), slots.numel()
-    b = _book(dev, book, page_rows)
+    b, _ = _book(dev, book, page_rows)
     s, g, src, dst = _vectors(dev, n, slots, granted, copy_src, copy_dst)
     c, = _vectors(dev, n + 1, cu)
-    _check(lib.txl_pages_reserve(ctypes.byref(b), s, c, n, g, src, dst, _stream(stream)), "txl_pages_reserve")
+    _check(lib.txl_pages_reserve(b, s, c, n, g, src, dst, _stream_on(dev, stream)), "txl_pages_reserve")
 
 
 def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new, stream=None):
@@ -497,7 +514,7 @@ def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_
     txl_pages_reserve named (copy_src, copy_dst, or None and None)."""
     dev, n = _device(slots), slots.numel()
     kp, vp, (_, H, P, D) = _pools(dev, k_pages, v_pages, book["refs"].numel())
-    b = _book(dev, book, P)
+    b, _ = _book(dev, book, P)
     s, g, src, dst = _vectors(dev, n, slots, granted, copy_src, copy_dst)
     c, = _vectors(dev, n + 1, cu)
     if (src is None) != (dst is None):
@@ -508,8 +525,8 @@ def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_
     if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
         raise ValueError("the pools and the new rows share a dtype")
     kn, vn = _tensors(dev, k_new, v_new)
-    _check(lib.txl_pages_append(ctypes.byref(b), kp, vp, H, D, s, c, n, g, src, dst, kn, vn, T,
-                                _dtype_code(k_pages.dtype), _stream(stream)), "txl_pages_append")
+    _check(lib.txl_pages_append(b, kp, vp, H, D, s, c, n, g, src, dst, kn, vn, T,
+                                _dtype_code(k_pages.dtype), _stream_on(dev, stream)), "txl_pages_append")
 
 
 def txl_pages_copy(k_pages, v_pages, src, dst, stream=None):
@@ -517,7 +534,7 @@ def txl_pages_copy(k_pages, v_pages, src, dst, stream=None):
     dev, n = _device(src), src.numel()
     kp, vp, (N, H, P, D) = _pools(dev, k_pages, v_pages)
     s, d = _vectors(dev, n, src, dst)
-    _check(lib.txl_pages_copy(kp, vp, N, H * P * D, s, d, n, _dtype_code(k_pages.dtype), _stream(stream)),
+    _check(lib.txl_pages_copy(kp, vp, N, H * P * D, s, d, n, _dtype_code(k_pages.dtype), _stream_on(dev, stream)),
            "txl_pages_copy")
 
 
@@ -525,17 +542,17 @@ def txl_pages_fork(book, page_rows, src, dst, ok, stream=None):
     """Empty slot dst[i] shares the pages of slot src[i]; ok (int32 [n])
     receives 1, or 0 where refused."""
     dev, n = _device(src), src.numel()
-    b = _book(dev, book, page_rows)
+    b, _ = _book(dev, book, page_rows)
     s, d, k = _vectors(dev, n, src, dst, ok)
-    _check(lib.txl_pages_fork(ctypes.byref(b), s, d, n, k, _stream(stream)), "txl_pages_fork")
+    _check(lib.txl_pages_fork(b, s, d, n, k, _stream_on(dev, stream)), "txl_pages_fork")
 
 
 def txl_pages_free(book, page_rows, slots, keep=None, stream=None):
     """Slot slots[i] keeps its newest keep[i] rows (None: none)."""
     dev, n = _device(slots), slots.numel()
-    b = _book(dev, book, page_rows)
+    b, _ = _book(dev, book, page_rows)
     s, k = _vectors(dev, n, slots, keep)
-    _check(lib.txl_pages_free(ctypes.byref(b), s, k, n, _stream(stream)), "txl_pages_free")
+    _check(lib.txl_pages_free(b, s, k, n, _stream_on(dev, stream)), "txl_pages_free")
 
 
 def txl_pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, stream=None):
@@ -543,10 +560,10 @@ def txl_pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, stream
     [pages]) and count (int32 [1]) receive the new ids and the moves, which
     txl_pages_copy(k_pages, v_pages, copy_src, copy_dst) then makes."""
     dev = _device(new_id)
-    b = _book(dev, book, page_rows)
-    ids, s, d = _vectors(dev, b.n_pages, new_id, copy_src, copy_dst)
+    b, n_pages = _book(dev, book, page_rows)
+    ids, s, d = _vectors(dev, n_pages, new_id, copy_src, copy_dst)
     c, = _vectors(dev, 1, count)
-    _check(lib.txl_pages_compact(ctypes.byref(b), ids, s, d, c, _stream(stream)), "txl_pages_compact")
+    _check(lib.txl_pages_compact(b, ids, s, d, c, _stream_on(dev, stream)), "txl_pages_compact")
 
 
 def txl_relattn_paged_workspace_bytes(n, T, H, D, dtype):
@@ -564,7 +581,7 @@ def txl_relattn_forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, b
     scale defaults to 1/sqrt(D)."""
     dev, n = _device(slots), slots.numel()
     kp, vp, (_, H, P, D) = _pools(dev, k_pages, v_pages, book["refs"].numel())
-    b = _book(dev, book, P)
+    b, _ = _book(dev, book, P)
     s, = _vectors(dev, n, slots)
     c, = _vectors(dev, n + 1, cu)
     T, n_r = q.shape[0], r.shape[0]
@@ -579,10 +596,10 @@ def txl_relattn_forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, b
     if lse is not None and (lse.shape != (H, T) or lse.dtype is not torch.float32):
         raise ValueError("lse must be fp32 [H, T]")
     qp, rp, up, vbp, op, lp, wp = _tensors(dev, q, r, bias_u, bias_v, o, lse, workspace)
-    st = lib.txl_relattn_forward_paged(qp, kp, vp, ctypes.byref(b), s, c, n, T, T if max_new is None else max_new, rp,
+    st = lib.txl_relattn_forward_paged(qp, kp, vp, b, s, c, n, T, T if max_new is None else max_new, rp,
                                        up, vbp, op, lp, H, D, n_r, D ** -0.5 if scale is None else scale,
                                        _dtype_code(q.dtype), _dtype_code(o.dtype), wp, workspace.nbytes,
-                                       _stream(stream))
+                                       _stream_on(dev, stream))
     _check(st, "txl_relattn_forward_paged")
     return o
 

@@ -72,6 +72,7 @@ struct Params {
   float* part;
   unsigned int* status;
   unsigned long long wait_ns;
+  bool behind_tiles;
 };
 
 struct Bars {
@@ -133,11 +134,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     fence_mbar_init();
   }
   __syncthreads();
-  grid_dep_wait();
+  // Behind the plan this kernel waits for it.  Behind the tile kernel it need
+  // not: that one let it start after its own wait for the plan; what it waits
+  // for, at its end, is that the kernels behind it may take both as complete.
+  if (!p.behind_tiles) grid_dep_wait();
   grid_dep_launch_dependents();
   const uint64_t wait_ns = p.wait_ns;
   typename C::Walk w;
-  bool more = w.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+  bool more = w.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
 
   if (warp == kWarps) {
     // ============================== producer ===============================
@@ -199,6 +203,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       const uint32_t n = s + ((g - 1 - s) / NS) * NS;
       mbar_wait_own(&bars->full[s], (n / NS) & 1, wait_ns);
     }
+    if (p.behind_tiles) grid_dep_wait();
     return;
   }
 
@@ -408,10 +413,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     }
   }
   if (!ok && lane == 0) report_timeout(abort, p.status);
+  if (p.behind_tiles) grid_dep_wait();
 }
 
 template <int D, bool O_BF16>
-cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc, cudaStream_t stream) {
+cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_tiles, const WaitCtl& wc,
+                   cudaStream_t stream) {
   using C = Cfg<D>;
   PFN_cuTensorMapEncodeTiled_v12000 encode = api_tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
@@ -441,7 +448,7 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCt
   }
   Params p{b, static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H, a.n_r,
            a.scale * 1.4426950408889634f, s.heads, s.seqs[0], s.starts[0], s.counters, s.part[0], wc.status,
-           wc.limit_ns};
+           wc.limit_ns, behind_tiles};
   auto kern = paged_decode_kernel<D, O_BF16>;
   static unsigned configured = 0;  // one bit per device ordinal < 32
   int dev = 0;
@@ -457,10 +464,11 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCt
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc,
+cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_tiles, const WaitCtl& wc,
                                 cudaStream_t stream) {
-  if (a.D == 64) return a.o_bf16 ? launch<64, true>(a, s, sms, wc, stream) : launch<64, false>(a, s, sms, wc, stream);
-  return a.o_bf16 ? launch<128, true>(a, s, sms, wc, stream) : launch<128, false>(a, s, sms, wc, stream);
+  auto run = [&](auto f) { return f(a, s, sms, behind_tiles, wc, stream); };
+  if (a.D == 64) return a.o_bf16 ? run(launch<64, true>) : run(launch<64, false>);
+  return a.o_bf16 ? run(launch<128, true>) : run(launch<128, false>);
 }
 
 }  // namespace txl

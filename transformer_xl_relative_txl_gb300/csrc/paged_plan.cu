@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PagedAttn a, const
   grid_dep_wait();
   grid_dep_launch_dependents();
   __shared__ Sum warp_sums[32];
+  __shared__ long long prefix[kThreads];  // costs before the first sequences of the list
   const int kind = blockIdx.x;
   const PageBook& b = a.book;
   PlanSeq* list = sp.seqs[kind];
@@ -89,7 +90,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PagedAttn a, const
     const Sum upto = scan(mine, warp_sums);
     if (mine.count != 0) {
       s.pre = before.cost + upto.cost - mine.cost;
-      list[before.count + upto.count - 1] = s;
+      const int at = before.count + upto.count - 1;
+      list[at] = s;
+      if (at < kThreads) prefix[at] = s.pre;
     }
     before.cost += warp_sums[31].cost;
     before.count += warp_sums[31].count;
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PagedAttn a, const
     int x = 0, y = before.count - 1;  // the last sequence with pre <= lo
     while (x < y) {
       const int mid = (x + y + 1) >> 1;
-      if (list[mid].pre <= lo)
+      if ((mid < kThreads ? prefix[mid] : list[mid].pre) <= lo)
         x = mid;
       else
         y = mid - 1;
@@ -234,10 +237,11 @@ cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_
   PlanSpace s;
   plan_space(a.workspace, a.n, a.T, a.D, &s);
   const int sms = paged_sms();
+  const bool tiles = a.max_new > kDecodeRows;
   cudaError_t e = launch_paged_plan(a, s, sms, wc.status, stream);
-  if (e == cudaSuccess) e = launch_paged_decode(a, s, sms, wc, stream);
-  if (e == cudaSuccess && a.max_new > kDecodeRows) e = launch_tiles(a, s, sms, wc, stream);
-  if (e == cudaSuccess && a.max_new > kDecodeRows) e = launch_paged_join(a, s, sms, stream);
+  if (e == cudaSuccess && tiles) e = launch_tiles(a, s, sms, wc, stream);
+  if (e == cudaSuccess) e = launch_paged_decode(a, s, sms, tiles, wc, stream);
+  if (e == cudaSuccess && tiles) e = launch_paged_join(a, s, sms, stream);
   return e;
 }
 

@@ -31,6 +31,7 @@ struct __align__(16) PlanSeq {
   long long pre;  // cost of the sequences before it
   int tok0, n, slot, start, rows, pad;
 };
+static_assert(sizeof(PlanSeq) == 32, "two 16-byte loads");
 
 // One kind's division.
 struct __align__(16) PlanHead {
@@ -94,6 +95,39 @@ __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int
 // that continues an earlier CTA's have a place each.
 __host__ __device__ __forceinline__ int plan_place(int c, int index) { return 2 * c + (index == 0 ? 1 : 0); }
 
+// The plan's data as a kernel reads it: from L2, since a kernel that overlaps
+// the one ahead of it on the stream may find older lines in L1.
+__host__ __device__ __forceinline__ PlanSeq plan_load(const PlanSeq* p) {
+#ifdef __CUDA_ARCH__
+  union {
+    int4 v[2];
+    PlanSeq s;
+  } u;
+  u.v[0] = __ldcg(reinterpret_cast<const int4*>(p));
+  u.v[1] = __ldcg(reinterpret_cast<const int4*>(p) + 1);
+  return u.s;
+#else
+  return *p;
+#endif
+}
+__host__ __device__ __forceinline__ int plan_load(const int* p) {
+#ifdef __CUDA_ARCH__
+  return __ldcg(p);
+#else
+  return *p;
+#endif
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ PlanHead plan_load(const PlanHead* p) {
+  union {
+    int4 v;
+    PlanHead h;
+  } u;
+  u.v = __ldcg(reinterpret_cast<const int4*>(p));
+  return u.h;
+}
+#endif
+
 // A walk over the units that CTA c has steps of.  Every role of a CTA walks
 // by itself.  BK: rows of a key step; TILE: queries of a unit (0: the unit
 // has all of the sequence's).
@@ -129,8 +163,8 @@ struct PlanWalk {
     H = heads;
     c = cta;
     if (c >= head.ctas) return false;
-    i = starts[c];
-    s = seqs[i];
+    i = plan_load(starts + c);
+    s = plan_load(seqs + i);
     lo = c * head.total / head.ctas;
     hi = (c + 1LL) * head.total / head.ctas;
     const long long per = cost_of_head();
@@ -152,7 +186,7 @@ struct PlanWalk {
     qt = 0;
     if (++h < H) return;
     h = 0;
-    if (++i < head.count) s = seqs[i];
+    if (++i < head.count) s = plan_load(seqs + i);
   }
   __host__ __device__ __forceinline__ bool settle() {
     for (; i < head.count && a < hi; step_unit()) {
@@ -226,7 +260,8 @@ inline size_t plan_space(void* base, int n, int T, int D, PlanSpace* out) {
 cudaError_t launch_paged_plan(const PagedAttn& a, const PlanSpace& s, int decode_bk, int sms, unsigned int* status,
                               cudaStream_t stream);
 cudaError_t launch_paged_join(const PagedAttn& a, const PlanSpace& s, int sms, cudaStream_t stream);
-cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, const WaitCtl& wc,
+// behind_tiles: launched behind the tile kernel, not behind the plan.
+cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_tiles, const WaitCtl& wc,
                                 cudaStream_t stream);
 // The pieces of every CTA of a kind (0: decode at head dimension D, 1: tiles) for n valid sequences, as rows (cta,
 // sequence, head, tile, t0, nks, first, index, pieces, place); host only.  Returns their number, -1 if cap is short.

@@ -133,12 +133,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
   // The kernels ahead on the stream, the plan among them, have completed from
   // here on.
   grid_dep_wait();
+  // The decode kernel behind this one needs the plan alone: its CTAs start as
+  // this one's end.
+  grid_dep_launch_dependents();
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
   if (threadIdx.x == kLoaderWarp * 32) {
-    const bool some = bars->walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+    const bool some = bars->walk.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
     bars->any = some ? 1 : 0;
     if (some) publish_unit(bars->walk, bars->units, 0, p.cuts);
   }
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
 
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
-    run_tile_loader<D, NK, 0, false>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, 1, false>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ============================ MMA issuer ===============================
     if (lane == 0) {

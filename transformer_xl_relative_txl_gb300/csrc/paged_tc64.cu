@@ -147,12 +147,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   // The kernels ahead on the stream, the plan among them, have completed from
   // here on.
   grid_dep_wait();
+  // The decode kernel behind this one needs the plan alone: its CTAs start as
+  // this one's end.
+  grid_dep_launch_dependents();
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
   if (threadIdx.x == kLoaderWarp * 32) {
-    const bool some = bars->walk.begin(p.seqs, *p.head, p.starts, p.H, blockIdx.x);
+    const bool some = bars->walk.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
     bars->any = some ? 1 : 0;
     if (some) publish_unit(bars->walk, bars->units, 0, p.cuts);
   }

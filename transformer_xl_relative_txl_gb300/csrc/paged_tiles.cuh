@@ -149,17 +149,22 @@ struct TileMaps {
 // LAG: V tiles trail the K and r tiles by so many.  A V stage is freed only
 // when the P.V MMA of its step completes, after that step's softmax, while a K
 // stage is free as soon as its score MMA is done; with V(t) beside K(t), K
-// would wait for the P.V of step t - NS and land just in time.  AHEAD: the raw
-// q tile of a unit is loaded a unit ahead; before that of the unit after next,
-// every queued V of a unit two or more back goes out, since the load waits for
-// the (q+u), (q+v) build of the next unit, which waits for the epilogue of the
-// unit before, which needs all of that unit's V tiles (a unit of one step would
-// otherwise hold them behind the load).
+// would wait for the P.V of step t - NS and land just in time (D = 128: 158 us
+// instead of 131 for 152 units of 100 steps).  AHEAD: the raw q tile of a unit
+// is loaded a unit ahead, and before that of the unit after next every queued V
+// of a unit two or more back goes out, since the load waits for the (q+u),
+// (q+v) build of the next unit, which waits for the epilogue of the unit
+// before, which needs all of that unit's V tiles (a unit of one step would
+// otherwise hold them behind the load).  Without AHEAD the build comes at the
+// end of a unit's steps, which may wait for its last V (rows that are not
+// live), and the next unit's r tiles wait for the build: the queue is emptied
+// at each unit.
 template <int D, int NS, int LAG, bool AHEAD, typename Bars>
 __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
                                                 uint8_t* sK, uint8_t* sV, uint8_t* sR) {
   static_assert((NS & (NS - 1)) == 0 && LAG <= 2, "stage arithmetic, queue");
   constexpr int kChunk = kStepKeys * 128, kTile = kChunk * (D / 64), kQChunk = kTileQueries * 128;
+  constexpr uint32_t kHold = AHEAD ? 2 : 1;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
   const int log_page = p.log_page_rows, log_box = min(log_page, 6);
@@ -234,7 +239,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     const int next_h = w.next_h, h = w.h, d0 = w.d0, start = w.start, last = w.last, tend = w.t0 + w.nks;
     const int* row = p.book.table + static_cast<size_t>(w.slot) * p.book.max_pages;
     int t = w.t0;
-    if (LAG > 0 && un >= 2) flush_v(un - 2);
+    if (LAG > 0 && un >= kHold) flush_v(un - kHold);
     if (!ok) break;
     if (next_h >= 0) {
       if (lane == 0) publish_unit(bars->walk, bars->units, un + 1, p.cuts);
