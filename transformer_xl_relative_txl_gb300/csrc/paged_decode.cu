@@ -51,8 +51,11 @@ struct Cfg {
   static constexpr int kStage = 2 * kTile + kTileR;
   static constexpr int kRow = D + 2;  // a query's partial result: o, m, l
   static constexpr int kOffPart = NS * kStage;
-  static constexpr int kOffBar = kOffPart + 2 * kWarps * kDecodeRows * kRow * 4;
-  static constexpr int kSmem = kOffBar + 256 + 1024;
+  static constexpr int kQuery = kDecodeRows * D * 2 + 2 * D * 4;  // a unit's rows of q, u and v
+  static constexpr int kOffQ = kOffPart + 2 * kWarps * kDecodeRows * kRow * 4;
+  static constexpr int kOffBar = kOffQ + 2 * kQuery;
+  static constexpr int kBarBytes = 384;
+  static constexpr int kSmem = kOffBar + kBarBytes + 1024;
   using Walk = PlanWalk<DecodeCost, BK, 0>;  // DecodeWalk64, DecodeWalk32
 };
 
@@ -75,11 +78,17 @@ struct Params {
   bool behind_tiles;
 };
 
+// A unit as the producer publishes it; nks 0: the CTA has no more.
+struct Unit {
+  int h, tok0, n, start, last, t0, nks, first, index, pieces;
+};
+
 struct Bars {
   uint64_t full[4], empty[4], joined;
+  uint64_t q_full[2], q_empty[2];  // by unit parity: the unit and its queries are there; read
+  Unit unit[2];
   int abort;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block too large");
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -105,6 +114,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Four bytes to shared memory, and an arrival on `bar` once this thread's
+// copies so far have landed.
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // The bf16 part `lo` (0: the value rounded, 1: what the rounding left) of a
 // and b, packed.
 __device__ __forceinline__ uint32_t split_part(float a, float b, bool lo) {
@@ -121,7 +139,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* joint = reinterpret_cast<float*>(smem + C::kOffPart);
+  uint8_t* queries = smem + C::kOffQ;
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
+  static_assert(sizeof(Bars) <= C::kBarBytes, "barrier block too large");
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -130,6 +150,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       mbar_init(&bars->empty[s], 1);
     }
     mbar_init(&bars->joined, kWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 33);  // the lanes' copies, and the unit
+      mbar_init(&bars->q_empty[s], kWarps);
+    }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -140,11 +164,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
   if (!p.behind_tiles) grid_dep_wait();
   grid_dep_launch_dependents();
   const uint64_t wait_ns = p.wait_ns;
-  typename C::Walk w;
-  bool more = w.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
 
   if (warp == kWarps) {
     // ============================== producer ===============================
+    typename C::Walk w;
+    bool more = w.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -152,9 +176,40 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     }
     const int P = p.book.page_rows;
     const int box = min(P, BK), boxes = BK / box;  // a tile is `boxes` boxes of rows
-    uint32_t g = 0;
+    uint32_t g = 0, units = 0;
     bool ok = true, bad = false;
+    // The next unit and its queries, on their way while its tiles are loaded:
+    // read by the consumers at the head of the unit, a global load's latency
+    // per unit was most of their time (decode batch: 163 us).
+    auto publish = [&](int nks) {
+      const int s = units & 1;
+      ok = warp_wait(&bars->q_empty[s], ((units >> 1) & 1) ^ 1, wait_ns, abort);
+      if (!ok) return;
+      if (nks > 0) {
+        uint8_t* at = queries + s * C::kQuery;
+        const int total = w.s.n * (D / 2);  // words of the queries' rows
+        for (int e = lane; e < total; e += 32)
+          copy4(at + e * 4, p.q + (static_cast<size_t>(w.s.tok0 + e / (D / 2)) * p.H + w.h) * D + e % (D / 2) * 2);
+#pragma unroll
+        for (int e = lane; e < D; e += 32) {
+          copy4(at + kDecodeRows * D * 2 + e * 4, p.bias_u + w.h * D + e);
+          copy4(at + kDecodeRows * D * 2 + (D + e) * 4, p.bias_v + w.h * D + e);
+        }
+      }
+      copies_arrive(&bars->q_full[s]);
+      if (lane == 0) {
+        Unit u{};
+        if (nks > 0)
+          u = Unit{w.h, w.s.tok0, w.s.n, w.s.start, w.s.start + w.s.rows - 1, w.p.t0, nks, w.p.first, w.p.index,
+                   w.p.pieces};
+        bars->unit[s] = u;
+        mbar_arrive(&bars->q_full[s]);
+      }
+      ++units;
+    };
     for (; ok && more; more = w.next()) {
+      publish(w.p.nks);
+      if (!ok) break;
       const int* row = p.book.table + static_cast<size_t>(w.s.slot) * p.book.max_pages;
       const int last = w.s.start + w.s.rows - 1;
       const int m = w.s.start + w.s.rows - w.s.n;
@@ -196,8 +251,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
         __syncwarp();
       }
     }
+    if (ok) publish(0);
     if (bad) atomicOr(p.status, kStatusPagesBit);
     if (!ok && lane == 0) report_timeout(abort, p.status);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // This warp's copies land before the CTA may exit.
     for (uint32_t s = 0; s < NS && s < g; ++s) {
       const uint32_t n = s + ((g - 1 - s) / NS) * NS;
@@ -210,28 +267,34 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
   // =============================== consumers ================================
   const int col_q = lane >> 3, part = lane >> 2 & 1;  // query and part of this lane's right-hand column
   const int my_q = lane & 3;                          // query of this lane's accumulators
-  uint32_t g = 0, units = 0;
+  uint32_t g = 0;
   bool ok = true;
-  for (; ok && more; more = w.next(), ++units) {
-    const int n = w.s.n, h = w.h;
+  for (uint32_t units = 0;; ++units) {
+    ok = warp_wait(&bars->q_full[units & 1], (units >> 1) & 1, wait_ns, abort);
+    if (!ok) break;
+    const Unit w = bars->unit[units & 1];
+    const int n = w.n, h = w.h;
     // (q + u), (q + v) in log2 units, as right-hand fragments.
     uint32_t qu[D / 8], qv[D / 8];
-    {
-      const __nv_bfloat16* q = p.q + (static_cast<size_t>(w.s.tok0 + min(col_q, n - 1)) * p.H + h) * D;
+    if (w.nks > 0) {
+      const uint8_t* at = queries + (units & 1) * C::kQuery;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(at) + min(col_q, n - 1) * (D / 2);
+      const float* bias = reinterpret_cast<const float*>(at + kDecodeRows * D * 2);
 #pragma unroll
       for (int e = 0; e < D / 8; ++e) {
         const int d = e * 8 + 2 * (lane & 3);
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d);
-        const float f = col_q < n ? p.scale_log2e : 0.f;
-        const float x0 = bf16_lo(x), x1 = bf16_hi(x);
-        const float* bu = p.bias_u + h * D + d;
-        const float* bv = p.bias_v + h * D + d;
-        qu[e] = col_q < n ? split_part((x0 + bu[0]) * f, (x1 + bu[1]) * f, part) : 0u;
-        qv[e] = col_q < n ? split_part((x0 + bv[0]) * f, (x1 + bv[1]) * f, part) : 0u;
+        const uint32_t x = q[d / 2];
+        const float f = p.scale_log2e, x0 = bf16_lo(x), x1 = bf16_hi(x);
+        const float2 bu = *reinterpret_cast<const float2*>(bias + d);
+        const float2 bv = *reinterpret_cast<const float2*>(bias + D + d);
+        qu[e] = col_q < n ? split_part((x0 + bu.x) * f, (x1 + bu.y) * f, part) : 0u;
+        qv[e] = col_q < n ? split_part((x0 + bv.x) * f, (x1 + bv.y) * f, part) : 0u;
       }
     }
-    const int last = w.s.start + w.s.rows - 1;
-    const int lim = w.s.start + w.s.rows - n + my_q;  // last row this lane's query sees
+    warp_arrive(&bars->q_empty[units & 1]);
+    if (w.nks == 0) break;
+    const int last = w.last;
+    const int lim = last + 1 - n + my_q;  // last row this lane's query sees
     float m_run = -INFINITY, l_run = 0.f;
     float acc[D / 16][4];
 #pragma unroll
@@ -242,9 +305,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     // This warp's tiles: those that the CTA loaded as number g with
     // g % kWarps == warp.
     const uint32_t g0 = g;
-    g += w.p.nks;
+    g += w.nks;
     for (uint32_t x = g0 + (warp + kWarps - g0 % kWarps) % kWarps; x < g; x += kWarps) {
-      const int row0 = (w.p.t0 + static_cast<int>(x - g0)) * BK;
+      const int row0 = (w.t0 + static_cast<int>(x - g0)) * BK;
       const int s = x % NS;
       ok = warp_wait(&bars->full[s], (x / NS) & 1, wait_ns, abort);
       if (!ok) break;
@@ -276,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
         }
       }
       // Scores of query my_q: rows row0 + 16 y + lane / 4 (+ 8).
-      const bool edge = row0 < w.s.start || row0 + BK - 1 > last - (n - 1);
+      const bool edge = row0 < w.start || row0 + BK - 1 > last - (n - 1);
       float sc[BK / 16][2];
       float best = -INFINITY;
 #pragma unroll
@@ -286,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
           float f = z[y][2 * u] + z[y][2 * u + 1];
           if (edge) {
             const int row = row0 + 16 * y + 8 * u + (lane >> 2);
-            f = row >= w.s.start && row <= lim ? f : -INFINITY;
+            f = row >= w.start && row <= lim ? f : -INFINITY;
           }
           sc[y][u] = f;
           best = fmaxf(best, f);
@@ -320,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
         // product as zeros, since 0 times NaN is not 0.
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (edge) {
-          auto live = [&](int row) { return row >= w.s.start && row <= last; };
+          auto live = [&](int row) { return row >= w.start && row <= last; };
           const int row = row0 + 16 * y + 2 * (lane & 3);
           keep0 = (live(row) ? 0xffffu : 0u) | (live(row + 1) ? 0xffff0000u : 0u);
           keep1 = (live(row + 8) ? 0xffffu : 0u) | (live(row + 9) ? 0xffff0000u : 0u);
@@ -367,30 +430,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[y * kStride + e * 32 + lane], o[e]);
       }
-      if (w.p.pieces > 1) {
+      if (w.pieces > 1) {
         // A piece's result goes to the workspace; the last of the unit's pieces
         // to arrive joins them in order, so the result does not depend on which
         // it is.
-        float* out = p.part + (static_cast<size_t>(plan_place(blockIdx.x, w.p.index)) * kDecodeRows + t) * C::kRow;
+        float* out = p.part + (static_cast<size_t>(plan_place(blockIdx.x, w.index)) * kDecodeRows + t) * C::kRow;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) __stcg(out + e * 32 + lane, o[e]);
         if (lane == 0) __stcg(out + D, m_all), __stcg(out + D + 1, l_all);
         __threadfence();
         __syncwarp();
         int arrived = 0;
-        if (lane == 0) arrived = atomicAdd(p.counters + w.p.first * 4 + t, 1);
-        if (__shfl_sync(0xffffffffu, arrived, 0) != w.p.pieces - 1) continue;
+        if (lane == 0) arrived = atomicAdd(p.counters + w.first * 4 + t, 1);
+        if (__shfl_sync(0xffffffffu, arrived, 0) != w.pieces - 1) continue;
         __threadfence();
         m_all = -INFINITY;
-        for (int y = 0; y < w.p.pieces; ++y)
-          m_all = fmaxf(m_all, __ldcg(p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + t) *
+        for (int y = 0; y < w.pieces; ++y)
+          m_all = fmaxf(m_all, __ldcg(p.part + (static_cast<size_t>(plan_place(w.first + y, y)) * kDecodeRows + t) *
                                                    C::kRow + D));
         const float m_eff2 = m_all == -INFINITY ? 0.f : m_all;
         l_all = 0.f;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-        for (int y = 0; y < w.p.pieces; ++y) {
-          const float* in = p.part + (static_cast<size_t>(plan_place(w.p.first + y, y)) * kDecodeRows + t) * C::kRow;
+        for (int y = 0; y < w.pieces; ++y) {
+          const float* in = p.part + (static_cast<size_t>(plan_place(w.first + y, y)) * kDecodeRows + t) * C::kRow;
           const float f = ex2(__ldcg(in + D) - m_eff2);
           l_all += f * __ldcg(in + D + 1);
 #pragma unroll
@@ -399,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       }
       const bool none = m_all == -INFINITY;
       const float inv = none ? 0.f : 1.f / l_all;
-      const size_t at = (static_cast<size_t>(w.s.tok0 + t) * p.H + h) * D;
+      const size_t at = (static_cast<size_t>(w.tok0 + t) * p.H + h) * D;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
         if (O_BF16)
@@ -408,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
           static_cast<float*>(p.o)[at + e * 32 + lane] = o[e] * inv;
       }
       if (p.lse != nullptr && lane == 0)
-        p.lse[static_cast<size_t>(h) * p.T + w.s.tok0 + t] =
+        p.lse[static_cast<size_t>(h) * p.T + w.tok0 + t] =
             none ? -INFINITY : (m_all + log2f(l_all)) * 0.69314718055994531f;
     }
   }

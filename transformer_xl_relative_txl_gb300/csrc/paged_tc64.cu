@@ -84,6 +84,7 @@ struct Bars {
   uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
   uint64_t q_full, q_empty;
   uint64_t q_ready, s_full[2], p_full[2], pv_done[2], o_full, o_free;
+  uint64_t begun[2];  // step g's softmax has its scores (index g % 2, phase g / 2)
   uint64_t sread[4];  // step g's S and distance window have been read (index g % 4, phase g / 4)
   uint64_t mma_final, pv_final, qr_final;
   uint64_t lbar[4];   // per quadrant: the non-owning warp's (m, l) of a unit is in `red`
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       mbar_init(&bars->s_full[s], 2);  // content and distance MMAs of a step
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->pv_done[s], 1);
+      mbar_init(&bars->begun[s], 1);
     }
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 8);
@@ -189,11 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           const uint32_t g = g0 + t, sb = g & 1;
           // S buffer sb was last read by step g-2.
           if (g >= 2 && !(ok = mbar_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
-          // The two parities run best half a step's time apart.  They start
-          // together (their first steps wait for the same instruction fetches)
-          // and would stay so: 0.98 us a step instead of 0.8.  Once, the odd
-          // one's scores are held back until the even one has read its own.
-          if (g == 3 && !(ok = mbar_wait(&bars->sread[2], 0, wait_ns, abort))) break;
+          // The two parities' warps share the schedulers, and run best half a
+          // step's time apart; started together they stay together, each
+          // waiting for the other's instructions (2165 cycles a step instead
+          // of 1500).  So a step's scores are issued when the step before has
+          // begun, which is one MMA latency, about that time, before they can
+          // be used.  Not for the first steps of a unit: the warps of the unit
+          // before may still be in its epilogue.
+          if (t >= 3 && !(ok = mbar_wait(&bars->begun[(g - 1) & 1], ((g - 1) >> 1) & 1, wait_ns, abort))) break;
           const int sk = nK % NK;
           if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
           tc_fence_after();
@@ -392,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       for (int t = first; t <= tl; t += 2) {
         const uint32_t g = g0 + t, sb = g & 1;
         if (!(ok = warp_wait(&bars->s_full[sb], (g >> 1) & 1, wait_ns, abort))) break;
+        if (quad == 0 && lane == 0) mbar_arrive(&bars->begun[sb]);
         tc_fence_after();
         // Distance window of this warp: ring-relative index z = 64 + a - c
         // (z < 64: tile t, < 128: tile t-1, else tile t-2).  Columns 0-31 use
