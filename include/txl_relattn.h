@@ -782,7 +782,8 @@ TXL_API int txl_debug_bwd_pairs_work(int B, int W, int M, int H, int split_qt, i
 /* Test hook, host only: how txl_relattn_forward_paged divides its work over
  * `ctas` CTAs.  kind 0: the decode kernel (entries of up to 4 tokens; key
  * steps of 64 rows at D = 64, 32 at D = 128), 1: the kernel for longer
- * entries (tiles of 128 queries, key steps of 64 rows).  n sequences of rows[i] live
+ * entries (tiles of 128 queries, key steps of 64 rows), 2: the fp32 kernel
+ * (tiles of 16 queries, key steps of 32 rows).  n sequences of rows[i] live
  * rows after start[i] dead ones, n_new[i] of them new.  Writes rows (CTA,
  * sequence, head, query tile, first key step, key steps, CTA of the unit's
  * first piece, index of this piece, pieces, place in the workspace) to out

@@ -270,18 +270,20 @@ def steps(start, rows, n, first, count, BK):
     return [start // BK] if x < start else list(range(start // BK, x // BK + 1))
 
 
-@pytest.mark.parametrize("kind,D", [(0, 64), (0, 128), (1, 64)])
+@pytest.mark.parametrize("kind,D", [(0, 64), (0, 128), (1, 64), (2, 40)])
 def test_every_step_has_one_cta(lib, kind, D):
     """The division of the paged attention: every key step of every unit on one CTA, the pieces of a unit numbered in
     key order on consecutive CTAs, their places distinct, and no CTA with much more than its share."""
     rng = np.random.default_rng(kind + D)
-    BK = 32 if kind == 0 and D == 128 else 64
+    BK = 32 if kind == 2 or (kind == 0 and D == 128) else 64
+    tile = (0, 128, 16)[kind]
+    unit = (3, 5, 1)[kind]  # cost of a unit besides its steps, in half steps
     for trial in range(120):
         n = int(rng.integers(1, [2, 5, 60][trial % 3] + 1))
         H = int(rng.integers(1, 9))
         start = rng.integers(0, [1, 16, 1024][trial % 3], n)
         rows = (10 ** rng.uniform(0, 4.5, n)).astype(int) * (rng.random(n) > 0.1)
-        new = rng.integers(1, 5, n) if kind == 0 else rng.integers(5, 700, n)
+        new = rng.integers(1, 5, n) if kind == 0 else rng.integers(5 if kind == 1 else 1, 700, n)
         ctas = int(rng.choice([1, 7, 152, 304]))
         got = lib.txl_debug_paged_pieces(kind, D, H, start, rows, new, ctas)
         assert (np.diff(got[:, 0]) >= 0).all() and got[:, 0].max() < ctas
@@ -292,20 +294,20 @@ def test_every_step_has_one_cta(lib, kind, D):
             if pieces > 1:
                 assert place not in places and place // 2 == c
                 places.add(place)
-            load[c] += 2 * nks + 3
+            load[c] += 2 * nks + unit
         count = {}
         for (i, h, qt), p in units.items():
-            want = steps(start[i], rows[i], new[i], 128 * qt if kind else 0, 128 if kind else 4, BK)
+            want = steps(start[i], rows[i], new[i], tile * qt, tile or 4, BK)
             assert [x[0] for x in p] == list(range(p[0][3]))
             assert [t for _, t0, nks, _ in p for t in range(t0, t0 + nks)] == want
             count[i] = count.get(i, 0) + 1
             first_pieces = [c for c, *r in got.tolist() if tuple(r[:3]) == (i, h, qt)] if n < 4 else []
             assert first_pieces == sorted(set(first_pieces))
         for i in range(n):
-            assert count[i] == H * (-(-int(new[i]) // 128) if kind else 1)
+            assert count[i] == H * (-(-int(new[i]) // tile) if kind else 1)
         # a CTA's range, a step more at its end, and what a unit costs besides its steps at each end
-        whole = sum(2 * x[2] for p in units.values() for x in p) + 3 * len(units)
-        assert load.max() <= whole / min(ctas, max(1, whole // 4)) + 2 + 2 * 3
+        whole = sum(2 * x[2] for p in units.values() for x in p) + unit * len(units)
+        assert load.max() <= whole / min(ctas, max(1, whole // 4)) + 2 + 2 * unit
 
 
 def test_one_split_unit_starts_per_cta(lib):

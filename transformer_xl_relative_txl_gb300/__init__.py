@@ -873,11 +873,11 @@ def txl_debug_paged_pieces(kind, D, H, start, rows, n_new, ctas):
     """Test hook (host only): the paged attention's division over `ctas` CTAs,
     an int32 array of rows (CTA, sequence, head, query tile, first key step,
     key steps, first CTA, index, pieces, place); kind 0: the decode kernel, 1:
-    the kernel for longer entries."""
+    the kernel for longer entries, 2: the fp32 kernel."""
     import numpy as np
 
     s, r, m = (np.ascontiguousarray(x, np.int32) for x in (start, rows, n_new))
-    tiles = sum(-(-int(x) // 128) for x in m) if kind else len(m)
+    tiles = sum(-(-int(x) // (128 if kind == 1 else 16)) for x in m) if kind else len(m)
     out = np.zeros((int(H) * tiles + int(ctas) + 1, 10), np.int32)
     n = lib.txl_debug_paged_pieces(int(kind), int(D), int(H), len(s), s.ctypes.data, r.ctypes.data, m.ctypes.data,
                                    int(ctas), out.ctypes.data, out.shape[0])

@@ -54,39 +54,35 @@ struct Cfg {
   static constexpr int kQuery = kDecodeRows * D * 2 + 2 * D * 4;  // a unit's rows of q, u and v
   static constexpr int kOffQ = kOffPart + 2 * kWarps * kDecodeRows * kRow * 4;
   static constexpr int kOffBar = kOffQ + 2 * kQuery;
-  static constexpr int kBarBytes = 384;
+  static constexpr int kBarBytes = 1408;
   static constexpr int kSmem = kOffBar + kBarBytes + 1024;
-  using Walk = PlanWalk<DecodeCost, BK, 0>;  // DecodeWalk64, DecodeWalk32
+  using Walk = PlanWalk<DecodeCost, BK, 0, 1, kDecodeRows>;  // DecodeWalk64, DecodeWalk32
 };
 
 struct Params {
-  PageBook book;
+  PlanArgs args;
   const __nv_bfloat16* q;
   const float* bias_u;
   const float* bias_v;
   void* o;
   float* lse;
-  int T, H, n_r;
   float scale_log2e;
-  const PlanHead* head;
-  const PlanSeq* seqs;
-  const int* starts;
-  int* counters;
+  PlanCut* cuts;
   float* part;
-  unsigned int* status;
   unsigned long long wait_ns;
   bool behind_tiles;
 };
 
 // A unit as the producer publishes it; nks 0: the CTA has no more.
 struct Unit {
-  int h, tok0, n, start, last, t0, nks, first, index, pieces;
+  int h, tok0, n, start, last, t0, nks, index, pieces;
 };
 
 struct Bars {
   uint64_t full[4], empty[4], joined;
   uint64_t q_full[2], q_empty[2];  // by unit parity: the unit and its queries are there; read
   Unit unit[2];
+  PlanState plan;
   int abort;
 };
 
@@ -158,23 +154,38 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     fence_mbar_init();
   }
   __syncthreads();
-  // Behind the plan this kernel waits for it.  Behind the tile kernel it need
-  // not: that one let it start after its own wait for the plan; what it waits
-  // for, at its end, is that the kernels behind it may take both as complete.
+  // Behind the tile kernel this one need not wait: that kernel lets it start
+  // after its own wait.  What it waits for then, at its end, is that the
+  // kernels behind it may take both as complete.
   if (!p.behind_tiles) grid_dep_wait();
   grid_dep_launch_dependents();
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
+  plan_begin<typename C::Walk>(p.args, static_cast<int>(gridDim.x), &bars->plan);
   const uint64_t wait_ns = p.wait_ns;
 
   if (warp == kWarps) {
     // ============================== producer ===============================
     typename C::Walk w;
-    bool more = w.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
+    PlanState* plan = &bars->plan;
+    PlanStep step = kPlanEnd;
+    auto filled = [&]() {  // the walker at a unit, or at the end
+      while (step == kPlanFill) {
+        const int count = plan_fill<typename C::Walk>(p.args, plan);
+        step = w.filled(count, plan->raw < p.args.n);
+      }
+    };
+    if (static_cast<int>(blockIdx.x) < plan->ctas) {
+      const int count = plan_fill<typename C::Walk>(p.args, plan);
+      step = w.begin(plan->seqs, count, plan->raw < p.args.n, plan->total, plan->ctas, p.args.H,
+                     static_cast<int>(blockIdx.x));
+      filled();
+    }
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_r);
     }
-    const int P = p.book.page_rows;
+    const int P = p.args.book.page_rows;
     const int box = min(P, BK), boxes = BK / box;  // a tile is `boxes` boxes of rows
     uint32_t g = 0, units = 0;
     bool ok = true, bad = false;
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
         uint8_t* at = queries + s * C::kQuery;
         const int total = w.s.n * (D / 2);  // words of the queries' rows
         for (int e = lane; e < total; e += 32)
-          copy4(at + e * 4, p.q + (static_cast<size_t>(w.s.tok0 + e / (D / 2)) * p.H + w.h) * D + e % (D / 2) * 2);
+          copy4(at + e * 4, p.q + (static_cast<size_t>(w.s.tok0 + e / (D / 2)) * p.args.H + w.h) * D + e % (D / 2) * 2);
 #pragma unroll
         for (int e = lane; e < D; e += 32) {
           copy4(at + kDecodeRows * D * 2 + e * 4, p.bias_u + w.h * D + e);
@@ -200,17 +211,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       if (lane == 0) {
         Unit u{};
         if (nks > 0)
-          u = Unit{w.h, w.s.tok0, w.s.n, w.s.start, w.s.start + w.s.rows - 1, w.p.t0, nks, w.p.first, w.p.index,
-                   w.p.pieces};
+          u = Unit{w.h, w.s.tok0, w.s.n, w.s.start, w.s.start + w.s.rows - 1, w.p.t0, nks, w.p.index, w.p.pieces};
         bars->unit[s] = u;
+        if (u.pieces > 1 && u.index == 0) p.cuts[blockIdx.x] = PlanCut{u.tok0, u.n, u.h, u.pieces};
         mbar_arrive(&bars->q_full[s]);
       }
       ++units;
     };
-    for (; ok && more; more = w.next()) {
+    for (; ok && step == kPlanUnit; step = w.next(), filled()) {
       publish(w.p.nks);
       if (!ok) break;
-      const int* row = p.book.table + static_cast<size_t>(w.s.slot) * p.book.max_pages;
+      const int* row = p.args.book.table + static_cast<size_t>(w.s.slot) * p.args.book.max_pages;
       const int last = w.s.start + w.s.rows - 1;
       const int m = w.s.start + w.s.rows - w.s.n;
       int id = -1, id0 = -32;  // this lane's page of the boxes from id0 on
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
           id = -1;
           if (x <= last && x + box > w.s.start) {
             id = row[x / P];
-            if (id < 0 || id >= p.book.n_pages) bad = true, id = p.book.n_pages;  // zero rows, nothing read
+            if (id < 0 || id >= p.args.book.n_pages) bad = true, id = p.args.book.n_pages;  // zero rows, nothing read
           }
         }
         const int s = g % NS;
@@ -252,8 +263,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       }
     }
     if (ok) publish(0);
-    if (bad) atomicOr(p.status, kStatusPagesBit);
-    if (!ok && lane == 0) report_timeout(abort, p.status);
+    if (bad) atomicOr(p.args.status, kStatusPagesBit);
+    if (!ok && lane == 0) report_timeout(abort, p.args.status);
     asm volatile("cp.async.wait_all;" ::: "memory");
     // This warp's copies land before the CTA may exit.
     for (uint32_t s = 0; s < NS && s < g; ++s) {
@@ -430,39 +441,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[y * kStride + e * 32 + lane], o[e]);
       }
-      if (w.pieces > 1) {
-        // A piece's result goes to the workspace; the last of the unit's pieces
-        // to arrive joins them in order, so the result does not depend on which
-        // it is.
-        float* out = p.part + (static_cast<size_t>(plan_place(blockIdx.x, w.index)) * kDecodeRows + t) * C::kRow;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) __stcg(out + e * 32 + lane, o[e]);
-        if (lane == 0) __stcg(out + D, m_all), __stcg(out + D + 1, l_all);
-        __threadfence();
-        __syncwarp();
-        int arrived = 0;
-        if (lane == 0) arrived = atomicAdd(p.counters + w.first * 4 + t, 1);
-        if (__shfl_sync(0xffffffffu, arrived, 0) != w.pieces - 1) continue;
-        __threadfence();
-        m_all = -INFINITY;
-        for (int y = 0; y < w.pieces; ++y)
-          m_all = fmaxf(m_all, __ldcg(p.part + (static_cast<size_t>(plan_place(w.first + y, y)) * kDecodeRows + t) *
-                                                   C::kRow + D));
-        const float m_eff2 = m_all == -INFINITY ? 0.f : m_all;
-        l_all = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-        for (int y = 0; y < w.pieces; ++y) {
-          const float* in = p.part + (static_cast<size_t>(plan_place(w.first + y, y)) * kDecodeRows + t) * C::kRow;
-          const float f = ex2(__ldcg(in + D) - m_eff2);
-          l_all += f * __ldcg(in + D + 1);
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, __ldcg(in + e * 32 + lane), o[e]);
-        }
-      }
       const bool none = m_all == -INFINITY;
       const float inv = none ? 0.f : 1.f / l_all;
-      const size_t at = (static_cast<size_t>(w.tok0 + t) * p.H + h) * D;
+      const float lse2 = none ? -INFINITY : m_all + log2f(l_all);
+      if (w.pieces > 1) {  // to the workspace, for the join
+        float* out = p.part + plan_place(static_cast<int>(blockIdx.x), w.index) * plan_part(kDecodeRows, D);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) out[t * D + e * 32 + lane] = o[e] * inv;
+        if (lane == 0) out[kDecodeRows * D + t] = lse2;
+        continue;
+      }
+      const size_t at = (static_cast<size_t>(w.tok0 + t) * p.args.H + h) * D;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
         if (O_BF16)
@@ -471,11 +460,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
           static_cast<float*>(p.o)[at + e * 32 + lane] = o[e] * inv;
       }
       if (p.lse != nullptr && lane == 0)
-        p.lse[static_cast<size_t>(h) * p.T + w.tok0 + t] =
-            none ? -INFINITY : (m_all + log2f(l_all)) * 0.69314718055994531f;
+        p.lse[static_cast<size_t>(h) * p.args.T + w.tok0 + t] = none ? -INFINITY : lse2 * 0.69314718055994531f;
     }
   }
-  if (!ok && lane == 0) report_timeout(abort, p.status);
+  if (!ok && lane == 0) report_timeout(abort, p.args.status);
   if (p.behind_tiles) grid_dep_wait();
 }
 
@@ -509,9 +497,8 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_
     const cuuint32_t box[3] = {64, 1, C::BR};
     if (!enc(&tm_r, a.r, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  Params p{b, static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse, a.T, a.H, a.n_r,
-           a.scale * 1.4426950408889634f, s.heads, s.seqs[0], s.starts[0], s.counters, s.part[0], wc.status,
-           wc.limit_ns, behind_tiles};
+  const Params p{plan_args(a, wc.status), static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse,
+                 a.scale * 1.4426950408889634f, s.decode.cuts, s.decode.part, wc.limit_ns, behind_tiles};
   auto kern = paged_decode_kernel<D, O_BF16>;
   static unsigned configured = 0;  // one bit per device ordinal < 32
   int dev = 0;

@@ -59,7 +59,7 @@ constexpr int kOffR = kOffV + NV * kRowTile;
 constexpr int kOffRed = kOffR + NR * kRowTile;
 constexpr int kRedFloats = 2 * 2 * BM + 2 * BM;  // [step parity][half][row] maxima, [unit parity][row] sums
 constexpr int kOffBar = kOffRed + kRedFloats * 4;
-constexpr int kBarBytes = 1024;
+constexpr int kBarBytes = 2304;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -73,6 +73,7 @@ struct Bars {
   uint64_t lbar[4];  // row-sum hand-over at the end of a unit (32 arrivals)
   TileUnit units[kUnitRing];
   TileWalk walk;
+  PlanState plan;
   int any;  // the CTA has a unit
   uint32_t tmem_base;
   int abort;
@@ -130,21 +131,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     bars->abort = 0;
     fence_mbar_init();
   }
-  // The kernels ahead on the stream, the plan among them, have completed from
-  // here on.
+  // The kernels ahead on the stream have completed from here on.
   grid_dep_wait();
-  // The decode kernel behind this one needs the plan alone: its CTAs start as
-  // this one's end.
+  // The decode kernel behind this one needs what this one does and no more: its
+  // CTAs start as this one's end.
   grid_dep_launch_dependents();
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (threadIdx.x == kLoaderWarp * 32) {
-    const bool some = bars->walk.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
-    bars->any = some ? 1 : 0;
-    if (some) publish_unit(bars->walk, bars->units, 0, p.cuts);
-  }
+  begin_units(bars, p.args, p.cuts, kLoaderWarp);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -195,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         gt = g0 + w.nks;
         ++un;
       }
-      if (!ok) report_timeout(abort, p.status);
+      if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->mma_final);
       mbar_wait_own(&bars->mma_final, 0, wait_ns);
     }
@@ -234,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         ++un;
         if (next_h < 0) break;
       }
-      if (!ok) report_timeout(abort, p.status);
+      if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->pv_final);
       mbar_wait_own(&bars->pv_final, 0, wait_ns);
     }
@@ -286,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         gt = g0 + w.nks;
         ++un;
       }
-      if (!ok) report_timeout(abort, p.status);
+      if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->qr_final);
       mbar_wait_own(&bars->qr_final, 0, wait_ns);
     }
@@ -477,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         if (unit->pieces > 1)
           store_piece<D>(*unit, a, ov, lse2, p.part);
         else
-          store_row<D, O_BF16>(*unit, a, ov, lse2, p.o, p.lse, p.T, p.H);
+          store_row<D, O_BF16>(*unit, a, ov, lse2, p.o, p.lse, p.args.T, p.args.H);
       } else if (unit->next_h >= 0 && !(ok = build_q(unit->next_h))) {
         break;
       }
@@ -485,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
       gt = g0 + nks;
       ++un;
     }
-    if (!ok) report_timeout(abort, p.status);
+    if (!ok) report_timeout(abort, p.args.status);
   }
 
   // ---- teardown ------------------------------------------------------------

@@ -49,10 +49,11 @@ constexpr int kPvWarp = 10;
 constexpr int kQrWarp = 11;
 constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, three MMA issuers)
 // Register split (launch: 168 per thread, 384 x 168 = 64512): softmax
-// warpgroups 224, producer warpgroup 56; 2*128*224 + 128*56 = 64512, and per
-// scheduler 224 + 224 + 56 = 504 <= 512 per thread-slot.
-constexpr uint32_t kRegsSoftmax = 224;
-constexpr uint32_t kRegsProducer = 56;
+// warpgroups 216, producer warpgroup 72; 2*128*216 + 128*72 = 64512.  (With 224
+// and 56 the loader spills: 107 us instead of 103 for 22 sequences of 512
+// tokens over 512 rows, 8 heads.)
+constexpr uint32_t kRegsSoftmax = 216;
+constexpr uint32_t kRegsProducer = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");
 constexpr uint32_t kColO = 0;    // O0, O1: 64 columns each
 constexpr uint32_t kColS = 128;  // S0, S1: 64 columns each
@@ -76,7 +77,7 @@ constexpr int kOffP = kOffR + NR * kRowTile;    // P (bf16): 2 buffers, same lay
 constexpr int kOffRed = kOffP + 2 * kQTile;     // [unit parity][m, l][row] handed to the epilogue
 constexpr int kOffBias = kOffRed + 2 * 2 * BM * 4;  // per softmax warp: 32 dims of u, then of v (fp32)
 constexpr int kOffBar = kOffBias + 8 * 64 * 4;
-constexpr int kBarBytes = 1152;
+constexpr int kBarBytes = 2304;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -84,13 +85,13 @@ struct Bars {
   uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
   uint64_t q_full, q_empty;
   uint64_t q_ready, s_full[2], p_full[2], pv_done[2], o_full, o_free;
-  uint64_t begun[2];  // step g's softmax has its scores (index g % 2, phase g / 2)
   uint64_t sread[4];  // step g's S and distance window have been read (index g % 4, phase g / 4)
   uint64_t mma_final, pv_final, qr_final;
   uint64_t lbar[4];   // per quadrant: the non-owning warp's (m, l) of a unit is in `red`
   uint64_t lfree[4];  // per quadrant: the epilogue has read it
   TileUnit units[kUnitRing];
   TileWalk walk;
+  PlanState plan;
   int any;            // the CTA has a unit
   uint32_t tmem_base;
   int abort;
@@ -133,7 +134,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       mbar_init(&bars->s_full[s], 2);  // content and distance MMAs of a step
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->pv_done[s], 1);
-      mbar_init(&bars->begun[s], 1);
     }
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 8);
@@ -146,21 +146,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     bars->abort = 0;
     fence_mbar_init();
   }
-  // The kernels ahead on the stream, the plan among them, have completed from
-  // here on.
+  // The kernels ahead on the stream have completed from here on.
   grid_dep_wait();
-  // The decode kernel behind this one needs the plan alone: its CTAs start as
-  // this one's end.
+  // The decode kernel behind this one needs what this one does and no more: its
+  // CTAs start as this one's end.
   grid_dep_launch_dependents();
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (threadIdx.x == kLoaderWarp * 32) {
-    const bool some = bars->walk.begin(p.seqs, plan_load(p.head), p.starts, p.H, blockIdx.x);
-    bars->any = some ? 1 : 0;
-    if (some) publish_unit(bars->walk, bars->units, 0, p.cuts);
-  }
+  begin_units(bars, p.args, p.cuts, kLoaderWarp);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -171,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
     setmaxnreg_dec<kRegsProducer>();
-    run_tile_loader<D, NK, 2, true>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, 0, true>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ===================== content-score MMA issuer ========================
     setmaxnreg_dec<kRegsProducer>();
@@ -191,14 +186,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           const uint32_t g = g0 + t, sb = g & 1;
           // S buffer sb was last read by step g-2.
           if (g >= 2 && !(ok = mbar_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
-          // The two parities' warps share the schedulers, and run best half a
-          // step's time apart; started together they stay together, each
-          // waiting for the other's instructions (2165 cycles a step instead
-          // of 1500).  So a step's scores are issued when the step before has
-          // begun, which is one MMA latency, about that time, before they can
-          // be used.  Not for the first steps of a unit: the warps of the unit
-          // before may still be in its epilogue.
-          if (t >= 3 && !(ok = mbar_wait(&bars->begun[(g - 1) & 1], ((g - 1) >> 1) & 1, wait_ns, abort))) break;
           const int sk = nK % NK;
           if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
           tc_fence_after();
@@ -215,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         gt = g0 + w.nks;
         ++un;
       }
-      if (!ok) report_timeout(abort, p.status);
+      if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->mma_final);
       mbar_wait_own(&bars->mma_final, 0, wait_ns);
     }
@@ -273,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         ++un;
         rb = (rb + w.nks + 2) & (kSlots - 1);
       }
-      if (!ok) report_timeout(abort, p.status);
+      if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->qr_final);
       mbar_wait_own(&bars->qr_final, 0, wait_ns);
     }
@@ -317,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         ++un;
         if (next_h < 0) break;
       }
-      if (!ok) report_timeout(abort, p.status);
+      if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->pv_final);
       mbar_wait_own(&bars->pv_final, 0, wait_ns);
     }
@@ -397,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       for (int t = first; t <= tl; t += 2) {
         const uint32_t g = g0 + t, sb = g & 1;
         if (!(ok = warp_wait(&bars->s_full[sb], (g >> 1) & 1, wait_ns, abort))) break;
-        if (quad == 0 && lane == 0) mbar_arrive(&bars->begun[sb]);
         tc_fence_after();
         // Distance window of this warp: ring-relative index z = 64 + a - c
         // (z < 64: tile t, < 128: tile t-1, else tile t-2).  Columns 0-31 use
@@ -516,15 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
         }
         l_run = l_run * alpha + sum;
-        // The next unit's (q+u), (q+v) go to the other buffer once this
-        // warp's first step of this unit has seen its scores: the MMAs of the
-        // unit before, which read that buffer, are complete by then.
-        bool build = t == first && has_next;
         if (has_dead_rows(*unit, kt)) {
-          // The value tile may wait in the loader's queue behind the load of
-          // the q after next, which waits for this build: so that goes first.
-          if (build && !(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
-          build = false;
           // The stage's phases go by in order before this warp: the P.V two
           // steps back is done, and the stage is refilled only after this
           // step's.
@@ -533,7 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         }
         tc_fence_before();  // orders the O rescale's tcgen05.st before the arrive
         warp_arrive_smem(&bars->p_full[sb]);
-        if (build && !(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
+        // The next unit's (q+u), (q+v) go to the other buffer once this
+        // warp's first step of this unit has seen its scores: the MMAs of the
+        // unit before, which read that buffer, are complete by then.
+        if (t == first && has_next && !(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
       }
       if (!ok) break;
       if (first > tl && has_next) {
@@ -611,10 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           }
           store_pending = true;
           if (p.lse != nullptr)
-            p.lse[static_cast<size_t>(w.h) * p.T + w.row0 + a] =
+            p.lse[static_cast<size_t>(w.h) * p.args.T + w.row0 + a] =
                 lse2 == -INFINITY ? -INFINITY : lse2 * 0.69314718055994531f;
         } else {
-          store_row<D, O_BF16>(w, a, ov, lse2, p.o, p.lse, p.T, p.H);
+          store_row<D, O_BF16>(w, a, ov, lse2, p.o, p.lse, p.args.T, p.args.H);
         }
       }
       if (!has_next) break;
@@ -622,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       ++un;
       rb = (rb + nks + 2) & (kSlots - 1);
     }
-    if (!ok) report_timeout(abort, p.status);
+    if (!ok) report_timeout(abort, p.args.status);
     // Output stores in flight must finish before the CTA's shared memory goes.
     if (lane == 0) bulk_wait_group0();
     __syncwarp();

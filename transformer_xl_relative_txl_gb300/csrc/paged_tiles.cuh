@@ -29,25 +29,61 @@ struct TileUnit {
   int next_h;          // head of the CTA's next unit, -1: none
 };
 
-// The walker's unit; moves the walker on.  The first piece of a cut unit is
-// noted for the kernel that joins the pieces.
-__device__ __forceinline__ void publish_unit(TileWalk& walk, TileUnit* ring, uint32_t k, TileCut* cuts) {
-  TileUnit u;
-  u.h = walk.h;
-  const int i0 = walk.qt * kTileQueries;
-  u.row0 = walk.s.tok0 + i0;
-  u.nq = min(kTileQueries, walk.s.n - i0);
-  u.t0 = walk.p.t0;
-  u.nks = walk.p.nks;
-  u.d0 = walk.s.start + walk.s.rows - walk.s.n + i0;
-  u.start = walk.s.start;
-  u.last = walk.s.start + walk.s.rows - 1;
-  u.slot = walk.s.slot;
-  u.index = walk.p.index;
-  u.pieces = walk.p.pieces;
-  if (u.pieces > 1 && u.index == 0) cuts[blockIdx.x] = TileCut{u.row0, u.nq, u.h, u.pieces};
-  u.next_h = walk.next() ? walk.h : -1;
-  ring[k % kUnitRing] = u;
+// One warp.  The walker's unit into the ring, the walker to the next; the first
+// piece of a cut unit is noted for the kernel that joins the pieces.
+template <typename Bars>
+__device__ __forceinline__ void publish_unit(Bars* bars, const PlanArgs& args, uint32_t k, PlanCut* cuts) {
+  const bool lead = (threadIdx.x & 31) == 0;
+  TileWalk& walk = bars->walk;
+  TileUnit& u = bars->units[k % kUnitRing];
+  PlanStep step = kPlanEnd;
+  if (lead) {
+    const int i0 = walk.qt * kTileQueries;
+    u.h = walk.h;
+    u.row0 = walk.s.tok0 + i0;
+    u.nq = min(kTileQueries, walk.s.n - i0);
+    u.t0 = walk.p.t0;
+    u.nks = walk.p.nks;
+    u.d0 = walk.s.start + walk.s.rows - walk.s.n + i0;
+    u.start = walk.s.start;
+    u.last = walk.s.start + walk.s.rows - 1;
+    u.slot = walk.s.slot;
+    u.index = walk.p.index;
+    u.pieces = walk.p.pieces;
+    if (u.pieces > 1 && u.index == 0) cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
+    step = walk.next();
+  }
+  while (__shfl_sync(0xffffffffu, step, 0) == kPlanFill) {
+    const int count = plan_fill<TileWalk>(args, &bars->plan);
+    if (lead) step = walk.filled(count, bars->plan.raw < args.n);
+  }
+  if (lead) u.next_h = step == kPlanUnit ? walk.h : -1;
+  __syncwarp();
+}
+
+// All threads of the CTA, behind grid_dep_wait: the division of the work; the
+// warp `loader` then publishes the CTA's first unit, if it has one (bars->any),
+// which the barrier that the caller has next makes known.
+template <typename Bars>
+__device__ __forceinline__ void begin_units(Bars* bars, const PlanArgs& args, PlanCut* cuts, int loader) {
+  if (threadIdx.x == 0) cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
+  plan_begin<TileWalk>(args, static_cast<int>(gridDim.x), &bars->plan);
+  if (static_cast<int>(threadIdx.x >> 5) != loader) return;
+  const bool lead = (threadIdx.x & 31) == 0;
+  PlanStep step = kPlanEnd;
+  if (static_cast<int>(blockIdx.x) < bars->plan.ctas) {
+    int count = plan_fill<TileWalk>(args, &bars->plan);
+    if (lead)
+      step = bars->walk.begin(bars->plan.seqs, count, bars->plan.raw < args.n, bars->plan.total, bars->plan.ctas,
+                              args.H, static_cast<int>(blockIdx.x));
+    while (__shfl_sync(0xffffffffu, step, 0) == kPlanFill) {
+      count = plan_fill<TileWalk>(args, &bars->plan);
+      if (lead) step = bars->walk.filled(count, bars->plan.raw < args.n);
+    }
+  }
+  const bool some = __shfl_sync(0xffffffffu, step, 0) == kPlanUnit;
+  if (lead) bars->any = some ? 1 : 0;
+  if (some) publish_unit(bars, args, 0, cuts);
 }
 
 // Zeroes the rows of a landed value tile that are not live: weight 0 times a
@@ -97,7 +133,7 @@ __device__ __forceinline__ void store_row(const TileUnit& u, int a, const float 
 // 512 tokens over 512 rows, 8 heads, where every CTA has two pieces.)
 template <int D>
 __device__ __forceinline__ void store_piece(const TileUnit& u, int a, const float (&ov)[D], float lse2, float* part) {
-  float* mine = part + plan_place(static_cast<int>(blockIdx.x), u.index) * static_cast<size_t>(tile_part(D));
+  float* mine = part + plan_place(static_cast<int>(blockIdx.x), u.index) * static_cast<size_t>(plan_part(kTileQueries, D));
   float4* po = reinterpret_cast<float4*>(mine + a * D);
 #pragma unroll
   for (int c = 0; c < D / 4; ++c) po[c] = make_float4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
@@ -106,21 +142,16 @@ __device__ __forceinline__ void store_piece(const TileUnit& u, int a, const floa
 
 // Kernel parameters common to both.
 struct TileParams {
-  PageBook book;
+  PlanArgs args;
   int log_page_rows;
   const float* bias_u;
   const float* bias_v;
   void* o;
   float* lse;
-  int T, H;
   float scale_log2e;  // |scale| * log2(e)
   float qsign;        // sign of scale, folded into (q+u), (q+v)
-  const PlanHead* head;
-  const PlanSeq* seqs;
-  const int* starts;
-  TileCut* cuts;
+  PlanCut* cuts;
   float* part;
-  unsigned int* status;
   unsigned long long wait_ns;
 };
 
@@ -237,13 +268,12 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
   for (uint32_t un = 0; ok; ++un) {
     const TileUnit& w = bars->units[un % kUnitRing];
     const int next_h = w.next_h, h = w.h, d0 = w.d0, start = w.start, last = w.last, tend = w.t0 + w.nks;
-    const int* row = p.book.table + static_cast<size_t>(w.slot) * p.book.max_pages;
+    const int* row = p.args.book.table + static_cast<size_t>(w.slot) * p.args.book.max_pages;
     int t = w.t0;
     if (LAG > 0 && un >= kHold) flush_v(un - kHold);
     if (!ok) break;
     if (next_h >= 0) {
-      if (lane == 0) publish_unit(bars->walk, bars->units, un + 1, p.cuts);
-      __syncwarp();
+      publish_unit(bars, p.args, un + 1, p.cuts);
       if (AHEAD) load_q(un + 1);
     }
     if (!AHEAD) load_q(un);
@@ -261,9 +291,9 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
       Tile e;
       e.page = -1;
       if (lv) {
-        const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.book.n_pages);
+        const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.args.book.n_pages);
         bad |= !good;
-        e.page = good ? id : p.book.n_pages;
+        e.page = good ? id : p.args.book.n_pages;
       }
       if (t + 1 < tend) id = live(t + 1) ? row[((t + 1) * kStepKeys + off) >> log_page] : 0;
       e.bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lv) & 0xf)) << (log_box + (D == 64 ? 7 : 8));
@@ -290,8 +320,8 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     if (next_h < 0) break;
   }
   if (LAG > 0) flush_v(0xffffffffu);
-  if (bad) atomicOr(p.status, kStatusPagesBit);
-  if (any && !ok && lane == 0) report_timeout(abort, p.status);
+  if (bad) atomicOr(p.args.status, kStatusPagesBit);
+  if (any && !ok && lane == 0) report_timeout(abort, p.args.status);
   // This warp's own copies land before the CTA may exit.
   if (nQ > 0) mbar_wait_own(&bars->q_full, (nQ - 1) & 1, p.wait_ns);
   if (leads)

@@ -54,7 +54,6 @@ struct PagedAttn {
 };
 size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16);
 cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_t stream);
-cudaError_t launch_paged_simt(const PagedAttn& a, unsigned int* status, cudaStream_t stream);
 
 // From api.cu: the status word with the wait bound, the tensor-map encoder.
 int api_wait_ctl(WaitCtl* wc);
