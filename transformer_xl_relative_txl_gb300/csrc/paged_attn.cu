@@ -21,7 +21,7 @@ int pieces_of(int H, int n, const int* start, const int* rows, const int* fresh,
   const int ctas = plan_ctas<typename Walk::Cost>(total, most);
   int count = 0;
   for (int c = 0, x = 0; c < ctas; ++c) {
-    while (x + 1 < n && list[x + 1].pre <= c * total / ctas) ++x;
+    while (x + 1 < n && list[x + 1].pre <= plan_cut(c, total, ctas)) ++x;
     Walk w;
     for (PlanStep s = w.begin(list.data() + x, n - x, false, total, ctas, H, c); s == kPlanUnit; s = w.next()) {
       if (count == cap) return -1;

@@ -20,6 +20,8 @@
 // of 16 queries).
 #pragma once
 
+#include <cstdint>
+
 #include <cuda_runtime.h>
 
 #include "pages.h"
@@ -54,9 +56,23 @@ __host__ __device__ __forceinline__ int plan_steps(int start, int x, int BK) {
   return x < start ? 1 : x / BK - start / BK + 1;
 }
 
-// The CTA whose range of the line holds position x.
+// Where CTA c's range begins: floor(c total / ctas).  (A 64-bit division takes
+// over 100 instructions; nearly every line is shorter than 2^31.)
+__host__ __device__ __forceinline__ long long plan_cut(int c, long long total, int ctas) {
+  if (total >> 31) return c * total / ctas;
+  const uint32_t n = static_cast<uint32_t>(ctas), q = static_cast<uint32_t>(total) / n;
+  const uint32_t rest = static_cast<uint32_t>(total) - q * n;
+  return static_cast<long long>(c) * q + static_cast<uint32_t>(c) * rest / n;  // c, rest < ctas < 2^16
+}
+
+// The CTA whose range of the line holds position x: the largest c with
+// plan_cut(c) <= x.  The estimate is off by one at most (ctas < 2^16).
 __host__ __device__ __forceinline__ int plan_owner(long long x, long long total, int ctas) {
-  return static_cast<int>(((x + 1) * ctas - 1) / total);
+  int c = static_cast<int>(static_cast<float>(x) / static_cast<float>(total) * static_cast<float>(ctas));
+  if (c >= ctas) c = ctas - 1;
+  while (c > 0 && plan_cut(c, total, ctas) > x) --c;
+  while (c + 1 < ctas && plan_cut(c + 1, total, ctas) <= x) ++c;
+  return c;
 }
 
 // CTAs that share a line of length `total`: a CTA's range holds at least two
@@ -64,7 +80,8 @@ __host__ __device__ __forceinline__ int plan_owner(long long x, long long total,
 // steps.
 template <typename Cost>
 __host__ __device__ __forceinline__ int plan_ctas(long long total, int most) {
-  const long long want = total / (2 * Cost::kStep);
+  static_assert(Cost::kStep == 2, "a shift");
+  const long long want = total >> 2;
   return total == 0 ? 0 : (want >= most ? most : (want < 1 ? 1 : static_cast<int>(want)));
 }
 
@@ -80,8 +97,9 @@ template <typename Cost>
 __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int base, int c, long long lo,
                                                      long long hi, long long total, int ctas) {
   const long long s0 = a + Cost::kUnit;
-  long long from = lo < s0 ? 0 : (lo - s0) / Cost::kStep;
-  long long to = hi < s0 ? 0 : (hi - s0) / Cost::kStep;
+  static_assert(Cost::kStep == 2, "shifts");
+  long long from = lo < s0 ? 0 : (lo - s0) >> 1;
+  long long to = hi < s0 ? 0 : (hi - s0) >> 1;
   if (from > steps) from = steps;
   if (to > steps) to = steps;
   Piece p;
@@ -151,12 +169,15 @@ struct PlanWalk {
     ctas = n_ctas;
     H = heads;
     c = cta;
-    lo = c * total / ctas;
-    hi = (c + 1LL) * total / ctas;
+    lo = plan_cut(c, total, ctas);
+    hi = plan_cut(c + 1, total, ctas);
     i = 0;
     s = seqs[0];
     const long long per = cost_of_head();
-    h = static_cast<int>((lo - s.pre) / per);
+    const long long past = lo - s.pre;
+    h = past >> 31 ? static_cast<int>(past / per)
+                   : static_cast<int>(static_cast<uint32_t>(past) /
+                                      static_cast<uint32_t>(per < past + 1 ? per : past + 1));
     a = s.pre + h * per;
     qt = 0;
     while (a + cost_of(qt) <= lo) a += cost_of(qt++);
@@ -285,7 +306,7 @@ __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanStat
   const int ctas = plan_ctas<typename Walk::Cost>(total, most);
   const int c = static_cast<int>(blockIdx.x);
   if (c < ctas) {
-    const long long lo = c * total / ctas;
+    const long long lo = plan_cut(c, total, ctas);
     long long upto = 0;
     for (int base = 0; base < p.n && upto <= lo; base += nt) {
       if (p.n > nt) before = scan(base, &mine, &all);  // else at hand

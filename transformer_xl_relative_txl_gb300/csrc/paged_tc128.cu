@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
       // Unit 0 is published before the CTA's first barrier, unit un + 1 before
       // the loads of unit un's keys.
       const TileUnit* unit = &bars->units[un % kUnitRing];
-      const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
+      const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start, last = unit->last;
       float m_use = -INFINITY;  // running max in log2 units (lazy)
       float l_half = 0.f;       // row sum over this half's columns
       const uint32_t g0 = gt;
@@ -375,9 +375,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         const int kt = t0 + t;                           // key step of the tile
         const int lim = d0 - BN * kt + a - 32 * half;    // column k visible iff low <= k <= lim
         const int low = start - BN * kt - 32 * half;
-        if (d0 - BN * kt + quad * 32 - 32 * half < 31 || low > 0) {  // some lane of the warp masks
+        const bool dead = start > BN * kt || BN * kt + BN - 1 > last;  // the tile has rows that are not live
+        if (d0 - BN * kt + quad * 32 - 32 * half < 31) {               // some lane of the warp masks
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (k <= lim && k >= low) ? x[k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) x[k] = (k <= lim) ? x[k] : -INFINITY;
+        }
+        if (low > 0) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = (k >= low) ? x[k] : -INFINITY;
         }
         float t3[11];
 #pragma unroll
@@ -433,12 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         tc_fence_after();
         tmem_st16(tmem + lane_base + kColP + sb * 32 + 16 * half, pk);
         tmem_wait_st();
-        if (has_dead_rows(*unit, kt)) {
+        if (dead) {
           // The stage's phases go by in order before this warp: the P.V two
           // steps back is done, and the stage is refilled only after this
           // step's.
           if (!(ok = warp_wait(&bars->fullV[g % NV], (g / NV) & 1, wait_ns, abort))) break;
-          zero_dead_rows<D>(*unit, kt, sV + (g % NV) * kRowTile, warp, 8, lane);
+          zero_dead_rows<D>(start, last, kt, sV + (g % NV) * kRowTile, warp, 8, lane);
           fence_proxy_async_smem();
         }
         warp_arrive_tc(&bars->p_full[sb]);

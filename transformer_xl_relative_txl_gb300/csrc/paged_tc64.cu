@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     while (any && ok) {
       // Published before the q tile that the build above waited for.
       const TileUnit* unit = &bars->units[un % kUnitRing];
-      const int next_h = unit->next_h, nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
+      const int next_h = unit->next_h, nks = unit->nks, t0 = unit->t0, d0 = unit->d0;
+      const int start = unit->start, last = unit->last;
       const uint32_t g0 = gt;
       const bool has_next = next_h >= 0;
       const float bu_next = has_next ? bias_of(next_h, p.bias_u) : 0.f;
@@ -397,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         const int kt = t0 + t;              // key step of the tile
         const int lim = d0 - BN * kt + a;   // column c visible iff low <= c <= lim
         const int low = start - BN * kt;
-        const bool diag = d0 - BN * kt + quad * 32 < 63 || low > 0;  // some lane of the warp masks
+        const bool diag = d0 - BN * kt + quad * 32 < 63;  // some lane of the warp masks
+        const bool dead = low > 0 || BN * kt + BN - 1 > last;  // the tile has rows that are not live
         const float m_old = m_use;
         float m_new = m_use;
         // All of this step's TMEM reads at once -- the 96-distance window and
@@ -435,7 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         }
         if (diag) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = (k <= lim && k >= low) ? x[k] : -INFINITY;
+          for (int k = 0; k < 64; ++k) x[k] = (k <= lim) ? x[k] : -INFINITY;
+        }
+        if (low > 0) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) x[k] = (k >= low) ? x[k] : -INFINITY;
         }
         // Lazy running max over the step's 64 scores (log2 units).
         float t3[22];
@@ -502,12 +508,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
         }
         l_run = l_run * alpha + sum;
-        if (has_dead_rows(*unit, kt)) {
+        if (dead) {
           // The stage's phases go by in order before this warp: the P.V two
           // steps back is done, and the stage is refilled only after this
           // step's.
           if (!(ok = warp_wait(&bars->fullV[g % NV], (g / NV) & 1, wait_ns, abort))) break;
-          zero_dead_rows<D>(*unit, kt, sV + (g % NV) * kRowTile, quad, 4, lane);
+          zero_dead_rows<D>(start, last, kt, sV + (g % NV) * kRowTile, quad, 4, lane);
         }
         tc_fence_before();  // orders the O rescale's tcgen05.st before the arrive
         warp_arrive_smem(&bars->p_full[sb]);

@@ -91,17 +91,14 @@ __device__ __forceinline__ void begin_units(Bars* bars, const PlanArgs& args, Pl
 // `warps` warps; the caller's proxy fence and arrival on the barrier that the
 // P.V issuer waits for follow.
 template <int D>
-__device__ __forceinline__ void zero_dead_rows(const TileUnit& u, int t, uint8_t* stage, int warp, int warps,
+__device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8_t* stage, int warp, int warps,
                                                int lane) {
   const int x0 = t * kStepKeys;
   for (int y = warp; y < kStepKeys; y += warps) {
-    if (x0 + y >= u.start && x0 + y <= u.last) continue;
+    if (x0 + y >= start && x0 + y <= last) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) *reinterpret_cast<uint32_t*>(stage + c * kStepKeys * 128 + y * 128 + lane * 4) = 0;
   }
-}
-__device__ __forceinline__ bool has_dead_rows(const TileUnit& u, int t) {
-  return t * kStepKeys < u.start || t * kStepKeys + kStepKeys - 1 > u.last;
 }
 
 // Row `a` of a unit (lane `lane` of quadrant `quad`), o normalised by its own
