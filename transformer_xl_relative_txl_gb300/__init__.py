@@ -420,19 +420,22 @@ def txl_dense(x, W, y, bias=None, relu=False, stream=None):
     return y
 
 
+_I32 = torch.int32
+
+
 def _vectors(dev, n, *tensors):
     """Pointers of contiguous int32 vectors of n entries on device dev, where
     the call launches; None stays None."""
-    out = []
+    out, shape = [], (n,)
     for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        elif t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"expected a contiguous int32 vector of {n} entries")
-        if t.get_device() != dev:
+        elif t.get_device() != dev:
             raise ValueError("tensors must live in the current device's memory")
-        out.append(t.data_ptr())
+        else:
+            out.append(t.data_ptr())
     return out
 
 
@@ -442,12 +445,12 @@ def _tensors(dev, *tensors):
     for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if not t.is_contiguous():
+        elif not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-        if t.get_device() != dev:
+        elif t.get_device() != dev:
             raise ValueError("tensors must live in the current device's memory")
-        out.append(t.data_ptr())
+        else:
+            out.append(t.data_ptr())
     return out
 
 
@@ -475,15 +478,15 @@ def _book(dev, book, page_rows):
     """The C struct of a page book as bytes, and its number of pages: a dict
     of int32 tensors table [slots, max_pages], start and rows [slots], refs
     [pages]."""
-    table, refs = book["table"], book["refs"]
-    if table.dtype is not torch.int32 or table.dim() != 2:
-        raise ValueError("table must be a contiguous int32 [slots, max_pages] tensor")
-    n_slots, max_pages = table.shape
+    table, start, rows, refs = book["table"], book["start"], book["rows"], book["refs"]
+    shape = table.shape
     n_pages = refs.numel()
-    table_p, = _tensors(dev, table)
-    start_p, rows_p = _vectors(dev, n_slots, book["start"], book["rows"])
-    refs_p, = _vectors(dev, n_pages, refs)
-    return _pack_book(table_p, start_p, rows_p, refs_p, n_slots, max_pages, n_pages, page_rows), n_pages
+    if len(shape) != 2 or start.shape != shape[:1] or rows.shape != start.shape or refs.dim() != 1:
+        raise ValueError("a book is table [slots, max_pages], start and rows [slots], refs [pages]")
+    for t in (table, start, rows, refs):
+        if t.dtype is not _I32:
+            raise ValueError("a book's tensors are int32")
+    return _pack_book(*_tensors(dev, table, start, rows, refs), *shape, n_pages, page_rows), n_pages
 
 
 def _pools(dev, k_pages, v_pages, n_pages=None):

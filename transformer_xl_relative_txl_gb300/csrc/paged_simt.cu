@@ -87,33 +87,37 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const Params p) {
   if (tid == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
   plan_begin<SimtWalk>(p.args, static_cast<int>(gridDim.x), &sh->plan);
 
-  // Warp 0: the walker's unit into `slot`; `step`: what the walker met.
-  auto publish = [&](int slot, PlanStep step) {
-    while (__shfl_sync(0xffffffffu, step, 0) == kPlanFill) {
+  // Warp 0, all lanes alike: the walker's unit into `slot`; `step`: what the
+  // walker met.  (The walker rests in shared memory and works in registers.)
+  auto publish = [&](int slot, SimtWalk& walk, PlanStep step) {
+    while (step == kPlanFill) {
       const int count = plan_fill<SimtWalk>(p.args, &sh->plan);
-      if (lane == 0) step = sh->walk.filled(count, sh->plan.raw < p.args.n);
+      step = walk.filled(count, sh->plan.raw < p.args.n);
     }
+    __syncwarp();  // every lane has read the walker
     if (lane == 0) {
       Unit u{};
       if (step == kPlanUnit) {
-        const SimtWalk& w = sh->walk;
-        const int i0 = w.qt * BQ;
-        u = Unit{w.h,    w.s.tok0 + i0, min(BQ, w.s.n - i0), w.p.t0,   w.p.nks,   w.s.start + w.s.rows - w.s.n + i0,
-                 w.s.start, w.s.start + w.s.rows - 1, w.s.slot, w.p.index, w.p.pieces};
+        const PlanSeq& s = walk.s;
+        const int i0 = walk.qt * BQ;
+        u = Unit{walk.h,     s.tok0 + i0,          min(BQ, s.n - i0), walk.p.t0,    walk.p.nks, s.start + s.rows - s.n + i0,
+                 s.start, s.start + s.rows - 1, s.slot,            walk.p.index, walk.p.pieces};
         if (u.pieces > 1 && u.index == 0) p.cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
       }
       sh->unit[slot] = u;
+      sh->walk = walk;
     }
+    __syncwarp();
   };
   if (warp == 0) {
     PlanStep step = kPlanEnd;
+    SimtWalk walk;
     if (static_cast<int>(blockIdx.x) < sh->plan.ctas) {
       const int count = plan_fill<SimtWalk>(p.args, &sh->plan);
-      if (lane == 0)
-        step = sh->walk.begin(sh->plan.seqs, count, sh->plan.raw < p.args.n, sh->plan.total, sh->plan.ctas, H,
-                              static_cast<int>(blockIdx.x));
+      step = walk.begin(sh->plan.seqs, count, sh->plan.raw < p.args.n, sh->plan.total, sh->plan.ctas, H,
+                        static_cast<int>(blockIdx.x));
     }
-    publish(0, step);
+    publish(0, walk, step);
   }
   __syncthreads();
 
@@ -122,9 +126,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const Params p) {
     const Unit w = sh->unit[un & 1];
     if (w.nks == 0) break;
     if (warp == 0) {
-      PlanStep step = kPlanEnd;
-      if (lane == 0) step = sh->walk.next();
-      publish((un + 1) & 1, step);
+      SimtWalk walk = sh->walk;
+      publish((un + 1) & 1, walk, walk.next());
     }
     for (int y = warp; y < BQ; y += kThreads / 32)
       for (int d = lane; d < D; d += 32) {

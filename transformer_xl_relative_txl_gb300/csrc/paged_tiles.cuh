@@ -34,14 +34,16 @@ struct TileUnit {
 template <typename Bars>
 __device__ __forceinline__ void publish_unit(Bars* bars, const PlanArgs& args, uint32_t k, PlanCut* cuts) {
   const bool lead = (threadIdx.x & 31) == 0;
-  TileWalk& walk = bars->walk;
   TileUnit& u = bars->units[k % kUnitRing];
-  PlanStep step = kPlanEnd;
+  // The walker works in registers: in place, each of its dependent steps would
+  // cost a shared-memory latency.
+  TileWalk walk = bars->walk;
+  const int i0 = walk.qt * kTileQueries;
   if (lead) {
-    const int i0 = walk.qt * kTileQueries;
+    const int nq = min(kTileQueries, walk.s.n - i0);
     u.h = walk.h;
     u.row0 = walk.s.tok0 + i0;
-    u.nq = min(kTileQueries, walk.s.n - i0);
+    u.nq = nq;
     u.t0 = walk.p.t0;
     u.nks = walk.p.nks;
     u.d0 = walk.s.start + walk.s.rows - walk.s.n + i0;
@@ -50,14 +52,19 @@ __device__ __forceinline__ void publish_unit(Bars* bars, const PlanArgs& args, u
     u.slot = walk.s.slot;
     u.index = walk.p.index;
     u.pieces = walk.p.pieces;
-    if (u.pieces > 1 && u.index == 0) cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
-    step = walk.next();
+    if (walk.p.pieces > 1 && walk.p.index == 0)
+      cuts[blockIdx.x] = PlanCut{walk.s.tok0 + i0, nq, walk.h, walk.p.pieces};
   }
-  while (__shfl_sync(0xffffffffu, step, 0) == kPlanFill) {
+  PlanStep step = walk.next();
+  while (step == kPlanFill) {
     const int count = plan_fill<TileWalk>(args, &bars->plan);
-    if (lead) step = walk.filled(count, bars->plan.raw < args.n);
+    step = walk.filled(count, bars->plan.raw < args.n);
   }
-  if (lead) u.next_h = step == kPlanUnit ? walk.h : -1;
+  __syncwarp();  // every lane has read the walker
+  if (lead) {
+    u.next_h = step == kPlanUnit ? walk.h : -1;
+    bars->walk = walk;
+  }
   __syncwarp();
 }
 
@@ -72,18 +79,19 @@ __device__ __forceinline__ void begin_units(Bars* bars, const PlanArgs& args, Pl
   const bool lead = (threadIdx.x & 31) == 0;
   PlanStep step = kPlanEnd;
   if (static_cast<int>(blockIdx.x) < bars->plan.ctas) {
+    TileWalk walk;
     int count = plan_fill<TileWalk>(args, &bars->plan);
-    if (lead)
-      step = bars->walk.begin(bars->plan.seqs, count, bars->plan.raw < args.n, bars->plan.total, bars->plan.ctas,
-                              args.H, static_cast<int>(blockIdx.x));
-    while (__shfl_sync(0xffffffffu, step, 0) == kPlanFill) {
+    step = walk.begin(bars->plan.seqs, count, bars->plan.raw < args.n, bars->plan.total, bars->plan.ctas, args.H,
+                      static_cast<int>(blockIdx.x));
+    while (step == kPlanFill) {
       count = plan_fill<TileWalk>(args, &bars->plan);
-      if (lead) step = bars->walk.filled(count, bars->plan.raw < args.n);
+      step = walk.filled(count, bars->plan.raw < args.n);
     }
+    if (lead) bars->walk = walk;
+    __syncwarp();
   }
-  const bool some = __shfl_sync(0xffffffffu, step, 0) == kPlanUnit;
-  if (lead) bars->any = some ? 1 : 0;
-  if (some) publish_unit(bars, args, 0, cuts);
+  if (lead) bars->any = step == kPlanUnit ? 1 : 0;
+  if (step == kPlanUnit) publish_unit(bars, args, 0, cuts);
 }
 
 // Zeroes the rows of a landed value tile that are not live: weight 0 times a
