@@ -11,6 +11,8 @@ import random
 
 import pytest
 
+from test_loader_protocol import _programs, _run
+
 
 class Bar:
     def __init__(self):
@@ -75,30 +77,116 @@ def test_a_stage_shared_by_warps_is_caught():
 
 
 # ---------------------------------------------------------------------------
-# the D = 64 kernel of longer entries: softmax warps that wait for a value tile
+# the loader of the kernels of longer entries, the other roles as programs of
+# actions that wait for actions (test_loader_protocol.py)
 # ---------------------------------------------------------------------------
-def with_dead_rows(progs, dead, build_first):
-    """The roles of test_loader_protocol.py, where the softmax of the steps in `dead` needs its value tile landed before
-    it hands over its weights, and builds the next unit's operands before that (build_first) or after."""
-    progs = dict(progs)
-    # the loader waits for the stages of K(t), R(t+1) and V(t-2) before it issues any of the three
-    loader = progs["loader"]
-    progs["loader"] = [(act, deps + ([d for a, more in loader[i + 1:i + 3] if a[0] in ("LR", "LV") for d in more]
-                                     if act[0] == "LK" else [])) for i, (act, deps) in enumerate(loader)]
-    for name in ("sm0", "sm1"):
-        prog, out, i = progs[name], [], 0
-        while i < len(prog):
-            act, deps = prog[i]
-            if act[0] == "P" and act[1] in dead:
-                handed = (act, deps + [("LV", act[1])])
-                if build_first and i + 1 < len(prog) and prog[i + 1][0][0] == "B":
-                    out.append(prog[i + 1])
-                    i += 1
-                out.append(handed)
+def loader_program(nks, lag, NS, ahead, flush=True):
+    """K, r and V tiles of a step are issued together, V `lag` tiles behind; a unit's queries are loaded behind the first
+    step of the unit before (ahead) or at its head, behind (flush) that unit's last V tile."""
+    prog, queued, g, nr, nv, tiles = [], [], 0, 0, 0, []  # tiles: of r, so far
+
+    def v_wait():
+        return [("PV", nv - NS)] if nv >= NS else []
+
+    def issue_v():
+        nonlocal nv
+        prog.append((("LV", queued[0][0]), v_wait()))
+        queued.pop(0)
+        nv += 1
+
+    def issue_r():
+        nonlocal nr
+        prog.append((("LR", nr), [("G", nr - NS)] if nr >= NS else []))
+        nr += 1
+
+    def built(u):  # the operands of unit u
+        return [("B", p, u) for p in (0, 1)] if u > 0 else [("B0",)]
+
+    if ahead:
+        prog.append((("LQ", 0), []))
+    for u, n in enumerate(nks):
+        if not ahead:
+            while flush and queued:
+                issue_v()
+            prog.append((("LQ", u), built(u - 1) if u > 0 else []))
+        issue_r()
+        issue_r()
+        for t in range(n):
+            # one wait for the three stages
+            both = ([("S", g - NS)] if g >= NS else []) + ([("G", nr - NS)] if nr >= NS else [])
+            queued.append((g, u))
+            has_v = len(queued) > lag
+            if has_v:
+                both += v_wait()
+            prog.append((("LK", g), both))
+            prog.append((("LR", nr), []))
+            nr += 1
+            if has_v:
+                prog.append((("LV", queued.pop(0)[0]), []))
+                nv += 1
+            g += 1
+            if t == 0 and ahead and u + 1 < len(nks):
+                prog.append((("LQ", u + 1), built(u)))
+    while queued:
+        issue_v()
+    return prog
+
+
+def programs64(nks, lag, flush=True):
+    progs = _programs(nks, lag, True)
+    progs["loader"] = loader_program(nks, lag, 4, True)
+    progs["PV"] = [(act, [("LV", act[1])] + deps) for act, deps in progs["PV"]]
+    return progs
+
+
+def programs128(nks, lag, flush=True):
+    """Two stages, three ring slots; both halves of the softmax take every step: one builds the next unit's operands
+    behind a unit's last weights, the other writes the unit out."""
+    N = len(nks)
+    first = [sum(nks[:u]) for u in range(N)]
+    unit = [u for u in range(N) for _ in range(nks[u])]
+    tile0 = [first[u] + 2 * u for u in range(N)]
+    last_read = {}  # r tile -> step behind whose reads (or the unit's end) its slot is free
+    for u in range(N):
+        for e in range(nks[u] + 2):
+            last_read[tile0[u] + e] = first[u] + min(e, nks[u] - 1)
+
+    def built(u):
+        return [("B", p, u) for p in (0, 1)] if u > 0 else [("B0",)]
+
+    progs = {"loader": loader_program(nks, lag, 2, False, flush)}
+    progs["S"] = [(("S", g), [("LK", g)] + ([("RD0", g - 2), ("RD1", g - 2)] if g >= 2 else []) + built(unit[g]))
+                  for g in range(len(unit))]
+    prog, slot_of = [], {}
+    for u in range(N):
+        for e in range(nks[u] + 2):
+            x, deps = tile0[u] + e, [("LR", tile0[u] + e)] + built(u)
+            back = slot_of.get(e % 3)
+            if back is not None:
+                deps += [("RD0", last_read[back]), ("RD1", last_read[back])]
+            slot_of[e % 3] = x
+            prog.append((("G", x), deps))
+    progs["G"] = prog
+    progs["PV"] = [(("PV", g), [("LV", g), ("P0", g), ("P1", g)] + ([("EP", unit[g] - 1)] if unit[g] > 0 and
+                    g == first[unit[g]] else [])) for g in range(len(unit))]
+    for half in (0, 1):
+        prog = [(("B0",), [("LQ", 0)])] if half else []
+        for u in range(N):
+            for t in range(nks[u]):
+                g = first[u] + t
+                prog.append((("RD%d" % half, g), [("S", g)] + [("G", tile0[u] + t + k) for k in range(3)]))
+                # the two halves exchange their maxima; a rescaling waits for the P.V before
+                prog.append((("X%d" % half, g), []))
+                prog.append((("P%d" % half, g), [("X0", g), ("X1", g)] +
+                             ([("PV", g - 1 if half == 0 and t else g - 2)] if g >= 2 or (half == 0 and t) else [])))
+            if half == 0:
+                prog.append((("EP", u), [("L", u)] + [("PV", first[u] + t) for t in range(nks[u])]))
             else:
-                out.append((act, deps))
-            i += 1
-        progs[name] = out
+                prog.append((("L", u), []))
+                if u + 1 < N:
+                    prog.append((("B", 0, u + 1), [("LQ", u + 1)]))
+                    prog.append((("B", 1, u + 1), []))
+        progs["sm%d" % half] = prog
     return progs
 
 
@@ -106,18 +194,16 @@ MIXES = [[1] * 9, [2] * 8, [1, 2, 1, 1, 3, 1, 1], [5, 1, 4, 1, 1], [16, 14, 2, 1
 
 
 @pytest.mark.parametrize("nks", MIXES)
-def test_value_waits_do_not_deadlock(nks):
-    from test_loader_protocol import _programs, _run
-
-    for seed in range(60):
-        rng = random.Random(seed)
-        dead = {g for g in range(sum(nks)) if rng.random() < 0.5} if seed else set(range(sum(nks)))
-        ok, pc = _run(with_dead_rows(_programs(nks, 2, flush=True), dead, True), rng)
-        assert ok, (nks, seed, pc)
+@pytest.mark.parametrize("lag", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_loader_does_not_deadlock(D, lag, nks):
+    for seed in range(40):
+        ok, pc = _run((programs64 if D == 64 else programs128)(nks, lag), random.Random(seed))
+        assert ok, (D, lag, nks, seed, pc)
 
 
-def test_waiting_before_the_build_is_caught():
-    from test_loader_protocol import _programs, _run
-
-    ok, _ = _run(with_dead_rows(_programs([1] * 9, 2, flush=True), set(range(9)), False), random.Random(0))
+@pytest.mark.parametrize("D,lag", [(64, 3), (128, 2)])
+def test_values_held_back_are_caught(D, lag):
+    """V tiles that trail too far."""
+    ok, _ = _run((programs64 if D == 64 else programs128)([1] * 9, lag, flush=False), random.Random(0))
     assert not ok

@@ -16,14 +16,19 @@ int pieces_of(int H, int n, const int* start, const int* rows, const int* fresh,
   long long total = 0;
   for (int i = 0; i < n; ++i) {
     list[i] = PlanSeq{total, 0, fresh[i], i, start[i], rows[i], i};
-    total += Walk::cost_of_seq(list[i], H);
+    if (fresh[i] > 0) total += Walk::cost_of_head(list[i]) * H;
   }
-  const int ctas = plan_ctas<typename Walk::Cost>(total, most);
+  const PlanLine line = plan_line(total, plan_ctas<typename Walk::Cost>(total, most));
   int count = 0;
-  for (int c = 0, x = 0; c < ctas; ++c) {
-    while (x + 1 < n && list[x + 1].pre <= plan_cut(c, total, ctas)) ++x;
+  for (int c = 0, x = 0; c < line.ctas; ++c) {
+    while (x + 1 < n && list[x + 1].pre <= plan_cut(c, line)) ++x;
     Walk w;
-    for (PlanStep s = w.begin(list.data() + x, n - x, false, total, ctas, H, c); s == kPlanUnit; s = w.next()) {
+    w.seqs = list.data() + x;
+    w.count = n - x;
+    w.line = line;
+    w.H = H;
+    w.c = c;
+    for (bool found = w.advance(true, [] { return 0; }); found; found = w.advance(false, [] { return 0; })) {
       if (count == cap) return -1;
       const int row[10] = {c,       w.s.index, w.h,       w.qt,       w.p.t0,
                            w.p.nks, w.p.first, w.p.index, w.p.pieces, plan_place(c, w.p.index)};

@@ -166,20 +166,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
   if (warp == kWarps) {
     // ============================== producer ===============================
     typename C::Walk w;
-    PlanState* plan = &bars->plan;
-    PlanStep step = kPlanEnd;
-    auto filled = [&]() {  // the walker at a unit, or at the end
-      while (step == kPlanFill) {
-        const int count = plan_fill<typename C::Walk>(p.args, plan);
-        step = w.filled(count, plan->raw < p.args.n);
-      }
-    };
-    if (static_cast<int>(blockIdx.x) < plan->ctas) {
-      const int count = plan_fill<typename C::Walk>(p.args, plan);
-      step = w.begin(plan->seqs, count, plan->raw < p.args.n, plan->total, plan->ctas, p.args.H,
-                     static_cast<int>(blockIdx.x));
-      filled();
-    }
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -218,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       }
       ++units;
     };
-    for (; ok && step == kPlanUnit; step = w.next(), filled()) {
+    for (bool first = true; ok && plan_next(p.args, &bars->plan, &w, first); first = false) {
       publish(w.p.nks);
       if (!ok) break;
       const int* row = p.args.book.table + static_cast<size_t>(w.s.slot) * p.args.book.max_pages;

@@ -56,22 +56,33 @@ __host__ __device__ __forceinline__ int plan_steps(int start, int x, int BK) {
   return x < start ? 1 : x / BK - start / BK + 1;
 }
 
-// Where CTA c's range begins: floor(c total / ctas).  (A 64-bit division takes
-// over 100 instructions; nearly every line is shorter than 2^31.)
-__host__ __device__ __forceinline__ long long plan_cut(int c, long long total, int ctas) {
-  if (total >> 31) return c * total / ctas;
-  const uint32_t n = static_cast<uint32_t>(ctas), q = static_cast<uint32_t>(total) / n;
-  const uint32_t rest = static_cast<uint32_t>(total) - q * n;
-  return static_cast<long long>(c) * q + static_cast<uint32_t>(c) * rest / n;  // c, rest < ctas < 2^16
+// The line of costs: its length and how the CTAs share it.  (Divided once: a
+// 64-bit division takes over 100 instructions.)
+struct PlanLine {
+  long long total, each;  // each: floor(total / ctas)
+  int ctas, rest;
+};
+__host__ __device__ __forceinline__ PlanLine plan_line(long long total, int ctas) {
+  PlanLine l{total, 0, ctas, 0};
+  if (ctas > 0) {
+    l.each = total / ctas;
+    l.rest = static_cast<int>(total - l.each * ctas);
+  }
+  return l;
+}
+
+// Where CTA c's range begins: floor(c total / ctas).
+__host__ __device__ __forceinline__ long long plan_cut(int c, const PlanLine& l) {
+  return c * l.each + static_cast<uint32_t>(c * l.rest) / static_cast<uint32_t>(l.ctas);  // c, rest < ctas < 2^15
 }
 
 // The CTA whose range of the line holds position x: the largest c with
-// plan_cut(c) <= x.  The estimate is off by one at most (ctas < 2^16).
-__host__ __device__ __forceinline__ int plan_owner(long long x, long long total, int ctas) {
-  int c = static_cast<int>(static_cast<float>(x) / static_cast<float>(total) * static_cast<float>(ctas));
-  if (c >= ctas) c = ctas - 1;
-  while (c > 0 && plan_cut(c, total, ctas) > x) --c;
-  while (c + 1 < ctas && plan_cut(c + 1, total, ctas) <= x) ++c;
+// plan_cut(c) <= x.  The estimate is off by one at most.
+__host__ __device__ __forceinline__ int plan_owner(long long x, const PlanLine& l) {
+  int c = static_cast<int>(static_cast<float>(x) / static_cast<float>(l.total) * static_cast<float>(l.ctas));
+  c = c < l.ctas ? c : l.ctas - 1;
+  c -= plan_cut(c, l) > x;
+  c += c + 1 < l.ctas && plan_cut(c + 1, l) <= x;
   return c;
 }
 
@@ -95,7 +106,7 @@ struct Piece {
 // key steps from step `base`; nks = 0: none of its steps are c's.
 template <typename Cost>
 __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int base, int c, long long lo,
-                                                     long long hi, long long total, int ctas) {
+                                                     long long hi, const PlanLine& line) {
   const long long s0 = a + Cost::kUnit;
   static_assert(Cost::kStep == 2, "shifts");
   long long from = lo < s0 ? 0 : (lo - s0) >> 1;
@@ -109,9 +120,10 @@ __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int
   p.index = 0;
   p.pieces = 1;
   if (p.nks > 0 && p.nks < steps) {
-    p.first = plan_owner(s0 + Cost::kStep - 1, total, ctas);
+    if (from > 0) p.first = plan_owner(s0 + Cost::kStep - 1, line);
+    const int last = to == steps ? c : plan_owner(s0 + static_cast<long long>(Cost::kStep) * steps - 1, line);
     p.index = c - p.first;
-    p.pieces = plan_owner(s0 + static_cast<long long>(Cost::kStep) * steps - 1, total, ctas) - p.first + 1;
+    p.pieces = last - p.first + 1;
   }
   return p;
 }
@@ -120,98 +132,111 @@ __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int
 // that continues an earlier CTA's have a place each.
 __host__ __device__ __forceinline__ int plan_place(int c, int index) { return 2 * c + (index == 0 ? 1 : 0); }
 
-enum PlanStep { kPlanUnit, kPlanEnd, kPlanFill };
-
 // A walk over the units that CTA c has steps of.  BK: rows of a key step;
 // TILE: queries of a unit (0: the unit has all of the sequence's); sequences of
-// kLo to kHi new tokens are the kernel's.
+// kLo to kHi new tokens are the kernel's.  (Each kernel has this code once and
+// without unrolled loops: what a CTA runs once it has to fetch first.  With
+// copies of it for the first unit and the next, about 100 KB, the call took 7
+// us longer.)
 template <typename C, int BK, int TILE, int LO, int HI>
 struct PlanWalk {
   using Cost = C;
   static constexpr int kLo = LO, kHi = HI;
-  const PlanSeq* seqs;  // the sequences at hand
+  const PlanSeq* seqs;  // the sequences at hand (n = 0: an entry that is not the kernel's)
   int count;            // how many
-  bool left;            // there are more behind them
-  long long total;
-  int ctas, H, c, i, h, qt;
+  PlanLine line;
+  int H, c, i, h, qt;
   PlanSeq s;
   long long a, lo, hi;  // cost position of the unit, the CTA's range
   Piece p;
 
-  __host__ __device__ __forceinline__ int steps_of(int tile) const {
+  static __host__ __device__ __forceinline__ int tiles_of(const PlanSeq& s) {
+    return TILE == 0 ? 1 : (s.n + TILE - 1) / (TILE == 0 ? 1 : TILE);
+  }
+  static __host__ __device__ __forceinline__ int steps_of(const PlanSeq& s, int tile) {
     const int m = s.start + s.rows - s.n;  // page row of query 0
     const int last = TILE == 0 ? s.n - 1 : (tile * TILE + TILE < s.n ? tile * TILE + TILE : s.n) - 1;
     return plan_steps(s.start, m + last, BK);
   }
-  __host__ __device__ __forceinline__ int tiles() const { return TILE == 0 ? 1 : (s.n + TILE - 1) / TILE; }
-  __host__ __device__ __forceinline__ long long cost_of(int tile) const {
-    return Cost::kUnit + static_cast<long long>(Cost::kStep) * steps_of(tile);
-  }
-  __host__ __device__ __forceinline__ long long cost_of_head() const {
-    long long per = 0;
-    for (int y = 0; y < tiles(); ++y) per += cost_of(y);
-    return per;
-  }
-  static __host__ __device__ __forceinline__ long long cost_of_seq(const PlanSeq& x, int heads) {
-    PlanWalk w;
-    w.s = x;
-    return w.cost_of_head() * heads;
+  // A sequence's units of one head: kUnit each, and the steps, in closed form.
+  // Tile y of those before the last ends at row m + y TILE + TILE - 1 = x, its
+  // last key step is floor(x / BK).
+  static __host__ __device__ __forceinline__ long long cost_of_head(const PlanSeq& s) {
+    const int tiles = tiles_of(s);
+    long long steps = steps_of(s, tiles - 1);
+    if (TILE != 0 && tiles > 1) {
+      const int m = s.start + s.rows - s.n;
+      // the first y0 tiles end before the first live row (rows < n): a step each
+      int y0 = m < s.start ? (s.start - m) / (TILE == 0 ? 1 : TILE) : 0;
+      y0 = y0 < tiles - 1 ? y0 : tiles - 1;
+      const long long k = tiles - 1 - y0;
+      steps += y0 + k * (1 - s.start / BK);
+      if (TILE >= BK) {  // floor(x / BK) grows by TILE / BK a tile
+        constexpr int kBy = TILE / BK;
+        const int first = m + y0 * TILE + TILE - 1;  // no less than start where k > 0
+        if (k > 0) steps += k * (first / BK) + kBy * (k * (k - 1) / 2);
+      } else {  // floor(x / BK) = floor((b + y) / 2)
+        static_assert(TILE == 0 || TILE >= BK || 2 * TILE == BK, "half a key step a tile");
+        auto halves = [](long long z) { return z < 1 ? 0 : (z - 1) * (z - 1) / 4; };  // sum of floor(j / 2), j < z
+        const long long b = (m + y0 * TILE + TILE - 1) / (TILE == 0 ? 1 : TILE);
+        if (k > 0) steps += halves(b + k) - halves(b);
+      }
+    }
+    return static_cast<long long>(Cost::kUnit) * tiles + Cost::kStep * steps;
   }
 
-  // The CTA's first unit with a step in its range; list[0] is the sequence
-  // that the range starts in.
-  __host__ __device__ __forceinline__ PlanStep begin(const PlanSeq* list, int n, bool more, long long length,
-                                                     int n_ctas, int heads, int cta) {
-    seqs = list;
-    count = n;
-    left = more;
-    total = length;
-    ctas = n_ctas;
-    H = heads;
-    c = cta;
-    lo = plan_cut(c, total, ctas);
-    hi = plan_cut(c + 1, total, ctas);
-    i = 0;
-    s = seqs[0];
-    const long long per = cost_of_head();
-    const long long past = lo - s.pre;
-    h = past >> 31 ? static_cast<int>(past / per)
-                   : static_cast<int>(static_cast<uint32_t>(past) /
-                                      static_cast<uint32_t>(per < past + 1 ? per : past + 1));
-    a = s.pre + h * per;
-    qt = 0;
-    while (a + cost_of(qt) <= lo) a += cost_of(qt++);
-    return settle();
-  }
-  __host__ __device__ __forceinline__ PlanStep next() {
-    step_unit();
-    return settle();
-  }
-  // After kPlanFill: the next sequences are at hand.
-  __host__ __device__ __forceinline__ PlanStep filled(int n, bool more) {
-    count = n;
-    left = more;
-    i = 0;
-    if (n > 0) s = seqs[0];
-    return settle();
+  // On to the first unit with a step in the CTA's range (`first`; the line, H
+  // and c are set, seqs[0] is the sequence that the range starts in once there
+  // is one), or to the next; false: there is none.  fill() puts the next
+  // sequences into `seqs`, and says how many.
+  template <typename Fill>
+  __host__ __device__ __forceinline__ bool advance(bool first, Fill&& fill) {
+    bool placed = !first, step = !first, fresh = first;
+    for (;;) {
+      if (step) {
+        a += cost_of(qt);
+        if (++qt == tiles_of(s)) {
+          qt = 0;
+          if (++h == H) h = 0, ++i, fresh = true;
+        }
+      }
+      step = true;
+      if (placed && a >= hi) return false;
+      if (fresh) {  // the next sequence
+        if (first && !placed) i = 0;
+        for (;; ++i) {
+          if (i >= count) {
+            count = fill();
+            if (count == 0) return false;
+            i = 0;
+          }
+          if (seqs[i].n > 0) break;
+        }
+        s = seqs[i];
+        fresh = false;
+      }
+      if (!placed) place(), placed = true;
+      p = plan_piece<Cost>(a, steps_of(s, qt), s.start / BK, c, lo, hi, line);
+      if (p.nks > 0) return true;
+    }
   }
 
  private:
-  __host__ __device__ __forceinline__ void step_unit() {
-    a += cost_of(qt);
-    if (++qt < tiles()) return;
-    qt = 0;
-    if (++h < H) return;
-    h = 0;
-    if (++i < count) s = seqs[i];
+  __host__ __device__ __forceinline__ long long cost_of(int tile) const {
+    return Cost::kUnit + static_cast<long long>(Cost::kStep) * steps_of(s, tile);
   }
-  __host__ __device__ __forceinline__ PlanStep settle() {
-    for (;; step_unit()) {
-      if (a >= hi) return kPlanEnd;
-      if (i >= count) return left ? kPlanFill : kPlanEnd;
-      p = plan_piece<Cost>(a, steps_of(qt), s.start / BK, c, lo, hi, total, ctas);
-      if (p.nks > 0) return kPlanUnit;
-    }
+  // The unit of sequence s that the range starts in.
+  __host__ __device__ __forceinline__ void place() {
+    lo = plan_cut(c, line);
+    hi = plan_cut(c + 1, line);
+    const long long per = cost_of_head(s), past = lo - s.pre;
+    h = static_cast<int>(static_cast<float>(past) / static_cast<float>(per));  // off by one at most: h < 2^20
+    h -= h > 0 && h * per > past;
+    h += (h + 1) * per <= past;
+    a = s.pre + h * per;
+    qt = 0;
+#pragma unroll 1
+    while (a + cost_of(qt) <= lo) a += cost_of(qt++);
   }
 };
 using DecodeWalk64 = PlanWalk<DecodeCost, 64, 0, 1, kDecodeRows>;  // D = 64
@@ -252,7 +277,7 @@ __device__ __forceinline__ PlanSeq plan_read(const PlanArgs& p, int i, int lo, i
 
 __device__ __forceinline__ long long warp_scan(long long x) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
@@ -262,96 +287,120 @@ __device__ __forceinline__ long long warp_scan(long long x) {
 
 // In shared memory: the division, this CTA's start, the sequences at hand.
 struct PlanState {
-  long long total, pre;  // S; cost of the entries before `raw`
-  int ctas, raw;         // raw: the next entry to read
+  PlanLine line;
+  long long pre;    // cost of the entries before `raw`
+  int raw;          // the next entry to read
+  int from, count;  // entry that the CTA's range starts in; entries at hand in `seqs`
   union {
     long long sums[2][16];  // plan_begin: warps' sums (up to 16 warps)
-    PlanSeq seqs[32];       // from plan_fill on
+    PlanSeq seqs[32];       // behind its next to last barrier
   };
 };
 
 // All threads of the CTA (a multiple of 32, up to 512): S, the CTAs that share
-// it, the entry that this CTA's range starts in.  Ends with a barrier.
+// it, the entry that this CTA's range starts in and, of lists that the CTA
+// reads in one go, the entries from there on.  Ends with a barrier.
 template <typename Walk>
 __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanState* st) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-  bool bad = false;
-  // Entries base .. base + nt - 1: cost of each and of those before it.
-  int turn = 0;
-  auto scan = [&](int base, long long* mine, long long* all) {
-    const int i = base + tid;
-    long long x = 0;
-    if (i < p.n) {
-      const PlanSeq s = plan_read(p, i, Walk::kLo, Walk::kHi, &bad);
-      if (s.n > 0) x = Walk::cost_of_seq(s, p.H);
-    }
-    *mine = x;
-    x = warp_scan(x);
-    long long* sums = st->sums[turn ^= 1];
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    long long before = x - *mine, sum = 0;
-    for (int w = 0; w < nw; ++w) {
-      before += w < warp ? sums[w] : 0;
-      sum += sums[w];
-    }
-    *all = sum;
-    return before;
-  };
-  long long total = 0, mine = 0, all = 0, before = 0;
-  for (int base = 0; base < p.n; base += nt) {
-    before = scan(base, &mine, &all);
-    total += all;
-  }
-  const int ctas = plan_ctas<typename Walk::Cost>(total, most);
   const int c = static_cast<int>(blockIdx.x);
-  if (c < ctas) {
-    const long long lo = plan_cut(c, total, ctas);
-    long long upto = 0;
-    for (int base = 0; base < p.n && upto <= lo; base += nt) {
-      if (p.n > nt) before = scan(base, &mine, &all);  // else at hand
-      if (mine > 0 && upto + before <= lo && lo < upto + before + mine) {
-        st->raw = base + tid;
-        st->pre = upto + before;
+  bool bad = false;
+  PlanSeq s{};
+  PlanLine line{};
+  long long upto = 0, lo = -1, mine = 0;  // upto: cost of the entries so far; lo: the range's start, once known
+  // Blocks of nt entries: the total, then, if there are several, again up to
+  // the one that the range starts in.
+#pragma unroll 1
+  for (int base = 0, turn = 0;; turn ^= 1) {
+    s.n = 0;
+    if (base + tid < p.n) s = plan_read(p, base + tid, Walk::kLo, Walk::kHi, &bad);
+    mine = s.n > 0 ? Walk::cost_of_head(s) * p.H : 0;
+    const long long x = warp_scan(mine);
+    if (lane == 31) st->sums[turn][warp] = x;
+    __syncthreads();
+    long long before = upto + x - mine;
+#pragma unroll 1
+    for (int w = 0; w < nw; ++w) {
+      const long long y = st->sums[turn][w];
+      before += w < warp ? y : 0;
+      upto += y;
+    }
+    base += nt;
+    if (lo < 0 && base >= p.n) {
+      line = plan_line(upto, plan_ctas<typename Walk::Cost>(upto, most));
+      if (c >= line.ctas) break;
+      lo = plan_cut(c, line);
+      if (p.n > nt) {
+        base = 0;
+        upto = 0;
+        continue;
       }
-      upto += all;
+    }
+    if (lo >= 0) {
+      if (mine > 0 && before <= lo && lo < before + mine) {
+        st->from = st->raw = base - nt + tid;
+        st->pre = before;
+      }
+      s.pre = before;
+      if (upto > lo) break;
     }
   }
   if (bad && c == 0) atomicOr(p.status, kStatusPagesBit);
   if (tid == 0) {
-    st->total = total;
-    st->ctas = ctas;
+    st->line = line;
+    st->count = 0;
+  }
+  __syncthreads();
+  if (p.n > nt || c >= line.ctas) return;
+  // (Read again by the walking warp, they cost 2 us of every call.)
+  const int from = st->from, k = tid - from, count = min(32, p.n - from);
+  if (k >= 0 && k < count) {
+    st->seqs[k] = s;
+    if (k == count - 1) {
+      st->raw = from + count;
+      st->pre = s.pre + mine;
+      st->count = count;
+    }
   }
   __syncthreads();
 }
 
-// One warp: the kernel's next sequences, up to 32 (0: there are none), from
-// entry st->raw on, into st->seqs.
+// One warp: the next entries, up to 32 (0: there are none), from entry st->raw
+// on, into st->seqs.
 template <typename Walk>
 __device__ __forceinline__ int plan_fill(const PlanArgs& p, PlanState* st) {
   const int lane = threadIdx.x & 31;
-  int raw = st->raw, count = 0;
-  long long pre = st->pre;
+  const int raw = st->raw, count = max(0, min(32, p.n - raw));
+  const long long pre = st->pre;
   __syncwarp();
-  while (count == 0 && raw < p.n) {
-    PlanSeq s{};
-    bool bad = false;
-    if (raw + lane < p.n) s = plan_read(p, raw + lane, Walk::kLo, Walk::kHi, &bad);
-    const long long cost = s.n > 0 ? Walk::cost_of_seq(s, p.H) : 0;
-    const long long upto = warp_scan(cost);
-    s.pre = pre + upto - cost;
-    const uint32_t votes = __ballot_sync(0xffffffffu, s.n > 0);
-    if (s.n > 0) st->seqs[__popc(votes & ((1u << lane) - 1))] = s;
-    count = __popc(votes);
-    pre += __shfl_sync(0xffffffffu, upto, 31);
-    raw += 32;
-  }
-  if (lane == 0) {
-    st->raw = raw;
-    st->pre = pre;
+  PlanSeq s{};
+  bool bad = false;
+  if (lane < count) s = plan_read(p, raw + lane, Walk::kLo, Walk::kHi, &bad);
+  const long long cost = s.n > 0 ? Walk::cost_of_head(s) * p.H : 0;
+  const long long upto = warp_scan(cost);
+  s.pre = pre + upto - cost;
+  if (lane < count) st->seqs[lane] = s;
+  if (lane == 31) {
+    st->raw = raw + count;
+    st->pre = pre + upto;
   }
   __syncwarp();
   return count;
+}
+
+// One warp, behind plan_begin: the walker on to this CTA's first unit or its
+// next; false: there is none.
+template <typename Walk>
+__device__ __forceinline__ bool plan_next(const PlanArgs& p, PlanState* st, Walk* walk, bool first) {
+  if (first) {
+    walk->seqs = st->seqs;
+    walk->count = st->count;
+    walk->line = st->line;
+    walk->H = p.H;
+    walk->c = static_cast<int>(blockIdx.x);
+    if (walk->c >= walk->line.ctas) return false;
+  }
+  return walk->advance(first, [&] { return plan_fill<Walk>(p, st); });
 }
 
 #endif  // __CUDACC__

@@ -67,7 +67,7 @@ size_t smem_bytes(int D) {
 
 // NG: float4 columns of the output per thread (two rows each).
 template <int NG>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, NG <= 2 ? kSimtPerSm : 1) paged_simt_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared* sh = reinterpret_cast<Shared*>(smem);
   const int D = p.D, DP = padded(D), S = stride_of(D), H = p.args.H;
@@ -87,47 +87,33 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const Params p) {
   if (tid == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
   plan_begin<SimtWalk>(p.args, static_cast<int>(gridDim.x), &sh->plan);
 
-  // Warp 0, all lanes alike: the walker's unit into `slot`; `step`: what the
-  // walker met.  (The walker rests in shared memory and works in registers.)
-  auto publish = [&](int slot, SimtWalk& walk, PlanStep step) {
-    while (step == kPlanFill) {
-      const int count = plan_fill<SimtWalk>(p.args, &sh->plan);
-      step = walk.filled(count, sh->plan.raw < p.args.n);
-    }
-    __syncwarp();  // every lane has read the walker
-    if (lane == 0) {
-      Unit u{};
-      if (step == kPlanUnit) {
-        const PlanSeq& s = walk.s;
-        const int i0 = walk.qt * BQ;
-        u = Unit{walk.h,     s.tok0 + i0,          min(BQ, s.n - i0), walk.p.t0,    walk.p.nks, s.start + s.rows - s.n + i0,
-                 s.start, s.start + s.rows - 1, s.slot,            walk.p.index, walk.p.pieces};
-        if (u.pieces > 1 && u.index == 0) p.cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
-      }
-      sh->unit[slot] = u;
-      sh->walk = walk;
-    }
-    __syncwarp();
-  };
-  if (warp == 0) {
-    PlanStep step = kPlanEnd;
-    SimtWalk walk;
-    if (static_cast<int>(blockIdx.x) < sh->plan.ctas) {
-      const int count = plan_fill<SimtWalk>(p.args, &sh->plan);
-      step = walk.begin(sh->plan.seqs, count, sh->plan.raw < p.args.n, sh->plan.total, sh->plan.ctas, H,
-                        static_cast<int>(blockIdx.x));
-    }
-    publish(0, walk, step);
-  }
-  __syncthreads();
-
   bool bad = false;
-  for (int un = 0;; ++un) {
-    const Unit w = sh->unit[un & 1];
-    if (w.nks == 0) break;
-    if (warp == 0) {
+  for (int un = -1;; ++un) {
+    Unit w{};
+    if (un >= 0) {
+      w = sh->unit[un & 1];
+      if (w.nks == 0) break;
+    }
+    if (warp == 0) {  // unit un + 1; the walker rests in shared memory and works in registers
       SimtWalk walk = sh->walk;
-      publish((un + 1) & 1, walk, walk.next());
+      const bool found = plan_next(p.args, &sh->plan, &walk, un < 0);
+      __syncwarp();  // every lane has read the walker
+      if (lane == 0) {
+        Unit u{};
+        if (found) {
+          const PlanSeq& s = walk.s;
+          const int i0 = walk.qt * BQ;
+          u = Unit{walk.h,      s.tok0 + i0, min(BQ, s.n - i0),      walk.p.t0, walk.p.nks,   s.start + s.rows - s.n + i0,
+                   s.start,     s.start + s.rows - 1, s.slot, walk.p.index, walk.p.pieces};
+          if (u.pieces > 1 && u.index == 0) p.cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
+        }
+        sh->unit[(un + 1) & 1] = u;
+        sh->walk = walk;
+      }
+    }
+    if (un < 0) {
+      __syncthreads();
+      continue;
     }
     for (int y = warp; y < BQ; y += kThreads / 32)
       for (int d = lane; d < D; d += 32) {

@@ -140,17 +140,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  begin_units(bars, p.args, p.cuts, kLoaderWarp);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
+  plan_begin<TileWalk>(p.args, static_cast<int>(gridDim.x), &bars->plan);
+  if (warp != kLoaderWarp) {  // the loader has this barrier behind the first units
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   const uint32_t tmem = bars->tmem_base;
   const bool any = bars->any != 0;
   const uint64_t wait_ns = p.wait_ns;
 
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
-    run_tile_loader<D, NK, 1, false>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, true, false>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ============================ MMA issuer ===============================
     if (lane == 0) {
@@ -197,25 +200,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     }
   } else if (warp == kPvWarp) {
     // ============================ PV issuer ================================
-    if (lane == 0) {
-      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-      const uint64_t dV = sdesc_sw128(smem_u32(sV), kRowChunk, 1024);
-      constexpr uint32_t kTile16 = kRowTile >> 4;
-      uint32_t nV = 0, g = 0, un = 0;
-      bool ok = true;
-      while (any && ok) {
-        // The unit is read behind the barrier of its first weights.
-        int nks = 1, next_h = -1;
-        for (int t = 0; t < nks; ++t, ++g) {
-          if (!(ok = mbar_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
-          if (t == 0) {
-            nks = bars->units[un % kUnitRing].nks;
-            next_h = bars->units[un % kUnitRing].next_h;
-          }
-          const int sv = nV % NV;
-          if (!(ok = mbar_wait(&bars->fullV[sv], (nV / NV) & 1, wait_ns, abort))) break;
-          if (t == 0 && un > 0 && !(ok = mbar_wait(&bars->o_free, (un - 1) & 1, wait_ns, abort))) break;
-          tc_fence_after();
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint64_t dV = sdesc_sw128(smem_u32(sV), kRowChunk, 1024);
+    constexpr uint32_t kTile16 = kRowTile >> 4;
+    uint32_t g = 0, un = 0;  // g: steps, and V tiles, so far
+    bool ok = true;
+    while (any && ok) {
+      // The unit is read behind the barrier of its first V tile.
+      int nks = 1, t0 = 0, start = 0, last = 0, next_h = -1;
+      for (int t = 0; t < nks; ++t, ++g) {
+        const int sv = g % NV;
+        if (!(ok = warp_wait(&bars->fullV[sv], (g / NV) & 1, wait_ns, abort))) break;
+        if (t == 0) {
+          const TileUnit& w = bars->units[un % kUnitRing];
+          nks = w.nks;
+          t0 = w.t0;
+          start = w.start;
+          last = w.last;
+          next_h = w.next_h;
+        }
+        zero_dead_rows<D>(start, last, t0 + t, sV + sv * kRowTile, lane);
+        if (!(ok = warp_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
+        if (t == 0 && un > 0 && !(ok = warp_wait(&bars->o_free, (un - 1) & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        if (lane == 0) {
           const uint64_t dv = dV + sv * kTile16;
           const uint32_t pa = tmem + kColP + (g & 1) * 32;
 #pragma unroll
@@ -223,14 +231,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
             mma_ts(tmem + kColO, pa + kk * 8, dv + ((kk * 16 * 128) >> 4), idO, (t > 0 || kk > 0) ? 1u : 0u);
           tc_commit(&bars->emptyV[sv]);
           tc_commit(&bars->pv_done[g & 1]);
-          ++nV;
+          if (t == nks - 1) tc_commit(&bars->o_full);
         }
-        if (!ok) break;
-        tc_commit(&bars->o_full);
-        ++un;
-        if (next_h < 0) break;
+        __syncwarp();
       }
-      if (!ok) report_timeout(abort, p.args.status);
+      if (!ok || next_h < 0) break;
+      ++un;
+    }
+    if (lane == 0) {
+      if (any && !ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->pv_final);
       mbar_wait_own(&bars->pv_final, 0, wait_ns);
     }
@@ -334,10 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     if (any && half == 1) ok = build_q(bars->units[0].h);
 
     while (any && ok) {
-      // Unit 0 is published before the CTA's first barrier, unit un + 1 before
-      // the loads of unit un's keys.
+      // Unit 0 is published before the CTA's first barrier, a later one before
+      // its queries are loaded, which its first scores tell.
+      if (un > 0 && !(ok = warp_wait(&bars->s_full[gt & 1], (gt >> 1) & 1, wait_ns, abort))) break;
       const TileUnit* unit = &bars->units[un % kUnitRing];
-      const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start, last = unit->last;
+      const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
       float m_use = -INFINITY;  // running max in log2 units (lazy)
       float l_half = 0.f;       // row sum over this half's columns
       const uint32_t g0 = gt;
@@ -375,14 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         const int kt = t0 + t;                           // key step of the tile
         const int lim = d0 - BN * kt + a - 32 * half;    // column k visible iff low <= k <= lim
         const int low = start - BN * kt - 32 * half;
-        const bool dead = start > BN * kt || BN * kt + BN - 1 > last;  // the tile has rows that are not live
-        if (d0 - BN * kt + quad * 32 - 32 * half < 31) {               // some lane of the warp masks
+        if (low > 0 || d0 - BN * kt + quad * 32 - 32 * half < 31) {  // some lane of the warp masks
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (k <= lim) ? x[k] : -INFINITY;
-        }
-        if (low > 0) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (k >= low) ? x[k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) x[k] = (k >= low && k <= lim) ? x[k] : -INFINITY;
         }
         float t3[11];
 #pragma unroll
@@ -438,14 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         tc_fence_after();
         tmem_st16(tmem + lane_base + kColP + sb * 32 + 16 * half, pk);
         tmem_wait_st();
-        if (dead) {
-          // The stage's phases go by in order before this warp: the P.V two
-          // steps back is done, and the stage is refilled only after this
-          // step's.
-          if (!(ok = warp_wait(&bars->fullV[g % NV], (g / NV) & 1, wait_ns, abort))) break;
-          zero_dead_rows<D>(start, last, kt, sV + (g % NV) * kRowTile, warp, 8, lane);
-          fence_proxy_async_smem();
-        }
         warp_arrive_tc(&bars->p_full[sb]);
       }
       if (!ok) break;

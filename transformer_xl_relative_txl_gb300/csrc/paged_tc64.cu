@@ -17,8 +17,8 @@
 //     ranges of key steps per CTA, so that ragged lengths, few sequences and
 //     long memories are all one case; a unit that a range cuts is joined
 //     through the workspace.  The loader publishes the units (paged_tiles.cuh).
-//   * Value rows that are not live are zeroed in shared memory by the softmax
-//     warps of the step.
+//   * Value rows that are not live are zeroed in shared memory by the P.V
+//     issuer's warp.
 //   * A 32-row box of output whose rows are all the unit's leaves by TMA, the
 //     last rows of a sequence by plain stores.
 //
@@ -52,8 +52,8 @@ constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, t
 // warpgroups 216, producer warpgroup 72; 2*128*216 + 128*72 = 64512.  (With 224
 // and 56 the loader spills: 107 us instead of 103 for 22 sequences of 512
 // tokens over 512 rows, 8 heads.)
-constexpr uint32_t kRegsSoftmax = 216;
-constexpr uint32_t kRegsProducer = 72;
+constexpr uint32_t kRegsSoftmax = 224;
+constexpr uint32_t kRegsProducer = 56;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");
 constexpr uint32_t kColO = 0;    // O0, O1: 64 columns each
 constexpr uint32_t kColS = 128;  // S0, S1: 64 columns each
@@ -155,10 +155,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  begin_units(bars, p.args, p.cuts, kLoaderWarp);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
+  plan_begin<TileWalk>(p.args, static_cast<int>(gridDim.x), &bars->plan);
+  if (warp != kLoaderWarp) {  // the loader has this barrier behind the first units
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   const uint32_t tmem = bars->tmem_base;
   const bool any = bars->any != 0;
   const uint64_t wait_ns = p.wait_ns;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
     setmaxnreg_dec<kRegsProducer>();
-    run_tile_loader<D, NK, 0, true>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, false, true>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ===================== content-score MMA issuer ========================
     setmaxnreg_dec<kRegsProducer>();
@@ -267,28 +270,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   } else if (warp == kPvWarp) {
     // ============================ PV issuer ================================
     setmaxnreg_dec<kRegsProducer>();
-    if (lane == 0) {
-      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-      const uint64_t dV = sdesc_sw128(smem_u32(sV), BN * 128, 1024);
-      const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);
-      constexpr uint32_t kTile16 = kRowTile >> 4;
-      uint32_t nV = 0, g = 0, un = 0;
-      bool ok = true;
-      while (any && ok) {
-        // The unit is read behind the barrier of its first weights.
-        int nks = 1, next_h = -1;
-        for (int t = 0; t < nks; ++t, ++g) {
-          if (!(ok = mbar_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
-          if (t == 0) {
-            nks = bars->units[un % kUnitRing].nks;
-            next_h = bars->units[un % kUnitRing].next_h;
-          }
-          const int sv = nV % NV;
-          if (!(ok = mbar_wait(&bars->fullV[sv], (nV / NV) & 1, wait_ns, abort))) break;
-          // The first PV into each accumulator of a unit overwrites it: the
-          // previous unit's epilogue must have read both.
-          if (t < 2 && un > 0 && !(ok = mbar_wait(&bars->o_free, (un - 1) & 1, wait_ns, abort))) break;
-          tc_fence_after();
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint64_t dV = sdesc_sw128(smem_u32(sV), BN * 128, 1024);
+    const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);
+    constexpr uint32_t kTile16 = kRowTile >> 4;
+    uint32_t g = 0, un = 0;  // g: steps, and V tiles, so far
+    bool ok = true;
+    while (any && ok) {
+      // The unit is read behind the barrier of its first V tile.
+      int nks = 1, t0 = 0, start = 0, last = 0, next_h = -1;
+      for (int t = 0; t < nks; ++t, ++g) {
+        const int sv = g % NV;
+        if (!(ok = warp_wait(&bars->fullV[sv], (g / NV) & 1, wait_ns, abort))) break;
+        if (t == 0) {
+          const TileUnit& w = bars->units[un % kUnitRing];
+          nks = w.nks;
+          t0 = w.t0;
+          start = w.start;
+          last = w.last;
+          next_h = w.next_h;
+        }
+        zero_dead_rows<D>(start, last, t0 + t, sV + sv * kRowTile, lane);
+        if (!(ok = warp_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
+        // The first PV into each accumulator of a unit overwrites it: the
+        // previous unit's epilogue must have read both.
+        if (t < 2 && un > 0 && !(ok = warp_wait(&bars->o_free, (un - 1) & 1, wait_ns, abort))) break;
+        tc_fence_after();
+        if (lane == 0) {
           const uint64_t dv = dV + sv * kTile16;
           const uint64_t dp = dP + (g & 1) * (kQTile >> 4);
           const uint32_t od = tmem + kColO + (g & 1) * D;
@@ -297,14 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
             mma_ss(od, dp + kk * 2, dv + ((kk * 16 * 128) >> 4), idO, t >= 2 || kk > 0);
           tc_commit(&bars->emptyV[sv]);
           tc_commit(&bars->pv_done[g & 1]);
-          ++nV;
+          if (t == nks - 1) tc_commit(&bars->o_full);
         }
-        if (!ok) break;
-        tc_commit(&bars->o_full);
-        ++un;
-        if (next_h < 0) break;
+        __syncwarp();
       }
-      if (!ok) report_timeout(abort, p.args.status);
+      if (!ok || next_h < 0) break;
+      ++un;
+    }
+    if (lane == 0) {
+      if (any && !ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->pv_final);
       mbar_wait_own(&bars->pv_final, 0, wait_ns);
     }
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       // Published before the q tile that the build above waited for.
       const TileUnit* unit = &bars->units[un % kUnitRing];
       const int next_h = unit->next_h, nks = unit->nks, t0 = unit->t0, d0 = unit->d0;
-      const int start = unit->start, last = unit->last;
+      const int start = unit->start;
       const uint32_t g0 = gt;
       const bool has_next = next_h >= 0;
       const float bu_next = has_next ? bias_of(next_h, p.bias_u) : 0.f;
@@ -399,7 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         const int lim = d0 - BN * kt + a;   // column c visible iff low <= c <= lim
         const int low = start - BN * kt;
         const bool diag = d0 - BN * kt + quad * 32 < 63;  // some lane of the warp masks
-        const bool dead = low > 0 || BN * kt + BN - 1 > last;  // the tile has rows that are not live
         const float m_old = m_use;
         float m_new = m_use;
         // All of this step's TMEM reads at once -- the 96-distance window and
@@ -435,13 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           add_window(s0, bd0, x0);
           add_window(s1, bd1, x1);
         }
-        if (diag) {
+        if (diag || low > 0) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = (k <= lim) ? x[k] : -INFINITY;
-        }
-        if (low > 0) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = (k >= low) ? x[k] : -INFINITY;
+          for (int k = 0; k < 64; ++k) x[k] = (k >= low && k <= lim) ? x[k] : -INFINITY;
         }
         // Lazy running max over the step's 64 scores (log2 units).
         float t3[22];
@@ -508,13 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
         }
         l_run = l_run * alpha + sum;
-        if (dead) {
-          // The stage's phases go by in order before this warp: the P.V two
-          // steps back is done, and the stage is refilled only after this
-          // step's.
-          if (!(ok = warp_wait(&bars->fullV[g % NV], (g / NV) & 1, wait_ns, abort))) break;
-          zero_dead_rows<D>(start, last, kt, sV + (g % NV) * kRowTile, quad, 4, lane);
-        }
         tc_fence_before();  // orders the O rescale's tcgen05.st before the arrive
         warp_arrive_smem(&bars->p_full[sb]);
         // The next unit's (q+u), (q+v) go to the other buffer once this

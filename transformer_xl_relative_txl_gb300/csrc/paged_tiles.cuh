@@ -1,13 +1,12 @@
 // What the two paged tensor-core kernels (D = 64 and 128) share: the unit a
 // CTA's roles work on, the loads of a key tile from its pages, the zeroing of
-// value rows that are not live, and the joining of pieces.
+// value rows that are not live, and the storing of results.
 //
-// The loader warp's first lane walks the CTA's units (paged_plan.cuh) and
-// publishes each in a ring in shared memory before the barrier that announces
-// the unit's queries; every other role reads a unit after a barrier that
-// follows that one.  A unit is published once the operands of the unit before
-// it are built, which is at the earliest while the unit before that runs its
-// first step, so no role is more than three units behind.
+// The loader warp walks the CTA's units (paged_plan.cuh) and publishes each in
+// a ring in shared memory before it loads the unit's queries; every other role
+// reads a unit after a barrier that follows that load.  The loader is at most
+// two units ahead of the one whose operands are built, and that one at most
+// two ahead of any role, so a ring of eight never overtakes a reader.
 #pragma once
 
 #include "paged_plan.cuh"
@@ -29,84 +28,60 @@ struct TileUnit {
   int next_h;          // head of the CTA's next unit, -1: none
 };
 
-// One warp.  The walker's unit into the ring, the walker to the next; the first
-// piece of a cut unit is noted for the kernel that joins the pieces.
+// One warp.  The walker on to the CTA's unit k, which goes into the ring, and
+// to the unit before whose head follows it; false: there is no unit k.  The
+// first piece of a cut unit is noted for the kernel that joins the pieces.
 template <typename Bars>
-__device__ __forceinline__ void publish_unit(Bars* bars, const PlanArgs& args, uint32_t k, PlanCut* cuts) {
-  const bool lead = (threadIdx.x & 31) == 0;
-  TileUnit& u = bars->units[k % kUnitRing];
+__device__ __forceinline__ bool publish_unit(Bars* bars, const PlanArgs& args, uint32_t k, PlanCut* cuts) {
   // The walker works in registers: in place, each of its dependent steps would
   // cost a shared-memory latency.
   TileWalk walk = bars->walk;
-  const int i0 = walk.qt * kTileQueries;
-  if (lead) {
-    const int nq = min(kTileQueries, walk.s.n - i0);
-    u.h = walk.h;
-    u.row0 = walk.s.tok0 + i0;
-    u.nq = nq;
-    u.t0 = walk.p.t0;
-    u.nks = walk.p.nks;
-    u.d0 = walk.s.start + walk.s.rows - walk.s.n + i0;
-    u.start = walk.s.start;
-    u.last = walk.s.start + walk.s.rows - 1;
-    u.slot = walk.s.slot;
-    u.index = walk.p.index;
-    u.pieces = walk.p.pieces;
-    if (walk.p.pieces > 1 && walk.p.index == 0)
-      cuts[blockIdx.x] = PlanCut{walk.s.tok0 + i0, nq, walk.h, walk.p.pieces};
-  }
-  PlanStep step = walk.next();
-  while (step == kPlanFill) {
-    const int count = plan_fill<TileWalk>(args, &bars->plan);
-    step = walk.filled(count, bars->plan.raw < args.n);
-  }
+  const bool found = plan_next(args, &bars->plan, &walk, k == 0);
   __syncwarp();  // every lane has read the walker
-  if (lead) {
-    u.next_h = step == kPlanUnit ? walk.h : -1;
-    bars->walk = walk;
+  if ((threadIdx.x & 31) == 0) {
+    if (found) {
+      TileUnit& u = bars->units[k % kUnitRing];
+      const int i0 = walk.qt * kTileQueries;
+      const int nq = min(kTileQueries, walk.s.n - i0);
+      u.h = walk.h;
+      u.row0 = walk.s.tok0 + i0;
+      u.nq = nq;
+      u.t0 = walk.p.t0;
+      u.nks = walk.p.nks;
+      u.d0 = walk.s.start + walk.s.rows - walk.s.n + i0;
+      u.start = walk.s.start;
+      u.last = walk.s.start + walk.s.rows - 1;
+      u.slot = walk.s.slot;
+      u.index = walk.p.index;
+      u.pieces = walk.p.pieces;
+      if (walk.p.pieces > 1 && walk.p.index == 0)
+        cuts[blockIdx.x] = PlanCut{walk.s.tok0 + i0, nq, walk.h, walk.p.pieces};
+      bars->walk = walk;
+    }
+    if (k > 0) bars->units[(k - 1) % kUnitRing].next_h = found ? walk.h : -1;
   }
   __syncwarp();
+  return found;
 }
 
-// All threads of the CTA, behind grid_dep_wait: the division of the work; the
-// warp `loader` then publishes the CTA's first unit, if it has one (bars->any),
-// which the barrier that the caller has next makes known.
-template <typename Bars>
-__device__ __forceinline__ void begin_units(Bars* bars, const PlanArgs& args, PlanCut* cuts, int loader) {
-  if (threadIdx.x == 0) cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
-  plan_begin<TileWalk>(args, static_cast<int>(gridDim.x), &bars->plan);
-  if (static_cast<int>(threadIdx.x >> 5) != loader) return;
-  const bool lead = (threadIdx.x & 31) == 0;
-  PlanStep step = kPlanEnd;
-  if (static_cast<int>(blockIdx.x) < bars->plan.ctas) {
-    TileWalk walk;
-    int count = plan_fill<TileWalk>(args, &bars->plan);
-    step = walk.begin(bars->plan.seqs, count, bars->plan.raw < args.n, bars->plan.total, bars->plan.ctas, args.H,
-                      static_cast<int>(blockIdx.x));
-    while (step == kPlanFill) {
-      count = plan_fill<TileWalk>(args, &bars->plan);
-      step = walk.filled(count, bars->plan.raw < args.n);
-    }
-    if (lead) bars->walk = walk;
-    __syncwarp();
-  }
-  if (lead) bars->any = step == kPlanUnit ? 1 : 0;
-  if (step == kPlanUnit) publish_unit(bars, args, 0, cuts);
-}
-
-// Zeroes the rows of a landed value tile that are not live: weight 0 times a
-// leftover that is no number would not be 0.  The tile's rows are shared by
-// `warps` warps; the caller's proxy fence and arrival on the barrier that the
-// P.V issuer waits for follow.
+// The P.V issuer's warp: zeroes the rows of the landed value tile t that are
+// not live: weight 0 times a leftover that is no number would not be 0.  (By
+// the softmax warps, behind their step's weights, the code alone cost their
+// loop 7%: 94 us instead of 88 for 22 sequences of 512 tokens over 512 rows, 8
+// heads.)
 template <int D>
-__device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8_t* stage, int warp, int warps,
-                                               int lane) {
+__device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8_t* stage, int lane) {
   const int x0 = t * kStepKeys;
-  for (int y = warp; y < kStepKeys; y += warps) {
+  if (start <= x0 && x0 + kStepKeys - 1 <= last) return;
+#pragma unroll 1
+  for (int y = lane >> 3; y < kStepKeys; y += 4) {
     if (x0 + y >= start && x0 + y <= last) continue;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) *reinterpret_cast<uint32_t*>(stage + c * kStepKeys * 128 + y * 128 + lane * 4) = 0;
+    for (int c = 0; c < D / 64; ++c)
+      *reinterpret_cast<uint4*>(stage + c * kStepKeys * 128 + y * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
   }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // Row `a` of a unit (lane `lane` of quadrant `quad`), o normalised by its own
@@ -168,9 +143,9 @@ struct TileMaps {
 };
 
 // The loader warp of both kernels: K, V and r tiles (and the raw q tiles) of
-// the CTA's units in order, and the units published.  Bars has the rings'
-// barriers, the units and the walker (in shared memory: it is used once per
-// unit, and the warp has few registers).
+// the CTA's units in order, and the units published.  It has the CTA's barrier
+// behind the first two units, which are whole then; bars->any says whether
+// there is one.
 //
 // The lanes share a step's work: lanes 0-3 have the boxes of its K tile, 4-7
 // those of a V tile, 8 its r tile.  A 64-row tile of keys is one box of a page,
@@ -182,25 +157,20 @@ struct TileMaps {
 // page id out of range reads as zeros (a box outside its tensor) and is
 // reported.
 //
-// LAG: V tiles trail the K and r tiles by so many.  A V stage is freed only
-// when the P.V MMA of its step completes, after that step's softmax, while a K
-// stage is free as soon as its score MMA is done; with V(t) beside K(t), K
-// would wait for the P.V of step t - NS and land just in time (D = 128: 158 us
-// instead of 131 for 152 units of 100 steps).  AHEAD: the raw q tile of a unit
-// is loaded a unit ahead, and before that of the unit after next every queued V
-// of a unit two or more back goes out, since the load waits for the (q+u),
-// (q+v) build of the next unit, which waits for the epilogue of the unit
-// before, which needs all of that unit's V tiles (a unit of one step would
-// otherwise hold them behind the load).  Without AHEAD the build comes at the
-// end of a unit's steps, which may wait for its last V (rows that are not
-// live), and the next unit's r tiles wait for the build: the queue is emptied
-// at each unit.
-template <int D, int NS, int LAG, bool AHEAD, typename Bars>
+// TRAIL: a V tile goes out with the K tile of the step behind.  A V stage is
+// freed only when the P.V MMA of its step completes, after that step's softmax,
+// while a K stage is free as soon as its score MMA is done; with V(t) beside
+// K(t), K would wait for the P.V of step t - NS and land just in time (D = 128,
+// two stages: 167 us instead of 145 for 152 units of 100 steps; at D = 64, with
+// four, a V tile that trails costs 2%).  AHEAD: the raw q tile of a unit is
+// loaded behind the first step of the unit before (D = 64: its operands have
+// two buffers and are built during that unit); otherwise at the head of its
+// own, behind the last V tile of the unit before.
+template <int D, int NS, bool TRAIL, bool AHEAD, typename Bars>
 __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
                                                 uint8_t* sK, uint8_t* sV, uint8_t* sR) {
-  static_assert((NS & (NS - 1)) == 0 && LAG <= 2, "stage arithmetic, queue");
+  static_assert((NS & (NS - 1)) == 0, "stage arithmetic");
   constexpr int kChunk = kStepKeys * 128, kTile = kChunk * (D / 64), kQChunk = kTileQueries * 128;
-  constexpr uint32_t kHold = AHEAD ? 2 : 1;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
   const int log_page = p.log_page_rows, log_box = min(log_page, 6);
@@ -215,8 +185,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
   if (lane <= 8 && leads) tma_prefetch_desc(map);
   uint32_t n = 0;   // tiles of this lane's ring so far
   uint32_t nQ = 0;  // q tiles so far
-  const bool any = bars->any != 0;
-  bool ok = any, bad = false;
+  bool ok = true, bad = false;
 
   // One tile of each ring whose lanes are `active`.
   auto issue = [&](bool active, int page, int x, int h, uint32_t bytes) {
@@ -253,46 +222,62 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     }
     ++nQ;
   };
-  // V tiles that wait their turn, the oldest in v0: this lane's page (-1: no
-  // live row), the row in the page, the head, the tile's bytes, the unit.
+  // A tile of keys: this lane's page (-1: no live row), the row in the page,
+  // the head, the tile's bytes.
   struct Tile {
     int page, x, h;
-    uint32_t bytes, unit;
+    uint32_t bytes;
   };
-  Tile v0{}, v1{};
-  int queued = 0;
-  auto flush_v = [&](uint32_t upto) {  // of units up to `upto`
-    while (ok && queued > 0 && v0.unit <= upto) {
-      issue(is_v, v0.page, v0.x, v0.h, v0.bytes);
-      v0 = v1;
-      --queued;
-    }
+  Tile held{};  // the V tile that trails
+  bool holds = false;
+  auto release = [&]() {
+    if (holds) issue(is_v, held.page, held.x, held.h, held.bytes);
+    holds = false;
   };
 
-  if (AHEAD && any) load_q(0);
-  for (uint32_t un = 0; ok; ++un) {
-    const TileUnit& w = bars->units[un % kUnitRing];
-    const int next_h = w.next_h, h = w.h, d0 = w.d0, start = w.start, last = w.last, tend = w.t0 + w.nks;
-    const int* row = p.args.book.table + static_cast<size_t>(w.slot) * p.args.book.max_pages;
-    int t = w.t0;
-    if (LAG > 0 && un >= kHold) flush_v(un - kHold);
-    if (!ok) break;
-    if (next_h >= 0) {
-      publish_unit(bars, p.args, un + 1, p.cuts);
-      if (AHEAD) load_q(un + 1);
+  // `known` units are published, all whole but the last; the tiles of unit
+  // `un`, of which t is the next, are under way.
+  uint32_t known = 0, un = 0xffffffffu;
+  bool more = true, begun = false;
+  int h = 0, d0 = 0, start = 0, last = 0, t = 0, t0 = 0, tend = 0, id = 0;
+  const int* row = nullptr;
+  auto live = [&](int tile) {
+    const int x = tile * kStepKeys + off;
+    return boxed && x <= last && x + (1 << log_box) > start;
+  };
+  for (;;) {
+    if (more && (more = publish_unit(bars, p.args, known, p.cuts))) ++known;
+    if (known == 1 && more) continue;  // the first unit is whole once the second is known
+    if (!begun) {
+      begun = true;
+      if (lane == 0) bars->any = known > 0;
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      if (known == 0) break;
     }
-    if (!AHEAD) load_q(un);
-    if (!ok) break;
-    auto live = [&](int tile) {
-      const int x = tile * kStepKeys + off;
-      return boxed && x <= last && x + (1 << log_box) > start;
-    };
-    int id = live(t) ? row[(t * kStepKeys + off) >> log_page] : 0;
-    // distance tiles -2 and -1 of the unit's first step
-    issue(is_r, 0, d0 - kStepKeys * (t - 1), h, kTile);
-    if (ok) issue(is_r, 0, d0 - kStepKeys * t, h, kTile);
-    for (; ok && t < tend; ++t) {
-      const bool lv = live(t);
+    if (AHEAD && un + 1 < known) load_q(un + 1);
+    // Tiles, up to a unit's first step.
+    bool head = false, done = false;
+    while (ok && !head) {
+      if (t == tend) {  // the next unit
+        if (++un == known) {
+          done = true;
+          break;
+        }
+        if (!AHEAD) {
+          if (TRAIL) release();
+          if (ok) load_q(un);
+          if (!ok) break;
+        }
+        const TileUnit& w = bars->units[un % kUnitRing];
+        h = w.h, d0 = w.d0, start = w.start, last = w.last, t0 = w.t0, tend = t0 + w.nks;
+        row = p.args.book.table + static_cast<size_t>(w.slot) * p.args.book.max_pages;
+        id = live(t0) ? row[(t0 * kStepKeys + off) >> log_page] : 0;
+        t = t0 - 2;  // its first step's other distance tiles
+      }
+      const bool step = t >= t0;
+      const bool lv = step && live(t);
       Tile e;
       e.page = -1;
       if (lv) {
@@ -300,33 +285,27 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
         bad |= !good;
         e.page = good ? id : p.args.book.n_pages;
       }
-      if (t + 1 < tend) id = live(t + 1) ? row[((t + 1) * kStepKeys + off) >> log_page] : 0;
+      if (step && t + 1 < tend) id = live(t + 1) ? row[((t + 1) * kStepKeys + off) >> log_page] : 0;
       e.bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lv) & 0xf)) << (log_box + (D == 64 ? 7 : 8));
       e.x = (t * kStepKeys) & ((1 << log_page) - 1);  // 0 for pages of up to 64 rows
       e.h = h;
-      e.unit = un;
-      const bool has_v = LAG == 0 || queued == LAG;
-      const Tile& v = LAG == 0 ? e : v0;
-      issue(is_k || is_r || (is_v && has_v), is_r ? 0 : (is_v ? v.page : e.page),
+      const bool has_v = step && (!TRAIL || holds);
+      const Tile& v = TRAIL ? held : e;
+      issue(is_r || (is_k && step) || (is_v && has_v), is_r ? 0 : (is_v ? v.page : e.page),
             is_r ? d0 - kStepKeys * (t + 1) : (is_v ? v.x : e.x), is_v ? v.h : h,
             is_r ? static_cast<uint32_t>(kTile) : (is_v ? v.bytes : e.bytes));
-      if (LAG > 0) {
-        if (has_v) {
-          v0 = v1;
-          --queued;
-        }
-        if (queued == 0)
-          v0 = e;
-        else
-          v1 = e;
-        ++queued;
+      if (TRAIL && step) {
+        held = e;
+        holds = true;
       }
+      head = t == t0;
+      ++t;
     }
-    if (next_h < 0) break;
+    if (!ok || done) break;
   }
-  if (LAG > 0) flush_v(0xffffffffu);
+  if (TRAIL && ok) release();
   if (bad) atomicOr(p.args.status, kStatusPagesBit);
-  if (any && !ok && lane == 0) report_timeout(abort, p.args.status);
+  if (!ok && lane == 0) report_timeout(abort, p.args.status);
   // This warp's own copies land before the CTA may exit.
   if (nQ > 0) mbar_wait_own(&bars->q_full, (nQ - 1) & 1, p.wait_ns);
   if (leads)
