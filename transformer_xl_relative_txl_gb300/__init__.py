@@ -2,8 +2,9 @@
 
 Thin ctypes binding of the C ABI in ``include/txl_relattn.h``: each function
 has the C entry point's name and only marshals torch tensors (device memory,
-CUDA streams) into pointers, sizes and dtype codes.  All computation runs in
-the library's CUDA kernels; there is no fallback.  Importing fails loudly if
+CUDA streams) into pointers, sizes and dtype codes; the paged memory's calls do
+so in the extension module _paged (csrc/paged_binding.cpp).  All computation
+runs in the library's CUDA kernels; there is no fallback.  Importing fails loudly if
 the library has not been built (``python transformer_xl_relative_txl_gb300/build.py``).
 """
 
@@ -12,7 +13,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 
 import torch
 
@@ -45,10 +45,13 @@ _STATUS = {0: "TXL_OK", 1: "TXL_ERR_INVALID_ARG", 2: "TXL_ERR_UNSUPPORTED", 3: "
            4: "TXL_ERR_CUDA", 5: "TXL_ERR_DEVICE_TIMEOUT", 6: "TXL_ERR_PAGES"}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtxl_relattn.so")
-if not os.path.exists(library_path):
-    raise ImportError(
-        f"{library_path} is missing: build it with `python transformer_xl_relative_txl_gb300/build.py`")
+_binding_path = os.path.join(os.path.dirname(library_path), "_paged.so")
+for _path in (library_path, _binding_path):
+    if not os.path.exists(_path):
+        raise ImportError(f"{_path} is missing: build it with `python transformer_xl_relative_txl_gb300/build.py`")
 lib = ctypes.CDLL(library_path)
+
+from . import _paged  # noqa: E402  (needs torch's libraries and the library above loaded)
 
 _p, _i, _ll, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 lib.txl_relattn_forward.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _i, _i, _p]
@@ -102,9 +105,7 @@ class _PageBook(ctypes.Structure):
         (n, ctypes.c_int) for n in ("n_slots", "max_pages", "n_pages", "page_rows")]
 
 
-_pack_book = struct.Struct("4P4i").pack  # the same struct as bytes, in a third of the time
-assert struct.calcsize("4P4i") == ctypes.sizeof(_PageBook)
-_pb = _p  # a pointer to the struct, or its bytes
+_pb = ctypes.POINTER(_PageBook)
 lib.txl_pages_reserve.argtypes = [_pb, _p, _p, _i, _p, _p, _p, _p]
 lib.txl_pages_reserve.restype = _i
 lib.txl_pages_append.argtypes = [_pb, _p, _p, _i, _i, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _p]
@@ -420,83 +421,9 @@ def txl_dense(x, W, y, bias=None, relu=False, stream=None):
     return y
 
 
-_I32 = torch.int32
-
-
-def _vectors(dev, n, *tensors):
-    """Pointers of contiguous int32 vectors of n entries on device dev, where
-    the call launches; None stays None."""
-    out, shape = [], (n,)
-    for t in tensors:
-        if t is None:
-            out.append(None)
-        elif t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"expected a contiguous int32 vector of {n} entries")
-        elif t.get_device() != dev:
-            raise ValueError("tensors must live in the current device's memory")
-        else:
-            out.append(t.data_ptr())
-    return out
-
-
-def _tensors(dev, *tensors):
-    """Pointers of contiguous tensors on device dev; None stays None."""
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-        elif not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        elif t.get_device() != dev:
-            raise ValueError("tensors must live in the current device's memory")
-        else:
-            out.append(t.data_ptr())
-    return out
-
-
-def _device(t):
-    """Device index of t, which must be the current device: the call launches
-    there."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("tensors must live in the current device's memory")
-    return dev
-
-
-# The current stream's handle without the Stream object, which costs as much
-# as a launch.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_on(dev, stream):
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    return _stream(stream)
-
-
-def _book(dev, book, page_rows):
-    """The C struct of a page book as bytes, and its number of pages: a dict
-    of int32 tensors table [slots, max_pages], start and rows [slots], refs
-    [pages]."""
-    table, start, rows, refs = book["table"], book["start"], book["rows"], book["refs"]
-    shape = table.shape
-    n_pages = refs.numel()
-    if len(shape) != 2 or start.shape != shape[:1] or rows.shape != start.shape or refs.dim() != 1:
-        raise ValueError("a book is table [slots, max_pages], start and rows [slots], refs [pages]")
-    for t in (table, start, rows, refs):
-        if t.dtype is not _I32:
-            raise ValueError("a book's tensors are int32")
-    return _pack_book(*_tensors(dev, table, start, rows, refs), *shape, n_pages, page_rows), n_pages
-
-
-def _pools(dev, k_pages, v_pages, n_pages=None):
-    """Pointers and shape of the pools."""
-    shape = k_pages.shape
-    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not k_pages.dtype:
-        raise ValueError("k_pages, v_pages must be [pages, H, page_rows, D] of one dtype")
-    if n_pages is not None and shape[0] != n_pages:
-        raise ValueError("the pools' pages must be those that refs counts")
-    return *_tensors(dev, k_pages, v_pages), shape
+def _handle(stream):
+    """A stream's handle; None: the current stream's, found by the call."""
+    return None if stream is None else _stream(stream)
 
 
 def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, stream=None):
@@ -504,69 +431,40 @@ def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, s
     dict of int32 tensors table [slots, max_pages], start, rows [slots], refs
     [pages].  granted, copy_src, copy_dst (int32 [n]) receive the rows granted
     and the pages that txl_pages_append has to copy."""
-    dev, n = _device(slots), slots.numel()
-    b, _ = _book(dev, book, page_rows)
-    s, g, src, dst = _vectors(dev, n, slots, granted, copy_src, copy_dst)
-    c, = _vectors(dev, n + 1, cu)
-    _check(lib.txl_pages_reserve(b, s, c, n, g, src, dst, _stream_on(dev, stream)), "txl_pages_reserve")
+    _check(_paged.pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, _handle(stream)),
+           "txl_pages_reserve")
 
 
 def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new, stream=None):
     """Rows cu[i] .. cu[i+1]-1 of k_new, v_new [T, H, D] into the last rows of
     slot slots[i] of the pools [pages, H, page_rows, D], after the copies that
     txl_pages_reserve named (copy_src, copy_dst, or None and None)."""
-    dev, n = _device(slots), slots.numel()
-    kp, vp, (_, H, P, D) = _pools(dev, k_pages, v_pages, book["refs"].numel())
-    b, _ = _book(dev, book, P)
-    s, g, src, dst = _vectors(dev, n, slots, granted, copy_src, copy_dst)
-    c, = _vectors(dev, n + 1, cu)
-    if (src is None) != (dst is None):
-        raise ValueError("copy_src and copy_dst come together")
-    T = k_new.shape[0]
-    if k_new.shape != (T, H, D) or v_new.shape != (T, H, D):
-        raise ValueError("k_new, v_new must be [T, H, D]")
-    if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
-        raise ValueError("the pools and the new rows share a dtype")
-    kn, vn = _tensors(dev, k_new, v_new)
-    _check(lib.txl_pages_append(b, kp, vp, H, D, s, c, n, g, src, dst, kn, vn, T,
-                                _dtype_code(k_pages.dtype), _stream_on(dev, stream)), "txl_pages_append")
+    _check(_paged.pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new,
+                               _handle(stream)), "txl_pages_append")
 
 
 def txl_pages_copy(k_pages, v_pages, src, dst, stream=None):
     """Whole pages src[i] -> dst[i] of both pools; pairs with -1 are left out."""
-    dev, n = _device(src), src.numel()
-    kp, vp, (N, H, P, D) = _pools(dev, k_pages, v_pages)
-    s, d = _vectors(dev, n, src, dst)
-    _check(lib.txl_pages_copy(kp, vp, N, H * P * D, s, d, n, _dtype_code(k_pages.dtype), _stream_on(dev, stream)),
-           "txl_pages_copy")
+    _check(_paged.pages_copy(k_pages, v_pages, src, dst, _handle(stream)), "txl_pages_copy")
 
 
 def txl_pages_fork(book, page_rows, src, dst, ok, stream=None):
     """Empty slot dst[i] shares the pages of slot src[i]; ok (int32 [n])
     receives 1, or 0 where refused."""
-    dev, n = _device(src), src.numel()
-    b, _ = _book(dev, book, page_rows)
-    s, d, k = _vectors(dev, n, src, dst, ok)
-    _check(lib.txl_pages_fork(b, s, d, n, k, _stream_on(dev, stream)), "txl_pages_fork")
+    _check(_paged.pages_fork(book, page_rows, src, dst, ok, _handle(stream)), "txl_pages_fork")
 
 
 def txl_pages_free(book, page_rows, slots, keep=None, stream=None):
     """Slot slots[i] keeps its newest keep[i] rows (None: none)."""
-    dev, n = _device(slots), slots.numel()
-    b, _ = _book(dev, book, page_rows)
-    s, k = _vectors(dev, n, slots, keep)
-    _check(lib.txl_pages_free(b, s, k, n, _stream_on(dev, stream)), "txl_pages_free")
+    _check(_paged.pages_free(book, page_rows, slots, keep, _handle(stream)), "txl_pages_free")
 
 
 def txl_pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, stream=None):
     """The live pages get the lowest ids.  new_id, copy_src, copy_dst (int32
     [pages]) and count (int32 [1]) receive the new ids and the moves, which
     txl_pages_copy(k_pages, v_pages, copy_src, copy_dst) then makes."""
-    dev = _device(new_id)
-    b, n_pages = _book(dev, book, page_rows)
-    ids, s, d = _vectors(dev, n_pages, new_id, copy_src, copy_dst)
-    c, = _vectors(dev, 1, count)
-    _check(lib.txl_pages_compact(b, ids, s, d, c, _stream_on(dev, stream)), "txl_pages_compact")
+    _check(_paged.pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, _handle(stream)),
+           "txl_pages_compact")
 
 
 def txl_relattn_paged_workspace_bytes(n, T, H, D, dtype):
@@ -582,28 +480,9 @@ def txl_relattn_forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, b
     [H, T] fp32 or None; max_new: the largest number of new rows of an entry
     (T when None); workspace: uint8, txl_relattn_paged_workspace_bytes(...).
     scale defaults to 1/sqrt(D)."""
-    dev, n = _device(slots), slots.numel()
-    kp, vp, (_, H, P, D) = _pools(dev, k_pages, v_pages, book["refs"].numel())
-    b, _ = _book(dev, book, P)
-    s, = _vectors(dev, n, slots)
-    c, = _vectors(dev, n + 1, cu)
-    T, n_r = q.shape[0], r.shape[0]
-    if q.shape != (T, H, D) or o.shape != q.shape:
-        raise ValueError("q and o must be [T, H, D]")
-    if r.shape != (n_r, H, D) or bias_u.shape != (H, D) or bias_v.shape != (H, D):
-        raise ValueError("r must be [n_r, H, D]; biases [H, D]")
-    if bias_u.dtype is not torch.float32 or bias_v.dtype is not torch.float32:
-        raise ValueError("biases are fp32")
-    if q.dtype is not k_pages.dtype or r.dtype is not k_pages.dtype:
-        raise ValueError("q, the pools and r share a dtype")
-    if lse is not None and (lse.shape != (H, T) or lse.dtype is not torch.float32):
-        raise ValueError("lse must be fp32 [H, T]")
-    qp, rp, up, vbp, op, lp, wp = _tensors(dev, q, r, bias_u, bias_v, o, lse, workspace)
-    st = lib.txl_relattn_forward_paged(qp, kp, vp, b, s, c, n, T, T if max_new is None else max_new, rp,
-                                       up, vbp, op, lp, H, D, n_r, D ** -0.5 if scale is None else scale,
-                                       _dtype_code(q.dtype), _dtype_code(o.dtype), wp, workspace.nbytes,
-                                       _stream_on(dev, stream))
-    _check(st, "txl_relattn_forward_paged")
+    _check(_paged.forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, bias_v, o, workspace, lse, max_new,
+                                q.shape[-1] ** -0.5 if scale is None else scale, _handle(stream)),
+           "txl_relattn_forward_paged")
     return o
 
 

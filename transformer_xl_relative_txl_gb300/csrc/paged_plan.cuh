@@ -30,7 +30,7 @@ namespace txl {
 
 constexpr int kDecodeRows = 4;  // sequences with up to this many new tokens go to the decode kernel
 constexpr int kMaxSms = 160;    // the workspace has room for the CTAs of so many SMs
-constexpr int kDecodePerSm = 2, kSimtPerSm = 4;
+constexpr int kDecodePerSm = 2, kSimtPerSm = 3;
 constexpr int kTileQueries = 128, kSimtQueries = 16;
 
 // One sequence.
