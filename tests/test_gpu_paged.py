@@ -394,6 +394,41 @@ def test_large_book(txl):
     assert txl.txl_get_device_status() == 0
 
 
+@pytest.mark.parametrize("n_slots,n", [(7000, 1024), (7000, 1025), (9000, 1), (16384, 1000), (1100, 1024)])
+def test_reserve_sizes(txl, n_slots, n):
+    """More pages than are placed at a time; either side of one entry a thread; shared last pages; too few pages left."""
+    rng = np.random.default_rng(n_slots + n)
+    assert txl.txl_get_device_status() == 0
+    P, n_pages, max_pages = 16, 17000, 12
+    book = Book(n_slots, max_pages, n_pages, P)
+    for page in rng.choice(n_pages, 5000, replace=False).tolist():  # held elsewhere
+        book.refs[page] = 1
+    dev = to_gpu(book)
+
+    def reserve(slots, counts):
+        cu = cu_of(counts)
+        out = [ints([9] * len(slots)) for _ in range(3)]
+        g, a, z, refused = book.reserve(slots, cu)
+        txl.txl_pages_reserve(dev, P, ints(slots), ints(cu), *out)
+        assert [x.tolist() for x in out] == [g, a, z]
+        same(dev, book)
+        assert (txl.txl_get_device_status() == 0) == (not refused)
+        return refused
+
+    order = rng.permutation(n_slots).tolist()
+    slots, others = order[:n], order[n:2 * n]
+    assert not reserve(slots, rng.integers(1, 9 * P, n).tolist())
+    pairs = min(len(others), n)
+    if pairs:
+        ok = book.fork(slots[:pairs], others[:pairs])
+        out = ints([9] * pairs)
+        txl.txl_pages_fork(dev, P, ints(slots[:pairs]), ints(others[:pairs]), out)
+        assert out.tolist() == ok
+    assert not reserve(slots, [1] * n)  # copies of shared last pages
+    reserve(slots + others[:pairs], rng.integers(0, 9 * P, n + pairs).tolist())  # some ask for too much
+    reserve(slots[::-1], [P] * n)  # until the pages are gone
+
+
 def test_pools_off_the_wide_path(txl):
     """Pools and rows on a 2-byte boundary go by the narrow copies."""
     rng = np.random.default_rng(22)

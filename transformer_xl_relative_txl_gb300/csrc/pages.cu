@@ -12,6 +12,7 @@
 //
 // Bad entries (a slot, page or length out of range, the same slot twice) are
 // refused, touch nothing and raise the pages bit of the status word.
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 
@@ -24,35 +25,40 @@ namespace {
 
 constexpr int kBlock = 1024;    // threads of the single-CTA kernels
 constexpr int kPerThread = 16;  // refs a thread looks at per tile
+constexpr int kList = 4096;     // pages placed at a time
 
 __device__ __forceinline__ void report_pages(unsigned int* status) { atomicOr(status, kStatusPagesBit); }
 
 __device__ __forceinline__ int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
 
-// Inclusive sum over the CTA, saturating at `cap` (min(a + b, cap) is
-// associative for non-negative terms; cap < 2^30, so no sum overflows).
-// warp_sums[31] holds the CTA's sum until the next call.
-__device__ int block_scan(int x, int cap, int* warp_sums) {
+// Inclusive sums of x and of y over the CTA, saturating at `cap` (min(a + b,
+// cap) is associative for non-negative terms; cap < 2^30, so no sum overflows),
+// and the CTA's sums.  Every warp adds up the warps' sums itself: one barrier,
+// and two buffers used in turn, so that a sum is read before it is replaced.
+struct Scan {
+  int2 at, all;
+};
+__device__ __forceinline__ Scan block_scan(int2 v, int cap, int2 (*sums)[32], int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x = min(x + y, cap);
-  }
-  __syncthreads();  // warp_sums of the scan before has been read
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
+  auto scan = [&](int2 a) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s = min(s + y, cap);
+      const int x = __shfl_up_sync(0xffffffffu, a.x, d), y = __shfl_up_sync(0xffffffffu, a.y, d);
+      if (lane >= d) a = make_int2(min(a.x + x, cap), min(a.y + y, cap));
     }
-    warp_sums[lane] = s;
-  }
+    return a;
+  };
+  v = scan(v);
+  turn ^= 1;
+  if (lane == 31) sums[turn][warp] = v;
   __syncthreads();
-  return warp > 0 ? min(x + warp_sums[warp - 1], cap) : x;
+  const int2 w = scan(sums[turn][lane]);
+  const int before = warp > 0 ? warp - 1 : 0;
+  const int2 b = make_int2(__shfl_sync(0xffffffffu, w.x, before), __shfl_sync(0xffffffffu, w.y, before));
+  Scan r;
+  r.at = warp > 0 ? make_int2(min(v.x + b.x, cap), min(v.y + b.y, cap)) : v;
+  r.all = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
+  return r;
 }
 static_assert(kBlock == 1024, "block_scan sums 32 warps");
 
@@ -103,6 +109,19 @@ __device__ __forceinline__ uint32_t used_mask(const PageBook& b, int base) {
 // found by scanning refs in ascending order, 16384 pages a step, only as far
 // as the needs go.  A free page's rank names its entry (binary search in the
 // sums) and its place in the entry's table row.
+//
+// Nothing here is large: the kernel is the chain of its loads (an entry's slot,
+// its lengths, its last page, that page's count, each a trip to L2) and its
+// barriers.  With SMALL, up to 1024 entries, a thread keeps its entry's answer
+// in registers and leaves what the pages' owners need of it in shared memory,
+// and the first 16384 pages are read once, beside the entries' first loads, and
+// counted in the same scan as the needs.
+struct Ask {  // what an entry asks for
+  int slot, count, have, need, last;  // need: pages (0 where it asks for none or is refused)
+  bool ok, shared, idle;              // shared: its last page, which is copied; idle: a valid entry without rows
+};
+
+template <bool SMALL>
 __global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* __restrict__ slots,
                                                          const int* __restrict__ cu, int n, int* granted,
                                                          int* copy_src, int* copy_dst, unsigned int* status) {
@@ -111,190 +130,247 @@ __global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* 
   extern __shared__ int smem[];
   int* first = smem;             // [n_slots] the entry that names the slot first
   int* upto = smem + b.n_slots;  // [n] pages needed by entries 0 .. i
-  __shared__ int warp_sums[32];
+  int* slot_of = upto + n;       // SMALL: [n] the entry's slot
+  int* place = slot_of + n;      // SMALL: [n] 2 * (its first new place in its table row) + (that place's page is copied)
+  __shared__ int2 sums[2][32];
   __shared__ int s_lim;
+  __shared__ int list[kList];  // pages of a window of ranks
   const int tid = threadIdx.x;
   const int cap = b.n_pages + 1;
+  constexpr int kTile = kBlock * kPerThread;
+  int turn = 0;
 
+  const uint32_t used0 = used_mask(b, 0);
   for (int i = tid; i < n; i += kBlock)
     if (const int s = slots[i]; s >= 0 && s < b.n_slots) first[s] = INT_MAX;
+  if (tid == 0) s_lim = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kBlock)
     if (const int s = slots[i]; s >= 0 && s < b.n_slots) atomicMin(&first[s], i);
-  if (tid == 0) s_lim = 0;
-  __syncthreads();
 
-  // What entry i asks for: pages (0 where it asks for none or is refused),
-  // whether its last page is shared and so copied, and whether it is valid.
-  struct Ask {
-    Slot sl;
-    int count, need, last;
-    bool ok, shared;
-  };
   auto ask = [&](int i) {
-    Ask a{read_slot(b, slots[i]), cu[i + 1] - cu[i], 0, -1, false, false};
-    a.ok = a.sl.ok && a.count > 0 && first[a.sl.s] == i;
-    if (a.ok) {
-      const long long end = static_cast<long long>(a.sl.start) + a.sl.rows;
-      const int have = ceil_div(end, b.page_rows);
-      const long long want = (end + a.count + b.page_rows - 1) / b.page_rows;
-      a.ok = want <= b.max_pages;
-      if (a.ok && end % b.page_rows != 0) {
-        a.last = table_row(b, a.sl.s)[have - 1];
-        a.ok = a.last >= 0 && a.last < b.n_pages;
-        a.shared = a.ok && b.refs[a.last] > 1;
-      }
-      if (a.ok) a.need = static_cast<int>(want) - have + (a.shared ? 1 : 0);
+    const Slot sl = read_slot(b, slots[i]);
+    Ask a{sl.s, cu[i + 1] - cu[i], 0, 0, -1, false, false, false};
+    if (!sl.ok) return a;
+    a.idle = a.count == 0;
+    const long long end = static_cast<long long>(sl.start) + sl.rows;
+    a.have = ceil_div(end, b.page_rows);
+    if (a.count <= 0) return a;
+    const long long want = (end + a.count + b.page_rows - 1) / b.page_rows;
+    a.ok = want <= b.max_pages;
+    if (a.ok && end % b.page_rows != 0) {
+      a.last = table_row(b, sl.s)[a.have - 1];
+      a.ok = a.last >= 0 && a.last < b.n_pages;
+      a.shared = a.ok && b.refs[a.last] > 1;
     }
+    if (a.ok) a.need = static_cast<int>(want) - a.have + (a.shared ? 1 : 0);
+    return a;
+  };
+  auto mine = [&](int i) {  // behind the barrier: of a slot named twice the first entry counts
+    Ask a = ask(i);
+    if (a.ok && first[a.slot] != i) a.ok = a.shared = false, a.need = 0;
     return a;
   };
 
+  Ask own{};
+  if (SMALL && tid < n) own = ask(tid);
+  __syncthreads();
+  if (SMALL && own.ok && first[own.slot] != tid) own.ok = own.shared = false, own.need = 0;
+
+  // Sums of the needs, and of the first tile's free pages.
+  const int free0 = kPerThread - __popc(used0);
   int carry = 0;
-  for (int base = 0; base < n; base += kBlock) {
+  Scan scan{};
+  for (int base = 0; base < n || base == 0; base += kBlock) {
     const int i = base + tid;
-    const int need = i < n ? min(ask(i).need, cap) : 0;
-    const int sum = min(carry + block_scan(need, cap, warp_sums), cap);
-    if (i < n) upto[i] = sum;
-    carry = min(carry + warp_sums[31], cap);
+    const int need = i < n ? min((SMALL ? own : mine(i)).need, cap) : 0;
+    scan = block_scan(make_int2(need, free0), cap, sums, turn);
+    if (i < n) upto[i] = min(carry + scan.at.x, cap);
+    carry = min(carry + scan.all.x, cap);
+  }
+  const int total = carry;
+  if (SMALL && tid < n) {
+    slot_of[tid] = own.slot;
+    place[tid] = 2 * (own.have - (own.shared ? 1 : 0)) + (own.shared ? 1 : 0);
   }
   __syncthreads();
-  const int total = carry;
 
   // Free pages there are, counted as far as `total`; lim: pages given out.
-  int lim = total;
-  if (total > 0) {
-    int found = 0;
-    for (int base = 0; base < b.n_pages && found < total; base += kBlock * kPerThread) {
-      block_scan(kPerThread - __popc(used_mask(b, base)), cap, warp_sums);
-      found = min(found + warp_sums[31], cap);
-    }
-    if (found < total) {
-      for (int i = tid; i < n; i += kBlock)
-        if (upto[i] <= found) atomicMax(&s_lim, upto[i]);
-      __syncthreads();
-      lim = s_lim;
-    }
+  int lim = total, found = scan.all.y;
+  const int rank_first = scan.at.y - free0;
+  for (int base = kTile; base < b.n_pages && found < total; base += kTile) {
+    const Scan x = block_scan(make_int2(kPerThread - __popc(used_mask(b, base)), 0), cap, sums, turn);
+    found = min(found + x.all.x, cap);
+  }
+  const int found_first = scan.all.y;
+  if (found < total) {
+    for (int i = tid; i < n; i += kBlock)
+      if (upto[i] <= found) atomicMax(&s_lim, upto[i]);
+    __syncthreads();
+    lim = s_lim;
   }
 
   // The entries' answers, from the state before any change; the pages of
   // the copies follow below.
   for (int i = tid; i < n; i += kBlock) {
-    const Ask a = ask(i);
+    const Ask a = SMALL ? own : mine(i);
     const bool given = a.ok && (a.need == 0 || upto[i] <= lim);
     granted[i] = given ? a.count : 0;
     copy_src[i] = given && a.shared ? a.last : -1;
     copy_dst[i] = -1;
-    if (!given && !(a.sl.ok && a.count == 0)) report_pages(status);
+    if (!given && !a.idle) report_pages(status);
   }
   __syncthreads();
 
   // Free pages 0 .. lim-1 to their places.  A page's ref changes only after
-  // the thread that owns it has read it.
+  // its tile has been read.
   int rank0 = 0;
-  for (int base = 0; base < b.n_pages && rank0 < lim; base += kBlock * kPerThread) {
-    const uint32_t used = used_mask(b, base);
-    const int mine = kPerThread - __popc(used);
-    int rank = rank0 + block_scan(mine, cap, warp_sums) - mine;
-    rank0 += warp_sums[31];
-    for (uint32_t m = ~used & 0xffffu; m != 0 && rank < lim; m &= m - 1, ++rank) {
-      const int page = base + tid * kPerThread + __ffs(m) - 1;
-      int lo = 0, hi = n - 1;  // the first entry with upto > rank
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (upto[mid] > rank)
-          hi = mid;
-        else
-          lo = mid + 1;
+  for (int base = 0; base < b.n_pages && rank0 < lim; base += kTile) {
+    const int tile_rank = rank0;
+    uint32_t used = used0;
+    int rank = rank_first;
+    if (base == 0) {
+      rank0 = found_first;
+    } else {
+      used = used_mask(b, base);
+      const int free = kPerThread - __popc(used);
+      const Scan x = block_scan(make_int2(free, 0), cap, sums, turn);
+      rank = rank0 + x.at.x - free;
+      rank0 += x.all.x;
+    }
+    // By rank in shared memory first: free pages stand together, so that one
+    // thread has up to 16 of them to place.
+    uint32_t m = ~used & 0xffffu;
+    const int end = min(rank0, lim);
+    for (int w0 = tile_rank; w0 < end; w0 += kList) {
+      const int w1 = min(w0 + kList, end);
+      for (; m != 0 && rank < w1; m &= m - 1, ++rank) list[rank - w0] = base + tid * kPerThread + __ffs(m) - 1;
+      __syncthreads();
+      for (int x = w0 + tid; x < w1; x += kBlock) {
+        int lo = 0, hi = n - 1;  // the first entry with upto > x
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (upto[mid] > x)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        const int j = x - (lo > 0 ? upto[lo - 1] : 0), page = list[x - w0];
+        int s, at, copied;
+        if (SMALL) {
+          s = slot_of[lo];
+          at = place[lo] >> 1;
+          copied = place[lo] & 1;
+        } else {
+          s = slots[lo];
+          copied = copy_src[lo] >= 0 ? 1 : 0;
+          at = ceil_div(static_cast<long long>(b.start[s]) + b.rows[s], b.page_rows) - copied;
+        }
+        b.refs[page] = 1;
+        table_row(b, s)[at + j] = page;
+        if (j < copied) copy_dst[lo] = page;
       }
-      const int j = rank - (lo > 0 ? upto[lo - 1] : 0);
-      const int s = slots[lo];
-      const int have = ceil_div(static_cast<long long>(b.start[s]) + b.rows[s], b.page_rows);
-      const int copied = copy_src[lo] >= 0 ? 1 : 0;
-      b.refs[page] = 1;
-      table_row(b, s)[have + j - copied] = page;
-      if (j < copied) copy_dst[lo] = page;
+      __syncthreads();
     }
   }
   __syncthreads();
   for (int i = tid; i < n; i += kBlock) {
-    if (granted[i] > 0) b.rows[slots[i]] += granted[i];
-    if (copy_src[i] >= 0) atomicSub(&b.refs[copy_src[i]], 1);
+    const int rows = granted[i], from = copy_src[i];
+    if (rows > 0) b.rows[slots[i]] += rows;
+    if (from >= 0) atomicSub(&b.refs[from], 1);
   }
 }
 
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
+// Division by a number that the host knows: q = (mulhi(x, m) + x) >> s, exact
+// for x < 2^31 (m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d)).
+struct Divisor {
+  uint32_t d, m, s;
+  explicit Divisor(uint32_t y) : d(y), s(0) {
+    while (s < 31 && (1u << s) < y) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - y)) / y + 1);
+  }
+  __device__ __forceinline__ uint32_t over(uint32_t x) const { return (__umulhi(x, m) + x) >> s; }
+};
+
 // CTA (x, i) writes rows of entry i: first the rows of the copied page that
-// lie before the new ones, then the new rows, each as H pieces of D values.
+// lie before the new ones, then the new rows, each as H pieces of D values,
+// `tile` rows (about 1024 vectors) at a time.  What it waits for is the chain
+// of its loads, so those that do not need one another go out together: an
+// entry's numbers, then its slot's lengths, then a tile's pages beside its new
+// rows.
 template <typename V>
 __global__ void __launch_bounds__(256) append_kernel(PageBook b, V* __restrict__ kp, V* __restrict__ vp, int H, int DV,
                                                      const int* __restrict__ slots, const int* __restrict__ cu,
                                                      const int* __restrict__ granted,
                                                      const int* __restrict__ copy_src,
                                                      const int* __restrict__ copy_dst, const V* __restrict__ kn,
-                                                     const V* __restrict__ vn, int T, unsigned int* status) {
+                                                     const V* __restrict__ vn, int T, int tile, Divisor by_row,
+                                                     Divisor by_head, int log_page, unsigned int* status) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int i = blockIdx.y;
-  const int count = granted[i];
+  const int count = granted[i], t0 = cu[i], t1 = cu[i + 1], s = slots[i];
+  int from = -1, to = -1;
+  if (copy_src != nullptr) from = copy_src[i], to = copy_dst[i];
+  const Slot sl = read_slot(b, s);
   if (count <= 0) return;
-  const int t0 = cu[i];
-  const Slot sl = read_slot(b, slots[i]);
-  if (!sl.ok || count > sl.rows || t0 < 0 || count != cu[i + 1] - t0 || static_cast<long long>(t0) + count > T) {
+  if (!sl.ok || count > sl.rows || t0 < 0 || count != t1 - t0 || static_cast<long long>(t0) + count > T) {
     if (threadIdx.x == 0) report_pages(status);
     return;
   }
   const int P = b.page_rows;
   const int x0 = sl.start + sl.rows - count;  // first new row
-  int from = -1, to = -1;
-  if (copy_src != nullptr) from = copy_src[i], to = copy_dst[i];
   const bool copies = from >= 0 && to >= 0;
   if (copies && (from >= b.n_pages || to >= b.n_pages)) {
     if (threadIdx.x == 0) report_pages(status);
     return;
   }
-  const int old = copies ? x0 % P : 0;
+  const int old = copies ? x0 & (P - 1) : 0;
   const int* row = table_row(b, sl.s);
-  const long long per = static_cast<long long>(H) * DV;  // vectors of a row
-  const long long total = (old + static_cast<long long>(count)) * per;
+  const uint32_t per = by_row.d;  // vectors of a row
   const size_t page = static_cast<size_t>(H) * P * DV;
   bool bad = false;
   constexpr int U = 4;
-  const long long step = static_cast<long long>(gridDim.x) * 256 * U;
-  for (long long e0 = static_cast<long long>(blockIdx.x) * 256 * U + threadIdx.x; e0 < total; e0 += step) {
-    V kx[U], vx[U];
-    size_t dst[U];
-    bool on[U];
+  for (int y0 = static_cast<int>(blockIdx.x) * tile; y0 < old + count; y0 += static_cast<int>(gridDim.x) * tile) {
+    const uint32_t total = static_cast<uint32_t>(min(tile, old + count - y0)) * per;
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 256 * U) {
+      V kx[U], vx[U];
+      size_t dst[U];
+      bool on[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long e = e0 + u * 256;
-      on[u] = e < total;
-      if (!on[u]) continue;
-      const int y = static_cast<int>(e / per), rem = static_cast<int>(e % per);
-      const int h = rem / DV, c = rem % DV;
-      if (y < old) {
-        const size_t at = (static_cast<size_t>(h) * P + y) * DV + c;
-        dst[u] = to * page + at;
-        kx[u] = kp[from * page + at];
-        vx[u] = vp[from * page + at];
-      } else {
-        const int x = x0 + y - old;
-        const int id = row[x / P];
-        on[u] = id >= 0 && id < b.n_pages;
-        bad |= !on[u];
-        dst[u] = id * page + (static_cast<size_t>(h) * P + x % P) * DV + c;
-        const size_t src = static_cast<size_t>(t0 + y - old) * per + rem;
-        kx[u] = __ldg(kn + src);
-        vx[u] = __ldg(vn + src);
+      for (int u = 0; u < U; ++u) {
+        const uint32_t e = e0 + u * 256;
+        on[u] = e < total;
+        if (!on[u]) continue;
+        const uint32_t line = by_row.over(e), rem = e - line * per;
+        const uint32_t h = by_head.over(rem), c = rem - h * by_head.d;
+        const int y = y0 + static_cast<int>(line);
+        if (y < old) {
+          const size_t at = (static_cast<size_t>(h) * P + y) * DV + c;
+          dst[u] = to * page + at;
+          kx[u] = kp[from * page + at];
+          vx[u] = vp[from * page + at];
+        } else {
+          const int x = x0 + y - old;
+          const int id = row[x >> log_page];
+          const size_t src = static_cast<size_t>(t0 + y - old) * per + rem;
+          kx[u] = __ldg(kn + src);
+          vx[u] = __ldg(vn + src);
+          on[u] = id >= 0 && id < b.n_pages;
+          bad |= !on[u];
+          dst[u] = id * page + (static_cast<size_t>(h) * P + (x & (P - 1))) * DV + c;
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (on[u]) {
+          kp[dst[u]] = kx[u];
+          vp[dst[u]] = vx[u];
+        }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (on[u]) {
-        kp[dst[u]] = kx[u];
-        vp[dst[u]] = vx[u];
-      }
   }
   if (bad) report_pages(status);
 }
@@ -464,19 +540,20 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(PageBook b, int* __rest
                                                          int* __restrict__ count) {
   grid_dep_wait();
   grid_dep_launch_dependents();
-  __shared__ int warp_sums[32];
+  __shared__ int2 sums[2][32];
   const int cap = b.n_pages + 1;
   constexpr int kTile = kBlock * kPerThread;
-  int live = 0;
+  int live = 0, turn = 0;
+  const uint32_t used0 = used_mask(b, 0);
   for (int base = 0; base < b.n_pages; base += kTile) {
     const int past = max(0, min(kPerThread, base + static_cast<int>(threadIdx.x + 1) * kPerThread - b.n_pages));
-    block_scan(__popc(used_mask(b, base)) - past, cap, warp_sums);
-    live += warp_sums[31];
+    const uint32_t used = base == 0 ? used0 : used_mask(b, base);
+    live += block_scan(make_int2(__popc(used) - past, 0), cap, sums, turn).all.x;
   }
   int holes = 0, moved = 0;
   for (int base = 0; base < b.n_pages; base += kTile) {
     const int p0 = base + threadIdx.x * kPerThread;
-    const uint32_t used = used_mask(b, base);
+    const uint32_t used = base == 0 ? used0 : used_mask(b, base);
     uint32_t hole = 0, move = 0;
 #pragma unroll
     for (int q = 0; q < kPerThread; ++q) {
@@ -487,10 +564,11 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(PageBook b, int* __rest
       move |= (u && p >= live ? 1u : 0u) << q;
       if (!u || p < live) new_id[p] = u ? p : -1;
     }
-    int h = holes + block_scan(__popc(hole), cap, warp_sums) - __popc(hole);
-    holes += warp_sums[31];
-    int m = moved + block_scan(__popc(move), cap, warp_sums) - __popc(move);
-    moved += warp_sums[31];
+    const Scan x = block_scan(make_int2(__popc(hole), __popc(move)), cap, sums, turn);
+    int h = holes + x.at.x - __popc(hole);
+    int m = moved + x.at.y - __popc(move);
+    holes += x.all.x;
+    moved += x.all.y;
     for (; hole != 0; hole &= hole - 1) copy_dst[h++] = p0 + __ffs(hole) - 1;
     for (; move != 0; move &= move - 1) copy_src[m++] = p0 + __ffs(move) - 1;
   }
@@ -542,13 +620,15 @@ cudaError_t by_vector(uintptr_t bits, F f) {
 
 cudaError_t launch_pages_reserve(const PageBook& b, const int* slots, const int* cu, int n, int* granted,
                                  int* copy_src, int* copy_dst, unsigned int* status, cudaStream_t stream) {
-  const size_t smem = (static_cast<size_t>(b.n_slots) + n) * sizeof(int);
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const bool small = n <= kBlock;
+  auto kern = small ? reserve_kernel<true> : reserve_kernel<false>;
+  const size_t smem = (static_cast<size_t>(b.n_slots) + (small ? 3 : 1) * static_cast<size_t>(n)) * sizeof(int);
+  if (smem > 24 * 1024) {  // beside 17 KB that every launch has
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                2 * kMaxSlots * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(reserve_kernel, dim3(1), dim3(kBlock), smem, stream, b, slots, cu, n, granted, copy_src,
+  return launch_dependent(kern, dim3(1), dim3(kBlock), smem, stream, b, slots, cu, n, granted, copy_src,
                           copy_dst, status);
 }
 
@@ -568,7 +648,9 @@ cudaError_t launch_pages_append(const PageBook& b, void* kp, void* vp, int H, in
     const dim3 grid(grid_for((rows * H * dv + 1023) / 1024, most), static_cast<unsigned>(n));
     return launch_dependent(append_kernel<V>, grid, dim3(256), 0, stream, b, static_cast<V*>(kp),
                             static_cast<V*>(vp), H, dv, slots, cu, granted, copy_src, copy_dst,
-                            static_cast<const V*>(kn), static_cast<const V*>(vn), T, status);
+                            static_cast<const V*>(kn), static_cast<const V*>(vn), T,
+                            std::max(1, 1024 / (H * dv)), Divisor(H * dv), Divisor(dv),
+                            __builtin_ctz(b.page_rows), status);
   });
 }
 
