@@ -10,28 +10,26 @@
 namespace txl {
 namespace {
 
-template <typename Walk>
+template <typename Units>
 int pieces_of(int H, int n, const int* start, const int* rows, const int* fresh, int most, int* out, int cap) {
   std::vector<PlanSeq> list(n);
   long long total = 0;
   for (int i = 0; i < n; ++i) {
     list[i] = PlanSeq{total, 0, fresh[i], i, start[i], rows[i], i};
-    if (fresh[i] > 0) total += Walk::cost_of_head(list[i]) * H;
+    if (fresh[i] > 0) total += Units::cost_of_head(list[i]) * H;
   }
-  const PlanLine line = plan_line(total, plan_ctas<typename Walk::Cost>(total, most));
+  const PlanLine line = plan_line(total, plan_ctas<typename Units::Cost>(total, most));
   int count = 0;
   for (int c = 0, x = 0; c < line.ctas; ++c) {
     while (x + 1 < n && list[x + 1].pre <= plan_cut(c, line)) ++x;
-    Walk w;
-    w.seqs = list.data() + x;
-    w.count = n - x;
-    w.line = line;
-    w.H = H;
-    w.c = c;
-    for (bool found = w.advance(true, [] { return 0; }); found; found = w.advance(false, [] { return 0; })) {
+    const long long lo = plan_cut(c, line), hi = plan_cut(c + 1, line);
+    PlanAt at = Units::place(list[x], lo);
+    at.i = x;
+    for (int r = 0; Units::find(list.data(), n, H, at, r, &at); r = 1) {
+      const Piece p = Units::piece(list[at.i], at, c, lo, hi, line);
+      if (p.nks == 0) break;
       if (count == cap) return -1;
-      const int row[10] = {c,       w.s.index, w.h,       w.qt,       w.p.t0,
-                           w.p.nks, w.p.first, w.p.index, w.p.pieces, plan_place(c, w.p.index)};
+      const int row[10] = {c, at.i, at.h, at.qt, p.t0, p.nks, p.first, p.index, p.pieces, plan_place(c, p.index)};
       std::copy(row, row + 10, out + 10 * static_cast<size_t>(count++));
     }
   }
@@ -98,10 +96,10 @@ int paged_sms() {
 
 int paged_pieces(int kind, int D, int H, int n, const int* start, const int* rows, const int* fresh, int ctas, int* out,
                  int cap) {
-  if (kind == 2) return pieces_of<SimtWalk>(H, n, start, rows, fresh, ctas, out, cap);
-  if (kind == 1) return pieces_of<TileWalk>(H, n, start, rows, fresh, ctas, out, cap);
-  return D == 64 ? pieces_of<DecodeWalk64>(H, n, start, rows, fresh, ctas, out, cap)
-                 : pieces_of<DecodeWalk32>(H, n, start, rows, fresh, ctas, out, cap);
+  if (kind == 2) return pieces_of<SimtUnits>(H, n, start, rows, fresh, ctas, out, cap);
+  if (kind == 1) return pieces_of<TileUnits>(H, n, start, rows, fresh, ctas, out, cap);
+  return D == 64 ? pieces_of<DecodeUnits64>(H, n, start, rows, fresh, ctas, out, cap)
+                 : pieces_of<DecodeUnits32>(H, n, start, rows, fresh, ctas, out, cap);
 }
 
 size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16) {

@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr int kOffBar = kOffQ + 2 * kQuery;
   static constexpr int kBarBytes = 1408;
   static constexpr int kSmem = kOffBar + kBarBytes + 1024;
-  using Walk = PlanWalk<DecodeCost, BK, 0, 1, kDecodeRows>;  // DecodeWalk64, DecodeWalk32
+  using Units = PlanUnits<DecodeCost, BK, 0, 1, kDecodeRows>;  // DecodeUnits64, DecodeUnits32
 };
 
 struct Params {
@@ -160,12 +160,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
   if (!p.behind_tiles) grid_dep_wait();
   grid_dep_launch_dependents();
   if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
-  plan_begin<typename C::Walk>(p.args, static_cast<int>(gridDim.x), &bars->plan);
+  plan_begin<typename C::Units>(p.args, static_cast<int>(gridDim.x), &bars->plan);
   const uint64_t wait_ns = p.wait_ns;
 
   if (warp == kWarps) {
     // ============================== producer ===============================
-    typename C::Walk w;
+    PlanFound w{};  // the unit at hand, of every lane
+    auto of_lane = [](const PlanFound& f, int x) {
+      PlanFound g;
+      g.s.tok0 = __shfl_sync(0xffffffffu, f.s.tok0, x);
+      g.s.n = __shfl_sync(0xffffffffu, f.s.n, x);
+      g.s.slot = __shfl_sync(0xffffffffu, f.s.slot, x);
+      g.s.start = __shfl_sync(0xffffffffu, f.s.start, x);
+      g.s.rows = __shfl_sync(0xffffffffu, f.s.rows, x);
+      g.h = __shfl_sync(0xffffffffu, f.h, x);
+      g.p.t0 = __shfl_sync(0xffffffffu, f.p.t0, x);
+      g.p.nks = __shfl_sync(0xffffffffu, f.p.nks, x);
+      g.p.index = __shfl_sync(0xffffffffu, f.p.index, x);
+      g.p.pieces = __shfl_sync(0xffffffffu, f.p.pieces, x);
+      return g;
+    };
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -204,7 +218,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       }
       ++units;
     };
-    for (bool first = true; ok && plan_next(p.args, &bars->plan, &w, first); first = false) {
+    PlanFound batch{};
+    int at = 0, found = 0;
+    bool last_batch = false, first = true;
+    for (;;) {
+      if (at == found) {
+        if (last_batch) break;
+        found = plan_batch<typename C::Units>(p.args, &bars->plan, first, &batch, &last_batch);
+        first = false;
+        at = 0;
+        if (found == 0) break;
+      }
+      w = of_lane(batch, at++);
       publish(w.p.nks);
       if (!ok) break;
       const int* row = p.args.book.table + static_cast<size_t>(w.s.slot) * p.args.book.max_pages;

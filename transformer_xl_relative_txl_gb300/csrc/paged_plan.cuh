@@ -132,23 +132,21 @@ __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int
 // that continues an earlier CTA's have a place each.
 __host__ __device__ __forceinline__ int plan_place(int c, int index) { return 2 * c + (index == 0 ? 1 : 0); }
 
-// A walk over the units that CTA c has steps of.  BK: rows of a key step;
-// TILE: queries of a unit (0: the unit has all of the sequence's); sequences of
-// kLo to kHi new tokens are the kernel's.  (Each kernel has this code once and
-// without unrolled loops: what a CTA runs once it has to fetch first.  With
-// copies of it for the first unit and the next, about 100 KB, the call took 7
-// us longer.)
+// A unit: entry of the list at hand, head, tile.
+struct PlanAt {
+  int i, h, qt;
+};
+
+// The units of a kernel.  BK: rows of a key step; TILE: queries of a unit (0:
+// the unit has all of the sequence's); sequences of kLo to kHi new tokens are
+// the kernel's.  Everything is found in closed form, so that the lanes of a
+// warp find a CTA's next 32 units at once (plan_batch).  (One after the other,
+// each cost the warp that loads the tiles about 3000 cycles: 600 dependent
+// instructions, the first time fetched as they run.)
 template <typename C, int BK, int TILE, int LO, int HI>
-struct PlanWalk {
+struct PlanUnits {
   using Cost = C;
   static constexpr int kLo = LO, kHi = HI;
-  const PlanSeq* seqs;  // the sequences at hand (n = 0: an entry that is not the kernel's)
-  int count;            // how many
-  PlanLine line;
-  int H, c, i, h, qt;
-  PlanSeq s;
-  long long a, lo, hi;  // cost position of the unit, the CTA's range
-  Piece p;
 
   static __host__ __device__ __forceinline__ int tiles_of(const PlanSeq& s) {
     return TILE == 0 ? 1 : (s.n + TILE - 1) / (TILE == 0 ? 1 : TILE);
@@ -158,91 +156,86 @@ struct PlanWalk {
     const int last = TILE == 0 ? s.n - 1 : (tile * TILE + TILE < s.n ? tile * TILE + TILE : s.n) - 1;
     return plan_steps(s.start, m + last, BK);
   }
-  // A sequence's units of one head: kUnit each, and the steps, in closed form.
+  // A sequence's units of one head before tile `to`: kUnit each, and the steps.
   // Tile y of those before the last ends at row m + y TILE + TILE - 1 = x, its
   // last key step is floor(x / BK).
-  static __host__ __device__ __forceinline__ long long cost_of_head(const PlanSeq& s) {
-    const int tiles = tiles_of(s);
-    long long steps = steps_of(s, tiles - 1);
-    if (TILE != 0 && tiles > 1) {
+  static __host__ __device__ __forceinline__ long long cost_before(const PlanSeq& s, int to) {
+    const int tiles = tiles_of(s), whole = to < tiles ? to : tiles - 1;
+    long long steps = to == tiles ? steps_of(s, tiles - 1) : 0;
+    if (TILE != 0 && whole > 0) {
       const int m = s.start + s.rows - s.n;
       // the first y0 tiles end before the first live row (rows < n): a step each
       int y0 = m < s.start ? (s.start - m) / (TILE == 0 ? 1 : TILE) : 0;
-      y0 = y0 < tiles - 1 ? y0 : tiles - 1;
-      const long long k = tiles - 1 - y0;
+      y0 = y0 < whole ? y0 : whole;
+      const long long k = whole - y0;
       steps += y0 + k * (1 - s.start / BK);
-      if (TILE >= BK) {  // floor(x / BK) grows by TILE / BK a tile
-        constexpr int kBy = TILE / BK;
-        const int first = m + y0 * TILE + TILE - 1;  // no less than start where k > 0
-        if (k > 0) steps += k * (first / BK) + kBy * (k * (k - 1) / 2);
-      } else {  // floor(x / BK) = floor((b + y) / 2)
-        static_assert(TILE == 0 || TILE >= BK || 2 * TILE == BK, "half a key step a tile");
-        auto halves = [](long long z) { return z < 1 ? 0 : (z - 1) * (z - 1) / 4; };  // sum of floor(j / 2), j < z
-        const long long b = (m + y0 * TILE + TILE - 1) / (TILE == 0 ? 1 : TILE);
-        if (k > 0) steps += halves(b + k) - halves(b);
-      }
-    }
-    return static_cast<long long>(Cost::kUnit) * tiles + Cost::kStep * steps;
-  }
-
-  // On to the first unit with a step in the CTA's range (`first`; the line, H
-  // and c are set, seqs[0] is the sequence that the range starts in once there
-  // is one), or to the next; false: there is none.  fill() puts the next
-  // sequences into `seqs`, and says how many.
-  template <typename Fill>
-  __host__ __device__ __forceinline__ bool advance(bool first, Fill&& fill) {
-    bool placed = !first, step = !first, fresh = first;
-    for (;;) {
-      if (step) {
-        a += cost_of(qt);
-        if (++qt == tiles_of(s)) {
-          qt = 0;
-          if (++h == H) h = 0, ++i, fresh = true;
+      if (k > 0) {
+        const int first = m + y0 * TILE + TILE - 1;  // no less than start
+        if (TILE >= BK) {                            // floor(x / BK) grows by TILE / BK a tile
+          constexpr int kBy = TILE / BK;
+          steps += k * (first / BK) + kBy * (k * (k - 1) / 2);
+        } else {  // floor(x / BK) = floor((b + y) / 2)
+          static_assert(TILE == 0 || TILE >= BK || 2 * TILE == BK, "half a key step a tile");
+          auto halves = [](long long z) { return z < 1 ? 0 : (z - 1) * (z - 1) / 4; };  // sum of floor(j / 2), j < z
+          const long long b = first / (TILE == 0 ? 1 : TILE);
+          steps += halves(b + k) - halves(b);
         }
       }
-      step = true;
-      if (placed && a >= hi) return false;
-      if (fresh) {  // the next sequence
-        if (first && !placed) i = 0;
-        for (;; ++i) {
-          if (i >= count) {
-            count = fill();
-            if (count == 0) return false;
-            i = 0;
-          }
-          if (seqs[i].n > 0) break;
-        }
-        s = seqs[i];
-        fresh = false;
-      }
-      if (!placed) place(), placed = true;
-      p = plan_piece<Cost>(a, steps_of(s, qt), s.start / BK, c, lo, hi, line);
-      if (p.nks > 0) return true;
     }
+    return static_cast<long long>(Cost::kUnit) * to + Cost::kStep * steps;
+  }
+  static __host__ __device__ __forceinline__ long long cost_of_head(const PlanSeq& s) {
+    return cost_before(s, tiles_of(s));
   }
 
- private:
-  __host__ __device__ __forceinline__ long long cost_of(int tile) const {
-    return Cost::kUnit + static_cast<long long>(Cost::kStep) * steps_of(s, tile);
+  // The unit of sequence s (list[0]) that position x of the line lies in.
+  static __host__ __device__ __forceinline__ PlanAt place(const PlanSeq& s, long long x) {
+    const long long per = cost_of_head(s), past = x - s.pre;
+    PlanAt at{0, static_cast<int>(static_cast<float>(past) / static_cast<float>(per)), 0};  // off by one at most: h < 2^20
+    at.h -= at.h > 0 && at.h * per > past;
+    at.h += (at.h + 1) * per <= past;
+    if (TILE != 0) {
+      const long long in = past - at.h * per;
+      int hi = tiles_of(s);  // the largest qt with cost_before(qt) <= in
+      while (at.qt + 1 < hi) {
+        const int mid = (at.qt + hi) >> 1;
+        if (cost_before(s, mid) <= in)
+          at.qt = mid;
+        else
+          hi = mid;
+      }
+    }
+    return at;
   }
-  // The unit of sequence s that the range starts in.
-  __host__ __device__ __forceinline__ void place() {
-    lo = plan_cut(c, line);
-    hi = plan_cut(c + 1, line);
-    const long long per = cost_of_head(s), past = lo - s.pre;
-    h = static_cast<int>(static_cast<float>(past) / static_cast<float>(per));  // off by one at most: h < 2^20
-    h -= h > 0 && h * per > past;
-    h += (h + 1) * per <= past;
-    a = s.pre + h * per;
-    qt = 0;
-#pragma unroll 1
-    while (a + cost_of(qt) <= lo) a += cost_of(qt++);
+  // The r-th unit (r < 32) behind `from` of the `count` entries of `list` (n = 0: not
+  // the kernel's); false: there is none.
+  static __host__ __device__ __forceinline__ bool find(const PlanSeq* list, int count, int H, PlanAt from, int r,
+                                                       PlanAt* to) {
+    for (; from.i < count; ++from.i) {
+      if (list[from.i].n == 0) continue;  // from.h, from.qt are 0 here
+      const int tiles = tiles_of(list[from.i]), x = from.qt + r;
+      const int dh = static_cast<uint32_t>(x) / static_cast<uint32_t>(tiles);
+      if (from.h + dh < H) {
+        *to = PlanAt{from.i, from.h + dh, x - dh * tiles};
+        return true;
+      }
+      r -= (H - from.h) * tiles - from.qt;  // no more than r
+      from.h = from.qt = 0;
+    }
+    return false;
+  }
+  // CTA c's (range [lo, hi)) piece of a unit; nks = 0: none of its steps are c's.
+  static __host__ __device__ __forceinline__ Piece piece(const PlanSeq& s, PlanAt at, int c, long long lo, long long hi,
+                                                         const PlanLine& line) {
+    const long long a = s.pre + at.h * cost_of_head(s) + cost_before(s, at.qt);
+    if (a >= hi) return Piece{0, 0, 0, 0, 0};
+    return plan_piece<Cost>(a, steps_of(s, at.qt), s.start / BK, c, lo, hi, line);
   }
 };
-using DecodeWalk64 = PlanWalk<DecodeCost, 64, 0, 1, kDecodeRows>;  // D = 64
-using DecodeWalk32 = PlanWalk<DecodeCost, 32, 0, 1, kDecodeRows>;  // D = 128
-using TileWalk = PlanWalk<TileCost, 64, kTileQueries, kDecodeRows + 1, 0x7fffffff>;
-using SimtWalk = PlanWalk<SimtCost, 32, kSimtQueries, 1, 0x7fffffff>;
+using DecodeUnits64 = PlanUnits<DecodeCost, 64, 0, 1, kDecodeRows>;  // D = 64
+using DecodeUnits32 = PlanUnits<DecodeCost, 32, 0, 1, kDecodeRows>;  // D = 128
+using TileUnits = PlanUnits<TileCost, 64, kTileQueries, kDecodeRows + 1, 0x7fffffff>;
+using SimtUnits = PlanUnits<SimtCost, 32, kSimtQueries, 1, 0x7fffffff>;
 
 #ifdef __CUDACC__
 
@@ -291,6 +284,7 @@ struct PlanState {
   long long pre;    // cost of the entries before `raw`
   int raw;          // the next entry to read
   int from, count;  // entry that the CTA's range starts in; entries at hand in `seqs`
+  PlanAt next;      // the unit to find next, in `seqs`
   union {
     long long sums[2][16];  // plan_begin: warps' sums (up to 16 warps)
     PlanSeq seqs[32];       // behind its next to last barrier
@@ -300,7 +294,7 @@ struct PlanState {
 // All threads of the CTA (a multiple of 32, up to 512): S, the CTAs that share
 // it, the entry that this CTA's range starts in and, of lists that the CTA
 // reads in one go, the entries from there on.  Ends with a barrier.
-template <typename Walk>
+template <typename Units>
 __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanState* st) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
   const int c = static_cast<int>(blockIdx.x);
@@ -313,8 +307,8 @@ __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanStat
 #pragma unroll 1
   for (int base = 0, turn = 0;; turn ^= 1) {
     s.n = 0;
-    if (base + tid < p.n) s = plan_read(p, base + tid, Walk::kLo, Walk::kHi, &bad);
-    mine = s.n > 0 ? Walk::cost_of_head(s) * p.H : 0;
+    if (base + tid < p.n) s = plan_read(p, base + tid, Units::kLo, Units::kHi, &bad);
+    mine = s.n > 0 ? Units::cost_of_head(s) * p.H : 0;
     const long long x = warp_scan(mine);
     if (lane == 31) st->sums[turn][warp] = x;
     __syncthreads();
@@ -327,7 +321,7 @@ __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanStat
     }
     base += nt;
     if (lo < 0 && base >= p.n) {
-      line = plan_line(upto, plan_ctas<typename Walk::Cost>(upto, most));
+      line = plan_line(upto, plan_ctas<typename Units::Cost>(upto, most));
       if (c >= line.ctas) break;
       lo = plan_cut(c, line);
       if (p.n > nt) {
@@ -367,7 +361,7 @@ __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanStat
 
 // One warp: the next entries, up to 32 (0: there are none), from entry st->raw
 // on, into st->seqs.
-template <typename Walk>
+template <typename Units>
 __device__ __forceinline__ int plan_fill(const PlanArgs& p, PlanState* st) {
   const int lane = threadIdx.x & 31;
   const int raw = st->raw, count = max(0, min(32, p.n - raw));
@@ -375,8 +369,8 @@ __device__ __forceinline__ int plan_fill(const PlanArgs& p, PlanState* st) {
   __syncwarp();
   PlanSeq s{};
   bool bad = false;
-  if (lane < count) s = plan_read(p, raw + lane, Walk::kLo, Walk::kHi, &bad);
-  const long long cost = s.n > 0 ? Walk::cost_of_head(s) * p.H : 0;
+  if (lane < count) s = plan_read(p, raw + lane, Units::kLo, Units::kHi, &bad);
+  const long long cost = s.n > 0 ? Units::cost_of_head(s) * p.H : 0;
   const long long upto = warp_scan(cost);
   s.pre = pre + upto - cost;
   if (lane < count) st->seqs[lane] = s;
@@ -388,19 +382,65 @@ __device__ __forceinline__ int plan_fill(const PlanArgs& p, PlanState* st) {
   return count;
 }
 
-// One warp, behind plan_begin: the walker on to this CTA's first unit or its
-// next; false: there is none.
-template <typename Walk>
-__device__ __forceinline__ bool plan_next(const PlanArgs& p, PlanState* st, Walk* walk, bool first) {
-  if (first) {
-    walk->seqs = st->seqs;
-    walk->count = st->count;
-    walk->line = st->line;
-    walk->H = p.H;
-    walk->c = static_cast<int>(blockIdx.x);
-    if (walk->c >= walk->line.ctas) return false;
+// A unit that a lane found.
+struct PlanFound {
+  PlanSeq s;
+  int h, qt;
+  Piece p;
+};
+
+// One warp, behind plan_begin: the CTA's next units, up to 32 (`first`: its
+// first ones), lane by lane; their number, 0 only where *last.  *last: there
+// are no more behind them.
+template <typename Units>
+__device__ __forceinline__ int plan_batch(const PlanArgs& p, PlanState* st, bool first, PlanFound* f, bool* last) {
+  const int lane = threadIdx.x & 31, c = static_cast<int>(blockIdx.x);
+  const PlanLine line = st->line;
+  *last = true;
+  if (c >= line.ctas) return 0;
+  const long long lo = plan_cut(c, line), hi = plan_cut(c + 1, line);
+  PlanAt from = st->next;
+  int count = st->count, found = 0;
+  bool fresh = first;
+#pragma unroll 1
+  for (;;) {
+    if (count == 0 && (count = plan_fill<Units>(p, st)) == 0) {
+      *last = true;
+      return 0;
+    }
+    if (fresh) from = Units::place(st->seqs[0], lo);
+    fresh = false;
+    PlanAt at{};
+    const bool any = Units::find(st->seqs, count, p.H, from, lane, &at);
+    f->p.nks = 0;
+    if (any) {
+      f->s = st->seqs[at.i];
+      f->h = at.h;
+      f->qt = at.qt;
+      f->p = Units::piece(f->s, at, c, lo, hi, line);
+    }
+    // The lanes with a unit come first: those behind the range's end, or the
+    // list's, have none.
+    found = __popc(__ballot_sync(0xffffffffu, f->p.nks > 0));
+    *last = __any_sync(0xffffffffu, any && f->p.nks == 0);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, any) && !*last) {  // the list is used up
+      *last = st->raw >= p.n;
+      count = 0;
+      from = PlanAt{0, 0, 0};
+    } else {
+      from.i = __shfl_sync(0xffffffffu, at.i, 31);
+      from.h = __shfl_sync(0xffffffffu, at.h, 31);
+      from.qt = __shfl_sync(0xffffffffu, at.qt, 31) + 1;  // past the head's last tile: find() goes on
+    }
+    if (found > 0 || *last) break;
   }
-  return walk->advance(first, [&] { return plan_fill<Walk>(p, st); });
+  if (lane == 0) {
+    st->next = from;
+    st->count = count;
+  }
+  __syncwarp();
+  return found;
 }
 
 #endif  // __CUDACC__

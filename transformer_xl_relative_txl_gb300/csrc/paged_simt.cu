@@ -49,10 +49,11 @@ struct Params {
   float* part;
 };
 
+constexpr int kRing = 64;  // units are found up to 32 at a time
+
 struct Shared {
   PlanState plan;
-  SimtWalk walk;
-  Unit unit[2];
+  Unit unit[kRing];
 };
 
 __host__ __device__ constexpr int padded(int D) { return (D + 3) / 4 * 4; }
@@ -85,31 +86,29 @@ __global__ void __launch_bounds__(kThreads, NG <= 2 ? kSimtPerSm : 1) paged_simt
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (tid == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
-  plan_begin<SimtWalk>(p.args, static_cast<int>(gridDim.x), &sh->plan);
+  plan_begin<SimtUnits>(p.args, static_cast<int>(gridDim.x), &sh->plan);
 
   bool bad = false;
+  int known = 0;  // warp 0: units found
+  bool ended = false;
   for (int un = -1;; ++un) {
     Unit w{};
     if (un >= 0) {
-      w = sh->unit[un & 1];
+      w = sh->unit[un % kRing];
       if (w.nks == 0) break;
     }
-    if (warp == 0) {  // unit un + 1; the walker rests in shared memory and works in registers
-      SimtWalk walk = sh->walk;
-      const bool found = plan_next(p.args, &sh->plan, &walk, un < 0);
-      __syncwarp();  // every lane has read the walker
-      if (lane == 0) {
-        Unit u{};
-        if (found) {
-          const PlanSeq& s = walk.s;
-          const int i0 = walk.qt * BQ;
-          u = Unit{walk.h,      s.tok0 + i0, min(BQ, s.n - i0),      walk.p.t0, walk.p.nks,   s.start + s.rows - s.n + i0,
-                   s.start,     s.start + s.rows - 1, s.slot, walk.p.index, walk.p.pieces};
-          if (u.pieces > 1 && u.index == 0) p.cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
-        }
-        sh->unit[(un + 1) & 1] = u;
-        sh->walk = walk;
+    if (warp == 0 && known == un + 1 && !ended) {  // units un + 1 ..., and behind the last one an empty one
+      PlanFound f{};
+      const int found = plan_batch<SimtUnits>(p.args, &sh->plan, un < 0, &f, &ended);
+      if (lane < found) {
+        const int i0 = f.qt * BQ;
+        const Unit u{f.h,       f.s.tok0 + i0,           min(BQ, f.s.n - i0), f.p.t0,    f.p.nks, f.s.start + f.s.rows - f.s.n + i0,
+                     f.s.start, f.s.start + f.s.rows - 1, f.s.slot,            f.p.index, f.p.pieces};
+        if (u.pieces > 1 && u.index == 0) p.cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
+        sh->unit[(known + lane) % kRing] = u;
       }
+      known += found;
+      if (ended && lane == 0) sh->unit[known % kRing] = Unit{};
     }
     if (un < 0) {
       __syncthreads();

@@ -59,7 +59,7 @@ constexpr int kOffR = kOffV + NV * kRowTile;
 constexpr int kOffRed = kOffR + NR * kRowTile;
 constexpr int kRedFloats = 2 * 2 * BM + 2 * BM;  // [step parity][half][row] maxima, [unit parity][row] sums
 constexpr int kOffBar = kOffRed + kRedFloats * 4;
-constexpr int kBarBytes = 2304;
+constexpr int kBarBytes = 5120;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -72,7 +72,6 @@ struct Bars {
   uint64_t xbar[4];  // row-max exchange of warps quad and quad+4 (64 arrivals per step)
   uint64_t lbar[4];  // row-sum hand-over at the end of a unit (32 arrivals)
   TileUnit units[kUnitRing];
-  TileWalk walk;
   PlanState plan;
   int any;  // the CTA has a unit
   uint32_t tmem_base;
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     tmem_relinquish();
   }
   if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
-  plan_begin<TileWalk>(p.args, static_cast<int>(gridDim.x), &bars->plan);
+  plan_begin<TileUnits>(p.args, static_cast<int>(gridDim.x), &bars->plan);
   if (warp != kLoaderWarp) {  // the loader has this barrier behind the first units
     tc_fence_before();
     __syncthreads();

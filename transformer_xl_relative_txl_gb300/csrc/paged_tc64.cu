@@ -77,7 +77,7 @@ constexpr int kOffP = kOffR + NR * kRowTile;    // P (bf16): 2 buffers, same lay
 constexpr int kOffRed = kOffP + 2 * kQTile;     // [unit parity][m, l][row] handed to the epilogue
 constexpr int kOffBias = kOffRed + 2 * 2 * BM * 4;  // per softmax warp: 32 dims of u, then of v (fp32)
 constexpr int kOffBar = kOffBias + 8 * 64 * 4;
-constexpr int kBarBytes = 2304;
+constexpr int kBarBytes = 5120;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -90,7 +90,6 @@ struct Bars {
   uint64_t lbar[4];   // per quadrant: the non-owning warp's (m, l) of a unit is in `red`
   uint64_t lfree[4];  // per quadrant: the epilogue has read it
   TileUnit units[kUnitRing];
-  TileWalk walk;
   PlanState plan;
   int any;            // the CTA has a unit
   uint32_t tmem_base;
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     tmem_relinquish();
   }
   if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
-  plan_begin<TileWalk>(p.args, static_cast<int>(gridDim.x), &bars->plan);
+  plan_begin<TileUnits>(p.args, static_cast<int>(gridDim.x), &bars->plan);
   if (warp != kLoaderWarp) {  // the loader has this barrier behind the first units
     tc_fence_before();
     __syncthreads();

@@ -2,11 +2,11 @@
 // CTA's roles work on, the loads of a key tile from its pages, the zeroing of
 // value rows that are not live, and the storing of results.
 //
-// The loader warp walks the CTA's units (paged_plan.cuh) and publishes each in
-// a ring in shared memory before it loads the unit's queries; every other role
-// reads a unit after a barrier that follows that load.  The loader is at most
-// two units ahead of the one whose operands are built, and that one at most
-// two ahead of any role, so a ring of eight never overtakes a reader.
+// The loader warp finds the CTA's units (paged_plan.cuh) and publishes them in
+// a ring in shared memory before it loads their queries; every other role
+// reads a unit after a barrier that follows that load.  It publishes up to 32
+// at a time, once fewer than two behind the one at hand are known, and no role
+// is more than four units behind it: a ring of 64 never overtakes a reader.
 #pragma once
 
 #include "paged_plan.cuh"
@@ -15,7 +15,7 @@
 
 namespace txl {
 
-constexpr int kUnitRing = 8;
+constexpr int kUnitRing = 64;
 
 struct TileUnit {
   int h;               // head
@@ -28,40 +28,38 @@ struct TileUnit {
   int next_h;          // head of the CTA's next unit, -1: none
 };
 
-// One warp.  The walker on to the CTA's unit k, which goes into the ring, and
-// to the unit before whose head follows it; false: there is no unit k.  The
-// first piece of a cut unit is noted for the kernel that joins the pieces.
+// One warp.  The CTA's next units into the ring, behind the `known` that it
+// has: how many there are then.  A unit is whole once the one behind it is
+// known, or known not to be (*ended).  The first piece of a cut unit is noted
+// for the kernel that joins the pieces.
 template <typename Bars>
-__device__ __forceinline__ bool publish_unit(Bars* bars, const PlanArgs& args, uint32_t k, PlanCut* cuts) {
-  // The walker works in registers: in place, each of its dependent steps would
-  // cost a shared-memory latency.
-  TileWalk walk = bars->walk;
-  const bool found = plan_next(args, &bars->plan, &walk, k == 0);
-  __syncwarp();  // every lane has read the walker
-  if ((threadIdx.x & 31) == 0) {
-    if (found) {
-      TileUnit& u = bars->units[k % kUnitRing];
-      const int i0 = walk.qt * kTileQueries;
-      const int nq = min(kTileQueries, walk.s.n - i0);
-      u.h = walk.h;
-      u.row0 = walk.s.tok0 + i0;
-      u.nq = nq;
-      u.t0 = walk.p.t0;
-      u.nks = walk.p.nks;
-      u.d0 = walk.s.start + walk.s.rows - walk.s.n + i0;
-      u.start = walk.s.start;
-      u.last = walk.s.start + walk.s.rows - 1;
-      u.slot = walk.s.slot;
-      u.index = walk.p.index;
-      u.pieces = walk.p.pieces;
-      if (walk.p.pieces > 1 && walk.p.index == 0)
-        cuts[blockIdx.x] = PlanCut{walk.s.tok0 + i0, nq, walk.h, walk.p.pieces};
-      bars->walk = walk;
-    }
-    if (k > 0) bars->units[(k - 1) % kUnitRing].next_h = found ? walk.h : -1;
+__device__ __forceinline__ uint32_t publish_units(Bars* bars, const PlanArgs& args, uint32_t known, PlanCut* cuts,
+                                                  bool* ended) {
+  const int lane = threadIdx.x & 31;
+  PlanFound f{};
+  const int found = plan_batch<TileUnits>(args, &bars->plan, known == 0, &f, ended);
+  int next_h = __shfl_down_sync(0xffffffffu, f.h, 1);
+  if (lane == found - 1) next_h = -1;
+  if (lane < found) {
+    TileUnit& u = bars->units[(known + lane) % kUnitRing];
+    const int i0 = f.qt * kTileQueries;
+    u.h = f.h;
+    u.row0 = f.s.tok0 + i0;
+    u.nq = min(kTileQueries, f.s.n - i0);
+    u.t0 = f.p.t0;
+    u.nks = f.p.nks;
+    u.d0 = f.s.start + f.s.rows - f.s.n + i0;
+    u.start = f.s.start;
+    u.last = f.s.start + f.s.rows - 1;
+    u.slot = f.s.slot;
+    u.index = f.p.index;
+    u.pieces = f.p.pieces;
+    u.next_h = next_h;
+    if (f.p.pieces > 1 && f.p.index == 0) cuts[blockIdx.x] = PlanCut{u.row0, u.nq, u.h, u.pieces};
   }
+  if (lane == 0 && known > 0) bars->units[(known - 1) % kUnitRing].next_h = found > 0 ? f.h : -1;
   __syncwarp();
-  return found;
+  return known + found;
 }
 
 // The P.V issuer's warp: zeroes the rows of the landed value tile t that are
@@ -144,8 +142,7 @@ struct TileMaps {
 
 // The loader warp of both kernels: K, V and r tiles (and the raw q tiles) of
 // the CTA's units in order, and the units published.  It has the CTA's barrier
-// behind the first two units, which are whole then; bars->any says whether
-// there is one.
+// behind the first units; bars->any says whether there is one.
 //
 // The lanes share a step's work: lanes 0-3 have the boxes of its K tile, 4-7
 // those of a V tile, 8 its r tile.  A 64-row tile of keys is one box of a page,
@@ -235,10 +232,10 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     holds = false;
   };
 
-  // `known` units are published, all whole but the last; the tiles of unit
-  // `un`, of which t is the next, are under way.
+  // `known` units are published, all whole but the last (`ended`: the last
+  // too); the tiles of unit `un`, of which t is the next, are under way.
   uint32_t known = 0, un = 0xffffffffu;
-  bool more = true, begun = false;
+  bool ended = false, begun = false;
   int h = 0, d0 = 0, start = 0, last = 0, t = 0, t0 = 0, tend = 0, id = 0;
   const int* row = nullptr;
   auto live = [&](int tile) {
@@ -246,8 +243,8 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     return boxed && x <= last && x + (1 << log_box) > start;
   };
   for (;;) {
-    if (more && (more = publish_unit(bars, p.args, known, p.cuts))) ++known;
-    if (known == 1 && more) continue;  // the first unit is whole once the second is known
+    // Unit un + 1 whole.
+    while (!ended && known < un + 3) known = publish_units(bars, p.args, known, p.cuts, &ended);
     if (!begun) {
       begun = true;
       if (lane == 0) bars->any = known > 0;
