@@ -15,8 +15,9 @@ int pieces_of(int H, int n, const int* start, const int* rows, const int* fresh,
   std::vector<PlanSeq> list(n);
   long long total = 0;
   for (int i = 0; i < n; ++i) {
-    list[i] = PlanSeq{total, 0, fresh[i], i, start[i], rows[i], i};
-    if (fresh[i] > 0) total += Units::cost_of_head(list[i]) * H;
+    list[i] = PlanSeq{total, 0, 0, fresh[i], i, start[i], rows[i]};
+    if (fresh[i] > 0) list[i].per = Units::cost_of_head(list[i]);
+    total += list[i].per * H;
   }
   const PlanLine line = plan_line(total, plan_ctas<typename Units::Cost>(total, most));
   int count = 0;
@@ -107,10 +108,12 @@ size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16) {
   return plan_space(nullptr, T, D, bf16, nullptr);
 }
 
-// fp32: the CUDA cores.  bf16: sequences of more than 4 new tokens by tiles of
-// 128 queries, the others by the decode kernel, which starts in the tiles'
-// tail; then the joins.  (max_new is the host's bound: the lengths themselves
-// are on the device, and either kernel finds its own.)
+// fp32: the CUDA cores.  bf16: sequences of up to 4 new tokens by the decode
+// kernel, the others by tiles of 128 queries, which start in its tail; then the
+// joins.  (max_new is the host's bound: the lengths themselves are on the
+// device, and either kernel finds its own.  The other way round, the decode
+// kernel of a batch without short sequences found that out behind the tiles: 3
+// us more.)
 cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_t stream) {
   PlanSpace s;
   plan_space(a.workspace, a.T, a.D, a.bf16, &s);
@@ -123,8 +126,8 @@ cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_
     return launch_paged_join(a, JoinPart{s.simt.cuts, s.simt.part, kSimtPerSm * sms, kSimtQueries}, none, stream);
   }
   const bool tiles = a.max_new > kDecodeRows;
-  if (tiles) e = launch_tiles(a, s, sms, wc, stream);
-  if (e == cudaSuccess) e = launch_paged_decode(a, s, sms, tiles, wc, stream);
+  e = launch_paged_decode(a, s, sms, tiles, wc, stream);
+  if (e == cudaSuccess && tiles) e = launch_tiles(a, s, sms, wc, stream);
   if (e != cudaSuccess) return e;
   return launch_paged_join(a, JoinPart{s.decode.cuts, s.decode.part, kDecodePerSm * sms, kDecodeRows},
                            tiles ? JoinPart{s.tiles.cuts, s.tiles.part, sms, kTileQueries} : none, stream);

@@ -54,7 +54,7 @@ struct Cfg {
   static constexpr int kQuery = kDecodeRows * D * 2 + 2 * D * 4;  // a unit's rows of q, u and v
   static constexpr int kOffQ = kOffPart + 2 * kWarps * kDecodeRows * kRow * 4;
   static constexpr int kOffBar = kOffQ + 2 * kQuery;
-  static constexpr int kBarBytes = 1408;
+  static constexpr int kBarBytes = 1792;
   static constexpr int kSmem = kOffBar + kBarBytes + 1024;
   using Units = PlanUnits<DecodeCost, BK, 0, 1, kDecodeRows>;  // DecodeUnits64, DecodeUnits32
 };
@@ -70,7 +70,7 @@ struct Params {
   PlanCut* cuts;
   float* part;
   unsigned long long wait_ns;
-  bool behind_tiles;
+  bool ahead_of_tiles;
 };
 
 // A unit as the producer publishes it; nks 0: the CTA has no more.
@@ -154,12 +154,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     fence_mbar_init();
   }
   __syncthreads();
-  // Behind the tile kernel this one need not wait: that kernel lets it start
-  // after its own wait.  What it waits for then, at its end, is that the
-  // kernels behind it may take both as complete.
-  if (!p.behind_tiles) grid_dep_wait();
+  grid_dep_wait();
+  // The tile kernel behind this one needs what this one does and no more: its
+  // CTAs start as this one's end.
   grid_dep_launch_dependents();
   if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
+  if (p.ahead_of_tiles) {  // most batches of longer entries have none of these
+    bool any = false;
+    for (int i = threadIdx.x; i < p.args.n; i += blockDim.x) {
+      const int n = p.args.cu[i + 1] - p.args.cu[i];
+      any |= n >= 1 && n <= kDecodeRows;
+    }
+    if (!__syncthreads_or(any)) return;
+  }
   plan_begin<typename C::Units>(p.args, static_cast<int>(gridDim.x), &bars->plan);
   const uint64_t wait_ns = p.wait_ns;
 
@@ -282,8 +289,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       const uint32_t n = s + ((g - 1 - s) / NS) * NS;
       mbar_wait_own(&bars->full[s], (n / NS) & 1, wait_ns);
     }
-    if (p.behind_tiles) grid_dep_wait();
-    return;
+      return;
   }
 
   // =============================== consumers ================================
@@ -475,11 +481,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     }
   }
   if (!ok && lane == 0) report_timeout(abort, p.args.status);
-  if (p.behind_tiles) grid_dep_wait();
 }
 
 template <int D, bool O_BF16>
-cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_tiles, const WaitCtl& wc,
+cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool ahead_of_tiles, const WaitCtl& wc,
                    cudaStream_t stream) {
   using C = Cfg<D>;
   PFN_cuTensorMapEncodeTiled_v12000 encode = api_tensor_map_encoder();
@@ -509,7 +514,7 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_
     if (!enc(&tm_r, a.r, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   const Params p{plan_args(a, wc.status), static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse,
-                 a.scale * 1.4426950408889634f, s.decode.cuts, s.decode.part, wc.limit_ns, behind_tiles};
+                 a.scale * 1.4426950408889634f, s.decode.cuts, s.decode.part, wc.limit_ns, ahead_of_tiles};
   auto kern = paged_decode_kernel<D, O_BF16>;
   static unsigned configured = 0;  // one bit per device ordinal < 32
   int dev = 0;
@@ -525,9 +530,9 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_tiles, const WaitCtl& wc,
+cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool ahead_of_tiles, const WaitCtl& wc,
                                 cudaStream_t stream) {
-  auto run = [&](auto f) { return f(a, s, sms, behind_tiles, wc, stream); };
+  auto run = [&](auto f) { return f(a, s, sms, ahead_of_tiles, wc, stream); };
   if (a.D == 64) return a.o_bf16 ? run(launch<64, true>) : run(launch<64, false>);
   return a.o_bf16 ? run(launch<128, true>) : run(launch<128, false>);
 }

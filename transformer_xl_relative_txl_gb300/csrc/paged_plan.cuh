@@ -36,7 +36,8 @@ constexpr int kTileQueries = 128, kSimtQueries = 16;
 // One sequence.
 struct __align__(16) PlanSeq {
   long long pre;  // cost of the sequences before it
-  int tok0, n, slot, start, rows, index;
+  long long per;  // cost of one head
+  int tok0, n, slot, start, rows;
 };
 
 template <int W, int U>
@@ -56,34 +57,41 @@ __host__ __device__ __forceinline__ int plan_steps(int start, int x, int BK) {
   return x < start ? 1 : x / BK - start / BK + 1;
 }
 
-// The line of costs: its length and how the CTAs share it.  (Divided once: a
-// 64-bit division takes over 100 instructions.)
+// The line of costs: its length and how the CTAs share it.  (What a CTA does
+// at its head is a chain of dependent instructions, so one division by ctas is
+// all there is, in 32 bits where the length allows.)
 struct PlanLine {
   long long total, each;  // each: floor(total / ctas)
   int ctas, rest;
+  float rate, inv;        // ctas / total, 1 / ctas
 };
 __host__ __device__ __forceinline__ PlanLine plan_line(long long total, int ctas) {
-  PlanLine l{total, 0, ctas, 0};
+  PlanLine l{total, 0, ctas, 0, 0.f, 0.f};
   if (ctas > 0) {
-    l.each = total / ctas;
+    l.each = total >> 32 ? total / ctas : static_cast<uint32_t>(total) / static_cast<uint32_t>(ctas);
     l.rest = static_cast<int>(total - l.each * ctas);
+    l.inv = 1.f / static_cast<float>(ctas);
+    l.rate = static_cast<float>(ctas) / static_cast<float>(total);
   }
   return l;
 }
 
-// Where CTA c's range begins: floor(c total / ctas).
+// Where CTA c's range begins: floor(c total / ctas) = c each + floor(c rest / ctas).
 __host__ __device__ __forceinline__ long long plan_cut(int c, const PlanLine& l) {
-  return c * l.each + static_cast<uint32_t>(c * l.rest) / static_cast<uint32_t>(l.ctas);  // c, rest < ctas < 2^15
+  const int x = c * l.rest;  // c, rest < ctas < 2^10: exact in fp32, the estimate off by one at most
+  int q = static_cast<int>(static_cast<float>(x) * l.inv);
+  const int r = x - q * l.ctas;
+  q += (r >= l.ctas) - (r < 0);
+  return c * l.each + q;
 }
 
 // The CTA whose range of the line holds position x: the largest c with
 // plan_cut(c) <= x.  The estimate is off by one at most.
 __host__ __device__ __forceinline__ int plan_owner(long long x, const PlanLine& l) {
-  int c = static_cast<int>(static_cast<float>(x) / static_cast<float>(l.total) * static_cast<float>(l.ctas));
+  int c = static_cast<int>(static_cast<float>(x) * l.rate);
   c = c < l.ctas ? c : l.ctas - 1;
-  c -= plan_cut(c, l) > x;
-  c += c + 1 < l.ctas && plan_cut(c + 1, l) <= x;
-  return c;
+  const bool less = plan_cut(c, l) > x, more = c + 1 < l.ctas && plan_cut(c + 1, l) <= x;
+  return c + more - less;
 }
 
 // CTAs that share a line of length `total`: a CTA's range holds at least two
@@ -120,10 +128,9 @@ __host__ __device__ __forceinline__ Piece plan_piece(long long a, int steps, int
   p.index = 0;
   p.pieces = 1;
   if (p.nks > 0 && p.nks < steps) {
-    if (from > 0) p.first = plan_owner(s0 + Cost::kStep - 1, line);
-    const int last = to == steps ? c : plan_owner(s0 + static_cast<long long>(Cost::kStep) * steps - 1, line);
+    p.first = plan_owner(s0 + Cost::kStep - 1, line);
     p.index = c - p.first;
-    p.pieces = last - p.first + 1;
+    p.pieces = plan_owner(s0 + static_cast<long long>(Cost::kStep) * steps - 1, line) - p.first + 1;
   }
   return p;
 }
@@ -167,18 +174,20 @@ struct PlanUnits {
       // the first y0 tiles end before the first live row (rows < n): a step each
       int y0 = m < s.start ? (s.start - m) / (TILE == 0 ? 1 : TILE) : 0;
       y0 = y0 < whole ? y0 : whole;
-      const long long k = whole - y0;
-      steps += y0 + k * (1 - s.start / BK);
+      const int k = whole - y0;
+      steps += y0;
       if (k > 0) {
-        const int first = m + y0 * TILE + TILE - 1;  // no less than start
-        if (TILE >= BK) {                            // floor(x / BK) grows by TILE / BK a tile
+        const uint32_t first = m + y0 * TILE + TILE - 1;  // no less than start
+        const int base = static_cast<int>(static_cast<uint32_t>(s.start) / BK) - 1;
+        if (TILE >= BK) {  // floor(x / BK) grows by TILE / BK a tile
           constexpr int kBy = TILE / BK;
-          steps += k * (first / BK) + kBy * (k * (k - 1) / 2);
+          steps += static_cast<long long>(k) * (static_cast<int>(first / BK) - base) +
+                   kBy * (static_cast<long long>(k) * (k - 1) >> 1);
         } else {  // floor(x / BK) = floor((b + y) / 2)
           static_assert(TILE == 0 || TILE >= BK || 2 * TILE == BK, "half a key step a tile");
-          auto halves = [](long long z) { return z < 1 ? 0 : (z - 1) * (z - 1) / 4; };  // sum of floor(j / 2), j < z
-          const long long b = first / (TILE == 0 ? 1 : TILE);
-          steps += halves(b + k) - halves(b);
+          auto halves = [](int z) { return z < 1 ? 0 : static_cast<long long>(z - 1) * (z - 1) >> 2; };  // sum of floor(j / 2), j < z
+          const int b = first / (TILE == 0 ? 1 : TILE);
+          steps += halves(b + k) - halves(b) - static_cast<long long>(k) * base;
         }
       }
     }
@@ -190,8 +199,13 @@ struct PlanUnits {
 
   // The unit of sequence s (list[0]) that position x of the line lies in.
   static __host__ __device__ __forceinline__ PlanAt place(const PlanSeq& s, long long x) {
-    const long long per = cost_of_head(s), past = x - s.pre;
-    PlanAt at{0, static_cast<int>(static_cast<float>(past) / static_cast<float>(per)), 0};  // off by one at most: h < 2^20
+    const long long per = s.per, past = x - s.pre;
+#ifdef __CUDA_ARCH__
+    const float ratio = __fdividef(static_cast<float>(past), static_cast<float>(per));
+#else
+    const float ratio = static_cast<float>(past) / static_cast<float>(per);
+#endif
+    PlanAt at{0, static_cast<int>(ratio), 0};  // off by one at most: h < 2^20
     at.h -= at.h > 0 && at.h * per > past;
     at.h += (at.h + 1) * per <= past;
     if (TILE != 0) {
@@ -227,7 +241,7 @@ struct PlanUnits {
   // CTA c's (range [lo, hi)) piece of a unit; nks = 0: none of its steps are c's.
   static __host__ __device__ __forceinline__ Piece piece(const PlanSeq& s, PlanAt at, int c, long long lo, long long hi,
                                                          const PlanLine& line) {
-    const long long a = s.pre + at.h * cost_of_head(s) + cost_before(s, at.qt);
+    const long long a = s.pre + at.h * s.per + (TILE == 0 ? 0 : cost_before(s, at.qt));
     if (a >= hi) return Piece{0, 0, 0, 0, 0};
     return plan_piece<Cost>(a, steps_of(s, at.qt), s.start / BK, c, lo, hi, line);
   }
@@ -251,7 +265,6 @@ struct PlanArgs {
 // Entry i; n = 0 where it is refused (noted in *bad) or not of lo .. hi tokens.
 __device__ __forceinline__ PlanSeq plan_read(const PlanArgs& p, int i, int lo, int hi, bool* bad) {
   PlanSeq s{};
-  s.index = i;
   s.tok0 = p.cu[i];
   const int n = p.cu[i + 1] - s.tok0;
   s.slot = p.slots[i];
@@ -270,7 +283,7 @@ __device__ __forceinline__ PlanSeq plan_read(const PlanArgs& p, int i, int lo, i
 
 __device__ __forceinline__ long long warp_scan(long long x) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
+#pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
@@ -308,14 +321,15 @@ __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanStat
   for (int base = 0, turn = 0;; turn ^= 1) {
     s.n = 0;
     if (base + tid < p.n) s = plan_read(p, base + tid, Units::kLo, Units::kHi, &bad);
-    mine = s.n > 0 ? Units::cost_of_head(s) * p.H : 0;
+    if (s.n > 0) s.per = Units::cost_of_head(s);
+    mine = s.n > 0 ? s.per * p.H : 0;
     const long long x = warp_scan(mine);
     if (lane == 31) st->sums[turn][warp] = x;
     __syncthreads();
     long long before = upto + x - mine;
-#pragma unroll 1
-    for (int w = 0; w < nw; ++w) {
-      const long long y = st->sums[turn][w];
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const long long y = w < nw ? st->sums[turn][w] : 0;
       before += w < warp ? y : 0;
       upto += y;
     }
@@ -370,7 +384,8 @@ __device__ __forceinline__ int plan_fill(const PlanArgs& p, PlanState* st) {
   PlanSeq s{};
   bool bad = false;
   if (lane < count) s = plan_read(p, raw + lane, Units::kLo, Units::kHi, &bad);
-  const long long cost = s.n > 0 ? Units::cost_of_head(s) * p.H : 0;
+  if (s.n > 0) s.per = Units::cost_of_head(s);
+  const long long cost = s.n > 0 ? s.per * p.H : 0;
   const long long upto = warp_scan(cost);
   s.pre = pre + upto - cost;
   if (lane < count) st->seqs[lane] = s;
@@ -501,9 +516,8 @@ struct JoinPart {
   int ctas, rows;
 };
 cudaError_t launch_paged_join(const PagedAttn& a, const JoinPart& x, const JoinPart& y, cudaStream_t stream);
-// behind_tiles: launched behind the tile kernel, whose end it need not wait
-// for before its own.
-cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool behind_tiles, const WaitCtl& wc,
+// ahead_of_tiles: the tile kernel follows, which starts in this one's tail.
+cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool ahead_of_tiles, const WaitCtl& wc,
                                 cudaStream_t stream);
 cudaError_t launch_paged_simt(const PagedAttn& a, const PlanSpace& s, int sms, unsigned int* status,
                               cudaStream_t stream);

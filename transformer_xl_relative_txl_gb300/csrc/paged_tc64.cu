@@ -145,10 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     bars->abort = 0;
     fence_mbar_init();
   }
-  // The kernels ahead on the stream have completed from here on.
-  grid_dep_wait();
-  // The decode kernel behind this one needs what this one does and no more: its
-  // CTAs start as this one's end.
+  // The decode kernel ahead let this one start once the kernels ahead of it had
+  // completed, and that is all this one needs.  It waits for that kernel at its
+  // end: the kernel behind takes both as complete then.
   grid_dep_launch_dependents();
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
@@ -618,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (threadIdx.x == 0) grid_dep_wait();
 }
 
 template <bool O_BF16>

@@ -246,6 +246,13 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     // Unit un + 1 whole.
     while (!ended && known < un + 3) known = publish_units(bars, p.args, known, p.cuts, &ended);
     if (!begun) {
+      if (known > 0) {  // the first tile's pages, on their way meanwhile
+        const TileUnit& w = bars->units[0];
+        const int x = w.t0 * kStepKeys + off;
+        if (boxed && x <= w.last && x + (1 << log_box) > w.start)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(
+              p.args.book.table + static_cast<size_t>(w.slot) * p.args.book.max_pages + (x >> log_page)));
+      }
       begun = true;
       if (lane == 0) bars->any = known > 0;
       tc_fence_before();
