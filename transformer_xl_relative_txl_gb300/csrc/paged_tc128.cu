@@ -384,8 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         const int lim = d0 - BN * kt + a - 32 * half;    // column k visible iff low <= k <= lim
         const int low = start - BN * kt - 32 * half;
         if (low > 0 || d0 - BN * kt + quad * 32 - 32 * half < 31) {  // some lane of the warp masks
+          const uint32_t v = visible_columns(low, lim);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (k >= low && k <= lim) ? x[k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) x[k] = v >> k & 1 ? x[k] : -INFINITY;
         }
         float t3[11];
 #pragma unroll

@@ -442,8 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           add_window(s1, bd1, x1);
         }
         if (diag || low > 0) {
+          const uint32_t v0 = visible_columns(low, lim), v1 = visible_columns(low - 32, lim - 32);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = (k >= low && k <= lim) ? x[k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) {
+            x[k] = v0 >> k & 1 ? x[k] : -INFINITY;
+            x[32 + k] = v1 >> k & 1 ? x[32 + k] : -INFINITY;
+          }
         }
         // Lazy running max over the step's 64 scores (log2 units).
         float t3[22];
