@@ -277,7 +277,7 @@ def test_every_step_has_one_cta(lib, kind, D):
     rng = np.random.default_rng(kind + D)
     BK = 32 if kind == 2 or (kind == 0 and D == 128) else 64
     tile = (0, 128, 16)[kind]
-    unit = (3, 5, 1)[kind]  # cost of a unit besides its steps, in half steps
+    unit = (4, 7, 3)[kind]  # cost of a unit besides its steps, in half steps
     for trial in range(120):
         n = int(rng.integers(1, [2, 5, 60][trial % 3] + 1))
         H = int(rng.integers(1, 9))

@@ -22,6 +22,11 @@
 // query t's rows of r are addressed upside down by ldmatrix, and the product
 // accumulates on top of the content term; the other queries' columns of the
 // right-hand side are zero for it.
+//
+// Measured: 64 sequences of one token over 300 to 4500 rows (16 heads of 64,
+// 757 MB) 125 us, 6.1 TB/s, 89% of a copy's rate; 48 over 1600 to 8100 rows (8
+// heads of 128, pages of 32 rows, 1.02 GB) 175 us, 5.8 TB/s, 86%.  What is left
+// is the CTAs' head and tail, about 8 us, and the join behind them.
 #include <cmath>
 #include <cstdint>
 
@@ -197,8 +202,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     uint32_t g = 0, units = 0;
     bool ok = true, bad = false;
     // The next unit and its queries, on their way while its tiles are loaded:
-    // read by the consumers at the head of the unit, a global load's latency
-    // per unit was most of their time (decode batch: 163 us).
+    // read by the consumers at the head of the unit, a global load's latency a
+    // unit made 163 us of the 125 that 64 sequences take (see above).
     auto publish = [&](int nks) {
       const int s = units & 1;
       ok = warp_wait(&bars->q_empty[s], ((units >> 1) & 1) ^ 1, wait_ns, abort);

@@ -11,9 +11,10 @@
 // that are not whole units.
 //
 // Each CTA finds S and the start of its own range by itself, at its head
-// (plan_begin: all of its threads sum the sequences' costs), and then reads the
-// sequences of its range 32 at a time (plan_fill).  That takes about 2 us where
-// a kernel that made a list for all CTAs took 5 and a launch.
+// (plan_begin: all of its threads sum the sequences' costs); then a warp finds
+// its units, 32 at a time (plan_batch).  That takes about 4 us of the 90 that 22
+// sequences of 512 tokens over 512 rows take (8 heads), half of it two trips to
+// L2, where a kernel that made a list for all CTAs took 5 and a launch.
 //
 // Three kernels divide their own sequences: those of up to kDecodeRows new
 // tokens (bf16), those of more (bf16, tiles of 128 queries), all (fp32, tiles
@@ -46,10 +47,12 @@ struct PlanCost {
   static constexpr int kUnit = U;  // cost of a unit besides its steps
 };
 // In half key steps: what a unit costs besides its steps is set by its
-// queries' load and its epilogue.
-using DecodeCost = PlanCost<2, 3>;
-using TileCost = PlanCost<2, 5>;
-using SimtCost = PlanCost<2, 1>;
+// queries' load and its epilogue.  (Measured on ragged batches: tiles 90.3 us at
+// 5, 88.1 at 7, 87.8 at 8, which is worse for 8 sequences of 768 tokens, D =
+// 128; fp32 27.0 at 1, 24.9 at 3, 28.1 at 4; decode within 0.5% from 2 to 6.)
+using DecodeCost = PlanCost<2, 4>;
+using TileCost = PlanCost<2, 7>;
+using SimtCost = PlanCost<2, 3>;
 
 // Key steps of `BK` rows from the first live row to row x (page rows counted
 // from the slot's first page); at least one.
@@ -360,7 +363,7 @@ __device__ __forceinline__ void plan_begin(const PlanArgs& p, int most, PlanStat
   }
   __syncthreads();
   if (p.n > nt || c >= line.ctas) return;
-  // (Read again by the walking warp, they cost 2 us of every call.)
+  // (Read again by the warp that finds the units, they cost 2 us of every call.)
   const int from = st->from, k = tid - from, count = min(32, p.n - from);
   if (k >= 0 && k < count) {
     st->seqs[k] = s;

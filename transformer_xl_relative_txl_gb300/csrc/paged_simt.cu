@@ -5,7 +5,7 @@
 //   o_t = softmax(s[t,.]) V,  m = rows - new tokens
 //
 // A unit is 16 queries of one (sequence, head), a key step 32 rows; the units'
-// steps are divided evenly over 4 CTAs per SM (paged_plan.cuh), so that few
+// steps are divided evenly over 3 CTAs per SM (paged_plan.cuh), so that few
 // long sequences fill the GPU too.  The distances that a step needs are 47
 // consecutive rows of r, d = m + t - j for 16 t and 32 j.
 //
@@ -14,7 +14,10 @@
 // (keys and r rows by lane, queries broadcast).  Rows in shared memory are
 // padded to an odd number of 16-byte pieces, so that a quarter warp's reads of
 // consecutive rows meet different banks.  The step's loads are coalesced rows,
-// 16 in flight per lane, hidden behind the other CTAs of the SM.
+// 16 in flight per lane, hidden behind the other CTAs of the SM.  A ragged
+// batch of 5 sequences of up to 130 tokens over up to 700 rows (4 heads, D = 40)
+// takes 25 us: few steps a CTA, each a chain of a page id, its rows and two
+// barriers.  (4 CTAs an SM leave 128 registers a thread, which spill: 28 us.)
 #include <cmath>
 #include <cstdint>
 

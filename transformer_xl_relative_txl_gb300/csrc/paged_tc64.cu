@@ -49,9 +49,9 @@ constexpr int kPvWarp = 10;
 constexpr int kQrWarp = 11;
 constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, three MMA issuers)
 // Register split (launch: 168 per thread, 384 x 168 = 64512): softmax
-// warpgroups 216, producer warpgroup 72; 2*128*216 + 128*72 = 64512.  (With 224
-// and 56 the loader spills: 107 us instead of 103 for 22 sequences of 512
-// tokens over 512 rows, 8 heads.)
+// warpgroups 224, producer warpgroup 56; 2*128*224 + 128*56 = 64512.  (At 216
+// the softmax spills, at 56 the search for units, once per CTA, by 19 words;
+// both splits time the same.)
 constexpr uint32_t kRegsSoftmax = 224;
 constexpr uint32_t kRegsProducer = 56;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");

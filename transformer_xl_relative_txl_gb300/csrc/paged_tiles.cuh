@@ -73,10 +73,9 @@ __device__ __forceinline__ uint32_t visible_columns(int low, int lim) {
 }
 
 // The P.V issuer's warp: zeroes the rows of the landed value tile t that are
-// not live: weight 0 times a leftover that is no number would not be 0.  (By
-// the softmax warps, behind their step's weights, the code alone cost their
-// loop 7%: 94 us instead of 88 for 22 sequences of 512 tokens over 512 rows, 8
-// heads.)
+// not live: weight 0 times a leftover that is no number would not be 0.  (In the
+// softmax warps, behind their step's weights, the code alone cost their loop
+// 7%, though almost no step runs it.)
 template <int D>
 __device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8_t* stage, int lane) {
   const int x0 = t * kStepKeys;
@@ -169,7 +168,7 @@ struct TileMaps {
 // while a K stage is free as soon as its score MMA is done; with V(t) beside
 // K(t), K would wait for the P.V of step t - NS and land just in time (D = 128,
 // two stages: 167 us instead of 145 for 152 units of 100 steps; at D = 64, with
-// four, a V tile that trails costs 2%).  AHEAD: the raw q tile of a unit is
+// four, 102 us so and 108 with a V tile that trails).  AHEAD: the raw q tile of a unit is
 // loaded behind the first step of the unit before (D = 64: its operands have
 // two buffers and are built during that unit); otherwise at the head of its
 // own, behind the last V tile of the unit before.

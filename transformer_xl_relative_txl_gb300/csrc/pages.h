@@ -1,4 +1,4 @@
-// Internal interface of the paged memory (pages.cu, paged_simt.cu) to its C
+// Internal interface of the paged memory (pages.cu, paged_attn.cu) to its C
 // entry points (pages_api.cu).  Arguments are validated by the caller.
 #pragma once
 
@@ -18,7 +18,7 @@ struct PageBook {
   int n_slots, max_pages, n_pages, page_rows;
 };
 
-constexpr int kMaxSlots = 16384;  // the reserve kernel keeps two ints per slot in shared memory
+constexpr int kMaxSlots = 16384;  // the reserve kernel keeps an int per slot and one per entry in shared memory
 
 cudaError_t launch_pages_reserve(const PageBook& b, const int* slots, const int* cu, int n, int* granted,
                                  int* copy_src, int* copy_dst, unsigned int* status, cudaStream_t stream);
