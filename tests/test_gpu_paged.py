@@ -172,6 +172,25 @@ def test_float32(txl, D):
     attend_case(txl, np.random.default_rng(D), spans, counts, 16, 2, D, F32, tail=2)
 
 
+MANY = {  # more than 32 units a block, more entries than threads, entries of the other kernel and empty ones between
+    "decode": (BF, 64, 16, 700, lambda rng: rng.choice([0, 1, 1, 1, 2, 7])),
+    "decode128": (BF, 128, 16, 700, lambda rng: rng.choice([0, 1, 1, 1, 4])),
+    "tiles": (BF, 64, 16, 450, lambda rng: rng.choice([0, 1, 5, 6, 9, 130], p=[.1, .1, .3, .3, .19, .01])),
+    "tiles128": (BF, 128, 16, 450, lambda rng: rng.choice([0, 3, 5, 8], p=[.05, .05, .5, .4])),
+    "float32": (F32, 8, 32, 560, lambda rng: rng.choice([0, 1, 3, 20])),
+}
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_many_units(txl, case):
+    dtype, D, H, n, draw = MANY[case]
+    rng = np.random.default_rng(n + D)
+    counts = [int(draw(rng)) for _ in range(n)]
+    counts[40:120] = [0] * 80  # the lists that a warp reads are empty for a while
+    spans = [(int(rng.integers(16)), c + int(rng.integers(0, 60))) for c in counts]
+    attend_case(txl, rng, spans, counts, 16, H, D, dtype, tail=3)
+
+
 @pytest.mark.parametrize("dtype,D,counts", [(BF, 64, [1, 1]), (BF, 128, [3, 2]), (BF, 64, [90, 20]), (BF, 128, [70, 9]),
                                             (F32, 24, [5, 1])])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
@@ -582,6 +601,47 @@ def test_a_stream_of_its_own(txl):
     txl.txl_relattn_forward_paged(*args, **kw, stream=s)
     s.synchronize()
     assert torch.equal(args[9], want)
+
+
+def test_refused_arguments(txl):
+    """What the binding turns away before any launch."""
+    rng = np.random.default_rng(5)
+    args, kw = attend_case(txl, rng, [(3, 40), (0, 9)], [2, 1], 16, 2, 64, BF)
+    q, k, v, book, slots, cu, r, u, vb, o, ws = args
+
+    def attend(**change):
+        names = "q k_pages v_pages book slots cu r bias_u bias_v o workspace".split()
+        full = dict(zip(names, args))
+        full.update(kw)
+        full.update(change)
+        return txl.txl_relattn_forward_paged(**full)
+
+    before = o.clone()
+    for change in (dict(slots=slots.long()), dict(slots=slots.cpu()), dict(cu=cu[:-1]), dict(cu=slots), dict(q=q[:, :1]),
+                   dict(q=q.float()), dict(r=r.float()), dict(bias_u=u.to(BF)), dict(bias_v=vb[:1]), dict(o=o[:-1]),
+                   dict(lse=torch.zeros(2, 2, device="cuda")), dict(k_pages=k[:-1], v_pages=v[:-1]), dict(v_pages=v[:-1]),
+                   dict(k_pages=k.transpose(1, 2)), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)),
+                   dict(slots=torch.stack([slots, slots], 1)[:, 0]), dict(book=dict(book, rows=book["rows"].long())),
+                   dict(book=dict(book, table=book["table"][0])), dict(book=dict(book, refs=book["refs"][:-1])),
+                   dict(max_new=2 ** 31), dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            attend(**change)
+    with pytest.raises(TypeError):
+        attend(book=list(book.values()))
+    with pytest.raises(KeyError):
+        attend(book={x: book[x] for x in ("table", "start", "rows")})
+    with pytest.raises(TypeError):
+        attend(scale="1")
+    with pytest.raises(txl.TxlError):
+        attend(workspace=ws[:16])
+    with pytest.raises(txl.TxlError):
+        txl.txl_pages_free(book, 24, slots)  # page rows: no power of two
+    with pytest.raises(ValueError):
+        txl.txl_pages_append(book, k, v, slots, cu, slots.clone(), slots.clone(), None, k[0], v[0])
+    torch.cuda.synchronize()
+    assert torch.equal(o, before) and txl.txl_get_device_status() == 0
+    attend()
+    assert torch.equal(o, before)
 
 
 def test_offsets_past_32_bits(txl):

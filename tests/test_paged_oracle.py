@@ -262,6 +262,12 @@ def test_binding_refuses(lib):
         lib.txl_pages_free(dict(book, start=z(3)), 16, z(1))
     with pytest.raises(ValueError):
         lib.txl_pages_copy(torch.zeros(8, 1, 16, 4), torch.zeros(8, 1, 16, 5), z(1), z(1))
+    with pytest.raises(TypeError):  # no tensor
+        lib.txl_pages_reserve(book, 16, [0], z(2), z(1), z(1), z(1))
+    with pytest.raises(TypeError):
+        lib.txl_pages_compact(book, 16, None, z(8), z(8), z(1))
+    with pytest.raises(TypeError):
+        lib.txl_relattn_forward_paged(z(1), z(1), z(1), book, 0, z(2), z(1), z(1), z(1), z(1), z(1))
 
 
 def steps(start, rows, n, first, count, BK):

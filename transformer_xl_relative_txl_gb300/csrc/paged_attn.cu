@@ -24,14 +24,20 @@ int pieces_of(int H, int n, const int* start, const int* rows, const int* fresh,
   for (int c = 0, x = 0; c < line.ctas; ++c) {
     while (x + 1 < n && list[x + 1].pre <= plan_cut(c, line)) ++x;
     const long long lo = plan_cut(c, line), hi = plan_cut(c + 1, line);
-    PlanAt at = Units::place(list[x], lo);
-    at.i = x;
-    for (int r = 0; Units::find(list.data(), n, H, at, r, &at); r = 1) {
-      const Piece p = Units::piece(list[at.i], at, c, lo, hi, line);
-      if (p.nks == 0) break;
-      if (count == cap) return -1;
-      const int row[10] = {c, at.i, at.h, at.qt, p.t0, p.nks, p.first, p.index, p.pieces, plan_place(c, p.index)};
-      std::copy(row, row + 10, out + 10 * static_cast<size_t>(count++));
+    PlanAt from = Units::place(list[x], lo);
+    from.i = x;
+    for (bool more = true; more;) {  // 32 at a time, as a warp does
+      PlanAt at{};
+      for (int r = 0; r < 32 && more; ++r) {
+        more = Units::find(list.data(), n, H, from, r, &at);
+        if (!more) break;
+        const Piece p = Units::piece(list[at.i], at, c, lo, hi, line);
+        if (!(more = p.nks > 0)) break;
+        if (count == cap) return -1;
+        const int row[10] = {c, at.i, at.h, at.qt, p.t0, p.nks, p.first, p.index, p.pieces, plan_place(c, p.index)};
+        std::copy(row, row + 10, out + 10 * static_cast<size_t>(count++));
+      }
+      from = PlanAt{at.i, at.h, at.qt + 1};
     }
   }
   return count;
