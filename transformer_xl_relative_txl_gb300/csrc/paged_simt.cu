@@ -139,6 +139,14 @@ __global__ void __launch_bounds__(kThreads, NG <= 2 ? kSimtPerSm : 1) paged_simt
     for (int y = 0; y < 4; ++y) mx[y] = -INFINITY, sum[y] = 0.f;
     const int end = min(w.last, w.d0 + w.nq - 1);  // last row any query sees
 
+    // Pages have at least 16 rows, a power of two, and steps are counted from a
+    // page's first: each half of a step lies in one page.
+    auto page_of = [&](int t, int half) {  // of rows 16 half .. 16 half + 15 of step t
+      const int x = t * BK + 16 * half;
+      return x + 15 >= w.start && x <= end ? table[x >> p.log_page] : 0;
+    };
+    int ids[2] = {page_of(w.t0, 0), page_of(w.t0, 1)};
+
     for (int t = w.t0; t < w.t0 + w.nks; ++t) {
       const int x0 = t * BK;
       // Rows of keys and values: warp + 4 y.  Rows that no query sees are not
@@ -150,37 +158,52 @@ __global__ void __launch_bounds__(kThreads, NG <= 2 ? kSimtPerSm : 1) paged_simt
         const int x = x0 + warp + 4 * y;
         int id = -1;
         if (x >= w.start && x <= end) {
-          id = table[x >> p.log_page];
+          id = ids[y / (BK / 8)];
           if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.args.book.n_pages)) bad = true, id = -1;
         }
         on[y] = id >= 0;
         off[y] = static_cast<size_t>(max(id, 0)) * page + head +
                  static_cast<size_t>(x & ((1 << p.log_page) - 1)) * D;
       }
+      if (t + 1 < w.t0 + w.nks) {  // on their way while this step runs
+        ids[0] = page_of(t + 1, 0);
+        ids[1] = page_of(t + 1, 1);
+      }
       const int dist0 = w.d0 - x0 - (BK - 1);  // distance of row 0 of rs
       __syncthreads();                         // the step before has read the tiles
-      for (int d = lane; d < D; d += 32) {
-        float kx[BK / 4], vx[BK / 4], rx[BR / 4 + 1];
+      // 64 dimensions at a time: a step of up to that many waits once.
+      for (int d0 = lane; d0 < D; d0 += 64) {
+        float kx[2][BK / 4], vx[2][BK / 4], rx[2][BR / 4 + 1];
 #pragma unroll
-        for (int y = 0; y < BK / 4; ++y) {
-          kx[y] = on[y] ? p.kp[off[y] + d] : 0.f;
-          vx[y] = on[y] ? p.vp[off[y] + d] : 0.f;
+        for (int c = 0; c < 2; ++c) {
+          const int d = d0 + 32 * c;
+          const bool in = d < D;
+#pragma unroll
+          for (int y = 0; y < BK / 4; ++y) {
+            kx[c][y] = in && on[y] ? p.kp[off[y] + d] : 0.f;
+            vx[c][y] = in && on[y] ? p.vp[off[y] + d] : 0.f;
+          }
+#pragma unroll
+          for (int y = 0; y < BR / 4 + 1; ++y) {
+            const int row = warp + 4 * y, dist = dist0 + row;
+            rx[c][y] = in && row < BR && dist >= 0 && dist < p.args.n_r
+                           ? __ldg(p.r + (static_cast<size_t>(dist) * H + w.h) * D + d)
+                           : 0.f;
+          }
         }
 #pragma unroll
-        for (int y = 0; y < BR / 4 + 1; ++y) {
-          const int row = warp + 4 * y, dist = dist0 + row;
-          rx[y] = row < BR && dist >= 0 && dist < p.args.n_r
-                      ? __ldg(p.r + (static_cast<size_t>(dist) * H + w.h) * D + d)
-                      : 0.f;
-        }
+        for (int c = 0; c < 2; ++c) {
+          const int d = d0 + 32 * c;
+          if (d >= D) continue;
 #pragma unroll
-        for (int y = 0; y < BK / 4; ++y) {
-          ks[(warp + 4 * y) * S + d] = kx[y];
-          vs[(warp + 4 * y) * S + d] = vx[y];
-        }
+          for (int y = 0; y < BK / 4; ++y) {
+            ks[(warp + 4 * y) * S + d] = kx[c][y];
+            vs[(warp + 4 * y) * S + d] = vx[c][y];
+          }
 #pragma unroll
-        for (int y = 0; y < BR / 4 + 1; ++y)
-          if (warp + 4 * y < BR) rs[(warp + 4 * y) * S + d] = rx[y];
+          for (int y = 0; y < BR / 4 + 1; ++y)
+            if (warp + 4 * y < BR) rs[(warp + 4 * y) * S + d] = rx[c][y];
+        }
       }
       __syncthreads();
       float z[4] = {0.f, 0.f, 0.f, 0.f};

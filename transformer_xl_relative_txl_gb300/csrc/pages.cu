@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t used_mask(const PageBook& b, int base) {
 // entries read anew in each phase and 64-bit divisions in append.  64 single
 // tokens: 9 us, about 3 a launch.)
 struct Ask {  // what an entry asks for
-  int slot, count, have, need, last;  // need: pages (0 where it asks for none or is refused)
+  int slot, rows, count, have, need, last;  // need: pages (0 where it asks for none or is refused)
   bool ok, shared, idle;              // shared: its last page, which is copied; idle: a valid entry without rows
 };
 
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* 
 
   auto ask = [&](int i) {
     const Slot sl = read_slot(b, slots[i]);
-    Ask a{sl.s, cu[i + 1] - cu[i], 0, 0, -1, false, false, false};
+    Ask a{sl.s, sl.rows, cu[i + 1] - cu[i], 0, 0, -1, false, false, false};
     if (!sl.ok) return a;
     a.idle = a.count == 0;
     const long long end = static_cast<long long>(sl.start) + sl.rows;
@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* 
   for (int i = tid; i < n; i += kBlock) {
     const Ask a = SMALL ? own : mine(i);
     const bool given = a.ok && (a.need == 0 || upto[i] <= lim);
+    if (SMALL) own.ok = given;  // from here on
     granted[i] = given ? a.count : 0;
     copy_src[i] = given && a.shared ? a.last : -1;
     copy_dst[i] = -1;
@@ -277,6 +278,13 @@ __global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* 
     }
   }
   __syncthreads();
+  if (SMALL) {
+    if (tid < n && own.ok) {
+      b.rows[own.slot] = own.rows + own.count;
+      if (own.shared) atomicSub(&b.refs[own.last], 1);
+    }
+    return;
+  }
   for (int i = tid; i < n; i += kBlock) {
     const int rows = granted[i], from = copy_src[i];
     if (rows > 0) b.rows[slots[i]] += rows;
@@ -489,20 +497,18 @@ __global__ void __launch_bounds__(128) free_kernel(PageBook b, const int* __rest
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int i = blockIdx.x;
-  const int s = slots[i];
-  bool ok = s >= 0 && s < b.n_slots;
-  for (int j = threadIdx.x; ok && j < i; j += blockDim.x) ok = slots[j] != s;
-  ok = __syncthreads_and(ok);
-  // Only the entry that names the slot first reads its state, which no other
-  // CTA then writes.
-  Slot a{s, 0, 0, false};
-  if (ok) a = read_slot(b, s);
-  ok = __syncthreads_and(a.ok);
-  if (!ok) {
+  const int s = slots[i], want = keep == nullptr ? 0 : keep[i];
+  // The entry that names the slot first changes it, which no other does; what a
+  // later one reads here, at whatever time, it does not use.
+  const Slot a = read_slot(b, s);
+  bool first = true;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) first &= slots[j] != s;
+  // (Every thread has read the state behind this barrier.)
+  if (!__syncthreads_and(first) || !__syncthreads_and(a.ok)) {
     if (threadIdx.x == 0) report_pages(status);
     return;
   }
-  const int kept = min(a.rows, max(keep == nullptr ? 0 : keep[i], 0));
+  const int kept = min(a.rows, max(want, 0));
   const int begin = a.start + (a.rows - kept);  // in range: start + rows <= max_pages * page_rows
   const int pages = ceil_div(static_cast<long long>(a.start) + a.rows, b.page_rows);
   const int dead = kept > 0 ? begin / b.page_rows : pages;
