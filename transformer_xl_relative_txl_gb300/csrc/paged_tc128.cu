@@ -303,47 +303,51 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     uint32_t gt = 0, un = 0, nQ = 0;
     bool ok = true;
 
-    // (q + u), (q + v) for this thread's row of a unit of head h: bf16,
-    // 128B-swizzled K-major shared-memory tiles.
-    auto build_q = [&](int h) -> bool {
+    // (q + u), (q + v) for this thread's row of unit k: bf16, 128B-swizzled
+    // K-major shared-memory tiles.
+    auto build_q = [&](uint32_t k) -> bool {
       if (!warp_wait(&bars->q_full, nQ & 1, wait_ns, abort)) return false;
+      const int h = bars->units[k % kUnitRing].h;
       const float* bu = p.bias_u + h * D;
       const float* bv = p.bias_v + h * D;
-      uint32_t qu[D / 2], qv[D / 2];
-#pragma unroll
+      // (The MMAs that read the unit before's are complete.)  A loop of no more
+      // than four, as everything that a step seldom runs: the step's own code
+      // has to stay in the instruction cache beside it.  (8 sequences of 768
+      // tokens over 768 rows: 96.7 us with one at a time, 92.3 with four, 92.7
+      // with all 16.)
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
         const int kc = c / 8, cc = c % 8;
         const int off = kc * kQChunk + (a / 8) * 1024 + (a % 8) * 128 + ((cc ^ (a % 8)) * 16);
         const uint4 raw = *reinterpret_cast<const uint4*>(sQ + off);
         const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t qu[4], qv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int d = c * 8 + 2 * e;
+          const int d = 8 * c + 2 * e;
           const float x0 = bf16_lo(w4[e]), x1 = bf16_hi(w4[e]);
-          qu[c * 4 + e] = pack_bf16x2((x0 + __ldg(bu + d)) * p.qsign, (x1 + __ldg(bu + d + 1)) * p.qsign);
-          qv[c * 4 + e] = pack_bf16x2((x0 + __ldg(bv + d)) * p.qsign, (x1 + __ldg(bv + d + 1)) * p.qsign);
+          qu[e] = pack_bf16x2((x0 + __ldg(bu + d)) * p.qsign, (x1 + __ldg(bu + d + 1)) * p.qsign);
+          qv[e] = pack_bf16x2((x0 + __ldg(bv + d)) * p.qsign, (x1 + __ldg(bv + d + 1)) * p.qsign);
         }
+        *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[0], qu[1], qu[2], qu[3]);
+        *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[0], qv[1], qv[2], qv[3]);
       }
       mbar_arrive(&bars->q_empty);
       ++nQ;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const int kc = c / 8, cc = c % 8;
-        const int off = kc * kQChunk + (a / 8) * 1024 + (a % 8) * 128 + ((cc ^ (a % 8)) * 16);
-        *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[4 * c], qu[4 * c + 1], qu[4 * c + 2], qu[4 * c + 3]);
-        *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[4 * c], qv[4 * c + 1], qv[4 * c + 2], qv[4 * c + 3]);
-      }
       fence_proxy_async_smem();
       mbar_arrive(&bars->q_ready);
       return true;
     };
 
-    if (any && half == 1) ok = build_q(bars->units[0].h);
-
     while (any && ok) {
       // Unit 0 is published before the CTA's first barrier, a later one before
-      // its queries are loaded, which its first scores tell.
-      if (un > 0 && !(ok = warp_wait(&bars->s_full[gt & 1], (gt >> 1) & 1, wait_ns, abort))) break;
+      // its queries are loaded: one half builds the operands from them, the
+      // other learns of it by the first scores.
+      if (half == 1) {
+        if (!(ok = build_q(un))) break;
+      } else if (un > 0 && !(ok = warp_wait(&bars->s_full[gt & 1], (gt >> 1) & 1, wait_ns, abort))) {
+        break;
+      }
       const TileUnit* unit = &bars->units[un % kUnitRing];
       const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
       float m_use = -INFINITY;  // running max in log2 units (lazy)
@@ -461,22 +465,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         const bool seen = m_use != -INFINITY;  // the row sees a key of this piece
         const float inv_l = seen ? 1.f / l : 0.f;
         const float lse2 = seen ? m_use + __log2f(l) : -INFINITY;
-        float ov[D];
-#pragma unroll
+        const TileUnit w = *unit;
+        store_lse(w, a, lse2, p.lse, p.part, p.args.T, D);
+#pragma unroll 1
         for (int oc = 0; oc < D / 32; ++oc) {
           uint32_t tmp[32];
+          float ov[32];
           tmem_ld32(tmem + lane_base + kColO + oc * 32, tmp);
           tmem_wait_ld(tmp);
+          if (oc == D / 32 - 1) warp_arrive_tc(&bars->o_free);
 #pragma unroll
-          for (int n = 0; n < 32; ++n) ov[oc * 32 + n] = __uint_as_float(tmp[n]) * inv_l;
+          for (int n = 0; n < 32; ++n) ov[n] = __uint_as_float(tmp[n]) * inv_l;
+          store_columns<D, O_BF16>(w, a, oc, ov, p.o, p.part, p.args.H);
         }
-        warp_arrive_tc(&bars->o_free);
-        if (unit->pieces > 1)
-          store_piece<D>(*unit, a, ov, lse2, p.part);
-        else
-          store_row<D, O_BF16>(*unit, a, ov, lse2, p.o, p.lse, p.args.T, p.args.H);
-      } else if (unit->next_h >= 0 && !(ok = build_q(unit->next_h))) {
-        break;
       }
       if (unit->next_h < 0) break;
       gt = g0 + nks;

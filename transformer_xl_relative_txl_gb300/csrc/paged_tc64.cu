@@ -339,19 +339,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       sb_w[32 + lane] = bv_l;
       __syncwarp();
       if (!warp_wait(&bars->q_full, nQ & 1, wait_ns, abort)) return false;
-      uint4 raw[4];
-#pragma unroll
+      // Short code, as with everything that a step seldom runs: the step's own
+      // has to stay in the instruction cache beside it (22 sequences of 512
+      // tokens over 512 rows: 93 us with these loops and the epilogue's
+      // unrolled, 87 so.  One copy of this code instead of three, by a loop
+      // that also turns where a warp has no step: 95).
+#pragma unroll 2
       for (int j = 0; j < 4; ++j) {
         const int c = 4 * par + j;
-        raw[j] = *reinterpret_cast<const uint4*>(sQ + (a / 8) * 1024 + (a % 8) * 128 + ((c ^ (a % 8)) * 16));
-      }
-      warp_arrive(&bars->q_empty);
-      ++nQ;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 4 * par + j;
-        const int off = buf * kQTile + (a / 8) * 1024 + (a % 8) * 128 + ((c ^ (a % 8)) * 16);
-        const uint32_t w4[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        const int at = (a / 8) * 1024 + (a % 8) * 128 + ((c ^ (a % 8)) * 16), off = buf * kQTile + at;
+        const uint4 raw = *reinterpret_cast<const uint4*>(sQ + at);
+        const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
         const float4 u0 = *reinterpret_cast<const float4*>(sb_w + 8 * j);
         const float4 u1 = *reinterpret_cast<const float4*>(sb_w + 8 * j + 4);
         const float4 v0 = *reinterpret_cast<const float4*>(sb_w + 32 + 8 * j);
@@ -368,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[0], qu[1], qu[2], qu[3]);
         *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[0], qv[1], qv[2], qv[3]);
       }
+      warp_arrive(&bars->q_empty);
+      ++nQ;
       warp_arrive_smem(&bars->q_ready);
       __syncwarp();  // sb_w is rewritten by the next build
       return true;
@@ -556,39 +556,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         const float inv_l = seen ? 1.f / l : 0.f;
         const float lse2 = seen ? m + __log2f(l) : -INFINITY;
         const float c0 = a0 * inv_l, c1 = a1 * inv_l;
-        // Read both accumulators into registers and hand them back to the PV
-        // issuer before the stores.
-        float ov[D];
-#pragma unroll
+        // 32 columns at a time, the accumulators handed back to the PV issuer
+        // behind the last.
+        const TileUnit w = *unit;
+        const bool boxed = O_BF16 && w.pieces == 1 && 32 * quad + 32 <= w.nq;
+        store_lse(w, a, lse2, p.lse, p.part, p.args.T, D);
+#pragma unroll 1
         for (int oc = 0; oc < D / 32; ++oc) {
-          uint32_t t0[32], t1[32];
-          if (has0) {
-            tmem_ld32(tmem + lane_base + kColO + par * D + oc * 32, t0);
-            tmem_wait_ld(t0);
-          }
-          if (has1) {
-            tmem_ld32(tmem + lane_base + kColO + (par ^ 1) * D + oc * 32, t1);
-            tmem_wait_ld(t1);
-          }
+          float ov[32];
+          {
+            uint32_t t0[32], t1[32];
+            if (has0) {
+              tmem_ld32(tmem + lane_base + kColO + par * D + oc * 32, t0);
+              tmem_wait_ld(t0);
+            }
+            if (has1) {
+              tmem_ld32(tmem + lane_base + kColO + (par ^ 1) * D + oc * 32, t1);
+              tmem_wait_ld(t1);
+            }
 #pragma unroll
-          for (int n = 0; n < 32; ++n)
-            ov[oc * 32 + n] =
-                (has0 ? __uint_as_float(t0[n]) * c0 : 0.f) + (has1 ? __uint_as_float(t1[n]) * c1 : 0.f);
+            for (int n = 0; n < 32; ++n)
+              ov[n] = (has0 ? __uint_as_float(t0[n]) * c0 : 0.f) + (has1 ? __uint_as_float(t1[n]) * c1 : 0.f);
+          }
+          if (boxed) {
+            // bf16 rows into this warp's quadrant of its own P buffer (free
+            // until its next step: the last PV that read it is complete), then
+            // one TMA store of the 32-row box, all of them the unit's.
+            uint8_t* orow_s = sP + par * kQTile + (a / 8) * 1024 + (a % 8) * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(orow_s + (((4 * oc + c) ^ (a % 8)) * 16)) =
+                  make_uint4(pack_bf16x2(ov[8 * c], ov[8 * c + 1]), pack_bf16x2(ov[8 * c + 2], ov[8 * c + 3]),
+                             pack_bf16x2(ov[8 * c + 4], ov[8 * c + 5]), pack_bf16x2(ov[8 * c + 6], ov[8 * c + 7]));
+          } else {
+            store_columns<D, O_BF16>(w, a, oc, ov, p.o, p.part, p.args.H);
+          }
         }
         warp_arrive_tc(&bars->o_free);
-        const TileUnit w = *unit;
-        if (w.pieces > 1) {
-          store_piece<D>(w, a, ov, lse2, p.part);
-        } else if (O_BF16 && 32 * quad + 32 <= w.nq) {
-          // bf16 rows into this warp's quadrant of its own P buffer (free
-          // until its next step: the last PV that read it is complete), then
-          // one TMA store of the 32-row box, all of them the unit's.
-          uint8_t* orow_s = sP + par * kQTile + (a / 8) * 1024 + (a % 8) * 128;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            *reinterpret_cast<uint4*>(orow_s + ((c ^ (a % 8)) * 16)) =
-                make_uint4(pack_bf16x2(ov[8 * c], ov[8 * c + 1]), pack_bf16x2(ov[8 * c + 2], ov[8 * c + 3]),
-                           pack_bf16x2(ov[8 * c + 4], ov[8 * c + 5]), pack_bf16x2(ov[8 * c + 6], ov[8 * c + 7]));
+        if (boxed) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -596,11 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
             bulk_commit_group();
           }
           store_pending = true;
-          if (p.lse != nullptr)
-            p.lse[static_cast<size_t>(w.h) * p.args.T + w.row0 + a] =
-                lse2 == -INFINITY ? -INFINITY : lse2 * 0.69314718055994531f;
-        } else {
-          store_row<D, O_BF16>(w, a, ov, lse2, p.o, p.lse, p.args.T, p.args.H);
         }
       }
       if (!has_next) break;

@@ -91,40 +91,45 @@ __device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8
   __syncwarp();
 }
 
-// Row `a` of a unit (lane `lane` of quadrant `quad`), o normalised by its own
-// sum, lse2 its log2-domain lse (-inf: no visible key), to the output; rows
-// past the unit's queries are not written.
-template <int D, bool O_BF16>
-__device__ __forceinline__ void store_row(const TileUnit& u, int a, const float (&ov)[D], float lse2, void* o,
-                                          float* lse, int T, int H) {
-  if (a >= u.nq) return;
-  const size_t at = (static_cast<size_t>(u.row0 + a) * H + u.h) * D;
-  if (O_BF16) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o) + at);
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      dst[c] = make_uint4(pack_bf16x2(ov[8 * c], ov[8 * c + 1]), pack_bf16x2(ov[8 * c + 2], ov[8 * c + 3]),
-                          pack_bf16x2(ov[8 * c + 4], ov[8 * c + 5]), pack_bf16x2(ov[8 * c + 6], ov[8 * c + 7]));
-  } else {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(o) + at);
-#pragma unroll
-    for (int c = 0; c < D / 4; ++c) dst[c] = make_float4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
-  }
-  if (lse != nullptr)
+// Results of a unit, o normalised by its own sum, lse2 its log2-domain lse
+// (-inf: no visible key).  A whole unit's go to the output, rows past its
+// queries are not written; a piece's go to the workspace, joined by the kernel
+// behind this one (paged_join.cu).  (With the last piece to arrive joining in
+// this kernel, its warps held up the CTA's softmax: 131 us instead of 90 for 22
+// sequences of 512 tokens over 512 rows, 8 heads, where every CTA has two
+// pieces.)
+__device__ __forceinline__ float* piece_of(const TileUnit& u, float* part, int D) {
+  return part + plan_place(static_cast<int>(blockIdx.x), u.index) * static_cast<size_t>(plan_part(kTileQueries, D));
+}
+__device__ __forceinline__ void store_lse(const TileUnit& u, int a, float lse2, float* lse, float* part, int T, int D) {
+  if (u.pieces > 1)
+    piece_of(u, part, D)[kTileQueries * D + a] = lse2;
+  else if (a < u.nq && lse != nullptr)
     lse[static_cast<size_t>(u.h) * T + u.row0 + a] = lse2 == -INFINITY ? -INFINITY : lse2 * 0.69314718055994531f;
 }
-
-// A piece's row goes to the workspace, joined by the kernel behind this one
-// (paged_join.cu).  (With the last piece to arrive joining in this kernel, its
-// warps held up the CTA's softmax: 131 us instead of 90 for 22 sequences of
-// 512 tokens over 512 rows, 8 heads, where every CTA has two pieces.)
-template <int D>
-__device__ __forceinline__ void store_piece(const TileUnit& u, int a, const float (&ov)[D], float lse2, float* part) {
-  float* mine = part + plan_place(static_cast<int>(blockIdx.x), u.index) * static_cast<size_t>(plan_part(kTileQueries, D));
-  float4* po = reinterpret_cast<float4*>(mine + a * D);
+// Columns 32 oc .. 32 oc + 31 of row a.
+template <int D, bool O_BF16>
+__device__ __forceinline__ void store_columns(const TileUnit& u, int a, int oc, const float (&ov)[32], void* o,
+                                              float* part, int H) {
+  float* to = nullptr;
+  if (u.pieces > 1) {
+    to = piece_of(u, part, D) + a * D;
+  } else {
+    if (a >= u.nq) return;
+    const size_t at = (static_cast<size_t>(u.row0 + a) * H + u.h) * D;
+    if (O_BF16) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o) + at) + 4 * oc;
 #pragma unroll
-  for (int c = 0; c < D / 4; ++c) po[c] = make_float4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
-  mine[kTileQueries * D + a] = lse2;
+      for (int c = 0; c < 4; ++c)
+        dst[c] = make_uint4(pack_bf16x2(ov[8 * c], ov[8 * c + 1]), pack_bf16x2(ov[8 * c + 2], ov[8 * c + 3]),
+                            pack_bf16x2(ov[8 * c + 4], ov[8 * c + 5]), pack_bf16x2(ov[8 * c + 6], ov[8 * c + 7]));
+      return;
+    }
+    to = static_cast<float*>(o) + at;
+  }
+  float4* dst = reinterpret_cast<float4*>(to) + 8 * oc;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) dst[c] = make_float4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
 }
 
 // Kernel parameters common to both.
