@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(PageBook b, int* __rest
   __shared__ int2 sums[2][32];
   const int cap = b.n_pages + 1;
   constexpr int kTile = kBlock * kPerThread;
+  __shared__ uint32_t masks[kBlock];
   int live = 0, turn = 0;
   const uint32_t used0 = used_mask(b, 0);
   for (int base = 0; base < b.n_pages; base += kTile) {
@@ -563,14 +564,16 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(PageBook b, int* __rest
   for (int base = 0; base < b.n_pages; base += kTile) {
     const int p0 = base + threadIdx.x * kPerThread;
     const uint32_t used = base == 0 ? used0 : used_mask(b, base);
-    uint32_t hole = 0, move = 0;
-#pragma unroll
-    for (int q = 0; q < kPerThread; ++q) {
-      const int p = p0 + q;
-      if (p >= b.n_pages) continue;
-      const bool u = used >> q & 1;
-      hole |= (!u && p < live ? 1u : 0u) << q;
-      move |= (u && p >= live ? 1u : 0u) << q;
+    // Bits of this thread's pages: in the pool, before N.
+    auto upto = [&](int end) { return 0xffffu >> (kPerThread - max(0, min(kPerThread, end - p0))); };
+    const uint32_t hole = ~used & upto(live), move = used & ~upto(live) & upto(b.n_pages);
+    masks[threadIdx.x] = used;
+    __syncthreads();
+#pragma unroll 4
+    for (int q = 0; q < kPerThread; ++q) {  // a warp's pages side by side
+      const int e = q * kBlock + threadIdx.x, p = base + e;
+      if (p >= b.n_pages) break;
+      const bool u = masks[e / kPerThread] >> (e % kPerThread) & 1;
       if (!u || p < live) new_id[p] = u ? p : -1;
     }
     const Scan x = block_scan(make_int2(__popc(hole), __popc(move)), cap, sums, turn);
@@ -578,19 +581,33 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(PageBook b, int* __rest
     int m = moved + x.at.y - __popc(move);
     holes += x.all.x;
     moved += x.all.y;
-    for (; hole != 0; hole &= hole - 1) copy_dst[h++] = p0 + __ffs(hole) - 1;
-    for (; move != 0; move &= move - 1) copy_src[m++] = p0 + __ffs(move) - 1;
+    for (uint32_t x = hole; x != 0; x &= x - 1) copy_dst[h++] = p0 + __ffs(x) - 1;
+    for (uint32_t x = move; x != 0; x &= x - 1) copy_src[m++] = p0 + __ffs(x) - 1;
   }
   __syncthreads();
   // As many holes before N as live pages past it: N pages are live.
-  for (int k = threadIdx.x; k < b.n_pages; k += kBlock) {
-    if (k < moved) {
-      const int a = copy_src[k], z = copy_dst[k];
-      new_id[a] = z;
-      b.refs[z] = b.refs[a];
-      b.refs[a] = 0;
-    } else {
-      copy_src[k] = copy_dst[k] = -1;
+  // No page is both, so a thread's four moves are loaded together.
+  constexpr int U = 4;
+  for (int k0 = threadIdx.x; k0 < b.n_pages; k0 += U * kBlock) {
+    int a[U], z[U], refs[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kBlock;
+      a[u] = k < moved ? copy_src[k] : -1;
+      z[u] = k < moved ? copy_dst[k] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) refs[u] = a[u] >= 0 ? b.refs[a[u]] : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kBlock;
+      if (a[u] >= 0) {
+        new_id[a[u]] = z[u];
+        b.refs[z[u]] = refs[u];
+        b.refs[a[u]] = 0;
+      } else if (k < b.n_pages) {
+        copy_src[k] = copy_dst[k] = -1;
+      }
     }
   }
   if (threadIdx.x == 0) *count = moved;
