@@ -780,7 +780,7 @@ TXL_API int txl_debug_unit_plan(int B, int H, int W, int M, int ctas, int* table
 TXL_API int txl_debug_bwd_pairs_work(int B, int W, int M, int H, int split_qt, int* n_ctas, int* n_tiles,
                                      int* ctas, int cap_ctas, int* tiles, int cap_tiles);
 /* Test hook, host only: how txl_relattn_forward_paged divides its work over
- * `ctas` CTAs.  kind 0: the decode kernel (entries of up to 4 tokens; key
+ * `ctas` (at most 1023) CTAs.  kind 0: the decode kernel (entries of up to 4 tokens; key
  * steps of 64 rows at D = 64, 32 at D = 128), 1: the kernel for longer
  * entries (tiles of 128 queries, key steps of 64 rows), 2: the fp32 kernel
  * (tiles of 16 queries, key steps of 32 rows).  n sequences of rows[i] live

@@ -238,7 +238,7 @@ int txl_relattn_forward_paged(const void* q, const void* k_pages, const void* v_
 
 int txl_debug_paged_pieces(int kind, int D, int H, int n, const int* start, const int* rows, const int* n_new,
                            int ctas, int* out, int cap) {
-  if (kind < 0 || kind > 2 || (kind == 0 && D != 64 && D != 128) || H <= 0 || n < 0 || ctas <= 0 || cap < 0 || start == nullptr ||
+  if (kind < 0 || kind > 2 || (kind == 0 && D != 64 && D != 128) || H <= 0 || n < 0 || ctas <= 0 || ctas > 1023 || cap < 0 || start == nullptr ||
       rows == nullptr || n_new == nullptr || out == nullptr)
     return -2;
   for (int i = 0; i < n; ++i)
