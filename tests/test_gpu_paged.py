@@ -157,6 +157,9 @@ CHUNKS = [
     (64, 2, 64, [(0, 0), (0, 40), (60, 70)], [0, 40, 0]),
     (16, 2, 64, [(3, 100), (0, 0), (15, 30)], [150, 40, 200]),
     (16, 2, 128, [(3, 100), (0, 0), (15, 30)], [150, 40, 200]),
+    # many tiles a head, cut in the middle of one
+    (64, 1, 64, [(9, 3500), (0, 50)], [2401, 50]),
+    (32, 1, 128, [(9, 3300), (0, 50)], [2111, 2]),
 ]
 
 
