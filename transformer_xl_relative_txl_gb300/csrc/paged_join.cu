@@ -4,14 +4,17 @@
 //   o = sum_c w_c o_c / sum_c w_c,   lse = top + log2 sum_c w_c,
 // the pieces taken in key order.
 //
-// A CTA has up to 32 rows of the unit whose first piece a CTA of the attention
+// A CTA has up to 16 rows of the unit whose first piece a CTA of the attention
 // kernel had, if any.  Bound by latency: the pieces lie in L2, at most one unit
 // per CTA of that kernel is cut, and most have few pieces.  So a thread takes
 // its values of a row through all pieces with a running maximum and sum of its
 // own, the loads of several pieces, and of their lse, in flight at once: behind
 // the cut's own load one trip to L2, no barrier.  (Maxima, sums and rows in
 // three passes over the pieces, with barriers between: 3.4 us of the 10.4 of a
-// single token over 512 rows.)
+// single token over 512 rows, 9.0 so.)  Units of tiles are nearly all cut in
+// two: 2 pieces in flight and 16 rows a CTA, 86.0 us for 22 sequences of 512
+// tokens over 512 rows against 87.0 with 4 and 32; fp32's have more, 21.7 us
+// with 4 in flight against 22.9 (5 sequences of up to 130 tokens).
 #include <cmath>
 #include <cstdint>
 
@@ -23,7 +26,7 @@
 namespace txl {
 namespace {
 
-constexpr int kThreads = 128, kRows = 32;
+constexpr int kThreads = 128, kRows = 16;
 
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const JoinPart x, 
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int D = DC > 0 ? DC : d_arg;
-  // Blocks of x first, each unit's blocks of 32 rows together.
+  // Blocks of x first, each unit's blocks of 16 rows together.
   const int bx = (x.rows + kRows - 1) / kRows, by = (y.rows + kRows - 1) / kRows;
   const bool second = static_cast<int>(blockIdx.x) >= x.ctas * bx;
   const JoinPart& j = second ? y : x;
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const JoinPart x, 
   if (rows <= kDecodeRows)  // up to 128 values a row of four
     join_rows<1, 8, TO, V>(j, cut, first, r0, rows, o, lse, T, H, D);
   else
-    join_rows<4, 4, TO, V>(j, cut, first, r0, rows, o, lse, T, H, D);
+    join_rows<2, (DC > 0 ? 2 : 4), TO, V>(j, cut, first, r0, rows, o, lse, T, H, D);
 }
 
 }  // namespace
