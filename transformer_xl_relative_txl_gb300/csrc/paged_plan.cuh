@@ -41,18 +41,22 @@ struct __align__(16) PlanSeq {
   int tok0, n, slot, start, rows;
 };
 
-template <int W, int U>
+template <int W, int U, int L>
 struct PlanCost {
-  static constexpr int kStep = W;  // cost of a key step
-  static constexpr int kUnit = U;  // cost of a unit besides its steps
+  static constexpr int kStep = W;   // cost of a key step
+  static constexpr int kUnit = U;   // cost of a unit besides its steps
+  static constexpr int kLeast = L;  // key steps that a CTA's range holds at least
 };
 // In half key steps: what a unit costs besides its steps is set by its
 // queries' load and its epilogue.  (Measured on ragged batches: tiles 90.3 us at
 // 5, 88.1 at 7, 87.8 at 8, which is worse for 8 sequences of 768 tokens, D =
-// 128; fp32 27.0 at 1, 24.9 at 3, 28.1 at 4; decode within 0.5% from 2 to 6.)
-using DecodeCost = PlanCost<2, 4>;
-using TileCost = PlanCost<2, 7>;
-using SimtCost = PlanCost<2, 3>;
+// 128; fp32 27.0 at 1, 24.9 at 3, 28.1 at 4; decode within 0.5% from 2 to 6.
+// Small calls are split as far as it pays: a token over 512 rows 9.0 us with two
+// steps a range at least, 9.5 with one; 4 sequences of up to 56 tokens in fp32,
+// whose steps are long, 12.3 and 10.8.)
+using DecodeCost = PlanCost<2, 4, 2>;
+using TileCost = PlanCost<2, 7, 2>;
+using SimtCost = PlanCost<2, 3, 1>;
 
 // Key steps of `BK` rows from the first live row to row x (page rows counted
 // from the slot's first page); at least one.
@@ -97,13 +101,13 @@ __host__ __device__ __forceinline__ int plan_owner(long long x, const PlanLine& 
   return c + more - less;
 }
 
-// CTAs that share a line of length `total`: a CTA's range holds at least two
-// key steps, so every CTA between a unit's first and last has one of its
+// CTAs that share a line of length `total`: a CTA's range is kLeast key steps
+// long at least, so every CTA between a unit's first and last has one of its
 // steps.
 template <typename Cost>
 __host__ __device__ __forceinline__ int plan_ctas(long long total, int most) {
-  static_assert(Cost::kStep == 2, "a shift");
-  const long long want = total >> 2;
+  static_assert(Cost::kStep == 2 && (Cost::kLeast == 1 || Cost::kLeast == 2), "a shift");
+  const long long want = total >> Cost::kLeast;
   return total == 0 ? 0 : (want >= most ? most : (want < 1 ? 1 : static_cast<int>(want)));
 }
 

@@ -16,8 +16,10 @@
 // consecutive rows meet different banks.  The step's loads are coalesced rows,
 // 16 in flight per lane, hidden behind the other CTAs of the SM.  A ragged
 // batch of 5 sequences of up to 130 tokens over up to 700 rows (4 heads, D = 40)
-// takes 25 us: few steps a CTA, each a chain of a page id, its rows and two
-// barriers.  (4 CTAs an SM leave 128 registers a thread, which spill: 28 us.)
+// takes 22 us: few steps a CTA, each a chain of its rows' loads and three
+// barriers; 9 us are the two launches, the division and the join.  (4 CTAs an SM
+// leave 128 registers a thread, which spill: 4% slower.  A step's rows held in
+// registers while the step before is computed: they spill, the same time.)
 #include <cmath>
 #include <cstdint>
 
