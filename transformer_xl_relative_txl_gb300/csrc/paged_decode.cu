@@ -286,6 +286,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
         }
         __syncwarp();
       }
+      // (Another unit's tiles would be taken, by their number, for the rest of
+      // this one's.)
+      if (!ok) break;
     }
     if (ok) publish(0);
     if (bad) atomicOr(p.args.status, kStatusPagesBit);
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       const uint32_t n = s + ((g - 1 - s) / NS) * NS;
       mbar_wait_own(&bars->full[s], (n / NS) & 1, wait_ns);
     }
-      return;
+    return;
   }
 
   // =============================== consumers ================================
