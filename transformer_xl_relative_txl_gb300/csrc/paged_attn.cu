@@ -115,11 +115,9 @@ size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16) {
 }
 
 // fp32: the CUDA cores.  bf16: sequences of up to 4 new tokens by the decode
-// kernel, the others by tiles of 128 queries, which start in its tail; then the
-// joins.  (max_new is the host's bound: the lengths themselves are on the
-// device, and either kernel finds its own.  The other way round, the decode
-// kernel of a batch without short sequences found that out behind the tiles: 3
-// us more.)
+// kernel, then the others by tiles of 128 queries; then the joins.  Each waits
+// for the one ahead.  (max_new is the host's bound: the lengths themselves are
+// on the device, and either kernel finds its own.)
 cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_t stream) {
   PlanSpace s;
   plan_space(a.workspace, a.T, a.D, a.bf16, &s);

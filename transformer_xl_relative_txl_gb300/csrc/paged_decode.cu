@@ -162,8 +162,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
   }
   __syncthreads();
   grid_dep_wait();
-  // The tile kernel behind this one needs what this one does and no more: its
-  // CTAs start as this one's end.
   grid_dep_launch_dependents();
   if (threadIdx.x == 0) p.cuts[blockIdx.x] = PlanCut{0, 0, 0, 0};
   if (p.ahead_of_tiles) {  // most batches of longer entries have none of these

@@ -523,7 +523,7 @@ struct JoinPart {
   int ctas, rows;
 };
 cudaError_t launch_paged_join(const PagedAttn& a, const JoinPart& x, const JoinPart& y, cudaStream_t stream);
-// ahead_of_tiles: the tile kernel follows, which starts in this one's tail.
+// ahead_of_tiles: the tile kernel follows.
 cudaError_t launch_paged_decode(const PagedAttn& a, const PlanSpace& s, int sms, bool ahead_of_tiles, const WaitCtl& wc,
                                 cudaStream_t stream);
 cudaError_t launch_paged_simt(const PagedAttn& a, const PlanSpace& s, int sms, unsigned int* status,

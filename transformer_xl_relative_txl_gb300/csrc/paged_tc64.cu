@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     bars->abort = 0;
     fence_mbar_init();
   }
-  // The decode kernel ahead let this one start once the kernels ahead of it had
-  // completed, and that is all this one needs.  It waits for that kernel at its
-  // end: the kernel behind takes both as complete then.
+  // What ran before the decode kernel ahead wrote the book, the queries and the
+  // pages: its writes, too, are this grid's to see only behind a wait of its own.
+  grid_dep_wait();
   grid_dep_launch_dependents();
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
@@ -633,7 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (threadIdx.x == 0) grid_dep_wait();
 }
 
 template <bool O_BF16>
