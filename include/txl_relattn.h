@@ -708,12 +708,13 @@ TXL_API int txl_version(void);
  * txl_debug_set_wait_limit_ns: upper bound, in nanoseconds, of every bounded
  * wait inside the kernels (default 2e9).  Values < 1000 are rejected.
  *
- * txl_debug_inject_stall: when nonzero, the next txl_relattn_forward or
- * txl_relattn_backward on a tensor-core path has its loads stop early (the
- * forward's loader after the first key tile, the backward's after the first
- * two key steps), so the consumers' bounded waits expire and the call reports
- * TXL_ERR_DEVICE_TIMEOUT through txl_get_device_status.  The flag clears
- * itself after that one call.
+ * txl_debug_inject_stall: when nonzero, the next txl_relattn_forward,
+ * txl_relattn_forward_paged or txl_relattn_backward on a tensor-core path has
+ * its loads stop early (the forward's loader after the first key tile, the
+ * backward's after the first two key steps; of the paged call in every second
+ * CTA, where in the others a role that gives stages back stops), so the bounded
+ * waits expire and the call reports TXL_ERR_DEVICE_TIMEOUT through
+ * txl_get_device_status.  The flag clears itself after that one call.
  */
 TXL_API int txl_debug_set_wait_limit_ns(unsigned long long ns);
 TXL_API int txl_debug_inject_stall(int on);

@@ -362,6 +362,7 @@ int ring_append_impl(void* const* mem, const void* const* h, int n, int cap, int
 namespace txl {
 
 int api_wait_ctl(WaitCtl* wc) { return wait_ctl(wc); }
+int api_take_stall() { return g_inject_stall.exchange(0); }
 PFN_cuTensorMapEncodeTiled_v12000 api_tensor_map_encoder() { return tensor_map_encoder(); }
 
 }  // namespace txl

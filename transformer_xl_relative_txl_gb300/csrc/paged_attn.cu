@@ -81,7 +81,7 @@ cudaError_t launch_tiles(const PagedAttn& a, const PlanSpace& s, int sms, const 
   // fp32 exactly as with 0, while masked keys keep an exponent of -inf.
   const TileParams p{plan_args(a, wc.status), __builtin_ctz(b.page_rows), a.bias_u, a.bias_v, a.o, a.lse,
                      std::max(std::fabs(a.scale), 1e-30f) * 1.4426950408889634f, a.scale < 0.f ? -1.f : 1.f,
-                     s.tiles.cuts, s.tiles.part, wc.limit_ns};
+                     s.tiles.cuts, s.tiles.part, wc.limit_ns, wc.inject_stall};
   return a.D == 64 ? launch_paged_tc64(m, p, a.o_bf16, sms, stream)
                    : launch_paged_tc128(m, p, a.o_bf16, sms, stream);
 }

@@ -78,6 +78,7 @@ struct Params {
   float* part;
   unsigned long long wait_ns;
   bool ahead_of_tiles;
+  int inject_stall;  // test hook: the producer (even CTAs) or a consumer (odd ones) stops behind a unit's first tile
 };
 
 // A unit as the producer publishes it; nks 0: the CTA has no more.
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     const int P = p.args.book.page_rows;
     const int box = min(P, BK), boxes = BK / box;  // a tile is `boxes` boxes of rows
     uint32_t g = 0, units = 0;
-    bool ok = true, bad = false;
+    bool ok = true, bad = false, stop = false;
     // The next unit and its queries, on their way while its tiles are loaded:
     // read by the consumers at the head of the unit, a global load's latency a
     // unit made 163 us of what now takes 123 (64 sequences, see above).
@@ -249,6 +250,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       const int m = w.s.start + w.s.rows - w.s.n;
       int id = -1, id0 = -32;  // this lane's page of the boxes from id0 on
       for (int t = w.p.t0; t < w.p.t0 + w.p.nks; ++t, ++g) {
+        if (p.inject_stall && t > w.p.t0 && blockIdx.x % 2 == 0) {
+          stop = true;
+          break;
+        }
         if (t * boxes - id0 + boxes > 32) {  // the next 32 boxes' pages at once (boxes divides 32)
           id0 = t * boxes;
           const long long x = static_cast<long long>(id0 + lane) * box;
@@ -286,9 +291,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
       }
       // (Another unit's tiles would be taken, by their number, for the rest of
       // this one's.)
-      if (!ok) break;
+      if (!ok || stop) break;
     }
-    if (ok) publish(0);
+    if (ok && !stop) publish(0);
     if (bad) atomicOr(p.args.status, kStatusPagesBit);
     if (!ok && lane == 0) report_timeout(abort, p.args.status);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -343,6 +348,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     const uint32_t g0 = g;
     g += w.nks;
     for (uint32_t x = g0 + (warp + kWarps - g0 % kWarps) % kWarps; x < g; x += kWarps) {
+      if (p.inject_stall && x > g0 && warp == 0 && blockIdx.x % 2 != 0) return;
       const int row0 = (w.t0 + static_cast<int>(x - g0)) * BK;
       const int s = x % NS;
       ok = warp_wait(&bars->full[s], (x / NS) & 1, wait_ns, abort);
@@ -522,7 +528,8 @@ cudaError_t launch(const PagedAttn& a, const PlanSpace& s, int sms, bool ahead_o
     if (!enc(&tm_r, a.r, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   const Params p{plan_args(a, wc.status), static_cast<const __nv_bfloat16*>(a.q), a.bias_u, a.bias_v, a.o, a.lse,
-                 a.scale * 1.4426950408889634f, s.decode.cuts, s.decode.part, wc.limit_ns, ahead_of_tiles};
+                 a.scale * 1.4426950408889634f, s.decode.cuts, s.decode.part, wc.limit_ns, ahead_of_tiles,
+                 wc.inject_stall};
   auto kern = paged_decode_kernel<D, O_BF16>;
   static unsigned configured = 0;  // one bit per device ordinal < 32
   int dev = 0;

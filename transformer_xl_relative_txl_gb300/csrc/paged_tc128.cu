@@ -82,7 +82,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block too large");
 
-template <bool O_BF16>
+template <bool O_BF16, bool STALL>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_constant__ TileMaps tm, const TileParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
 
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
-    run_tile_loader<D, NK, true, false>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, true, false, STALL>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ============================ MMA issuer ===============================
     if (lane == 0) {
@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
           start = w.start;
           last = w.last;
           next_h = w.next_h;
+          if (STALL && blockIdx.x % 2 != 0) nks = 1, next_h = -1;
         }
         zero_dead_rows<D>(start, last, t0 + t, sV + sv * kRowTile, lane);
         if (!(ok = warp_wait(&bars->p_full[g & 1], (g >> 1) & 1, wait_ns, abort))) break;
@@ -499,9 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
   }
 }
 
-template <bool O_BF16>
+template <bool O_BF16, bool STALL>
 cudaError_t launch(const TileMaps& m, const TileParams& p, int sms, cudaStream_t stream) {
-  auto kern = paged_tc128_kernel<O_BF16>;
+  auto kern = paged_tc128_kernel<O_BF16, STALL>;
   static unsigned configured = 0;  // one bit per device ordinal < 32
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -517,7 +518,8 @@ cudaError_t launch(const TileMaps& m, const TileParams& p, int sms, cudaStream_t
 }  // namespace
 
 cudaError_t launch_paged_tc128(const TileMaps& m, const TileParams& p, bool o_bf16, int sms, cudaStream_t stream) {
-  return o_bf16 ? launch<true>(m, p, sms, stream) : launch<false>(m, p, sms, stream);
+  if (p.inject_stall) return o_bf16 ? launch<true, true>(m, p, sms, stream) : launch<false, true>(m, p, sms, stream);
+  return o_bf16 ? launch<true, false>(m, p, sms, stream) : launch<false, false>(m, p, sms, stream);
 }
 
 }  // namespace txl

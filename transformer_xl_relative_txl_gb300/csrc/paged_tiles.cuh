@@ -145,6 +145,7 @@ struct TileParams {
   PlanCut* cuts;
   float* part;
   unsigned long long wait_ns;
+  int inject_stall;
 };
 
 // Tensor maps: q over {D, H, T} with a {64, 1, 128} box, the pools over
@@ -177,7 +178,11 @@ struct TileMaps {
 // loaded behind the first step of the unit before (D = 64: its operands have
 // two buffers and are built during that unit); otherwise at the head of its
 // own, behind the last V tile of the unit before.
-template <int D, int NS, bool TRAIL, bool AHEAD, typename Bars>
+//
+// STALL: the kernels' instances for the test hook, in which the loader of even
+// CTAs, and the P.V issuer of odd ones, stops behind its first unit's first
+// step.  (As a test of a parameter it cost the D = 64 kernel 2 to 4 us of 90.)
+template <int D, int NS, bool TRAIL, bool AHEAD, bool STALL, typename Bars>
 __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
                                                 uint8_t* sK, uint8_t* sV, uint8_t* sR) {
   static_assert((NS & (NS - 1)) == 0, "stage arithmetic");
@@ -250,6 +255,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
   // too); the tiles of unit `un`, of which t is the next, are under way.
   uint32_t known = 0, un = 0xffffffffu;
   bool ended = false, begun = false;
+  const bool stall = STALL && blockIdx.x % 2 == 0;
   int h = 0, d0 = 0, start = 0, last = 0, t = 0, t0 = 0, tend = 0, id = 0;
   const int* row = nullptr;
   auto live = [&](int tile) {
@@ -279,7 +285,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     bool head = false, done = false;
     while (ok && !head) {
       if (t == tend) {  // the next unit
-        if (++un == known) {
+        if (++un == known || (stall && un > 0)) {
           done = true;
           break;
         }
@@ -289,7 +295,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
           if (!ok) break;
         }
         const TileUnit& w = bars->units[un % kUnitRing];
-        h = w.h, d0 = w.d0, start = w.start, last = w.last, t0 = w.t0, tend = t0 + w.nks;
+        h = w.h, d0 = w.d0, start = w.start, last = w.last, t0 = w.t0, tend = t0 + (stall ? 1 : w.nks);
         row = p.args.book.table + static_cast<size_t>(w.slot) * p.args.book.max_pages;
         id = live(t0) ? row[(t0 * kStepKeys + off) >> log_page] : 0;
         t = t0 - 2;  // its first step's other distance tiles

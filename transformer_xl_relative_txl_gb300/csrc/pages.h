@@ -55,8 +55,9 @@ struct PagedAttn {
 size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16);
 cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_t stream);
 
-// From api.cu: the status word with the wait bound, the tensor-map encoder.
+// From api.cu: the status word with the wait bound, the test hook, the tensor-map encoder.
 int api_wait_ctl(WaitCtl* wc);
+int api_take_stall();  // the stall asked for by the test hook, once
 PFN_cuTensorMapEncodeTiled_v12000 api_tensor_map_encoder();
 
 }  // namespace txl

@@ -233,6 +233,7 @@ int txl_relattn_forward_paged(const void* q, const void* k_pages, const void* v_
                    dtype == TXL_BF16, o_dtype == TXL_BF16, workspace};
   txl::WaitCtl wc;
   if (txl::api_wait_ctl(&wc) != TXL_OK) return TXL_ERR_CUDA;
+  if (a.bf16) wc.inject_stall = txl::api_take_stall();
   return from_cuda(txl::launch_paged_attn(a, wc, stream));
 }
 
