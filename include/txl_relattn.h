@@ -466,12 +466,18 @@ TXL_API int txl_stack_forward(const void* h, void* out, int n_layers, void* cons
  * captured into a graph whose replays find other lengths.  Calls that read or
  * change one book follow each other on one stream (or are ordered by events).
  *
- * Refusals on the device.  An entry whose slot, length, start or page is out
- * of range, a slot that a call changes and that an earlier entry of the call
- * names too, rows that do not fit the table or the free pages: such an entry
- * changes nothing, its output rows stay as they were, and
- * txl_get_device_status returns TXL_ERR_PAGES.  The other entries are served.
- * A page id out of range inside a slot's table is never followed.
+ * Refusals on the device.  An entry whose slot, length or start is out of
+ * range, a slot that a call changes and that an earlier entry of the call names
+ * too, rows that do not fit the table or the free pages: such an entry changes
+ * nothing, its output rows stay as they were, and txl_get_device_status returns
+ * TXL_ERR_PAGES.  The other entries are served.
+ *
+ * A page id out of range inside a slot's table is never followed, and is
+ * reported alike where a call meets it.  An entry of txl_pages_reserve (which
+ * reads the slot's last page), txl_pages_append (the new rows' pages),
+ * txl_pages_fork (all) or txl_pages_free (all, where a page leaves) is then
+ * refused as above.  txl_relattn_forward_paged takes that page's rows as zeros,
+ * keys and values; txl_pages_compact leaves the table entry as it is.
  *
  * Limits (TXL_ERR_UNSUPPORTED): n_slots and n at most 16384, n_pages at most
  * 2^28, max_pages * page_rows at most 2^30.

@@ -11,7 +11,8 @@
 // the order of the call's entries, whatever order the threads run in.
 //
 // Bad entries (a slot, page or length out of range, the same slot twice) are
-// refused, touch nothing and raise the pages bit of the status word.
+// refused, touch nothing and raise the pages bit of the status word.  A page id
+// is looked at where a call reads it, ahead of the entry's first change.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -341,9 +342,17 @@ __global__ void __launch_bounds__(256) append_kernel(PageBook b, V* __restrict__
   }
   const int old = copies ? x0 & (P - 1) : 0;
   const int* row = table_row(b, sl.s);
+  // Every page of the new rows ahead of the first write: each warp looks for
+  // itself, at what all of them see.
+  bool pages_ok = true;
+  for (int j = (x0 >> log_page) + (threadIdx.x & 31); j <= (x0 + count - 1) >> log_page; j += 32)
+    pages_ok &= static_cast<unsigned>(row[j]) < static_cast<unsigned>(b.n_pages);
+  if (!__all_sync(0xffffffffu, pages_ok)) {
+    if (threadIdx.x == 0) report_pages(status);
+    return;
+  }
   const uint32_t per = by_row.d;  // vectors of a row
   const size_t page = static_cast<size_t>(H) * P * DV;
-  bool bad = false;
   constexpr int U = 4;
   for (int y0 = static_cast<int>(blockIdx.x) * tile; y0 < old + count; y0 += static_cast<int>(gridDim.x) * tile) {
     const uint32_t total = static_cast<uint32_t>(min(tile, old + count - y0)) * per;
@@ -370,8 +379,6 @@ __global__ void __launch_bounds__(256) append_kernel(PageBook b, V* __restrict__
           const size_t src = static_cast<size_t>(t0 + y - old) * per + rem;
           kx[u] = __ldg(kn + src);
           vx[u] = __ldg(vn + src);
-          on[u] = id >= 0 && id < b.n_pages;
-          bad |= !on[u];
           dst[u] = id * page + (static_cast<size_t>(h) * P + (x & (P - 1))) * DV + c;
         }
       }
@@ -383,7 +390,6 @@ __global__ void __launch_bounds__(256) append_kernel(PageBook b, V* __restrict__
         }
     }
   }
-  if (bad) report_pages(status);
 }
 
 // ---------------------------------------------------------------------------
@@ -512,21 +518,21 @@ __global__ void __launch_bounds__(128) free_kernel(PageBook b, const int* __rest
   const int begin = a.start + (a.rows - kept);  // in range: start + rows <= max_pages * page_rows
   const int pages = ceil_div(static_cast<long long>(a.start) + a.rows, b.page_rows);
   const int dead = kept > 0 ? begin / b.page_rows : pages;
+  int* row = table_row(b, a.s);
+  if (dead > 0) {  // the row is read: every page of it ahead of the first change
+    bool good = true;
+    for (int j = threadIdx.x; j < pages; j += blockDim.x) good &= row[j] >= 0 && row[j] < b.n_pages;
+    if (!__syncthreads_and(good)) {
+      if (threadIdx.x == 0) report_pages(status);
+      return;
+    }
+  }
   if (threadIdx.x == 0) {
     b.start[a.s] = kept > 0 ? begin % b.page_rows : 0;
     b.rows[a.s] = kept;
   }
   if (dead == 0) return;
-  int* row = table_row(b, a.s);
-  bool bad = false;
-  for (int j = threadIdx.x; j < dead; j += blockDim.x) {
-    const int p = row[j];
-    if (p >= 0 && p < b.n_pages)
-      atomicSub(&b.refs[p], 1);
-    else
-      bad = true;
-  }
-  if (bad) report_pages(status);
+  for (int j = threadIdx.x; j < dead; j += blockDim.x) atomicSub(&b.refs[row[j]], 1);
   // The row moves up `dead` places, a block of entries at a time: a block's
   // entries are read before any is written, and lie above every entry written
   // before it.
