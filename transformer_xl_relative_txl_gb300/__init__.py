@@ -3,9 +3,10 @@
 Thin ctypes binding of the C ABI in ``include/txl_relattn.h``: each function
 has the C entry point's name and only marshals torch tensors (device memory,
 CUDA streams) into pointers, sizes and dtype codes; the paged memory's calls do
-so in the extension module _paged (csrc/paged_binding.cpp).  All computation
-runs in the library's CUDA kernels; there is no fallback.  Importing fails loudly if
-the library has not been built (``python transformer_xl_relative_txl_gb300/build.py``).
+so in the extension module _paged (csrc/paged_binding.cpp), which the first of
+them loads: it is built against one PyTorch, the rest of the package is not.  All
+computation runs in the library's CUDA kernels; there is no fallback.  Importing
+fails loudly if the library has not been built (``python transformer_xl_relative_txl_gb300/build.py``).
 """
 
 from __future__ import annotations
@@ -45,13 +46,10 @@ _STATUS = {0: "TXL_OK", 1: "TXL_ERR_INVALID_ARG", 2: "TXL_ERR_UNSUPPORTED", 3: "
            4: "TXL_ERR_CUDA", 5: "TXL_ERR_DEVICE_TIMEOUT", 6: "TXL_ERR_PAGES"}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtxl_relattn.so")
-_binding_path = os.path.join(os.path.dirname(library_path), "_paged.so")
-for _path in (library_path, _binding_path):
-    if not os.path.exists(_path):
-        raise ImportError(f"{_path} is missing: build it with `python transformer_xl_relative_txl_gb300/build.py`")
+if not os.path.exists(library_path):
+    raise ImportError(
+        f"{library_path} is missing: build it with `python transformer_xl_relative_txl_gb300/build.py`")
 lib = ctypes.CDLL(library_path)
-
-from . import _paged  # noqa: E402  (needs torch's libraries and the library above loaded)
 
 _p, _i, _ll, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 lib.txl_relattn_forward.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _i, _i, _p]
@@ -421,6 +419,22 @@ def txl_dense(x, W, y, bias=None, relu=False, stream=None):
     return y
 
 
+_calls = None
+
+
+def _paged_calls():
+    """The extension module of the paged memory's calls, loaded by the first of them."""
+    global _calls
+    if _calls is None:
+        try:
+            from . import _paged
+        except ImportError as e:
+            raise ImportError("the paged memory's extension module (_paged.so) is missing or was built for another "
+                              "PyTorch: build it with `python transformer_xl_relative_txl_gb300/build.py`") from e
+        _calls = _paged
+    return _calls
+
+
 def _handle(stream):
     """A stream's handle; None: the current stream's, found by the call."""
     return None if stream is None else _stream(stream)
@@ -431,7 +445,7 @@ def txl_pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, s
     dict of int32 tensors table [slots, max_pages], start, rows [slots], refs
     [pages].  granted, copy_src, copy_dst (int32 [n]) receive the rows granted
     and the pages that txl_pages_append has to copy."""
-    _check(_paged.pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, _handle(stream)),
+    _check(_paged_calls().pages_reserve(book, page_rows, slots, cu, granted, copy_src, copy_dst, _handle(stream)),
            "txl_pages_reserve")
 
 
@@ -439,31 +453,31 @@ def txl_pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_
     """Rows cu[i] .. cu[i+1]-1 of k_new, v_new [T, H, D] into the last rows of
     slot slots[i] of the pools [pages, H, page_rows, D], after the copies that
     txl_pages_reserve named (copy_src, copy_dst, or None and None)."""
-    _check(_paged.pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new,
-                               _handle(stream)), "txl_pages_append")
+    _check(_paged_calls().pages_append(book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new,
+                                       _handle(stream)), "txl_pages_append")
 
 
 def txl_pages_copy(k_pages, v_pages, src, dst, stream=None):
     """Whole pages src[i] -> dst[i] of both pools; pairs with -1 are left out."""
-    _check(_paged.pages_copy(k_pages, v_pages, src, dst, _handle(stream)), "txl_pages_copy")
+    _check(_paged_calls().pages_copy(k_pages, v_pages, src, dst, _handle(stream)), "txl_pages_copy")
 
 
 def txl_pages_fork(book, page_rows, src, dst, ok, stream=None):
     """Empty slot dst[i] shares the pages of slot src[i]; ok (int32 [n])
     receives 1, or 0 where refused."""
-    _check(_paged.pages_fork(book, page_rows, src, dst, ok, _handle(stream)), "txl_pages_fork")
+    _check(_paged_calls().pages_fork(book, page_rows, src, dst, ok, _handle(stream)), "txl_pages_fork")
 
 
 def txl_pages_free(book, page_rows, slots, keep=None, stream=None):
     """Slot slots[i] keeps its newest keep[i] rows (None: none)."""
-    _check(_paged.pages_free(book, page_rows, slots, keep, _handle(stream)), "txl_pages_free")
+    _check(_paged_calls().pages_free(book, page_rows, slots, keep, _handle(stream)), "txl_pages_free")
 
 
 def txl_pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, stream=None):
     """The live pages get the lowest ids.  new_id, copy_src, copy_dst (int32
     [pages]) and count (int32 [1]) receive the new ids and the moves, which
     txl_pages_copy(k_pages, v_pages, copy_src, copy_dst) then makes."""
-    _check(_paged.pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, _handle(stream)),
+    _check(_paged_calls().pages_compact(book, page_rows, new_id, copy_src, copy_dst, count, _handle(stream)),
            "txl_pages_compact")
 
 
@@ -480,8 +494,8 @@ def txl_relattn_forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, b
     [H, T] fp32 or None; max_new: the largest number of new rows of an entry
     (T when None); workspace: uint8, txl_relattn_paged_workspace_bytes(...).
     scale defaults to 1/sqrt(D)."""
-    _check(_paged.forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, bias_v, o, workspace, lse, max_new,
-                                q.shape[-1] ** -0.5 if scale is None else scale, _handle(stream)),
+    _check(_paged_calls().forward_paged(q, k_pages, v_pages, book, slots, cu, r, bias_u, bias_v, o, workspace, lse,
+                                        max_new, q.shape[-1] ** -0.5 if scale is None else scale, _handle(stream)),
            "txl_relattn_forward_paged")
     return o
 

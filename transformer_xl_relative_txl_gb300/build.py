@@ -81,15 +81,16 @@ def build(verbose: bool = False, extra=()) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, list(extra)), srcs))
-        obj, torch_lib = binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, err in results:
             if err.strip():
                 print(err, file=sys.stderr)
     _link([_nvcc(), *ARCH, "-shared", *objs], LIB)
-    _link([shutil.which("g++") or "c++", "-shared", obj, f"-L{PKG}", "-l:libtxl_relattn.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
-           "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], BINDING)
+    # Behind the library, which every other call needs and this one's headers are not part of.
+    obj, torch_lib = binding.result()
+    _link([shutil.which("g++") or "c++", "-shared", obj, f"-L{PKG}", "-l:libtxl_relattn.so", f"-L{torch_lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], BINDING)
     return LIB
 
 
