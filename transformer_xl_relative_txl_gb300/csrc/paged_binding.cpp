@@ -146,14 +146,25 @@ struct Pools {
   }
 };
 
+// Entry point f on arguments that are made with the interpreter's lock held, run
+// without it: a launch waits where the device's queue is full.
+template <typename... P, typename... A>
+int call(int (*f)(P...), A... args) {
+  struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  } unlocked;
+  return f(args...);
+}
+
 // (book, page_rows, slots, cu, granted, copy_src, copy_dst, stream)
 int reserve(PyObject* const* a) {
   const at::Tensor& slots = tensor(a[2]);
   const Place place(slots);
   const long long n = slots.numel();
   const txl_page_book b = book_of(place, a[0], integer(a[1]));
-  return txl_pages_reserve(&b, place.vector(a[2], n), place.vector(a[3], n + 1), count(n), place.vector(a[4], n),
-                           place.vector(a[5], n), place.vector(a[6], n), place.stream(a[7]));
+  return call(txl_pages_reserve, &b, place.vector(a[2], n), place.vector(a[3], n + 1), count(n), place.vector(a[4], n),
+              place.vector(a[5], n), place.vector(a[6], n), place.stream(a[7]));
 }
 
 // (book, k_pages, v_pages, slots, cu, granted, copy_src, copy_dst, k_new, v_new, stream)
@@ -171,9 +182,9 @@ int append(PyObject* const* a) {
     throw BadArgument("k_new, v_new must be [T, H, D]");
   if (k.scalar_type() != pools.kt.scalar_type() || v.scalar_type() != pools.kt.scalar_type())
     throw BadArgument("the pools and the new rows share a dtype");
-  return txl_pages_append(&b, pools.k, pools.v, pools.H, pools.D, place.vector(a[3], n), place.vector(a[4], n + 1),
-                          count(n), place.vector(a[5], n), place.vector(a[6], n), place.vector(a[7], n), place.of(k),
-                          place.of(v), count(T), pools.dtype, place.stream(a[10]));
+  return call(txl_pages_append, &b, pools.k, pools.v, pools.H, pools.D, place.vector(a[3], n),
+              place.vector(a[4], n + 1), count(n), place.vector(a[5], n), place.vector(a[6], n), place.vector(a[7], n),
+              place.of(k), place.of(v), count(T), pools.dtype, place.stream(a[10]));
 }
 
 // (k_pages, v_pages, src, dst, stream)
@@ -182,8 +193,9 @@ int copy(PyObject* const* a) {
   const Place place(src);
   const long long n = src.numel();
   const Pools pools(place, a[0], a[1]);
-  return txl_pages_copy(pools.k, pools.v, pools.pages, static_cast<long long>(pools.H) * pools.page_rows * pools.D,
-                        place.vector(a[2], n), place.vector(a[3], n), count(n), pools.dtype, place.stream(a[4]));
+  return call(txl_pages_copy, pools.k, pools.v, pools.pages,
+              static_cast<long long>(pools.H) * pools.page_rows * pools.D, place.vector(a[2], n), place.vector(a[3], n),
+              count(n), pools.dtype, place.stream(a[4]));
 }
 
 // (book, page_rows, src, dst, ok, stream)
@@ -192,8 +204,8 @@ int fork(PyObject* const* a) {
   const Place place(src);
   const long long n = src.numel();
   const txl_page_book b = book_of(place, a[0], integer(a[1]));
-  return txl_pages_fork(&b, place.vector(a[2], n), place.vector(a[3], n), count(n), place.vector(a[4], n),
-                        place.stream(a[5]));
+  return call(txl_pages_fork, &b, place.vector(a[2], n), place.vector(a[3], n), count(n), place.vector(a[4], n),
+              place.stream(a[5]));
 }
 
 // (book, page_rows, slots, keep, stream)
@@ -202,15 +214,15 @@ int free_(PyObject* const* a) {
   const Place place(slots);
   const long long n = slots.numel();
   const txl_page_book b = book_of(place, a[0], integer(a[1]));
-  return txl_pages_free(&b, place.vector(a[2], n), place.vector(a[3], n), count(n), place.stream(a[4]));
+  return call(txl_pages_free, &b, place.vector(a[2], n), place.vector(a[3], n), count(n), place.stream(a[4]));
 }
 
 // (book, page_rows, new_id, copy_src, copy_dst, count, stream)
 int compact(PyObject* const* a) {
   const Place place(tensor(a[2]));
   const txl_page_book b = book_of(place, a[0], integer(a[1]));
-  return txl_pages_compact(&b, place.vector(a[2], b.n_pages), place.vector(a[3], b.n_pages),
-                           place.vector(a[4], b.n_pages), place.vector(a[5], 1), place.stream(a[6]));
+  return call(txl_pages_compact, &b, place.vector(a[2], b.n_pages), place.vector(a[3], b.n_pages),
+              place.vector(a[4], b.n_pages), place.vector(a[5], 1), place.stream(a[6]));
 }
 
 // (q, k_pages, v_pages, book, slots, cu, r, bias_u, bias_v, o, workspace, lse, max_new, scale, stream)
@@ -240,11 +252,10 @@ int attend(PyObject* const* a) {
   const int most = a[12] == Py_None ? count(T) : integer(a[12]);
   const double scale = PyFloat_AsDouble(a[13]);
   if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
-  return txl_relattn_forward_paged(place.of(q), pools.k, pools.v, &b, place.vector(a[4], n), place.vector(a[5], n + 1),
-                                   count(n), count(T), most, place.of(r), static_cast<float*>(place.of(u)),
-                                   static_cast<float*>(place.of(v)), place.of(o), lse, H, D, count(n_r),
-                                   static_cast<float>(scale), pools.dtype, dtype_of(o), place.of(ws), ws.nbytes(),
-                                   place.stream(a[14]));
+  return call(txl_relattn_forward_paged, place.of(q), pools.k, pools.v, &b, place.vector(a[4], n),
+              place.vector(a[5], n + 1), count(n), count(T), most, place.of(r), static_cast<float*>(place.of(u)),
+              static_cast<float*>(place.of(v)), place.of(o), lse, H, D, count(n_r), static_cast<float>(scale),
+              pools.dtype, dtype_of(o), place.of(ws), ws.nbytes(), place.stream(a[14]));
 }
 
 // The status of call F with its N arguments.
