@@ -480,7 +480,7 @@ TXL_API int txl_stack_forward(const void* h, void* out, int n_layers, void* cons
  * keys and values; txl_pages_compact leaves the table entry as it is.
  *
  * Limits (TXL_ERR_UNSUPPORTED): n_slots and n at most 16384, n_pages at most
- * 2^28, max_pages * page_rows at most 2^30.
+ * 2^28, max_pages * page_rows and the attention's T at most 2^30.
  */
 typedef struct {
   int* table;

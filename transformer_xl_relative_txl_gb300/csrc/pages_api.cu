@@ -215,7 +215,7 @@ int txl_relattn_forward_paged(const void* q, const void* k_pages, const void* v_
       !pointers_ok(16, static_cast<const char*>(o)) || !pointers_ok(4, slots, cu) ||
       !pointers_ok(4, bias_u, bias_v) || !aligned(lse, 4) || n_r == 0)
     return TXL_ERR_INVALID_ARG;
-  if (n > txl::kMaxSlots || H > 65535) return TXL_ERR_UNSUPPORTED;
+  if (n > txl::kMaxSlots || H > 65535 || T > (1 << 30)) return TXL_ERR_UNSUPPORTED;
   if (dtype == TXL_F32 ? (o_dtype != TXL_F32 || D > 256) : (D != 64 && D != 128)) return TXL_ERR_UNSUPPORTED;
   if (!pointers_ok(256, static_cast<const char*>(workspace)) ||
       workspace_bytes < txl_relattn_paged_workspace_bytes(n, T, H, D, dtype))
