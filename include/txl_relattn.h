@@ -466,11 +466,13 @@ TXL_API int txl_stack_forward(const void* h, void* out, int n_layers, void* cons
  * captured into a graph whose replays find other lengths.  Calls that read or
  * change one book follow each other on one stream (or are ordered by events).
  *
- * Refusals on the device.  An entry whose slot, length or start is out of
- * range, a slot that a call changes and that an earlier entry of the call names
- * too, rows that do not fit the table or the free pages: such an entry changes
- * nothing, its output rows stay as they were, and txl_get_device_status returns
- * TXL_ERR_PAGES.  The other entries are served.
+ * Refusals on the device.  An entry whose slot, rows (cu), length or start is
+ * out of range, a slot that a call changes and that an earlier entry of the
+ * call names too, rows that do not fit the table or the free pages: such an
+ * entry changes nothing, its output rows stay as they were, and
+ * txl_get_device_status returns TXL_ERR_PAGES.  The other entries are served
+ * (where cu falls, so that two of them own a row of the output, it gets the
+ * result of either).
  *
  * A page id out of range inside a slot's table is never followed, and is
  * reported alike where a call meets it.  An entry of txl_pages_reserve (which
@@ -501,6 +503,7 @@ typedef struct {
  * once one does not fit, later ones that need pages do not either.
  *
  *   granted            device, [n] out: the entry's row count, 0 when refused
+ *                      (txl_pages_append takes it as written here)
  *   copy_src, copy_dst device, [n] out: pages to copy from and to, or -1
  * table, rows and refs are updated (rows already count the new rows).
  * A page freed by the copy on write may be given out again by the next

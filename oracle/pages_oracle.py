@@ -39,9 +39,9 @@ class Book:
             fresh = s not in seen
             seen.add(s)
             g, a, z = 0, -1, -1
-            if self.good(s) and count == 0:
+            if self.good(s) and count == 0 and cu[i] >= 0:
                 pass
-            elif not self.good(s) or count < 0 or not fresh:
+            elif not self.good(s) or count < 0 or cu[i] < 0 or not fresh:
                 refused = True
             else:
                 end = self.start[s] + self.rows[s]

@@ -78,3 +78,18 @@ def test_a_bad_page_counts_as_zeros(txl, dtype, D, counts, bad):
     txl.txl_relattn_forward_paged(*args, **kw)
     assert txl.txl_get_device_status() == PAGES
     assert torch.equal(o, want) and torch.equal(kw["lse"], want_l)
+
+
+def test_reserve_refuses_rows_before_the_first(txl):
+    """Rows that append would not find: nothing is granted, 1024 entries or fewer and more."""
+    for n in (4, 1100):
+        book, _ = filled(np.random.default_rng(n), [(0, 5)] * n, 16, 1, 4, BF, spare=2 * n)
+        dev = to_gpu(book)
+        cu = [-9, -4, -4, 6] + list(range(7, 4 + n))  # entry 1 is empty, entry 2 starts before row 0
+        out = [ints([9] * n) for _ in range(3)]
+        g, a, z, refused = book.reserve(list(range(n)), cu)
+        txl.txl_pages_reserve(dev, 16, ints(list(range(n))), ints(cu), *out)
+        assert refused and len(cu) == n + 1 and g[:4] == [0, 0, 0, 1]
+        assert [x.tolist() for x in out] == [g, a, z]
+        assert txl.txl_get_device_status() == PAGES
+        same(dev, book)

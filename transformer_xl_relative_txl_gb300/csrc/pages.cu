@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(kBlock) reserve_kernel(PageBook b, const int* 
 
   auto ask = [&](int i) {
     const Slot sl = read_slot(b, slots[i]);
-    Ask a{sl.s, sl.rows, cu[i + 1] - cu[i], 0, 0, -1, false, false, false};
-    if (!sl.ok) return a;
+    const int row0 = cu[i];
+    Ask a{sl.s, sl.rows, cu[i + 1] - row0, 0, 0, -1, false, false, false};
+    if (!sl.ok || row0 < 0) return a;  // (append has no such row, and would leave what is granted unwritten)
     a.idle = a.count == 0;
     const long long end = static_cast<long long>(sl.start) + sl.rows;
     a.have = ceil_div(end, b.page_rows);
