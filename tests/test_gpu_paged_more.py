@@ -57,6 +57,27 @@ def test_low_parts(txl, D, n, L):
     assert (off <= each).all() and (off ** 2).sum() <= room
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,L", [(9, 60), (20, 40), (70, 90), (130, 131)])
+def test_low_parts_of_tiles(txl, D, n, L):
+    """More tokens: the weights keep both parts, the distance part its 32 bits, q its own; u and v both parts at D = 128,
+    and at D = 64, where they are rounded to bf16, they are bf16 numbers here."""
+    rng = np.random.default_rng(D)
+    H = 2
+    q, k, v, r, u, vb = case(rng, n, L, H, D)
+    if D == 64:
+        u, vb = (torch.from_numpy(x).to(BF).double().numpy() for x in (u, vb))
+    book, pools = paged(rng, k, v, 16, 5)
+    f = lambda x: torch.from_numpy(np.ascontiguousarray(x)).float().cuda()  # noqa: E731
+    o = torch.empty(n, H, D, device="cuda")
+    txl.txl_relattn_forward_paged(f(q).to(BF), *pools, to_gpu(book), ints([0]), ints([0, n]), f(r).to(BF), f(u), f(vb), o,
+                                  workspace(txl, 1, n, H, D, BF), max_new=n)
+    assert txl.txl_get_device_status() == 0
+    want, each, room = bounds(q, k, v, r, u, vb, D ** -0.5)
+    off = np.abs(o.double().cpu().numpy() - want)
+    assert (off <= each).all() and (off ** 2).sum() <= room
+
+
 @pytest.mark.parametrize("D,new", [(16, 5), (64, 1), (128, 40)])
 def test_float32_beside_refused_entries(txl, D, new):
     """The entries that are served, against the oracle at fp32's own tolerance."""

@@ -1,7 +1,8 @@
-"""What the decode kernel's two-part operands leave: (q + u), (q + v) and the
-weights as two bf16 numbers each, hi + lo, products and sums in fp32.  The bounds
-that the GPU test holds it to, and on the CPU that arithmetic of this kind keeps
-them while leaving out any one of the low parts does not."""
+"""What the bf16 kernels' two-part operands leave: (q + u), (q + v), or u and v
+beside an exact q, and the weights as two bf16 numbers each, hi + lo, products
+and sums in fp32.  The bounds that the GPU tests hold them to, and on the CPU that
+arithmetic of this kind keeps them while leaving out any one of the low parts,
+or rounding the distance part, does not."""
 
 import numpy as np
 import pytest
@@ -48,17 +49,18 @@ def computed(q, k, v, r, u, vb, scale, without=""):
             m = len(k) - n + t
             a = parts(scale * (q[t, h] + u[h]), without != "u")
             b = parts(scale * (q[t, h] + vb[h]), without != "v")
-            z = k[:m + 1, h] @ a + r[m::-1, h] @ b
+            far = r[m::-1, h] @ b
+            z = k[:m + 1, h] @ a + (bf(far) if without == "distance" else far)
             w = np.exp(z - z.max())
             o[t, h] = parts(w, without != "weights") @ v[:m + 1, h] / w.sum()
     return o
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("without", ["", "u", "v", "weights"])
+@pytest.mark.parametrize("without", ["", "u", "v", "weights", "distance"])
 def test_each_low_part_shows(D, without):
     rng = np.random.default_rng(D)
-    for n, L in ((1, 30), (2, 60), (4, 90)):
+    for n, L in ((1, 30), (2, 60), (4, 90), (9, 60), (20, 40)):
         c = case(rng, n, L, 2, D)
         want, each, room = bounds(*c, D ** -0.5)
         off = (computed(*c, D ** -0.5, without=without) - want) ** 2

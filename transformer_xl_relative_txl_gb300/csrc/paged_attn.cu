@@ -76,11 +76,11 @@ cudaError_t launch_tiles(const PagedAttn& a, const PlanSpace& s, int sms, const 
   if (!enc(&m.q, a.q, 3, tokens, row, box_q)) return cudaErrorInvalidValue;
   m.o = m.q;  // stands in where the output is not bf16 and never touched
   if (a.o_bf16 && !enc(&m.o, a.o, 3, tokens, row, box_o)) return cudaErrorInvalidValue;
-  // The sign of the scale is folded into (q+u), (q+v) (exact in bf16); a zero
+  // The sign of the scale is the score products' (exact); a zero
   // scale becomes 1e-30, for which every visible exponent rounds to 2^0 in
   // fp32 exactly as with 0, while masked keys keep an exponent of -inf.
   const TileParams p{plan_args(a, wc.status), __builtin_ctz(b.page_rows), a.bias_u, a.bias_v, a.o, a.lse,
-                     std::max(std::fabs(a.scale), 1e-30f) * 1.4426950408889634f, a.scale < 0.f ? -1.f : 1.f,
+                     std::max(std::fabs(a.scale), 1e-30f) * 1.4426950408889634f, a.scale < 0.f,
                      s.tiles.cuts, s.tiles.part, wc.limit_ns, wc.inject_stall};
   return a.D == 64 ? launch_paged_tc64(m, p, a.o_bf16, sms, stream)
                    : launch_paged_tc128(m, p, a.o_bf16, sms, stream);

@@ -9,10 +9,14 @@
 // softmax warps of which two share a lane quadrant and halve each 64-key step,
 // the distance window shifted per lane.  Keys are counted in page rows, the
 // work is divided on the device and cut units joined, value rows that are not
-// live are zeroed, as in paged_tc64.cu; the roundings are those given there.
+// live are zeroed, and only the output is rounded to bf16, as in paged_tc64.cu; u
+// and v have two parts here, appended to the tiles (paged_tiles.cuh), and the
+// weights' second parts lie in shared memory, since tensor memory has no room.
 //
-// Measured: 8 sequences of 768 tokens over 768 rows, 8 heads, 91 us, 477
-// TFLOP/s.  Bound by the step chain of the softmax warps, as relattn_tc.cu.
+// Measured: 8 sequences of 768 tokens over 768 rows, 8 heads, 110 us, 395
+// TFLOP/s; 92 us with the roundings of relattn_tc.cu, which leave 3.2e-3 of the
+// exact result where this leaves 1.7e-3.  Bound by the step chain of the softmax
+// warps, as there.
 //
 // TMEM (512 columns): O [0,128), P0, P1 [128,192) (bf16 pairs), S0, S1
 // [192,320), distance ring [320,512).  Warps: 0-7 softmax (warp w: lane
@@ -53,13 +57,15 @@ constexpr int kRowTile = kChunks * kRowChunk;
 constexpr int kQChunk = BM * 128;    // 128 rows x 128 B
 constexpr int kQTile = kChunks * kQChunk;
 constexpr int NK = 2, NV = 2, NR = 2;  // the loader takes one stage count
-constexpr int kOffQ = 0;
-constexpr int kOffQu = kOffQ + kQTile;
-constexpr int kOffQv = kOffQu + kQTile;
-constexpr int kOffK = kOffQv + kQTile;
+constexpr int kPTile = BM * 128;        // 128 rows of 64 weights
+constexpr int kOffQ = 0;                       // q: 2 buffers
+constexpr int kOffK = kOffQ + 2 * kQTile;
 constexpr int kOffV = kOffK + NK * kRowTile;
 constexpr int kOffR = kOffV + NV * kRowTile;
-constexpr int kOffRed = kOffR + NR * kRowTile;
+constexpr int kOffPlo = kOffR + NR * kRowTile;  // P's lo parts (bf16): 2 buffers
+constexpr int kOffTermK = kOffPlo + 2 * kPTile;    // bias terms of the K tiles, then of the R tiles
+constexpr int kOffTermR = kOffTermK + BiasTerm<D, NK>::kBytes;
+constexpr int kOffRed = kOffTermR + BiasTerm<D, NR>::kBytes;
 constexpr int kRedFloats = 2 * 2 * BM + 2 * BM;  // [step parity][half][row] maxima, [unit parity][row] sums
 constexpr int kOffBar = kOffRed + kRedFloats * 4;
 constexpr int kBarBytes = 5120;
@@ -68,8 +74,8 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Bars {
   uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
-  uint64_t q_full, q_empty;
-  uint64_t q_ready, s_full[2], s_free[2], p_full[2], pv_done[2], o_full, o_free, g_free[kSlots], mma_final,
+  uint64_t q_full[2], q_empty[2];  // by unit parity
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_full, o_free, g_free[kSlots], mma_final,
       pv_final;
   uint64_t g_full[2], qr_final;  // distance tile of a step ready (per S buffer parity); QR issuer done
   uint64_t xbar[4];  // row-max exchange of warps quad and quad+4 (64 arrivals per step)
@@ -88,11 +94,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   uint8_t* sQ = smem + kOffQ;
-  uint8_t* sQu = smem + kOffQu;
-  uint8_t* sQv = smem + kOffQv;
+  uint8_t* sTermK = smem + kOffTermK;
+  uint8_t* sTermR = smem + kOffTermR;
   uint8_t* sK = smem + kOffK;
   uint8_t* sV = smem + kOffV;
   uint8_t* sR = smem + kOffR;
+  uint8_t* sPlo = smem + kOffPlo;
   float* red = reinterpret_cast<float*>(smem + kOffRed);
   float* lred = red + 2 * 2 * BM;
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
@@ -121,10 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
       mbar_init(&bars->s_free[s], 8);
       mbar_init(&bars->p_full[s], 8);
       mbar_init(&bars->pv_done[s], 1);
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 10);  // the softmax warps have seen the unit, both score products are done
     }
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 128);
-    mbar_init(&bars->q_ready, 128);
     mbar_init(&bars->o_full, 1);
     mbar_init(&bars->o_free, 4);
     mbar_init(&bars->mma_final, 1);
@@ -154,47 +160,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
 
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
-    run_tile_loader<D, NK, true, false, STALL>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, true, STALL>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ============================ MMA issuer ===============================
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
-      // Descriptor bases; the start-address field holds address / 16 in its
-      // low 14 bits, so byte offsets inside shared memory are added as
-      // offset / 16 (no carry: shared addresses stay below 256 KB).
-      const uint64_t dQu = sdesc_sw128(smem_u32(sQu), 16, 1024);
-      const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
-      constexpr uint32_t kTile16 = kRowTile >> 4;
-      uint32_t nK = 0, gt = 0, un = 0;
-      bool ok = true;
-      while (any && ok) {
-        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
-        const TileUnit w = bars->units[un % kUnitRing];
-        tc_fence_after();
-        const uint32_t g0 = gt;
-        for (int t = 0; t < w.nks; ++t) {
-          const uint32_t g = g0 + t, sb = g & 1;
-          if (g >= 2 && !(ok = mbar_wait(&bars->s_free[sb], ((g - 2) >> 1) & 1, wait_ns, abort))) break;
-          const int sk = nK % NK;
-          if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
+    const uint32_t idS = idesc_bf16(128, BN, false, false) | (p.negative ? kNegateA : 0u);
+    // Descriptor bases; the start-address field holds address / 16 in its
+    // low 14 bits, so byte offsets inside shared memory are added as
+    // offset / 16 (no carry: shared addresses stay below 256 KB).
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    BiasTerm<D, NK> term(sTermK);
+    const uint64_t dTerm = term.term_desc(), dOnes = term.ones_desc();
+    const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+    constexpr uint32_t kTile16 = kRowTile >> 4;
+    uint32_t gt = 0, un = 0;  // gt: steps, and K tiles, so far
+    bool ok = true;
+    while (any && ok) {
+      if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
+      const int nks = bars->units[un % kUnitRing].nks, next_h = bars->units[un % kUnitRing].next_h;
+      const uint32_t g0 = gt;
+      const uint64_t dq = dQ + (un & 1) * (kQTile >> 4);
+      term.load(p.bias_u, bars->units[un % kUnitRing].h);
+      for (int t = 0; t < nks; ++t) {
+        const uint32_t g = g0 + t, sb = g & 1;
+        const int sk = g % NK;
+        if (!(ok = warp_wait(&bars->fullK[sk], (g / NK) & 1, wait_ns, abort))) break;
+        term.append(sK + sk * kRowTile, sk);
+        // S buffer sb was last read by step g-2.
+        if (g >= 2 && !(ok = warp_wait(&bars->s_free[sb], ((g - 2) >> 1) & 1, wait_ns, abort))) break;
+        if (lane == 0) {
           tc_fence_after();
-          {
-            const uint64_t dk = dK + sk * kTile16;
-            const uint32_t sd = tmem + kColS + sb * BN;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t koff16 = ((kk / 4) * kRowChunk + (kk % 4) * 32) >> 4;
-              mma_ss(sd, dQu + (((kk / 4) * kQChunk + (kk % 4) * 32) >> 4), dk + koff16, idS, kk > 0);
-            }
-          }
+          mma_scores<D>(tmem + kColS + sb * BN, dq, dK + sk * kTile16, dOnes, dTerm + sk * (kBiasStage >> 4), idS);
           tc_commit(&bars->emptyK[sk]);
-          ++nK;
           tc_commit(&bars->s_full[sb]);
+          if (t == nks - 1) tc_commit(&bars->q_empty[un & 1]);
         }
-        if (!ok || w.next_h < 0) break;
-        gt = g0 + w.nks;
-        ++un;
+        __syncwarp();
       }
+      if (!ok || next_h < 0) break;
+      gt = g0 + nks;
+      ++un;
+    }
+    if (lane == 0) {
       if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->mma_final);
       mbar_wait_own(&bars->mma_final, 0, wait_ns);
@@ -203,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     // ============================ PV issuer ================================
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
     const uint64_t dV = sdesc_sw128(smem_u32(sV), kRowChunk, 1024);
+    const uint64_t dP = sdesc_sw128(smem_u32(sPlo), 16, 1024);
     constexpr uint32_t kTile16 = kRowTile >> 4;
     uint32_t g = 0, un = 0;  // g: steps, and V tiles, so far
     bool ok = true;
@@ -231,6 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             mma_ts(tmem + kColO, pa + kk * 8, dv + ((kk * 16 * 128) >> 4), idO, (t > 0 || kk > 0) ? 1u : 0u);
+          const uint64_t dp = dP + (g & 1) * (kPTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk) mma_ss(tmem + kColO, dp + kk * 2, dv + ((kk * 16 * 128) >> 4), idO, 1);
           tc_commit(&bars->emptyV[sv]);
           tc_commit(&bars->pv_done[g & 1]);
           if (t == nks - 1) tc_commit(&bars->o_full);
@@ -251,48 +261,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     // released the slot's previous tile; tiles -2 and -1 of a unit with its
     // first step.  Its own thread, so the ring never waits behind the S
     // MMAs' barriers (and the reverse); it commits g_full per step.
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
-      const uint64_t dQv = sdesc_sw128(smem_u32(sQv), 16, 1024);
-      const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
-      constexpr uint32_t kTile16 = kRowTile >> 4;
-      uint32_t nR = 0, gt = 0, un = 0;
-      uint32_t gsu0 = 0, gsu1 = 0, gsu2 = 0;  // writes per ring slot so far
-      bool ok = true;
-      while (any && ok) {
-        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
-        const TileUnit w = bars->units[un % kUnitRing];
-        tc_fence_after();
-        const uint32_t g0 = gt;
-        for (int t = 0; t < w.nks; ++t) {
-          const uint32_t g = g0 + t, sb = g & 1;
-          for (int e = (t == 0 ? -2 : t); ok && e <= t; ++e) {
-            const int slot = (e + 2) % kSlots;
-            const uint32_t used = slot == 0 ? gsu0 : (slot == 1 ? gsu1 : gsu2);
-            if (used > 0 && !(ok = mbar_wait(&bars->g_free[slot], (used - 1) & 1, wait_ns, abort))) break;
-            const int sr = nR % NR;
-            if (!(ok = mbar_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
+    const uint32_t idS = idesc_bf16(128, BN, false, false) | (p.negative ? kNegateA : 0u);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    BiasTerm<D, NR> term(sTermR);
+    const uint64_t dTerm = term.term_desc(), dOnes = term.ones_desc();
+    const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
+    constexpr uint32_t kTile16 = kRowTile >> 4;
+    uint32_t nR = 0, gt = 0, un = 0;
+    uint32_t gsu0 = 0, gsu1 = 0, gsu2 = 0;  // writes per ring slot so far
+    bool ok = true;
+    while (any && ok) {
+      if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
+      const int nks = bars->units[un % kUnitRing].nks, next_h = bars->units[un % kUnitRing].next_h;
+      const uint32_t g0 = gt;
+      const uint64_t dq = dQ + (un & 1) * (kQTile >> 4);
+      term.load(p.bias_v, bars->units[un % kUnitRing].h);
+      for (int t = 0; t < nks; ++t) {
+        const uint32_t g = g0 + t, sb = g & 1;
+        for (int e = (t == 0 ? -2 : t); e <= t; ++e) {
+          const int sr = nR % NR;
+          if (!(ok = warp_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
+          term.append(sR + sr * kRowTile, sr);
+          const int slot = (e + 2) % kSlots;
+          const uint32_t used = slot == 0 ? gsu0 : (slot == 1 ? gsu1 : gsu2);
+          if (used > 0 && !(ok = warp_wait(&bars->g_free[slot], (used - 1) & 1, wait_ns, abort))) break;
+          if (lane == 0) {
             tc_fence_after();
-            const uint64_t dr = dR + sr * kTile16;
-            const uint32_t gd = tmem + kColG + slot * BN;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t koff16 = ((kk / 4) * kRowChunk + (kk % 4) * 32) >> 4;
-              mma_ss(gd, dQv + (((kk / 4) * kQChunk + (kk % 4) * 32) >> 4), dr + koff16, idS, kk > 0);
-            }
+            mma_scores<D>(tmem + kColG + slot * BN, dq, dR + sr * kTile16, dOnes, dTerm + sr * (kBiasStage >> 4), idS);
             tc_commit(&bars->emptyR[sr]);
-            ++nR;
-            gsu0 += slot == 0;
-            gsu1 += slot == 1;
-            gsu2 += slot == 2;
           }
-          if (!ok) break;
-          tc_commit(&bars->g_full[sb]);
+          ++nR;
+          gsu0 += slot == 0;
+          gsu1 += slot == 1;
+          gsu2 += slot == 2;
+          __syncwarp();
         }
-        if (!ok || w.next_h < 0) break;
-        gt = g0 + w.nks;
-        ++un;
+        if (!ok) break;
+        if (lane == 0) {
+          tc_commit(&bars->g_full[sb]);
+          if (t == nks - 1) tc_commit(&bars->q_empty[un & 1]);
+        }
+        __syncwarp();
       }
+      if (!ok || next_h < 0) break;
+      gt = g0 + nks;
+      ++un;
+    }
+    if (lane == 0) {
       if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->qr_final);
       mbar_wait_own(&bars->qr_final, 0, wait_ns);
@@ -304,56 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
     const int a = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const float sl2 = p.scale_log2e;
-    uint32_t gt = 0, un = 0, nQ = 0;
+    uint32_t gt = 0, un = 0;
     bool ok = true;
 
-    // (q + u), (q + v) for this thread's row of unit k: bf16, 128B-swizzled
-    // K-major shared-memory tiles.
-    auto build_q = [&](uint32_t k) -> bool {
-      if (!warp_wait(&bars->q_full, nQ & 1, wait_ns, abort)) return false;
-      const int h = bars->units[k % kUnitRing].h;
-      const float* bu = p.bias_u + h * D;
-      const float* bv = p.bias_v + h * D;
-      // (The MMAs that read the unit before's are complete.)  A loop of no more
-      // than four, as everything that a step seldom runs: the step's own code
-      // has to stay in the instruction cache beside it.  (8 sequences of 768
-      // tokens over 768 rows: 96.7 us with one at a time, 92.3 with four, 92.7
-      // with all 16.)
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const int kc = c / 8, cc = c % 8;
-        const int off = kc * kQChunk + (a / 8) * 1024 + (a % 8) * 128 + ((cc ^ (a % 8)) * 16);
-        const uint4 raw = *reinterpret_cast<const uint4*>(sQ + off);
-        const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t qu[4], qv[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int d = 8 * c + 2 * e;
-          const float x0 = bf16_lo(w4[e]), x1 = bf16_hi(w4[e]);
-          qu[e] = pack_bf16x2((x0 + __ldg(bu + d)) * p.qsign, (x1 + __ldg(bu + d + 1)) * p.qsign);
-          qv[e] = pack_bf16x2((x0 + __ldg(bv + d)) * p.qsign, (x1 + __ldg(bv + d + 1)) * p.qsign);
-        }
-        *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[0], qu[1], qu[2], qu[3]);
-        *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[0], qv[1], qv[2], qv[3]);
-      }
-      mbar_arrive(&bars->q_empty);
-      ++nQ;
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->q_ready);
-      return true;
-    };
-
     while (any && ok) {
-      // Unit 0 is published before the CTA's first barrier, a later one before
-      // its queries are loaded: one half builds the operands from them, the
-      // other learns of it by the first scores.
-      if (half == 1) {
-        if (!(ok = build_q(un))) break;
-      } else if (un > 0 && !(ok = warp_wait(&bars->s_full[gt & 1], (gt >> 1) & 1, wait_ns, abort))) {
-        break;
-      }
+      // Published before the q tile was loaded.
+      if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
       const TileUnit* unit = &bars->units[un % kUnitRing];
       const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
+      const bool has_next = unit->next_h >= 0;
+      warp_arrive(&bars->q_empty[un & 1]);
       float m_use = -INFINITY;  // running max in log2 units (lazy)
       float l_half = 0.f;       // row sum over this half's columns
       const uint32_t g0 = gt;
@@ -377,16 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         tmem_wait_ld(x1);
         warp_arrive_tc(&bars->s_free[sb]);              // S buffer may be refilled
         warp_arrive_tc(&bars->g_free[t % kSlots]);      // distance tile t-2: last read
-        uint32_t bd[16];
-        window_shift(x0, x1, lane, bd);
-        // x[k] = content + distance score of key column 32*half + k; the
-        // distance value sits at window position 31 - k.
+        // x[k] = content + distance score of key column 32*half + k
         float x[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int i = 31 - k;
-          x[k] = (i & 1) ? add_bf16hi(bd[i >> 1], __uint_as_float(sraw[k]))
-                         : add_bf16lo(bd[i >> 1], __uint_as_float(sraw[k]));
+        {
+          uint32_t bd[32];
+          window_shift_f32(x0, x1, lane, bd);
+          add_columns(sraw, bd, x);
         }
         const int kt = t0 + t;                           // key step of the tile
         const int lim = d0 - BN * kt + a - 32 * half;    // column k visible iff low <= k <= lim
@@ -416,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         // A row with no visible key yet keeps m_new = -inf; its exponents are
         // then taken against 0 (all -inf, so every p is 0).
         const float m_eff = m_new == -INFINITY ? 0.f : m_new;
-        uint32_t pk[16];
+        uint32_t pk[16], pl[16];
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
         const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_eff, -m_eff);
 #pragma unroll
@@ -427,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
             acc1 = __fadd2_rn(acc1, e);
           else
             acc0 = __fadd2_rn(acc0, e);
-          pk[n] = pack_bf16x2(e.x, e.y);
+          split_weights(e, pk[n], pl[n]);
         }
         l_half = l_half * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
         if (half == 0 && t > 0 && __any_sync(0xffffffffu, alpha < 1.f)) {
@@ -449,8 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
         if (g >= 2 && !(ok = warp_wait(&bars->pv_done[sb], ((g - 2) >> 1) & 1, wait_ns, abort))) break;
         tc_fence_after();
         tmem_st16(tmem + lane_base + kColP + sb * 32 + 16 * half, pk);
+        uint8_t* prow = sPlo + sb * kPTile + (a / 8) * 1024 + (a % 8) * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(prow + (((4 * half + c) ^ (a % 8)) * 16)) =
+              make_uint4(pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
         tmem_wait_st();
-        warp_arrive_tc(&bars->p_full[sb]);
+        tc_fence_before();
+        warp_arrive_smem(&bars->p_full[sb]);
       }
       if (!ok) break;
       // Distance tiles nks-2 and nks-1 are not read any more in this unit.
@@ -483,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc128_kernel(const __grid_c
           store_columns<D, O_BF16>(w, a, oc, ov, p.o, p.part, p.args.H);
         }
       }
-      if (unit->next_h < 0) break;
+      if (!has_next) break;
       gt = g0 + nks;
       ++un;
     }

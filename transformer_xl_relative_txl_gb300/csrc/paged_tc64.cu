@@ -22,17 +22,21 @@
 //   * A 32-row box of output whose rows are all the unit's leaves by TMA, the
 //     last rows of a sequence by plain stores.
 //
-// Rounded to bf16, as in the other bf16 calls: (q+u) and (q+v), the operands of
-// the MMAs; the distance scores, which pass the shift two to a register (in
-// fp32 it would take twice the selects, the larger part of a step); the
-// weights, operands again; the output.  Together 3.2e-3 of the exact result
-// (relative L2), where rounding the output alone is 1.7e-3.  Scores, maxima,
-// sums and accumulators are fp32.
+// Rounded to bf16: u and v, as operands, and the output.  Everything else keeps
+// what it has: q is an operand as it comes, the bias terms are products of their
+// own (paged_tiles.cuh), the distance scores pass the shift in fp32, the weights
+// are two bf16 parts each (P.V twice); scores, maxima, sums and accumulators are
+// fp32.  Together 1.7e-3 of the exact result (relative L2), which is the
+// output's rounding.  With (q+u), (q+v), the distance scores and the weights
+// rounded to bf16, as relattn_tc64.cu has them, it was 3.2e-3 and 89 us for what
+// now takes 116: of those 27 us the weights' second part takes 7, the shift 6, the
+// bias products 13.
 //
-// Measured: 22 sequences of 512 tokens over 512 rows, 8 heads, 87 us, 305
+// Measured: 22 sequences of 512 tokens over 512 rows, 8 heads, 116 us, 228
 // TFLOP/s counted without the distances that the shift leaves out.  Bound by
-// the softmax warps, about 1000 instructions a step: the tensor pipe is 17%
-// busy, DRAM 9%, and nearly a fifth of the warps' waiting is for instructions.
+// the softmax warps, about 1250 instructions a step: the tensor pipe is 26%
+// busy, and of the time that warps wait the largest part, a quarter, is for
+// instructions.
 //
 // TMEM (512 columns): O0 [0,64) O1 [64,128) S0 [128,192) S1 [192,256)
 // distance ring [256,512).  Warps: 0-7 softmax (warp w: lane quadrant w%4,
@@ -61,11 +65,12 @@ constexpr int kPvWarp = 10;
 constexpr int kQrWarp = 11;
 constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, three MMA issuers)
 // Register split (launch: 168 per thread, 384 x 168 = 64512): softmax
-// warpgroups 224, producer warpgroup 56; 2*128*224 + 128*56 = 64512.  (At 216
-// the softmax spills, at 56 the search for units, once per CTA, by 19 words;
-// both splits time the same.)
-constexpr uint32_t kRegsSoftmax = 224;
-constexpr uint32_t kRegsProducer = 56;
+// warpgroups 216, producer warpgroup 72; 2*128*216 + 128*72 = 64512.  (The
+// search for units, once per CTA, spills 74 bytes there.  At 56 the issuers'
+// loops spill too, 242 bytes: the same for 512 tokens over 512 rows, 126 us
+// instead of 121 for a mixed batch; 208 and 88 time as these.)
+constexpr uint32_t kRegsSoftmax = 216;
+constexpr uint32_t kRegsProducer = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");
 constexpr uint32_t kColO = 0;    // O0, O1: 64 columns each
 constexpr uint32_t kColS = 128;  // S0, S1: 64 columns each
@@ -79,24 +84,23 @@ constexpr int kRowTile = BN * 128;  // 64 rows x 64 bf16 (8 KB)
 constexpr int kQTile = BM * 128;    // 128 rows x 64 bf16 (16 KB)
 constexpr int NK = 4, NV = 4, NR = 4;  // K, V, R tile stages
 static_assert(NK == NV && NK == NR, "the loader takes one stage count");
-constexpr int kOffQ = 0;                        // raw q tile of the next unit (TMA)
-constexpr int kOffQu = kOffQ + kQTile;          // (q+u): 2 buffers
-constexpr int kOffQv = kOffQu + 2 * kQTile;     // (q+v): 2 buffers
-constexpr int kOffK = kOffQv + 2 * kQTile;
+constexpr int kOffQ = 0;                        // q: 2 buffers
+constexpr int kOffBias = kOffQ + 2 * kQTile;    // u and v: 2 buffers each
+constexpr int kOffK = kOffBias + 4 * BiasTile::kBytes;
 constexpr int kOffV = kOffK + NK * kRowTile;
 constexpr int kOffR = kOffV + NV * kRowTile;
-constexpr int kOffP = kOffR + NR * kRowTile;    // P (bf16): 2 buffers, same layout as (q+u)
-constexpr int kOffRed = kOffP + 2 * kQTile;     // [unit parity][m, l][row] handed to the epilogue
-constexpr int kOffBias = kOffRed + 2 * 2 * BM * 4;  // per softmax warp: 32 dims of u, then of v (fp32)
-constexpr int kOffBar = kOffBias + 8 * 64 * 4;
+constexpr int kOffP = kOffR + NR * kRowTile;    // P (bf16), hi parts: 2 buffers, same layout as q
+constexpr int kOffPlo = kOffP + 2 * kQTile;     // lo parts
+constexpr int kOffRed = kOffPlo + 2 * kQTile;   // [unit parity][m, l][row] handed to the epilogue
+constexpr int kOffBar = kOffRed + 2 * 2 * BM * 4;
 constexpr int kBarBytes = 5120;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Bars {
   uint64_t fullK[NK], emptyK[NK], fullV[NV], emptyV[NV], fullR[NR], emptyR[NR];
-  uint64_t q_full, q_empty;
-  uint64_t q_ready, s_full[2], p_full[2], pv_done[2], o_full, o_free;
+  uint64_t q_full[2], q_empty[2];  // by unit parity
+  uint64_t s_full[2], p_full[2], pv_done[2], o_full, o_free;
   uint64_t sread[4];  // step g's S and distance window have been read (index g % 4, phase g / 4)
   uint64_t mma_final, pv_final, qr_final;
   uint64_t lbar[4];   // per quadrant: the non-owning warp's (m, l) of a unit is in `red`
@@ -115,14 +119,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   uint8_t* sQ = smem + kOffQ;
-  uint8_t* sQu = smem + kOffQu;
-  uint8_t* sQv = smem + kOffQv;
+  uint8_t* sB = smem + kOffBias;
   uint8_t* sK = smem + kOffK;
   uint8_t* sV = smem + kOffV;
   uint8_t* sR = smem + kOffR;
   uint8_t* sP = smem + kOffP;
   float* red = reinterpret_cast<float*>(smem + kOffRed);
-  float* sbias = reinterpret_cast<float*>(smem + kOffBias);
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   volatile int* abort = &bars->abort;
 
@@ -145,10 +147,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       mbar_init(&bars->s_full[s], 2);  // content and distance MMAs of a step
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->pv_done[s], 1);
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 10);  // the softmax warps have seen the unit, both score products are done
     }
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 8);
-    mbar_init(&bars->q_ready, 8);
     mbar_init(&bars->o_full, 1);
     mbar_init(&bars->o_free, 4);
     mbar_init(&bars->mma_final, 1);
@@ -179,42 +180,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   if (warp == kLoaderWarp) {
     // ============================ TMA loader ===============================
     setmaxnreg_dec<kRegsProducer>();
-    run_tile_loader<D, NK, false, true, STALL>(bars, tm, p, sQ, sK, sV, sR);
+    run_tile_loader<D, NK, false, STALL>(bars, tm, p, sQ, sK, sV, sR);
   } else if (warp == kMmaWarp) {
     // ===================== content-score MMA issuer ========================
     setmaxnreg_dec<kRegsProducer>();
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
-      const uint64_t dQu = sdesc_sw128(smem_u32(sQu), 16, 1024);
-      const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
-      constexpr uint32_t kTile16 = kRowTile >> 4;
-      uint32_t nK = 0, gt = 0, un = 0;
-      bool ok = true;
-      while (any && ok) {
-        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
-        const TileUnit w = bars->units[un % kUnitRing];
+    const uint32_t idS = idesc_bf16(128, BN, false, false) | (p.negative ? kNegateA : 0u);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dU = sdesc_sw128(smem_u32(sB), 16, 0);
+    const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+    constexpr uint32_t kTile16 = kRowTile >> 4;
+    BiasTile u;
+    if (any) u.load(p.bias_u, bars->units[0].h);
+    uint32_t gt = 0, un = 0;  // gt: steps, and K tiles, so far
+    bool ok = true;
+    while (any && ok) {
+      if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
+      const int nks = bars->units[un % kUnitRing].nks, next_h = bars->units[un % kUnitRing].next_h;
+      const uint32_t g0 = gt;
+      // The bias buffer was read by the unit before the last, whose products are
+      // done once the scores of step g0 - 2 have been read.
+      if (g0 >= 2 && !(ok = warp_wait(&bars->sread[(g0 - 2) & 3], ((g0 - 2) >> 2) & 1, wait_ns, abort))) break;
+      u.store(sB + (un & 1) * BiasTile::kBytes);
+      if (next_h >= 0) u.load(p.bias_u, next_h);
+      if (lane == 0) {
         tc_fence_after();
-        const uint32_t g0 = gt;
-        for (int t = 0; t < w.nks; ++t) {
+        const uint64_t dq = dQ + (un & 1) * (kQTile >> 4), du = dU + (un & 1) * (BiasTile::kBytes >> 4);
+        for (int t = 0; t < nks; ++t) {
           const uint32_t g = g0 + t, sb = g & 1;
           // S buffer sb was last read by step g-2.
           if (g >= 2 && !(ok = mbar_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
-          const int sk = nK % NK;
-          if (!(ok = mbar_wait(&bars->fullK[sk], (nK / NK) & 1, wait_ns, abort))) break;
+          const int sk = g % NK;
+          if (!(ok = mbar_wait(&bars->fullK[sk], (g / NK) & 1, wait_ns, abort))) break;
           tc_fence_after();
-          const uint64_t dk = dK + sk * kTile16;
-          const uint32_t sd = tmem + kColS + sb * BN;
-          const uint64_t dq = dQu + (un & 1) * (kQTile >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) mma_ss(sd, dq + kk * 2, dk + kk * 2, idS, kk > 0);
+          mma_scores64(tmem + kColS + sb * BN, dq, du, dK + sk * kTile16, idS);
           tc_commit(&bars->emptyK[sk]);
           tc_commit(&bars->s_full[sb]);
-          ++nK;
         }
-        if (!ok || w.next_h < 0) break;
-        gt = g0 + w.nks;
-        ++un;
+        tc_commit(&bars->q_empty[un & 1]);
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok || next_h < 0) break;
+      gt = g0 + nks;
+      ++un;
+    }
+    if (lane == 0) {
       if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->mma_final);
       mbar_wait_own(&bars->mma_final, 0, wait_ns);
@@ -222,23 +231,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   } else if (warp == kQrWarp) {
     // ==================== distance-score MMA issuer ========================
     setmaxnreg_dec<kRegsProducer>();
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, BN, false, false);
-      const uint64_t dQv = sdesc_sw128(smem_u32(sQv), 16, 1024);
-      const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
-      constexpr uint32_t kTile16 = kRowTile >> 4;
-      uint32_t nR = 0, gt = 0, un = 0;
-      // Last global step that reads the tile now in each ring slot (-1: none).
-      int last0 = -1, last1 = -1, last2 = -1, last3 = -1;
-      int rb = 0;  // ring slot of the first distance tile (-2) of the unit
-      bool ok = true;
-      while (any && ok) {
-        if (!(ok = mbar_wait(&bars->q_ready, un & 1, wait_ns, abort))) break;
-        const TileUnit w = bars->units[un % kUnitRing];
+    const uint32_t idS = idesc_bf16(128, BN, false, false) | (p.negative ? kNegateA : 0u);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dV = sdesc_sw128(smem_u32(sB + 2 * BiasTile::kBytes), 16, 0);
+    const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
+    constexpr uint32_t kTile16 = kRowTile >> 4;
+    BiasTile v;
+    if (any) v.load(p.bias_v, bars->units[0].h);
+    uint32_t nR = 0, gt = 0, un = 0;
+    // Last global step that reads the tile now in each ring slot (-1: none).
+    int last0 = -1, last1 = -1, last2 = -1, last3 = -1;
+    int rb = 0;  // ring slot of the first distance tile (-2) of the unit
+    bool ok = true;
+    while (any && ok) {
+      if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
+      const int nks = bars->units[un % kUnitRing].nks, next_h = bars->units[un % kUnitRing].next_h;
+      const uint32_t g0 = gt;
+      if (g0 >= 2 && !(ok = warp_wait(&bars->sread[(g0 - 2) & 3], ((g0 - 2) >> 2) & 1, wait_ns, abort))) break;
+      v.store(sB + (2 + (un & 1)) * BiasTile::kBytes);
+      if (next_h >= 0) v.load(p.bias_v, next_h);
+      if (lane == 0) {
         tc_fence_after();
-        const uint32_t g0 = gt;
-        const uint64_t dq = dQv + (un & 1) * (kQTile >> 4);
-        for (int t = 0; ok && t < w.nks; ++t) {
+        const uint64_t dq = dQ + (un & 1) * (kQTile >> 4), dv = dV + (un & 1) * (BiasTile::kBytes >> 4);
+        for (int t = 0; ok && t < nks; ++t) {
           const uint32_t sb = (g0 + t) & 1;
           for (int e = (t == 0 ? -2 : t); e <= t; ++e) {
             const int slot = (rb + e + 2) & (kSlots - 1);
@@ -253,13 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
             const int sr = nR % NR;
             if (!(ok = mbar_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
             tc_fence_after();
-            const uint64_t dr = dR + sr * kTile16;
-            const uint32_t gd = tmem + kColG + slot * BN;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) mma_ss(gd, dq + kk * 2, dr + kk * 2, idS, kk > 0);
+            mma_scores64(tmem + kColG + slot * BN, dq, dv, dR + sr * kTile16, idS);
             tc_commit(&bars->emptyR[sr]);
             ++nR;
-            const int lr = static_cast<int>(g0) + min(e + 2, w.nks - 1);  // tile e's last reader
+            const int lr = static_cast<int>(g0) + min(e + 2, nks - 1);  // tile e's last reader
             last0 = slot == 0 ? lr : last0;
             last1 = slot == 1 ? lr : last1;
             last2 = slot == 2 ? lr : last2;
@@ -268,11 +280,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           if (!ok) break;
           tc_commit(&bars->s_full[sb]);
         }
-        if (!ok || w.next_h < 0) break;
-        gt = g0 + w.nks;
-        ++un;
-        rb = (rb + w.nks + 2) & (kSlots - 1);
+        tc_commit(&bars->q_empty[un & 1]);
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok || next_h < 0) break;
+      gt = g0 + nks;
+      ++un;
+      rb = (rb + nks + 2) & (kSlots - 1);
+    }
+    if (lane == 0) {
       if (!ok) report_timeout(abort, p.args.status);
       tc_commit(&bars->qr_final);
       mbar_wait_own(&bars->qr_final, 0, wait_ns);
@@ -283,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
     const uint64_t dV = sdesc_sw128(smem_u32(sV), BN * 128, 1024);
     const uint64_t dP = sdesc_sw128(smem_u32(sP), 16, 1024);
+    constexpr uint32_t kLo16 = (kOffPlo - kOffP) >> 4;
     constexpr uint32_t kTile16 = kRowTile >> 4;
     uint32_t g = 0, un = 0;  // g: steps, and V tiles, so far
     bool ok = true;
@@ -314,6 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             mma_ss(od, dp + kk * 2, dv + ((kk * 16 * 128) >> 4), idO, t >= 2 || kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk) mma_ss(od, dp + kLo16 + kk * 2, dv + ((kk * 16 * 128) >> 4), idO, 1);
           tc_commit(&bars->emptyV[sv]);
           tc_commit(&bars->pv_done[g & 1]);
           if (t == nks - 1) tc_commit(&bars->o_full);
@@ -336,68 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     const int a = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const float sl2 = p.scale_log2e;
-    uint32_t gt = 0, un = 0, nQ = 0;
+    uint32_t gt = 0, un = 0;
     int rb = 0;  // ring slot of the unit's distance tile -2 (continues across units)
     bool store_pending = false;  // lane 0 has a TMA store out of this warp's P quadrant
     bool ok = true;
 
-    // (q + u), (q + v) of a unit into buffer `buf` (128B-swizzled K-major
-    // tiles): this warp's row, head dimensions [32 par, 32 par + 32).
-    // bu_l, bv_l: this lane's dims 32 par + lane of the unit's u and v (loaded
-    // ahead by the caller, so their latency overlaps other work).
-    auto build_q = [&](int buf, float bu_l, float bv_l) -> bool {
-      // This warp's 32 dims of u and v, staged once for broadcast reads.
-      float* sb_w = sbias + warp * 64;
-      sb_w[lane] = bu_l;
-      sb_w[32 + lane] = bv_l;
-      __syncwarp();
-      if (!warp_wait(&bars->q_full, nQ & 1, wait_ns, abort)) return false;
-      // Short code, as with everything that a step seldom runs: the step's own
-      // has to stay in the instruction cache beside it (22 sequences of 512
-      // tokens over 512 rows: 93 us with these loops and the epilogue's
-      // unrolled, 87 so.  One copy of this code instead of three, by a loop
-      // that also turns where a warp has no step: 95).
-#pragma unroll 2
-      for (int j = 0; j < 4; ++j) {
-        const int c = 4 * par + j;
-        const int at = (a / 8) * 1024 + (a % 8) * 128 + ((c ^ (a % 8)) * 16), off = buf * kQTile + at;
-        const uint4 raw = *reinterpret_cast<const uint4*>(sQ + at);
-        const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
-        const float4 u0 = *reinterpret_cast<const float4*>(sb_w + 8 * j);
-        const float4 u1 = *reinterpret_cast<const float4*>(sb_w + 8 * j + 4);
-        const float4 v0 = *reinterpret_cast<const float4*>(sb_w + 32 + 8 * j);
-        const float4 v1 = *reinterpret_cast<const float4*>(sb_w + 32 + 8 * j + 4);
-        const float ub[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-        const float vb[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        uint32_t qu[4], qv[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x0 = bf16_lo(w4[e]), x1 = bf16_hi(w4[e]);
-          qu[e] = pack_bf16x2((x0 + ub[2 * e]) * p.qsign, (x1 + ub[2 * e + 1]) * p.qsign);
-          qv[e] = pack_bf16x2((x0 + vb[2 * e]) * p.qsign, (x1 + vb[2 * e + 1]) * p.qsign);
-        }
-        *reinterpret_cast<uint4*>(sQu + off) = make_uint4(qu[0], qu[1], qu[2], qu[3]);
-        *reinterpret_cast<uint4*>(sQv + off) = make_uint4(qv[0], qv[1], qv[2], qv[3]);
-      }
-      warp_arrive(&bars->q_empty);
-      ++nQ;
-      warp_arrive_smem(&bars->q_ready);
-      __syncwarp();  // sb_w is rewritten by the next build
-      return true;
-    };
-
-    auto bias_of = [&](int h, const float* bias) -> float { return __ldg(bias + h * D + 32 * par + lane); };
-    if (any) ok = build_q(0, bias_of(bars->units[0].h, p.bias_u), bias_of(bars->units[0].h, p.bias_v));
-
     while (any && ok) {
-      // Published before the q tile that the build above waited for.
+      // Published before the q tile was loaded.
+      if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
       const TileUnit* unit = &bars->units[un % kUnitRing];
-      const int next_h = unit->next_h, nks = unit->nks, t0 = unit->t0, d0 = unit->d0;
-      const int start = unit->start;
+      const int nks = unit->nks, t0 = unit->t0, d0 = unit->d0, start = unit->start;
+      const bool has_next = unit->next_h >= 0;
+      warp_arrive(&bars->q_empty[un & 1]);
       const uint32_t g0 = gt;
-      const bool has_next = next_h >= 0;
-      const float bu_next = has_next ? bias_of(next_h, p.bias_u) : 0.f;
-      const float bv_next = has_next ? bias_of(next_h, p.bias_v) : 0.f;
       const int tl = nks - 1;
       const int first = (par - static_cast<int>(g0)) & 1;  // first local step of this warp
       float m_use = -INFINITY;  // running max in log2 units (lazy)
@@ -421,38 +391,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         const bool diag = d0 - BN * kt + quad * 32 < 63;  // some lane of the warp masks
         const float m_old = m_use;
         float m_new = m_use;
-        // All of this step's TMEM reads at once -- the 96-distance window and
-        // both halves of S -- then one arrival hands the S buffer and the
-        // ring slots back to the MMA issuers.
+        // Half of the columns at a time: the fp32 windows of both, 160 values with
+        // the scores, would not leave the shifts their registers.  The middle of
+        // the 96-distance window serves both halves; behind the second half's
+        // loads one arrival hands the S buffer and the ring slots back.
         float x[64];  // scores of the step's 64 columns
         {
-          uint32_t bd0[16], bd1[16];
-          uint32_t s0[32], s1[32];
+          uint32_t xa[32], xb[32], bd[32];
           {
-            uint32_t xa[32], xb[32], xc[32];
-            tmem_ld32(tmem + lane_base + zcol(32 * quad), xa);
+            uint32_t s0[32], xc[32];
             tmem_ld32(tmem + lane_base + zcol(32 * quad + 32), xb);
             tmem_ld32(tmem + lane_base + zcol(32 * quad + 64), xc);
             tmem_ld32(sc, s0);
-            tmem_ld32(sc + 32, s1);
-            tmem_wait_ld(xa);
             tmem_wait_ld(xb);
             tmem_wait_ld(xc);
             tmem_wait_ld(s0);
-            tmem_wait_ld(s1);
-            warp_arrive_tc(&bars->sread[g & 3]);
-            uint32_t pa[16], pb[16], pc[16];
-            pack32(xa, pa);
-            pack32(xb, pb);
-            pack32(xc, pc);
             // columns 0-31 use window positions [32, 96), columns 32-63 [0, 64)
-            window_shift_packed(pb, pc, lane, bd0);
-            window_shift_packed(pa, pb, lane, bd1);
+            window_shift_f32(xb, xc, lane, bd);
+            add_columns(s0, bd, x);
           }
-          float* x0 = x;
-          float* x1 = x + 32;
-          add_window(s0, bd0, x0);
-          add_window(s1, bd1, x1);
+          uint32_t s1[32];
+          tmem_ld32(tmem + lane_base + zcol(32 * quad), xa);
+          tmem_ld32(sc + 32, s1);
+          tmem_wait_ld(xa);
+          tmem_wait_ld(s1);
+          warp_arrive_tc(&bars->sread[g & 3]);
+          window_shift_f32(xa, xb, lane, bd);
+          add_columns(s1, bd, x + 32);
         }
         if (diag || low > 0) {
           const uint32_t v0 = visible_columns(low, lim), v1 = visible_columns(low - 32, lim - 32);
@@ -504,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         float sum;
         {
           // Exponentials, their row sum, and the P row a into buffer sb
-          // (128B-swizzled K-major, as (q+u)), eight columns per store.
+          // (128B-swizzled K-major, as q), eight columns per store.
           uint8_t* prow = sP + sb * kQTile + (a / 8) * 1024 + (a % 8) * 128;
           float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
           const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_eff, -m_eff);
 #pragma unroll
           for (int c = 0; c < BN / 8; ++c) {
-            uint32_t pk[4];
+            uint32_t pk[4], pl[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int n = 4 * c + i;
@@ -520,27 +485,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
                 acc1 = __fadd2_rn(acc1, e);
               else
                 acc0 = __fadd2_rn(acc0, e);
-              pk[i] = pack_bf16x2(e.x, e.y);
+              split_weights(e, pk[i], pl[i]);
             }
-            *reinterpret_cast<uint4*>(prow + ((c ^ (a % 8)) * 16)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            uint8_t* at = prow + ((c ^ (a % 8)) * 16);
+            *reinterpret_cast<uint4*>(at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(at + (kOffPlo - kOffP)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
           }
           sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
         }
         l_run = l_run * alpha + sum;
         tc_fence_before();  // orders the O rescale's tcgen05.st before the arrive
         warp_arrive_smem(&bars->p_full[sb]);
-        // The next unit's (q+u), (q+v) go to the other buffer once this
-        // warp's first step of this unit has seen its scores: the MMAs of the
-        // unit before, which read that buffer, are complete by then.
-        if (t == first && has_next && !(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
       }
       if (!ok) break;
-      if (first > tl && has_next) {
-        // No step of this unit: build after its last step's scores instead.
-        const uint32_t gl = g0 + tl;
-        if (!(ok = warp_wait(&bars->s_full[gl & 1], (gl >> 1) & 1, wait_ns, abort))) break;
-        if (!(ok = build_q((un + 1) & 1, bu_next, bv_next))) break;
-      }
       // The warps of the unit's last step merge the two accumulators and
       // write the output; the other parity hands over its (m, l) and moves on
       // to the next unit, whose first step is its own.

@@ -91,6 +91,168 @@ __device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8
   __syncwarp();
 }
 
+// The score products' bias terms: (q + u) . k = q . k + u . k, and q . k has exact
+// operands, where q + u rounded to bf16 is off by 1.65e-3 (rms) of a score's
+// content part, as much as the output's own rounding.  u . k is a number a key,
+// the same for every query.
+//
+// D = 64: products of their own, u rounded to bf16 (off by 1.65e-3 of u . k, which
+// a bias is far smaller than q for), the same 128 rows, so that the tile is one
+// group of 8 rows (1 KB, 128-byte swizzle) that every row group reads: a stride
+// of 0 between groups in the descriptor.  A second part of u would be 18 us more
+// of 117 (22 sequences of 512 tokens over 512 rows, 8 heads), the way of D = 128
+// 13 more.
+struct BiasTile {
+  static constexpr int kBytes = 1024;
+  uint32_t x;  // dimensions 2 l and 2 l + 1, l the lane
+  __device__ __forceinline__ void load(const float* bias, int h) {
+    const float* at = bias + static_cast<size_t>(h) * 64 + 2 * (threadIdx.x & 31);
+    x = pack_bf16x2(__ldg(at), __ldg(at + 1));
+  }
+  // One warp.
+  __device__ __forceinline__ void store(uint8_t* tile) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      *reinterpret_cast<uint32_t*>(tile + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4) = x;
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+};
+// One thread: D[128 x 64] = (q + bias) B^T of a tile B of 64 rows of 64.
+__device__ __forceinline__ void mma_scores64(uint32_t d, uint64_t q, uint64_t bias, uint64_t b, uint32_t id) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) mma_ss(d, q + kk * 2, b + kk * 2, id, kk > 0);
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) mma_ss(d, bias + kk * 2, b + kk * 2, id, 1);
+}
+
+// D = 128: the issuer's warp computes the terms of a landed tile, u in two bf16
+// parts, and appends them to the tile in three (24 bits), which one more product
+// of 16 columns multiplies by ones: 110 us, and 124 as products of their own with
+// one part of u, 148 with two (8 sequences of 768 tokens over 768 rows, 8 heads).
+//
+// Per stage of the ring, 2 KB: the 64 rows' first 8 columns, 16 bytes a row, then
+// as many zeros; behind the stages 8 rows of ones (three columns), which all of
+// the 128 rows read.
+constexpr int kBiasStage = 2 * kStepKeys * 16;
+constexpr int kBiasOnes = 256;
+
+// One warp's.
+template <int D, int STAGES>
+struct BiasTerm {
+  static constexpr int kBytes = STAGES * kBiasStage + kBiasOnes;
+  uint8_t* area;
+  uint32_t u[D / 16][2];  // right-hand fragments: column n of 8 has part n % 2 of u
+
+  // At the kernel's head: the parts of the area that stay.
+  __device__ __forceinline__ explicit BiasTerm(uint8_t* at) : area(at) {
+    constexpr int kOnes = STAGES * kBiasStage / 16;
+    for (int e = threadIdx.x & 31; e < kBytes / 16; e += 32)
+      reinterpret_cast<uint4*>(area)[e] =
+          e >= kOnes && e < kOnes + 8 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void load(const float* bias, int h) {
+    const int lane = threadIdx.x & 31;
+    const float* at = bias + static_cast<size_t>(h) * D + 2 * (lane & 3);
+#pragma unroll
+    for (int e = 0; e < D / 8; ++e) {
+      const float x = __ldg(at + 8 * e), y = __ldg(at + 8 * e + 1);
+      const uint32_t hi = pack_bf16x2(x, y);
+      u[e / 2][e % 2] = lane >> 2 & 1 ? pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi)) : hi;
+    }
+  }
+  // The terms of a tile's 64 rows (128-byte swizzle): of each 16 rows, lane l has
+  // those of rows l / 4 and l / 4 + 8, and puts down the (l % 4)-th 16's.
+  // (As multiply-adds it is 119 us in a loop, 194 in a line: the softmax's code
+  // pushes it out of the instruction cache between any two tiles.)
+  __device__ __forceinline__ void append(const uint8_t* tile, int s) const {
+    const int lane = threadIdx.x & 31, r16 = lane & 15, half = lane >> 4;
+    float mine[2] = {0.f, 0.f};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        uint32_t a[4];
+        ldsm4(smem_u32(tile) + (e / 4) * kStepKeys * 128 + (16 * y + r16) * 128 +
+                  ((((e % 4) * 2 + half) ^ (r16 & 7)) << 4), a);
+        mma16816(z, a, u[e][0], u[e][1]);
+      }
+      if ((lane & 3) == y) mine[0] = z[0] + z[1], mine[1] = z[2] + z[3];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // (A term that is not finite has no further parts.)
+      const float hi = __bfloat162float(__float2bfloat16(mine[i]));
+      const float rest = isfinite(hi) ? mine[i] - hi : 0.f;
+      const uint32_t two = pack_bf16x2(hi, rest);
+      *reinterpret_cast<uint4*>(area + s * kBiasStage + (16 * (lane & 3) + 8 * i + (lane >> 2)) * 16) =
+          make_uint4(two, pack_bf16x2(rest - bf16_hi(two), 0.f), 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  __device__ __forceinline__ uint64_t ones_desc() const {
+    return sdesc_plain(smem_u32(area + STAGES * kBiasStage), kBiasOnes / 2, 0);
+  }
+  __device__ __forceinline__ uint64_t term_desc() const { return sdesc_plain(smem_u32(area), kBiasStage / 2, 128); }
+};
+
+// One thread: D[128 x 64] = q B^T + the bias term, of a tile B of 64 rows.  q, b:
+// descriptors (64-dimension chunks kTileQueries and kStepKeys rows apart), ones,
+// term: of the bias area.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t b, uint64_t ones, uint64_t term,
+                                           uint32_t id) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_ss(d, q + (((kk / 4) * kTileQueries * 128 + (kk % 4) * 32) >> 4),
+           b + (((kk / 4) * kStepKeys * 128 + (kk % 4) * 32) >> 4), id, kk > 0);
+  mma_ss(d, ones, term, id, 1);
+}
+
+// Per-lane window shift in fp32: lo, hi hold the window X[0..63]; out[k] =
+// X[lane + 32 - k], k = 0..31, the distance value of key column k.  (In bf16
+// pairs, packed and unpacked, it is 102 selects of 372 shorter, less the adds
+// that take two columns at a time here; it rounds the distance part to 2^-8.)
+__device__ __forceinline__ void window_shift_f32(const uint32_t (&lo)[32], const uint32_t (&hi)[32], int lane,
+                                                 uint32_t (&out)[32]) {
+  uint32_t R[63];
+#pragma unroll
+  for (int i = 0; i < 63; ++i) R[i] = i < 31 ? lo[i + 1] : hi[i - 31];
+  const bool b16 = lane & 16, b8 = lane & 8, b4 = lane & 4, b2 = lane & 2, b1 = lane & 1;
+#pragma unroll
+  for (int j = 0; j < 47; ++j) R[j] = b16 ? R[j + 16] : R[j];
+#pragma unroll
+  for (int j = 0; j < 39; ++j) R[j] = b8 ? R[j + 8] : R[j];
+#pragma unroll
+  for (int j = 0; j < 35; ++j) R[j] = b4 ? R[j + 4] : R[j];
+#pragma unroll
+  for (int j = 0; j < 33; ++j) R[j] = b2 ? R[j + 2] : R[j];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) out[k] = b1 ? R[32 - k] : R[31 - k];
+}
+// x[k] = s[k] + d[k]
+__device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const uint32_t (&d)[32], float* x) {
+#pragma unroll
+  for (int n = 0; n < 16; ++n) {
+    const float2 y = __fadd2_rn(make_float2(__uint_as_float(s[2 * n]), __uint_as_float(s[2 * n + 1])),
+                                make_float2(__uint_as_float(d[2 * n]), __uint_as_float(d[2 * n + 1])));
+    x[2 * n] = y.x;
+    x[2 * n + 1] = y.y;
+  }
+}
+
+// A pair of weights as two bf16 pairs, hi + lo.
+__device__ __forceinline__ void split_weights(float2 e, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(e.x, e.y);
+  const float2 rest = __ffma2_rn(make_float2(bf16_lo(hi), bf16_hi(hi)), make_float2(-1.f, -1.f), e);
+  lo = pack_bf16x2(rest.x, rest.y);
+}
+
 // Results of a unit, o normalised by its own sum, lse2 its log2-domain lse
 // (-inf: no visible key).  A whole unit's go to the output, rows past its
 // queries are not written; a piece's go to the workspace, joined by the kernel
@@ -141,7 +303,7 @@ struct TileParams {
   void* o;
   float* lse;
   float scale_log2e;  // |scale| * log2(e)
-  float qsign;        // sign of scale, folded into (q+u), (q+v)
+  bool negative;      // of scale: the score products negate their A operand
   PlanCut* cuts;
   float* part;
   unsigned long long wait_ns;
@@ -174,15 +336,14 @@ struct TileMaps {
 // while a K stage is free as soon as its score MMA is done; with V(t) beside
 // K(t), K would wait for the P.V of step t - NS and land just in time (D = 128,
 // two stages: 167 us instead of 145 for 152 units of 100 steps; at D = 64, with
-// four, 102 us so and 108 with a V tile that trails).  AHEAD: the raw q tile of a unit is
-// loaded behind the first step of the unit before (D = 64: its operands have
-// two buffers and are built during that unit); otherwise at the head of its
-// own, behind the last V tile of the unit before.
+// four, 102 us so and 108 with a V tile that trails).  The q tile of a unit is
+// loaded ahead of its first step, into the one of two buffers that the score
+// products of the unit before the last have read.
 //
 // STALL: the kernels' instances for the test hook, in which the loader of even
 // CTAs, and the P.V issuer of odd ones, stops behind its first unit's first
 // step.  (As a test of a parameter it cost the D = 64 kernel 2 to 4 us of 90.)
-template <int D, int NS, bool TRAIL, bool AHEAD, bool STALL, typename Bars>
+template <int D, int NS, bool TRAIL, bool STALL, typename Bars>
 __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
                                                 uint8_t* sK, uint8_t* sV, uint8_t* sR) {
   static_assert((NS & (NS - 1)) == 0, "stage arithmetic");
@@ -200,7 +361,7 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
   uint8_t* const mine = stages + (is_r ? 0 : off * 128);
   if (lane <= 8 && leads) tma_prefetch_desc(map);
   uint32_t n = 0;   // tiles of this lane's ring so far
-  uint32_t nQ = 0;  // q tiles so far
+  uint32_t loaded = 0;  // q tiles so far
   bool ok = true, bad = false;
 
   // One tile of each ring whose lanes are `active`.
@@ -229,14 +390,16 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
     if (active) ++n;
   };
   auto load_q = [&](uint32_t un) {
-    if (!(ok = warp_wait(&bars->q_empty, (nQ & 1) ^ 1, p.wait_ns, abort))) return;
+    const uint32_t s = un & 1;
+    if (!(ok = warp_wait(&bars->q_empty[s], ((un >> 1) & 1) ^ 1, p.wait_ns, abort))) return;
     if (lane == 0) {
       const TileUnit& w = bars->units[un % kUnitRing];
-      mbar_arrive_expect_tx(&bars->q_full, kQChunk * (D / 64));
+      mbar_arrive_expect_tx(&bars->q_full[s], kQChunk * (D / 64));
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) tma_load_3d(sQ + c * kQChunk, &tm.q, &bars->q_full, c * 64, w.h, w.row0);
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(sQ + (s * (D / 64) + c) * kQChunk, &tm.q, &bars->q_full[s], c * 64, w.h, w.row0);
     }
-    ++nQ;
+    loaded = un + 1;
   };
   // A tile of keys: this lane's page (-1: no live row), the row in the page,
   // the head, the tile's bytes.
@@ -280,7 +443,6 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
       tc_fence_after();
       if (known == 0) break;
     }
-    if (AHEAD && un + 1 < known) load_q(un + 1);
     // Tiles, up to a unit's first step.
     bool head = false, done = false;
     while (ok && !head) {
@@ -289,11 +451,8 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
           done = true;
           break;
         }
-        if (!AHEAD) {
-          if (TRAIL) release();
-          if (ok) load_q(un);
-          if (!ok) break;
-        }
+        load_q(un);
+        if (!ok) break;
         const TileUnit& w = bars->units[un % kUnitRing];
         h = w.h, d0 = w.d0, start = w.start, last = w.last, t0 = w.t0, tend = t0 + (stall ? 1 : w.nks);
         row = p.args.book.table + static_cast<size_t>(w.slot) * p.args.book.max_pages;
@@ -331,7 +490,8 @@ __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, 
   if (bad) atomicOr(p.args.status, kStatusPagesBit);
   if (!ok && lane == 0) report_timeout(abort, p.args.status);
   // This warp's own copies land before the CTA may exit.
-  if (nQ > 0) mbar_wait_own(&bars->q_full, (nQ - 1) & 1, p.wait_ns);
+  for (uint32_t un = loaded > 2 ? loaded - 2 : 0; un < loaded; ++un)
+    mbar_wait_own(&bars->q_full[un & 1], (un >> 1) & 1, p.wait_ns);
   if (leads)
     for (uint32_t s = 0; s < NS && s < n; ++s) {
       const uint32_t z = s + ((n - 1 - s) / NS) * NS;
