@@ -29,14 +29,13 @@
 // fp32.  Together 1.7e-3 of the exact result (relative L2), which is the
 // output's rounding.  With (q+u), (q+v), the distance scores and the weights
 // rounded to bf16, as relattn_tc64.cu has them, it was 3.2e-3 and 89 us for what
-// now takes 116: of those 27 us the weights' second part takes 7, the shift 6, the
-// bias products 13.
+// now takes 101; the bias products take 6 of that, those with the weights' second
+// parts 2.
 //
-// Measured: 22 sequences of 512 tokens over 512 rows, 8 heads, 116 us, 228
+// Measured: 22 sequences of 512 tokens over 512 rows, 8 heads, 101 us, 263
 // TFLOP/s counted without the distances that the shift leaves out.  Bound by
-// the softmax warps, about 1250 instructions a step: the tensor pipe is 26%
-// busy, and of the time that warps wait the largest part, a quarter, is for
-// instructions.
+// the softmax warps, about 1300 instructions a step, half of them on the ALU
+// pipe (52% busy; the tensor pipe 27%, DRAM 8%).
 //
 // TMEM (512 columns): O0 [0,64) O1 [64,128) S0 [128,192) S1 [192,256)
 // distance ring [256,512).  Warps: 0-7 softmax (warp w: lane quadrant w%4,
@@ -65,12 +64,11 @@ constexpr int kPvWarp = 10;
 constexpr int kQrWarp = 11;
 constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, three MMA issuers)
 // Register split (launch: 168 per thread, 384 x 168 = 64512): softmax
-// warpgroups 216, producer warpgroup 72; 2*128*216 + 128*72 = 64512.  (The
-// search for units, once per CTA, spills 74 bytes there.  At 56 the issuers'
-// loops spill too, 242 bytes: the same for 512 tokens over 512 rows, 126 us
-// instead of 121 for a mixed batch; 208 and 88 time as these.)
-constexpr uint32_t kRegsSoftmax = 216;
-constexpr uint32_t kRegsProducer = 72;
+// warpgroups 200, producer warpgroup 104; 2*128*200 + 128*104 = 64512.  (22
+// sequences of 512 tokens over 512 rows 100.4 us; 101.9 with 208 and 88, 102.9
+// with 216 and 72, where the producers spill, 100.8 with 184 and 136.)
+constexpr uint32_t kRegsSoftmax = 200;
+constexpr uint32_t kRegsProducer = 104;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");
 constexpr uint32_t kColO = 0;    // O0, O1: 64 columns each
 constexpr uint32_t kColS = 128;  // S0, S1: 64 columns each
@@ -391,52 +389,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         const bool diag = d0 - BN * kt + quad * 32 < 63;  // some lane of the warp masks
         const float m_old = m_use;
         float m_new = m_use;
-        // Half of the columns at a time: the fp32 windows of both, 160 values with
-        // the scores, would not leave the shifts their registers.  The middle of
-        // the 96-distance window serves both halves; behind the second half's
-        // loads one arrival hands the S buffer and the ring slots back.
-        float x[64];  // scores of the step's 64 columns
-        {
-          uint32_t xa[32], xb[32], bd[32];
-          {
-            uint32_t s0[32], xc[32];
-            tmem_ld32(tmem + lane_base + zcol(32 * quad + 32), xb);
-            tmem_ld32(tmem + lane_base + zcol(32 * quad + 64), xc);
-            tmem_ld32(sc, s0);
-            tmem_wait_ld(xb);
-            tmem_wait_ld(xc);
-            tmem_wait_ld(s0);
-            // columns 0-31 use window positions [32, 96), columns 32-63 [0, 64)
-            window_shift_f32(xb, xc, lane, bd);
-            add_columns(s0, bd, x);
+        // Scores, half of the columns a turn, back into their place in tensor memory;
+        // then, the maximum known, the weights, half a turn.  The step's code is what
+        // bounds it otherwise: with all 64 columns in a line, in registers, 117 us for
+        // 22 sequences of 512 tokens over 512 rows, a quarter of the warps' waiting for
+        // instructions, and 101 so, a tenth.  (The weights in quarters 105, the scores
+        // alone in halves 129.)
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int hc = 0; hc < 64; hc += 32) {
+          uint32_t s32[32], w0[32], w1[32], bd[32];
+          tmem_ld32(tmem + lane_base + zcol(32 * quad + 32 - hc), w0);
+          tmem_ld32(tmem + lane_base + zcol(32 * quad + 64 - hc), w1);
+          tmem_ld32(sc + hc, s32);
+          tmem_wait_ld(w0);
+          tmem_wait_ld(w1);
+          tmem_wait_ld(s32);
+          float x[32];
+          window_shift_f32(w0, w1, lane, bd);
+          add_columns(s32, bd, x);
+          if (diag || low > 0) {
+            const uint32_t v = visible_columns(low - hc, lim - hc);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = v >> k & 1 ? x[k] : -INFINITY;
           }
-          uint32_t s1[32];
-          tmem_ld32(tmem + lane_base + zcol(32 * quad), xa);
-          tmem_ld32(sc + 32, s1);
-          tmem_wait_ld(xa);
-          tmem_wait_ld(s1);
-          warp_arrive_tc(&bars->sread[g & 3]);
-          window_shift_f32(xa, xb, lane, bd);
-          add_columns(s1, bd, x + 32);
+          float t3[11];
+#pragma unroll
+          for (int n = 0; n < 10; ++n) t3[n] = max3f(x[3 * n], x[3 * n + 1], x[3 * n + 2]);
+          t3[10] = fmaxf(x[30], x[31]);
+          mx = fmaxf(mx, max3f(max3f(t3[0], t3[1], t3[2]), max3f(t3[3], t3[4], t3[5]),
+                               max3f(max3f(t3[6], t3[7], t3[8]), t3[9], t3[10])));
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s32[k] = __float_as_uint(x[k]);
+          tmem_st32(sc + hc, s32);
         }
-        if (diag || low > 0) {
-          const uint32_t v0 = visible_columns(low, lim), v1 = visible_columns(low - 32, lim - 32);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            x[k] = v0 >> k & 1 ? x[k] : -INFINITY;
-            x[32 + k] = v1 >> k & 1 ? x[32 + k] : -INFINITY;
-          }
-        }
-        // Lazy running max over the step's 64 scores (log2 units).
-        float t3[22];
-#pragma unroll
-        for (int n = 0; n < 21; ++n) t3[n] = max3f(x[3 * n], x[3 * n + 1], x[3 * n + 2]);
-        t3[21] = x[63];
-        float u7[8];
-#pragma unroll
-        for (int n = 0; n < 7; ++n) u7[n] = max3f(t3[3 * n], t3[3 * n + 1], t3[3 * n + 2]);
-        u7[7] = t3[21];
-        const float mx = max3f(max3f(u7[0], u7[1], u7[2]), max3f(u7[3], u7[4], u7[5]), fmaxf(u7[6], u7[7])) * sl2;
+        tmem_wait_st();
+        mx *= sl2;
         if (mx > m_new + kLazy) m_new = mx;
         const float alpha = (m_old == -INFINITY) ? 0.f : ex2(m_old - m_new);  // m_new >= m_old
         // The PV of step g-2 (same P buffer, same accumulator) must be done
@@ -473,23 +461,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
           uint8_t* prow = sP + sb * kQTile + (a / 8) * 1024 + (a % 8) * 128;
           float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
           const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_eff, -m_eff);
+#pragma unroll 1
+          for (int hc = 0; hc < 64; hc += 32) {
+            uint32_t x[32];
+            tmem_ld32(sc + hc, x);
+            tmem_wait_ld(x);
+            if (hc != 0) warp_arrive_tc(&bars->sread[g & 3]);
 #pragma unroll
-          for (int c = 0; c < BN / 8; ++c) {
-            uint32_t pk[4], pl[4];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[4], pl[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = 4 * c + i;
-              const float2 y = __ffma2_rn(make_float2(x[2 * n], x[2 * n + 1]), sc2, nm2);
-              const float2 e = make_float2(ex2(y.x), ex2(y.y));
-              if (i & 1)
-                acc1 = __fadd2_rn(acc1, e);
-              else
-                acc0 = __fadd2_rn(acc0, e);
-              split_weights(e, pk[i], pl[i]);
+              for (int i = 0; i < 4; ++i) {
+                const int n = 4 * c + i;
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * n]), __uint_as_float(x[2 * n + 1])), sc2, nm2);
+                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                if (i & 1)
+                  acc1 = __fadd2_rn(acc1, e);
+                else
+                  acc0 = __fadd2_rn(acc0, e);
+                split_weights(e, pk[i], pl[i]);
+              }
+              uint8_t* at = prow + (((hc / 8 + c) ^ (a % 8)) * 16);
+              *reinterpret_cast<uint4*>(at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              *reinterpret_cast<uint4*>(at + (kOffPlo - kOffP)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             }
-            uint8_t* at = prow + ((c ^ (a % 8)) * 16);
-            *reinterpret_cast<uint4*>(at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4*>(at + (kOffPlo - kOffP)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
           }
           sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
         }

@@ -99,9 +99,8 @@ __device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8
 // D = 64: products of their own, u rounded to bf16 (off by 1.65e-3 of u . k, which
 // a bias is far smaller than q for), the same 128 rows, so that the tile is one
 // group of 8 rows (1 KB, 128-byte swizzle) that every row group reads: a stride
-// of 0 between groups in the descriptor.  A second part of u would be 18 us more
-// of 117 (22 sequences of 512 tokens over 512 rows, 8 heads), the way of D = 128
-// 13 more.
+// of 0 between groups in the descriptor.  (22 sequences of 512 tokens over 512
+// rows, 8 heads: 101 us; a second part of u is 18 us more, the way of D = 128 8.)
 struct BiasTile {
   static constexpr int kBytes = 1024;
   uint32_t x;  // dimensions 2 l and 2 l + 1, l the lane
