@@ -117,7 +117,8 @@ size_t paged_workspace_bytes(int n, int T, int H, int D, bool bf16) {
 // fp32: the CUDA cores.  bf16: sequences of up to 4 new tokens by the decode
 // kernel, then the others by tiles of 128 queries; then the joins.  Each waits
 // for the one ahead.  (max_new is the host's bound: the lengths themselves are
-// on the device, and either kernel finds its own.)
+// on the device, and either kernel finds its own.  The decode kernel behind the
+// tiles makes a batch without short sequences 2.5 to 3.7 us longer.)
 cudaError_t launch_paged_attn(const PagedAttn& a, const WaitCtl& wc, cudaStream_t stream) {
   PlanSpace s;
   plan_space(a.workspace, a.T, a.D, a.bf16, &s);

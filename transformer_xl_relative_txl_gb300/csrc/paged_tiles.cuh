@@ -64,8 +64,8 @@ __device__ __forceinline__ uint32_t publish_units(Bars* bars, const PlanArgs& ar
 
 // Bit k: column k of 32 lies in low .. lim.  (Masking by bits, the test of a
 // column is short code for a block that most steps pass by: with two compares
-// a column, 100 us instead of 89 for 22 sequences of 512 tokens over 512 rows,
-// 8 heads, though almost no step runs it.)
+// a column, and the columns in a line, 12% longer for 22 sequences of 512 tokens
+// over 512 rows, though almost no step runs it.)
 __device__ __forceinline__ uint32_t visible_columns(int low, int lim) {
   const uint32_t upto = lim < 0 ? 0u : 0xffffffffu >> max(31 - lim, 0);
   const uint32_t from = low > 31 ? 0u : 0xffffffffu << max(low, 0);
@@ -256,7 +256,7 @@ __device__ __forceinline__ void split_weights(float2 e, uint32_t& hi, uint32_t& 
 // (-inf: no visible key).  A whole unit's go to the output, rows past its
 // queries are not written; a piece's go to the workspace, joined by the kernel
 // behind this one (paged_join.cu).  (With the last piece to arrive joining in
-// this kernel, its warps held up the CTA's softmax: 131 us instead of 90 for 22
+// this kernel, its warps held up the CTA's softmax: half as long again for 22
 // sequences of 512 tokens over 512 rows, 8 heads, where every CTA has two
 // pieces.)
 __device__ __forceinline__ float* piece_of(const TileUnit& u, float* part, int D) {
@@ -334,14 +334,14 @@ struct TileMaps {
 // freed only when the P.V MMA of its step completes, after that step's softmax,
 // while a K stage is free as soon as its score MMA is done; with V(t) beside
 // K(t), K would wait for the P.V of step t - NS and land just in time (D = 128,
-// two stages: 167 us instead of 145 for 152 units of 100 steps; at D = 64, with
-// four, 102 us so and 108 with a V tile that trails).  The q tile of a unit is
+// two stages: 15% longer for 152 units of 100 steps; at D = 64, with four stages, a
+// V tile that trails takes 6% longer).  The q tile of a unit is
 // loaded ahead of its first step, into the one of two buffers that the score
 // products of the unit before the last have read.
 //
 // STALL: the kernels' instances for the test hook, in which the loader of even
 // CTAs, and the P.V issuer of odd ones, stops behind its first unit's first
-// step.  (As a test of a parameter it cost the D = 64 kernel 2 to 4 us of 90.)
+// step.  (As a test of a parameter it cost the D = 64 kernel 2 to 5%.)
 template <int D, int NS, bool TRAIL, bool STALL, typename Bars>
 __device__ __forceinline__ void run_tile_loader(Bars* bars, const TileMaps& tm, const TileParams& p, uint8_t* sQ,
                                                 uint8_t* sK, uint8_t* sV, uint8_t* sR) {

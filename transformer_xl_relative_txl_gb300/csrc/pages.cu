@@ -117,9 +117,9 @@ __device__ __forceinline__ uint32_t used_mask(const PageBook& b, int base) {
 // in registers and leaves what the pages' owners need of it in shared memory,
 // and the first 16384 pages are read once, beside the entries' first loads, and
 // counted in the same scan as the needs.  (With reserve, append and free, 22
-// segments of 512 rows: 15 us, of which 7 are append's 46 MB; 24 with the
-// entries read anew in each phase and 64-bit divisions in append.  64 single
-// tokens: 9 us, about 3 a launch.)
+// segments of 512 rows: 18 us, of which 7 are append's 46 MB; half as long again
+// with the entries read anew in each phase and 64-bit divisions in append.  64
+// single tokens: 9 us, about 3 a launch.)
 struct Ask {  // what an entry asks for
   int slot, rows, count, have, need, last;  // need: pages (0 where it asks for none or is refused)
   bool ok, shared, idle;              // shared: its last page, which is copied; idle: a valid entry without rows
