@@ -92,13 +92,15 @@ def programs(D, nks, lag):
                 g = first[u] + t
                 if D == 64 and owner(g) != w:
                     continue
-                prog.append((("RD", w, g), [("S", g)] + [("G", tile0[u] + t + k) for k in range(3)]))
-                if D == 64:
-                    prog.append((("P", w, g), [("PV", g - 2)] if g >= 2 else []))
-                else:
-                    prog.append((("X", w, g), []))  # the halves exchange their maxima; a rescaling waits for the P.V before
-                    prog.append((("P", w, g), [("X", 0, g), ("X", 1, g)] + ([("PV", g - 1)] if w == 0 and t else []) +
-                                 ([("PV", g - 2)] if g >= 2 else [])))
+                seen = [("S", g)] + [("G", tile0[u] + t + k) for k in range(3)]
+                if D == 64:  # the scores lie in tensor memory until the weights are made, into the buffer of step g - 2
+                    prog.append((("RD", w, g), seen + ([("PV", g - 2)] if g >= 2 else [])))
+                    prog.append((("P", w, g), []))
+                    continue
+                prog.append((("RD", w, g), seen))
+                prog.append((("X", w, g), []))  # the halves exchange their maxima; a rescaling waits for the P.V before
+                prog.append((("P", w, g), [("X", 0, g), ("X", 1, g)] + ([("PV", g - 1)] if w == 0 and t else []) +
+                             ([("PV", g - 2)] if g >= 2 else [])))
             last = first[u] + nks[u] - 1
             if w == (owner(last) if D == 64 else 0):
                 prog.append((("EP", u), [("L", u)] + [("PV", first[u] + t) for t in range(nks[u])]))
