@@ -600,8 +600,7 @@ TXL_API int txl_pages_compact(const txl_page_book* book, int* new_id, int* copy_
  * dtype, o_dtype, D, scale, alignments and alias rules as in
  * txl_relattn_forward.  In bf16 the output's rounding is the only one of its
  * size: (q + u), (q + v), the distance scores and the weights keep 16 bits or
- * more, but for u and v at D = 64 in entries of more than 4 tokens, which are
- * rounded to bf16.
+ * more.
  */
 TXL_API size_t txl_relattn_paged_workspace_bytes(int n, int T, int H, int D, txl_dtype dtype);
 

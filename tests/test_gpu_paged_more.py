@@ -60,13 +60,10 @@ def test_low_parts(txl, D, n, L):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n,L", [(9, 60), (20, 40), (70, 90), (130, 131)])
 def test_low_parts_of_tiles(txl, D, n, L):
-    """More tokens: the weights keep both parts, the distance part its 32 bits, q its own; u and v both parts at D = 128,
-    and at D = 64, where they are rounded to bf16, they are bf16 numbers here."""
+    """More tokens: q + u, q + v and the weights keep both their parts, the distance part its 32 bits."""
     rng = np.random.default_rng(D)
     H = 2
     q, k, v, r, u, vb = case(rng, n, L, H, D)
-    if D == 64:
-        u, vb = (torch.from_numpy(x).to(BF).double().numpy() for x in (u, vb))
     book, pools = paged(rng, k, v, 16, 5)
     f = lambda x: torch.from_numpy(np.ascontiguousarray(x)).float().cuda()  # noqa: E731
     o = torch.empty(n, H, D, device="cuda")

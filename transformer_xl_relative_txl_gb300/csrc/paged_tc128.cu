@@ -9,8 +9,7 @@
 // softmax warps of which two share a lane quadrant and halve each 64-key step,
 // the distance window shifted per lane.  Keys are counted in page rows, the
 // work is divided on the device and cut units joined, value rows that are not
-// live are zeroed, and only the output is rounded to bf16, as in paged_tc64.cu; u
-// and v have two parts here, appended to the tiles (paged_tiles.cuh), and the
+// live are zeroed, and only the output is rounded to bf16, as in paged_tc64.cu; the
 // weights' second parts lie in shared memory, since tensor memory has no room.
 //
 // Measured: 8 sequences of 768 tokens over 768 rows, 8 heads, 110 us, 395

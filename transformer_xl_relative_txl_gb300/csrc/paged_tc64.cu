@@ -22,20 +22,17 @@
 //   * A 32-row box of output whose rows are all the unit's leaves by TMA, the
 //     last rows of a sequence by plain stores.
 //
-// Rounded to bf16: u and v, as operands, and the output.  Everything else keeps
-// what it has: q is an operand as it comes, the bias terms are products of their
-// own (paged_tiles.cuh), the distance scores pass the shift in fp32, the weights
-// are two bf16 parts each (P.V twice); scores, maxima, sums and accumulators are
-// fp32.  Together 1.7e-3 of the exact result (relative L2), which is the
-// output's rounding.  With (q+u), (q+v), the distance scores and the weights
-// rounded to bf16, as relattn_tc64.cu has them, it was 3.2e-3 and 89 us for what
-// now takes 101; the bias products take 6 of that, those with the weights' second
-// parts 2.
+// Rounded to bf16: the output alone.  q is an operand as it comes, the bias terms
+// are added apart (paged_tiles.cuh), the distance scores pass the shift in fp32,
+// the weights are two bf16 parts each (P.V twice); scores, maxima, sums and
+// accumulators are fp32.  That is 1.7e-3 of the exact result (relative L2).  With
+// (q+u), (q+v), the distance scores and the weights rounded to bf16, as
+// relattn_tc64.cu has them, it was 3.2e-3, and 89 us for what now takes 104.
 //
-// Measured: 22 sequences of 512 tokens over 512 rows, 8 heads, 101 us, 263
+// Measured: 22 sequences of 512 tokens over 512 rows, 8 heads, 104 us, 256
 // TFLOP/s counted without the distances that the shift leaves out.  Bound by
 // the softmax warps, about 1300 instructions a step, half of them on the ALU
-// pipe (52% busy; the tensor pipe 27%, DRAM 8%).
+// pipe.
 //
 // TMEM (512 columns): O0 [0,64) O1 [64,128) S0 [128,192) S1 [192,256)
 // distance ring [256,512).  Warps: 0-7 softmax (warp w: lane quadrant w%4,
@@ -64,11 +61,12 @@ constexpr int kPvWarp = 10;
 constexpr int kQrWarp = 11;
 constexpr int kThreads = 384;  // 3 warpgroups: 2 softmax, 1 producer (loader, three MMA issuers)
 // Register split (launch: 168 per thread, 384 x 168 = 64512): softmax
-// warpgroups 200, producer warpgroup 104; 2*128*200 + 128*104 = 64512.  (22
-// sequences of 512 tokens over 512 rows 100.4 us; 101.9 with 208 and 88, 102.9
-// with 216 and 72, where the producers spill, 100.8 with 184 and 136.)
-constexpr uint32_t kRegsSoftmax = 200;
-constexpr uint32_t kRegsProducer = 104;
+// warpgroups 192, producer warpgroup 120; 2*128*192 + 128*120 = 64512.  (22
+// sequences of 512 tokens over 512 rows, and a mixed batch: 104.4 and 103.0 us;
+// 104.3 and 104.7 with 208 and 88, 108.2 and 107.0 with 200 and 104, 109.5 and 110.2
+// with 216 and 72.)
+constexpr uint32_t kRegsSoftmax = 192;
+constexpr uint32_t kRegsProducer = 120;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsProducer <= kThreads * 168, "register split");
 constexpr uint32_t kColO = 0;    // O0, O1: 64 columns each
 constexpr uint32_t kColS = 128;  // S0, S1: 64 columns each
@@ -83,13 +81,14 @@ constexpr int kQTile = BM * 128;    // 128 rows x 64 bf16 (16 KB)
 constexpr int NK = 4, NV = 4, NR = 4;  // K, V, R tile stages
 static_assert(NK == NV && NK == NR, "the loader takes one stage count");
 constexpr int kOffQ = 0;                        // q: 2 buffers
-constexpr int kOffBias = kOffQ + 2 * kQTile;    // u and v: 2 buffers each
-constexpr int kOffK = kOffBias + 4 * BiasTile::kBytes;
+constexpr int kOffK = kOffQ + 2 * kQTile;
 constexpr int kOffV = kOffK + NK * kRowTile;
 constexpr int kOffR = kOffV + NV * kRowTile;
 constexpr int kOffP = kOffR + NR * kRowTile;    // P (bf16), hi parts: 2 buffers, same layout as q
 constexpr int kOffPlo = kOffP + 2 * kQTile;     // lo parts
-constexpr int kOffRed = kOffPlo + 2 * kQTile;   // [unit parity][m, l][row] handed to the epilogue
+constexpr int kOffTermK = kOffPlo + 2 * kQTile;  // bias terms of the K tiles, then of the R tiles
+constexpr int kOffTermR = kOffTermK + BiasTerm<D, NK>::kBytes;
+constexpr int kOffRed = kOffTermR + BiasTerm<D, NR>::kBytes;  // [unit parity][m, l][row] handed to the epilogue
 constexpr int kOffBar = kOffRed + 2 * 2 * BM * 4;
 constexpr int kBarBytes = 5120;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
@@ -117,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   uint8_t* sQ = smem + kOffQ;
-  uint8_t* sB = smem + kOffBias;
+  uint8_t* sTermK = smem + kOffTermK;
+  uint8_t* sTermR = smem + kOffTermR;
   uint8_t* sK = smem + kOffK;
   uint8_t* sV = smem + kOffV;
   uint8_t* sR = smem + kOffR;
@@ -184,39 +184,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     setmaxnreg_dec<kRegsProducer>();
     const uint32_t idS = idesc_bf16(128, BN, false, false) | (p.negative ? kNegateA : 0u);
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dU = sdesc_sw128(smem_u32(sB), 16, 0);
+    BiasTerm<D, NK> term(sTermK);
+    const uint64_t dTerm = term.term_desc(), dOnes = term.ones_desc();
     const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
     constexpr uint32_t kTile16 = kRowTile >> 4;
-    BiasTile u;
-    if (any) u.load(p.bias_u, bars->units[0].h);
     uint32_t gt = 0, un = 0;  // gt: steps, and K tiles, so far
     bool ok = true;
     while (any && ok) {
       if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
       const int nks = bars->units[un % kUnitRing].nks, next_h = bars->units[un % kUnitRing].next_h;
       const uint32_t g0 = gt;
-      // The bias buffer was read by the unit before the last, whose products are
-      // done once the scores of step g0 - 2 have been read.
-      if (g0 >= 2 && !(ok = warp_wait(&bars->sread[(g0 - 2) & 3], ((g0 - 2) >> 2) & 1, wait_ns, abort))) break;
-      u.store(sB + (un & 1) * BiasTile::kBytes);
-      if (next_h >= 0) u.load(p.bias_u, next_h);
-      if (lane == 0) {
-        tc_fence_after();
-        const uint64_t dq = dQ + (un & 1) * (kQTile >> 4), du = dU + (un & 1) * (BiasTile::kBytes >> 4);
-        for (int t = 0; t < nks; ++t) {
-          const uint32_t g = g0 + t, sb = g & 1;
-          // S buffer sb was last read by step g-2.
-          if (g >= 2 && !(ok = mbar_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
-          const int sk = g % NK;
-          if (!(ok = mbar_wait(&bars->fullK[sk], (g / NK) & 1, wait_ns, abort))) break;
+      const uint64_t dq = dQ + (un & 1) * (kQTile >> 4);
+      term.load(p.bias_u, bars->units[un % kUnitRing].h);
+      for (int t = 0; t < nks; ++t) {
+        const uint32_t g = g0 + t, sb = g & 1;
+        const int sk = g % NK;
+        if (!(ok = warp_wait(&bars->fullK[sk], (g / NK) & 1, wait_ns, abort))) break;
+        term.append(sK + sk * kRowTile, sk);
+        // S buffer sb was last read by step g-2.
+        if (g >= 2 && !(ok = warp_wait(&bars->sread[(g - 2) & 3], ((g - 2) >> 2) & 1, wait_ns, abort))) break;
+        if (lane == 0) {
           tc_fence_after();
-          mma_scores64(tmem + kColS + sb * BN, dq, du, dK + sk * kTile16, idS);
+          mma_scores<D>(tmem + kColS + sb * BN, dq, dK + sk * kTile16, dOnes, dTerm + sk * (kBiasStage >> 4), idS);
           tc_commit(&bars->emptyK[sk]);
           tc_commit(&bars->s_full[sb]);
+          if (t == nks - 1) tc_commit(&bars->q_empty[un & 1]);
         }
-        tc_commit(&bars->q_empty[un & 1]);
+        __syncwarp();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok || next_h < 0) break;
       gt = g0 + nks;
       ++un;
@@ -231,11 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
     setmaxnreg_dec<kRegsProducer>();
     const uint32_t idS = idesc_bf16(128, BN, false, false) | (p.negative ? kNegateA : 0u);
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dV = sdesc_sw128(smem_u32(sB + 2 * BiasTile::kBytes), 16, 0);
+    BiasTerm<D, NR> term(sTermR);
+    const uint64_t dTerm = term.term_desc(), dOnes = term.ones_desc();
     const uint64_t dR = sdesc_sw128(smem_u32(sR), 16, 1024);
     constexpr uint32_t kTile16 = kRowTile >> 4;
-    BiasTile v;
-    if (any) v.load(p.bias_v, bars->units[0].h);
     uint32_t nR = 0, gt = 0, un = 0;
     // Last global step that reads the tile now in each ring slot (-1: none).
     int last0 = -1, last1 = -1, last2 = -1, last3 = -1;
@@ -245,42 +239,43 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
       if (!(ok = warp_wait(&bars->q_full[un & 1], (un >> 1) & 1, wait_ns, abort))) break;
       const int nks = bars->units[un % kUnitRing].nks, next_h = bars->units[un % kUnitRing].next_h;
       const uint32_t g0 = gt;
-      if (g0 >= 2 && !(ok = warp_wait(&bars->sread[(g0 - 2) & 3], ((g0 - 2) >> 2) & 1, wait_ns, abort))) break;
-      v.store(sB + (2 + (un & 1)) * BiasTile::kBytes);
-      if (next_h >= 0) v.load(p.bias_v, next_h);
-      if (lane == 0) {
-        tc_fence_after();
-        const uint64_t dq = dQ + (un & 1) * (kQTile >> 4), dv = dV + (un & 1) * (BiasTile::kBytes >> 4);
-        for (int t = 0; ok && t < nks; ++t) {
-          const uint32_t sb = (g0 + t) & 1;
-          for (int e = (t == 0 ? -2 : t); e <= t; ++e) {
-            const int slot = (rb + e + 2) & (kSlots - 1);
-            // The slot's previous tile is free once every step up to its
-            // last reader L has read: steps of one parity read in order, so
-            // waiting for steps L and L-1 covers both parities.  (Four
-            // barriers by step % 4 keep these waits from aliasing: step L+3
-            // cannot have read before this tile exists.)
-            const int L = slot == 0 ? last0 : (slot == 1 ? last1 : (slot == 2 ? last2 : last3));
-            if (L >= 0 && !(ok = mbar_wait(&bars->sread[L & 3], (L >> 2) & 1, wait_ns, abort))) break;
-            if (L >= 1 && !(ok = mbar_wait(&bars->sread[(L - 1) & 3], ((L - 1) >> 2) & 1, wait_ns, abort))) break;
-            const int sr = nR % NR;
-            if (!(ok = mbar_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
+      const uint64_t dq = dQ + (un & 1) * (kQTile >> 4);
+      term.load(p.bias_v, bars->units[un % kUnitRing].h);
+      for (int t = 0; ok && t < nks; ++t) {
+        const uint32_t sb = (g0 + t) & 1;
+        for (int e = (t == 0 ? -2 : t); e <= t; ++e) {
+          const int sr = nR % NR;
+          if (!(ok = warp_wait(&bars->fullR[sr], (nR / NR) & 1, wait_ns, abort))) break;
+          term.append(sR + sr * kRowTile, sr);
+          const int slot = (rb + e + 2) & (kSlots - 1);
+          // The slot's previous tile is free once every step up to its
+          // last reader L has read: steps of one parity read in order, so
+          // waiting for steps L and L-1 covers both parities.  (Four
+          // barriers by step % 4 keep these waits from aliasing: step L+3
+          // cannot have read before this tile exists.)
+          const int L = slot == 0 ? last0 : (slot == 1 ? last1 : (slot == 2 ? last2 : last3));
+          if (L >= 0 && !(ok = warp_wait(&bars->sread[L & 3], (L >> 2) & 1, wait_ns, abort))) break;
+          if (L >= 1 && !(ok = warp_wait(&bars->sread[(L - 1) & 3], ((L - 1) >> 2) & 1, wait_ns, abort))) break;
+          if (lane == 0) {
             tc_fence_after();
-            mma_scores64(tmem + kColG + slot * BN, dq, dv, dR + sr * kTile16, idS);
+            mma_scores<D>(tmem + kColG + slot * BN, dq, dR + sr * kTile16, dOnes, dTerm + sr * (kBiasStage >> 4), idS);
             tc_commit(&bars->emptyR[sr]);
-            ++nR;
-            const int lr = static_cast<int>(g0) + min(e + 2, nks - 1);  // tile e's last reader
-            last0 = slot == 0 ? lr : last0;
-            last1 = slot == 1 ? lr : last1;
-            last2 = slot == 2 ? lr : last2;
-            last3 = slot == 3 ? lr : last3;
           }
-          if (!ok) break;
-          tc_commit(&bars->s_full[sb]);
+          ++nR;
+          const int lr = static_cast<int>(g0) + min(e + 2, nks - 1);  // tile e's last reader
+          last0 = slot == 0 ? lr : last0;
+          last1 = slot == 1 ? lr : last1;
+          last2 = slot == 2 ? lr : last2;
+          last3 = slot == 3 ? lr : last3;
+          __syncwarp();
         }
-        tc_commit(&bars->q_empty[un & 1]);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_commit(&bars->s_full[sb]);
+          if (t == nks - 1) tc_commit(&bars->q_empty[un & 1]);
+        }
+        __syncwarp();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok || next_h < 0) break;
       gt = g0 + nks;
       ++un;
@@ -391,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         float m_new = m_use;
         // Scores, half of the columns a turn, back into their place in tensor memory;
         // then, the maximum known, the weights, half a turn.  The step's code is what
-        // bounds it otherwise: with all 64 columns in a line, in registers, 117 us for
-        // 22 sequences of 512 tokens over 512 rows, a quarter of the warps' waiting for
-        // instructions, and 103 so, a tenth.  (The weights in quarters 108, the scores
-        // alone in halves 129.)
+        // bounds it otherwise: with all 64 columns in a line, in registers, 14% longer
+        // for 22 sequences of 512 tokens over 512 rows, a quarter of the warps' waiting
+        // for instructions, a tenth so.  (The weights in quarters 5% longer, the scores
+        // alone in halves 25%.)
         float mx = -INFINITY;
 #pragma unroll 1
         for (int hc = 0; hc < 64; hc += 32) {

@@ -92,48 +92,18 @@ __device__ __forceinline__ void zero_dead_rows(int start, int last, int t, uint8
 }
 
 // The score products' bias terms: (q + u) . k = q . k + u . k, and q . k has exact
-// operands, where q + u rounded to bf16 is off by 1.65e-3 (rms) of a score's
-// content part, as much as the output's own rounding.  u . k is a number a key,
-// the same for every query.
-//
-// D = 64: products of their own, u rounded to bf16 (off by 1.65e-3 of u . k, which
-// a bias is far smaller than q for), the same 128 rows, so that the tile is one
-// group of 8 rows (1 KB, 128-byte swizzle) that every row group reads: a stride
-// of 0 between groups in the descriptor.  (22 sequences of 512 tokens over 512
-// rows, 8 heads: 101 us; a second part of u is 18 us more, the way of D = 128 8.)
-struct BiasTile {
-  static constexpr int kBytes = 1024;
-  uint32_t x;  // dimensions 2 l and 2 l + 1, l the lane
-  __device__ __forceinline__ void load(const float* bias, int h) {
-    const float* at = bias + static_cast<size_t>(h) * 64 + 2 * (threadIdx.x & 31);
-    x = pack_bf16x2(__ldg(at), __ldg(at + 1));
-  }
-  // One warp.
-  __device__ __forceinline__ void store(uint8_t* tile) const {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-      *reinterpret_cast<uint32_t*>(tile + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4) = x;
-    fence_proxy_async_smem();
-    __syncwarp();
-  }
-};
-// One thread: D[128 x 64] = (q + bias) B^T of a tile B of 64 rows of 64.
-__device__ __forceinline__ void mma_scores64(uint32_t d, uint64_t q, uint64_t bias, uint64_t b, uint32_t id) {
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) mma_ss(d, q + kk * 2, b + kk * 2, id, kk > 0);
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) mma_ss(d, bias + kk * 2, b + kk * 2, id, 1);
-}
-
-// D = 128: the issuer's warp computes the terms of a landed tile, u in two bf16
-// parts, and appends them to the tile in three (24 bits), which one more product
-// of 16 columns multiplies by ones: 110 us, and 124 as products of their own with
-// one part of u, 148 with two (8 sequences of 768 tokens over 768 rows, 8 heads).
+// operands.  u . k is a number a key, the same for every query, so the issuer's
+// warp computes it from the landed tile, u in two bf16 parts, and appends it to
+// the tile in three (24 bits), which one more product of 16 columns multiplies
+// by ones.  (q + u rounded to bf16 is off by 1.65e-3 (rms) of a score's content
+// part, as much as the output's own rounding.  Measured, us of 22 sequences of
+// 512 tokens over 512 rows, D = 64, and of 8 of 768 over 768, D = 128, 8 heads: 104
+// and 110; as products of their own with u's parts repeated for 128 rows, 114 and
+// 148, with one part only 101 and 124.)
 //
 // Per stage of the ring, 2 KB: the 64 rows' first 8 columns, 16 bytes a row, then
 // as many zeros; behind the stages 8 rows of ones (three columns), which all of
-// the 128 rows read.
+// the 128 rows read: a stride of 0 between groups of 8 in the descriptor.
 constexpr int kBiasStage = 2 * kStepKeys * 16;
 constexpr int kBiasOnes = 256;
 
@@ -165,8 +135,8 @@ struct BiasTerm {
   }
   // The terms of a tile's 64 rows (128-byte swizzle): of each 16 rows, lane l has
   // those of rows l / 4 and l / 4 + 8, and puts down the (l % 4)-th 16's.
-  // (As multiply-adds it is 119 us in a loop, 194 in a line: the softmax's code
-  // pushes it out of the instruction cache between any two tiles.)
+  // (As multiply-adds 119 us at D = 128 in a loop, 194 in a line: the softmax's
+  // code pushes it out of the instruction cache between any two tiles.)
   __device__ __forceinline__ void append(const uint8_t* tile, int s) const {
     const int lane = threadIdx.x & 31, r16 = lane & 15, half = lane >> 4;
     float mine[2] = {0.f, 0.f};
