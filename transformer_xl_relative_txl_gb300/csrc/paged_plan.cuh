@@ -12,7 +12,7 @@
 //
 // Each CTA finds S and the start of its own range by itself, at its head
 // (plan_begin: all of its threads sum the sequences' costs); then a warp finds
-// its units, 32 at a time (plan_batch).  That takes about 4 us of the 101 that 22
+// its units, 32 at a time (plan_batch).  That takes about 4 us of the 104 that 22
 // sequences of 512 tokens over 512 rows take (8 heads), half of it two trips to
 // L2, where a kernel that made a list for all CTAs took 5 and a launch.
 //
@@ -31,9 +31,9 @@ namespace txl {
 
 // Sequences with up to this many new tokens go to the decode kernel, whose eight
 // columns hold four queries in two parts.  (1 to 4 tokens there and in tiles: 64
-// sequences over 300 to 4500 rows, 16 heads of 64, 97 to 104 us and 295; 48 over
-// 1600 to 8100 rows, 8 heads of 128, 157 to 170 and 293; 256 over 64 rows, 8 heads
-// of 64, 27 to 31 and 69.)
+// sequences over 300 to 4500 rows, 16 heads of 64, 97 to 104 us and 286; 48 over
+// 1600 to 8100 rows, 8 heads of 128, 157 to 170 and 292; 256 over 64 rows, 8 heads
+// of 64, 27 to 31 and 74.)
 constexpr int kDecodeRows = 4;
 constexpr int kMaxSms = 160;    // the workspace has room for the CTAs of so many SMs
 constexpr int kDecodePerSm = 2, kSimtPerSm = 3;
