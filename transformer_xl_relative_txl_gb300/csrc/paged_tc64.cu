@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc64_kernel(const __grid_co
         // then, the maximum known, the weights, half a turn.  The step's code is what
         // bounds it otherwise: with all 64 columns in a line, in registers, 14% longer
         // for 22 sequences of 512 tokens over 512 rows, a quarter of the warps' waiting
-        // for instructions, a tenth so.  (The weights in quarters 5% longer, the scores
+        // for instructions, an eighth so.  (The weights in quarters 5% longer, the scores
         // alone in halves 25%.)
         float mx = -INFINITY;
 #pragma unroll 1
