@@ -210,9 +210,7 @@ def _library(s):
     if s["op"] == "embed":
         return txl.txl_embed_forward(s["tokens"], s["table"], s["o"], scale=s["scale"])
     if s["op"] == "grad":
-        if "workspace" not in s:  # kept by a program beside its gradients
-            s["workspace"] = torch.empty(txl.txl_embed_workspace_bytes(s["T"], s["d"]), dtype=torch.uint8, device="cuda")
-        return txl.txl_embed_backward(s["tokens"], s["dout"], s["dtable"], s["workspace"], scale=s["scale"], accumulate=s["accumulate"])
+        return txl.txl_embed_backward(s["tokens"], s["dout"], s["dtable"], scale=s["scale"], accumulate=s["accumulate"])
     if s["op"] == "dense4":
         return txl.txl_dense_w4(s["x"], s["codes"], s["scales"], s["y"], bias=s["b"], relu=s["relu"])
     txl.txl_sample(s["z"], s["u"], s["tokens"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"], prob=s["prob"])
