@@ -14,6 +14,9 @@
  *     done by the attention kernel from the tiles it loads, where it can);
  *   - txl_pages_* and txl_relattn_forward_paged: the memory of a ragged batch
  *     kept in pages of a pool, and the attention over it;
+ *   - txl_embed_forward, txl_dense_w4 and txl_sample: a decoding step's way from
+ *     token ids to the layers and from the last product to the next ids, with
+ *     txl_embed_backward for training;
  *   - txl_sinusoid_rel: the parameter-free sinusoidal distance table R.
  *
  * Conventions shared by every entry point
@@ -668,6 +671,102 @@ TXL_API int txl_relattn_backward(const void* q, const void* k, const void* v, co
                          float* dbias_u, float* dbias_v,
                          int B, int W, int M, int H, int D, int n_r, float scale,
                          txl_dtype dtype, txl_dtype go_dtype, cudaStream_t stream);
+
+/*
+ * The operators around the layers: token ids to the rows that a segment's first
+ * layer reads, products of a few tokens with 4-bit weights, tokens from the
+ * logits of the last product.  All lengths and settings that change from step to
+ * step are device data, so a decoding step can be captured into a graph; no call
+ * allocates or keeps anything, and calls on several streams do not meet.
+ */
+
+/*
+ * txl_embed_forward -- rows of an embedding table: out[t] = scale table[tokens[t]].
+ *
+ *   tokens  device, [T] int32; one outside 0 .. V-1 is padding: its row of out
+ *           is zeros
+ *   table   device, [V, d] `table_dtype`
+ *   out     device, [T, d] `out_dtype`, rounded once
+ *   scale   sqrt(d) where the table is shared with the output product
+ * Every pointer aligned to its type (rows of 16-byte vectors are faster: d a
+ * multiple of 8, table and out 16-byte aligned).  out must not overlap tokens or
+ * table (TXL_ERR_ALIAS).  Limits (TXL_ERR_UNSUPPORTED): T at most 2^30, V 2^24,
+ * d 2^20.  T == 0 is an empty call.
+ */
+TXL_API int txl_embed_forward(const int* tokens, const void* table, void* out, int T, int V, int d, float scale,
+                              txl_dtype table_dtype, txl_dtype out_dtype, cudaStream_t stream);
+
+/*
+ * txl_embed_backward -- the table's gradient from dout = dL/dout:
+ *
+ *   dtable[v] = (accumulate: dtable[v] +) scale * sum of dout[t], tokens[t] == v
+ *
+ *   dout    device, [T, d] `dtype`; the rows of padding are not read
+ *   dtable  device, [V, d] fp32.  accumulate zero: overwritten whole, rows that
+ *           no token names with zeros (T == 0: all of it); else those rows are
+ *           neither read nor written (T == 0: an empty call)
+ * tokens, scale, alignments and limits as in txl_embed_forward; dtable must not
+ * overlap tokens or dout.  Sums are fp32, in an order that only the tokens decide:
+ * the same call gives the same bits.
+ */
+TXL_API int txl_embed_backward(const int* tokens, const void* dout, float* dtable, int T, int V, int d, float scale,
+                               int accumulate, txl_dtype dtype, cudaStream_t stream);
+
+/*
+ * txl_dense_w4 -- txl_dense of a few rows with 4-bit weights: y = x W (+ bias)
+ * (then ReLU),
+ *
+ *   W[j, i] = scales[j / group, i] * (code[i, j] - 8),  code 0 .. 15
+ *
+ *   x       device, [m, k] bf16
+ *   codes   device, [n, k / 2] bytes: byte b of row i holds code[i, 2b] in its low
+ *           four bits and code[i, 2b + 1] in its high four
+ *   scales  device, [k / group, n] bf16;  group 32, 64 or 128, a divisor of k
+ *   y       device, [m, n] `y_dtype`
+ *   bias    device, [n] fp32 or NULL;  relu  nonzero: ReLU after the bias
+ * Sums are fp32 of exact products, rounded once at the end.  n a multiple of 8;
+ * x, codes and scales 16-byte aligned; y must not overlap the inputs
+ * (TXL_ERR_ALIAS).  Limits (TXL_ERR_UNSUPPORTED): m at most 2^20, n 2^30, k 2^24.
+ * The weights are read once for every 32 rows of x.  m == 0 is an empty call.
+ */
+TXL_API int txl_dense_w4(const void* x, const void* codes, const void* scales, void* y, int m, int n, int k, int group,
+                         const float* bias, int relu, txl_dtype y_dtype, cudaStream_t stream);
+
+/*
+ * txl_sample -- a token for each of B rows of logits.
+ *
+ * Of row b, with weights w_i = exp((z_i - max z) / temperature[b]), the tokens
+ * are kept that every filter keeps, the filters in this order:
+ *
+ *   top_k  the top_k[b] largest logits
+ *   top_p  of those, the shortest beginning of their order by falling logit
+ *          whose weights make up top_p[b] of them, one token at least
+ *   min_p  those with w_i >= min_p[b] (the largest has w = 1)
+ *
+ * Among equal logits the lower index comes first.  The token is the first, by
+ * index, at which the running sum of the kept weights is over uniform[b] times
+ * their whole sum.
+ *
+ *   logits       device, [B, V] `dtype`, rows row_stride elements apart (>= V).
+ *                -inf and NaN are never kept, +inf counts as the largest float
+ *   uniform      device, [B] fp32, in [0, 1) (below: as 0; from 1 on: the last
+ *                kept token)
+ *   temperature  device, [B] fp32 or NULL (1); not over 0: the largest logit's
+ *                token, whatever the other settings
+ *   top_k        device, [B] int32 or NULL; <= 0: off
+ *   top_p        device, [B] fp32 or NULL; not under 1: off
+ *   min_p        device, [B] fp32 or NULL; not over 0: off, over 1: as 1
+ *   tokens       device, [B] int32 out; -1 for a row without a logit to keep
+ *   prob         device, [B] fp32 out or NULL: the token's share of the kept
+ *                weights
+ * Sums of weights are whole numbers (2^-44 of the largest weight), so neither the
+ * order of the sums nor the batch around a row changes its token.  tokens and
+ * prob must not overlap each other or an input (TXL_ERR_ALIAS).  Limits
+ * (TXL_ERR_UNSUPPORTED): V at most 2^18, B 65535.  B == 0 is an empty call.
+ */
+TXL_API int txl_sample(const void* logits, long long row_stride, int B, int V, const float* uniform,
+                       const float* temperature, const int* top_k, const float* top_p, const float* min_p, int* tokens,
+                       float* prob, txl_dtype dtype, cudaStream_t stream);
 
 /*
  * txl_sinusoid_rel -- the raw sinusoidal distance table R[n_dist, dim].

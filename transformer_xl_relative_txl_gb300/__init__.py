@@ -2,9 +2,11 @@
 
 Thin ctypes binding of the C ABI in ``include/txl_relattn.h``: each function
 has the C entry point's name and only marshals torch tensors (device memory,
-CUDA streams) into pointers, sizes and dtype codes; the paged memory's calls do
-so in the extension module _paged (csrc/paged_binding.cpp), which the first of
-them loads: it is built against one PyTorch, the rest of the package is not.  All
+CUDA streams) into pointers, sizes and dtype codes; the calls of a decoding step
+(the paged memory's, the embedding's, 4-bit products, sampling) do so in the
+extension module _paged (csrc/paged_binding.cpp, csrc/tokens_binding.cpp), which
+the first of them loads: it is built against one PyTorch, the rest of the package
+is not.  All
 computation runs in the library's CUDA kernels; there is no fallback.  Importing
 fails loudly if the library has not been built (``python transformer_xl_relative_txl_gb300/build.py``).
 """
@@ -26,6 +28,7 @@ __all__ = [
     "txl_stack_workspace_bytes",
     "txl_pages_reserve", "txl_pages_append", "txl_pages_copy", "txl_pages_fork", "txl_pages_free",
     "txl_pages_compact", "txl_relattn_forward_paged", "txl_relattn_paged_workspace_bytes",
+    "txl_embed_forward", "txl_embed_backward", "txl_dense_w4", "txl_sample",
     "txl_sinusoid_rel",
     "txl_get_device_status", "txl_release_cached", "txl_status_string", "txl_version",
     "txl_debug_set_wait_limit_ns", "txl_debug_inject_stall", "txl_debug_force_split",
@@ -121,6 +124,14 @@ lib.txl_relattn_paged_workspace_bytes.restype = ctypes.c_size_t
 lib.txl_relattn_forward_paged.argtypes = [_p, _p, _p, _pb, _p, _p, _i, _i, _i, _p, _p, _p, _p, _p, _i, _i, _i, _f, _i,
                                           _i, _p, ctypes.c_size_t, _p]
 lib.txl_relattn_forward_paged.restype = _i
+lib.txl_embed_forward.argtypes = [_p, _p, _p, _i, _i, _i, _f, _i, _i, _p]
+lib.txl_embed_forward.restype = _i
+lib.txl_embed_backward.argtypes = [_p, _p, _p, _i, _i, _i, _f, _i, _i, _p]
+lib.txl_embed_backward.restype = _i
+lib.txl_dense_w4.argtypes = [_p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p]
+lib.txl_dense_w4.restype = _i
+lib.txl_sample.argtypes = [_p, _ll, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _p]
+lib.txl_sample.restype = _i
 lib.txl_sinusoid_rel.argtypes = [_p, _i, _i, _i, _p]
 lib.txl_sinusoid_rel.restype = _i
 lib.txl_get_device_status.argtypes = [_p]
@@ -423,14 +434,14 @@ _calls = None
 
 
 def _paged_calls():
-    """The extension module of the paged memory's calls, loaded by the first of them."""
+    """The extension module of a decoding step's calls, loaded by the first of them."""
     global _calls
     if _calls is None:
         try:
             from . import _paged
         except ImportError as e:
-            raise ImportError("the paged memory's extension module (_paged.so) is missing or was built for another "
-                              "PyTorch: build it with `python transformer_xl_relative_txl_gb300/build.py`") from e
+            raise ImportError("the extension module of the paged memory's and the tokens' calls (_paged.so) is missing "
+                              "or was built for another PyTorch: build it with `python transformer_xl_relative_txl_gb300/build.py`") from e
         _calls = _paged
     return _calls
 
@@ -642,6 +653,40 @@ def txl_mem_update_kv(k_mem, v_mem, k_h, v_h, k_out, v_out, m, stream=None) -> i
                                _stream(stream))
     _check(st, "txl_mem_update_kv")
     return m_out.value
+
+
+def txl_embed_forward(tokens, table, out, scale=1.0, stream=None):
+    """out [*tokens.shape, d] <- scale * table[tokens] (table [V, d], each fp32
+    or bf16; tokens int32, one outside 0 .. V-1 gives zeros)."""
+    _check(_paged_calls().embed_forward(tokens, table, out, scale, _handle(stream)), "txl_embed_forward")
+    return out
+
+
+def txl_embed_backward(tokens, dout, dtable, scale=1.0, accumulate=False, stream=None):
+    """dtable [V, d] (fp32) <- scale * the sums of dout [*tokens.shape, d] by
+    token, added to what is there where `accumulate`."""
+    _check(_paged_calls().embed_backward(tokens, dout, dtable, scale, accumulate, _handle(stream)),
+           "txl_embed_backward")
+    return dtable
+
+
+def txl_dense_w4(x, codes, scales, y, bias=None, relu=False, stream=None):
+    """y [m, n] = x [m, k] W (+ bias) (then ReLU), W[j, i] = scales[j // group, i]
+    * (code[i, j] - 8): codes [n, k / 2] uint8, the low four bits for the even
+    j; scales [k / group, n] bf16, group 32, 64 or 128; x bf16, y bf16 or fp32,
+    bias fp32 [n] or None."""
+    _check(_paged_calls().dense_w4(x, codes, scales, y, bias, relu, _handle(stream)), "txl_dense_w4")
+    return y
+
+
+def txl_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, stream=None):
+    """tokens [B] (int32) <- a token for each row of logits [B, V] (fp32 or bf16,
+    rows any distance apart) by uniform [B] (fp32 in [0, 1)) and the row's
+    temperature, top_p, min_p (fp32 [B]) and top_k (int32 [B]), each or None;
+    prob (fp32 [B]) receives its share of the kept weights."""
+    _check(_paged_calls().sample(logits, uniform, tokens, temperature, top_k, top_p, min_p, prob, _handle(stream)),
+           "txl_sample")
+    return tokens
 
 
 def txl_sinusoid_rel(R, stream=None):

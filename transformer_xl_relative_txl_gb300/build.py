@@ -3,7 +3,7 @@ extension module _paged.so that hands torch tensors to it.
 
 Each CUDA translation unit under csrc/ is compiled in parallel with nvcc to an
 object in _build/, then nvcc links the shared library next to this file.  The
-module is one host file compiled beside them against the headers of Python and
+module is two host files compiled beside them against the headers of Python and
 of the installed PyTorch.  No cmake; a few seconds per unit.  Run ``python transformer_xl_relative_txl_gb300/build.py``
 (it does not import the package, which needs the library).
 """
@@ -58,13 +58,19 @@ def _compile_binding():
     include = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"), INCLUDE]
-    obj = os.path.join(BUILD, "paged_binding.o")
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-           *[f"-I{d}" for d in include], "-c", os.path.join(CSRC, "paged_binding.cpp"), "-o", obj]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for paged_binding.cpp:\n{res.stdout}\n{res.stderr}")
-    return obj, os.path.join(torch, "lib")
+
+    def one(name):
+        obj = os.path.join(BUILD, name + ".o")
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               *[f"-I{d}" for d in include], "-c", os.path.join(CSRC, name + ".cpp"), "-o", obj]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed for {name}.cpp:\n{res.stdout}\n{res.stderr}")
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
+        objs = list(ex.map(one, ["paged_binding", "tokens_binding"]))
+    return objs, os.path.join(torch, "lib")
 
 
 def _link(cmd, target):
@@ -88,8 +94,8 @@ def build(verbose: bool = False, extra=()) -> str:
                 print(err, file=sys.stderr)
     _link([_nvcc(), *ARCH, "-shared", *objs], LIB)
     # Behind the library, which every other call needs and this one's headers are not part of.
-    obj, torch_lib = binding.result()
-    _link([shutil.which("g++") or "c++", "-shared", obj, f"-L{PKG}", "-l:libtxl_relattn.so", f"-L{torch_lib}",
+    objs, torch_lib = binding.result()
+    _link([shutil.which("g++") or "c++", "-shared", *objs, f"-L{PKG}", "-l:libtxl_relattn.so", f"-L{torch_lib}",
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], BINDING)
     return LIB
 
