@@ -36,12 +36,14 @@ namespace txl {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
+constexpr int kGroup = 32, kGroups = kBins / kGroup;  // bins that are first looked at together
 constexpr int kFew = 256;        // tokens that are compared each with each
 constexpr int kMaxCluster = 8;
 constexpr int kTable = 512;      // steps of the powers' table
 constexpr int kOne = 44;         // the largest weight is 2^kOne
-constexpr int kCells = 1024;
+constexpr int kCell = 256;       // tokens that a warp takes at once, 8 a lane
+constexpr int kCells = 128;      // of a CTA's stretch, at most
 
 // 2^(-j / kTable) in units of 2^-44, from nine square roots of a half by
 // Newton's method.
@@ -103,28 +105,33 @@ __device__ __forceinline__ unsigned long long share_of(float p, unsigned long lo
 // exp((z - top) / T) in units of 2^-44.  With y = (top - z) log2(e) / T as the
 // sum of two floats, y = k / 512 + r, the weight is 2^-(k/512), from the table,
 // times 1 - q, q = 1 - 2^-r by its series in whole numbers of 2^-40: |r| <=
-// 2^-10, so three terms do.
+// 2^-10, so three terms do.  Floats become whole numbers by adding a power of two
+// and taking the bits: conversions run at an eighth of the rate.
 __device__ __forceinline__ unsigned long long weight(float z, float top, Scale c, const unsigned long long* table) {
   float d = top - z;
   const float back = d - top;
   float err = (top - (d - back)) - (z + back);  // top - z = d + err
   if (d > 3.0e38f) d = FLT_MAX, err = 0.f;
   const float y = d * c.hi;
-  const float y2 = fmaf(d, c.hi, -y) + fmaf(d, c.lo, err * c.hi);
   if (!(y < 45.f)) return 0;
-  const float kf = rintf(y * kTable);
-  const float f = fmaf(kf, -1.f / kTable, y);
-  const int k = static_cast<int>(kf);
-  const int r = __float2int_rn(f * 0x1p40f) + __float2int_rn(y2 * 0x1p40f);
-  // ln 2 in units of 2^-31
-  const int x = static_cast<int>((static_cast<long long>(r) * 1488522236LL + (1LL << 30)) >> 31);
-  const int x2 = static_cast<int>((static_cast<long long>(x) * x) >> 41);      // x^2 / 2
-  const int x3 = static_cast<int>((static_cast<long long>(x2) * x) >> 40) / 3;  // x^3 / 6
+  const float y2 = fmaf(d, c.hi, -y) + fmaf(d, c.lo, err * c.hi);
+  constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: one unit of its last place is 1
+  const float at = fmaf(y, static_cast<float>(kTable), kWhole);
+  const int k = __float_as_int(at) - __float_as_int(kWhole);
+  const float f = fmaf(at - kWhole, -1.f / kTable, y);
+  // r = f + y2: f in units of 2^-24, what that leaves and y2 (< 2^-17) in units of 2^-39
+  constexpr float kCoarse = 0.75f, kFine = 0x1.8p-16f;
+  const float coarse = f + kCoarse;
+  const float fine = (f - (coarse - kCoarse)) + y2 + kFine;
+  const int r = ((__float_as_int(coarse) - __float_as_int(kCoarse)) << 16) +
+                ((__float_as_int(fine) - __float_as_int(kFine)) << 1);  // units of 2^-40
+  const int x = __mulhi(r, 1488522236) << 1;        // r ln 2; ln 2 in units of 2^-31
+  const int x2 = __mulhi(x, x) >> 9;                // x^2 / 2
+  const int x3 = __mulhi(__mulhi(x2, x), 5592405);  // x^3 / 6: a third of 2^-8
   const int q = x - x2 + x3;
   const unsigned long long p = table[k & (kTable - 1)];
-  const int p31 = static_cast<int>(min(p >> (kOne - 31), 0x7fffffffULL));
-  const long long less = (static_cast<long long>(q) * p31) >> (31 - (kOne - 40));
-  return static_cast<unsigned long long>(static_cast<long long>(p) - less) >> (k / kTable);
+  const long long less = __mulhi(q << 1, static_cast<int>(p >> (kOne - 30)));  // units of 2^-39
+  return (p - static_cast<unsigned long long>(less << (kOne - 39))) >> (k / kTable);
 }
 
 // A float's place in the order of floats, as a whole number.
@@ -136,9 +143,6 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 
-constexpr int kGroup = 32, kGroups = kBins / kGroup;  // bins that are first looked at together
-static_assert(kGroups == 64 && kThreads == 8 * kGroups, "eight threads a group");
-
 // What a CTA tells the others of its cluster, written into their memory ahead of
 // a barrier; read there, an exchange would take a second way to and fro.
 struct Found {
@@ -149,36 +153,33 @@ struct Kept {
   unsigned long long over;  // weights over the threshold
   int ties;                 // tokens at it
 };
+struct Candidate {
+  float z;
+  int token;
+};
 
 struct Shared {
   unsigned long long table[kTable];
-  union {
-    unsigned long long bins[kBins];  // of the range at hand: sums of weights, or counts
-    struct {                         // at the end: of cells of 32 tokens
-      unsigned long long over[kCells];
-      int ties[kCells];
-    } cells;
-  };
+  unsigned long long bins[kBins];  // of the range at hand: sums of weights, or counts
   unsigned long long groups[kMaxCluster][kGroups];
-  uint4 ends[kMaxCluster];  // ordered: the smallest logit, the largest, a bound (below); how many
+  float top[kMaxCluster];
+  uint32_t cut[kMaxCluster];
   Found found[kMaxCluster];
   Kept kept[kMaxCluster];
-  float seg_z[kMaxCluster][kFew];
-  int seg_i[kMaxCluster][kFew];
-  float cand[kFew];
-  int cand_i[kFew];
+  Candidate seg[2 * kFew];  // a part for each CTA
+  Candidate cand[kFew];
   unsigned long long cand_w[kFew];
   unsigned long long warp_sum[kWarps];
-  int warp_ties[kWarps];
-  uint32_t lo, hi, cut;  // of this CTA
-  int live, n;
-  int bin;                   // where the border lies,
-  unsigned long long above;  // and the sum ahead of it
+  float warp_top[kWarps];
+  uint32_t warp_cut[kWarps];
+  unsigned long long cell_over[kCells];
+  int cell_ties[kCells];
+  uint32_t lo, hi;  // of a bin's tokens in this CTA
+  int n;            // how many
+  int bin;                           // where the border lies,
+  unsigned long long above, in_bin;  // the sum ahead of it, and its own
   float value;
   unsigned long long value_above;
-  int cell;
-  unsigned long long rest;
-  int ties_before;
 };
 
 // Inclusive sum over a warp.
@@ -199,26 +200,35 @@ __device__ __forceinline__ T warp_sum(T x) {
   return x;
 }
 
-// The bins of a range of logits, largest first.  Linear between its ends, in
-// halves so that no difference overflows; by the floats' order where `keys`
-// (for ranges that the linear map does not separate).
+// The bins of a range of logits, largest first: linear between its ends, or by
+// the floats' order where `keys` (for ranges that the linear map does not
+// separate).  Either falls with z; nothing else is asked of it.
 struct Range {
   float lo, hi;
   bool keys;
   int shift;
-  float inv;
+  float per, at_hi;  // bins per unit, bins of the upper end from 0
   __device__ __forceinline__ void set(float l, float h, bool k) {
     lo = l, hi = h, keys = k;
     const uint32_t span = ordered(h) - ordered(l);
-    shift = max(0, 32 - __clz(span) - 11);
-    inv = kBins / (0.5f * h - 0.5f * l);
+    shift = max(0, 32 - __clz(span) - 10);
+    per = (kBins - 1) * 0.5f / (0.5f * h - 0.5f * l);
+    at_hi = h * per;
   }
   __device__ __forceinline__ bool has(float z) const { return z >= lo && z <= hi; }
   __device__ __forceinline__ int bin(float z) const {
-    if (keys) return static_cast<int>((ordered(hi) - ordered(z)) >> shift);
-    return static_cast<int>(fminf((0.5f * hi - 0.5f * z) * inv, kBins - 1.f));  // (0 * inf: NaN, bin 0 or the last)
+    if (keys) return static_cast<int>((ordered(hi) - ordered(z + 0.f)) >> shift);  // (-0 is 0)
+    const float x = fmaxf(fminf(fmaf(z, -per, at_hi), kBins - 1.f), 0.f);
+    return __float_as_int(x + 8388608.f) & (2 * kBins - 1);
+  }
+  // Ends outside of which no token is in bin b (or in a later one, in an earlier).
+  __device__ __forceinline__ void near(int b, float* from, float* to) const {
+    const bool fine = !keys && fabsf(at_hi) < 1048576.f && fabsf(lo * per) < 1048576.f && per > 0x1p-100f;
+    *from = fine ? fmaxf(lo, hi - (b + 2) / per) : lo;
+    *to = fine ? fminf(hi, hi - (b - 2) / per) : hi;
   }
 };
+static_assert(kBins == 1024, "ten bits");
 
 // Sum over the threads ahead, and of all.
 __device__ __forceinline__ unsigned long long block_scan(Shared& sh, unsigned long long x, unsigned long long* all) {
@@ -248,69 +258,87 @@ __device__ __forceinline__ void add64(unsigned long long* at, unsigned long long
   if (hi != 0) atomicAdd(half + 1, hi);
 }
 
-// The CTA's stretch of a row, in shared memory: -inf in place of NaN, the
-// largest float of +inf, 0 of -0.
-struct Row {
-  float* z;
-  int n, first;
-};
+template <typename T>
+__device__ __forceinline__ float largest() {  // that T holds
+  return sizeof(T) == 2 ? __uint_as_float(0x7F7F0000u) : FLT_MAX;
+}
 
-// A thread's smallest and largest logit, ordered, and how many it has.
-struct Ends {
-  uint32_t lo = 0xffffffffu, hi = 0;
-  int n = 0;
-  __device__ __forceinline__ void take(float z) {
-    if (z == -INFINITY) return;
-    lo = min(lo, ordered(z));
-    hi = max(hi, ordered(z));
-    ++n;
+// The CTA's stretch of a row, in shared memory as it came, and -inf up to whole
+// cells.  (NaN is in no range and over no threshold.)
+template <typename T>
+struct Row {
+  T* z;
+  int cells, first;
+  __device__ __forceinline__ void get(int cell, float (&v)[8]) const {
+    const int i = cell * kCell + (threadIdx.x & 31) * 8;
+    if constexpr (sizeof(T) == 2) {
+      const uint4 x = *reinterpret_cast<const uint4*>(z + i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(z + i), y = *reinterpret_cast<const float4*>(z + i + 4);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    }
+  }
+  __device__ __forceinline__ int token(int cell, int e) const {
+    return first + cell * kCell + static_cast<int>(threadIdx.x & 31) * 8 + e;
+  }
+  // +inf as the largest number.  (Only where there is one.)
+  __device__ __forceinline__ void bound() const {
+    for (int i = threadIdx.x; i < cells * kCell; i += kThreads) {
+      if constexpr (sizeof(T) == 2) {
+        if (__bfloat162float(z[i]) == INFINITY) z[i] = __float2bfloat16(largest<T>());
+      } else {
+        if (z[i] == INFINITY) z[i] = largest<T>();
+      }
+    }
+    __syncthreads();
   }
 };
 
+// n logits into shared memory; this thread's largest.
 template <typename T, int VEC>
-__device__ __forceinline__ Ends load_row(const Row& row, const T* from) {
-  Ends ends;
-  const auto clean = [](float x) { return isnan(x) ? -INFINITY : fminf(x + 0.f, FLT_MAX); };
+__device__ __forceinline__ float load_row(const Row<T>& row, const T* from, int n) {
+  float top = -INFINITY;
   if constexpr (VEC == 1) {
 #pragma unroll 8
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
-      float x;
-      if constexpr (sizeof(T) == 2) x = clean(__bfloat162float(from[i]));
-      else x = clean(from[i]);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const T x = from[i];
       row.z[i] = x;
-      ends.take(x);
+      top = fmaxf(top, static_cast<float>(x));
     }
   } else {
     static_assert(VEC * sizeof(T) == 16, "16 bytes");
+    __nv_bfloat162 pair = __halves2bfloat162(__float2bfloat16(-INFINITY), __float2bfloat16(-INFINITY));
 #pragma unroll 4
-    for (int i = threadIdx.x * VEC; i < row.n; i += kThreads * VEC) {  // row.n is a multiple of VEC
+    for (int i = threadIdx.x * VEC; i < n; i += kThreads * VEC) {  // n is a multiple of VEC
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(from + i));
+      *reinterpret_cast<uint4*>(row.z + i) = v;
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float x[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if constexpr (sizeof(T) == 2) x[e] = clean(e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]));
-        else x[e] = clean(__uint_as_float(w[e]));
-        ends.take(x[e]);
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) pair = __hmax2(pair, *reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+        else top = fmaxf(top, __uint_as_float(w[e]));
       }
-#pragma unroll
-      for (int e = 0; e < VEC; e += 4)
-        *reinterpret_cast<float4*>(row.z + i + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
     }
+    if constexpr (sizeof(T) == 2) top = fmaxf(__low2float(pair), __high2float(pair));
   }
-  return ends;
+  for (int i = n + threadIdx.x; i < row.cells * kCell; i += kThreads) {
+    if constexpr (sizeof(T) == 2) row.z[i] = __float2bfloat16(-INFINITY);
+    else row.z[i] = -INFINITY;
+  }
+  return top;
 }
 
-// A border's candidates, brought together from the CTAs' lists: thread i has the
-// i-th, sh.cand and sh.cand_i have all.
+// A border's candidates, brought together from the CTAs' parts.
 template <int CTAS>
 __device__ __forceinline__ void collect(Shared& sh, int n) {
   int i = threadIdx.x;
   if (i < n) {
     int r = 0;
     for (; r < CTAS - 1 && i >= sh.found[r].n; ++r) i -= sh.found[r].n;
-    sh.cand[threadIdx.x] = sh.seg_z[r][i];
-    sh.cand_i[threadIdx.x] = sh.seg_i[r][i];
+    sh.cand[threadIdx.x] = sh.seg[r * (2 * kFew / CTAS) + i];
   }
   __syncthreads();
 }
@@ -329,11 +357,13 @@ struct Border {
 // target, at least 1; where it is past the whole sum the border's value is
 // -inf.  All threads of the cluster find the same.  Counts whose tokens down to
 // the border are few end as a list.
-template <bool WEIGHTED, int CTAS, typename F>
-__device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh, const Row& row, float lo, float hi,
+template <bool WEIGHTED, int CTAS, typename T, typename F>
+__device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float hi,
                                          float top, Scale c, F target_of) {
+  constexpr int kPart = CTAS == 1 ? kFew : 2 * kFew / CTAS;  // candidates from one CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = static_cast<int>(cluster.block_rank());
   unsigned long long above = 0, target = 0;
+  bool lists = !WEIGHTED;
   Range range;
   for (int level = 0;; ++level) {
     range.set(lo, hi, level >= 2);
@@ -341,37 +371,35 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
       *reinterpret_cast<uint4*>(&sh.bins[2 * i]) = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) sh.n = 0, sh.lo = 0xffffffffu, sh.hi = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
-      const float z = row.z[i];
-      if (!range.has(z)) continue;
-      if constexpr (WEIGHTED) {
-        const unsigned long long w = weight(z, top, c, sh.table);
-        if (w != 0) add64(&sh.bins[range.bin(z)], w);
-      } else {
-        atomicAdd(reinterpret_cast<unsigned int*>(&sh.bins[range.bin(z)]), 1u);
+    for (int cell = warp; cell < row.cells; cell += kWarps) {
+      float z[8];
+      row.get(cell, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (!range.has(z[e])) continue;
+        if constexpr (WEIGHTED) {
+          const unsigned long long w = weight(z[e], top, c, sh.table);
+          if (w != 0) add64(&sh.bins[range.bin(z[e])], w);
+        } else {
+          atomicAdd(reinterpret_cast<unsigned int*>(&sh.bins[range.bin(z[e])]), 1u);
+        }
       }
     }
     __syncthreads();
-    {  // the groups' sums, to all CTAs: of a group's eight threads each tells one
-      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sh.bins[4 * threadIdx.x]);
-      const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&sh.bins[4 * threadIdx.x + 2]);
-      unsigned long long sum = x.x + x.y + y.x + y.y;
+    {  // the groups' sums, to all CTAs: of a group's 16 threads some tell one each
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sh.bins[2 * threadIdx.x]);
+      unsigned long long sum = x.x + x.y;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const int to = lane & 7;
-      if (to < CTAS) cluster.map_shared_rank(&sh, to)->groups[rank][threadIdx.x >> 3] = sum;
+      for (int o = 1; o < kGroup / 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int to = lane & (kGroup / 2 - 1);
+      if (to < CTAS) cluster.map_shared_rank(&sh, to)->groups[rank][threadIdx.x / (kGroup / 2)] = sum;
     }
     cluster.sync();
     // Every warp finds the border's group; the first one then its bin.
-    unsigned long long g[2] = {0, 0};
+    unsigned long long g = 0;
 #pragma unroll
-    for (int r = 0; r < CTAS; ++r) {
-      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh.groups[r][2 * lane]);
-      g[0] += v.x;
-      g[1] += v.y;
-    }
-    const unsigned long long upto = above + warp_scan(g[0] + g[1]);
+    for (int r = 0; r < CTAS; ++r) g += sh.groups[r][lane];
+    const unsigned long long upto = above + warp_scan(g);
     const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31) - above;
     if (level == 0) {
       target = target_of(all);
@@ -380,13 +408,9 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
         return Border{-INFINITY, all, target, 0};
       }
     }
-    const int at_lane = __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1;
-    const unsigned long long from = __shfl_sync(0xffffffffu, upto - g[0] - g[1], at_lane);
-    const unsigned long long half = __shfl_sync(0xffffffffu, g[0], at_lane);
-    const bool second = from + half < target;
-    const int group = 2 * at_lane + second;
     if (warp == 0) {
-      const unsigned long long before = from + (second ? half : 0ULL);
+      const int group = __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1;
+      const unsigned long long before = __shfl_sync(0xffffffffu, upto - g, group);
       unsigned long long b = 0, part[CTAS];
 #pragma unroll
       for (int r = 0; r < CTAS; ++r) part[r] = cluster.map_shared_rank(sh.bins, r)[group * kGroup + lane];
@@ -394,32 +418,38 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
       for (int r = 0; r < CTAS; ++r) b += part[r];
       const unsigned long long s = before + warp_scan(b);
       const int at = __ffs(__ballot_sync(0xffffffffu, s >= target)) - 1;
-      if (lane == at) sh.bin = group * kGroup + lane, sh.above = s - b, sh.rest = b;
+      if (lane == at) sh.bin = group * kGroup + lane, sh.above = s - b, sh.in_bin = b;
     }
     __syncthreads();
     const int bin = sh.bin;
-    above = sh.above;
     // All tokens down to the border where they are few (counts), else the bin's;
     // and the bin's ends.
-    const bool list = !WEIGHTED && level == 0 && above + sh.rest <= kFew;
+    const bool list = lists && level == 0 && sh.above + sh.in_bin <= kFew;
+    float from, to;
+    range.near(bin, &from, &to);
+    if (list) to = hi;
     uint32_t l = 0xffffffffu, h = 0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
-      const float z = row.z[i];
-      if (!range.has(z)) continue;
-      const int mine = range.bin(z);
-      if (mine > bin || (mine < bin && !list)) continue;
-      l = min(l, ordered(z));
-      h = max(h, ordered(z));
-      const int at = atomicAdd(&sh.n, 1);
-      if (at >= kFew) continue;
-      if (list) {
-        Shared* to = cluster.map_shared_rank(&sh, 0);
-        to->seg_z[rank][at] = z;
-        to->seg_i[rank][at] = row.first + i;
-      } else {
+    for (int cell = warp; cell < row.cells; cell += kWarps) {
+      float z[8];
+      row.get(cell, z);
 #pragma unroll
-        for (int r = 0; r < CTAS; ++r) cluster.map_shared_rank(&sh, r)->seg_z[rank][at] = z;
+      for (int e = 0; e < 8; ++e) {
+        if (!(z[e] >= from && z[e] <= to)) continue;
+        const int mine = range.bin(z[e]);
+        if (mine > bin || (mine < bin && !list)) continue;
+        const float clean = z[e] + 0.f;  // -0 is 0
+        l = min(l, ordered(clean));
+        h = max(h, ordered(clean));
+        const int at = atomicAdd(&sh.n, 1);
+        if (at >= kPart) continue;
+        const Candidate one{clean, row.token(cell, e)};
+        const int place = rank * kPart + at;
+        if (list) {
+          cluster.map_shared_rank(&sh, 0)->seg[place] = one;
+        } else {
+#pragma unroll
+          for (int r = 0; r < CTAS; ++r) cluster.map_shared_rank(&sh, r)->seg[place] = one;
+        }
       }
     }
     l = __reduce_min_sync(0xffffffffu, l);
@@ -432,6 +462,7 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     if (threadIdx.x < CTAS) cluster.map_shared_rank(&sh, threadIdx.x)->found[rank] = Found{sh.n, sh.lo, sh.hi};
     cluster.sync();
     int n = 0;
+    bool fits = true;
     l = 0xffffffffu, h = 0;
 #pragma unroll
     for (int r = 0; r < CTAS; ++r) {
@@ -439,26 +470,34 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
       l = min(l, f.lo);
       h = max(h, f.hi);
       n += f.n;
+      fits = fits && f.n <= kPart;
     }
     if (list) {
-      if (rank == 0) collect<CTAS>(sh, n);
-      return Border{0.f, 0, target, n};
+      if (fits) {
+        if (rank == 0) collect<CTAS>(sh, n);
+        return Border{0.f, 0, target, n};
+      }
+      lists = false;  // most of them in one CTA's part: the same again, without the list
+      --level;
+      above = 0;
+      continue;
     }
+    above = sh.above;
     lo = unordered(l), hi = unordered(h);
     if (l == h) return Border{hi, above, target, 0};
-    if (n > kFew) continue;
+    if (!fits || n > kFew) continue;
     collect<CTAS>(sh, n);
     if (static_cast<int>(threadIdx.x) < n)
-      sh.cand_w[threadIdx.x] = WEIGHTED ? weight(sh.cand[threadIdx.x], top, c, sh.table) : 1ULL;
+      sh.cand_w[threadIdx.x] = WEIGHTED ? weight(sh.cand[threadIdx.x].z, top, c, sh.table) : 1ULL;
     __syncthreads();
     // Two threads for each of them: what lies above it, what equals it.
     static_assert(2 * kFew <= kThreads, "two threads a candidate");
-    const float mine = sh.cand[min(static_cast<int>(threadIdx.x >> 1), n - 1)];
+    const float mine = sh.cand[min(static_cast<int>(threadIdx.x >> 1), n - 1)].z;
     unsigned long long over = 0, same = 0;
     for (int i = threadIdx.x & 1; i < n; i += 2) {
       const unsigned long long w = sh.cand_w[i];
-      over += sh.cand[i] > mine ? w : 0ULL;
-      same += sh.cand[i] == mine ? w : 0ULL;
+      over += sh.cand[i].z > mine ? w : 0ULL;
+      same += sh.cand[i].z == mine ? w : 0ULL;
     }
     over += above + __shfl_xor_sync(0xffffffffu, over, 1);
     same += __shfl_xor_sync(0xffffffffu, same, 1);
@@ -489,18 +528,18 @@ __device__ __forceinline__ void put(const SampleArgs& p, int b, int token, unsig
 __device__ __forceinline__ void finish_list(Shared& sh, int n, const Settings& set, float top, Scale c,
                                             const SampleArgs& p, int b) {
   const int t = static_cast<int>(threadIdx.x), mine = t >> 1;
-  const float z = sh.cand[min(mine, n - 1)];
-  const int index = sh.cand_i[min(mine, n - 1)];
+  const Candidate me = sh.cand[min(mine, n - 1)];
   int by_z = 0, by_i = 0;  // how many come first
   for (int i = t & 1; i < n; i += 2) {
-    const bool lower = sh.cand_i[i] < index;
-    by_z += sh.cand[i] > z || (sh.cand[i] == z && lower);
+    const Candidate other = sh.cand[i];
+    const bool lower = other.token < me.token;
+    by_z += other.z > me.z || (other.z == me.z && lower);
     by_i += lower;
   }
   by_z += __shfl_xor_sync(0xffffffffu, by_z, 1);
   by_i += __shfl_xor_sync(0xffffffffu, by_i, 1);
   const bool is = mine < n && (t & 1) == 0;
-  const unsigned long long w = is && by_z < set.top_k ? weight(z, top, c, sh.table) : 0ULL;
+  const unsigned long long w = is && by_z < set.top_k ? weight(me.z, top, c, sh.table) : 0ULL;
   unsigned long long* sorted = sh.bins;  // the bins have served
   for (int i = t; i < 2 * kFew; i += kThreads) sorted[i] = 0;
   __syncthreads();
@@ -515,7 +554,7 @@ __device__ __forceinline__ void finish_list(Shared& sh, int n, const Settings& s
   __syncthreads();
   if (is) {
     sorted[kFew + by_i] = sorted[by_z];
-    sh.cand_w[by_i] = static_cast<unsigned long long>(index);
+    sh.cand_w[by_i] = static_cast<unsigned long long>(me.token);
   }
   __syncthreads();
   unsigned long long whole;
@@ -533,10 +572,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   const int rank = static_cast<int>(cluster.block_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = static_cast<int>(blockIdx.y);
-  const int first = rank * stretch;
-  const Row row{reinterpret_cast<float*>(smem + sizeof(Shared)), max(0, min(stretch, p.V - first)), first};
-  if (threadIdx.x == 0) sh.lo = 0xffffffffu, sh.hi = 0, sh.cut = 0xffffffffu, sh.live = 0, sh.cell = -1;
-  __syncthreads();
+  const int n_row = max(0, min(stretch, p.V - rank * stretch));
+  const Row<T> row{reinterpret_cast<T*>(smem + sizeof(Shared)), (n_row + kCell - 1) / kCell, rank * stretch};
+  cluster.barrier_arrive();  // a CTA that runs may be written to
   grid_dep_wait();
   grid_dep_launch_dependents();
   const float temperature = p.temperature != nullptr ? __ldg(p.temperature + b) : 1.f;
@@ -546,68 +584,67 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   Settings set;
   set.u = __ldg(p.uniform + b);
   for (int i = threadIdx.x; i < kTable; i += kThreads) sh.table[i] = kPowers.v[i];
-  Ends mine = load_row<T, VEC>(row, static_cast<const T*>(p.logits) + b * p.row_stride + first);
+  float top = load_row<T, VEC>(row, static_cast<const T*>(p.logits) + b * p.row_stride + row.first, n_row);
   const bool greedy = !(temperature > 0.f);
   set.top_k = greedy ? 1 : k_asked;
   set.top_p = !greedy && p_asked < 1.f ? p_asked : 1.f;
   set.least = !greedy && m_asked > 0.f ? __float2ull_ru(fminf(m_asked, 1.f) * 0x1p44f) : 0ULL;
   const Scale c = greedy ? Scale{0.f, 0.f} : scale_of(temperature);
 
-  // The row's largest and smallest logit, how many it has.  And a logit that is
-  // not over the top_k-th largest, without which the search would put the whole
-  // row into bins: of `parts` parts of the row, at least top_k, the smallest of
-  // their largest.
+  // The row's largest logit.  And one that is not over the top_k-th largest,
+  // without which the search would put the whole row into bins: of `parts` parts
+  // of the row, at least top_k, the smallest of their largest.
+  float cut = top;
   {
     int o = 32;  // threads of a part
     while (o > 1 && CTAS * kThreads / o < set.top_k) o >>= 1;
-    uint32_t cut = mine.hi;
-    for (int x = 1; x < o; x <<= 1) cut = max(cut, __shfl_xor_sync(0xffffffffu, cut, x));
-    cut = __reduce_min_sync(0xffffffffu, cut);
-    if (CTAS * kThreads < set.top_k) cut = 0;
-    const uint32_t l = __reduce_min_sync(0xffffffffu, mine.lo), h = __reduce_max_sync(0xffffffffu, mine.hi);
-    const int n = __reduce_add_sync(0xffffffffu, mine.n);
-    if (lane == 0) {
-      atomicMin(&sh.lo, l);
-      atomicMax(&sh.hi, h);
-      atomicMin(&sh.cut, cut);
-      atomicAdd(&sh.live, n);
-    }
+    for (int x = 1; x < o; x <<= 1) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, x));
+    const uint32_t l = __reduce_min_sync(0xffffffffu, ordered(cut)), h = __reduce_max_sync(0xffffffffu, ordered(top));
+    if (lane == 0) sh.warp_cut[warp] = l, sh.warp_top[warp] = unordered(h);
   }
   __syncthreads();
-  if (threadIdx.x < CTAS)
-    cluster.map_shared_rank(&sh, threadIdx.x)->ends[rank] =
-        make_uint4(sh.lo, sh.hi, sh.cut, static_cast<unsigned>(sh.live));
+  cluster.barrier_wait();
+  if (warp == 0) {
+    const uint32_t l = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh.warp_cut[lane] : 0xffffffffu);
+    const uint32_t h = __reduce_max_sync(0xffffffffu, lane < kWarps ? ordered(sh.warp_top[lane]) : 0u);
+    if (lane < CTAS) {
+      Shared* other = cluster.map_shared_rank(&sh, lane);
+      other->top[rank] = unordered(h);
+      other->cut[rank] = l;
+    }
+  }
   cluster.sync();
-  uint32_t l = 0xffffffffu, h = 0, cut = 0xffffffffu;
-  int live = 0;
+  uint32_t cut_at = 0xffffffffu;
 #pragma unroll
   for (int r = 0; r < CTAS; ++r) {
-    const uint4 e = sh.ends[r];
-    l = min(l, e.x);
-    h = max(h, e.y);
-    cut = min(cut, e.z);
-    live += static_cast<int>(e.w);
+    top = r == 0 ? sh.top[0] : fmaxf(top, sh.top[r]);
+    cut_at = min(cut_at, sh.cut[r]);
   }
-  if (live == 0) {
+  if (top == -INFINITY) {
     if (rank == 0 && threadIdx.x == 0) put(p, b, -1, 0, 0);
     return;  // the whole cluster
   }
-  const float top = unordered(h), bottom = unordered(l);
+  top += 0.f;  // -0 is 0
+  if (top == INFINITY) {
+    row.bound();
+    top = largest<T>();
+  }
+  cut = set.top_k <= CTAS * kThreads ? fminf(unordered(cut_at), top) : -INFINITY;
 
   // The threshold: tokens over `value`, and the first `ties` of those at it.
   float value = -INFINITY;
   long long ties = 0;
   if (set.top_k == 1) {
     value = top, ties = 1;
-  } else if (set.top_k > 0 && set.top_k < live) {
+  } else if (set.top_k > 0 && set.top_k < p.V) {
     const auto target_of = [&](unsigned long long) { return static_cast<unsigned long long>(set.top_k); };
-    const Border k = search<false, CTAS>(cluster, sh, row, unordered(max(l, cut)), top, top, c, target_of);
+    const Border k = search<false, CTAS>(cluster, sh, row, fmaxf(cut, -FLT_MAX), top, top, c, target_of);
     if (k.list > 0) {
       if (rank == 0) finish_list(sh, k.list, set, top, c, p, b);
       return;
     }
-    value = k.value;
-    ties = static_cast<long long>(k.target - k.above);
+    value = k.value;  // -inf: there are no more than top_k
+    ties = value == -INFINITY ? 0 : static_cast<long long>(k.target - k.above);
   }
   if (set.top_p < 1.f) {
     // The smallest part of what is left that makes up top_p of it.
@@ -618,8 +655,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     unsigned long long above = 0, target;
     float at = -INFINITY;
     if (value < top) {
-      const Border s = search<true, CTAS>(cluster, sh, row, value == -INFINITY ? bottom : unordered(ordered(value) + 1),
-                                          top, top, c, target_of);
+      const float reach = top - 45.5f / c.hi;  // below, weights are 0
+      const float next = value == -INFINITY ? -FLT_MAX : unordered(ordered(value) + 1);
+      const Border s = search<true, CTAS>(cluster, sh, row, fmaxf(next, reach), top, top, c, target_of);
       at = s.value, above = s.above, target = s.target;
     } else {
       target = target_of(0);
@@ -633,97 +671,106 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   const unsigned long long w_tie = ties > 0 ? weight(value, top, c, sh.table) : 0ULL;
   if (w_tie < set.least) ties = 0;
 
-  // The kept weights of every cell of 32 tokens, then of the CTA, then of the row.
-  const int cells = (row.n + 31) / 32;
-  for (int cell = warp; cell < cells; cell += kWarps) {
-    const int i = cell * 32 + lane;
-    const float z = i < row.n ? row.z[i] : -INFINITY;
-    unsigned long long w = z > value ? weight(z, top, c, sh.table) : 0ULL;
-    if (w < set.least) w = 0;
+  // The kept weights of every cell, then of the CTA, then of the row.
+  const auto kept_weight = [&](float z) {
+    const unsigned long long w = z > value ? weight(z, top, c, sh.table) : 0ULL;
+    return w < set.least ? 0ULL : w;
+  };
+  for (int cell = warp; cell < row.cells; cell += kWarps) {
+    float z[8];
+    row.get(cell, z);
+    unsigned long long w = 0;
+    int at = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w += kept_weight(z[e]);
+      at += z[e] == value;
+    }
     if (__any_sync(0xffffffffu, w != 0)) w = warp_sum(w);
-    const int at = __popc(__ballot_sync(0xffffffffu, z == value && z > -INFINITY));
-    if (lane == 0) sh.cells.over[cell] = w, sh.cells.ties[cell] = at;
+    at = __reduce_add_sync(0xffffffffu, at);
+    if (lane == 0) sh.cell_over[cell] = w, sh.cell_ties[cell] = at;
   }
   __syncthreads();
-  // A thread's two cells, and what lies ahead of them.
-  static_assert(kCells == 2 * kThreads && kSampleMaxVocab <= kMaxCluster * kCells * 32, "cells");
-  unsigned long long over[2], over_before;
-  int at[2], at_before;
-  {
+  // The first warp goes on with four cells a lane, and what lies ahead of them.
+  unsigned long long over[4], over_before = 0;
+  int at[4], at_before = 0;
+  if (warp == 0) {
+    static_assert(kCells == 4 * 32 && kSampleMaxVocab <= kMaxCluster * kCells * kCell, "cells");
+    unsigned long long sum = 0;
+    int sum_at = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int cell = 2 * static_cast<int>(threadIdx.x) + i;
-      over[i] = cell < cells ? sh.cells.over[cell] : 0ULL;
-      at[i] = cell < cells ? sh.cells.ties[cell] : 0;
+    for (int i = 0; i < 4; ++i) {
+      const bool is = 4 * lane + i < row.cells;
+      over[i] = is ? sh.cell_over[4 * lane + i] : 0ULL;
+      at[i] = is ? sh.cell_ties[4 * lane + i] : 0;
+      sum += over[i];
+      sum_at += at[i];
     }
-    const unsigned long long s = warp_scan(over[0] + over[1]);
-    const int t = warp_scan(at[0] + at[1]);
-    if (lane == 31) sh.warp_sum[warp] = s, sh.warp_ties[warp] = t;
-    __syncthreads();
-    over_before = s - over[0] - over[1];
-    at_before = t - at[0] - at[1];
-    unsigned long long all = 0;
-    int all_at = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      over_before += w < warp ? sh.warp_sum[w] : 0ULL;
-      at_before += w < warp ? sh.warp_ties[w] : 0;
-      all += sh.warp_sum[w];
-      all_at += sh.warp_ties[w];
-    }
-    if (threadIdx.x < CTAS) cluster.map_shared_rank(&sh, threadIdx.x)->kept[rank] = Kept{all, all_at};
+    const unsigned long long upto = warp_scan(sum);
+    const int at_upto = warp_scan(sum_at);
+    over_before = upto - sum;
+    at_before = at_upto - sum_at;
+    const Kept all{__shfl_sync(0xffffffffu, upto, 31), __shfl_sync(0xffffffffu, at_upto, 31)};
+    if (lane < CTAS) cluster.map_shared_rank(&sh, lane)->kept[rank] = all;
   }
   cluster.sync();  // the last: nobody writes to another CTA from here on
+  if (warp != 0) return;
   const auto kept = [](long long left, int n) {
     return static_cast<unsigned long long>(min(left, static_cast<long long>(n)));
   };
   unsigned long long whole = 0, ahead = 0;
-  long long ties_left = 0;  // for this CTA and those behind it
-  {
-    long long left = ties;
+  long long ties_left = 0, left = ties;  // for this CTA and those behind it
 #pragma unroll
-    for (int r = 0; r < CTAS; ++r) {
-      const Kept other = sh.kept[r];
-      if (r == rank) ahead = whole, ties_left = left;
-      const unsigned long long take = kept(left, other.ties);
-      whole += other.over + take * w_tie;
-      left -= static_cast<long long>(take);
-    }
+  for (int r = 0; r < CTAS; ++r) {
+    const Kept other = sh.kept[r];
+    if (r == rank) ahead = whole, ties_left = left;
+    const unsigned long long take = kept(left, other.ties);
+    whole += other.over + take * w_tie;
+    left -= static_cast<long long>(take);
   }
   const unsigned long long target = drawn(set.u, whole);  // the token's running sum is the first over it
-  // The cell, in this CTA or another; then, by its warp, the token.
+  // The cell, in this CTA or another; then the token.
+  int cell = -1, cell_at = 0;
+  unsigned long long rest = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const unsigned long long from = ahead + over_before + kept(ties_left, at_before) * w_tie;
+    const int before = at_before;
     over_before += over[i];
     at_before += at[i];
     const unsigned long long to = ahead + over_before + kept(ties_left, at_before) * w_tie;
-    if (from <= target && target < to) {
-      sh.cell = 2 * static_cast<int>(threadIdx.x) + i;
-      sh.rest = target - from;
-      sh.ties_before = at_before - at[i];
-    }
+    if (from <= target && target < to) cell = 4 * lane + i, cell_at = before, rest = target - from;
   }
-  __syncthreads();
-  const int cell = sh.cell;
-  if (cell < 0 || cell % kWarps != warp) return;
-  const unsigned long long rest = sh.rest;
-  ties_left -= min(ties_left, static_cast<long long>(sh.ties_before));
-  const int i = cell * 32 + lane;
-  const float z = i < row.n ? row.z[i] : -INFINITY;
-  const bool tie = z == value && z > -INFINITY;
-  unsigned long long w = z > value ? weight(z, top, c, sh.table) : 0ULL;
-  if (w < set.least) w = 0;
-  const int rank_at = __popc(__ballot_sync(0xffffffffu, tie) & ((1u << lane) - 1));
-  if (tie && rank_at < ties_left) w = w_tie;
-  const unsigned long long upto = warp_scan(w);
-  if (upto - w <= rest && rest < upto) put(p, b, first + i, w, whole);
+  const uint32_t who = __ballot_sync(0xffffffffu, cell >= 0);
+  if (who == 0) return;
+  cell = __shfl_sync(0xffffffffu, cell, __ffs(who) - 1);
+  cell_at = __shfl_sync(0xffffffffu, cell_at, __ffs(who) - 1);
+  rest = __shfl_sync(0xffffffffu, rest, __ffs(who) - 1);
+  float z[8];
+  row.get(cell, z);
+  unsigned long long w[8], sum = 0;
+  int n_at = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) n_at += z[e] == value;
+  int rank_at = cell_at + warp_scan(n_at) - n_at;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    w[e] = kept_weight(z[e]);
+    if (z[e] == value) w[e] = rank_at++ < ties_left ? w_tie : 0ULL;
+    sum += w[e];
+  }
+  unsigned long long from = warp_scan(sum) - sum;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (from <= rest && rest < from + w[e]) put(p, b, row.token(cell, e), w[e], whole);
+    from += w[e];
+  }
 }
 
 template <typename T, int VEC, int CTAS>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
-  const int stretch = ((a.V + CTAS - 1) / CTAS + 31) / 32 * 32;
-  const size_t smem = sizeof(Shared) + static_cast<size_t>(stretch) * sizeof(float);
+  const int stretch = ((a.V + CTAS - 1) / CTAS + kCell - 1) / kCell * kCell;
+  const size_t smem = sizeof(Shared) + static_cast<size_t>(stretch) * sizeof(T);
   auto kernel = sample_kernel<T, VEC, CTAS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
