@@ -105,15 +105,15 @@ __device__ __forceinline__ unsigned long long share_of(float p, unsigned long lo
 // exp((z - top) / T) in units of 2^-44.  With y = (top - z) log2(e) / T as the
 // sum of two floats, y = k / 512 + r, the weight is 2^-(k/512), from the table,
 // times 1 - q, q = 1 - 2^-r by its series in whole numbers of 2^-40: |r| <=
-// 2^-10, so three terms do.  Floats become whole numbers by adding a power of two
+// 2^-10, so three terms do.  No branch, so that several run at once: one takes 250
+// cycles, of which its instructions are a fifth.  Floats become whole numbers by adding a power of two
 // and taking the bits: conversions run at an eighth of the rate.
 __device__ __forceinline__ unsigned long long weight(float z, float top, Scale c, const unsigned long long* table) {
   float d = top - z;
   const float back = d - top;
   float err = (top - (d - back)) - (z + back);  // top - z = d + err
   if (d > 3.0e38f) d = FLT_MAX, err = 0.f;
-  const float y = d * c.hi;
-  if (!(y < 45.f)) return 0;
+  const float y = fminf(d * c.hi, 45.f);  // from 45 on 0: the last shift
   const float y2 = fmaf(d, c.hi, -y) + fmaf(d, c.lo, err * c.hi);
   constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: one unit of its last place is 1
   const float at = fmaf(y, static_cast<float>(kTable), kWhole);
@@ -153,6 +153,9 @@ struct Kept {
   unsigned long long over;  // weights over the threshold
   int ties;                 // tokens at it
 };
+struct Mass {
+  unsigned long long all, above;  // weights: of all tokens, of those above the window
+};
 struct Candidate {
   float z;
   int token;
@@ -166,6 +169,7 @@ struct Shared {
   uint32_t cut[kMaxCluster];
   Found found[kMaxCluster];
   Kept kept[kMaxCluster];
+  Mass mass[kMaxCluster];
   Candidate seg[2 * kFew];  // a part for each CTA
   Candidate cand[kFew];
   unsigned long long cand_w[kFew];
@@ -284,6 +288,10 @@ struct Row {
   __device__ __forceinline__ int token(int cell, int e) const {
     return first + cell * kCell + static_cast<int>(threadIdx.x & 31) * 8 + e;
   }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 2) return __bfloat162float(z[i]);
+    else return z[i];
+  }
   // +inf as the largest number.  (Only where there is one.)
   __device__ __forceinline__ void bound() const {
     for (int i = threadIdx.x; i < cells * kCell; i += kThreads) {
@@ -343,6 +351,12 @@ __device__ __forceinline__ void collect(Shared& sh, int n) {
   __syncthreads();
 }
 
+__device__ __forceinline__ void clear_bins(Shared& sh) {
+  for (int i = threadIdx.x; i < kBins / 2; i += kThreads)
+    *reinterpret_cast<uint4*>(&sh.bins[2 * i]) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+
 // What a search finds: the value at which the sum by falling value reaches the
 // target, the sum over larger values, and the target.  Or `list`: sh.cand has
 // all tokens that can be kept (in CTA 0).
@@ -352,36 +366,46 @@ struct Border {
   int list;
 };
 
+// A stretch of logits that a border lies in by all appearances, with its weights in
+// sh.bins and the row's in sh.mass, each CTA's own.
+struct Window {
+  bool is;
+  Range range;
+};
+
 // The border of the sum of 1 (WEIGHTED false) or of the weights over the row's
 // tokens with lo <= z <= hi, by falling z.  target_of(whole sum) gives the
 // target, at least 1; where it is past the whole sum the border's value is
 // -inf.  All threads of the cluster find the same.  Counts whose tokens down to
-// the border are few end as a list.
+// the border are few end as a list.  A border that is not in the window: `list`
+// is -1.
 template <bool WEIGHTED, int CTAS, typename T, typename F>
 __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float hi,
-                                         float top, Scale c, F target_of) {
+                                         float top, Scale c, F target_of, const Window& window = Window{false, {}}) {
   constexpr int kPart = CTAS == 1 ? kFew : 2 * kFew / CTAS;  // candidates from one CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = static_cast<int>(cluster.block_rank());
   unsigned long long above = 0, target = 0;
   bool lists = !WEIGHTED;
   Range range;
   for (int level = 0;; ++level) {
-    range.set(lo, hi, level >= 2);
-    for (int i = threadIdx.x; i < kBins / 2; i += kThreads)
-      *reinterpret_cast<uint4*>(&sh.bins[2 * i]) = make_uint4(0, 0, 0, 0);
+    const bool ready = WEIGHTED && level == 0 && window.is;
+    if (ready) range = window.range;
+    else range.set(lo, hi, level >= 2);
     if (threadIdx.x == 0) sh.n = 0, sh.lo = 0xffffffffu, sh.hi = 0;
-    __syncthreads();
-    for (int cell = warp; cell < row.cells; cell += kWarps) {
-      float z[8];
-      row.get(cell, z);
+    if (!ready) {
+      clear_bins(sh);
+      for (int cell = warp; cell < row.cells; cell += kWarps) {
+        float z[8];
+        row.get(cell, z);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (!range.has(z[e])) continue;
-        if constexpr (WEIGHTED) {
-          const unsigned long long w = weight(z[e], top, c, sh.table);
-          if (w != 0) add64(&sh.bins[range.bin(z[e])], w);
-        } else {
-          atomicAdd(reinterpret_cast<unsigned int*>(&sh.bins[range.bin(z[e])]), 1u);
+        for (int e = 0; e < 8; ++e) {
+          if (!range.has(z[e])) continue;
+          if constexpr (WEIGHTED) {
+            const unsigned long long w = weight(z[e], top, c, sh.table);
+            if (w != 0) add64(&sh.bins[range.bin(z[e])], w);
+          } else {
+            atomicAdd(reinterpret_cast<unsigned int*>(&sh.bins[range.bin(z[e])]), 1u);
+          }
         }
       }
     }
@@ -396,16 +420,20 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     }
     cluster.sync();
     // Every warp finds the border's group; the first one then its bin.
-    unsigned long long g = 0;
+    unsigned long long g = 0, all = 0;
 #pragma unroll
     for (int r = 0; r < CTAS; ++r) g += sh.groups[r][lane];
-    const unsigned long long upto = above + warp_scan(g);
-    const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31) - above;
+    if (ready) {
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) above += sh.mass[r].above, all += sh.mass[r].all;
+    }
+    const unsigned long long upto = above + warp_scan(g), end = __shfl_sync(0xffffffffu, upto, 31);
     if (level == 0) {
+      if (!ready) all = end;
       target = target_of(all);
-      if (target > all) {
+      if (target > all || target <= above || target > end) {
         cluster.sync();  // all have read the groups
-        return Border{-INFINITY, all, target, 0};
+        return Border{-INFINITY, all, target, target > all ? 0 : -1};
       }
     }
     if (warp == 0) {
@@ -432,24 +460,24 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     for (int cell = warp; cell < row.cells; cell += kWarps) {
       float z[8];
       row.get(cell, z);
+      uint32_t in = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (!(z[e] >= from && z[e] <= to)) continue;
-        const int mine = range.bin(z[e]);
+      for (int e = 0; e < 8; ++e) in |= static_cast<uint32_t>(z[e] >= from && z[e] <= to) << e;
+      while (in != 0) {  // seldom
+        const int e = __ffs(in) - 1;
+        in &= in - 1;
+        const int i = cell * kCell + lane * 8 + e;
+        const float clean = row.at(i) + 0.f;  // -0 is 0
+        const int mine = range.bin(clean);
         if (mine > bin || (mine < bin && !list)) continue;
-        const float clean = z[e] + 0.f;  // -0 is 0
         l = min(l, ordered(clean));
         h = max(h, ordered(clean));
         const int at = atomicAdd(&sh.n, 1);
         if (at >= kPart) continue;
-        const Candidate one{clean, row.token(cell, e)};
+        const Candidate one{clean, row.first + i};
         const int place = rank * kPart + at;
-        if (list) {
-          cluster.map_shared_rank(&sh, 0)->seg[place] = one;
-        } else {
-#pragma unroll
-          for (int r = 0; r < CTAS; ++r) cluster.map_shared_rank(&sh, r)->seg[place] = one;
-        }
+#pragma unroll 1
+        for (int r = 0; r < (list ? 1 : CTAS); ++r) cluster.map_shared_rank(&sh, r)->seg[place] = one;
       }
     }
     l = __reduce_min_sync(0xffffffffu, l);
@@ -505,6 +533,93 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     __syncthreads();
     return Border{sh.value, sh.value_above, target, 0};
   }
+}
+
+// Looks for the logit at which the weights over `lo` make up `part` of all, by
+// counts in bins and the weight in each bin's middle.  Then every token's weight,
+// once: the sum of all, for every cell the sum (kept: of weights from `least` on)
+// of its tokens above a window around that logit, and the window's in bins.  With
+// the middles, 4 bins either way missed a border only where single tokens make
+// up most of the row; such rows are searched again without a window.
+template <int CTAS, typename T>
+__device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float top,
+                                       Scale c, float part, unsigned long long least) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = static_cast<int>(cluster.block_rank());
+  Range range;
+  range.set(lo, top, false);
+  clear_bins(sh);
+  unsigned int* counts = reinterpret_cast<unsigned int*>(sh.bins);
+  for (int cell = warp; cell < row.cells; cell += kWarps) {
+    float z[8];
+    row.get(cell, z);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (range.has(z[e])) atomicAdd(&counts[range.bin(z[e])], 1u);
+  }
+  __syncthreads();
+  const float step = -c.hi / range.per;  // log2 of the weights from bin to bin
+  {
+    const int b = 2 * static_cast<int>(threadIdx.x);
+    float sum = counts[b] * ex2(b * step) + counts[b + 1] * ex2((b + 1) * step);
+#pragma unroll
+    for (int o = 1; o < kGroup / 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int to = lane & (kGroup / 2 - 1);
+    if (to < CTAS)
+      reinterpret_cast<float*>(cluster.map_shared_rank(&sh, to)->groups[rank])[threadIdx.x / (kGroup / 2)] = sum;
+  }
+  cluster.sync();
+  if (warp == 0) {
+    float g = 0.f;
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) g += reinterpret_cast<const float*>(sh.groups[r])[lane];
+    const float upto = warp_scan(g);
+    const float want = part * __shfl_sync(0xffffffffu, upto, 31);
+    const uint32_t over = __ballot_sync(0xffffffffu, upto >= want);
+    const int group = over != 0 ? __ffs(over) - 1 : 31;
+    const float before = __shfl_sync(0xffffffffu, upto - g, group);
+    unsigned int n[CTAS], count = 0;
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r)
+      n[r] = reinterpret_cast<const unsigned int*>(cluster.map_shared_rank(sh.bins, r))[group * kGroup + lane];
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) count += n[r];
+    const int b = group * kGroup + lane;
+    const uint32_t past = __ballot_sync(0xffffffffu, before + warp_scan(count * ex2(b * step)) >= want);
+    if (lane == 0) sh.bin = group * kGroup + (past != 0 ? __ffs(past) - 1 : 31);
+  }
+  cluster.sync();  // all have read the others' counts
+  const float from = fmaxf(lo, top - (sh.bin + 4) / range.per), to = fminf(top, top - (sh.bin - 4) / range.per);
+  Window window{true, {}};
+  window.range.set(from, to, false);
+  clear_bins(sh);
+  unsigned long long all = 0, above = 0;
+  for (int cell = warp; cell < row.cells; cell += kWarps) {
+    unsigned long long kept = 0;
+    float z[8];
+    row.get(cell, z);
+#pragma unroll
+    for (int half = 0; half < 8; half += 4) {
+      unsigned long long w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = weight(z[half + e], top, c, sh.table);
+        w[e] = z[half + e] >= lo ? w[e] : 0ULL;
+        all += w[e];
+        const unsigned long long over = z[half + e] > to ? w[e] : 0ULL;
+        above += over;
+        kept += over >= least ? over : 0ULL;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (z[half + e] >= from && z[half + e] <= to) add64(&sh.bins[window.range.bin(z[half + e])], w[e]);
+    }
+    if (__any_sync(0xffffffffu, kept != 0)) kept = warp_sum(kept);
+    if (lane == 0) sh.cell_over[cell] = kept;
+  }
+  block_scan(sh, all, &all);
+  block_scan(sh, above, &above);
+  if (threadIdx.x < CTAS) cluster.map_shared_rank(&sh, threadIdx.x)->mass[rank] = Mass{all, above};
+  return window;
 }
 
 struct Settings {
@@ -634,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   // The threshold: tokens over `value`, and the first `ties` of those at it.
   float value = -INFINITY;
   long long ties = 0;
+  float counted = INFINITY;  // cell_over has the tokens over it
   if (set.top_k == 1) {
     value = top, ties = 1;
   } else if (set.top_k > 0 && set.top_k < p.V) {
@@ -657,7 +773,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     if (value < top) {
       const float reach = top - 45.5f / c.hi;  // below, weights are 0
       const float next = value == -INFINITY ? -FLT_MAX : unordered(ordered(value) + 1);
-      const Border s = search<true, CTAS>(cluster, sh, row, fmaxf(next, reach), top, top, c, target_of);
+      const float lo = fmaxf(next, reach);
+      Border s{0.f, 0, 0, -1};
+      if (value == -INFINITY) {
+        const Window window = look<CTAS>(cluster, sh, row, lo, top, c, set.top_p, set.least);
+        s = search<true, CTAS>(cluster, sh, row, lo, top, top, c, target_of, window);
+        if (s.list == 0) counted = window.range.hi;
+      }
+      if (s.list < 0) s = search<true, CTAS>(cluster, sh, row, lo, top, top, c, target_of);
       at = s.value, above = s.above, target = s.target;
     } else {
       target = target_of(0);
@@ -677,18 +800,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     return w < set.least ? 0ULL : w;
   };
   for (int cell = warp; cell < row.cells; cell += kWarps) {
-    float z[8];
-    row.get(cell, z);
     unsigned long long w = 0;
     int at = 0;
+    float z[8];
+    row.get(cell, z);
+    if (value == -INFINITY) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w += kept_weight(z[e]);
-      at += z[e] == value;
+      for (int e = 0; e < 8; ++e) w += kept_weight(z[e]);
+    } else {
+      uint32_t in = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        in |= static_cast<uint32_t>(z[e] > value && z[e] <= counted) << e;
+        at += z[e] == value;
+      }
+      for (; in != 0; in &= in - 1) w += kept_weight(row.at(cell * kCell + lane * 8 + __ffs(in) - 1));  // few
     }
     if (__any_sync(0xffffffffu, w != 0)) w = warp_sum(w);
     at = __reduce_add_sync(0xffffffffu, at);
-    if (lane == 0) sh.cell_over[cell] = w, sh.cell_ties[cell] = at;
+    if (lane == 0) {
+      if (counted < INFINITY) w += sh.cell_over[cell];
+      sh.cell_over[cell] = w;
+      sh.cell_ties[cell] = at;
+    }
   }
   __syncthreads();
   // The first warp goes on with four cells a lane, and what lies ahead of them.
