@@ -18,6 +18,7 @@
 // every 8, and one ldmatrix hands each lane the words that it needs: lane (g,
 // t) gets word t of chunk w of row g, codes 32 w + 8 t .. + 7, so that the 16
 // values of a step lie within one group of 32 or more.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,14 +28,16 @@
 #include "tokens.h"
 #include "txl_device.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace txl {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kBlockK = 256;               // codes of a row in a block: 128 bytes
-constexpr int kStages = 4;                 // blocks in flight per warp
 constexpr int kCodeBytes = 16 * kBlockK / 2;
 constexpr int kXBytes = 64 * 1024;         // of x in shared memory
+constexpr int kMaxSplit = 8;
 
 struct Args {
   const __nv_bfloat16* x;
@@ -44,13 +47,15 @@ struct Args {
   const float* bias;
   int m, n, k;
   int wr_log;  // 2^wr_log of the warps stand along n, the others share the blocks of k
-  int kx;      // rows of k whose x is in shared memory at a time, a multiple of kBlockK
+  int split;   // CTAs of a cluster that share k
+  int ks;      // rows of k of one of them, a multiple of kBlockK
+  int kx;      // of these, rows whose x is in shared memory at a time, a multiple of kBlockK
   bool relu;
 };
 
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -61,82 +66,129 @@ __device__ __forceinline__ void copies_wait() {
 // Codes j and j + 4 of a word, less 8, as bf16.
 template <int J>
 __device__ __forceinline__ uint32_t pair_of(uint32_t word) {
-  const uint32_t w = (word >> (4 * J) & 0x000F000Fu) | 0x43004300u;
-  const uint32_t less = 0xC308C308u;  // -136
-  uint32_t r;
+  const uint32_t at = word >> (4 * J), mask = 0x000F000Fu, base = 0x43004300u, less = 0xC308C308u;  // less: -136
+  uint32_t w, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(w) : "r"(at), "r"(mask), "r"(base));  // at & mask | base
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(less));
   return r;
 }
 
 template <int G, int MT>
 struct Shape {
+  static constexpr int kStages = MT == 1 ? 3 : 4;  // blocks of a warp, one less in flight
+  static constexpr int kPerSm = MT == 1 ? 3 : 2;
   static constexpr int kGroups = kBlockK / G;  // of a block
   static constexpr int kScaleBytes = kGroups * 32;
   static constexpr int kStage = kCodeBytes + kScaleBytes;
   static constexpr int kTokens = 8 * MT;
+  static constexpr int kPartBytes = kWarps * 16 * kTokens * 4;  // the warps' sums
   // A token's row of x: 8 lanes' 16-byte reads (two tokens, 64 bytes of each)
   // meet all banks where rows are 64 bytes off a multiple of 128.
   static constexpr int pitch(int kx) { return kx * 2 + 64; }
-  static constexpr int smem(int kx) { return kWarps * kStages * kStage + kTokens * pitch(kx); }
+  static constexpr int smem(int kx) { return kWarps * kStages * kStage + kPartBytes + kTokens * pitch(kx); }
 };
 
-// YB: y is bf16.
+// Output i, from its sum.
+template <bool YB>
+__device__ __forceinline__ void put(const Args& p, size_t i, float v) {
+  if (p.relu) v = v < 0.f ? 0.f : v;  // NaN stays
+  if constexpr (YB) static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16(v);
+  else static_cast<float*>(p.y)[i] = v;
+}
+
+// YB: y is bf16.  A CTA takes tiles of 16 * 2^wr_log columns of W and its part of
+// k; a warp's blocks, of one tile after the other, are one line, of which the
+// next kStages - 1 are always on their way.
 template <int G, int MT, bool YB>
-__global__ void __launch_bounds__(kThreads, 1) dense_w4_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kernel(const Args p) {
   using S = Shape<G, MT>;
+  constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* stages = smem + warp * kStages * S::kStage;
-  uint8_t* xs = smem + kWarps * kStages * S::kStage;
+  float* parts = reinterpret_cast<float*>(smem + kWarps * kStages * S::kStage);  // [warp][token][16]
+  uint8_t* xs = smem + kWarps * kStages * S::kStage + S::kPartBytes;
   const int pitch = S::pitch(p.kx);
   const int wr = 1 << p.wr_log, wk = kWarps >> p.wr_log;
   const int my_r = warp & (wr - 1), my_k = warp >> p.wr_log;
   const int tiles = (p.n + 16 * wr - 1) / (16 * wr);
+  const int rank = static_cast<int>(blockIdx.x) % p.split;
+  const int tile0 = static_cast<int>(blockIdx.x) / p.split, tile_step = static_cast<int>(gridDim.x) / p.split;
+  const int ka = rank * p.ks, ke = min(p.k, ka + p.ks);  // this CTA's rows of k
+  const int blocks = ke > ka ? (ke - ka + kBlockK - 1) / kBlockK : 0;
   const int tok0 = static_cast<int>(blockIdx.y) * S::kTokens;
   const int tokens = min(S::kTokens, p.m - tok0);
   const int g = lane >> 2, t = lane & 3;
+  if (p.split > 1) cg::this_cluster().barrier_arrive();
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  // The line of this warp's blocks: where the copies are.  A lane copies chunk
+  // lane % 8 of rows lane / 8, + 4, + 8 and + 12, and, of some lanes, 8 scales.
+  int f_tile = tile0, f_block = my_k, f_slot = 0;
+  const uint32_t to = smem_u32(stages) + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+  const uint32_t to_odd = smem_u32(stages) + (lane >> 3) * 128 + (((lane & 7) ^ (4 + (lane >> 3))) << 4);  // of rows + 4
+  const size_t row_bytes = static_cast<size_t>(p.k) / 2, rows4 = 4 * row_bytes;
+  const uint8_t* from;
+  const __nv_bfloat16* from_s;
+  bool whole;  // no row of the tile past the end
+  const auto place = [&]() {
+    const int n0 = (f_tile * wr + my_r) * 16, kb = ka + f_block * kBlockK;
+    from = p.codes + (n0 + (lane >> 3)) * row_bytes + kb / 2 + (lane & 7) * 16;
+    from_s = p.scales + static_cast<size_t>(kb / G + (lane >> 1)) * p.n + n0 + (lane & 1) * 8;
+    whole = n0 + 16 <= p.n;
+  };
+  if (f_block < blocks) place();
+  const auto fetch = [&]() {
+    if (f_tile < tiles && f_block < blocks) {
+      const uint32_t at = f_slot * S::kStage;
+      const int kb = ka + f_block * kBlockK;
+      if (whole && kb + kBlockK <= ke) {
+        copy16(to + at, from, true);
+        copy16(to_odd + at + 4 * 128, from + rows4, true);
+        copy16(to + at + 8 * 128, from + 2 * rows4, true);
+        copy16(to_odd + at + 12 * 128, from + 3 * rows4, true);
+        if (lane < 2 * S::kGroups) copy16(smem_u32(stages) + at + kCodeBytes + lane * 16, from_s, true);
+      } else {
+        const int n0 = (f_tile * wr + my_r) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool there = n0 + i * 4 + (lane >> 3) < p.n && kb + (lane & 7) * 32 < ke;
+          copy16((i & 1 ? to_odd : to) + at + i * 512, there ? from + i * rows4 : p.codes, there);
+        }
+        if (lane < 2 * S::kGroups) {
+          const bool there = kb + (lane >> 1) * G < ke && n0 + (lane & 1) * 8 < p.n;
+          copy16(smem_u32(stages) + at + kCodeBytes + lane * 16, there ? from_s : p.scales, there);
+        }
+      }
+      f_block += wk;
+      from += wk * (kBlockK / 2);
+      from_s += static_cast<size_t>(wk * S::kGroups) * p.n;
+      if (f_block >= blocks) {
+        f_block = my_k, f_tile += tile_step;
+        if (f_tile < tiles) place();
+      }
+    }
+    copies_commit();
+    f_slot = f_slot == kStages - 1 ? 0 : f_slot + 1;
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch();
+
+  int slot = 0;
+  for (int tile = tile0; tile < tiles; tile += tile_step) {
     const int n0 = (tile * wr + my_r) * 16;
     float total[MT][4];
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
       for (int e = 0; e < 4; ++e) total[a][e] = 0.f;
-    for (int k0 = 0; k0 < p.k; k0 += p.kx) {
-      const int k1 = min(p.k, k0 + p.kx);
-      const int blocks = (k1 - k0 + kBlockK - 1) / kBlockK;
-      // Blocks my_k, my_k + wk, ... of this stretch of k.
-      const auto fetch = [&](int b, int slot) {
-        if (b < blocks) {
-          uint8_t* at = stages + slot * S::kStage;
-          const int kb = k0 + b * kBlockK;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = i * 4 + (lane >> 3), chunk = lane & 7;
-            const bool there = n0 + row < p.n && kb + chunk * 32 < k1;
-            const uint8_t* src = p.codes;
-            if (there) src += static_cast<size_t>(n0 + row) * (p.k / 2) + kb / 2 + chunk * 16;
-            copy16(at + row * 128 + ((chunk ^ (row & 7)) << 4), src, there);
-          }
-          if (lane < 2 * S::kGroups) {
-            const int group = kb / G + (lane >> 1), col = n0 + (lane & 1) * 8;
-            const bool there = group < p.k / G && col < p.n;
-            const __nv_bfloat16* src = p.scales;
-            if (there) src += static_cast<size_t>(group) * p.n + col;
-            copy16(at + kCodeBytes + lane * 16, src, there);
-          }
-        }
-        copies_commit();
-      };
-#pragma unroll
-      for (int s = 0; s < kStages - 1; ++s) fetch(my_k + s * wk, s);
-      if (p.k > p.kx || tile == static_cast<int>(blockIdx.x)) {
+    for (int k0 = ka; k0 < ke; k0 += p.kx) {
+      const int k1 = min(ke, k0 + p.kx);
+      if (p.ks > p.kx || tile == tile0) {
         // x of this stretch, by pairs; zeros past its end.
-        if (p.k > p.kx) __syncthreads();
-        const int octets = blocks * (kBlockK / 8);
+        if (p.ks > p.kx) __syncthreads();
+        const int octets = (k1 - k0 + kBlockK - 1) / kBlockK * (kBlockK / 8);
         for (int i = threadIdx.x; i < S::kTokens * octets; i += kThreads) {
           const int row = i / octets, o = i - row * octets;
           uint4 v = make_uint4(0, 0, 0, 0);
@@ -151,15 +203,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_w4_kernel(const Args p) {
         }
         __syncthreads();
       }
-      int slot = 0;
-      for (int b = my_k; b < blocks; b += wk) {
+      // This warp's blocks of the stretch.
+      const int b0 = (k0 - ka) / kBlockK, b1 = (k1 - ka + kBlockK - 1) / kBlockK;
+      for (int b = b0 + ((my_k - b0) & (wk - 1)); b < b1; b += wk) {
         copies_wait<kStages - 2>();
         __syncwarp();  // every lane's copies are there, and all have read the slot that is filled next
-        fetch(b + (kStages - 1) * wk, slot == 0 ? kStages - 1 : slot - 1);
+        fetch();
         const uint8_t* at = stages + slot * S::kStage;
         const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(at + kCodeBytes);
-        const uint8_t* xb = xs + g * pitch + (b * kBlockK + t * 8) * 2;
-        float acc[MT][4];
+        const uint8_t* xb = xs + g * pitch + ((b - b0) * kBlockK + t * 8) * 2;
+        // Two sums at a time for a single column of tokens: the products of one wait for each other.
+        constexpr int kSums = MT == 1 ? 2 : 1;
+        float acc[kSums][MT][4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int row = lane & 7, chunk = half * 4 + (lane >> 3);
@@ -172,96 +227,129 @@ __global__ void __launch_bounds__(kThreads, 1) dense_w4_kernel(const Args p) {
             const int c = half * 4 + w;  // chunk of 32 codes
             if (c % (G / 32) == 0) {
 #pragma unroll
-              for (int a = 0; a < MT; ++a)
+              for (int s = 0; s < kSums; ++s)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[a][e] = 0.f;
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[s][a][e] = 0.f;
             }
             const uint32_t wa[4] = {pair_of<0>(lo[w]), pair_of<0>(hi[w]), pair_of<1>(lo[w]), pair_of<1>(hi[w])};
             const uint32_t wb[4] = {pair_of<2>(lo[w]), pair_of<2>(hi[w]), pair_of<3>(lo[w]), pair_of<3>(hi[w])};
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
               const uint4 v = *reinterpret_cast<const uint4*>(xb + a * 8 * pitch + c * 64);
-              mma16816(acc[a], wa, v.x, v.y);
-              mma16816(acc[a], wb, v.z, v.w);
+              mma16816(acc[0][a], wa, v.x, v.y);
+              mma16816(acc[kSums - 1][a], wb, v.z, v.w);
             }
             if ((c + 1) % (G / 32) == 0) {
               const int group = c / (G / 32);
               const float s0 = __bfloat162float(sc[group * 16 + g]), s1 = __bfloat162float(sc[group * 16 + g + 8]);
 #pragma unroll
-              for (int a = 0; a < MT; ++a) {
-                total[a][0] = fmaf(acc[a][0], s0, total[a][0]);
-                total[a][1] = fmaf(acc[a][1], s0, total[a][1]);
-                total[a][2] = fmaf(acc[a][2], s1, total[a][2]);
-                total[a][3] = fmaf(acc[a][3], s1, total[a][3]);
-              }
+              for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float sum = kSums == 2 ? acc[0][a][e] + acc[kSums - 1][a][e] : acc[0][a][e];
+                  total[a][e] = fmaf(sum, e < 2 ? s0 : s1, total[a][e]);
+                }
             }
           }
         }
         slot = slot == kStages - 1 ? 0 : slot + 1;
       }
-      copies_wait<0>();
-      __syncwarp();
     }
-    // The warps that shared k add up, in order, over the first one's stages.
-    if (wk > 1) {
-      float* parts = reinterpret_cast<float*>(stages);
-      __syncthreads();
-      if (my_k > 0) {
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) parts[(a * 4 + e) * 32 + lane] = total[a][e];
-      }
-      __syncthreads();
-      if (my_k == 0) {
-        for (int w = 1; w < wk; ++w) {
-          const float* from = reinterpret_cast<const float*>(smem + (warp + w * wr) * kStages * S::kStage);
-#pragma unroll
-          for (int a = 0; a < MT; ++a)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) total[a][e] += from[(a * 4 + e) * 32 + lane];
-        }
-      }
-      __syncthreads();
-    }
-    if (my_k == 0) {
+    if (wk == 1 && p.split == 1) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int col = n0 + g + 8 * r;
         if (col >= p.n) continue;
-        const float b = p.bias != nullptr ? __ldg(p.bias + col) : 0.f;
+        const float bias = p.bias != nullptr ? __ldg(p.bias + col) : 0.f;
+        size_t i = static_cast<size_t>(tok0 + 2 * t) * p.n + col;
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int token = a * 8 + 2 * t + e;
-            if (token >= tokens) continue;
-            float v = total[a][2 * r + e] + b;
-            if (p.relu) v = v < 0.f ? 0.f : v;  // NaN stays
-            const size_t i = static_cast<size_t>(tok0 + token) * p.n + col;
-            if constexpr (YB) static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16(v);
-            else static_cast<float*>(p.y)[i] = v;
-          }
+        for (int a = 0; a < MT; ++a, i += 8 * static_cast<size_t>(p.n)) {
+          if (a * 8 + 2 * t < tokens) put<YB>(p, i, total[a][2 * r] + bias);
+          if (a * 8 + 2 * t + 1 < tokens) put<YB>(p, i + p.n, total[a][2 * r + 1] + bias);
+        }
       }
+      continue;
     }
+    // The warps, and the CTAs, that shared k add up, in order: the sums go to
+    // shared memory, and each CTA of the cluster takes its share of the outputs.
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        parts[(warp * S::kTokens + a * 8 + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = total[a][e];
+    if (p.split > 1) {
+      if (tile == tile0) cg::this_cluster().barrier_wait();
+      cg::this_cluster().sync();
+    } else {
+      __syncthreads();
+    }
+    const int cols_log = 4 + p.wr_log, outs = tokens << cols_log;
+    const int o0 = outs * rank / p.split, o1 = outs * (rank + 1) / p.split;
+    for (int o = o0 + static_cast<int>(threadIdx.x); o < o1; o += kThreads) {
+      const int token = o >> cols_log, c = o & ((1 << cols_log) - 1);
+      const int at = ((c >> 4) * S::kTokens + token) * 16 + (c & 15);
+      float v = 0.f;
+      for (int r = 0; r < p.split; ++r) {
+        const float* from = p.split > 1 ? cg::this_cluster().map_shared_rank(parts, r) : parts;
+        for (int w = 0; w < wk; ++w) v += from[w * wr * S::kTokens * 16 + at];
+      }
+      const int col = tile * 16 * wr + c;
+      if (col >= p.n) continue;
+      if (p.bias != nullptr) v += __ldg(p.bias + col);
+      put<YB>(p, static_cast<size_t>(tok0 + token) * p.n + col, v);
+    }
+    if (p.split > 1) cg::this_cluster().sync();
+    else __syncthreads();
   }
+  copies_wait<0>();
 }
 
 template <int G, int MT, bool YB>
 cudaError_t launch(Args a, cudaStream_t stream) {
   using S = Shape<G, MT>;
-  a.kx = std::min((a.k + kBlockK - 1) / kBlockK * kBlockK, kXBytes / (2 * S::kTokens) / kBlockK * kBlockK);
-  // As many warps along n as leave a tile for every SM.
-  a.wr_log = 3;
-  while (a.wr_log > 0 && (a.n + (16 << a.wr_log) - 1) / (16 << a.wr_log) < 152) --a.wr_log;
+  constexpr int kMaxX = kXBytes / (2 * S::kTokens) / kBlockK * kBlockK;
+  const int blocks = (a.k + kBlockK - 1) / kBlockK;
+  // How many warps stand along n and how many CTAs share k: what makes the
+  // longest warp's work, the copies of x and the sums at the end least.
+  long long best = -1;
+  for (int wr_log = 3; wr_log >= 0; --wr_log)
+    for (int split = 1; split <= kMaxSplit; split *= 2) {
+      if (split > 1 && split > blocks) break;
+      const int tiles = (a.n + (16 << wr_log) - 1) / (16 << wr_log);
+      const int mine = (blocks + split - 1) / split, wk = kWarps >> wr_log;
+      const long long waves = (static_cast<long long>(tiles) * split + 303) / 304;
+      const long long warp_blocks = waves * ((mine + wk - 1) / wk);
+      const long long copies = static_cast<long long>(mine) * kBlockK * S::kTokens / 16;  // 32 bytes a cycle
+      const long long cost = warp_blocks * (300 + 200 * MT) + copies * (mine * kBlockK > kMaxX ? waves : 1) +
+                             waves * ((split > 1 ? 3000 : 0) + (wk > 1 ? 800 : 0));
+      if (best < 0 || cost < best) best = cost, a.wr_log = wr_log, a.split = split;
+    }
+  a.ks = (blocks + a.split - 1) / a.split * kBlockK;
+  a.kx = std::min(a.ks, kMaxX);
   const int tiles = (a.n + (16 << a.wr_log) - 1) / (16 << a.wr_log);
   const int smem = S::smem(a.kx);
   auto kernel = dense_w4_kernel<G, MT, YB>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int per_sm = std::max(1, std::min(8, 227 * 1024 / (smem + 1024)));
-  const dim3 grid(std::min(tiles, 152 * per_sm), (a.m + S::kTokens - 1) / S::kTokens);
-  return launch_dependent(kernel, grid, dim3(kThreads), smem, stream, a);
+  const int per_sm = std::max(1, std::min(S::kPerSm, 227 * 1024 / (smem + 1024)));
+  cudaLaunchConfig_t cfg = {};
+  const int clusters = std::min(tiles, std::max(1, 152 * per_sm / a.split));
+  cfg.gridDim = dim3(clusters * a.split, (a.m + S::kTokens - 1) / S::kTokens);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int G, bool YB>
@@ -285,8 +373,14 @@ cudaError_t by_group(const Args& a, int group, cudaStream_t stream) {
 
 cudaError_t launch_dense_w4(const void* x, const unsigned char* codes, const void* scales, void* y, const float* bias,
                             int m, int n, int k, int group, bool relu, bool y_bf16, cudaStream_t stream) {
-  const Args a{static_cast<const __nv_bfloat16*>(x), codes, static_cast<const __nv_bfloat16*>(scales), y, bias, m, n,
-               k, 0, 0, relu};
+  Args a{};
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.codes = codes;
+  a.scales = static_cast<const __nv_bfloat16*>(scales);
+  a.y = y;
+  a.bias = bias;
+  a.m = m, a.n = n, a.k = k;
+  a.relu = relu;
   return y_bf16 ? by_group<true>(a, group, stream) : by_group<false>(a, group, stream);
 }
 
