@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kerne
         // x of this stretch, by pairs; zeros past its end.
         if (p.ks > p.kx) __syncthreads();
         const int octets = (k1 - k0 + kBlockK - 1) / kBlockK * (kBlockK / 8);
+#pragma unroll 4
         for (int i = threadIdx.x; i < S::kTokens * octets; i += kThreads) {
           const int row = i / octets, o = i - row * octets;
           uint4 v = make_uint4(0, 0, 0, 0);
@@ -279,29 +280,52 @@ __global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kerne
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         parts[(warp * S::kTokens + a * 8 + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = total[a][e];
-    if (p.split > 1) {
-      if (tile == tile0) cg::this_cluster().barrier_wait();
-      cg::this_cluster().sync();
-    } else {
-      __syncthreads();
-    }
     const int cols_log = 4 + p.wr_log, outs = tokens << cols_log;
-    const int o0 = outs * rank / p.split, o1 = outs * (rank + 1) / p.split;
-    for (int o = o0 + static_cast<int>(threadIdx.x); o < o1; o += kThreads) {
+    const auto place_of = [&](int o) {
       const int token = o >> cols_log, c = o & ((1 << cols_log) - 1);
-      const int at = ((c >> 4) * S::kTokens + token) * 16 + (c & 15);
-      float v = 0.f;
-      for (int r = 0; r < p.split; ++r) {
-        const float* from = p.split > 1 ? cg::this_cluster().map_shared_rank(parts, r) : parts;
-        for (int w = 0; w < wk; ++w) v += from[w * wr * S::kTokens * 16 + at];
-      }
-      const int col = tile * 16 * wr + c;
-      if (col >= p.n) continue;
+      return ((c >> 4) * S::kTokens + token) * 16 + (c & 15);
+    };
+    const auto finish = [&](int o, float v) {
+      const int col = tile * 16 * wr + (o & ((1 << cols_log) - 1));
+      if (col >= p.n) return;
       if (p.bias != nullptr) v += __ldg(p.bias + col);
-      put<YB>(p, static_cast<size_t>(tok0 + token) * p.n + col, v);
+      put<YB>(p, static_cast<size_t>(tok0 + (o >> cols_log)) * p.n + col, v);
+    };
+    const int warp_part = wr * S::kTokens * 16;  // from one warp's sums to those of the next that shares its columns
+    __syncthreads();
+    if (p.split == 1) {
+      for (int o = threadIdx.x; o < outs; o += kThreads) {
+        const int at = place_of(o);
+        float v = parts[at];
+        for (int w = 1; w < wk; ++w) v += parts[w * warp_part + at];
+        finish(o, v);
+      }
+      __syncthreads();
+      continue;
     }
-    if (p.split > 1) cg::this_cluster().sync();
-    else __syncthreads();
+    cg::cluster_group cluster = cg::this_cluster();
+    if (wk > 1) {
+      for (int o = threadIdx.x; o < outs; o += kThreads) {
+        const int at = place_of(o);
+        float v = parts[at];
+        for (int w = 1; w < wk; ++w) v += parts[w * warp_part + at];
+        parts[at] = v;
+      }
+    }
+    if (tile == tile0) cluster.barrier_wait();
+    cluster.sync();
+    const int o1 = outs * (rank + 1) / p.split;
+    for (int o = outs * rank / p.split + static_cast<int>(threadIdx.x); o < o1; o += kThreads) {
+      float part[kMaxSplit];  // all on their way together
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        part[r] = r < p.split ? cluster.map_shared_rank(parts, r)[place_of(o)] : 0.f;
+      float v = part[0];
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r) v += part[r];
+      finish(o, v);
+    }
+    cluster.sync();
   }
   copies_wait<0>();
 }
@@ -323,7 +347,7 @@ cudaError_t launch(Args a, cudaStream_t stream) {
       const long long warp_blocks = waves * ((mine + wk - 1) / wk);
       const long long copies = static_cast<long long>(mine) * kBlockK * S::kTokens / 16;  // 32 bytes a cycle
       const long long cost = warp_blocks * (300 + 200 * MT) + copies * (mine * kBlockK > kMaxX ? waves : 1) +
-                             waves * ((split > 1 ? 3000 : 0) + (wk > 1 ? 800 : 0));
+                             waves * ((split > 1 ? 2000 : 0) + (wk > 1 ? 500 : 0));
       if (best < 0 || cost < best) best = cost, a.wr_log = wr_log, a.split = split;
     }
   a.ks = (blocks + a.split - 1) / a.split * kBlockK;
