@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kerne
   // lane % 8 of rows lane / 8, + 4, + 8 and + 12, and, of some lanes, 8 scales.
   int f_tile = tile0, f_block = my_k, f_slot = 0;
   const uint32_t to = smem_u32(stages) + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
-  const uint32_t to_odd = smem_u32(stages) + (lane >> 3) * 128 + (((lane & 7) ^ (4 + (lane >> 3))) << 4);  // of rows + 4
+  const uint32_t to_odd = smem_u32(stages) + (lane >> 3) * 128 + (((lane & 7) ^ (4 + (lane >> 3))) << 4);
   const size_t row_bytes = static_cast<size_t>(p.k) / 2, rows4 = 4 * row_bytes;
   const uint8_t* from;
   const __nv_bfloat16* from_s;
@@ -188,19 +188,26 @@ __global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kerne
       if (p.ks > p.kx || tile == tile0) {
         // x of this stretch, by pairs; zeros past its end.
         if (p.ks > p.kx) __syncthreads();
-        const int octets = (k1 - k0 + kBlockK - 1) / kBlockK * (kBlockK / 8);
-#pragma unroll 4
-        for (int i = threadIdx.x; i < S::kTokens * octets; i += kThreads) {
-          const int row = i / octets, o = i - row * octets;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < tokens && k0 + o * 8 < k1)
-            v = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(tok0 + row) * p.k + k0 + o * 8));
-          uint4 w;
-          w.x = __byte_perm(v.x, v.z, 0x5410);
-          w.y = __byte_perm(v.x, v.z, 0x7632);
-          w.z = __byte_perm(v.y, v.w, 0x5410);
-          w.w = __byte_perm(v.y, v.w, 0x7632);
-          *reinterpret_cast<uint4*>(xs + row * pitch + o * 16) = w;
+        const int octets = (k1 - k0 + kBlockK - 1) / kBlockK * (kBlockK / 8);  // of a token, a multiple of 32
+        // Warp w takes tokens w, w + 8, ...: eight of a lane's copies at a time.
+        const int there = (k1 - k0) / 8;
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(tok0 + warp) * p.k + k0);
+        for (int o = lane; o < octets; o += 256 / MT) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int a = i % MT, at = o + i / MT * 32;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (warp + 8 * a < tokens && at < there) v[i] = __ldg(src + static_cast<size_t>(a) * p.k + at);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int a = i % MT, at = o + i / MT * 32;
+            if (at < octets)
+              *reinterpret_cast<uint4*>(xs + (warp + 8 * a) * pitch + at * 16) =
+                  make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                             __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
+          }
         }
         __syncthreads();
       }
@@ -335,34 +342,40 @@ cudaError_t launch(Args a, cudaStream_t stream) {
   using S = Shape<G, MT>;
   constexpr int kMaxX = kXBytes / (2 * S::kTokens) / kBlockK * kBlockK;
   const int blocks = (a.k + kBlockK - 1) / kBlockK;
-  // How many warps stand along n and how many CTAs share k: what makes the
-  // longest warp's work, the copies of x and the sums at the end least.
+  // How many warps stand along n and how many CTAs share k, by the time that a
+  // pair takes: fitted to 250 measured ones (m 1 to 32, k 128 to 4096, n 512 to
+  // 131072), whose best it misses by 11% at most.  In ns: a block to a warp, an SM
+  // full of warps a block, a sum of warps, of CTAs, 1 KB of x.  Both ends: 32
+  // tokens, k = 4096, n = 1024 take 21 us with a CTA for 128 columns and all of k,
+  // 6.3 with a cluster of four for 32; 8 tokens, k = 1024, n = 131072 take 21 with
+  // the first and 94 with a cluster of two.
+  constexpr int kAlone = MT == 1 ? 560 : MT == 2 ? 640 : 1250, kFull = MT == 1 ? 100 : MT == 2 ? 120 : 250;
   long long best = -1;
+  int best_clusters = 1, best_smem = 0;
   for (int wr_log = 3; wr_log >= 0; --wr_log)
-    for (int split = 1; split <= kMaxSplit; split *= 2) {
-      if (split > 1 && split > blocks) break;
-      const int tiles = (a.n + (16 << wr_log) - 1) / (16 << wr_log);
-      const int mine = (blocks + split - 1) / split, wk = kWarps >> wr_log;
-      const long long waves = (static_cast<long long>(tiles) * split + 303) / 304;
-      const long long warp_blocks = waves * ((mine + wk - 1) / wk);
-      const long long copies = static_cast<long long>(mine) * kBlockK * S::kTokens / 16;  // 32 bytes a cycle
-      const long long cost = warp_blocks * (300 + 200 * MT) + copies * (mine * kBlockK > kMaxX ? waves : 1) +
-                             waves * ((split > 1 ? 2000 : 0) + (wk > 1 ? 500 : 0));
-      if (best < 0 || cost < best) best = cost, a.wr_log = wr_log, a.split = split;
+    for (int split = 1; split <= kMaxSplit && (split == 1 || split <= blocks); split *= 2) {
+      const int tiles = (a.n + (16 << wr_log) - 1) / (16 << wr_log), wk = kWarps >> wr_log;
+      const int mine = (blocks + split - 1) / split, kx = std::min(mine * kBlockK, kMaxX);
+      const int smem = S::smem(kx);
+      const int per_sm = std::max(1, std::min(S::kPerSm, 227 * 1024 / (smem + 1024)));
+      // (12 clusters of 8 find room at a time, of 19 that there are SMs for.)
+      const int clusters = std::min(tiles, split == 8 ? 12 * per_sm : 152 * per_sm / split);
+      const long long rounds = (tiles + clusters - 1) / clusters;
+      const long long alone = rounds * ((mine + wk - 1) / wk) * kAlone;
+      const long long full = (static_cast<long long>(tiles) << wr_log) * blocks * kFull / 152;
+      const long long ns = std::max(alone, full) + rounds * ((wk > 1 ? 320 : 0) + (split > 1 ? 1650 : 0)) +
+                           12LL * mine * kBlockK * S::kTokens * 2 / 1024 * (mine * kBlockK > kMaxX ? rounds : 1);
+      if (best >= 0 && ns >= best) continue;
+      best = ns, best_clusters = clusters, best_smem = smem;
+      a.wr_log = wr_log, a.split = split, a.ks = mine * kBlockK, a.kx = kx;
     }
-  a.ks = (blocks + a.split - 1) / a.split * kBlockK;
-  a.kx = std::min(a.ks, kMaxX);
-  const int tiles = (a.n + (16 << a.wr_log) - 1) / (16 << a.wr_log);
-  const int smem = S::smem(a.kx);
   auto kernel = dense_w4_kernel<G, MT, YB>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, best_smem);
   if (e != cudaSuccess) return e;
-  const int per_sm = std::max(1, std::min(S::kPerSm, 227 * 1024 / (smem + 1024)));
   cudaLaunchConfig_t cfg = {};
-  const int clusters = std::min(tiles, std::max(1, 152 * per_sm / a.split));
-  cfg.gridDim = dim3(clusters * a.split, (a.m + S::kTokens - 1) / S::kTokens);
+  cfg.gridDim = dim3(best_clusters * a.split, (a.m + S::kTokens - 1) / S::kTokens);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = best_smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
