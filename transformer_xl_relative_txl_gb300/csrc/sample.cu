@@ -167,6 +167,7 @@ struct Shared {
   unsigned long long groups[kMaxCluster][kGroups];
   float top[kMaxCluster];
   uint32_t cut[kMaxCluster];
+  int parts[kMaxCluster];
   Found found[kMaxCluster];
   Kept kept[kMaxCluster];
   Mass mass[kMaxCluster];
@@ -176,6 +177,7 @@ struct Shared {
   unsigned long long warp_sum[kWarps];
   float warp_top[kWarps];
   uint32_t warp_cut[kWarps];
+  int warp_parts[kWarps];
   unsigned long long cell_over[kCells];
   int cell_ties[kCells];
   uint32_t lo, hi;  // of a bin's tokens in this CTA
@@ -708,32 +710,52 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
 
   // The row's largest logit.  And one that is not over the top_k-th largest,
   // without which the search would put the whole row into bins: of `parts` parts
-  // of the row, at least top_k, the smallest of their largest.
+  // of the row, at least top_k, the smallest of their largest.  (A part is a
+  // thread's logits or several threads'; parts without any do not count.)  Where
+  // there are too few threads, the smallest logit.
   float cut = top;
+  int parts = 0;
   {
+    const int busy = CTAS * min(kThreads, (min(stretch, p.V) + VEC - 1) / VEC);  // of the row, about
     int o = 32;  // threads of a part
-    while (o > 1 && CTAS * kThreads / o < set.top_k) o >>= 1;
+    while (o > 1 && busy / o < set.top_k) o >>= 1;
     for (int x = 1; x < o; x <<= 1) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, x));
+    if (busy < set.top_k) {
+      __syncthreads();
+      cut = INFINITY;
+      for (int i = threadIdx.x; i < row.cells * kCell; i += kThreads) {
+        const float z = row.at(i);
+        if (z > -INFINITY) cut = fminf(cut, z);
+      }
+      parts = 1 << 20;
+    } else {
+      parts = __popc(__ballot_sync(0xffffffffu, cut > -INFINITY && (lane & (o - 1)) == 0));
+      if (cut == -INFINITY) cut = INFINITY;
+    }
     const uint32_t l = __reduce_min_sync(0xffffffffu, ordered(cut)), h = __reduce_max_sync(0xffffffffu, ordered(top));
-    if (lane == 0) sh.warp_cut[warp] = l, sh.warp_top[warp] = unordered(h);
+    if (lane == 0) sh.warp_cut[warp] = l, sh.warp_top[warp] = unordered(h), sh.warp_parts[warp] = parts;
   }
   __syncthreads();
   cluster.barrier_wait();
   if (warp == 0) {
     const uint32_t l = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh.warp_cut[lane] : 0xffffffffu);
     const uint32_t h = __reduce_max_sync(0xffffffffu, lane < kWarps ? ordered(sh.warp_top[lane]) : 0u);
+    const int n = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_parts[lane] : 0);
     if (lane < CTAS) {
       Shared* other = cluster.map_shared_rank(&sh, lane);
       other->top[rank] = unordered(h);
       other->cut[rank] = l;
+      other->parts[rank] = n;
     }
   }
   cluster.sync();
   uint32_t cut_at = 0xffffffffu;
+  parts = 0;
 #pragma unroll
   for (int r = 0; r < CTAS; ++r) {
     top = r == 0 ? sh.top[0] : fmaxf(top, sh.top[r]);
     cut_at = min(cut_at, sh.cut[r]);
+    parts += sh.parts[r];
   }
   if (top == -INFINITY) {
     if (rank == 0 && threadIdx.x == 0) put(p, b, -1, 0, 0);
@@ -744,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     row.bound();
     top = largest<T>();
   }
-  cut = set.top_k <= CTAS * kThreads ? fminf(unordered(cut_at), top) : -INFINITY;
+  cut = parts >= set.top_k ? fminf(unordered(cut_at), top) : -INFINITY;
 
   // The threshold: tokens over `value`, and the first `ties` of those at it.
   float value = -INFINITY;
@@ -927,10 +949,16 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
 
 template <typename T, int VEC>
 cudaError_t by_size(const SampleArgs& a, cudaStream_t stream) {
-  // CTAs of a row: enough for at most 16384 values each (32768 in the longest
-  // rows), and more where the rows alone would not fill the GPU.
+  // CTAs of a row: enough for at most 32768 values each, up to 4 of them for at
+  // most 64 KB; and more, of 4096 values at least, where the rows alone would leave
+  // most SMs without work.  64 rows of 131072 in bf16, top-p: 66 us by 4 CTAs each,
+  // 81 by 8; one row 36 and 25.  256 rows of 32768: bf16 60 by one CTA, 69 by 2, fp32
+  // 76 and 71.  (Few clusters of 8 find room at a time.)
   int ctas = 1;
-  while (ctas < kMaxCluster && (a.V > ctas * 16384 || (a.B * ctas < 152 && a.V > ctas * kThreads * 4))) ctas *= 2;
+  while (ctas < kMaxCluster &&
+         (a.V > ctas * kCells * kCell || (ctas < 4 && a.V * sizeof(T) > ctas * 65536ULL) ||
+          (a.B * ctas < 100 && a.V > ctas * 4096 && (ctas < 4 || a.B <= 12))))
+    ctas *= 2;
   switch (ctas) {
     case 1: return launch<T, VEC, 1>(a, stream);
     case 2: return launch<T, VEC, 2>(a, stream);
