@@ -132,26 +132,33 @@ cudaError_t forward_any(const int* tokens, const void* table, void* out, int T, 
 // backward
 // ---------------------------------------------------------------------------
 // One kernel, in which every CTA owns some rows of the table, of which it
-// writes kCols columns: the rows v with v % classes == its class, so that the
+// writes COLS columns: the rows v with v % classes == its class, so that the
 // common ids, which vocabularies number first, are spread over all CTAs.  It
 // reads all ids, keeps its own in the order of their places, sorts them by row
-// and sums each row's gradients, which its warps share equally whatever the
-// rows' lengths.  Nothing is added by atomics: a row's sum has one order,
-// which the ids alone decide.
+// and place and sums each row's gradients, in shares that are equal whatever the
+// rows' lengths.  A row's sum has one order, which the ids alone decide, and is
+// put into the table once: added to it, by one atomic whose result nothing waits
+// for, or stored.
+//
+// The gradients' rows are asked for as soon as the ids are listed, so that they
+// are on their way to L2 while the list is sorted and the other rows zeroed.
 constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
-constexpr int kCols = 128;        // columns of a CTA
-constexpr int kMaxLocal = 8192;   // rows of a CTA
-constexpr int kChunk = 8192;      // ids at a time
-constexpr int kRounds = kChunk / kGradThreads;
-constexpr int kPlaceBits = 13;    // of a place in a chunk
-constexpr int kAhead = 4;         // gradient rows in flight per warp
-static_assert(kChunk <= 1 << kPlaceBits && kMaxLocal <= 1 << (32 - kPlaceBits), "an entry fits 32 bits");
+constexpr int kMaxLocal = 16384;  // rows of a CTA
+constexpr int kPlaceBits = 15;
+constexpr int kChunk = 1 << kPlaceBits;  // ids at a time
+constexpr int kList = 4096;       // of them a CTA's own
+constexpr int kWarpList = kList / kGradWarps;
+constexpr int kAhead = 8;         // gradient rows in flight per worker
+constexpr uint32_t kNone = 0xffffffffu;
+static_assert(kMaxLocal <= 1 << (32 - kPlaceBits - 1), "an entry, row and place, fits 31 bits");
 
-struct GradSmem {  // ahead of first[local + 1], list[chunk], sorted[chunk]
-  float part[kGradWarps][2][kCols];
-  int counts[kRounds * kGradWarps];
+struct GradSmem {  // ahead of end[local rows]
+  uint32_t list[kList];  // by warp
+  uint32_t line[kList];  // all, by place; then
+  uint32_t sorted[kList];
+  float part[kGradThreads][2][4];
+  int counts[kGradWarps];
   int sums[kGradWarps];
-  int total;
 };
 
 struct GradArgs {
@@ -162,57 +169,63 @@ struct GradArgs {
   unsigned long long inverse;  // 2^40 / classes + 1
   float scale;
   bool accumulate;
-  int local, chunk;  // the shared arrays' lengths
 };
 
-// Exclusive sum over the block, and the total.
-__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int s = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
-  }
-  if (lane == 31) sums[warp] = s;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kGradWarps; ++w) {
-    const int y = sums[w];
-    before += w < warp ? y : 0;
-    all += y;
-  }
-  __syncthreads();
-  *total = all;
-  return before + s - x;
-}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// A warp's columns of a row: 4 a lane in a line (N = 4) or every 32nd (N = 1,
-// where rows do not start on 16 bytes).
-template <int N>
+// A worker's columns of a row, COLS / 4 lanes: 4 a lane in a line (N = 4) or
+// COLS / 4 apart (N = 1, where rows do not start on 16 bytes).
+template <typename T, int N, int COLS>
 struct Columns {
+  static constexpr int kLanes = COLS / 4;
   int c0, left;  // the slice's first column, how many it has
+  struct Raw {
+    uint32_t w[N == 4 ? static_cast<int>(sizeof(T)) : 4];
+  };
   __device__ __forceinline__ int at(int e) const {
-    return N == 4 ? (threadIdx.x & 31) * 4 + e : (threadIdx.x & 31) + 32 * e;
+    const int l = static_cast<int>(threadIdx.x) % kLanes;
+    return N == 4 ? l * 4 + e : l + kLanes * e;
   }
-  template <typename T>
-  __device__ __forceinline__ void load(const T* row, float (&v)[4]) const {
+  __device__ __forceinline__ void load(const T* row, Raw* r) const {
+    if constexpr (N == 4 && sizeof(T) == 2) {
+      if (at(0) < left) *reinterpret_cast<uint2*>(r->w) = __ldg(reinterpret_cast<const uint2*>(row + c0 + at(0)));
+    } else if constexpr (N == 4) {
+      if (at(0) < left) *reinterpret_cast<uint4*>(r->w) = __ldg(reinterpret_cast<const uint4*>(row + c0 + at(0)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (at(e) >= left) continue;
+        float x[1];
+        load_n<T, 1>(row + c0 + at(e), x);
+        r->w[e] = __float_as_uint(x[0]);
+      }
+    }
+  }
+  __device__ __forceinline__ void add(const Raw& r, float (&sum)[4]) const {
+    if constexpr (N == 4 && sizeof(T) == 2) {
+      sum[0] += bf16_lo(r.w[0]), sum[1] += bf16_hi(r.w[0]);
+      sum[2] += bf16_lo(r.w[1]), sum[3] += bf16_hi(r.w[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += __uint_as_float(r.w[e]);
+    }
+  }
+  // To what is there (a subnormal result becomes 0).
+  __device__ __forceinline__ void add_to(float* row, const float (&v)[4]) const {
     if constexpr (N == 4) {
-      if (at(0) < left) load_n<T, 4>(row + c0 + at(0), v);
+      if (at(0) < left)
+        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(row + c0 + at(0)), "f"(v[0]), "f"(v[1]),
+                     "f"(v[2]), "f"(v[3])
+                     : "memory");
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (at(e) < left) {
-          float x[1];
-          load_n<T, 1>(row + c0 + at(e), x);
-          v[e] = x[0];
-        }
+        if (at(e) < left) atomicAdd(row + c0 + at(e), v[e]);
     }
   }
   __device__ __forceinline__ void store(float* row, const float (&v)[4]) const {
     if constexpr (N == 4) {
-      if (at(0) < left) store_n<float, 4>(row + c0 + at(0), v);
+      if (at(0) < left) *reinterpret_cast<float4*>(row + c0 + at(0)) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -221,184 +234,217 @@ struct Columns {
   }
 };
 
-template <typename T, int N>
+template <typename T, int N, int COLS>
 __global__ void __launch_bounds__(kGradThreads, 2) embed_backward_kernel(const GradArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   GradSmem& sh = *reinterpret_cast<GradSmem*>(smem);
-  int* first = reinterpret_cast<int*>(smem + sizeof(GradSmem));  // of each local row, in `sorted`
-  uint32_t* list = reinterpret_cast<uint32_t*>(first + p.local + 1);
-  uint32_t* sorted = list + p.chunk;
+  int* end = reinterpret_cast<int*>(smem + sizeof(GradSmem));  // of a local row's entries in `sorted`
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mine = static_cast<int>(blockIdx.x);
-  const int rows = (p.V - mine + p.classes - 1) / p.classes;  // <= p.local
-  Columns<N> cols;
-  cols.c0 = static_cast<int>(blockIdx.y) * kCols;
-  cols.left = min(kCols, p.d - cols.c0);
+  const int rows = (p.V - mine + p.classes - 1) / p.classes;  // <= kMaxLocal
+  using C = Columns<T, N, COLS>;
+  constexpr int kWorkers = kGradThreads / C::kLanes;
+  const int worker = static_cast<int>(threadIdx.x) / C::kLanes;
+  C cols;
+  cols.c0 = static_cast<int>(blockIdx.y) * COLS;
+  cols.left = min(COLS, p.d - cols.c0);
   const T* dout = static_cast<const T*>(p.dout);
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  for (long long base = 0; base == 0 || base < p.T; base += p.chunk) {  // (without ids: zeros)
-    const int n = static_cast<int>(min(static_cast<long long>(p.chunk), p.T - base));
-    const bool add = p.accumulate || base > 0;
-    // The ids of this CTA's rows, in order.
-    uint32_t entry[kRounds];
-    uint32_t own = 0;
+  long long base = 0;
+  for (bool begun = false; !begun || base < p.T; begun = true) {  // (without ids: zeros)
+    int n = static_cast<int>(min(static_cast<long long>(kChunk), p.T - base));
+    const bool add = p.accumulate || begun;
+    for (int i = threadIdx.x; i < rows; i += kGradThreads) end[i] = 0;
+    int total, before;
+    for (;;) {
+      // The ids of this CTA's rows, in order: each warp lists those of its stretch.
+      const int part = (n + kGradThreads - 1) / kGradThreads * 32;
+      const int i0 = min(n, warp * part), i1 = min(n, i0 + part);
+      uint32_t* list = sh.list + warp * kWarpList;
+      int count = 0;
+      for (int i = i0; i < i1; i += 256) {
+        int v[8];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int i = r * kGradThreads + static_cast<int>(threadIdx.x);
-      const int v = i < n ? __ldg(p.tokens + base + i) : -1;
-      const uint32_t q = static_cast<uint32_t>(static_cast<uint32_t>(v) * p.inverse >> 40);  // v / classes, v < 2^24
-      const bool is = v >= 0 && v < p.V && v - static_cast<int>(q) * p.classes == mine;
-      entry[r] = q << kPlaceBits | static_cast<uint32_t>(i);
-      const uint32_t b = __ballot_sync(0xffffffffu, is);
-      own |= static_cast<uint32_t>(is) << r;
-      if (lane == 0) sh.counts[r * kGradWarps + warp] = __popc(b);
+        for (int u = 0; u < 8; ++u) {
+          const int at = i + u * 32 + lane;
+          v[u] = at < i1 ? __ldg(p.tokens + base + at) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t q = static_cast<uint32_t>(static_cast<uint32_t>(v[u]) * p.inverse >> 40);  // v / classes
+          const bool is = v[u] >= 0 && v[u] < p.V && v[u] - static_cast<int>(q) * p.classes == mine;
+          const uint32_t b = __ballot_sync(0xffffffffu, is);
+          const int at = count + __popc(b & ((1u << lane) - 1));
+          if (is && at < kWarpList) list[at] = q << kPlaceBits | static_cast<uint32_t>(i + u * 32 + lane);
+          count += __popc(b);
+        }
+      }
+      if (lane == 0) sh.counts[warp] = count;
+      __syncthreads();
+      total = before = 0;
+      bool fits = true;
+#pragma unroll
+      for (int w = 0; w < kGradWarps; ++w) {
+        const int c = sh.counts[w];
+        before += w < warp ? c : 0;
+        total += c;
+        fits = fits && c <= kWarpList;
+      }
+      if (fits) break;
+      __syncthreads();
+      n /= 2;  // many ids of this CTA in a row: fewer at a time (kList of them always fit)
     }
-    for (int i = threadIdx.x; i <= rows; i += kGradThreads) first[i] = 0;
-    __syncthreads();
-    static_assert(kRounds * kGradWarps <= kGradThreads, "a count a thread");
+    // All in one line, counted by row; their rows on the way to L2.
     {
-      int total;
-      const int x = threadIdx.x < kRounds * kGradWarps ? sh.counts[threadIdx.x] : 0;
-      const int before = block_scan(x, sh.sums, &total);
-      if (threadIdx.x < kRounds * kGradWarps) sh.counts[threadIdx.x] = before;
-      if (threadIdx.x == 0) sh.total = total;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const bool is = own >> r & 1;
-      const uint32_t b = __ballot_sync(0xffffffffu, is);
-      if (is) {
-        list[sh.counts[r * kGradWarps + warp] + __popc(b & ((1u << lane) - 1))] = entry[r];
-        atomicAdd(&first[entry[r] >> kPlaceBits], 1);
+      const int count = sh.counts[warp];
+      const uint32_t* list = sh.list + warp * kWarpList;
+      constexpr int kBytes = COLS * static_cast<int>(sizeof(T)), kLines = (kBytes + 127) / 128;
+      for (int i = lane; i < count * kLines; i += 32) {
+        const int c = i % kLines * (128 / static_cast<int>(sizeof(T)));
+        if (c < cols.left) prefetch_l2(dout + (base + (list[i / kLines] & (kChunk - 1))) * p.d + cols.c0 + c);
+      }
+      for (int i = lane; i < count; i += 32) {
+        const uint32_t e = list[i];
+        sh.line[before + i] = e;
+        atomicAdd(&end[e >> kPlaceBits], 1);
       }
     }
     __syncthreads();
-    const int total = sh.total;
-    // Rows without an id are zeros.  (Before the counts become places.)
+    const long long first = base;
+    base += n;
+    // Rows without an id are zeros.
     if (!add) {
       const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = warp; i < rows; i += kGradWarps)
-        if (first[i] == 0) cols.store(p.dtable + (static_cast<size_t>(i) * p.classes + mine) * p.d, zero);
-      __syncthreads();
+      for (int i = worker; i < rows; i += kWorkers)
+        if (end[i] == 0) cols.store(p.dtable + (static_cast<size_t>(i) * p.classes + mine) * p.d, zero);
     }
-    if (total == 0) continue;  // the same for all threads
-    {
+    if (total == 0) {  // the same for all threads
+      __syncthreads();
+      continue;
+    }
+    if (!add) __syncthreads();
+    {  // where each row's entries begin
       const int per = (rows + kGradThreads - 1) / kGradThreads;
       const int lo = min(rows, static_cast<int>(threadIdx.x) * per), hi = min(rows, lo + per);
       int x = 0;
-      for (int i = lo; i < hi; ++i) x += first[i];
-      int all;
-      int at = block_scan(x, sh.sums, &all);
+      for (int i = lo; i < hi; ++i) x += end[i];
+      int s = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      if (lane == 31) sh.sums[warp] = s;
+      __syncthreads();
+      int at = s - x;
+#pragma unroll
+      for (int w = 0; w < kGradWarps; ++w) at += w < warp ? sh.sums[w] : 0;
       for (int i = lo; i < hi; ++i) {
-        const int c = first[i];
-        first[i] = at;
+        const int c = end[i];
+        end[i] = at;
         at += c;
       }
-      if (threadIdx.x == 0) first[rows] = all;
     }
     __syncthreads();
-    // By row, and within a row by place: one warp, 32 entries at a time.
-    // `first` moves on to each row's end.
+    // By row, and within a row by place: one warp, 128 entries at a time, of which
+    // only the rows' counters are a chain.  They move on to each row's end.
     if (warp == 0) {
-      for (int i = 0; i < total; i += 32) {
-        const bool in = i + lane < total;
-        const uint32_t e = in ? list[i + lane] : 0xffffffffu;
-        const uint32_t same = __match_any_sync(0xffffffffu, e >> kPlaceBits);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        int at = 0;
-        if (in && rank == 0) {
-          at = first[e >> kPlaceBits];
-          first[e >> kPlaceBits] = at + __popc(same);
+      for (int i = 0; i < total; i += 128) {
+        uint32_t e[4], same[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = i + u * 32 + lane < total ? sh.line[i + u * 32 + lane] : kNone;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) same[u] = __match_any_sync(0xffffffffu, e[u] >> kPlaceBits);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int rank = __popc(same[u] & ((1u << lane) - 1));
+          const bool in = e[u] != kNone;
+          const int at = in ? end[e[u] >> kPlaceBits] : 0;
+          __syncwarp();
+          if (in && rank == 0) end[e[u] >> kPlaceBits] = at + __popc(same[u]);
+          if (in) sh.sorted[at + rank] = e[u];
+          __syncwarp();
         }
-        at = __shfl_sync(0xffffffffu, at, __ffs(same) - 1);
-        if (in) sorted[at + rank] = e;
-        __syncwarp();
       }
     }
     __syncthreads();
-    // Equal shares of the sorted entries.  A row that a share's border cuts is
-    // put together from the warps' parts.  first[i] is now row i's end.
-    const int per = (total + kGradWarps - 1) / kGradWarps;
-    const int p0 = min(total, warp * per), p1 = min(total, p0 + per);
-    const auto begin_of = [&](int i) { return i == 0 ? 0 : first[i - 1]; };
-    const auto put = [&](int row, const float (&sum)[4], const float (&old)[4]) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = add ? fmaf(sum[e], p.scale, old[e]) : sum[e] * p.scale;
-      cols.store(p.dtable + (static_cast<size_t>(row) * p.classes + mine) * p.d, v);
+    // Equal shares of the entries.  A row that a share's border cuts is put
+    // together from the workers' parts.
+    const int per = (total + kWorkers - 1) / kWorkers;
+    const int p0 = min(total, worker * per), p1 = min(total, p0 + per);
+    const uint32_t row_before = p0 > 0 ? sh.sorted[p0 - 1] >> kPlaceBits : kNone;
+    const uint32_t row_behind = p1 < total ? sh.sorted[p1] >> kPlaceBits : kNone;
+    const auto put = [&](uint32_t row, const float (&sum)[4]) {
+      const float v[4] = {sum[0] * p.scale, sum[1] * p.scale, sum[2] * p.scale, sum[3] * p.scale};
+      float* to = p.dtable + (static_cast<size_t>(row) * p.classes + mine) * p.d;
+      if (add) cols.add_to(to, v);
+      else cols.store(to, v);
     };
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int q = p0; q < p1; q += kAhead) {
-      float v[kAhead][4], old[kAhead][4];
-      uint32_t e[kAhead + 1];
+      typename C::Raw v[kAhead] = {};
 #pragma unroll
-      for (int u = 0; u <= kAhead; ++u) e[u] = q + u < p1 ? sorted[q + u] : 0xffffffffu;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) v[u][x] = 0.f, old[u][x] = 0.f;
-        if (q + u < p1) {
-          cols.load(dout + (base + (e[u] & ((1u << kPlaceBits) - 1))) * p.d, v[u]);
-          const int row = static_cast<int>(e[u] >> kPlaceBits);
-          if (add && e[u + 1] >> kPlaceBits != e[u] >> kPlaceBits && first[row] <= p1 && begin_of(row) >= p0)
-            cols.load(p.dtable + (static_cast<size_t>(row) * p.classes + mine) * p.d, old[u]);
-        }
-      }
+      for (int u = 0; u < kAhead; ++u)
+        if (q + u < p1) cols.load(dout + (first + (sh.sorted[q + u] & (kChunk - 1))) * p.d, &v[u]);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (q + u >= p1) break;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sum[x] += v[u][x];
-        if (e[u + 1] >> kPlaceBits == e[u] >> kPlaceBits) continue;
-        const int row = static_cast<int>(e[u] >> kPlaceBits);
-        const bool from_here = begin_of(row) >= p0;
-        if (from_here && first[row] <= p1) {
-          put(row, sum, old[u]);
+        cols.add(v[u], sum);
+        const uint32_t row = sh.sorted[q + u] >> kPlaceBits;
+        if (q + u + 1 < p1 && sh.sorted[q + u + 1] >> kPlaceBits == row) continue;
+        const bool cut_before = row == row_before, cut_behind = q + u + 1 == p1 && row == row_behind;
+        if (!cut_before && !cut_behind) {
+          put(row, sum);
         } else {
-          float* part = sh.part[warp][from_here];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) part[lane + 32 * x] = sum[x];
+          float* part = sh.part[threadIdx.x][!cut_before];  // 0: the end, or the middle, of an earlier worker's row
+          *reinterpret_cast<float4*>(part) = make_float4(sum[0], sum[1], sum[2], sum[3]);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) sum[x] = 0.f;
       }
     }
     __syncthreads();
-    if (p0 < p1) {  // a row that begins in this warp's share and ends in another's
-      const int row = static_cast<int>(sorted[p1 - 1] >> kPlaceBits);
-      if (begin_of(row) >= p0 && first[row] > p1) {
-        float old[4] = {0.f, 0.f, 0.f, 0.f};
-        if (add) cols.load(p.dtable + (static_cast<size_t>(row) * p.classes + mine) * p.d, old);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sum[x] = sh.part[warp][1][lane + 32 * x];
-        for (int w = warp + 1; w < kGradWarps && w * per < first[row]; ++w)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sum[x] += sh.part[w][0][lane + 32 * x];
-        put(row, sum, old);
+    if (p0 < p1 && row_behind != kNone) {  // a row that begins in this worker's share and ends in another's
+      const uint32_t row = sh.sorted[p1 - 1] >> kPlaceBits;
+      if (row == row_behind && row != row_before) {
+        const int last = (end[row] - 1) / per;
+        float4 x = *reinterpret_cast<const float4*>(sh.part[threadIdx.x][1]);
+#pragma unroll 4
+        for (int w = worker + 1; w <= last; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(sh.part[threadIdx.x + (w - worker) * C::kLanes][0]);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const float all[4] = {x.x, x.y, x.z, x.w};
+        put(row, all);
       }
     }
     __syncthreads();
   }
 }
 
-template <typename T, int N>
-cudaError_t backward_typed(GradArgs a, cudaStream_t stream) {
-  const int slices = (a.d + kCols - 1) / kCols;
-  if (slices > 65535) return cudaErrorInvalidValue;
+template <typename T, int N, int COLS>
+cudaError_t backward_sliced(GradArgs a, cudaStream_t stream) {
+  const int slices = (a.d + COLS - 1) / COLS;
   // Two CTAs for each SM, and no more rows a CTA than it has room for.
   a.classes = std::max({1, 2 * 152 / slices, (a.V + kMaxLocal - 1) / kMaxLocal});
   a.classes = std::min(a.classes, a.V);
   a.inverse = (1ULL << 40) / a.classes + 1;
-  a.local = (a.V + a.classes - 1) / a.classes;
-  a.chunk = std::min(kChunk, a.T / 32 * 32 + 32);
-  const size_t smem = sizeof(GradSmem) + (static_cast<size_t>(a.local) + 1 + 2 * a.chunk) * 4;
-  auto kernel = embed_backward_kernel<T, N>;
+  const size_t smem = sizeof(GradSmem) + static_cast<size_t>((a.V + a.classes - 1) / a.classes) * sizeof(int);
+  auto kernel = embed_backward_kernel<T, N, COLS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3(a.classes, slices), dim3(kGradThreads), smem, stream, a);
+}
+
+template <typename T, int N>
+cudaError_t backward_typed(const GradArgs& a, cudaStream_t stream) {
+  // Narrow slices share a common id's rows among more CTAs; wide ones leave each
+  // CTA fewer ids to sort.  About 16 slices.
+  if (a.d <= 512) return backward_sliced<T, N, 32>(a, stream);
+  if (a.d <= 1024) return backward_sliced<T, N, 64>(a, stream);
+  return backward_sliced<T, N, 128>(a, stream);
 }
 
 }  // namespace
@@ -414,7 +460,7 @@ cudaError_t launch_embed_forward(const int* tokens, const void* table, void* out
 
 cudaError_t launch_embed_backward(const int* tokens, const void* dout, float* dtable, int T, int V, int d, float scale,
                                   bool accumulate, bool dout_bf16, cudaStream_t stream) {
-  GradArgs a{tokens, dout, dtable, T, V, d, 0, 0, scale, accumulate, 0, 0};
+  GradArgs a{tokens, dout, dtable, T, V, d, 0, 0, scale, accumulate};
   const bool vec = d % 4 == 0 && on16(dtable) && reinterpret_cast<uintptr_t>(dout) % (dout_bf16 ? 8 : 16) == 0;
   if (dout_bf16)
     return vec ? backward_typed<__nv_bfloat16, 4>(a, stream) : backward_typed<__nv_bfloat16, 1>(a, stream);
