@@ -148,13 +148,13 @@ constexpr int kPlaceBits = 15;
 constexpr int kChunk = 1 << kPlaceBits;  // ids at a time
 constexpr int kList = 4096;       // of them a CTA's own
 constexpr int kWarpList = kList / kGradWarps;
-constexpr int kAhead = 8;         // gradient rows in flight per worker
+constexpr int kAhead = 4;         // gradient rows of a worker; as many again in flight
 constexpr uint32_t kNone = 0xffffffffu;
 static_assert(kMaxLocal <= 1 << (32 - kPlaceBits - 1), "an entry, row and place, fits 31 bits");
 
 struct GradSmem {  // ahead of end[local rows]
-  uint32_t list[kList];  // by warp
-  uint32_t line[kList];  // all, by place; then
+  uint32_t list[kList];  // by warp; then the ranks of the next's
+  uint32_t line[kList];  // all, by place
   uint32_t sorted[kList];
   float part[kGradThreads][2][4];
   int counts[kGradWarps];
@@ -165,8 +165,9 @@ struct GradArgs {
   const int* tokens;
   const void* dout;
   float* dtable;
-  int T, V, d, classes;
-  unsigned long long inverse;  // 2^40 / classes + 1
+  int T, V, d;
+  int classes;       // odd
+  uint32_t inverse;  // of classes, modulo 2^32
   float scale;
   bool accumulate;
 };
@@ -264,17 +265,21 @@ __global__ void __launch_bounds__(kGradThreads, 2) embed_backward_kernel(const G
       const int i0 = min(n, warp * part), i1 = min(n, i0 + part);
       uint32_t* list = sh.list + warp * kWarpList;
       int count = 0;
-      for (int i = i0; i < i1; i += 256) {
-        int v[8];
+      constexpr int kRead = 16;  // ids of a lane on their way
+      for (int i = i0; i < i1; i += kRead * 32) {
+        int v[kRead];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kRead; ++u) {
           const int at = i + u * 32 + lane;
           v[u] = at < i1 ? __ldg(p.tokens + base + at) : -1;
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint32_t q = static_cast<uint32_t>(static_cast<uint32_t>(v[u]) * p.inverse >> 40);  // v / classes
-          const bool is = v[u] >= 0 && v[u] < p.V && v[u] - static_cast<int>(q) * p.classes == mine;
+        for (int u = 0; u < kRead; ++u) {
+          if (i + u * 32 >= i1) break;
+          // Of this class: v - mine a multiple of classes, q classes by 32-bit words,
+          // and not one of those that wrap: q below the local rows (no padding is).
+          const uint32_t q = (static_cast<uint32_t>(v[u]) - static_cast<uint32_t>(mine)) * p.inverse;
+          const bool is = q < static_cast<uint32_t>(rows);
           const uint32_t b = __ballot_sync(0xffffffffu, is);
           const int at = count + __popc(b & ((1u << lane) - 1));
           if (is && at < kWarpList) list[at] = q << kPlaceBits | static_cast<uint32_t>(i + u * 32 + lane);
@@ -317,8 +322,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) embed_backward_kernel(const G
     // Rows without an id are zeros.
     if (!add) {
       const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = worker; i < rows; i += kWorkers)
-        if (end[i] == 0) cols.store(p.dtable + (static_cast<size_t>(i) * p.classes + mine) * p.d, zero);
+      const size_t step = static_cast<size_t>(kWorkers) * p.classes * p.d;
+      float* to = p.dtable + (static_cast<size_t>(worker) * p.classes + mine) * p.d;
+#pragma unroll 4
+      for (int i = worker; i < rows; i += kWorkers, to += step)
+        if (end[i] == 0) cols.store(to, zero);
     }
     if (total == 0) {  // the same for all threads
       __syncthreads();
@@ -348,25 +356,29 @@ __global__ void __launch_bounds__(kGradThreads, 2) embed_backward_kernel(const G
       }
     }
     __syncthreads();
-    // By row, and within a row by place: one warp, 128 entries at a time, of which
-    // only the rows' counters are a chain.  They move on to each row's end.
+    // By row, and within a row by place.  All warps look, among 32 entries, how
+    // many come ahead of one in its row, and how many there are; then the first warp
+    // takes the 32 through the rows' counters, which move on to each row's end.
+    uint32_t* ranks = sh.list;
+    for (int i = warp * 32; i < total; i += kGradThreads) {
+      const uint32_t row = i + lane < total ? sh.line[i + lane] >> kPlaceBits : kNone;
+      const uint32_t same = __match_any_sync(0xffffffffu, row);
+      ranks[i + lane] = __popc(same & ((1u << lane) - 1)) | static_cast<uint32_t>(__popc(same)) << 8;
+    }
+    __syncthreads();
     if (warp == 0) {
-      for (int i = 0; i < total; i += 128) {
-        uint32_t e[4], same[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) e[u] = i + u * 32 + lane < total ? sh.line[i + u * 32 + lane] : kNone;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) same[u] = __match_any_sync(0xffffffffu, e[u] >> kPlaceBits);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int rank = __popc(same[u] & ((1u << lane) - 1));
-          const bool in = e[u] != kNone;
-          const int at = in ? end[e[u] >> kPlaceBits] : 0;
-          __syncwarp();
-          if (in && rank == 0) end[e[u] >> kPlaceBits] = at + __popc(same[u]);
-          if (in) sh.sorted[at + rank] = e[u];
-          __syncwarp();
-        }
+      uint32_t e = lane < total ? sh.line[lane] : kNone, r = ranks[lane];
+      for (int i = 0; i < total; i += 32) {
+        const bool in = e != kNone;
+        int* counter = end + (in ? e >> kPlaceBits : 0);
+        const int at = in ? *counter : 0;
+        __syncwarp();
+        if (in && (r & 255) == 0) *counter = at + static_cast<int>(r >> 8);
+        if (in) sh.sorted[at + static_cast<int>(r & 255)] = e;
+        const int j = i + 32 + lane;
+        e = j < total ? sh.line[j] : kNone;
+        r = j < total ? ranks[j] : 0;
+        __syncwarp();
       }
     }
     __syncthreads();
@@ -383,11 +395,19 @@ __global__ void __launch_bounds__(kGradThreads, 2) embed_backward_kernel(const G
       else cols.store(to, v);
     };
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int q = p0; q < p1; q += kAhead) {
-      typename C::Raw v[kAhead] = {};
+    typename C::Raw next[kAhead] = {};
+    const T* from = dout + first * p.d;
+    const auto read = [&](int q) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (q + u < p1) cols.load(dout + (first + (sh.sorted[q + u] & (kChunk - 1))) * p.d, &v[u]);
+        if (q + u < p1) cols.load(from + static_cast<size_t>(sh.sorted[q + u] & (kChunk - 1)) * p.d, &next[u]);
+    };
+    read(p0);
+    for (int q = p0; q < p1; q += kAhead) {
+      typename C::Raw v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) v[u] = next[u];
+      read(q + kAhead);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (q + u >= p1) break;
@@ -427,10 +447,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) embed_backward_kernel(const G
 template <typename T, int N, int COLS>
 cudaError_t backward_sliced(GradArgs a, cudaStream_t stream) {
   const int slices = (a.d + COLS - 1) / COLS;
-  // Two CTAs for each SM, and no more rows a CTA than it has room for.
-  a.classes = std::max({1, 2 * 152 / slices, (a.V + kMaxLocal - 1) / kMaxLocal});
-  a.classes = std::min(a.classes, a.V);
-  a.inverse = (1ULL << 40) / a.classes + 1;
+  // Two CTAs for each SM, and no more rows a CTA than it has room for; odd.
+  a.classes = std::max((2 * 152 / slices - 1) | 1, ((a.V + kMaxLocal - 1) / kMaxLocal) | 1);
+  a.classes = std::min(a.classes, (a.V - 1) | 1);
+  a.inverse = 1;  // Newton's steps: each doubles the bits that are right
+  for (int i = 0; i < 5; ++i) a.inverse *= 2 - static_cast<uint32_t>(a.classes) * a.inverse;
   const size_t smem = sizeof(GradSmem) + static_cast<size_t>((a.V + a.classes - 1) / a.classes) * sizeof(int);
   auto kernel = embed_backward_kernel<T, N, COLS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -442,7 +463,7 @@ template <typename T, int N>
 cudaError_t backward_typed(const GradArgs& a, cudaStream_t stream) {
   // Narrow slices share a common id's rows among more CTAs; wide ones leave each
   // CTA fewer ids to sort.  About 16 slices.
-  if (a.d <= 512) return backward_sliced<T, N, 32>(a, stream);
+  if (a.d <= 400) return backward_sliced<T, N, 32>(a, stream);
   if (a.d <= 1024) return backward_sliced<T, N, 64>(a, stream);
   return backward_sliced<T, N, 128>(a, stream);
 }
