@@ -4,6 +4,7 @@ type (2^-8 of the value in bf16, 2^-24 in fp32), 2^-24 of the terms' sizes for
 each fp32 addition, 2^-23 for those of the tensor cores, which may cut off."""
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -127,6 +128,17 @@ def test_embed_backward(txl, T, V, d, pad, ids, accumulate, dtype):
     assert torch.equal(got.view(torch.int32), again.view(torch.int32))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("T,V,d,pad,ids", [
+    (70000, 500, 40, 0.1, "z"), (33001, 9, 20, 0.0, "s"), (40000, 70000, 8, 0.0, "u"), (33000, 5000, 130, 0.2, "z"),
+    (2000, 300, 701, 0.0, "z"), (1500, 200, 1201, 0.1, "z"), (9000, 2, 1100, 0.0, "u"),
+])
+def test_embed_backward_long(txl, T, V, d, pad, ids, accumulate, dtype):
+    """More ids than one pass takes, more of one row than a warp lists, and wide rows that start anywhere."""
+    test_embed_backward(txl, T, V, d, pad, ids, accumulate, dtype)
+
+
 def test_embed_backward_unaligned(txl):
     rng = np.random.default_rng(3)
     tokens, V, d = _zipf(rng, 400, 60), 60, 64
@@ -214,6 +226,16 @@ def test_dense_w4_exact(txl, m, k, n, group):
     y = torch.empty(m, n, device=dev())
     txl.txl_dense_w4(x, codes, scales, y)
     assert np.array_equal(_host(y), _host(x) @ O.unpack_w4(codes.cpu().numpy(), _host(scales)))
+
+
+@pytest.mark.parametrize("m,k,n,group", [
+    (32, 4096, 1024, 128), (32, 4096, 4096, 64), (8, 4096, 1024, 32), (70, 4096, 256, 128), (32, 4096, 64, 64), (9, 8320, 264, 64),
+    (1, 8192, 40, 32), (16, 4096, 512, 32),
+])
+def test_dense_w4_shared_k(txl, m, k, n, group):
+    """Sizes at which clusters of CTAs share k, x in one stretch and in several."""
+    test_dense_w4_exact(txl, m, k, n, group)
+    test_dense_w4(txl, m, k, n, group, "bf16")
 
 
 def test_dense_w4_rows_do_not_meet(txl):
@@ -385,6 +407,59 @@ def test_sample_longest_rows(txl):
     assert int(tokens[0]) == math.floor(float(u[0]) * math.ceil(0.5 * (V - 1)))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,V", [(1, 131072), (3, 70000), (20, 90000), (60, 20000), (30, 20000), (160, 20011), (12, 70001), (2, 1 << 18)])
+def test_sample_shared_rows(txl, B, V, dtype):
+    """Rows that one, two, four or eight CTAs share."""
+    rng = np.random.default_rng(V + B)
+    z = _tensor(2.0 * rng.standard_normal((B, V)) + 6 * (rng.random((B, V)) < 30 / V), NAMES[dtype])
+    _check_sample(txl, z, rng.random(B), top_k=rng.integers(0, 600, B), top_p=rng.uniform(0.5, 1.1, B), min_p=rng.uniform(0, 0.01, B))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", [0, 300, 50000, 130800])
+def test_sample_largest_together(txl, first, dtype):
+    """The largest tokens in one CTA's stretch, more than it can hand over at once."""
+    rng = np.random.default_rng(first)
+    z = rng.standard_normal((4, 131072))
+    z[:, first:first + 240] += 9
+    z = _tensor(z, NAMES[dtype])
+    for k in (60, 100, 200, 256, 700):
+        for s in ({}, dict(top_p=[0.3, 0.8, 0.95, 1.0]), dict(min_p=[0.5, 0.1, 0.01, 0.0])):
+            _check_sample(txl, z[:1], rng.random(1), top_k=[k], **{n: v[:1] for n, v in s.items()})
+            _check_sample(txl, z, rng.random(4), top_k=[k] * 4, **s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [700, 20000, 131072])
+def test_sample_few_that_matter(txl, V, dtype):
+    """A few tokens with most of the weight: the border of top-p is far from where the bins' middles put it."""
+    rng = np.random.default_rng(V)
+    for lead in (1, 2, 3, 9):
+        z = rng.standard_normal((5, V))
+        at = rng.integers(0, V, (5, lead))
+        np.put_along_axis(z, at, 18 + rng.random((5, lead)), 1)
+        _check_sample(txl, _tensor(z, NAMES[dtype]), rng.random(5), top_p=[0.2, 0.6, 0.9, 0.999, 0.9999999])
+        _check_sample(txl, _tensor(40 * z, NAMES[dtype]), rng.random(5), top_p=[0.2, 0.6, 0.9, 0.999, 0.9999999], temperature=[30.0] * 5)
+
+
+@pytest.mark.parametrize("V", [64, 5000, 40000])
+def test_sample_hard_rows_bf16(txl, V):
+    """In bf16: equal logits (there are few values), +inf, masks of -inf and of the type's lowest value, NaN."""
+    rng = np.random.default_rng(V + 1)
+    z = rng.integers(-2, 3, (6, V)).astype(np.float64)
+    z[1, rng.random(V) < 0.5] = -np.inf
+    z[2, rng.random(V) < 0.5] = -3.3895313892515355e38
+    z[3, ::5] = np.inf
+    z[4, rng.random(V) < 0.5] = np.nan
+    z[5] = -np.inf
+    z = _tensor(z, BF)
+    u = rng.random(6)
+    for s in ({}, dict(top_k=[1, 3, V // 2, V, 9, 4]), dict(top_p=[0.1, 0.5, 0.9, 0.3, 0.99, 0.5]),
+              dict(top_k=[200, 20, V // 3, 2, 0, 1], top_p=[0.7] * 6, min_p=[0.2] * 6), dict(temperature=[0.0] * 6)):
+        _check_sample(txl, z, u, **s)
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
@@ -441,6 +516,46 @@ def test_calls_on_streams_and_graphs(txl):
     txl.txl_sample(logits, u, out, top_k=k, top_p=p, stream=side)
     txl.txl_embed_backward(tokens, h, grad, 0.5, stream=side)
     assert all(torch.equal(a, b) for a, b in zip(results(), want))
+
+
+def test_calls_of_many_threads(txl):
+    """Calls of other sizes from several threads, each on its own stream, at the same time: a call's shared memory is
+    its own, whatever the last one of the same kernel needed."""
+    lib, ptr = txl.lib, torch.Tensor.data_ptr  # (the binding's calls hold the interpreter's lock)
+    rng = np.random.default_rng(15)
+    jobs = []
+    for V, k, n in ((64, 128, 64), (30000, 4096, 256), (2000, 512, 64), (20000, 2048, 128)):
+        z, u, out = _tensor(rng.standard_normal((2, V)), F32), torch.full((2,), 0.5, device=dev()), torch.empty(2, device=dev(), dtype=torch.int32)
+        x, codes, scales = _product(rng, 4, k, n, 32)
+        y, tokens = torch.empty(4, n, device=dev(), dtype=BF), _ints(rng.integers(0, V, 100))
+        dout, grad = _tensor(rng.standard_normal((100, 16)), F32), torch.empty(V, 16, device=dev())
+        jobs.append((V, k, n, z, u, out, x, codes, scales, y, tokens, dout, grad, torch.cuda.Stream()))
+    want = []
+    for V, k, n, z, u, out, x, codes, scales, y, tokens, dout, grad, _ in jobs:
+        txl.txl_sample(z, u, out)
+        txl.txl_dense_w4(x, codes, scales, y)
+        txl.txl_embed_backward(tokens, dout, grad)
+        want.append([t.clone() for t in (out, y, grad)])
+    _settle()
+    bad, start = [], threading.Barrier(len(jobs))
+
+    def run(V, k, n, z, u, out, x, codes, scales, y, tokens, dout, grad, stream):
+        s = stream.cuda_stream
+        start.wait()
+        for _ in range(300):
+            bad.append(lib.txl_sample(ptr(z), V, 2, V, ptr(u), None, None, None, None, ptr(out), None, 0, s))
+            bad.append(lib.txl_dense_w4(ptr(x), ptr(codes), ptr(scales), ptr(y), 4, n, k, 32, None, 0, 1, s))
+            bad.append(lib.txl_embed_backward(ptr(tokens), ptr(dout), ptr(grad), 100, V, 16, 1.0, 0, 0, s))
+
+    threads = [threading.Thread(target=run, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _settle()
+    assert sum(bad) == 0, (sum(b != 0 for b in bad), len(bad))
+    for (_, _, _, _, _, out, _, _, _, y, _, _, grad, _), w in zip(jobs, want):
+        assert all(torch.equal(a, b) for a, b in zip((out, y, grad), w))
 
 
 def test_decoding_over_pages(txl):

@@ -370,7 +370,8 @@ cudaError_t launch(Args a, cudaStream_t stream) {
       a.wr_log = wr_log, a.split = split, a.ks = mine * kBlockK, a.kx = kx;
     }
   auto kernel = dense_w4_kernel<G, MT, YB>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, best_smem);
+  // The most that any call needs: another thread may set it at the same time.
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem(kMaxX));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(best_clusters * a.split, (a.m + S::kTokens - 1) / S::kTokens);

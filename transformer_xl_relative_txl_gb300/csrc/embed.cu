@@ -454,7 +454,9 @@ cudaError_t backward_sliced(GradArgs a, cudaStream_t stream) {
   for (int i = 0; i < 5; ++i) a.inverse *= 2 - static_cast<uint32_t>(a.classes) * a.inverse;
   const size_t smem = sizeof(GradSmem) + static_cast<size_t>((a.V + a.classes - 1) / a.classes) * sizeof(int);
   auto kernel = embed_backward_kernel<T, N, COLS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The most that any call needs: another thread may set it at the same time.
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       sizeof(GradSmem) + kMaxLocal * sizeof(int));
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3(a.classes, slices), dim3(kGradThreads), smem, stream, a);
 }

@@ -928,7 +928,9 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   const int stretch = ((a.V + CTAS - 1) / CTAS + kCell - 1) / kCell * kCell;
   const size_t smem = sizeof(Shared) + static_cast<size_t>(stretch) * sizeof(T);
   auto kernel = sample_kernel<T, VEC, CTAS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The most that any call needs: another thread may set it at the same time.
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       sizeof(Shared) + kCells * kCell * sizeof(T));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CTAS, a.B);
