@@ -43,7 +43,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kTable = 512;      // steps of the powers' table
 constexpr int kOne = 44;         // the largest weight is 2^kOne
 constexpr int kCell = 256;       // tokens that a warp takes at once, 8 a lane
-constexpr int kCells = 128;      // of a CTA's stretch, at most
+constexpr int kCells = 256;      // of a CTA's stretch, at most
+constexpr int kLaneCells = kCells / 32;
 
 // 2^(-j / kTable) in units of 2^-44, from nine square roots of a half by
 // Newton's method.
@@ -847,18 +848,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     }
   }
   __syncthreads();
-  // The first warp goes on with four cells a lane, and what lies ahead of them.
-  unsigned long long over[4], over_before = 0;
-  int at[4], at_before = 0;
+  // The first warp goes on with kLaneCells cells a lane, and what lies ahead of them.
+  unsigned long long over[kLaneCells], over_before = 0;
+  int at[kLaneCells], at_before = 0;
   if (warp == 0) {
-    static_assert(kCells == 4 * 32 && kSampleMaxVocab <= kMaxCluster * kCells * kCell, "cells");
     unsigned long long sum = 0;
     int sum_at = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool is = 4 * lane + i < row.cells;
-      over[i] = is ? sh.cell_over[4 * lane + i] : 0ULL;
-      at[i] = is ? sh.cell_ties[4 * lane + i] : 0;
+    for (int i = 0; i < kLaneCells; ++i) {
+      const bool is = kLaneCells * lane + i < row.cells;
+      over[i] = is ? sh.cell_over[kLaneCells * lane + i] : 0ULL;
+      at[i] = is ? sh.cell_ties[kLaneCells * lane + i] : 0;
       sum += over[i];
       sum_at += at[i];
     }
@@ -889,13 +889,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   int cell = -1, cell_at = 0;
   unsigned long long rest = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kLaneCells; ++i) {
     const unsigned long long from = ahead + over_before + kept(ties_left, at_before) * w_tie;
     const int before = at_before;
     over_before += over[i];
     at_before += at[i];
     const unsigned long long to = ahead + over_before + kept(ties_left, at_before) * w_tie;
-    if (from <= target && target < to) cell = 4 * lane + i, cell_at = before, rest = target - from;
+    if (from <= target && target < to) cell = kLaneCells * lane + i, cell_at = before, rest = target - from;
   }
   const uint32_t who = __ballot_sync(0xffffffffu, cell >= 0);
   if (who == 0) return;
@@ -923,6 +923,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   }
 }
 
+// Of type T, with all else that a CTA has in shared memory.
+template <typename T>
+constexpr int max_cells() {
+  return std::min(kCells, static_cast<int>((227 * 1024 - sizeof(Shared)) / (kCell * sizeof(T))));
+}
+static_assert(kSampleMaxVocab <= kMaxCluster * max_cells<float>() * kCell, "a cluster has room for a row");
+
 template <typename T, int VEC, int CTAS>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   const int stretch = ((a.V + CTAS - 1) / CTAS + kCell - 1) / kCell * kCell;
@@ -930,7 +937,7 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   auto kernel = sample_kernel<T, VEC, CTAS>;
   // The most that any call needs: another thread may set it at the same time.
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       sizeof(Shared) + kCells * kCell * sizeof(T));
+                                       sizeof(Shared) + max_cells<T>() * kCell * sizeof(T));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CTAS, a.B);
@@ -951,22 +958,32 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
 
 template <typename T, int VEC>
 cudaError_t by_size(const SampleArgs& a, cudaStream_t stream) {
-  // CTAs of a row: enough for at most 32768 values each, up to 4 of them for at
-  // most 64 KB; and more, of 4096 values at least, where the rows alone would leave
-  // most SMs without work.  64 rows of 131072 in bf16, top-p: 66 us by 4 CTAs each,
-  // 81 by 8; one row 36 and 25.  256 rows of 32768: bf16 60 by one CTA, 69 by 2, fp32
-  // 76 and 71.  (Few clusters of 8 find room at a time.)
-  int ctas = 1;
-  while (ctas < kMaxCluster &&
-         (a.V > ctas * kCells * kCell || (ctas < 4 && a.V * sizeof(T) > ctas * 65536ULL) ||
-          (a.B * ctas < 100 && a.V > ctas * 4096 && (ctas < 4 || a.B <= 12))))
-    ctas *= 2;
+  // CTAs of a row, by the time that they take: fitted to 220 measured ones (1 to 256
+  // rows of 4096 to 131072, bf16 and fp32, with and without top-k and top-p), whose
+  // best it misses by 1% on average and 18% at most.  Some rows find room at a time,
+  // two CTAs on an SM where their stretches fit, the others follow; 37 clusters
+  // of 4 and 18 of 8 do where there are SMs for 38 and 19.  Both ends, by top-p:
+  // one row of 131072 takes 25 us by 8 CTAs and 60 by 2, 256 of 16384 take 36 by one
+  // each and 121 by 8.
+  int ctas = 0;
+  double best = 0;
+  for (int log = 0; 1 << log <= kMaxCluster; ++log) {
+    const int c = 1 << log, stretch = ((a.V + c - 1) / c + kCell - 1) / kCell * kCell;
+    if (stretch > max_cells<T>() * kCell) continue;
+    const bool two = 2 * (sizeof(Shared) + stretch * sizeof(T) + 1024) <= 228 * 1024;
+    constexpr int kPlaces[] = {152, 76, 37, 18};
+    const int places = kPlaces[log] * (two ? 2 : 1), rest = a.B % places;
+    const auto us = [&](bool shared) { return 10 + 1.5 * log + stretch / 1200.0 * (shared ? 1.9 : 1.0); };
+    const double all = a.B / places * us(two) + (rest == 0 ? 0.0 : us(rest > kPlaces[log]));
+    if (ctas == 0 || all < best) ctas = c, best = all;
+  }
   switch (ctas) {
     case 1: return launch<T, VEC, 1>(a, stream);
     case 2: return launch<T, VEC, 2>(a, stream);
     case 4: return launch<T, VEC, 4>(a, stream);
-    default: return launch<T, VEC, 8>(a, stream);
+    case 8: return launch<T, VEC, 8>(a, stream);
   }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
