@@ -707,7 +707,9 @@ TXL_API int txl_embed_forward(const int* tokens, const void* table, void* out, i
  *           neither read nor written (T == 0: an empty call)
  * tokens, scale, alignments and limits as in txl_embed_forward; dtable must not
  * overlap tokens or dout.  Sums are fp32, in an order that only the tokens decide:
- * the same call gives the same bits.
+ * the same call gives the same bits.  A sum is rounded, then its product with
+ * scale, then, with accumulate, that added to the row, where subnormal numbers
+ * count and are left as 0.
  */
 TXL_API int txl_embed_backward(const int* tokens, const void* dout, float* dtable, int T, int V, int d, float scale,
                                int accumulate, txl_dtype dtype, cudaStream_t stream);
@@ -748,7 +750,8 @@ TXL_API int txl_dense_w4(const void* x, const void* codes, const void* scales, v
  * their whole sum.
  *
  *   logits       device, [B, V] `dtype`, rows row_stride elements apart (>= V).
- *                -inf and NaN are never kept, +inf counts as the largest float
+ *                -inf and NaN are never kept, +inf counts as the largest
+ *                number of its type
  *   uniform      device, [B] fp32, in [0, 1) (below: as 0; from 1 on: the last
  *                kept token)
  *   temperature  device, [B] fp32 or NULL (1); not over 0: the largest logit's
@@ -757,6 +760,7 @@ TXL_API int txl_dense_w4(const void* x, const void* codes, const void* scales, v
  *   top_p        device, [B] fp32 or NULL; not under 1: off
  *   min_p        device, [B] fp32 or NULL; not over 0: off, over 1: as 1
  *   tokens       device, [B] int32 out; -1 for a row without a logit to keep
+ *                (its prob 0)
  *   prob         device, [B] fp32 out or NULL: the token's share of the kept
  *                weights
  * Sums of weights are whole numbers (2^-44 of the largest weight), so neither the

@@ -2,22 +2,33 @@
 //
 //   W[j, i] = scales[j / G, i] * (code[i, j] - 8),   codes two to a byte along j
 //
-// Bound by reading the codes once.  The weights are the long operand, on the M
-// side of mma.sync m16n8k16: a warp takes 16 of W's columns (n) by 256 rows (k)
-// at a time, 2 KB of codes, which it brings to its own shared memory by
-// cp.async, several blocks ahead, without any other warp's part.  The tokens
-// are the 8 columns of the right-hand side, 8, 16 or 32 of them.
+// Its floor is reading the codes once; what it meets is the issue of instructions,
+// of which those that make bf16 of codes are the most (131072 columns of 1024, 8
+// tokens: 19.4 us, 3.8 TB/s), or, in small products, the chain of launch, first
+// blocks and sums: 512 x 512 for one token 2.8 us, 4096 x 1024 for 32 6.1.
+//
+// The weights are the long operand, on the M side of mma.sync m16n8k16: a warp takes
+// 16 of W's columns (n) by 256 rows (k) at a time, 2 KB of codes, which it brings to
+// its own shared memory by cp.async, several blocks ahead, without any other warp's
+// part.  The tokens are the 8 columns of the right-hand side, 8, 16 or 32 of them.
+// (tcgen05 wants both operands in shared or tensor memory: the bf16 values of the
+// codes would be stored and read once more, four times the codes' bytes, for tensor
+// cores that are a fifth busy.)
 //
 // Nothing is rounded on the way: a code less 8 is exact in bf16 and so is x, the
 // products are summed in fp32 over a group and the sum times the scale is added
-// to the fp32 total.
+// to the fp32 total.  (Both in units of 1 / 64, see below: exact, but for sums near
+// 2^-126.)
 //
-// A code becomes a bf16 value by 0x4300 | code = 128 + code, less 136, two at a
-// time: codes c and c + 4 of a 32-bit word of 8.  The sum over k has no order,
-// so x is laid out in shared memory by the same pairs, (0,4) (1,5) (2,6) (3,7) of
-// every 8, and one ldmatrix hands each lane the words that it needs: lane (g,
-// t) gets word t of chunk w of row g, codes 32 w + 8 t .. + 7, so that the 16
-// values of a step lie within one group of 32 or more.
+// The low 8 bits of a bf16 number are its multiple of 2^-133, so a code, alone in
+// the lower or upper four of them, becomes its value less 8, in units of 1 / 64, by
+// one fma with 2^127 or 2^123, two codes at a time: codes c and c + 4 of a 32-bit
+// word of 8.  (As 128 + code, less 136, it needs two shifts more for 8 codes: 21.1
+// us against 19.4 for 131072 columns of 1024.)  The sum over k has no order, so x is
+// laid out in shared memory by the same pairs, (0,4) (1,5) (2,6) (3,7) of every 8,
+// and one ldmatrix hands each lane the words that it needs: lane (g, t) gets word t
+// of chunk w of row g, codes 32 w + 8 t .. + 7, so that the 16 values of a step lie
+// within one group of 32 or more.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -63,14 +74,23 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Codes j and j + 4 of a word, less 8, as bf16.
-template <int J>
-__device__ __forceinline__ uint32_t pair_of(uint32_t word) {
-  const uint32_t at = word >> (4 * J), mask = 0x000F000Fu, base = 0x43004300u, less = 0xC308C308u;  // less: -136
-  uint32_t w, r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(w) : "r"(at), "r"(mask), "r"(base));  // at & mask | base
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(less));
+// Codes j and j + 4 of a word, less 8, times kUnit, as bf16.
+constexpr float kUnit = 1.f / 64;
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
+}
+struct Codes {
+  uint32_t at[4];
+};
+__device__ __forceinline__ Codes codes_of(uint32_t word) {
+  const uint32_t upper = word >> 8;
+  constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;        // the codes' places
+  constexpr uint32_t kOfLo = 0x7F007F00u, kOfHi = 0x7D007D00u;    // 2^127 and 2^123
+  constexpr uint32_t kLess = 0xBE00BE00u;                         // -8 / 64
+  return Codes{{fma_bf16x2(word & kLo, kOfLo, kLess), fma_bf16x2(word & kHi, kOfHi, kLess),
+                fma_bf16x2(upper & kLo, kOfLo, kLess), fma_bf16x2(upper & kHi, kOfHi, kLess)}};
 }
 
 template <int G, int MT>
@@ -241,8 +261,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kerne
 #pragma unroll
                   for (int e = 0; e < 4; ++e) acc[s][a][e] = 0.f;
             }
-            const uint32_t wa[4] = {pair_of<0>(lo[w]), pair_of<0>(hi[w]), pair_of<1>(lo[w]), pair_of<1>(hi[w])};
-            const uint32_t wb[4] = {pair_of<2>(lo[w]), pair_of<2>(hi[w]), pair_of<3>(lo[w]), pair_of<3>(hi[w])};
+            const Codes l = codes_of(lo[w]), h = codes_of(hi[w]);
+            const uint32_t wa[4] = {l.at[0], h.at[0], l.at[1], h.at[1]};
+            const uint32_t wb[4] = {l.at[2], h.at[2], l.at[3], h.at[3]};
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
               const uint4 v = *reinterpret_cast<const uint4*>(xb + a * 8 * pitch + c * 64);
@@ -265,6 +286,10 @@ __global__ void __launch_bounds__(kThreads, Shape<G, MT>::kPerSm) dense_w4_kerne
         slot = slot == kStages - 1 ? 0 : slot + 1;
       }
     }
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[a][e] *= 1.f / kUnit;
     if (wk == 1 && p.split == 1) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -343,13 +368,13 @@ cudaError_t launch(Args a, cudaStream_t stream) {
   constexpr int kMaxX = kXBytes / (2 * S::kTokens) / kBlockK * kBlockK;
   const int blocks = (a.k + kBlockK - 1) / kBlockK;
   // How many warps stand along n and how many CTAs share k, by the time that a
-  // pair takes: fitted to 250 measured ones (m 1 to 32, k 128 to 4096, n 512 to
-  // 131072), whose best it misses by 11% at most.  In ns: a block to a warp, an SM
-  // full of warps a block, a sum of warps, of CTAs, 1 KB of x.  Both ends: 32
-  // tokens, k = 4096, n = 1024 take 21 us with a CTA for 128 columns and all of k,
-  // 6.3 with a cluster of four for 32; 8 tokens, k = 1024, n = 131072 take 21 with
-  // the first and 94 with a cluster of two.
-  constexpr int kAlone = MT == 1 ? 560 : MT == 2 ? 640 : 1250, kFull = MT == 1 ? 100 : MT == 2 ? 120 : 250;
+  // pair takes: fitted to 250 measured ones (m 1 to 32, k 128 to 8192, n 512 to
+  // 131072), whose best it misses by 12% at most.  In ns: each block of the SM with
+  // the most, a sum of warps, of CTAs, 1 KB of x.  Both ends: 32 tokens, k =
+  // 4096, n = 1024 take 21 us with a CTA for 128 columns and all of k, 6.3 with a
+  // cluster of four for 32; 8 tokens, k = 1024, n = 131072 take 19.4 with the first
+  // and 98 with a cluster of four for 64.
+  constexpr int kEach = MT == 1 ? 70 : MT == 2 ? 90 : 190;
   long long best = -1;
   int best_clusters = 1, best_smem = 0;
   for (int wr_log = 3; wr_log >= 0; --wr_log)
@@ -361,10 +386,9 @@ cudaError_t launch(Args a, cudaStream_t stream) {
       // (12 clusters of 8 find room at a time, of 19 that there are SMs for.)
       const int clusters = std::min(tiles, split == 8 ? 12 * per_sm : 152 * per_sm / split);
       const long long rounds = (tiles + clusters - 1) / clusters;
-      const long long alone = rounds * ((mine + wk - 1) / wk) * kAlone;
-      const long long full = (static_cast<long long>(tiles) << wr_log) * blocks * kFull / 152;
-      const long long ns = std::max(alone, full) + rounds * ((wk > 1 ? 320 : 0) + (split > 1 ? 1650 : 0)) +
-                           12LL * mine * kBlockK * S::kTokens * 2 / 1024 * (mine * kBlockK > kMaxX ? rounds : 1);
+      const long long on_sm = (static_cast<long long>(tiles) * split + 151) / 152 * mine << wr_log;  // blocks
+      const long long ns = on_sm * kEach + rounds * ((wk > 1 ? 670 : 0) + (split > 1 ? 2100 : 0)) +
+                           8LL * mine * kBlockK * S::kTokens * 2 / 1024 * (mine * kBlockK > kMaxX ? rounds : 1);
       if (best >= 0 && ns >= best) continue;
       best = ns, best_clusters = clusters, best_smem = smem;
       a.wr_log = wr_log, a.split = split, a.ks = mine * kBlockK, a.kx = kx;
