@@ -604,7 +604,7 @@ __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, c
   clear_bins(sh);
   unsigned long long all = 0, above = 0;
   for (int cell = warp; cell < row.cells; cell += kWarps) {
-    unsigned long long kept = 0;
+    unsigned long long over = 0, less = 0;  // above the window; of those, what min_p does not keep
     float z[8];
     row.get(cell, z);
 #pragma unroll
@@ -615,14 +615,18 @@ __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, c
         w[e] = weight(z[half + e], top, c, sh.table);
         w[e] = z[half + e] >= lo ? w[e] : 0ULL;
         all += w[e];
-        const unsigned long long over = z[half + e] > to ? w[e] : 0ULL;
-        above += over;
-        kept += over >= least ? over : 0ULL;
+        over += z[half + e] > to ? w[e] : 0ULL;
+      }
+      if (least != 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) less += z[half + e] > to && w[e] < least ? w[e] : 0ULL;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (z[half + e] >= from && z[half + e] <= to) add64(&sh.bins[window.range.bin(z[half + e])], w[e]);
     }
+    above += over;
+    unsigned long long kept = over - less;
     if (__any_sync(0xffffffffu, kept != 0)) kept = warp_sum(kept);
     if (lane == 0) sh.cell_over[cell] = kept;
   }
