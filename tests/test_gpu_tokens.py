@@ -296,6 +296,7 @@ def _check_sample(txl, z, u, **settings):
 SETTINGS = [
     {}, dict(temperature=(0.3, 1.7)), dict(top_k=(1, 40)), dict(top_p=(0.1, 0.999)), dict(min_p=(0.001, 0.3)), dict(top_k=(1, 3000), top_p=(0.3, 1.0)),
     dict(temperature=(0.2, 2.0), top_k=(5, 500), top_p=(0.5, 0.99), min_p=(0.0001, 0.05)), dict(temperature=(0.5, 1.5), top_p=(0.9, 0.9999)),
+    dict(top_p=(0.8, 0.999), min_p=(0.0001, 0.2)), dict(temperature=(0.01, 50.0), min_p=(0.0001, 1.0)),
 ]
 
 
@@ -521,7 +522,7 @@ def test_calls_on_streams_and_graphs(txl):
 def test_calls_of_many_threads(txl):
     """Calls of other sizes from several threads, each on its own stream, at the same time: a call's shared memory is
     its own, whatever the last one of the same kernel needed."""
-    lib, ptr = txl.lib, torch.Tensor.data_ptr  # (the binding's calls hold the interpreter's lock)
+    lib, ptr = txl.lib, torch.Tensor.data_ptr
     rng = np.random.default_rng(15)
     jobs = []
     for V, k, n in ((64, 128, 64), (30000, 4096, 256), (2000, 512, 64), (20000, 2048, 128)):

@@ -3,6 +3,8 @@ share its steps with, and the calls' refusals, which come before any launch."""
 
 import ctypes
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -151,3 +153,32 @@ def test_binding_refuses_host_tensors(lib):
     with pytest.raises(TypeError):
         txl.txl_sample(None, f, i)
     assert ctypes.sizeof(ctypes.c_longlong) == 8
+
+
+# ---------------------------------------------------------------------------
+# what the kernels' sources say
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("name", ["embed", "dense_w4", "sample"])
+def test_nothing_is_touched_ahead_of_the_wait(name):
+    """A kernel that starts while the one before it runs reads and writes no global memory, no other CTA's, and lets no
+    kernel start, until it has waited; and it waits whatever its arguments."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "transformer_xl_relative_txl_gb300", "csrc", name + ".cu")
+    with open(path) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    bodies = re.findall(r"__global__ void\s+__launch_bounds__.*?\{(.*?)\n\}\n", text, re.S)
+    assert len(bodies) == {"embed": 2, "dense_w4": 1, "sample": 1}[name]
+    for body in bodies:
+        ahead, wait, _ = body.partition("grid_dep_wait();")
+        assert wait
+        assert not re.search(r"__ldg|load|copy16|fetch|atomic|\bred\b|prefetch|map_shared_rank|launch_dependents|return|p\.\w+\[|kPowers", ahead)
+
+
+@pytest.mark.parametrize("name", ["embed", "dense_w4", "sample"])
+def test_the_cap_on_shared_memory_is_no_call_s_own(name):
+    """Two threads' calls of one kernel must not undo each other's cap: it is a constant of the kernel."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "transformer_xl_relative_txl_gb300", "csrc", name + ".cu")
+    with open(path) as f:
+        text = re.sub(r"\s+", " ", f.read())
+    caps = re.findall(r"cudaFuncSetAttribute\(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (.*?)\);", text)
+    assert caps == [{"embed": "sizeof(GradSmem) + kMaxLocal * sizeof(int)", "dense_w4": "S::smem(kMaxX)",
+                     "sample": "sizeof(Shared) + max_cells<T>() * kCell * sizeof(T)"}[name]]
