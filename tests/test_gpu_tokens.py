@@ -429,6 +429,10 @@ def test_sample_largest_together(txl, first, dtype):
         for s in ({}, dict(top_p=[0.3, 0.8, 0.95, 1.0]), dict(min_p=[0.5, 0.1, 0.01, 0.0])):
             _check_sample(txl, z[:1], rng.random(1), top_k=[k], **{n: v[:1] for n, v in s.items()})
             _check_sample(txl, z, rng.random(4), top_k=[k] * 4, **s)
+    wide = rng.standard_normal((3, 131072))
+    wide[:, first:first + 480] += 9
+    for k in (300, 450, 480, 512, 513):
+        _check_sample(txl, _tensor(wide, F32), rng.random(3), top_k=[k] * 3, top_p=[0.6, 0.99, 1.0])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

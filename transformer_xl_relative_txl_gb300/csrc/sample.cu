@@ -23,7 +23,7 @@
 // Bound by chains of dependent instructions: some 85 for 32 exact weights, 25 for 32
 // logits put into bins, and ten or so barriers of a cluster, 1000 to 2000 cycles
 // each with what is done between them.  One row of 32768 in bf16, top-k 50 of it
-// and top-p: 8.5 us; 64 of 131072 with settings of their own: 33 us (17 MB: 0.5 TB/s);
+// and top-p: 8.5 us; 64 of 131072, top-k 100 to 300 and more: 26 us (17 MB: 0.65 TB/s);
 // 128 of 50021 in fp32 by top-p, where every logit's weight counts: 57 us (0.45 TB/s),
 // of 107000 cycles of a CTA 50000 for the weights, 17000 for the last look at the
 // cells, 10000 for the counts, 7000 for the reading.  There the schedulers issue 41%
@@ -47,7 +47,9 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kGroup = 32, kGroups = kBins / kGroup;  // bins that are first looked at together
-constexpr int kFew = 256;        // tokens that are compared each with each
+constexpr int kFew = 256;        // tokens of a bin that are compared each with each
+constexpr int kList = 512;       // or all down to a border of counts, that are sorted
+constexpr int kCounted = 256;    // by counting
 constexpr int kMaxCluster = 8;
 constexpr int kTable = 512;      // steps of the powers' table
 constexpr int kOne = 44;         // the largest weight is 2^kOne
@@ -181,8 +183,8 @@ struct Shared {
   Found found[kMaxCluster];
   Kept kept[kMaxCluster];
   Mass mass[kMaxCluster];
-  Candidate seg[2 * kFew];  // a part for each CTA
-  Candidate cand[kFew];
+  Candidate seg[kList];  // a part for each CTA
+  Candidate cand[kList];
   unsigned long long cand_w[kFew];
   unsigned long long warp_sum[kWarps];
   float warp_top[kWarps];
@@ -236,6 +238,12 @@ struct Range {
     if (keys) return static_cast<int>((ordered(hi) - ordered(z + 0.f)) >> shift);  // (-0 is 0)
     const float x = fmaxf(fminf(fmaf(z, -per, at_hi), kBins - 1.f), 0.f);
     return __float_as_int(x + 8388608.f) & (2 * kBins - 1);
+  }
+  // How far a linear bin's token is behind its middle, in kOffset-ths of a bin.
+  static constexpr float kOffset = 16384.f;
+  __device__ __forceinline__ int offset(float z, int b) const {
+    const float x = fmaf(z, -per, at_hi) - static_cast<float>(b);
+    return __float2int_rn(fminf(fmaxf(x, -0.5f), 0.5f) * kOffset);
   }
   // Ends outside of which no token is in bin b (or in a later one, in an earlier).
   __device__ __forceinline__ void near(int b, float* from, float* to) const {
@@ -358,7 +366,7 @@ __device__ __forceinline__ void collect(Shared& sh, int n) {
   if (i < n) {
     int r = 0;
     for (; r < CTAS - 1 && i >= sh.found[r].n; ++r) i -= sh.found[r].n;
-    sh.cand[threadIdx.x] = sh.seg[r * (2 * kFew / CTAS) + i];
+    sh.cand[threadIdx.x] = sh.seg[r * (kList / CTAS) + i];
   }
   __syncthreads();
 }
@@ -394,10 +402,9 @@ struct Window {
 template <bool WEIGHTED, int CTAS, typename T, typename F>
 __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float hi,
                                          float top, Scale c, F target_of, const Window& window = Window{false, {}}) {
-  constexpr int kPart = CTAS == 1 ? kFew : 2 * kFew / CTAS;  // candidates from one CTA
+  constexpr int kPart = kList / CTAS;  // candidates from one CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = static_cast<int>(cluster.block_rank());
   unsigned long long above = 0, target = 0;
-  bool lists = !WEIGHTED;
   Range range;
   for (int level = 0;; ++level) {
     const bool ready = WEIGHTED && level == 0 && window.is;
@@ -464,7 +471,7 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     const int bin = sh.bin;
     // All tokens down to the border where they are few (counts), else the bin's;
     // and the bin's ends.
-    const bool list = lists && level == 0 && sh.above + sh.in_bin <= kFew;
+    const bool list = !WEIGHTED && level == 0 && sh.above + sh.in_bin <= kList;
     float from, to;
     range.near(bin, &from, &to);
     if (list) to = hi;
@@ -484,12 +491,15 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
         if (mine > bin || (mine < bin && !list)) continue;
         l = min(l, ordered(clean));
         h = max(h, ordered(clean));
-        const int at = atomicAdd(&sh.n, 1);
-        if (at >= kPart) continue;
+        const int at = atomicAdd(&sh.n, 1), place = rank * kPart + at;
         const Candidate one{clean, row.first + i};
-        const int place = rank * kPart + at;
+        if (list) {
+          (rank == 0 ? sh.cand : sh.seg)[min(at, kList - 1)] = one;  // (they are not more)
+          if (rank != 0 && at < kPart) cluster.map_shared_rank(&sh, 0)->seg[place] = one;
+        } else if (at < kPart) {
 #pragma unroll 1
-        for (int r = 0; r < (list ? 1 : CTAS); ++r) cluster.map_shared_rank(&sh, r)->seg[place] = one;
+          for (int r = 0; r < CTAS; ++r) cluster.map_shared_rank(&sh, r)->seg[place] = one;
+        }
       }
     }
     l = __reduce_min_sync(0xffffffffu, l);
@@ -502,7 +512,7 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     if (threadIdx.x < CTAS) cluster.map_shared_rank(&sh, threadIdx.x)->found[rank] = Found{sh.n, sh.lo, sh.hi};
     cluster.sync();
     int n = 0;
-    bool fits = true;
+    bool fits = true;  // the others' parts
     l = 0xffffffffu, h = 0;
 #pragma unroll
     for (int r = 0; r < CTAS; ++r) {
@@ -510,17 +520,19 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
       l = min(l, f.lo);
       h = max(h, f.hi);
       n += f.n;
-      fits = fits && f.n <= kPart;
+      fits = fits && (f.n <= kPart || (list && r == 0));
     }
     if (list) {
-      if (fits) {
-        if (rank == 0) collect<CTAS>(sh, n);
-        return Border{0.f, 0, target, n};
+      if (rank == 0) {
+        int i = threadIdx.x, r = 0;
+        if (i < n) {
+          for (; r < CTAS - 1 && i >= sh.found[r].n; ++r) i -= sh.found[r].n;
+          if (r > 0) sh.cand[threadIdx.x] = fits ? sh.seg[r * kPart + i] : cluster.map_shared_rank(&sh, r)->seg[i];
+        }
+        __syncthreads();
       }
-      lists = false;  // most of them in one CTA's part: the same again, without the list
-      --level;
-      above = 0;
-      continue;
+      if (!fits) cluster.sync();  // the first CTA has read the others'
+      return Border{0.f, 0, target, n};
     }
     above = sh.above;
     lo = unordered(l), hi = unordered(h);
@@ -548,11 +560,15 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
 }
 
 // Looks for the logit at which the weights over `lo` make up `part` of all, by
-// counts in bins and the weight in each bin's middle.  Then every token's weight,
-// once: the sum of all, for every cell the sum (kept: of weights from `least` on)
-// of its tokens above a window around that logit, and the window's in bins.  A border
-// that is not in the window, as where a few tokens make up most of the row, is
-// searched for again without one.
+// counts in bins and the weight in each bin's middle; for the first kSharp bins, whose
+// tokens are few and heavy, also by how far off the middle they are.  Then every
+// token's weight, once: the sum of all, for every cell the sum (kept: of weights from
+// `least` on) of its tokens above a window around that logit, and the window's in
+// bins.  The window is 2 bins either way: of 5000 rows drawn (normal logits, some
+// likely ones among them, in bf16 and fp32) the border was 1.8 off at most; without
+// the first bins' offsets, 0.4% were off by more than 3.5.  A border that is not in
+// the window is searched for again without one.
+constexpr int kSharp = 256;
 template <int CTAS, typename T>
 __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float top,
                                        Scale c, float part, unsigned long long least) {
@@ -561,18 +577,27 @@ __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, c
   range.set(lo, top, false);
   clear_bins(sh);
   unsigned int* counts = reinterpret_cast<unsigned int*>(sh.bins);
+  static_assert(kBins + kSharp <= 2 * kBins, "room beside the counts");
+  int* offsets = reinterpret_cast<int*>(sh.bins) + kBins;
   for (int cell = warp; cell < row.cells; cell += kWarps) {
     float z[8];
     row.get(cell, z);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (range.has(z[e])) atomicAdd(&counts[range.bin(z[e])], 1u);
+    for (int e = 0; e < 8; ++e) {
+      if (!range.has(z[e])) continue;
+      const int b = range.bin(z[e]);
+      atomicAdd(&counts[b], 1u);
+      if (b < kSharp) atomicAdd(&offsets[b], range.offset(z[e], b));
+    }
   }
   __syncthreads();
   const float step = -c.hi / range.per;  // log2 of the weights from bin to bin
+  const float per_offset = step * 0.693147181f / Range::kOffset;
   {
     const int b = 2 * static_cast<int>(threadIdx.x);
-    float sum = counts[b] * ex2(b * step) + counts[b + 1] * ex2((b + 1) * step);
+    float n0 = counts[b], n1 = counts[b + 1];
+    if (b < kSharp) n0 += offsets[b] * per_offset, n1 += offsets[b + 1] * per_offset;
+    float sum = n0 * ex2(b * step) + n1 * ex2((b + 1) * step);
 #pragma unroll
     for (int o = 1; o < kGroup / 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int to = lane & (kGroup / 2 - 1);
@@ -589,18 +614,24 @@ __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, c
     const uint32_t over = __ballot_sync(0xffffffffu, upto >= want);
     const int group = over != 0 ? __ffs(over) - 1 : 31;
     const float before = __shfl_sync(0xffffffffu, upto - g, group);
-    unsigned int n[CTAS], count = 0;
-#pragma unroll
-    for (int r = 0; r < CTAS; ++r)
-      n[r] = reinterpret_cast<const unsigned int*>(cluster.map_shared_rank(sh.bins, r))[group * kGroup + lane];
-#pragma unroll
-    for (int r = 0; r < CTAS; ++r) count += n[r];
     const int b = group * kGroup + lane;
+    const bool sharp = group < kSharp / kGroup;
+    unsigned int n[CTAS], whole = 0;
+    int off[CTAS], off_middle = 0;
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) {
+      const unsigned int* other = reinterpret_cast<const unsigned int*>(cluster.map_shared_rank(sh.bins, r));
+      n[r] = other[b];
+      off[r] = sharp ? static_cast<int>(other[kBins + b]) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) whole += n[r], off_middle += off[r];
+    const float count = whole + off_middle * per_offset;
     const uint32_t past = __ballot_sync(0xffffffffu, before + warp_scan(count * ex2(b * step)) >= want);
     if (lane == 0) sh.bin = group * kGroup + (past != 0 ? __ffs(past) - 1 : 31);
   }
   cluster.sync();  // all have read the others' counts
-  const float from = fmaxf(lo, top - (sh.bin + 4) / range.per), to = fminf(top, top - (sh.bin - 4) / range.per);
+  const float from = fmaxf(lo, top - (sh.bin + 2) / range.per), to = fminf(top, top - (sh.bin - 2) / range.per);
   Window window{true, {}};
   window.range.set(from, to, false);
   clear_bins(sh);
@@ -654,45 +685,75 @@ __device__ __forceinline__ void put(const SampleArgs& p, int b, int token, unsig
   if (p.prob != nullptr) p.prob[b] = whole != 0 ? __ull2float_rn(w) / __ull2float_rn(whole) : 0.f;
 }
 
-// The token of one of n <= kFew candidates, by one CTA: their places by falling
-// logit and by index, then the filters and the draw on sums in those orders.
+// The keys of the first n threads sorted: thread t's is the t-th.  Only the largest
+// number, which is behind all and which the others have, may come twice.  Few are
+// counted each with each, four or two threads a key; more go through Batcher's
+// bitonic network, whose 45 steps for 512 keys each wait for the one before: by top-k
+// 50 and 120 of a row of 32768 the whole call takes 8.4 and 9.0 us counted, 9.8 and
+// 10.7 by the network, which for 400 takes 12.9, counted 17.2.
+__device__ __forceinline__ unsigned long long sort_keys(Shared& sh, unsigned long long key, int n) {
+  static_assert(kList <= kThreads && 2 * kList <= kBins, "a thread a key, two buffers in the bins, which have served");
+  const int t = static_cast<int>(threadIdx.x);
+  if (n <= kCounted) {
+    static_assert(2 * kCounted <= kThreads, "two threads a key, or four");
+    const int log = n <= kThreads / 4 ? 2 : 1, mine = t >> log, part = t & ((1 << log) - 1);
+    if (t < n) sh.bins[t] = key, sh.bins[kList + t] = ~0ULL;
+    __syncthreads();
+    const unsigned long long me = sh.bins[min(mine, n - 1)];
+    int less = 0;
+#pragma unroll 4
+    for (int i = part; i < n; i += 1 << log) less += sh.bins[i] < me;
+    less += __shfl_xor_sync(0xffffffffu, less, 1);
+    if (log == 2) less += __shfl_xor_sync(0xffffffffu, less, 2);
+    if (part == 0 && mine < n) sh.bins[kList + less] = me;
+    __syncthreads();
+    return t < n ? sh.bins[kList + t] : ~0ULL;
+  }
+  int size = 2 * kCounted, buffer = 0;
+  while (size < n) size <<= 1;
+  for (int k = 2; k <= size; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      unsigned long long other;
+      if (j >= 32) {
+        sh.bins[buffer + t] = key;
+        __syncthreads();
+        other = sh.bins[buffer + (t ^ j)];
+        buffer ^= kList;
+      } else {
+        other = __shfl_xor_sync(0xffffffffu, key, j);
+      }
+      const bool least = ((t & k) == 0) == ((t & j) == 0);
+      key = (other < key) == least ? other : key;
+    }
+  return key;
+}
+
+// The token of one of n <= kList candidates, by one CTA: sorted by falling logit,
+// equal ones by index, for the filters; then by index, for the draw.
 __device__ __forceinline__ void finish_list(Shared& sh, int n, const Settings& set, float top, Scale c,
                                             const SampleArgs& p, int b) {
-  const int t = static_cast<int>(threadIdx.x), mine = t >> 1;
-  const Candidate me = sh.cand[min(mine, n - 1)];
-  int by_z = 0, by_i = 0;  // how many come first
-  for (int i = t & 1; i < n; i += 2) {
-    const Candidate other = sh.cand[i];
-    const bool lower = other.token < me.token;
-    by_z += other.z > me.z || (other.z == me.z && lower);
-    by_i += lower;
+  static_assert(kSampleMaxVocab <= 1 << 18 && kOne == 44, "a token and its weight fit 63 bits");
+  const int t = static_cast<int>(threadIdx.x);
+  unsigned long long key = ~0ULL;
+  if (t < n) {
+    const Candidate me = sh.cand[t];
+    key = static_cast<unsigned long long>(~ordered(me.z)) << 32 | static_cast<uint32_t>(me.token);
   }
-  by_z += __shfl_xor_sync(0xffffffffu, by_z, 1);
-  by_i += __shfl_xor_sync(0xffffffffu, by_i, 1);
-  const bool is = mine < n && (t & 1) == 0;
-  const unsigned long long w = is && by_z < set.top_k ? weight(me.z, top, c, sh.table) : 0ULL;
-  unsigned long long* sorted = sh.bins;  // the bins have served
-  for (int i = t; i < 2 * kFew; i += kThreads) sorted[i] = 0;
   __syncthreads();
-  if (is) sorted[by_z] = w;
-  __syncthreads();
+  key = sort_keys(sh, key, n);
+  const unsigned long long x =
+      t < n && t < set.top_k ? weight(unordered(~static_cast<uint32_t>(key >> 32)), top, c, sh.table) : 0ULL;
   unsigned long long all;
-  const unsigned long long x = t < kFew ? sorted[t] : 0ULL;
   const unsigned long long before = block_scan(sh, x, &all);
   const unsigned long long target =
       set.top_p < 1.f ? (set.top_p > 0.f ? max(1ULL, share_of(set.top_p, all, true)) : 1ULL) : all;
-  if (t < kFew) sorted[t] = before < target && x >= set.least ? x : 0ULL;
-  __syncthreads();
-  if (is) {
-    sorted[kFew + by_i] = sorted[by_z];
-    sh.cand_w[by_i] = static_cast<unsigned long long>(me.token);
-  }
-  __syncthreads();
+  const bool kept = before < target && x >= set.least && x != 0;
+  key = sort_keys(sh, kept ? (key & 0xffffffffu) << (kOne + 1) | x : ~0ULL, n);
+  const unsigned long long y = key != ~0ULL ? key & ((2ULL << kOne) - 1) : 0ULL;
   unsigned long long whole;
-  const unsigned long long y = t < kFew ? sorted[kFew + t] : 0ULL;
   const unsigned long long from = block_scan(sh, y, &whole);
   const unsigned long long at = drawn(set.u, whole);
-  if (from <= at && at < from + y) put(p, b, static_cast<int>(sh.cand_w[t]), y, whole);
+  if (from <= at && at < from + y) put(p, b, static_cast<int>(key >> (kOne + 1)), y, whole);
 }
 
 template <typename T, int VEC, int CTAS>
