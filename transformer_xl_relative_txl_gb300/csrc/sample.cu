@@ -82,15 +82,23 @@ constexpr Powers powers() {
 }
 __device__ constexpr Powers kPowers = powers();
 
-struct Scale {  // log2(e) / T in two parts
-  float hi, lo;
+// A row's logits and its T, times a power of two: log2(e) / T in two parts, the
+// largest logit, the power.
+struct Scale {
+  float hi, lo, top, by;
 };
-// (In fp64 this alone would take a microsecond.)
-__device__ __forceinline__ Scale scale_of(float temperature) {
+// The power is 1 but for the ends of T.  A quarter where logits may be further
+// apart than the largest float and still have weights.  2^40 where 1 / T may be
+// over it; but for a largest logit whose own steps are 2^56 T or more, where every
+// other weight is 0.  (In fp64 this alone would take a microsecond.)
+__device__ __forceinline__ Scale scale_of(float temperature, float top) {
   constexpr float kHi = 1.442695041f, kLo = static_cast<float>(1.4426950408889634 - static_cast<double>(kHi));
-  const float hi = kHi / temperature;
-  if (!(hi > 0.f) || hi > FLT_MAX) return Scale{fminf(hi, FLT_MAX), 0.f};
-  return Scale{hi, (fmaf(-hi, temperature, kHi) + kLo) / temperature};
+  float by = 1.f;
+  if (temperature > 0x1p100f) by = 0.25f;
+  else if (temperature < 0x1p-100f && fabsf(top) < 0x1p-20f) by = 0x1p40f;
+  const float t = temperature * by, hi = kHi / t;
+  if (!(hi > 0.f) || hi > FLT_MAX) return Scale{fminf(hi, FLT_MAX), 0.f, top * by, by};
+  return Scale{hi, (fmaf(-hi, t, kHi) + kLo) / t, top * by, by};
 }
 
 // p x in whole numbers, rounded up or down, exactly; 0 < p < 1.
@@ -120,10 +128,10 @@ __device__ __forceinline__ unsigned long long share_of(float p, unsigned long lo
 // 2^-10, so three terms do.  No branch, so that several run at once: one takes 250
 // cycles, of which its instructions are a fifth.  Floats become whole numbers by adding a power of two
 // and taking the bits: conversions run at an eighth of the rate.
-__device__ __forceinline__ unsigned long long weight(float z, float top, Scale c, const unsigned long long* table) {
-  float d = top - z;
-  const float back = d - top;
-  float err = (top - (d - back)) - (z + back);  // top - z = d + err
+__device__ __forceinline__ unsigned long long weight(float z, const Scale& c, const unsigned long long* table) {
+  float d = fmaf(-z, c.by, c.top);
+  const float back = d - c.top;
+  float err = (c.top - (d - back)) - fmaf(z, c.by, back);  // top - z = d + err
   if (d > 3.0e38f) d = FLT_MAX, err = 0.f;
   const float y = fminf(d * c.hi, 45.f);  // from 45 on 0: the last shift
   const float y2 = fmaf(d, c.hi, -y) + fmaf(d, c.lo, err * c.hi);
@@ -401,7 +409,7 @@ struct Window {
 // is -1.
 template <bool WEIGHTED, int CTAS, typename T, typename F>
 __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float hi,
-                                         float top, Scale c, F target_of, const Window& window = Window{false, {}}) {
+                                         const Scale& c, F target_of, const Window& window = Window{false, {}}) {
   constexpr int kPart = kList / CTAS;  // candidates from one CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = static_cast<int>(cluster.block_rank());
   unsigned long long above = 0, target = 0;
@@ -420,7 +428,7 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
         for (int e = 0; e < 8; ++e) {
           if (!range.has(z[e])) continue;
           if constexpr (WEIGHTED) {
-            const unsigned long long w = weight(z[e], top, c, sh.table);
+            const unsigned long long w = weight(z[e], c, sh.table);
             if (w != 0) add64(&sh.bins[range.bin(z[e])], w);
           } else {
             atomicAdd(reinterpret_cast<unsigned int*>(&sh.bins[range.bin(z[e])]), 1u);
@@ -540,7 +548,7 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
     if (!fits || n > kFew) continue;
     collect<CTAS>(sh, n);
     if (static_cast<int>(threadIdx.x) < n)
-      sh.cand_w[threadIdx.x] = WEIGHTED ? weight(sh.cand[threadIdx.x].z, top, c, sh.table) : 1ULL;
+      sh.cand_w[threadIdx.x] = WEIGHTED ? weight(sh.cand[threadIdx.x].z, c, sh.table) : 1ULL;
     __syncthreads();
     // Two threads for each of them: what lies above it, what equals it.
     static_assert(2 * kFew <= kThreads, "two threads a candidate");
@@ -571,7 +579,7 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
 constexpr int kSharp = 256;
 template <int CTAS, typename T>
 __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float top,
-                                       Scale c, float part, unsigned long long least) {
+                                       const Scale& c, float part, unsigned long long least) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = static_cast<int>(cluster.block_rank());
   Range range;
   range.set(lo, top, false);
@@ -591,7 +599,7 @@ __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, c
     }
   }
   __syncthreads();
-  const float step = -c.hi / range.per;  // log2 of the weights from bin to bin
+  const float step = -c.hi / range.per * c.by;  // log2 of the weights from bin to bin
   const float per_offset = step * 0.693147181f / Range::kOffset;
   {
     const int b = 2 * static_cast<int>(threadIdx.x);
@@ -645,7 +653,7 @@ __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, c
       unsigned long long w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        w[e] = weight(z[half + e], top, c, sh.table);
+        w[e] = weight(z[half + e], c, sh.table);
         w[e] = z[half + e] >= lo ? w[e] : 0ULL;
         all += w[e];
         over += z[half + e] > to ? w[e] : 0ULL;
@@ -730,7 +738,7 @@ __device__ __forceinline__ unsigned long long sort_keys(Shared& sh, unsigned lon
 
 // The token of one of n <= kList candidates, by one CTA: sorted by falling logit,
 // equal ones by index, for the filters; then by index, for the draw.
-__device__ __forceinline__ void finish_list(Shared& sh, int n, const Settings& set, float top, Scale c,
+__device__ __forceinline__ void finish_list(Shared& sh, int n, const Settings& set, const Scale& c,
                                             const SampleArgs& p, int b) {
   static_assert(kSampleMaxVocab <= 1 << 18 && kOne == 44, "a token and its weight fit 63 bits");
   const int t = static_cast<int>(threadIdx.x);
@@ -742,7 +750,7 @@ __device__ __forceinline__ void finish_list(Shared& sh, int n, const Settings& s
   __syncthreads();
   key = sort_keys(sh, key, n);
   const unsigned long long x =
-      t < n && t < set.top_k ? weight(unordered(~static_cast<uint32_t>(key >> 32)), top, c, sh.table) : 0ULL;
+      t < n && t < set.top_k ? weight(unordered(~static_cast<uint32_t>(key >> 32)), c, sh.table) : 0ULL;
   unsigned long long all;
   const unsigned long long before = block_scan(sh, x, &all);
   const unsigned long long target =
@@ -781,7 +789,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   set.top_k = greedy ? 1 : k_asked;
   set.top_p = !greedy && p_asked < 1.f ? p_asked : 1.f;
   set.least = !greedy && m_asked > 0.f ? __float2ull_ru(fminf(m_asked, 1.f) * 0x1p44f) : 0ULL;
-  const Scale c = greedy ? Scale{0.f, 0.f} : scale_of(temperature);
 
   // The row's largest logit.  And one that is not over the top_k-th largest,
   // without which the search would put the whole row into bins: of `parts` parts
@@ -842,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     top = largest<T>();
   }
   cut = parts >= set.top_k ? fminf(unordered(cut_at), top) : -INFINITY;
+  const Scale c = greedy ? Scale{0.f, 0.f, top, 1.f} : scale_of(temperature, top);
 
   // The threshold: tokens over `value`, and the first `ties` of those at it.
   float value = -INFINITY;
@@ -851,9 +859,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
     value = top, ties = 1;
   } else if (set.top_k > 0 && set.top_k < p.V) {
     const auto target_of = [&](unsigned long long) { return static_cast<unsigned long long>(set.top_k); };
-    const Border k = search<false, CTAS>(cluster, sh, row, fmaxf(cut, -FLT_MAX), top, top, c, target_of);
+    const Border k = search<false, CTAS>(cluster, sh, row, fmaxf(cut, -FLT_MAX), top, c, target_of);
     if (k.list > 0) {
-      if (rank == 0) finish_list(sh, k.list, set, top, c, p, b);
+      if (rank == 0) finish_list(sh, k.list, set, c, p, b);
       return;
     }
     value = k.value;  // -inf: there are no more than top_k
@@ -861,39 +869,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p,
   }
   if (set.top_p < 1.f) {
     // The smallest part of what is left that makes up top_p of it.
-    const unsigned long long at_value = ties > 0 ? ties * weight(value, top, c, sh.table) : 0ULL;
+    const unsigned long long at_value = ties > 0 ? ties * weight(value, c, sh.table) : 0ULL;
     const auto target_of = [&](unsigned long long all) {
       return set.top_p > 0.f ? max(1ULL, share_of(set.top_p, all + at_value, true)) : 1ULL;
     };
     unsigned long long above = 0, target;
     float at = -INFINITY;
     if (value < top) {
-      const float reach = top - 45.5f / c.hi;  // below, weights are 0
+      const float reach = top - 45.5f / c.hi / c.by;  // below, weights are 0
       const float next = value == -INFINITY ? -FLT_MAX : unordered(ordered(value) + 1);
       const float lo = fmaxf(next, reach);
       Border s{0.f, 0, 0, -1};
       if (value == -INFINITY) {
         const Window window = look<CTAS>(cluster, sh, row, lo, top, c, set.top_p, set.least);
-        s = search<true, CTAS>(cluster, sh, row, lo, top, top, c, target_of, window);
+        s = search<true, CTAS>(cluster, sh, row, lo, top, c, target_of, window);
         if (s.list == 0) counted = window.range.hi;
       }
-      if (s.list < 0) s = search<true, CTAS>(cluster, sh, row, lo, top, top, c, target_of);
+      if (s.list < 0) s = search<true, CTAS>(cluster, sh, row, lo, top, c, target_of);
       at = s.value, above = s.above, target = s.target;
     } else {
       target = target_of(0);
     }
     // (Rounded up; none of the weights that the sums count is 0.)
-    const unsigned long long w = weight(at == -INFINITY ? value : at, top, c, sh.table);
+    const unsigned long long w = weight(at == -INFINITY ? value : at, c, sh.table);
     const long long need = static_cast<long long>((target - above + w - 1) / w);
     ties = at == -INFINITY ? min(ties, need) : need;
     value = at == -INFINITY ? value : at;
   }
-  const unsigned long long w_tie = ties > 0 ? weight(value, top, c, sh.table) : 0ULL;
+  const unsigned long long w_tie = ties > 0 ? weight(value, c, sh.table) : 0ULL;
   if (w_tie < set.least) ties = 0;
 
   // The kept weights of every cell, then of the CTA, then of the row.
   const auto kept_weight = [&](float z) {
-    const unsigned long long w = z > value ? weight(z, top, c, sh.table) : 0ULL;
+    const unsigned long long w = z > value ? weight(z, c, sh.table) : 0ULL;
     return w < set.least ? 0ULL : w;
   };
   for (int cell = warp; cell < row.cells; cell += kWarps) {
