@@ -169,7 +169,7 @@ struct GradSmem {  // ahead of end[local rows]
   uint32_t list[kList];  // by warp; then the ranks of the next's
   uint32_t line[kList];  // all, by place
   uint32_t sorted[kList];
-  float part[kGradThreads][2][4];
+  alignas(16) float part[kGradThreads][2][4];
   int counts[kGradWarps];
   int sums[kGradWarps];
 };

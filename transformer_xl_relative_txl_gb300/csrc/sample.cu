@@ -181,9 +181,9 @@ struct Candidate {
   int token;
 };
 
-struct Shared {
+struct alignas(16) Shared {
   unsigned long long table[kTable];
-  unsigned long long bins[kBins];  // of the range at hand: sums of weights, or counts
+  alignas(16) unsigned long long bins[kBins];  // of the range at hand: sums of weights, or counts
   unsigned long long groups[kMaxCluster][kGroups];
   float top[kMaxCluster];
   uint32_t cut[kMaxCluster];
@@ -207,6 +207,7 @@ struct Shared {
   float value;
   unsigned long long value_above;
 };
+static_assert(sizeof(Shared) % 16 == 0, "the stretch behind it is read 16 bytes at a time");
 
 // Inclusive sum over a warp.
 template <typename T>
