@@ -1,6 +1,8 @@
 """The operators around the layers on streams of the caller's and beside each other: outputs that no earlier call can
 have left, work that runs only behind what its own stream holds, calls in flight at the same time."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -112,3 +114,46 @@ def test_replays_of_a_graph_beside_calls(txl):  # noqa: F811
         bad.append(steps[1].differ(wants[1]))
     torch.cuda.synchronize()
     assert [int(b) for b in bad] == [0] * len(bad)
+
+
+def test_every_call_of_many_threads(txl):  # noqa: F811
+    """Calls of other sizes from several threads at once, each with outputs of its own that hold nothing before it: not
+    one that returns without having written."""
+    lib, ptr, rounds, slots = txl.lib, torch.Tensor.data_ptr, 12, 25
+    rng = np.random.default_rng(25)
+    jobs = []
+    for V, k, n in ((64, 128, 64), (30000, 4096, 256), (2000, 512, 64), (20000, 2048, 128)):
+        x, codes, scales = _product(rng, 4, k, n, 32)
+        job = dict(V=V, k=k, n=n, x=x, codes=codes, scales=scales, z=_tensor(rng.standard_normal((2, V)), F32),
+                   u=torch.full((2,), 0.5, device=dev()), tokens=_ints(rng.integers(0, V, 100)), dout=_tensor(rng.standard_normal((100, 16)), F32),
+                   out=torch.empty(slots, 2, device=dev(), dtype=torch.int32), y=torch.empty(slots, 4, n, device=dev(), dtype=BF),
+                   grad=torch.empty(slots, V, 16, device=dev()), stream=torch.cuda.Stream())
+        alone = [torch.full_like(job[t][0], -7) for t in ("out", "y", "grad")]
+        txl.txl_sample(job["z"], job["u"], alone[0])
+        txl.txl_dense_w4(x, codes, scales, alone[1])
+        txl.txl_embed_backward(job["tokens"], job["dout"], alone[2])
+        jobs.append((job, alone))
+    torch.cuda.synchronize()
+    failed, differ, start = [], [], threading.Barrier(len(jobs))
+
+    def run(job, alone):
+        s = job["stream"].cuda_stream
+        with torch.cuda.stream(job["stream"]):
+            for _ in range(rounds):
+                for t in ("out", "y", "grad"):
+                    job[t].fill_(-7)
+                start.wait()
+                for i in range(slots):
+                    failed.append(lib.txl_sample(ptr(job["z"]), job["V"], 2, job["V"], ptr(job["u"]), None, None, None, None, ptr(job["out"][i]), None, 0, s))
+                    failed.append(lib.txl_dense_w4(ptr(job["x"]), ptr(job["codes"]), ptr(job["scales"]), ptr(job["y"][i]), 4, job["n"], job["k"], 32, None, 0, 1, s))
+                    failed.append(lib.txl_embed_backward(ptr(job["tokens"]), ptr(job["dout"]), ptr(job["grad"][i]), 100, job["V"], 16, 1.0, 0, 0, s))
+                differ.append(sum((job[t] != w).sum() for t, w in zip(("out", "y", "grad"), alone)))
+
+    threads = [threading.Thread(target=run, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(failed) == 3 * slots * rounds * len(jobs) and not any(failed), (sum(f != 0 for f in failed), len(failed))
+    assert [int(d) for d in differ] == [0] * rounds * len(jobs)
