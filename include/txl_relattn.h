@@ -706,10 +706,13 @@ TXL_API int txl_embed_forward(const int* tokens, const void* table, void* out, i
  *           no token names with zeros (T == 0: all of it); else those rows are
  *           neither read nor written (T == 0: an empty call)
  * tokens, scale, alignments and limits as in txl_embed_forward; dtable must not
- * overlap tokens or dout.  Sums are fp32, in an order that only the tokens decide:
- * the same call gives the same bits.  A sum is rounded, then its product with
- * scale, then, with accumulate, that added to the row, where subnormal numbers
- * count and are left as 0.
+ * overlap tokens or dout.  Sums are fp32, in an order that the tokens, V and d
+ * decide: the same call gives the same bits, whatever dout's type and the
+ * addresses.  A sum is rounded, then its product with scale.  With more than
+ * 4096 tokens, a row's sum may come in parts, of 2048 or more tokens in a line
+ * each (the last: of what is left), each summed, multiplied and rounded so and
+ * added to the row.  Where something is added to a row (with accumulate; a sum's
+ * parts but for the first), subnormal numbers count and are left as 0.
  */
 TXL_API int txl_embed_backward(const int* tokens, const void* dout, float* dtable, int T, int V, int d, float scale,
                                int accumulate, txl_dtype dtype, cudaStream_t stream);

@@ -140,9 +140,12 @@ cudaError_t forward_any(const int* tokens, const void* table, void* out, int T, 
 // common ids, which vocabularies number first, are spread over all CTAs.  It
 // reads all ids, keeps its own in the order of their places, sorts them by row
 // and place and sums each row's gradients, in shares that are equal whatever the
-// rows' lengths.  A row's sum has one order, which the ids alone decide, and is
-// put into the table once: added to it, by one atomic whose result nothing waits
-// for, or stored.
+// rows' lengths.  A row's sum has one order, which the ids, V and d decide, and is
+// put into the table once a pass: added to it, by one atomic whose result nothing
+// waits for, or stored.  A pass takes up to 32768 ids, of which a CTA's own must fit
+// its lists: where a row has most of them, a half, a quarter or an eighth of that,
+// and each length tried reads its ids again, in every pass (of 11264 equal ids 47168
+// are read).
 //
 // The gradients' rows are asked for as soon as the ids are listed, so that they
 // are on their way to L2 while the list is sorted and the other rows zeroed.
