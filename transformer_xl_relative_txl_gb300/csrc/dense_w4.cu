@@ -373,18 +373,20 @@ cudaError_t launch(Args a, cudaStream_t stream) {
   // the most, a sum of warps, of CTAs, 1 KB of x.  Both ends: 32 tokens, k =
   // 4096, n = 1024 take 21 us with a CTA for 128 columns and all of k, 6.3 with a
   // cluster of four for 32; 8 tokens, k = 1024, n = 131072 take 19.4 with the first
-  // and 98 with a cluster of four for 64.
+  // and 98 with a cluster of four for 64.  (Fitted with fewer clusters of 8 at a
+  // time than there is room for, 12, 24 and 36, and more of 4, 38, 76 and 114; where
+  // that decides, the true counts give: 8 tokens, k = 8192, n = 5792 10.4 us for
+  // 14.2, 16 tokens, 8192, 23168 41 for 62, 16 tokens, 8192, 4096 10.5 for 10.2.)
   constexpr int kEach = MT == 1 ? 70 : MT == 2 ? 90 : 190;
   long long best = -1;
   int best_clusters = 1, best_smem = 0;
   for (int wr_log = 3; wr_log >= 0; --wr_log)
-    for (int split = 1; split <= kMaxSplit && (split == 1 || split <= blocks); split *= 2) {
+    for (int log = 0, split = 1; split <= kMaxSplit && (split == 1 || split <= blocks); split = 1 << ++log) {
       const int tiles = (a.n + (16 << wr_log) - 1) / (16 << wr_log), wk = kWarps >> wr_log;
       const int mine = (blocks + split - 1) / split, kx = std::min(mine * kBlockK, kMaxX);
       const int smem = S::smem(kx);
       const int per_sm = std::max(1, std::min(S::kPerSm, 227 * 1024 / (smem + 1024)));
-      // (12 clusters of 8 find room at a time, of 19 that there are SMs for.)
-      const int clusters = std::min(tiles, split == 8 ? 12 * per_sm : 152 * per_sm / split);
+      const int clusters = std::min(tiles, clusters_at_a_time(log, per_sm));
       const long long rounds = (tiles + clusters - 1) / clusters;
       const long long on_sm = (static_cast<long long>(tiles) * split + 151) / 152 * mine << wr_log;  // blocks
       const long long ns = on_sm * kEach + rounds * ((wk > 1 ? 670 : 0) + (split > 1 ? 2100 : 0)) +

@@ -1044,20 +1044,21 @@ cudaError_t by_size(const SampleArgs& a, cudaStream_t stream) {
   // CTAs of a row, by the time that they take: fitted to 220 measured ones (1 to 256
   // rows of 4096 to 131072, bf16 and fp32, with and without top-k and top-p), whose
   // best it misses by 1% on average and 18% at most.  Some rows find room at a time,
-  // two CTAs on an SM where their stretches fit, the others follow; 37 clusters
-  // of 4 and 18 of 8 do where there are SMs for 38 and 19.  Both ends, by top-p:
-  // one row of 131072 takes 25 us by 8 CTAs and 60 by 2, 256 of 16384 take 36 by one
-  // each and 121 by 8.
+  // two CTAs on an SM where their stretches fit, the others follow.  Both ends, by
+  // top-p: one row of 131072 takes 25 us by 8 CTAs and 60 by 2, 256 of 16384 take 36
+  // by one each and 121 by 8.  (Fitted with room for one cluster of 4 and three of 8
+  // more than there is; where that decides, the true counts give, by top-p and by
+  // top-k: 37 rows of 131072 in fp32 56 us for 70 and 22 for 20.5, 148 of them 167
+  // for 185 and 58 both, 16 of 185364 51 for 60 and 15 for 20.)
   int ctas = 0;
   double best = 0;
   for (int log = 0; 1 << log <= kMaxCluster; ++log) {
     const int c = 1 << log, stretch = ((a.V + c - 1) / c + kCell - 1) / kCell * kCell;
     if (stretch > max_cells<T>() * kCell) continue;
     const bool two = 2 * (sizeof(Shared) + stretch * sizeof(T) + 1024) <= 228 * 1024;
-    constexpr int kPlaces[] = {152, 76, 37, 18};
-    const int places = kPlaces[log] * (two ? 2 : 1), rest = a.B % places;
+    const int places = clusters_at_a_time(log, two ? 2 : 1), rest = a.B % places;
     const auto us = [&](bool shared) { return 10 + 1.5 * log + stretch / 1200.0 * (shared ? 1.9 : 1.0); };
-    const double all = a.B / places * us(two) + (rest == 0 ? 0.0 : us(rest > kPlaces[log]));
+    const double all = a.B / places * us(two) + (rest == 0 ? 0.0 : us(two && rest > places / 2));
     if (ctas == 0 || all < best) ctas = c, best = all;
   }
   switch (ctas) {

@@ -7,6 +7,15 @@
 
 namespace txl {
 
+// How many clusters of 2^log CTAs, of which an SM has room for per_sm, run at a
+// time: cudaOccupancyMaxActiveClusters' answers for the products' and the sampler's
+// kernels, which depend on per_sm alone.  A cluster stays within one group of SMs,
+// so that those of 4 and 8 leave some idle.
+inline int clusters_at_a_time(int log, int per_sm) {
+  constexpr int kAt[3][4] = {{152, 76, 36, 15}, {304, 152, 74, 36}, {456, 228, 110, 51}};
+  return kAt[per_sm - 1][log];
+}
+
 constexpr int kEmbedMaxRows = 1 << 24;    // rows of an embedding table
 constexpr int kSampleMaxVocab = 1 << 18;  // logits of a row: its weights' sum fits 64 bits
 
