@@ -766,8 +766,12 @@ TXL_API int txl_dense_w4(const void* x, const void* codes, const void* scales, v
  *                (its prob 0)
  *   prob         device, [B] fp32 out or NULL: the token's share of the kept
  *                weights
- * Sums of weights are whole numbers (2^-44 of the largest weight), so neither the
- * order of the sums nor the batch around a row changes its token.  tokens and
+ * A weight is cut to a whole multiple of 2^-44 of the largest (one that is less
+ * counts as 0: its token is kept but never named), so neither the order of the sums
+ * nor the batch around a row changes its token.  With that and the weights' own
+ * errors, the kept tokens' shares, and the places of uniform[b] and top_p[b] among
+ * them, are off by V 2^-43 + 2^-38 at most: 2^-25 where all of 2^18 tokens but one
+ * weigh next to nothing.  tokens and
  * prob must not overlap each other or an input (TXL_ERR_ALIAS).  Limits
  * (TXL_ERR_UNSUPPORTED): V at most 2^18, B 65535.  B == 0 is an empty call.
  */

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import dev
-from test_gpu_tokens import BF, F32, _check_sample, _tensor, txl  # noqa: F401
+from test_gpu_tokens import BF, F32, _check_sample, _host, _tensor, txl  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,24 @@ def test_sample_cold_rows(txl, V):  # noqa: F811
     for s in ({}, dict(top_p=[0.1, 0.5, 0.9, 0.99, 0.999, 0.7])):
         _check_sample(txl, _tensor(wide, F32), u, temperature=cold, **s)
         _check_sample(txl, _tensor(wide, BF), u, temperature=[1e-30] * 6, **s)
+
+
+@pytest.mark.parametrize("V", [5000, 131072, 1 << 18])
+@pytest.mark.parametrize("low", [14.3, 20.8, 27.9, 30.1])
+def test_sample_far_tails(txl, low, V):  # noqa: F811
+    """Many tokens of little weight, of which a weight is cut to whole multiples of 2^-44 of the largest: the token's
+    stretch of running shares holds the uniform number but for V of these, and what the weights leave (2^-39), both
+    in the sum and in the whole."""
+    rng = np.random.default_rng(V + int(low))
+    z = -low + 0.01 * rng.standard_normal((5, V))
+    z[:, -1] = 0.0
+    z = _tensor(z, F32)
+    w = np.exp(_host(z))
+    upto = w.cumsum(1) / w.sum(1, keepdims=True)
+    u = np.float32(upto[:, -2] * [0.1, 0.3, 0.5, 0.9, 0.999])  # among the tail
+    tokens, prob = torch.empty(5, device=dev(), dtype=torch.int32), torch.empty(5, device=dev())
+    txl.txl_sample(z, _tensor(u, F32), tokens, prob=prob)
+    off = 2 * (V * 2.0 ** -44 + 2.0 ** -39)
+    for b, t in enumerate(tokens.tolist()):
+        assert (upto[b, t - 1] if t else 0.0) - off <= u[b] <= upto[b, t] + off, (b, t)
+        assert abs(float(prob[b]) - w[b, t] / w[b].sum()) <= 2.0 ** -22 * float(prob[b]) + off

@@ -15,10 +15,10 @@
 // is added up over distributed shared memory.
 //
 // Sums decide tokens, so they are exact: a weight is a whole number of 2^-44 of
-// the largest weight (to about 2^-39 of its own size) and 64-bit sums of at most
-// 2^18 of them do not depend on their order.  In fp32, sums over 100000 tokens
-// would name another token once in a hundred rows or so, and this chip's fp64 is
-// far too slow for the exponentials.
+// the largest weight, cut off (right to 2^-39 of its own size before that), and
+// 64-bit sums of at most 2^18 of them do not depend on their order.  In fp32, sums
+// over 100000 tokens would name another token once in a hundred rows or so, and
+// this chip's fp64 is far too slow for the exponentials.
 //
 // Bound by chains of dependent instructions: some 85 for 32 exact weights, 25 for 32
 // logits put into bins, and ten or so barriers of a cluster, 1000 to 2000 cycles
