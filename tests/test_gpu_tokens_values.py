@@ -49,6 +49,29 @@ def test_sample_cold_rows(txl, V):  # noqa: F811
         _check_sample(txl, _tensor(wide, BF), u, temperature=[1e-30] * 6, **s)
 
 
+def _ledge(rng, V):
+    """A row of twenty tokens with three quarters of the weight and, far lower, the others, of which the largest comes
+    last, and shares of top-p next to that of the twenty: the nearest floats but one to three."""
+    z = np.log(60 / V) + 6 + 0.1 * rng.standard_normal(V)
+    z[-1] = np.log(60 / V) + 6.7
+    z[rng.choice(V - 1, 20, replace=False)] = rng.uniform(7, 9, 20)
+    z = np.float32(z)
+    w = np.exp(z.astype(np.float64) - z.max())
+    share = w[z >= 7].sum() / w.sum()
+    return z, [float(np.float32(share) + np.float32(j * 2.0 ** -24)) for j in (-3, -2, -1, 1, 2, 3)]
+
+
+@pytest.mark.parametrize("V", [3000, 50021, 131072])
+def test_sample_by_the_edge_of_a_gap(txl, V):  # noqa: F811
+    """The share of top-p ends just before or just behind a wide gap of logits, so that a guess from counts in bins puts
+    the border on its other side, and the row is searched again.  A uniform number of 1 names the last kept token."""
+    rng = np.random.default_rng(V)
+    for _ in range(4):
+        z, p = _ledge(rng, V)
+        _check_sample(txl, _tensor(np.tile(z, (6, 1)), F32), [1.0] * 6, top_p=p)
+        _check_sample(txl, _tensor(np.tile(z, (6, 1)), F32), [1.0] * 6, top_p=p, min_p=[1e-9] * 6)
+
+
 @pytest.mark.parametrize("V", [5000, 131072, 1 << 18])
 @pytest.mark.parametrize("low", [14.3, 20.8, 27.9, 30.1])
 def test_sample_far_tails(txl, low, V):  # noqa: F811

@@ -575,8 +575,11 @@ __device__ __forceinline__ Border search(cg::cluster_group& cluster, Shared& sh,
 // `least` on) of its tokens above a window around that logit, and the window's in
 // bins.  The window is 2 bins either way: of 5000 rows drawn (normal logits, some
 // likely ones among them, in bf16 and fp32) the border was 1.8 off at most; without
-// the first bins' offsets, 0.4% were off by more than 3.5.  A border that is not in
-// the window is searched for again without one.
+// the first bins' offsets, 0.4% were off by more than 3.5.  Of 34000 rows of other
+// shapes (power laws, exponential, groups, masked; temperatures of 0.1 to 4; top-p
+// 0.3 to 0.999) 26 missed it, of one shape at one temperature (rank^-3, 1.5) 3 of
+// 150: where the border lies at a gap.  It is searched for again then without a
+// window: 128 rows of 50021, all of which miss it, take 73 us against 50.
 constexpr int kSharp = 256;
 template <int CTAS, typename T>
 __device__ __forceinline__ Window look(cg::cluster_group& cluster, Shared& sh, const Row<T>& row, float lo, float top,
