@@ -2,10 +2,18 @@
 //
 //   W[j, i] = scales[j / G, i] * (code[i, j] - 8),   codes two to a byte along j
 //
-// Its floor is reading the codes once; what it meets is the issue of instructions,
-// of which those that make bf16 of codes are the most (131072 columns of 1024, 8
-// tokens: 19.4 us, 3.8 TB/s), or, in small products, the chain of launch, first
-// blocks and sums: 512 x 512 for one token 2.8 us, 4096 x 1024 for 32 6.1.
+// Its floor is reading the codes once.  131072 columns of 1024 for 8 tokens take
+// 19.4 us, 3.8 TB/s: a warp executes 24.8 instructions for each word of 8 codes, of
+// which 9, by the source, make bf16 of them; the others are the products, x from
+// shared memory for every 16 columns, the groups' sums, copies and their addresses.
+// The schedulers issue in 66% of the active cycles and no pipe is over 51%, so that
+// none alone is what bounds it.  Small products are a chain of launch, first blocks
+// and sums: 512 x 512 for one token 3.0 us; 4096 x 1024 for 32 6.1, of whose 9200
+// cycles, when nothing runs beside it, x takes 2200 (most of them the first load's
+// way), the blocks of codes 2000 and the sums of the cluster's CTAs 4500.
+//
+// All instantiations for 16 and 32 tokens (128 registers) and that of groups of 64
+// for 8 (80) spill, 12 to 28 bytes.
 //
 // The weights are the long operand, on the M side of mma.sync m16n8k16: a warp takes
 // 16 of W's columns (n) by 256 rows (k) at a time, 2 KB of codes, which it brings to
@@ -377,6 +385,8 @@ cudaError_t launch(Args a, cudaStream_t stream) {
   // time than there is room for, 12, 24 and 36, and more of 4, 38, 76 and 114; where
   // that decides, the true counts give: 8 tokens, k = 8192, n = 5792 10.4 us for
   // 14.2, 16 tokens, 8192, 23168 41 for 62, 16 tokens, 8192, 4096 10.5 for 10.2.)
+  // It plans for one block of tokens: of more than 32 rows each block of 32 has such
+  // a grid, side by side (64 rows, k = 1024, n = 4096 take 8.5 us, 512 56).
   constexpr int kEach = MT == 1 ? 70 : MT == 2 ? 90 : 190;
   long long best = -1;
   int best_clusters = 1, best_smem = 0;

@@ -122,6 +122,9 @@ cudaError_t forward_typed(const int* tokens, const void* table, void* out, int T
   return go(embed_forward_kernel<TI, TO, N, 1>, 1);
 }
 
+// Rows of 16-byte vectors, or elements one by one: 11264 rows (anywhere) of 300 in
+// bf16 take 6.2 us, of 304 3.8, of which the bytes need 2.0; from fp32 7.5 and 5.1;
+// of 512 from fp32 9.4 where out starts off 16 bytes and 6.9 on them.
 bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <typename TI, typename TO>
@@ -157,7 +160,7 @@ cudaError_t forward_any(const int* tokens, const void* table, void* out, int T, 
 // 11.6; added to a table 18.4, of 4.2.  A chain of steps, each short: at 2 CTAs an
 // SM the schedulers issue half of the time, shared memory's and the barriers'
 // latencies the rest.  A row with a large part of all ids is summed by one CTA a
-// slice: 11264 equal ids take 107 us.
+// slice: 11264 equal ids take 107 us (table written whole: 119), 4096 35.
 constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
 constexpr int kMaxLocal = 16384;  // rows of a CTA
 constexpr int kPlaceBits = 15;

@@ -23,7 +23,7 @@
 // Bound by chains of dependent instructions: some 85 for 32 exact weights, 25 for 32
 // logits put into bins, and ten or so barriers of a cluster, 1000 to 2000 cycles
 // each with what is done between them.  One row of 32768 in bf16, top-k 50 of it
-// and top-p: 8.5 us; 64 of 131072, top-k 100 to 300 and more: 26 us (17 MB: 0.65 TB/s);
+// and top-p: 8.7 us; 64 of 131072, top-k 100 to 300 and more: 26 us (17 MB: 0.65 TB/s);
 // 128 of 50021 in fp32 by top-p, where every logit's weight counts: 57 us (0.45 TB/s),
 // of 107000 cycles of a CTA 50000 for the weights, 17000 for the last look at the
 // cells, 10000 for the counts, 7000 for the reading.  There the schedulers issue 41%
