@@ -64,7 +64,7 @@ def test_calls_run_on_the_given_stream(txl, how):  # noqa: F811
     step.spoil()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(20_000_000)  # some ten milliseconds
+        torch.cuda._sleep(400_000_000)  # a fifth of a second or so
         step.tokens.copy_(right)
         if how == "current":
             step.calls()
